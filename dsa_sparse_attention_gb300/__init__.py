@@ -11,7 +11,9 @@ Names mirror the C ABI: dsa_workspace_size, dsa_indexer_score, dsa_topk,
 dsa_sparse_mla, dsa_layer_step, dsa_layer_step_host (and
 prepare_layer_step_host, the same call with its arguments marshalled once),
 dsa_topk_noalloc, dsa_indexer_front, dsa_write_latent, dsa_selftest_wait_timeout,
-dsa_check, dsa_status_string, dsa_abi_version.
+dsa_check, dsa_status_string, dsa_abi_version; for trees of drafted tokens
+dsa_tree_mla, dsa_tree_topk, dsa_tree_commit; for the rows of the cache
+dsa_cache_copy, dsa_cache_fork, dsa_cache_free, dsa_cache_compact.
 """
 import ctypes
 import os
@@ -50,6 +52,16 @@ class dsa_batch(ctypes.Structure):
                 ("bt_stride", ctypes.c_int32), ("flags", ctypes.c_int32), ("max_ctx_len", ctypes.c_int64)]
 
 
+class dsa_tree(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("mask", ctypes.c_void_p), ("mask_words", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class dsa_pages(ctypes.Structure):
+    _fields_ = [("ref_count", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("ctx_lens", ctypes.c_void_p),
+                ("num_reqs", ctypes.c_int32), ("bt_stride", ctypes.c_int32)]
+
+
 class dsa_host_io(ctypes.Structure):
     _fields_ = [("q_idx", ctypes.c_void_p), ("w", ctypes.c_void_p), ("q", ctypes.c_void_p), ("q_req", ctypes.c_void_p),
                 ("q_pos", ctypes.c_void_p), ("ctx_lens", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
@@ -61,7 +73,7 @@ def _load():
         raise ImportError(f"DSA CUDA library not built ({_LIB_PATH}); run dsa_sparse_attention_gb300.build.build()")
     lib = ctypes.CDLL(_LIB_PATH)
     P = ctypes.POINTER
-    L, B = P(dsa_kv_layout), P(dsa_batch)
+    L, B, R, G = P(dsa_kv_layout), P(dsa_batch), P(dsa_tree), P(dsa_pages)
     vp, i32, i64, sz, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
     sig = {
         "dsa_abi_version": (i32, []),
@@ -78,6 +90,15 @@ def _load():
         "dsa_selftest_wait_timeout": (i32, [vp, sz, i64, vp]),
         "dsa_indexer_front": (i32, [L, B, vp, i32, vp, f32, vp, vp, vp, vp, vp, vp, sz, vp]),
         "dsa_write_latent": (i32, [L, B, vp, vp, sz, vp]),
+        "dsa_tree_workspace_size": (sz, [L, B]),
+        "dsa_tree_mla": (i32, [L, B, R, vp, f32, vp, vp, vp, sz, vp]),
+        "dsa_tree_topk": (i32, [L, B, R, vp, i64, i32, vp, vp, vp, sz, vp]),
+        "dsa_tree_commit": (i32, [L, B, vp, vp, i32, vp, vp, sz, vp]),
+        "dsa_cache_workspace_size": (sz, [L, i32]),
+        "dsa_cache_copy": (i32, [L, vp, vp, i32, vp, vp, sz, vp]),
+        "dsa_cache_fork": (i32, [L, G, vp, vp, i32, vp, vp, vp, sz, vp]),
+        "dsa_cache_free": (i32, [L, G, vp, i32, vp, sz, vp]),
+        "dsa_cache_compact": (i32, [L, G, G, vp, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -251,6 +272,117 @@ def dsa_write_latent(layout, batch, latent, ws=None, stream=None):
     """The new tokens' latents (bf16 [T, 576]) into their cache slots, in the pool's format."""
     _check(library().dsa_write_latent(ctypes.byref(layout), ctypes.byref(batch), _ptr(latent), _ptr(ws), ws.numel(),
                                       _stream(stream)), "dsa_write_latent")
+
+
+def _int32(name, t, ndim):
+    """An int32 tensor whose elements lie one behind the other, as the C ABI reads it."""
+    if t is not None and (t.dtype != torch.int32 or t.dim() != ndim or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {ndim} dimension(s)")
+    return t
+
+
+def make_tree(base, mask):
+    """Descriptor of the drafted tokens' trees over device int32 tensors (kept alive by the
+    caller): base [B] committed tokens, mask [T, words], bit i of row t set where token t sees
+    drafted slot i."""
+    _int32("base", base, 1), _int32("mask", mask, 2)
+    return dsa_tree(_ptr(base), _ptr(mask), int(mask.shape[1]), 0)
+
+
+def dsa_tree_workspace_size(layout, batch):
+    return int(library().dsa_tree_workspace_size(ctypes.byref(layout), ctypes.byref(batch)))
+
+
+def alloc_tree_workspace(layout, batch, device="cuda"):
+    """A zeroed workspace for dsa_tree_mla."""
+    n = dsa_tree_workspace_size(layout, batch)
+    if n == 0:
+        raise DSAError(-1, "dsa_tree_workspace_size")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def dsa_tree_mla(layout, batch, tree, q, sm_scale, out, lse=None, ws=None, stream=None):
+    """Dense attention of drafted tokens over the positions each sees (bf16 q [T, 96, 576])."""
+    _check(library().dsa_tree_mla(ctypes.byref(layout), ctypes.byref(batch), ctypes.byref(tree), _ptr(q),
+                                  float(sm_scale), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)),
+           "dsa_tree_mla")
+
+
+def dsa_tree_topk(layout, batch, tree, scores, ld, topk, idx, phys_slots=None, ws=None, stream=None):
+    """dsa_topk over the positions each drafted token sees (workspace as dsa_topk)."""
+    lay = ctypes.byref(layout) if layout is not None else None
+    _check(library().dsa_tree_topk(lay, ctypes.byref(batch), ctypes.byref(tree), _ptr(scores), int(ld), int(topk),
+                                   _ptr(idx), _ptr(phys_slots), _ptr(ws), ws.numel(), _stream(stream)),
+           "dsa_tree_topk")
+
+
+def dsa_tree_commit(layout, batch, base, accept, new_lens=None, ws=None, stream=None):
+    """The accepted drafted slots (accept [B, max_accept], -1 behind the last) become the
+    positions behind the committed ones; new_lens [B] receives the committed lengths."""
+    _int32("base", base, 1), _int32("accept", accept, 2), _int32("new_lens", new_lens, 1)
+    _check(library().dsa_tree_commit(ctypes.byref(layout), ctypes.byref(batch), _ptr(base), _ptr(accept),
+                                     int(accept.shape[1]), _ptr(new_lens), _ptr(ws), ws.numel(), _stream(stream)),
+           "dsa_tree_commit")
+
+
+def make_pages(ref_count, block_table, ctx_lens):
+    """Descriptor of who holds which rows, over device int32 tensors (kept alive by the caller)."""
+    _int32("ref_count", ref_count, 1), _int32("block_table", block_table, 2), _int32("ctx_lens", ctx_lens, 1)
+    if block_table.shape[0] != ctx_lens.shape[0]:
+        raise ValueError("block_table and ctx_lens must have a row and a length for every request")
+    return dsa_pages(_ptr(ref_count), _ptr(block_table), _ptr(ctx_lens), int(ctx_lens.shape[0]),
+                     int(block_table.shape[1]))
+
+
+def dsa_cache_workspace_size(layout, num_reqs):
+    return int(library().dsa_cache_workspace_size(ctypes.byref(layout), int(num_reqs)))
+
+
+def alloc_cache_workspace(layout, num_reqs, device="cuda"):
+    """A zeroed workspace for dsa_tree_commit and the dsa_cache_* calls."""
+    n = dsa_cache_workspace_size(layout, num_reqs)
+    if n == 0:
+        raise DSAError(-1, "dsa_cache_workspace_size")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def dsa_cache_copy(layout, src, dst, count=None, ws=None, stream=None):
+    """Rows src[i] of the pool copied to rows dst[i]; count: a device int32 that says how many."""
+    _int32("src", src, 1), _int32("dst", dst, 1)
+    if src.shape != dst.shape:
+        raise ValueError("src and dst must be of one length")
+    _check(library().dsa_cache_copy(ctypes.byref(layout), _ptr(src), _ptr(dst), int(src.numel()), _ptr(count),
+                                    _ptr(ws), ws.numel(), _stream(stream)), "dsa_cache_copy")
+
+
+def dsa_cache_fork(layout, pages, parent, child, copy_src, copy_dst, ws=None, stream=None):
+    """Requests child[i] become copies of parent[i] that share its full blocks; copy_src and
+    copy_dst receive the rows dsa_cache_copy must copy (-1 where none)."""
+    for name, t in (("parent", parent), ("child", child), ("copy_src", copy_src), ("copy_dst", copy_dst)):
+        if _int32(name, t, 1).numel() != parent.numel():
+            raise ValueError("parent, child, copy_src and copy_dst must be of one length")
+    _check(library().dsa_cache_fork(ctypes.byref(layout), ctypes.byref(pages), _ptr(parent), _ptr(child),
+                                    int(parent.numel()), _ptr(copy_src), _ptr(copy_dst), _ptr(ws), ws.numel(),
+                                    _stream(stream)), "dsa_cache_fork")
+
+
+def dsa_cache_free(layout, pages, reqs, ws=None, stream=None):
+    """Requests' blocks given back: table rows -1, counts down by one, lengths 0."""
+    _int32("reqs", reqs, 1)
+    _check(library().dsa_cache_free(ctypes.byref(layout), ctypes.byref(pages), _ptr(reqs), int(reqs.numel()),
+                                    _ptr(ws), ws.numel(), _stream(stream)), "dsa_cache_free")
+
+
+def dsa_cache_compact(layout, pages, to, copy_src, copy_dst, counts, ws=None, stream=None):
+    """Plans the moves that bring the used rows to the front of the pool: counts and tables
+    afterwards into `to`, (rows used, moves) into counts, the moves into copy_src -> copy_dst
+    ([num_rows // 2], -1 behind the last), for dsa_cache_copy with count=counts[1:]."""
+    _int32("copy_src", copy_src, 1), _int32("copy_dst", copy_dst, 1), _int32("counts", counts, 1)
+    if min(copy_src.numel(), copy_dst.numel()) < max(1, layout.num_rows // 2) or counts.numel() < 2:
+        raise ValueError("copy_src and copy_dst need num_rows // 2 elements, counts two")
+    _check(library().dsa_cache_compact(ctypes.byref(layout), ctypes.byref(pages), ctypes.byref(to), _ptr(copy_src),
+                                       _ptr(copy_dst), _ptr(counts), _ptr(ws), ws.numel(), _stream(stream)),
+           "dsa_cache_compact")
 
 
 def dsa_check(ws, stream=None):

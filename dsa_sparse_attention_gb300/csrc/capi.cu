@@ -11,9 +11,11 @@
 
 #include "../../include/dsa.h"
 
+#include "cache.cuh"
 #include "hostcopy.cuh"
 #include "mla_q.cuh"
 #include "params.cuh"
+#include "tree_mla.cuh"
 
 using namespace dsa;
 
@@ -300,7 +302,65 @@ BatchView batch_view(const dsa_batch* b) {
   return v;
 }
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// A workspace of which only the first `need` bytes are used.
+dsa_status check_ws_bytes(const void* ws, size_t bytes, size_t need) {
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) || bytes < need) return DSA_ERR_WORKSPACE;
+  return DSA_OK;
+}
+
+dsa_status check_tree(const dsa_tree* t, const dsa_batch* b) {
+  if (!t || t->reserved != 0 || t->mask_words < 1 || t->mask_words > DSA_MAX_TREE_WORDS) return DSA_ERR_INVALID_ARG;
+  if (b->num_tokens > 0 && (!t->base || !t->mask)) return DSA_ERR_INVALID_ARG;
+  if (!aligned4(t->base) || !aligned4(t->mask)) return DSA_ERR_INVALID_ARG;
+  return DSA_OK;
+}
+
+TreeView tree_view(const dsa_tree* t) { return TreeView{t->base, t->mask, t->mask_words}; }
+
+// Workspace of dsa_tree_mla.
+struct TreeWs {
+  size_t status = 0, starts = 0, part_o = 0, part_ml = 0, total = 0;
+};
+
+TreeWs plan_tree_ws(const dsa_batch* b) {
+  TreeWs w;
+  const size_t slots = 2 * size_t(num_sms());
+  w.starts = kStatusBytes;
+  w.part_o = align_up(w.starts + (size_t(b->num_tokens) + 1) * sizeof(int64_t));
+  w.part_ml = align_up(w.part_o + slots * kMlaHeads * kVDim * 2);
+  w.total = align_up(w.part_ml + slots * kMlaHeads * sizeof(float2));
+  return w;
+}
+
+// Workspace of the calls on the cache's rows.
+struct CacheWs {
+  size_t rows = 0, plan = 0, marks = 0, total = 0;   // rows: the map of a compaction, or a fork's free rows
+};
+
+CacheWs plan_cache_ws(int64_t num_rows, int32_t num_reqs) {
+  CacheWs w;
+  w.rows = kStatusBytes;
+  w.plan = align_up(w.rows + size_t(num_rows > num_reqs ? num_rows : num_reqs) * 4);
+  w.marks = align_up(w.plan + size_t(num_reqs) * 4);
+  w.total = align_up(w.marks + size_t(num_reqs) * 4);
+  return w;
+}
+
+dsa_status check_pages(const dsa_pages* g) {
+  if (!g || g->num_reqs < 1 || g->bt_stride < 1 || !g->ref_count || !g->block_table || !g->ctx_lens)
+    return DSA_ERR_INVALID_ARG;
+  if (!aligned4(g->ref_count) || !aligned4(g->block_table) || !aligned4(g->ctx_lens)) return DSA_ERR_INVALID_ARG;
+  return DSA_OK;
+}
+
+int log2_of(int v) {
+  int lg = 0;
+  while ((1 << lg) < v) ++lg;
+  return lg;
+}
 
 dsa_status check_ws(void* ws, size_t bytes, const Ws& w) {
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1))) return DSA_ERR_WORKSPACE;
@@ -375,9 +435,10 @@ dsa_status run_indexer(const dsa_kv_layout* l, const dsa_batch* b, const void* q
 // `pre_hist`: histograms the scorer left for these scores, or null.
 dsa_status run_topk(const dsa_kv_layout* l, const dsa_batch* b, const float* scores, int64_t ld, int topk,
                     int32_t* idx, int32_t* phys, void* ws, const Ws& wl, cudaStream_t st, bool chained,
-                    uint32_t* pre_hist = nullptr, bool zeroed = false) {
+                    uint32_t* pre_hist = nullptr, bool zeroed = false, const dsa_tree* tree = nullptr) {
   if (b->num_tokens == 0) return DSA_OK;
   TopkParams p;
+  if (tree) p.tree = tree_view(tree);
   p.b = batch_view(b);
   p.scores = scores;
   p.ld = ld;
@@ -800,6 +861,192 @@ dsa_status dsa_write_latent(const dsa_kv_layout* layout, const dsa_batch* batch,
   p.pool_w = static_cast<uint8_t*>(const_cast<void*>(layout->pool));
   p.status = static_cast<uint32_t*>(workspace);
   return cuda_status(launch_write_latent(p, stream));
+}
+
+size_t dsa_tree_workspace_size(const dsa_kv_layout* layout, const dsa_batch* batch) {
+  if (check_layout(layout, false) != DSA_OK || check_batch(batch, layout->block_size) != DSA_OK) return 0;
+  return plan_tree_ws(batch).total;
+}
+
+dsa_status dsa_tree_mla(const dsa_kv_layout* layout, const dsa_batch* batch, const dsa_tree* tree, const void* q,
+                        float sm_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                        dsa_stream_t stream) {
+  dsa_status s = check_layout(layout);
+  if (s != DSA_OK) return s;
+  if ((s = check_batch(batch, layout->block_size)) != DSA_OK) return s;
+  if ((s = check_tree(tree, batch)) != DSA_OK) return s;
+  if (!std::isfinite(sm_scale)) return DSA_ERR_INVALID_ARG;
+  const int T = batch->num_tokens;
+  if (T > 65535) return DSA_ERR_UNSUPPORTED;   // the merge's launch grid
+  if (T > 0 && (!q || !out || !aligned16(q) || !aligned16(out) || !aligned4(lse)))
+    return DSA_ERR_INVALID_ARG;
+  const TreeWs wl = plan_tree_ws(batch);
+  if ((s = check_ws_bytes(workspace, workspace_bytes, wl.total)) != DSA_OK) return s;
+  if (T == 0) return DSA_OK;
+  TreeMlaParams p;
+  p.pool = pool_view(layout);
+  p.b = batch_view(batch);
+  p.tree = tree_view(tree);
+  p.scale_log2 = sm_scale * 1.4426950408889634f;
+  p.starts = at<int64_t>(workspace, wl.starts);
+  p.max_ctas = num_sms();
+  p.whole = (batch->flags & DSA_BATCH_INVARIANT) ? 1 : 0;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.part_o = at<__half>(workspace, wl.part_o);
+  p.part_ml = at<float2>(workspace, wl.part_ml);
+  p.status = at<uint32_t>(workspace, wl.status);
+  CUtensorMap qmap;
+  if (!make_q_map(&qmap, q, T)) return encode_fail();
+  const cudaError_t e = launch_tree_plan(p.b, p.tree, at<int64_t>(workspace, wl.starts), p.status, stream);
+  if (e != cudaSuccess) return cuda_fail(e);
+  return cuda_status(launch_tree_mla(qmap, p, stream));
+}
+
+dsa_status dsa_tree_topk(const dsa_kv_layout* layout, const dsa_batch* batch, const dsa_tree* tree,
+                         const float* scores, int64_t ld_scores, int32_t topk, int32_t* idx, int32_t* phys_slots,
+                         void* workspace, size_t workspace_bytes, dsa_stream_t stream) {
+  dsa_status s = validate_topk_args(layout, batch, scores, ld_scores, topk, idx, phys_slots);
+  if (s != DSA_OK) return s;
+  if ((s = check_tree(tree, batch)) != DSA_OK) return s;
+  dsa_kv_layout dummy{};
+  dummy.num_rows = 1;
+  dummy.block_size = 64;
+  const Ws wl = plan_ws(layout ? layout : &dummy, batch, topk);
+  if ((s = check_ws(workspace, workspace_bytes, wl)) != DSA_OK) return s;
+  return run_topk(layout, batch, scores, ld_scores, topk, idx, phys_slots, workspace, wl, stream, false, nullptr, false,
+                  tree);
+}
+
+dsa_status dsa_tree_commit(const dsa_kv_layout* layout, const dsa_batch* batch, const int32_t* base,
+                           const int32_t* accept, int32_t max_accept, int32_t* new_lens, void* workspace,
+                           size_t workspace_bytes, dsa_stream_t stream) {
+  dsa_status s = check_layout(layout);
+  if (s != DSA_OK) return s;
+  if (!batch || batch->num_reqs < 1 || !batch->ctx_lens || !batch->block_table || batch->bt_stride < 1 ||
+      batch->max_ctx_len < 1 || batch->max_ctx_len > (int64_t(1) << 30) ||
+      batch->max_ctx_len > int64_t(batch->bt_stride) * layout->block_size)
+    return DSA_ERR_INVALID_ARG;
+  if (!base || max_accept < 0 || (max_accept > 0 && !accept) || !aligned4(base) || !aligned4(accept) ||
+      !aligned4(new_lens))
+    return DSA_ERR_INVALID_ARG;
+  if ((s = check_ws_bytes(workspace, workspace_bytes, kStatusBytes)) != DSA_OK) return s;
+  CommitParams p;
+  p.pool = pool_view(layout);
+  p.pool_w = static_cast<uint8_t*>(const_cast<void*>(layout->pool));
+  p.base = base;
+  p.ctx = batch->ctx_lens;
+  p.bt = batch->block_table;
+  p.bt_stride = batch->bt_stride;
+  p.max_ctx = static_cast<int32_t>(batch->max_ctx_len);
+  p.accept = accept;
+  p.max_accept = max_accept;
+  p.new_lens = new_lens;
+  p.status = static_cast<uint32_t*>(workspace);
+  return cuda_status(launch_tree_commit(p, batch->num_reqs, stream));
+}
+
+size_t dsa_cache_workspace_size(const dsa_kv_layout* layout, int32_t num_reqs) {
+  if (check_layout(layout, false) != DSA_OK || num_reqs < 1) return 0;
+  return plan_cache_ws(layout->num_rows, num_reqs).total;
+}
+
+dsa_status dsa_cache_copy(const dsa_kv_layout* layout, const int32_t* src, const int32_t* dst, int32_t n,
+                          const int32_t* count, void* workspace, size_t workspace_bytes, dsa_stream_t stream) {
+  dsa_status s = check_layout(layout);
+  if (s != DSA_OK) return s;
+  if (n < 0 || (n > 0 && (!src || !dst)) || !aligned4(src) || !aligned4(dst) || !aligned4(count))
+    return DSA_ERR_INVALID_ARG;
+  if ((s = check_ws_bytes(workspace, workspace_bytes, kStatusBytes)) != DSA_OK) return s;
+  CacheCopyParams p;
+  p.pool = static_cast<uint8_t*>(const_cast<void*>(layout->pool));
+  p.num_rows = layout->num_rows;
+  p.row_stride = layout->row_stride_bytes;
+  p.row_bytes = layout->row_stride_bytes;
+  p.src = src;
+  p.dst = dst;
+  p.n = n;
+  p.count = count;
+  p.status = static_cast<uint32_t*>(workspace);
+  return cuda_status(launch_cache_copy(p, num_sms(), stream));
+}
+
+dsa_status dsa_cache_fork(const dsa_kv_layout* layout, const dsa_pages* pages, const int32_t* parent,
+                          const int32_t* child, int32_t n, int32_t* copy_src, int32_t* copy_dst, void* workspace,
+                          size_t workspace_bytes, dsa_stream_t stream) {
+  dsa_status s = check_layout(layout, false);
+  if (s != DSA_OK) return s;
+  if ((s = check_pages(pages)) != DSA_OK) return s;
+  if (n < 0 || n > pages->num_reqs || (n > 0 && (!parent || !child || !copy_src || !copy_dst)) || !aligned4(parent) ||
+      !aligned4(child) || !aligned4(copy_src) || !aligned4(copy_dst))
+    return DSA_ERR_INVALID_ARG;
+  const CacheWs wl = plan_cache_ws(layout->num_rows, pages->num_reqs);
+  if ((s = check_ws_bytes(workspace, workspace_bytes, wl.total)) != DSA_OK) return s;
+  ForkParams p;
+  p.num_rows = layout->num_rows;
+  p.log2_bs = log2_of(layout->block_size);
+  p.ref = pages->ref_count;
+  p.bt = pages->block_table;
+  p.ctx = pages->ctx_lens;
+  p.num_reqs = pages->num_reqs;
+  p.bt_stride = pages->bt_stride;
+  p.parent = parent;
+  p.child = child;
+  p.n = n;
+  p.copy_src = copy_src;
+  p.copy_dst = copy_dst;
+  p.free_list = at<int32_t>(workspace, wl.rows);
+  p.plan = at<int32_t>(workspace, wl.plan);
+  p.marks = at<int32_t>(workspace, wl.marks);
+  p.status = static_cast<uint32_t*>(workspace);
+  return cuda_status(launch_cache_fork(p, stream));
+}
+
+dsa_status dsa_cache_free(const dsa_kv_layout* layout, const dsa_pages* pages, const int32_t* reqs, int32_t n,
+                          void* workspace, size_t workspace_bytes, dsa_stream_t stream) {
+  dsa_status s = check_layout(layout, false);
+  if (s != DSA_OK) return s;
+  if ((s = check_pages(pages)) != DSA_OK) return s;
+  if (n < 0 || (n > 0 && !reqs) || !aligned4(reqs)) return DSA_ERR_INVALID_ARG;
+  if ((s = check_ws_bytes(workspace, workspace_bytes, kStatusBytes)) != DSA_OK) return s;
+  FreeParams p;
+  p.num_rows = layout->num_rows;
+  p.ref = pages->ref_count;
+  p.bt = pages->block_table;
+  p.ctx = pages->ctx_lens;
+  p.num_reqs = pages->num_reqs;
+  p.bt_stride = pages->bt_stride;
+  p.reqs = reqs;
+  p.n = n;
+  p.status = static_cast<uint32_t*>(workspace);
+  return cuda_status(launch_cache_free(p, stream));
+}
+
+dsa_status dsa_cache_compact(const dsa_kv_layout* layout, const dsa_pages* from, const dsa_pages* to,
+                             int32_t* copy_src, int32_t* copy_dst, int32_t* counts, void* workspace,
+                             size_t workspace_bytes, dsa_stream_t stream) {
+  dsa_status s = check_layout(layout, false);
+  if (s != DSA_OK) return s;
+  if ((s = check_pages(from)) != DSA_OK || (s = check_pages(to)) != DSA_OK) return s;
+  if (from->num_reqs != to->num_reqs || from->bt_stride != to->bt_stride || !copy_src || !copy_dst || !counts ||
+      !aligned4(copy_src) || !aligned4(copy_dst) || !aligned4(counts))
+    return DSA_ERR_INVALID_ARG;
+  const CacheWs wl = plan_cache_ws(layout->num_rows, from->num_reqs);
+  if ((s = check_ws_bytes(workspace, workspace_bytes, wl.total)) != DSA_OK) return s;
+  CompactParams p;
+  p.num_rows = layout->num_rows;
+  p.ref = from->ref_count;
+  p.bt = from->block_table;
+  p.to_ref = to->ref_count;
+  p.to_bt = to->block_table;
+  p.num_reqs = from->num_reqs;
+  p.bt_stride = from->bt_stride;
+  p.copy_src = copy_src;
+  p.copy_dst = copy_dst;
+  p.counts = counts;
+  p.remap = at<int32_t>(workspace, wl.rows);
+  p.status = static_cast<uint32_t*>(workspace);
+  return cuda_status(launch_cache_compact(p, num_sms(), stream));
 }
 
 dsa_status dsa_check(void* workspace, size_t workspace_bytes, dsa_stream_t stream) {

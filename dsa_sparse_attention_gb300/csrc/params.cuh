@@ -49,6 +49,7 @@ struct TopkParams {
   uint32_t* status;
   uint32_t* pre_hist;   // [T, 2048] or null: top-digit counts left by the scorer (a hint, verified
                         // before use); the cluster top-k zeroes each row after reading it
+  TreeView tree = {};   // mask != null: only positions the token sees in its tree take part
 };
 
 struct MlaParams {

@@ -1,0 +1,82 @@
+// tree_mla.cuh — parameters, work partition and launchers of the dense attention of
+// drafted tokens (tree_mla.cu).
+#pragma once
+#include "params.cuh"
+
+namespace dsa {
+
+// The work is a list of key tiles (128 positions) in token order: token t's tiles are
+// [starts[t], starts[t + 1]), W = starts[T] in all.  CTA c of G takes the contiguous
+// share [W c / G, W (c + 1) / G); the part of a token inside a share is a segment.  A
+// segment that holds all of its token writes the output; any other writes a partial
+// to the CTA's slot 2c (its first segment) or 2c + 1 (its last), and the combine
+// merges a token's partials in tile order.  With `whole` (DSA_BATCH_INVARIANT) CTA c
+// takes the tokens c, c + G, ... whole.
+struct TreeMlaParams {
+  PoolView pool;
+  BatchView b;
+  TreeView tree;
+  float scale_log2;          // sm_scale * log2(e)
+  const int64_t* starts;     // [T + 1]
+  int max_ctas;              // G = min(max_ctas, W)
+  int whole;
+  __nv_bfloat16* out;        // [T, 96, 512]
+  float* lse;                // [T, 96] or null
+  __half* part_o;            // [2 max_ctas, 96, 512], each normalised by its own sum
+  float2* part_ml;           // [2 max_ctas, 96]: (max in log2 units, sum)
+  uint32_t* status;
+};
+
+// One segment: key tiles [j0, j1) of token t.
+struct Segment {
+  int t, j0, j1;
+  int slot;   // partial slot, or -1 when the segment is the whole token
+};
+
+// A CTA's segments in order.  Every role of the CTA walks its own copy.
+struct SegmentWalk {
+  const int64_t* starts;
+  int T, G, whole, cta;
+  int64_t g0, g, g1;    // share, and the next tile
+  int t;
+  __device__ bool next(Segment& s) {
+    if (whole) {
+      while (t < T) {
+        const int64_t u0 = __ldg(starts + t), u1 = __ldg(starts + t + 1);
+        const int tt = t;
+        t += G;
+        if (u1 > u0) {
+          s = Segment{tt, 0, static_cast<int>(u1 - u0), -1};
+          return true;
+        }
+      }
+      return false;
+    }
+    if (g >= g1) return false;
+    int64_t u0 = __ldg(starts + t), u1 = __ldg(starts + t + 1);
+    while (u1 <= g) {   // padding tokens hold no tiles
+      ++t;
+      u0 = u1;
+      u1 = __ldg(starts + t + 1);
+    }
+    const int64_t e = u1 < g1 ? u1 : g1;
+    s.t = t;
+    s.j0 = static_cast<int>(g - u0);
+    s.j1 = static_cast<int>(e - u0);
+    s.slot = (g == u0 && e == u1) ? -1 : 2 * cta + (g == g0 ? 0 : 1);
+    g = e;
+    return true;
+  }
+};
+
+__host__ __device__ inline int64_t share_begin(int64_t W, int G, int c) { return W * c / G; }
+// The CTA whose share holds tile u.
+__host__ __device__ inline int share_of(int64_t W, int G, int64_t u) {
+  return static_cast<int>(((u + 1) * G - 1) / W);
+}
+
+cudaError_t launch_tree_plan(const BatchView& b, const TreeView& tree, int64_t* starts, uint32_t* status,
+                             cudaStream_t st);
+cudaError_t launch_tree_mla(const CUtensorMap& qmap, const TreeMlaParams& p, cudaStream_t st);
+
+}  // namespace dsa

@@ -364,6 +364,150 @@ dsa_status dsa_write_latent(const dsa_kv_layout *layout, const dsa_batch *batch,
                             void *workspace, size_t workspace_bytes, dsa_stream_t stream);
 
 /*
+ * Trees of drafted tokens, and the rows of the cache (the vLLM post's "MTP decode"
+ * verifies a chain of drafted tokens; a tree of them, and the calls that keep, fork,
+ * free and move what the cache holds, extend the same cache and batch).
+ *
+ * A request's drafted tokens take the cache slots behind its committed context:
+ * drafted slot i sits at position base + i, its index key and latent written there
+ * like any new token's, parents before children.  ctx_lens counts them.  Query token
+ * t sees position s of its request r = q_req[t] when s <= q_pos[t] and
+ *   s < base[r]   or   bit (s - base[r]) of mask row t is set
+ * (bit i % 32 of word i / 32; positions behind the last bit are not seen; a token
+ * that is to see itself has its own bit set).  base[r] = ctx_lens[r] makes a token
+ * causal whatever its mask.  A token with q_req[t] < 0 is padding: its output rows
+ * are left as they are.  A token that sees nothing has output 0 and lse -inf, and
+ * no selection.  What lies in the cache at positions nobody sees never reaches a
+ * result, NaN codes included.
+ */
+typedef struct {
+  const int32_t *base;    /* device [B]: committed tokens of each request, 0..ctx_lens[r] */
+  const uint32_t *mask;   /* device [T, mask_words] */
+  int32_t mask_words;     /* 1..DSA_MAX_TREE_WORDS */
+  int32_t reserved;       /* must be 0 */
+} dsa_tree;
+#define DSA_MAX_TREE_WORDS 32
+
+/* Bytes of workspace dsa_tree_mla needs (256-byte aligned, zeroed once); 0 on invalid arguments. */
+size_t dsa_tree_workspace_size(const dsa_kv_layout *layout, const dsa_batch *batch);
+
+/*
+ * Dense MLA attention of drafted tokens: for each token t and head h < 96, over the
+ * visible positions V_t of its request,
+ *   logit(s) = sm_scale * q[t,h,:] . c(s)          (all 576 dims)
+ *   out[t,h,:] = sum_{s in V_t} softmax(logit)(s) * c(s)[0:512]
+ *   lse[t,h]  = ln sum_{s in V_t} exp(logit(s))
+ *  q  : device bf16 [T, 96, 576], finite;  out: device bf16 [T, 96, 512];  both 16-byte aligned
+ *  lse: device fp32 [T, 96] or NULL
+ * Work is split over the positions and merged by log-sum-exp.  The split follows the
+ * batch; with DSA_BATCH_INVARIANT it does not (every token's positions are then summed
+ * in one order, whatever else the batch holds).  A block id outside the pool is recorded
+ * in the status word and never dereferenced; the results of its request's tokens are
+ * then unspecified.
+ */
+dsa_status dsa_tree_mla(const dsa_kv_layout *layout, const dsa_batch *batch, const dsa_tree *tree, const void *q,
+                        float sm_scale, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                        dsa_stream_t stream);
+
+/*
+ * dsa_topk over the visible positions of each token: the topk largest of
+ * scores[t, s], s in V_t, equal scores by lower position; ascending, then -1.
+ * Scores at other positions are not compared (they may be anything).  Arguments and
+ * workspace (dsa_workspace_size) as dsa_topk.  dsa_indexer_score before and
+ * dsa_sparse_mla after it make the sparse step of a tree.
+ */
+dsa_status dsa_tree_topk(const dsa_kv_layout *layout, const dsa_batch *batch, const dsa_tree *tree,
+                         const float *scores, int64_t ld_scores, int32_t topk, int32_t *idx, int32_t *phys_slots,
+                         void *workspace, size_t workspace_bytes, dsa_stream_t stream);
+
+/*
+ * Keeps the accepted path of each request's tree: the records (index key, key scale,
+ * latent) of drafted slots accept[r, 0..m-1] become those of positions base[r] + 0 ..
+ * base[r] + m - 1, as if all were read before any is written, and new_lens[r] =
+ * base[r] + m.  m is the number of entries before the row's first negative one (at
+ * most max_accept); they must ascend and lie below ctx_lens[r] - base[r].  A row that
+ * breaks this, or a block id outside the pool, is recorded in the status word and the
+ * request is left as it was (new_lens[r] too).
+ *  batch   : only num_reqs, ctx_lens, block_table, bt_stride and max_ctx_len are read
+ *  base    : device [B];  accept: device int32 [B, max_accept];  new_lens: device [B] or
+ *            NULL (it may be the ctx_lens array itself)
+ *  workspace: only its status word is used (>= 256 bytes)
+ * The pool is written.  One call moves one layer's records.
+ */
+dsa_status dsa_tree_commit(const dsa_kv_layout *layout, const dsa_batch *batch, const int32_t *base,
+                           const int32_t *accept, int32_t max_accept, int32_t *new_lens, void *workspace,
+                           size_t workspace_bytes, dsa_stream_t stream);
+
+/*
+ * Who holds which rows of the pool.  ref_count[i] is the number of block-table entries
+ * that hold row i; a row with count 0 is free.  A request's blocks are the entries >= 0
+ * of its block-table row; every entry that holds no block is -1.  All device memory.
+ * The calls below change these arrays on `stream`; calls that share them are issued in
+ * order on one stream.
+ */
+typedef struct {
+  int32_t *ref_count;     /* [num_rows of the layout] */
+  int32_t *block_table;   /* [num_reqs, bt_stride] */
+  int32_t *ctx_lens;      /* [num_reqs] */
+  int32_t num_reqs;
+  int32_t bt_stride;
+} dsa_pages;
+
+/* Bytes of workspace the calls below need (256-byte aligned, zeroed once); 0 on invalid arguments. */
+size_t dsa_cache_workspace_size(const dsa_kv_layout *layout, int32_t num_reqs);
+
+/*
+ * Copies whole rows of the pool: row dst[i] <- row src[i] for i < n (i < min(n, *count)
+ * with count given, a device int32).  Entries with both ids negative are skipped; any
+ * other id outside the pool is recorded in the status word and its pair skipped.  A
+ * source may repeat; a destination may not, and may be no pair's source (but its own).
+ * One call per pool: with a pool per layer, the pairs that fork and compact write serve
+ * every layer.
+ */
+dsa_status dsa_cache_copy(const dsa_kv_layout *layout, const int32_t *src, const int32_t *dst, int32_t n,
+                          const int32_t *count, void *workspace, size_t workspace_bytes, dsa_stream_t stream);
+
+/*
+ * Forks requests: for i < n, request child[i] becomes a copy of request parent[i].  The
+ * child's table holds the parent's full blocks (their counts grow by one) and, where
+ * ctx_lens[parent] is not a multiple of the block size, a free row for the last, partial
+ * block: the lowest-numbered free rows, in the order of i.  The child's ctx_lens is its
+ * parent's.  copy_src[i], copy_dst[i] name the rows whose content dsa_cache_copy must
+ * copy then (-1, -1 where none).  parent[i] < 0 skips i.  A parent may repeat.  A child
+ * must hold nothing (ctx_lens 0; free it first), appear once and be no parent; a fork
+ * that breaks this, names a request outside 0..num_reqs-1, or finds no free row, is
+ * recorded in the status word and left out, the others are made.
+ *  layout: only num_rows and block_size are read (pool may be NULL);  0 <= n <= num_reqs
+ */
+dsa_status dsa_cache_fork(const dsa_kv_layout *layout, const dsa_pages *pages, const int32_t *parent,
+                          const int32_t *child, int32_t n, int32_t *copy_src, int32_t *copy_dst, void *workspace,
+                          size_t workspace_bytes, dsa_stream_t stream);
+
+/*
+ * Frees requests: every entry of their table rows becomes -1 and the counts of the rows
+ * they held shrink by one; ctx_lens becomes 0.  A negative id is skipped, one that is
+ * named twice is freed once; an id >= num_reqs, an entry outside the pool and a count
+ * that is already 0 are recorded in the status word.
+ */
+dsa_status dsa_cache_free(const dsa_kv_layout *layout, const dsa_pages *pages, const int32_t *reqs, int32_t n,
+                          void *workspace, size_t workspace_bytes, dsa_stream_t stream);
+
+/*
+ * Compacts a pool: with L rows in use (count > 0), the i-th used row at or behind L moves
+ * to the i-th free row before L, in ascending order, so that rows 0..L-1 are in use and
+ * the rest of the pool is free.  Writes the counts and tables that hold then into `to`
+ * (which may be `from` itself or other arrays of the same shape; ctx_lens is not
+ * touched), counts[0] = L, counts[1] = the number of moves m, and the moves as pairs
+ * copy_src[i] -> copy_dst[i], -1 for i >= m.  dsa_cache_copy (count = counts + 1) must
+ * move the rows of every pool before the new tables are used.
+ *  copy_src, copy_dst: device int32 [num_rows / 2] (at least one element)
+ * A table entry >= 0 that names no used row is recorded in the status word and becomes -1.
+ */
+dsa_status dsa_cache_compact(const dsa_kv_layout *layout, const dsa_pages *from, const dsa_pages *to,
+                             int32_t *copy_src, int32_t *copy_dst, int32_t *counts, void *workspace,
+                             size_t workspace_bytes, dsa_stream_t stream);
+
+/*
  * Synchronises `stream`, reads the workspace status word written by earlier
  * calls, clears it, and returns DSA_OK, DSA_ERR_TIMEOUT or DSA_ERR_DEVICE_CHECK.
  */
