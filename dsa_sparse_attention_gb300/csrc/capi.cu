@@ -229,6 +229,21 @@ bool make_q_map(CUtensorMap* m, const void* q, int T) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The FP8 latents of every page, {576 dims, block slots, rows}: a box is `width` dims
+// (128 or 64, swizzled over as many bytes) of up to 128 positions of one page.
+bool make_latent_map(CUtensorMap* m, const dsa_kv_layout* l, int width) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {kLatDim, cuuint64_t(l->block_size), cuuint64_t(l->num_rows)};
+  cuuint64_t strides[2] = {kLatDim, cuuint64_t(l->row_stride_bytes)};
+  cuuint32_t box[3] = {cuuint32_t(width), cuuint32_t(l->block_size < kSelTile ? l->block_size : kSelTile), 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  void* base = const_cast<uint8_t*>(static_cast<const uint8_t*>(l->pool)) + l->lat_page_offset;
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             width == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // The FP8 attention's split partials [rows = T * nsplit * 512 dims][96 heads] fp16,
 // box 32 heads x 256 rows, 64-byte swizzle (tensor stores from shared memory).
 bool make_part_map(CUtensorMap* m, void* part_o, int64_t rows) {
@@ -322,14 +337,15 @@ TreeView tree_view(const dsa_tree* t) { return TreeView{t->base, t->mask, t->mas
 
 // Workspace of dsa_tree_mla.
 struct TreeWs {
-  size_t status = 0, starts = 0, part_o = 0, part_ml = 0, total = 0;
+  size_t status = 0, starts = 0, q_terms = 0, part_o = 0, part_ml = 0, total = 0;
 };
 
-TreeWs plan_tree_ws(const dsa_batch* b) {
+TreeWs plan_tree_ws(const dsa_kv_layout* l, const dsa_batch* b) {
   TreeWs w;
   const size_t slots = 2 * size_t(num_sms());
   w.starts = kStatusBytes;
-  w.part_o = align_up(w.starts + (size_t(b->num_tokens) + 1) * sizeof(int64_t));
+  w.q_terms = align_up(w.starts + (size_t(b->num_tokens) + 1) * sizeof(int64_t));
+  w.part_o = align_up(w.q_terms + (l->lat_fmt == DSA_LAT_FP8 ? size_t(b->num_tokens) * kQTokenBytes : 0));
   w.part_ml = align_up(w.part_o + slots * kMlaHeads * kVDim * 2);
   w.total = align_up(w.part_ml + slots * kMlaHeads * sizeof(float2));
   return w;
@@ -865,7 +881,7 @@ dsa_status dsa_write_latent(const dsa_kv_layout* layout, const dsa_batch* batch,
 
 size_t dsa_tree_workspace_size(const dsa_kv_layout* layout, const dsa_batch* batch) {
   if (check_layout(layout, false) != DSA_OK || check_batch(batch, layout->block_size) != DSA_OK) return 0;
-  return plan_tree_ws(batch).total;
+  return plan_tree_ws(layout, batch).total;
 }
 
 dsa_status dsa_tree_mla(const dsa_kv_layout* layout, const dsa_batch* batch, const dsa_tree* tree, const void* q,
@@ -880,7 +896,7 @@ dsa_status dsa_tree_mla(const dsa_kv_layout* layout, const dsa_batch* batch, con
   if (T > 65535) return DSA_ERR_UNSUPPORTED;   // the merge's launch grid
   if (T > 0 && (!q || !out || !aligned16(q) || !aligned16(out) || !aligned4(lse)))
     return DSA_ERR_INVALID_ARG;
-  const TreeWs wl = plan_tree_ws(batch);
+  const TreeWs wl = plan_tree_ws(layout, batch);
   if ((s = check_ws_bytes(workspace, workspace_bytes, wl.total)) != DSA_OK) return s;
   if (T == 0) return DSA_OK;
   TreeMlaParams p;
@@ -896,11 +912,16 @@ dsa_status dsa_tree_mla(const dsa_kv_layout* layout, const dsa_batch* batch, con
   p.part_o = at<__half>(workspace, wl.part_o);
   p.part_ml = at<float2>(workspace, wl.part_ml);
   p.status = at<uint32_t>(workspace, wl.status);
-  CUtensorMap qmap;
-  if (!make_q_map(&qmap, q, T)) return encode_fail();
-  const cudaError_t e = launch_tree_plan(p.b, p.tree, at<int64_t>(workspace, wl.starts), p.status, stream);
+  const bool fp8 = layout->lat_fmt == DSA_LAT_FP8;
+  uint8_t* terms = fp8 ? at<uint8_t>(workspace, wl.q_terms) : nullptr;
+  p.q_terms = terms;
+  CUtensorMap amap, bmap;
+  if (fp8 ? !(make_latent_map(&amap, layout, 128) && make_latent_map(&bmap, layout, 64)) : !make_q_map(&amap, q, T))
+    return encode_fail();
+  const cudaError_t e = launch_tree_prep(p.b, p.tree, static_cast<const __nv_bfloat16*>(q), terms,
+                                         at<int64_t>(workspace, wl.starts), p.status, stream);
   if (e != cudaSuccess) return cuda_fail(e);
-  return cuda_status(launch_tree_mla(qmap, p, stream));
+  return cuda_status(fp8 ? launch_tree_mla_fp8(amap, bmap, p, stream) : launch_tree_mla_nvfp4(amap, p, stream));
 }
 
 dsa_status dsa_tree_topk(const dsa_kv_layout* layout, const dsa_batch* batch, const dsa_tree* tree,

@@ -14,20 +14,31 @@
 #include <cuda_fp16.h>
 
 #include "mla_conv.cuh"
+#include "mla_q.cuh"
 #include "tree_mla.cuh"
 
 namespace dsa {
 
-// ------------------------------------------------------------------------- plan
+// --------------------------------------------------------- plan and query terms
+//
+// Block 0 sums the tokens' tiles; the other blocks (FP8 latents) split the queries
+// into the attention's e4m3 terms, one warp per head, three blocks of 32 heads a token.
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPrepThreads = 1024;
 
-__global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(BatchView b, TreeView tree, int64_t* starts,
-                                                                 uint32_t* status) {
-  __shared__ int64_t wsum[kPlanThreads / 32];
+__global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(BatchView b, TreeView tree, const __nv_bfloat16* q,
+                                                                 uint8_t* terms, int64_t* starts, uint32_t* status) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (blockIdx.x > 0) {
+    const int t = (blockIdx.x - 1) / 3, h = (blockIdx.x - 1) % 3 * 32 + warp;
+    uint8_t* tok = terms + static_cast<int64_t>(t) * kQTokenBytes;
+    q_head_to_terms(q + static_cast<int64_t>(t) * kMlaHeads * kLatDim, h, tok,
+                    reinterpret_cast<int32_t*>(tok + kQTermBytes));
+    return;
+  }
+  __shared__ int64_t wsum[kPrepThreads / 32];
   int64_t base = 0;
-  for (int t0 = 0; t0 < b.T; t0 += kPlanThreads) {
+  for (int t0 = 0; t0 < b.T; t0 += kPrepThreads) {
     const int t = t0 + threadIdx.x;
     int64_t v = 0;
     if (t < b.T) {
@@ -43,7 +54,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(BatchView b, Tr
     if (lane == 31) wsum[warp] = x;
     __syncthreads();
     int64_t before = 0, total = 0;
-    for (int w = 0; w < kPlanThreads / 32; ++w) {
+    for (int w = 0; w < kPrepThreads / 32; ++w) {
       if (w < warp) before += wsum[w];
       total += wsum[w];
     }
@@ -54,9 +65,10 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(BatchView b, Tr
   if (threadIdx.x == 0) starts[b.T] = base;
 }
 
-cudaError_t launch_tree_plan(const BatchView& b, const TreeView& tree, int64_t* starts, uint32_t* status,
-                             cudaStream_t st) {
-  return launch_ex(tree_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, false, 0u, b, tree, starts, status);
+cudaError_t launch_tree_prep(const BatchView& b, const TreeView& tree, const __nv_bfloat16* q, uint8_t* terms,
+                             int64_t* starts, uint32_t* status, cudaStream_t st) {
+  return launch_ex(tree_prep_kernel, dim3(terms ? 1 + 3 * b.T : 1), dim3(kPrepThreads), 0, st, false, 0u, b, tree, q,
+                   terms, starts, status);
 }
 
 // The first token of share [g0, ...): every thread of the CTA searches.
@@ -158,12 +170,10 @@ __device__ __forceinline__ void store_heads(const TreeMlaParams& p, const Segmen
   }
 }
 
-template <int LATF>
 __global__ void __launch_bounds__(tconv::THREADS, 1)
-    tree_mla_conv_kernel(const __grid_constant__ CUtensorMap qmap, TreeMlaParams p) {
+    tree_mla_nvfp4_kernel(const __grid_constant__ CUtensorMap qmap, TreeMlaParams p) {
   using namespace tconv;
-  constexpr bool NV = LATF == 1;
-  constexpr int ROWB = NV ? 352 : kLatDim;
+  constexpr int ROWB = 352;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024_tree(smem_raw);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BARS);
@@ -339,7 +349,7 @@ __global__ void __launch_bounds__(tconv::THREADS, 1)
           if (ok && lane == 0) mbar_arrive(rows_ready);
           LatPiece cb[4];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) cb[u] = load_piece<NV>(src, u, hf);
+          for (int u = 0; u < 4; ++u) cb[u] = load_piece<true>(src, u, hf);
 #pragma unroll 1
           for (int kb = 0; kb < QCHUNKS; kb += 4) {
 #pragma unroll
@@ -354,7 +364,7 @@ __global__ void __launch_bounds__(tconv::THREADS, 1)
                 for (int q2 = 0; q2 < 2; ++q2) {
                   const int q4 = 2 * hf + q2;
                   uint32_t o[8];
-                  piece_to_bf16<NV>(cb[u], q2, o);
+                  piece_to_bf16<true>(cb[u], q2, o);
                   sts128(dst + sw128_off(row & 7, 2 * q4), o);
                   sts128(dst + sw128_off(row & 7, 2 * q4 + 1), o + 4);
                 }
@@ -363,13 +373,13 @@ __global__ void __launch_bounds__(tconv::THREADS, 1)
               __syncwarp();
               if (ok && lane == 0) mbar_arrive(&ring_full[slot]);
               ++fc;
-              if (kc + 4 < QCHUNKS) cb[u] = load_piece<NV>(src, kc + 4, hf);
+              if (kc + 4 < QCHUNKS) cb[u] = load_piece<true>(src, kc + 4, hf);
             }
           }
           // V half-blocks: the warps of rows 0..63 fill the even ring fills, the others the odd ones
 #pragma unroll 1
           for (int v = 0; v < 4; ++v) {
-            LatPiece c0 = load_piece<NV>(src, 2 * v, hf), c1 = load_piece<NV>(src, 2 * v + 1, hf);
+            LatPiece c0 = load_piece<true>(src, 2 * v, hf), c1 = load_piece<true>(src, 2 * v + 1, hf);
             const int myfc = fc + 2 * v + vg;
             const int slot = myfc % RSLOTS;
             if (myfc >= RSLOTS) ok = warp_wait(&ring_empty[slot], ((myfc / RSLOTS) - 1) & 1, ab, ok);
@@ -381,7 +391,7 @@ __global__ void __launch_bounds__(tconv::THREADS, 1)
                 for (int q2 = 0; q2 < 2; ++q2) {
                   const int q4 = 2 * hf + q2;
                   uint32_t o[8];
-                  piece_to_f16<NV>(a ? c1 : c0, q2, o);
+                  piece_to_f16<true>(a ? c1 : c0, q2, o);
                   sts128(dst + a * 8192 + sw128_off(tl & 7, 2 * q4), o);
                   sts128(dst + a * 8192 + sw128_off(tl & 7, 2 * q4 + 1), o + 4);
                 }
@@ -550,6 +560,407 @@ __global__ void __launch_bounds__(tconv::THREADS, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
+// ------------------------------------------------- attention with FP8 latents
+//
+// No conversion: e4m3 is the tensor core's operand type, and one copy of the tile in
+// shared memory, brought by TMA, is the B operand of the scores (K-major) and the A
+// operand of the values (MN-major).
+//   S[head, token] = sum_k q_term[head, k] . c[token, k]    M=128 (heads 0..95), N=128, K=1152
+//   O^T[dim, head] += V^T[dim, token] . P_term^T[token, head]   M=128 (x4 dim blocks), N=96, K=3 x 128
+// q arrives as two e4m3 terms (mla_q.cuh, exact).  Heads on TMEM lanes keep the softmax
+// inside a thread.  P is rounded once to 9 significant bits (half the error of a bf16 P)
+// and split exactly into three e5m2 terms of 3 bits: e5m2 is the upper byte of an fp16,
+// so the split is two subtractions and byte picks, and its range (2^-16 .. 2^15 with the
+// reference at 2^11) keeps weights down to 2^-27 of the largest, which a million
+// positions beside one heavy one need; e4m3 terms would lose those below 2^-18.
+// O is normalised by the sum of the rounded weights, the lse uses the unrounded sum.
+// TMEM: S in columns [0, 128), O^T blocks at 128 + 96 v: all 512.
+// Shared memory holds the query terms (108 KB), one tile (72 KB: four 16 KB slices of
+// 128 dims and an 8 KB slice of the last 64) and P (36 KB).  A slice is refilled as soon
+// as the PV block that reads it is done, with the next tile prefetched into L2 meanwhile.
+// Roles: warp 3 issues MMAs; warp 7 loads; the 12 warps of lane quarters 0..2 run the
+// softmax, four per head with 32 tokens each; warps 11 and 15 serve lane quarter 3 of O.
+namespace t8 {
+constexpr int THREADS = 512;
+constexpr int QCHUNK = 96 * 128;
+constexpr int SLICE = 128 * 128;
+constexpr int OFF_Q = 0;
+constexpr int OFF_LAT = kQTermBytes;              // four slices
+constexpr int OFF_TAIL = OFF_LAT + 4 * SLICE;     // dims 512..575: [128 tokens x 64 B], 64-byte swizzle
+constexpr int OFF_P = OFF_TAIL + 128 * 64;
+constexpr int P_TERM = 96 * 128;
+constexpr int OFF_QEXP = OFF_P + 3 * P_TERM;      // [96] int
+constexpr int OFF_REDM = OFF_QEXP + 96 * 4;   // [4][96] float
+constexpr int OFF_REDL = OFF_REDM + 4 * 96 * 4;   // [4][96] float2: sums of the rounded and the unrounded weights
+constexpr int OFF_ALPHA = OFF_REDL + 4 * 96 * 8;  // [96] float
+constexpr int OFF_INV = OFF_ALPHA + 96 * 4;       // [96] float
+constexpr int OFF_BARS = OFF_INV + 96 * 4;
+constexpr int N_BARS = 20;
+constexpr int OFF_MISC = OFF_BARS + N_BARS * 8;
+constexpr int SMEM_BYTES = OFF_MISC + 64 + 1024;
+constexpr int MMA_WARP = 3, LOAD_WARP = 7, AUX_WARP0 = 11;   // and 15
+constexpr int MATH = 448;                         // threads of the softmax and auxiliary warps
+constexpr int S_COL = 0;
+constexpr int O_COL = 128;
+constexpr float TAU = 4.0f;                       // log2 headroom before the reference moves
+constexpr float SHIFT = 11.0f;                    // weights are scaled by 2^11: at most 2^15, below e5m2's 57344
+static_assert(OFF_LAT % 1024 == 0 && OFF_TAIL % 1024 == 0 && OFF_P % 1024 == 0, "align");
+static_assert(OFF_ALPHA % 16 == 0 && OFF_INV % 16 == 0 && OFF_QEXP % 16 == 0 && OFF_BARS % 8 == 0, "align");
+static_assert(SMEM_BYTES <= 232448, "smem");
+}  // namespace t8
+
+// Position s0 + lane of the request seen by the token, as a ballot.
+__device__ __forceinline__ uint32_t seen_word(const TreeView& tr, const uint32_t* mrow, int base, int pos, int s) {
+  return __ballot_sync(0xffffffffu, s <= pos && tree_sees(mrow, tr.words, base, s));
+}
+
+__global__ void __launch_bounds__(t8::THREADS, 1)
+    tree_mla_fp8_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ CUtensorMap tmap,
+                        TreeMlaParams p) {
+  using namespace t8;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024_tree(smem_raw);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BARS);
+  uint64_t* lat_full = bars + 0;    // [4]
+  uint64_t* lat_empty = bars + 4;   // [4]
+  uint64_t* tail_full = bars + 8;
+  uint64_t* tail_empty = bars + 9;
+  uint64_t* q_full = bars + 10;
+  uint64_t* q_done = bars + 11;     // a segment's QKs are done
+  uint64_t* s_full = bars + 12;     // a tile's QK (and the PV before it) is done
+  uint64_t* p_full = bars + 13;
+  uint64_t* o_done = bars + 14;     // a segment's last PV is done
+  uint64_t* drain = bars + 15;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
+  int* abortf = reinterpret_cast<int*>(smem + OFF_MISC + 8);
+  int* first_sh = reinterpret_cast<int*>(smem + OFF_MISC + 16);
+  float* red_m = reinterpret_cast<float*>(smem + OFF_REDM);
+  float2* red_l = reinterpret_cast<float2*>(smem + OFF_REDL);
+  float* alpha_sh = reinterpret_cast<float*>(smem + OFF_ALPHA);
+  float* inv_sh = reinterpret_cast<float*>(smem + OFF_INV);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 13; ++i) mbar_init(&bars[i], 1);
+    mbar_init(p_full, MATH / 32);
+    mbar_init(o_done, 1);
+    mbar_init(drain, 1);
+    *abortf = 0;
+    *first_sh = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&lmap);
+    prefetch_tensormap(&tmap);
+  }
+  if (warp == 0) tmem_alloc(tslot, 512);
+  grid_dep_wait();   // the plan and the query terms
+  grid_dep_launch();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  SegmentWalk walk = make_walk(p, first_sh);
+  const uint32_t tmem = *tslot;
+  const Abort ab{abortf, p.status};
+  Segment s;
+
+  if (warp == LOAD_WARP) {
+    // ---------------------------------------------------------------- loads
+    const int lg = p.pool.log2_bs;
+    const int box = min(p.pool.bs, kSelTile);     // positions of one copy
+    const int nbox = kSelTile / box;              // copies (lanes) per slice
+    bool ok = true;
+    int it = 0, q_issued = -1;   // q_issued: parity of the last query copy
+    for (int seg = 0; ok && walk.next(s); ++seg) {
+      int req, pos, base;
+      load_tree_token(p.b, p.tree, s.t, p.status, req, pos, base);
+      const int32_t* btrow = p.b.bt + static_cast<int64_t>(req) * p.b.bt_stride;
+      // this lane's page of tile j: pool row (num_rows, which reads as zeros, for a bad id)
+      auto page = [&](int j) {
+        const int s0 = j * kSelTile + lane * box;
+        if (lane >= nbox || s0 > pos) return -1;
+        const int32_t id = __ldg(btrow + (s0 >> lg));
+        if (id >= 0 && id < p.pool.num_rows) return static_cast<int>(id);
+        atomicOr(p.status, DEV_BAD_BLOCK);
+        return static_cast<int>(p.pool.num_rows);
+      };
+      auto prefetch = [&](int j, int row) {   // the page's latents of tile j into L2
+        if (row >= 0 && row < p.pool.num_rows)
+          bulk_prefetch_l2(p.pool.pool + static_cast<int64_t>(row) * p.pool.row_stride + p.pool.lat_off +
+                               static_cast<int64_t>((j * kSelTile + lane * box) & (p.pool.bs - 1)) * kLatDim,
+                           box * kLatDim);
+      };
+      int row = page(s.j0);
+      prefetch(s.j0, row);
+      if (seg > 0) ok = warp_wait(q_done, (seg - 1) & 1, ab, ok);
+      if (!ok) break;
+      q_issued = seg & 1;
+      if (lane == 0) {
+        const uint8_t* src = p.q_terms + static_cast<int64_t>(s.t) * kQTokenBytes;
+        mbar_arrive_expect_tx(q_full, kQTokenBytes);
+        for (int c = 0; c < kQChunks; ++c) bulk_load(smem + OFF_Q + c * QCHUNK, src + c * QCHUNK, QCHUNK, q_full);
+        bulk_load(smem + OFF_QEXP, src + kQTermBytes, kMlaHeads * 4, q_full);
+      }
+      for (int j = s.j0; ok && j < s.j1; ++j, ++it) {
+        const int c1 = (j * kSelTile + lane * box) & (p.pool.bs - 1);
+        const int n = __popc(__ballot_sync(0xffffffffu, row >= 0));
+        const int next = j + 1 < s.j1 ? page(j + 1) : -1;
+        if (it > 0) ok = warp_wait(tail_empty, (it - 1) & 1, ab, ok);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(tail_full, n * box * 64);
+        __syncwarp();
+        if (row >= 0) tma_load_3d(smem + OFF_TAIL + lane * box * 64, &tmap, tail_full, 512, c1, row);
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+          if (it > 0) ok = warp_wait(&lat_empty[k], (it - 1) & 1, ab, ok);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&lat_full[k], n * box * 128);
+          __syncwarp();
+          if (row >= 0) tma_load_3d(smem + OFF_LAT + k * SLICE + lane * box * 128, &lmap, &lat_full[k], 128 * k, c1, row);
+        }
+        row = next;
+        prefetch(j + 1, row);
+      }
+    }
+    // after a failed wait: no copy into shared memory outlives the CTA (a barrier whose copy
+    // was not issued in this round keeps its earlier phase; the wait is bounded)
+    if (!ok && lane == 0) {
+      if (q_issued >= 0) drain_wait(q_full, q_issued);
+      drain_wait(tail_full, it & 1);
+      for (int k = 0; k < 4; ++k) drain_wait(&lat_full[k], it & 1);
+    }
+  } else if (warp == MMA_WARP) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      const uint32_t idesc_qk = make_idesc(0, 0, false, false, 128, 128);
+      const uint32_t idesc_pv = make_idesc(0, 1, true, false, 128, kMlaHeads);
+      const uint64_t dq = make_sdesc_sw128(smem_u32(smem + OFF_Q), 16, 1024);        // query terms, K-major
+      const uint64_t dl = make_sdesc_sw128(smem_u32(smem + OFF_LAT), 16, 1024);      // latents, K-major (QK)
+      const uint64_t dt = make_sdesc_sw64(smem_u32(smem + OFF_TAIL), 16, 512);       // their last 64 dims
+      const uint64_t dv = make_sdesc_sw128(smem_u32(smem + OFF_LAT), SLICE, 1024);   // latents, MN-major (PV)
+      const uint64_t dp = make_sdesc_sw128(smem_u32(smem + OFF_P), 16, 1024);        // P terms, K-major
+      bool ok = true;
+      int it = 0;
+      for (int seg = 0; ok && walk.next(s); ++seg) {
+        ok = mbar_wait(q_full, seg & 1, ab);
+        for (int j = s.j0; ok && j < s.j1; ++j, ++it) {
+          if (!(ok = mbar_wait_inline(tail_full, it & 1, ab))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)   // chunk 4 of the query: hi | lo of dims 512..575
+            mma_f8f6f4(tmem + S_COL, dq + ((4 * QCHUNK + 32 * kk) >> 4), dt + ((32 * (kk & 1)) >> 4), idesc_qk,
+                       kk ? 1u : 0u);
+          tc_commit(tail_empty);
+#pragma unroll 1
+          for (int k = 0; k < 4; ++k) {
+            if (!(ok = mbar_wait_inline(&lat_full[k], it & 1, ab))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int term = 0; term < 2; ++term)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_f8f6f4(tmem + S_COL, dq + (((k + 5 * term) * QCHUNK + 32 * kk) >> 4),
+                           dl + ((k * SLICE + 32 * kk) >> 4), idesc_qk, 1u);
+          }
+          if (!ok) break;
+          tc_commit(s_full);
+          if (!(ok = mbar_wait_inline(p_full, it & 1, ab))) break;
+          // the query may go once every softmax warp is past its own wait for it, too
+          if (j == s.j1 - 1) tc_commit(q_done);
+          tc_fence_after();
+          const uint32_t acc = j > s.j0 ? 1u : 0u;
+#pragma unroll 1
+          for (int v = 0; v < 4; ++v) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint32_t d = tmem + O_COL + 96 * v;
+              const uint64_t a = dv + ((v * SLICE + kk * 4096) >> 4), b = dp + ((32 * kk) >> 4);
+              mma_f8f6f4_keep_a<KeepA::kFill>(d, a, b, idesc_pv, kk ? 1u : acc);
+              mma_f8f6f4_keep_a<KeepA::kUse>(d, a, b + (P_TERM >> 4), idesc_pv, 1u);
+              mma_f8f6f4_keep_a<KeepA::kLast>(d, a, b + (2 * P_TERM >> 4), idesc_pv, 1u);
+            }
+            tc_commit(&lat_empty[v]);
+          }
+          if (j == s.j1 - 1) tc_commit(o_done);
+        }
+      }
+      if (!ok) {
+        tc_commit(drain);
+        drain_wait(drain, 0);
+      }
+    }
+  } else {
+    // ------------------------- softmax (quarters 0..2), and the epilogue of all quarters
+    const int quarter = warp & 3, u = warp >> 2;   // heads 32 quarter .., tokens 32 u .. of a tile
+    const bool soft = quarter < 3;
+    const int h = quarter * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const int v0 = soft ? u : (warp == AUX_WARP0 ? 0 : 2), v1 = soft ? u + 1 : v0 + 2;   // dim blocks of O
+    bool ok = true;
+    int it = 0;
+    for (int seg = 0; walk.next(s); ++seg) {
+      int req, pos, base;
+      load_tree_token(p.b, p.tree, s.t, p.status, req, pos, base);
+      const uint32_t* mrow = p.tree.mask + static_cast<int64_t>(s.t) * p.tree.words;
+      const int plain = min(base, pos + 1);   // positions below are all seen
+      ok = warp_wait(q_full, seg & 1, ab, ok);
+      const int qe = soft ? *reinterpret_cast<const int*>(smem + OFF_QEXP + 4 * h) : 0;
+      const float c = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - qe) << 23);
+      float m_ref = -INFINITY, l_r = 0.f, l_x = 0.f;
+      for (int j = s.j0; j < s.j1; ++j, ++it) {
+        ok = warp_wait(s_full, it & 1, ab, ok);
+        tc_fence_after();
+        uint32_t rr[32];
+        float* x = reinterpret_cast<float*>(rr);
+        float mx = -INFINITY;
+        uint32_t seen = 0xFFFFFFFFu;
+        if (soft) {
+          DSA_TMEM_LD32(tmem + S_COL + 32 * u + lane_off, rr);
+          const int s0 = j * kSelTile + 32 * u;
+          if (s0 + 32 > plain) seen = seen_word(p.tree, mrow, base, pos, s0 + lane);
+          tmem_wait_ld();
+          if (seen == 0xFFFFFFFFu) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              x[i] = __uint_as_float(rr[i]) * c;
+              mx = fmaxf(mx, x[i]);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              x[i] = (seen >> i) & 1u ? __uint_as_float(rr[i]) * c : -INFINITY;
+              mx = fmaxf(mx, x[i]);
+            }
+          }
+        }
+        if (named_bar_any(1, MATH, mx > m_ref + TAU)) {
+          // some head's reference moves: all four threads of a head agree on it
+          float alpha = 1.f;
+          if (soft) red_m[u * kMlaHeads + h] = mx;
+          named_bar_sync(2, MATH);
+          if (soft) {
+            const float m = fmaxf(fmaxf(red_m[h], red_m[kMlaHeads + h]),
+                                  fmaxf(red_m[2 * kMlaHeads + h], red_m[3 * kMlaHeads + h]));
+            if (m > m_ref + TAU) {
+              alpha = exp2f(m_ref - m);
+              m_ref = m;
+            }
+            l_r *= alpha;
+            l_x *= alpha;
+            if (u == 0) alpha_sh[h] = alpha;
+          }
+          named_bar_sync(2, MATH);
+          if (j > s.j0 && ok) {
+#pragma unroll 1
+            for (int v = v0; v < v1; ++v) {
+#pragma unroll 1
+              for (int cc = 0; cc < 6; ++cc) {   // 16 heads at a time: the logits stay in registers
+                uint32_t o[16];
+                const uint32_t ta = tmem + O_COL + 96 * v + 16 * cc + lane_off;
+                DSA_TMEM_LD16(ta, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha_sh[16 * cc + i]);
+                DSA_TMEM_ST16(ta, o);
+              }
+            }
+            tmem_wait_st();
+          }
+        }
+        if (soft) {
+          const float shift = m_ref == -INFINITY ? 0.f : SHIFT - m_ref;
+          uint32_t t0[8], t1[8], t2[8];   // the three e5m2 terms of 32 weights, 4 per word
+#pragma unroll
+          for (int w = 0; w < 8; ++w) {
+            uint32_t hw[2], r1[2], lo[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float p0 = ex2_fast(x[4 * w + 2 * e] + shift), p1 = ex2_fast(x[4 * w + 2 * e + 1] + shift);
+              l_x += p0 + p1;
+              // 9 significant bits, to nearest (positive values: carry into the exponent is right)
+              const float a0 = __uint_as_float((__float_as_uint(p0) + 0x4000u) & 0xFFFF8000u);
+              const float a1 = __uint_as_float((__float_as_uint(p1) + 0x4000u) & 0xFFFF8000u);
+              l_r += a0 + a1;
+              const __half2 ph = __floats2half2_rn(a0, a1);
+              hw[e] = *reinterpret_cast<const uint32_t*>(&ph);
+              const uint32_t hi = hw[e] & 0xFF00FF00u;
+              const __half2 d1 = __hsub2(ph, *reinterpret_cast<const __half2*>(&hi));
+              r1[e] = *reinterpret_cast<const uint32_t*>(&d1);
+              const uint32_t mid = r1[e] & 0xFF00FF00u;
+              const __half2 d2 = __hsub2(d1, *reinterpret_cast<const __half2*>(&mid));
+              lo[e] = static_cast<uint32_t>(
+                  __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&d2), __NV_SATFINITE, __NV_E5M2));
+            }
+            t0[w] = __byte_perm(hw[0], hw[1], 0x7531);
+            t1[w] = __byte_perm(r1[0], r1[1], 0x7531);
+            t2[w] = lo[0] | (lo[1] << 16);
+          }
+          if (ok) {
+            uint8_t* prow = smem + OFF_P + (h >> 3) * 1024 + (h & 7) * 128;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int ch = ((2 * u + i) ^ (h & 7)) << 4;
+              sts128(prow + ch, t0 + 4 * i);
+              sts128(prow + P_TERM + ch, t1 + 4 * i);
+              sts128(prow + 2 * P_TERM + ch, t2 + 4 * i);
+            }
+            // Latents nobody sees are zeroed before the values read them (a weight of zero
+            // does not cancel a NaN): one row is 32 lanes x 16 bytes, three warps share the rows.
+            if (seen != 0xFFFFFFFFu) {
+              uint32_t gone = ~seen;
+              for (int n = 0; gone; ++n) {
+                const int r = 32 * u + __ffs(gone) - 1;
+                gone &= gone - 1;
+                if (n % 3 == quarter)
+                  *reinterpret_cast<uint4*>(smem + OFF_LAT + (lane >> 3) * SLICE + r * 128 + (lane & 7) * 16) =
+                      make_uint4(0u, 0u, 0u, 0u);
+              }
+            }
+            fence_proxy_async_smem();
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(p_full);
+      }
+      // ---- the segment's result: TMEM (thread = dim) -> global
+      if (soft) red_l[u * kMlaHeads + h] = make_float2(l_r, l_x);
+      named_bar_sync(2, MATH);
+      if (soft && u == 0) {
+        float lr = 0.f, lx = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          lr += red_l[i * kMlaHeads + h].x;
+          lx += red_l[i * kMlaHeads + h].y;
+        }
+        inv_sh[h] = lr == 0.f ? 0.f : (lx == lx ? 1.f / lr : lx);   // nothing seen: output 0; a NaN logit: NaN
+        const float m = m_ref == -INFINITY ? 0.f : m_ref - SHIFT;
+        if (ok) {
+          if (s.slot >= 0) p.part_ml[static_cast<int64_t>(s.slot) * kMlaHeads + h] = make_float2(m, lx);
+          else if (p.lse) p.lse[static_cast<int64_t>(s.t) * kMlaHeads + h] = (m + log2f(lx)) * 0.69314718055994531f;
+        }
+      }
+      named_bar_sync(2, MATH);
+      ok = warp_wait(o_done, seg & 1, ab, ok);
+      tc_fence_after();
+      if (ok) {
+#pragma unroll 1
+        for (int v = v0; v < v1; ++v) {
+#pragma unroll 1
+          for (int cc = 0; cc < 3; ++cc) {
+            uint32_t rr[32];
+            DSA_TMEM_LD32(tmem + O_COL + 96 * v + 32 * cc + lane_off, rr);
+            tmem_wait_ld();
+            store_heads(p, s, rr, inv_sh, 32 * cc, v * 128 + quarter * 32 + lane);
+          }
+        }
+      }
+      tc_fence_before();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
 // Merge of a token's partials: out = sum_j w_j o_j, w_j = l_j 2^(m_j - M) / sum.
 // Grid (96 heads, T); a block's 256 threads are 64 groups of 8 dims times 4 interleaved
 // quarters of the partials.  Tokens with one segment have their output already.
@@ -612,19 +1023,26 @@ __global__ void __launch_bounds__(kTreeCombThreads) tree_combine_kernel(TreeMlaP
   if (d8 == 0 && p.lse) p.lse[static_cast<int64_t>(t) * kMlaHeads + h] = (M + log2f(Ls)) * 0.69314718055994531f;
 }
 
-template <int LATF>
-static cudaError_t launch_conv(const CUtensorMap& qmap, const TreeMlaParams& p, cudaStream_t st) {
-  cudaError_t e = set_func_attr_once(reinterpret_cast<const void*>(tree_mla_conv_kernel<LATF>),
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, tconv::SMEM_BYTES);
-  if (e != cudaSuccess) return e;
-  return launch_ex(tree_mla_conv_kernel<LATF>, dim3(p.max_ctas), dim3(tconv::THREADS), tconv::SMEM_BYTES, st, true, 0u,
-                   qmap, p);
+static cudaError_t launch_combine(const TreeMlaParams& p, cudaStream_t st) {
+  if (p.whole) return cudaSuccess;
+  return launch_ex(tree_combine_kernel, dim3(kMlaHeads, p.b.T), dim3(kTreeCombThreads), 0, st, true, 0u, p);
 }
 
-cudaError_t launch_tree_mla(const CUtensorMap& qmap, const TreeMlaParams& p, cudaStream_t st) {
-  cudaError_t e = p.pool.lat_fmt == 1 ? launch_conv<1>(qmap, p, st) : launch_conv<0>(qmap, p, st);
-  if (e != cudaSuccess || p.whole) return e;
-  return launch_ex(tree_combine_kernel, dim3(kMlaHeads, p.b.T), dim3(kTreeCombThreads), 0, st, true, 0u, p);
+cudaError_t launch_tree_mla_fp8(const CUtensorMap& lmap, const CUtensorMap& tmap, const TreeMlaParams& p,
+                                cudaStream_t st) {
+  cudaError_t e = set_func_attr_once(reinterpret_cast<const void*>(tree_mla_fp8_kernel),
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, t8::SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  e = launch_ex(tree_mla_fp8_kernel, dim3(p.max_ctas), dim3(t8::THREADS), t8::SMEM_BYTES, st, true, 0u, lmap, tmap, p);
+  return e != cudaSuccess ? e : launch_combine(p, st);
+}
+
+cudaError_t launch_tree_mla_nvfp4(const CUtensorMap& qmap, const TreeMlaParams& p, cudaStream_t st) {
+  cudaError_t e = set_func_attr_once(reinterpret_cast<const void*>(tree_mla_nvfp4_kernel),
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, tconv::SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  e = launch_ex(tree_mla_nvfp4_kernel, dim3(p.max_ctas), dim3(tconv::THREADS), tconv::SMEM_BYTES, st, true, 0u, qmap, p);
+  return e != cudaSuccess ? e : launch_combine(p, st);
 }
 
 }  // namespace dsa
