@@ -23,6 +23,16 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// True in one lane of the (converged) warp.  A role that issues tensor-core work runs its
+// loop in the whole warp and issues under this predicate: descriptors then stay in
+// uniform registers, where a loop inside a one-lane branch moves each of them there per
+// instruction and issues slower than the tensor core runs.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 // ------------------------------------------------- clusters and launch chaining
 
 __device__ __forceinline__ uint32_t cluster_rank() {

@@ -729,30 +729,34 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
     }
   } else if (warp == MMA_WARP) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      const uint32_t idesc_qk = make_idesc(0, 0, false, false, 128, 128);
-      const uint32_t idesc_pv = make_idesc(0, 1, true, false, 128, kMlaHeads);
-      const uint64_t dq = make_sdesc_sw128(smem_u32(smem + OFF_Q), 16, 1024);        // query terms, K-major
-      const uint64_t dl = make_sdesc_sw128(smem_u32(smem + OFF_LAT), 16, 1024);      // latents, K-major (QK)
-      const uint64_t dt = make_sdesc_sw64(smem_u32(smem + OFF_TAIL), 16, 512);       // their last 64 dims
-      const uint64_t dv = make_sdesc_sw128(smem_u32(smem + OFF_LAT), SLICE, 1024);   // latents, MN-major (PV)
-      const uint64_t dp = make_sdesc_sw128(smem_u32(smem + OFF_P), 16, 1024);        // P terms, K-major
-      bool ok = true;
-      int it = 0;
-      for (int seg = 0; ok && walk.next(s); ++seg) {
-        ok = mbar_wait(q_full, seg & 1, ab);
-        for (int j = s.j0; ok && j < s.j1; ++j, ++it) {
-          if (!(ok = mbar_wait_inline(tail_full, it & 1, ab))) break;
-          tc_fence_after();
+    const bool leader = elect_one();
+    const uint32_t idesc_qk = make_idesc(0, 0, false, false, 128, 128);
+    const uint32_t idesc_pv = make_idesc(0, 1, true, false, 128, kMlaHeads);
+    const uint64_t dq = make_sdesc_sw128(smem_u32(smem + OFF_Q), 16, 1024);        // query terms, K-major
+    const uint64_t dl = make_sdesc_sw128(smem_u32(smem + OFF_LAT), 16, 1024);      // latents, K-major (QK)
+    const uint64_t dt = make_sdesc_sw64(smem_u32(smem + OFF_TAIL), 16, 512);       // their last 64 dims
+    const uint64_t dv = make_sdesc_sw128(smem_u32(smem + OFF_LAT), SLICE, 1024);   // latents, MN-major (PV)
+    const uint64_t dp = make_sdesc_sw128(smem_u32(smem + OFF_P), 16, 1024);        // P terms, K-major
+    bool ok = true;
+    int it = 0;
+    for (int seg = 0; ok && walk.next(s); ++seg) {
+      ok = warp_wait(q_full, seg & 1, ab, ok);
+      for (int j = s.j0; ok && j < s.j1; ++j, ++it) {
+        if (!(ok = warp_wait(tail_full, it & 1, ab, ok))) break;
+        tc_fence_after();
+        if (leader) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)   // chunk 4 of the query: hi | lo of dims 512..575
             mma_f8f6f4(tmem + S_COL, dq + ((4 * QCHUNK + 32 * kk) >> 4), dt + ((32 * (kk & 1)) >> 4), idesc_qk,
                        kk ? 1u : 0u);
           tc_commit(tail_empty);
-#pragma unroll 1
-          for (int k = 0; k < 4; ++k) {
-            if (!(ok = mbar_wait_inline(&lat_full[k], it & 1, ab))) break;
-            tc_fence_after();
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          ok = warp_wait(&lat_full[k], it & 1, ab, ok);
+          tc_fence_after();
+          if (leader && ok) {
 #pragma unroll
             for (int term = 0; term < 2; ++term)
 #pragma unroll
@@ -760,14 +764,19 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
                 mma_f8f6f4(tmem + S_COL, dq + (((k + 5 * term) * QCHUNK + 32 * kk) >> 4),
                            dl + ((k * SLICE + 32 * kk) >> 4), idesc_qk, 1u);
           }
-          if (!ok) break;
-          tc_commit(s_full);
-          if (!(ok = mbar_wait_inline(p_full, it & 1, ab))) break;
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (leader) tc_commit(s_full);
+        __syncwarp();
+        if (!(ok = warp_wait(p_full, it & 1, ab, ok))) break;
+        tc_fence_after();
+        const uint32_t acc = j > s.j0 ? 1u : 0u;
+        const bool last = j == s.j1 - 1;
+        if (leader) {
           // the query may go once every softmax warp is past its own wait for it, too
-          if (j == s.j1 - 1) tc_commit(q_done);
-          tc_fence_after();
-          const uint32_t acc = j > s.j0 ? 1u : 0u;
-#pragma unroll 1
+          if (last) tc_commit(q_done);
+#pragma unroll
           for (int v = 0; v < 4; ++v) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
@@ -779,14 +788,16 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
             }
             tc_commit(&lat_empty[v]);
           }
-          if (j == s.j1 - 1) tc_commit(o_done);
+          if (last) tc_commit(o_done);
         }
-      }
-      if (!ok) {
-        tc_commit(drain);
-        drain_wait(drain, 0);
+        __syncwarp();
       }
     }
+    if (!ok && leader) {
+      tc_commit(drain);
+      drain_wait(drain, 0);
+    }
+    __syncwarp();
   } else {
     // ------------------------- softmax (quarters 0..2), and the epilogue of all quarters
     const int quarter = warp & 3, u = warp >> 2;   // heads 32 quarter .., tokens 32 u .. of a tile
