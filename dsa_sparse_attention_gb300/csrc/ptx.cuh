@@ -399,6 +399,11 @@ __device__ __forceinline__ uint64_t make_sdesc_sw64(uint32_t saddr, uint32_t lbo
   return (make_sdesc_sw128(saddr, lbo, sbo) & ~(static_cast<uint64_t>(7) << 61)) | (static_cast<uint64_t>(4) << 61);
 }
 
+// And with a 32-byte swizzle.
+__device__ __forceinline__ uint64_t make_sdesc_sw32(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return (make_sdesc_sw128(saddr, lbo, sbo) & ~(static_cast<uint64_t>(7) << 61)) | (static_cast<uint64_t>(6) << 61);
+}
+
 // 32 lanes x 32 consecutive 32-bit columns: thread i of the warp gets lane
 // (warp's lane quarter * 32 + i), columns [col, col + 32).
 #define DSA_TMEM_LD32(taddr, r)                                                                                     \

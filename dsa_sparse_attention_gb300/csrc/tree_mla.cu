@@ -563,55 +563,104 @@ __global__ void __launch_bounds__(tconv::THREADS, 1)
 // ------------------------------------------------- attention with FP8 latents
 //
 // No conversion: e4m3 is the tensor core's operand type, and one copy of the tile in
-// shared memory, brought by TMA, is the B operand of the scores (K-major) and the A
-// operand of the values (MN-major).
-//   S[head, token] = sum_k q_term[head, k] . c[token, k]    M=128 (heads 0..95), N=128, K=1152
+// shared memory, brought by TMA, is the A operand of both products (K-major for the
+// scores, MN-major for the values).
+//   S^T[token, head] = sum_k c[token, k] . q_term[head, k]      M=128, N=96, K=1152
 //   O^T[dim, head] += V^T[dim, token] . P_term^T[token, head]   M=128 (x4 dim blocks), N=96, K=3 x 128
-// q arrives as two e4m3 terms (mla_q.cuh, exact).  Heads on TMEM lanes keep the softmax
-// inside a thread.  P is rounded once to 9 significant bits (half the error of a bf16 P)
-// and split exactly into three e5m2 terms of 3 bits: e5m2 is the upper byte of an fp16,
-// so the split is two subtractions and byte picks, and its range (2^-16 .. 2^15 with the
+// q arrives as two e4m3 terms (mla_q.cuh, exact).  P is the sum of three e5m2 terms,
+// each the nearest to what the ones before it left: off by at most 2^-9 of it, half the
+// error of a bf16 P.  e5m2 is the upper byte of an fp16, so a term is an addition, a mask
+// and a subtraction on two weights at a time, and its range (2^-16 .. 2^15 with the
 // reference at 2^11) keeps weights down to 2^-27 of the largest, which a million
-// positions beside one heavy one need; e4m3 terms would lose those below 2^-18.
-// O is normalised by the sum of the rounded weights, the lse uses the unrounded sum.
-// TMEM: S in columns [0, 128), O^T blocks at 128 + 96 v: all 512.
+// positions beside one heavy one need; e4m3 terms would lose those below 2^-18.  The sum
+// of the weights is of the unrounded ones, in fp32.
+// Tokens on TMEM lanes use all four lane quarters and waste no rows (96 heads are N);
+// the price, maxima across lanes, is not paid per tile: weights are taken against a
+// reference per head, and only when some logit exceeds it by 2^4 do the warps reduce the
+// tile's maxima, move the reference and rescale O.
+// Every run of MMAs on one A operand (both query terms; all three terms of P) keeps A in
+// the tensor core's buffer: 49 cycles an MMA instead of 57 (measured; 128 bytes of shared
+// memory a cycle bound it otherwise).
+// TMEM: S^T in columns [0, 96), O^T blocks at 128 + 96 v: 480 of 512.
 // Shared memory holds the query terms (108 KB), one tile (72 KB: four 16 KB slices of
 // 128 dims and an 8 KB slice of the last 64) and P (36 KB).  A slice is refilled as soon
 // as the PV block that reads it is done, with the next tile prefetched into L2 meanwhile.
-// Roles: warp 3 issues MMAs; warp 7 loads; the 12 warps of lane quarters 0..2 run the
-// softmax, four per head with 32 tokens each; warps 11 and 15 serve lane quarter 3 of O.
+// Roles: warps 0..11 run the softmax and the epilogue (lane quarter w % 4, heads
+// 32 (w / 4) ..); warp 12 issues MMAs; warp 13 loads.
 namespace t8 {
-constexpr int THREADS = 512;
+constexpr int THREADS = 448;
 constexpr int QCHUNK = 96 * 128;
 constexpr int SLICE = 128 * 128;
 constexpr int OFF_Q = 0;
 constexpr int OFF_LAT = kQTermBytes;              // four slices
 constexpr int OFF_TAIL = OFF_LAT + 4 * SLICE;     // dims 512..575: [128 tokens x 64 B], 64-byte swizzle
-constexpr int OFF_P = OFF_TAIL + 128 * 64;
+constexpr int OFF_P = OFF_TAIL + 128 * 64;        // per term: three [128 tokens x 32 heads] blocks, 32-byte swizzle
 constexpr int P_TERM = 96 * 128;
+constexpr int P_BLOCK = 128 * 32;
 constexpr int OFF_QEXP = OFF_P + 3 * P_TERM;      // [96] int
-constexpr int OFF_REDM = OFF_QEXP + 96 * 4;   // [4][96] float
-constexpr int OFF_REDL = OFF_REDM + 4 * 96 * 4;   // [4][96] float2: sums of the rounded and the unrounded weights
-constexpr int OFF_ALPHA = OFF_REDL + 4 * 96 * 8;  // [96] float
+constexpr int OFF_REDM = OFF_QEXP + 96 * 4;       // [4][96] float: maxima, then sums, per lane quarter
+constexpr int OFF_C = OFF_REDM + 4 * 96 * 4;      // [96] float: logit scale of each head, log2 units
+constexpr int OFF_SH = OFF_C + 96 * 4;            // [96] float: SHIFT - reference (+inf before the first tile)
+constexpr int OFF_ALPHA = OFF_SH + 96 * 4;        // [96] float
 constexpr int OFF_INV = OFF_ALPHA + 96 * 4;       // [96] float
 constexpr int OFF_BARS = OFF_INV + 96 * 4;
 constexpr int N_BARS = 20;
 constexpr int OFF_MISC = OFF_BARS + N_BARS * 8;
 constexpr int SMEM_BYTES = OFF_MISC + 64 + 1024;
-constexpr int MMA_WARP = 3, LOAD_WARP = 7, AUX_WARP0 = 11;   // and 15
-constexpr int MATH = 448;                         // threads of the softmax and auxiliary warps
+constexpr int MATH_WARPS = 12;
+constexpr int MATH = MATH_WARPS * 32;
+constexpr int MMA_WARP = 12, LOAD_WARP = 13;
 constexpr int S_COL = 0;
 constexpr int O_COL = 128;
 constexpr float TAU = 4.0f;                       // log2 headroom before the reference moves
 constexpr float SHIFT = 11.0f;                    // weights are scaled by 2^11: at most 2^15, below e5m2's 57344
 static_assert(OFF_LAT % 1024 == 0 && OFF_TAIL % 1024 == 0 && OFF_P % 1024 == 0, "align");
-static_assert(OFF_ALPHA % 16 == 0 && OFF_INV % 16 == 0 && OFF_QEXP % 16 == 0 && OFF_BARS % 8 == 0, "align");
-static_assert(SMEM_BYTES <= 232448, "smem");
+static_assert(OFF_C % 16 == 0 && OFF_SH % 16 == 0 && OFF_ALPHA % 16 == 0 && OFF_INV % 16 == 0 && OFF_QEXP % 16 == 0,
+              "vectors are read 16 bytes at a time");
+static_assert(OFF_BARS % 8 == 0 && SMEM_BYTES <= 232448, "smem");
 }  // namespace t8
 
-// Position s0 + lane of the request seen by the token, as a ballot.
-__device__ __forceinline__ uint32_t seen_word(const TreeView& tr, const uint32_t* mrow, int base, int pos, int s) {
-  return __ballot_sync(0xffffffffu, s <= pos && tree_sees(mrow, tr.words, base, s));
+// One term of two fp16 values, both to nearest: the upper byte of each half of the result
+// is the e5m2 value (fp16 and e5m2 share sign and exponent, so adding half a step of the
+// upper byte rounds the magnitude; ties go up).  `rest` is what the term leaves, exactly.
+__device__ __forceinline__ uint32_t e5m2_term(uint32_t v, uint32_t& rest) {
+  const uint32_t t = v + 0x00800080u;
+  const uint32_t hi = t & 0xFF00FF00u;
+  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&hi));
+  rest = *reinterpret_cast<const uint32_t*>(&d);
+  return t;
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)),
+        "l"(reinterpret_cast<const uint64_t&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
+  return d;
+}
+
+// Sums of 32 values per lane over the lanes: lane i gets the sum of every lane's v[i].
+__device__ __forceinline__ float transpose_sum(float (&v)[32]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const bool up = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const float keep = up ? v[i + o] : v[i], send = up ? v[i] : v[i + o];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+    }
+  }
+  return v[0];
 }
 
 __global__ void __launch_bounds__(t8::THREADS, 1)
@@ -634,15 +683,16 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
   int* abortf = reinterpret_cast<int*>(smem + OFF_MISC + 8);
   int* first_sh = reinterpret_cast<int*>(smem + OFF_MISC + 16);
-  float* red_m = reinterpret_cast<float*>(smem + OFF_REDM);
-  float2* red_l = reinterpret_cast<float2*>(smem + OFF_REDL);
+  float* red = reinterpret_cast<float*>(smem + OFF_REDM);
+  float* c_sh = reinterpret_cast<float*>(smem + OFF_C);
+  float* sh_sh = reinterpret_cast<float*>(smem + OFF_SH);
   float* alpha_sh = reinterpret_cast<float*>(smem + OFF_ALPHA);
   float* inv_sh = reinterpret_cast<float*>(smem + OFF_INV);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 13; ++i) mbar_init(&bars[i], 1);
-    mbar_init(p_full, MATH / 32);
+    mbar_init(p_full, MATH_WARPS);
     mbar_init(o_done, 1);
     mbar_init(drain, 1);
     *abortf = 0;
@@ -730,13 +780,13 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
   } else if (warp == MMA_WARP) {
     // ------------------------------------------------------------ MMA issuer
     const bool leader = elect_one();
-    const uint32_t idesc_qk = make_idesc(0, 0, false, false, 128, 128);
-    const uint32_t idesc_pv = make_idesc(0, 1, true, false, 128, kMlaHeads);
+    const uint32_t idesc_qk = make_idesc(0, 0, false, false, 128, kMlaHeads);
+    const uint32_t idesc_pv = make_idesc(0, 1, true, true, 128, kMlaHeads);
     const uint64_t dq = make_sdesc_sw128(smem_u32(smem + OFF_Q), 16, 1024);        // query terms, K-major
     const uint64_t dl = make_sdesc_sw128(smem_u32(smem + OFF_LAT), 16, 1024);      // latents, K-major (QK)
     const uint64_t dt = make_sdesc_sw64(smem_u32(smem + OFF_TAIL), 16, 512);       // their last 64 dims
     const uint64_t dv = make_sdesc_sw128(smem_u32(smem + OFF_LAT), SLICE, 1024);   // latents, MN-major (PV)
-    const uint64_t dp = make_sdesc_sw128(smem_u32(smem + OFF_P), 16, 1024);        // P terms, K-major
+    const uint64_t dp = make_sdesc_sw32(smem_u32(smem + OFF_P), P_BLOCK, 256);     // P terms, MN-major
     bool ok = true;
     int it = 0;
     for (int seg = 0; ok && walk.next(s); ++seg) {
@@ -746,9 +796,11 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
         tc_fence_after();
         if (leader) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)   // chunk 4 of the query: hi | lo of dims 512..575
-            mma_f8f6f4(tmem + S_COL, dq + ((4 * QCHUNK + 32 * kk) >> 4), dt + ((32 * (kk & 1)) >> 4), idesc_qk,
-                       kk ? 1u : 0u);
+          for (int kk = 0; kk < 2; ++kk) {   // chunk 4 of the query: hi | lo of dims 512..575
+            const uint64_t a = dt + ((32 * kk) >> 4), b = dq + ((4 * QCHUNK + 32 * kk) >> 4);
+            mma_f8f6f4_keep_a<KeepA::kFill>(tmem + S_COL, a, b, idesc_qk, kk ? 1u : 0u);
+            mma_f8f6f4_keep_a<KeepA::kLast>(tmem + S_COL, a, b + (64 >> 4), idesc_qk, 1u);
+          }
           tc_commit(tail_empty);
         }
         __syncwarp();
@@ -758,11 +810,11 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
           tc_fence_after();
           if (leader && ok) {
 #pragma unroll
-            for (int term = 0; term < 2; ++term)
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_f8f6f4(tmem + S_COL, dq + (((k + 5 * term) * QCHUNK + 32 * kk) >> 4),
-                           dl + ((k * SLICE + 32 * kk) >> 4), idesc_qk, 1u);
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint64_t a = dl + ((k * SLICE + 32 * kk) >> 4), b = dq + ((k * QCHUNK + 32 * kk) >> 4);
+              mma_f8f6f4_keep_a<KeepA::kFill>(tmem + S_COL, a, b, idesc_qk, 1u);
+              mma_f8f6f4_keep_a<KeepA::kLast>(tmem + S_COL, a, b + (5 * QCHUNK >> 4), idesc_qk, 1u);
+            }
           }
           __syncwarp();
         }
@@ -781,7 +833,7 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
               const uint32_t d = tmem + O_COL + 96 * v;
-              const uint64_t a = dv + ((v * SLICE + kk * 4096) >> 4), b = dp + ((32 * kk) >> 4);
+              const uint64_t a = dv + ((v * SLICE + kk * 4096) >> 4), b = dp + ((1024 * kk) >> 4);
               mma_f8f6f4_keep_a<KeepA::kFill>(d, a, b, idesc_pv, kk ? 1u : acc);
               mma_f8f6f4_keep_a<KeepA::kUse>(d, a, b + (P_TERM >> 4), idesc_pv, 1u);
               mma_f8f6f4_keep_a<KeepA::kLast>(d, a, b + (2 * P_TERM >> 4), idesc_pv, 1u);
@@ -799,12 +851,14 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
     }
     __syncwarp();
   } else {
-    // ------------------------- softmax (quarters 0..2), and the epilogue of all quarters
-    const int quarter = warp & 3, u = warp >> 2;   // heads 32 quarter .., tokens 32 u .. of a tile
-    const bool soft = quarter < 3;
-    const int h = quarter * 32 + lane;
+    // ------------------------------------------------ softmax and epilogue (0..11)
+    const int quarter = warp & 3, g = warp >> 2;   // tokens 32 quarter .. of a tile, heads 32 g ..
+    const int r = quarter * 32 + lane;             // this thread's token in the tile
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const int v0 = soft ? u : (warp == AUX_WARP0 ? 0 : 2), v1 = soft ? u + 1 : v0 + 2;   // dim blocks of O
+    const float4* c4 = reinterpret_cast<const float4*>(c_sh + 32 * g);
+    const float4* sh4 = reinterpret_cast<const float4*>(sh_sh + 32 * g);
+    uint8_t* prow = smem + OFF_P + g * P_BLOCK + r * 32;
+    const int swz = (r >> 2) & 1;                  // 32-byte swizzle: the halves of rows 4..7 of 8 are swapped
     bool ok = true;
     int it = 0;
     for (int seg = 0; walk.next(s); ++seg) {
@@ -813,140 +867,155 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
       const uint32_t* mrow = p.tree.mask + static_cast<int64_t>(s.t) * p.tree.words;
       const int plain = min(base, pos + 1);   // positions below are all seen
       ok = warp_wait(q_full, seg & 1, ab, ok);
-      const int qe = soft ? *reinterpret_cast<const int*>(smem + OFF_QEXP + 4 * h) : 0;
-      const float c = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - qe) << 23);
-      float m_ref = -INFINITY, l_r = 0.f, l_x = 0.f;
+      float m_ref = -INFINITY;                // quarter 0: reference of head 32 g + lane
+      if (quarter == 0) {
+        const int qe = *reinterpret_cast<const int*>(smem + OFF_QEXP + 4 * (32 * g + lane));
+        c_sh[32 * g + lane] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - qe) << 23);
+        sh_sh[32 * g + lane] = INFINITY;      // any logit seen exceeds the reference
+      }
+      named_bar_sync(2, MATH);
+      float2 l2[16];                          // sums of the weights of this token row, per head
+#pragma unroll
+      for (int i = 0; i < 16; ++i) l2[i] = make_float2(0.f, 0.f);
       for (int j = s.j0; j < s.j1; ++j, ++it) {
         ok = warp_wait(s_full, it & 1, ab, ok);
         tc_fence_after();
         uint32_t rr[32];
-        float* x = reinterpret_cast<float*>(rr);
-        float mx = -INFINITY;
-        uint32_t seen = 0xFFFFFFFFu;
-        if (soft) {
-          DSA_TMEM_LD32(tmem + S_COL + 32 * u + lane_off, rr);
-          const int s0 = j * kSelTile + 32 * u;
-          if (s0 + 32 > plain) seen = seen_word(p.tree, mrow, base, pos, s0 + lane);
-          tmem_wait_ld();
-          if (seen == 0xFFFFFFFFu) {
+        float2* y = reinterpret_cast<float2*>(rr);   // logits in log2 units less the reference, plus SHIFT
+        DSA_TMEM_LD32(tmem + S_COL + 32 * g + lane_off, rr);
+        const int s0 = j * kSelTile + r;
+        const bool border = (j + 1) * kSelTile > plain;
+        const bool seen = !border || (s0 <= pos && tree_sees(mrow, p.tree.words, base, s0));
+        tmem_wait_ld();
+        auto logits = [&]() {
+          float mx = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              x[i] = __uint_as_float(rr[i]) * c;
-              mx = fmaxf(mx, x[i]);
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              x[i] = (seen >> i) & 1u ? __uint_as_float(rr[i]) * c : -INFINITY;
-              mx = fmaxf(mx, x[i]);
-            }
+          for (int i = 0; i < 8; ++i) {
+            const float4 cv = c4[i], sv = sh4[i];
+            y[2 * i] = fma2(y[2 * i], make_float2(cv.x, cv.y), make_float2(sv.x, sv.y));
+            y[2 * i + 1] = fma2(y[2 * i + 1], make_float2(cv.z, cv.w), make_float2(sv.z, sv.w));
           }
-        }
-        if (named_bar_any(1, MATH, mx > m_ref + TAU)) {
-          // some head's reference moves: all four threads of a head agree on it
-          float alpha = 1.f;
-          if (soft) red_m[u * kMlaHeads + h] = mx;
+          if (!seen) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) y[i] = make_float2(-INFINITY, -INFINITY);
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) mx = fmaxf(fmaxf(mx, y[i].x), y[i].y);
+          return mx;
+        };
+        const float mx = logits();
+        if (named_bar_any(1, MATH, mx > SHIFT + TAU)) {
+          // some reference moves: the tile's maxima per head, from the logits themselves
+          DSA_TMEM_LD32(tmem + S_COL + 32 * g + lane_off, rr);
+          tmem_wait_ld();
+          float mine = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float m = warp_max_f32(seen ? __uint_as_float(rr[i]) * c_sh[32 * g + i] : -INFINITY);
+            if (lane == i) mine = m;
+          }
+          red[quarter * kMlaHeads + 32 * g + lane] = mine;
           named_bar_sync(2, MATH);
-          if (soft) {
-            const float m = fmaxf(fmaxf(red_m[h], red_m[kMlaHeads + h]),
-                                  fmaxf(red_m[2 * kMlaHeads + h], red_m[3 * kMlaHeads + h]));
+          if (quarter == 0) {
+            const int h = 32 * g + lane;
+            const float m = fmaxf(fmaxf(red[h], red[kMlaHeads + h]), fmaxf(red[2 * kMlaHeads + h], red[3 * kMlaHeads + h]));
+            float alpha = 1.f;
             if (m > m_ref + TAU) {
               alpha = exp2f(m_ref - m);
               m_ref = m;
+              sh_sh[h] = SHIFT - m;
             }
-            l_r *= alpha;
-            l_x *= alpha;
-            if (u == 0) alpha_sh[h] = alpha;
+            alpha_sh[h] = alpha;
           }
           named_bar_sync(2, MATH);
+          const float4* al4 = reinterpret_cast<const float4*>(alpha_sh + 32 * g);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 av = al4[i];
+            l2[2 * i].x *= av.x;
+            l2[2 * i].y *= av.y;
+            l2[2 * i + 1].x *= av.z;
+            l2[2 * i + 1].y *= av.w;
+          }
           if (j > s.j0 && ok) {
 #pragma unroll 1
-            for (int v = v0; v < v1; ++v) {
+            for (int v = 0; v < 4; ++v) {          // this warp's heads in all dim blocks, 16 at a time
 #pragma unroll 1
-              for (int cc = 0; cc < 6; ++cc) {   // 16 heads at a time: the logits stay in registers
+              for (int cc = 0; cc < 2; ++cc) {
                 uint32_t o[16];
-                const uint32_t ta = tmem + O_COL + 96 * v + 16 * cc + lane_off;
+                const uint32_t ta = tmem + O_COL + 96 * v + 32 * g + 16 * cc + lane_off;
                 DSA_TMEM_LD16(ta, o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha_sh[16 * cc + i]);
+                for (int i = 0; i < 16; ++i)
+                  o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha_sh[32 * g + 16 * cc + i]);
                 DSA_TMEM_ST16(ta, o);
               }
             }
             tmem_wait_st();
           }
+          logits();
         }
-        if (soft) {
-          const float shift = m_ref == -INFINITY ? 0.f : SHIFT - m_ref;
-          uint32_t t0[8], t1[8], t2[8];   // the three e5m2 terms of 32 weights, 4 per word
 #pragma unroll
-          for (int w = 0; w < 8; ++w) {
-            uint32_t hw[2], r1[2], lo[2];
+        for (int i = 0; i < 2; ++i) {
+          uint32_t t0[4], t1[4], t2[4];   // the three e5m2 terms of 16 weights, 4 per word
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint32_t hi[2], mid[2], lo[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float p0 = ex2_fast(x[4 * w + 2 * e] + shift), p1 = ex2_fast(x[4 * w + 2 * e + 1] + shift);
-              l_x += p0 + p1;
-              // 9 significant bits, to nearest (positive values: carry into the exponent is right)
-              const float a0 = __uint_as_float((__float_as_uint(p0) + 0x4000u) & 0xFFFF8000u);
-              const float a1 = __uint_as_float((__float_as_uint(p1) + 0x4000u) & 0xFFFF8000u);
-              l_r += a0 + a1;
-              const __half2 ph = __floats2half2_rn(a0, a1);
-              hw[e] = *reinterpret_cast<const uint32_t*>(&ph);
-              const uint32_t hi = hw[e] & 0xFF00FF00u;
-              const __half2 d1 = __hsub2(ph, *reinterpret_cast<const __half2*>(&hi));
-              r1[e] = *reinterpret_cast<const uint32_t*>(&d1);
-              const uint32_t mid = r1[e] & 0xFF00FF00u;
-              const __half2 d2 = __hsub2(d1, *reinterpret_cast<const __half2*>(&mid));
-              lo[e] = static_cast<uint32_t>(
-                  __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&d2), __NV_SATFINITE, __NV_E5M2));
+              const int k = 8 * i + 2 * w + e;
+              float2 pe = y[k];
+              pe.x = ex2_fast(pe.x);
+              pe.y = ex2_fast(pe.y);
+              l2[k] = add2(l2[k], pe);
+              const __half2 ph = __floats2half2_rn(pe.x, pe.y);
+              uint32_t r1, r2, r3;
+              hi[e] = e5m2_term(*reinterpret_cast<const uint32_t*>(&ph), r1);
+              mid[e] = e5m2_term(r1, r2);
+              lo[e] = e5m2_term(r2, r3);
             }
-            t0[w] = __byte_perm(hw[0], hw[1], 0x7531);
-            t1[w] = __byte_perm(r1[0], r1[1], 0x7531);
-            t2[w] = lo[0] | (lo[1] << 16);
+            t0[w] = __byte_perm(hi[0], hi[1], 0x7531);
+            t1[w] = __byte_perm(mid[0], mid[1], 0x7531);
+            t2[w] = __byte_perm(lo[0], lo[1], 0x7531);
           }
           if (ok) {
-            uint8_t* prow = smem + OFF_P + (h >> 3) * 1024 + (h & 7) * 128;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int ch = ((2 * u + i) ^ (h & 7)) << 4;
-              sts128(prow + ch, t0 + 4 * i);
-              sts128(prow + P_TERM + ch, t1 + 4 * i);
-              sts128(prow + 2 * P_TERM + ch, t2 + 4 * i);
-            }
-            // Latents nobody sees are zeroed before the values read them (a weight of zero
-            // does not cancel a NaN): one row is 32 lanes x 16 bytes, three warps share the rows.
-            if (seen != 0xFFFFFFFFu) {
-              uint32_t gone = ~seen;
-              for (int n = 0; gone; ++n) {
-                const int r = 32 * u + __ffs(gone) - 1;
-                gone &= gone - 1;
-                if (n % 3 == quarter)
-                  *reinterpret_cast<uint4*>(smem + OFF_LAT + (lane >> 3) * SLICE + r * 128 + (lane & 7) * 16) =
-                      make_uint4(0u, 0u, 0u, 0u);
-              }
-            }
-            fence_proxy_async_smem();
+            uint8_t* dst = prow + ((i ^ swz) << 4);
+            sts128(dst, t0);
+            sts128(dst + P_TERM, t1);
+            sts128(dst + 2 * P_TERM, t2);
           }
+        }
+        if (ok) {
+          // Latents nobody sees are zeroed before the values read them (a weight of zero
+          // does not cancel a NaN): one row is 32 lanes x 16 bytes, three warps share the rows.
+          if (border) {
+            uint32_t gone = __ballot_sync(0xffffffffu, !seen);
+            for (int n = 0; gone; ++n) {
+              const int row = 32 * quarter + __ffs(gone) - 1;
+              gone &= gone - 1;
+              if (n % 3 == g)
+                *reinterpret_cast<uint4*>(smem + OFF_LAT + (lane >> 3) * SLICE + row * 128 + (lane & 7) * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+          fence_proxy_async_smem();
         }
         tc_fence_before();
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(p_full);
       }
-      // ---- the segment's result: TMEM (thread = dim) -> global
-      if (soft) red_l[u * kMlaHeads + h] = make_float2(l_r, l_x);
+      // ---- the segment's result: sums over the tokens, then TMEM (thread = dim) -> global
+      red[quarter * kMlaHeads + 32 * g + lane] = transpose_sum(*reinterpret_cast<float(*)[32]>(l2));
       named_bar_sync(2, MATH);
-      if (soft && u == 0) {
-        float lr = 0.f, lx = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          lr += red_l[i * kMlaHeads + h].x;
-          lx += red_l[i * kMlaHeads + h].y;
-        }
-        inv_sh[h] = lr == 0.f ? 0.f : (lx == lx ? 1.f / lr : lx);   // nothing seen: output 0; a NaN logit: NaN
+      if (quarter == 0) {
+        const int h = 32 * g + lane;
+        const float l = (red[h] + red[kMlaHeads + h]) + (red[2 * kMlaHeads + h] + red[3 * kMlaHeads + h]);
+        inv_sh[h] = l == 0.f ? 0.f : 1.f / l;   // nothing seen: output 0
         const float m = m_ref == -INFINITY ? 0.f : m_ref - SHIFT;
         if (ok) {
-          if (s.slot >= 0) p.part_ml[static_cast<int64_t>(s.slot) * kMlaHeads + h] = make_float2(m, lx);
-          else if (p.lse) p.lse[static_cast<int64_t>(s.t) * kMlaHeads + h] = (m + log2f(lx)) * 0.69314718055994531f;
+          if (s.slot >= 0) p.part_ml[static_cast<int64_t>(s.slot) * kMlaHeads + h] = make_float2(m, l);
+          else if (p.lse) p.lse[static_cast<int64_t>(s.t) * kMlaHeads + h] = (m + log2f(l)) * 0.69314718055994531f;
         }
       }
       named_bar_sync(2, MATH);
@@ -954,14 +1023,11 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
       tc_fence_after();
       if (ok) {
 #pragma unroll 1
-        for (int v = v0; v < v1; ++v) {
-#pragma unroll 1
-          for (int cc = 0; cc < 3; ++cc) {
-            uint32_t rr[32];
-            DSA_TMEM_LD32(tmem + O_COL + 96 * v + 32 * cc + lane_off, rr);
-            tmem_wait_ld();
-            store_heads(p, s, rr, inv_sh, 32 * cc, v * 128 + quarter * 32 + lane);
-          }
+        for (int v = 0; v < 4; ++v) {
+          uint32_t rr[32];
+          DSA_TMEM_LD32(tmem + O_COL + 96 * v + 32 * g + lane_off, rr);
+          tmem_wait_ld();
+          store_heads(p, s, rr, inv_sh, 32 * g, v * 128 + r);
         }
       }
       tc_fence_before();
