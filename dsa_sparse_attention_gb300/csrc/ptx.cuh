@@ -442,6 +442,17 @@ __device__ __forceinline__ uint64_t make_sdesc_sw32(uint32_t saddr, uint32_t lbo
                "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])                      \
                : "memory")
 
+// 16 lanes (from the address's lane) x 32 columns as blocks of 8 columns: thread l gets, of
+// block b, lane l / 4 columns 2 (l % 4) and + 1 in r[4b], r[4b + 1], lane l / 4 + 8 in r[4b + 2], r[4b + 3].
+#define DSA_TMEM_LD_16X256_X4(taddr, r)                                                                              \
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, "    \
+               "[%16];"                                                                                              \
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),      \
+                 "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),             \
+                 "=r"(r[15])                                                                                         \
+               : "r"(taddr)                                                                                          \
+               : "memory")
+
 #define DSA_TMEM_LD8(taddr, r)                                                                                      \
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"                            \
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])      \

@@ -152,9 +152,13 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Abort 
   return __all_sync(0xffffffffu, ok && mbar_wait_inline(bar, parity, ab));
 }
 
+// Head, in its group of 32, of column n of the group in the FP8 kernel's P and O.
+__device__ __forceinline__ constexpr int head_of_column(int n) { return 8 * ((n >> 1) & 3) + 2 * (n >> 3) + (n & 1); }
+
 // Writes 32 heads of one dim per lane: the segment's output (bf16) or its normalised
 // partial (fp16: 11 significant bits, above the output's 8), both [96][512], as 64
-// contiguous bytes per warp and head.
+// contiguous bytes per warp and head.  PERM: the columns hold heads by head_of_column.
+template <bool PERM>
 __device__ __forceinline__ void store_heads(const TreeMlaParams& p, const Segment& s, const uint32_t (&rr)[32],
                                             const float* inv, int h0, int dim) {
   float al[32];
@@ -162,11 +166,13 @@ __device__ __forceinline__ void store_heads(const TreeMlaParams& p, const Segmen
   if (s.slot < 0) {
     __nv_bfloat16* o = p.out + (static_cast<int64_t>(s.t) * kMlaHeads + h0) * kVDim + dim;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) o[i * kVDim] = __float2bfloat16_rn(__uint_as_float(rr[i]) * al[i]);
+    for (int i = 0; i < 32; ++i)
+      o[(PERM ? head_of_column(i) : i) * kVDim] = __float2bfloat16_rn(__uint_as_float(rr[i]) * al[i]);
   } else {
     __half* o = p.part_o + (static_cast<int64_t>(s.slot) * kMlaHeads + h0) * kVDim + dim;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) o[i * kVDim] = __float2half_rn(__uint_as_float(rr[i]) * al[i]);
+    for (int i = 0; i < 32; ++i)
+      o[(PERM ? head_of_column(i) : i) * kVDim] = __float2half_rn(__uint_as_float(rr[i]) * al[i]);
   }
 }
 
@@ -541,7 +547,7 @@ __global__ void __launch_bounds__(tconv::THREADS, 1)
           uint32_t rr[32];
           DSA_TMEM_LD32(tmem + O_COL + 96 * v + 32 * c + lane_off, rr);
           tmem_wait_ld();
-          store_heads(p, s, rr, inv_sh, 32 * c, v * 128 + quarter * 32 + lane);
+          store_heads<false>(p, s, rr, inv_sh, 32 * c, v * 128 + quarter * 32 + lane);
         }
         const int h = mw * 32 + lane;
         if (h < kMlaHeads) {
@@ -599,8 +605,7 @@ constexpr int P_TERM = 96 * 128;
 constexpr int P_BLOCK = 128 * 32;
 constexpr int OFF_QEXP = OFF_P + 3 * P_TERM;      // [96] int
 constexpr int OFF_REDM = OFF_QEXP + 96 * 4;       // [4][96] float: maxima, then sums, per lane quarter
-constexpr int OFF_C = OFF_REDM + 4 * 96 * 4;      // [96] float: logit scale of each head, log2 units
-constexpr int OFF_SH = OFF_C + 96 * 4;            // [96] float: SHIFT - reference (+inf before the first tile)
+constexpr int OFF_SH = OFF_REDM + 4 * 96 * 4;     // [96] float: SHIFT - reference
 constexpr int OFF_ALPHA = OFF_SH + 96 * 4;        // [96] float
 constexpr int OFF_INV = OFF_ALPHA + 96 * 4;       // [96] float
 constexpr int OFF_BARS = OFF_INV + 96 * 4;
@@ -615,7 +620,7 @@ constexpr int O_COL = 128;
 constexpr float TAU = 4.0f;                       // log2 headroom before the reference moves
 constexpr float SHIFT = 11.0f;                    // weights are scaled by 2^11: at most 2^15, below e5m2's 57344
 static_assert(OFF_LAT % 1024 == 0 && OFF_TAIL % 1024 == 0 && OFF_P % 1024 == 0, "align");
-static_assert(OFF_C % 16 == 0 && OFF_SH % 16 == 0 && OFF_ALPHA % 16 == 0 && OFF_INV % 16 == 0 && OFF_QEXP % 16 == 0,
+static_assert(OFF_SH % 16 == 0 && OFF_ALPHA % 16 == 0 && OFF_INV % 16 == 0 && OFF_QEXP % 16 == 0,
               "vectors are read 16 bytes at a time");
 static_assert(OFF_BARS % 8 == 0 && SMEM_BYTES <= 232448, "smem");
 }  // namespace t8
@@ -648,21 +653,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
-// Sums of 32 values per lane over the lanes: lane i gets the sum of every lane's v[i].
-__device__ __forceinline__ float transpose_sum(float (&v)[32]) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const bool up = (lane & o) != 0;
-#pragma unroll
-    for (int i = 0; i < o; ++i) {
-      const float keep = up ? v[i + o] : v[i], send = up ? v[i] : v[i + o];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-    }
-  }
-  return v[0];
-}
-
 __global__ void __launch_bounds__(t8::THREADS, 1)
     tree_mla_fp8_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ CUtensorMap tmap,
                         TreeMlaParams p) {
@@ -684,7 +674,6 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
   int* abortf = reinterpret_cast<int*>(smem + OFF_MISC + 8);
   int* first_sh = reinterpret_cast<int*>(smem + OFF_MISC + 16);
   float* red = reinterpret_cast<float*>(smem + OFF_REDM);
-  float* c_sh = reinterpret_cast<float*>(smem + OFF_C);
   float* sh_sh = reinterpret_cast<float*>(smem + OFF_SH);
   float* alpha_sh = reinterpret_cast<float*>(smem + OFF_ALPHA);
   float* inv_sh = reinterpret_cast<float*>(smem + OFF_INV);
@@ -852,13 +841,14 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------ softmax and epilogue (0..11)
+    // Scores are loaded 16 lanes x 8 columns at a time: thread l holds, for the tokens
+    // l / 4 + 8 i (i < 4) of its warp's lane quarter, the heads 8 b + 2 a + e (a = l % 4, b < 4,
+    // e < 2) of its group: 8 heads, whose scale, reference and sum stay in registers.  P and
+    // O hold the group's heads in the order 8 a + 2 b + e, a thread's 8 side by side.
     const int quarter = warp & 3, g = warp >> 2;   // tokens 32 quarter .. of a tile, heads 32 g ..
-    const int r = quarter * 32 + lane;             // this thread's token in the tile
+    const int a = lane & 3, r4 = lane >> 2;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const float4* c4 = reinterpret_cast<const float4*>(c_sh + 32 * g);
-    const float4* sh4 = reinterpret_cast<const float4*>(sh_sh + 32 * g);
-    uint8_t* prow = smem + OFF_P + g * P_BLOCK + r * 32;
-    const int swz = (r >> 2) & 1;                  // 32-byte swizzle: the halves of rows 4..7 of 8 are swapped
+    const int my_head = 32 * g + head_of_column(lane);   // of column 32 g + lane of O
     bool ok = true;
     int it = 0;
     for (int seg = 0; walk.next(s); ++seg) {
@@ -867,75 +857,95 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
       const uint32_t* mrow = p.tree.mask + static_cast<int64_t>(s.t) * p.tree.words;
       const int plain = min(base, pos + 1);   // positions below are all seen
       ok = warp_wait(q_full, seg & 1, ab, ok);
-      float m_ref = -INFINITY;                // quarter 0: reference of head 32 g + lane
-      if (quarter == 0) {
-        const int qe = *reinterpret_cast<const int*>(smem + OFF_QEXP + 4 * (32 * g + lane));
-        c_sh[32 * g + lane] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - qe) << 23);
-        sh_sh[32 * g + lane] = INFINITY;      // any logit seen exceeds the reference
-      }
-      named_bar_sync(2, MATH);
-      float2 l2[16];                          // sums of the weights of this token row, per head
+      float2 c2[4], sh2[4], l2[4];            // per head pair b: logit scale (log2 units), SHIFT - reference, sum
 #pragma unroll
-      for (int i = 0; i < 16; ++i) l2[i] = make_float2(0.f, 0.f);
+      for (int b = 0; b < 4; ++b) {
+        const int2 qe = *reinterpret_cast<const int2*>(smem + OFF_QEXP + 4 * (32 * g + 8 * b + 2 * a));
+        c2[b] = make_float2(p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - qe.x) << 23),
+                            p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - qe.y) << 23));
+        sh2[b] = make_float2(INFINITY, INFINITY);   // any logit seen exceeds the reference
+        l2[b] = make_float2(0.f, 0.f);
+      }
+      float m_ref = -INFINITY;                // quarter 0: reference of column 32 g + lane
       for (int j = s.j0; j < s.j1; ++j, ++it) {
         ok = warp_wait(s_full, it & 1, ab, ok);
         tc_fence_after();
-        uint32_t rr[32];
-        float2* y = reinterpret_cast<float2*>(rr);   // logits in log2 units less the reference, plus SHIFT
-        DSA_TMEM_LD32(tmem + S_COL + 32 * g + lane_off, rr);
-        const int s0 = j * kSelTile + r;
+        // y[i][b]: logits in log2 units less the reference, plus SHIFT
+        uint32_t rr[2][16];
+        const uint32_t ts = tmem + S_COL + 32 * g + lane_off;
+        DSA_TMEM_LD_16X256_X4(ts, rr[0]);
+        DSA_TMEM_LD_16X256_X4(ts + (16u << 16), rr[1]);
         const bool border = (j + 1) * kSelTile > plain;
-        const bool seen = !border || (s0 <= pos && tree_sees(mrow, p.tree.words, base, s0));
+        uint32_t seen = 15u;                  // bit i: token i of this thread is seen
+        if (border) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int s0 = j * kSelTile + 32 * quarter + r4 + 8 * i;
+            if (!(s0 <= pos && tree_sees(mrow, p.tree.words, base, s0))) seen &= ~(1u << i);
+          }
+        }
         tmem_wait_ld();
+        float2 y[4][4];
+        auto raw = [&](int i, int b) {
+          return make_float2(__uint_as_float(rr[i >> 1][4 * b + 2 * (i & 1)]),
+                             __uint_as_float(rr[i >> 1][4 * b + 2 * (i & 1) + 1]));
+        };
         auto logits = [&]() {
           float mx = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 cv = c4[i], sv = sh4[i];
-            y[2 * i] = fma2(y[2 * i], make_float2(cv.x, cv.y), make_float2(sv.x, sv.y));
-            y[2 * i + 1] = fma2(y[2 * i + 1], make_float2(cv.z, cv.w), make_float2(sv.z, sv.w));
-          }
-          if (!seen) {
+          for (int i = 0; i < 4; ++i) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) y[i] = make_float2(-INFINITY, -INFINITY);
+            for (int b = 0; b < 4; ++b) {
+              y[i][b] = fma2(raw(i, b), c2[b], sh2[b]);
+              if (!((seen >> i) & 1u)) y[i][b] = make_float2(-INFINITY, -INFINITY);
+              mx = fmaxf(fmaxf(mx, y[i][b].x), y[i][b].y);
+            }
           }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) mx = fmaxf(fmaxf(mx, y[i].x), y[i].y);
           return mx;
         };
         const float mx = logits();
         if (named_bar_any(1, MATH, mx > SHIFT + TAU)) {
-          // some reference moves: the tile's maxima per head, from the logits themselves
-          DSA_TMEM_LD32(tmem + S_COL + 32 * g + lane_off, rr);
-          tmem_wait_ld();
-          float mine = -INFINITY;
+          // some reference moves: the tile's maxima per head
+          float hm[8];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float m = warp_max_f32(seen ? __uint_as_float(rr[i]) * c_sh[32 * g + i] : -INFINITY);
-            if (lane == i) mine = m;
+          for (int b = 0; b < 4; ++b) {
+            hm[2 * b] = hm[2 * b + 1] = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 x = raw(i, b);
+              if ((seen >> i) & 1u) {
+                hm[2 * b] = fmaxf(hm[2 * b], x.x * c2[b].x);
+                hm[2 * b + 1] = fmaxf(hm[2 * b + 1], x.y * c2[b].y);
+              }
+            }
           }
-          red[quarter * kMlaHeads + 32 * g + lane] = mine;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) hm[k] = fmaxf(hm[k], __shfl_xor_sync(0xffffffffu, hm[k], o));
+          if (r4 == 0) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) red[quarter * kMlaHeads + 32 * g + 8 * a + k] = hm[k];
+          }
           named_bar_sync(2, MATH);
           if (quarter == 0) {
-            const int h = 32 * g + lane;
-            const float m = fmaxf(fmaxf(red[h], red[kMlaHeads + h]), fmaxf(red[2 * kMlaHeads + h], red[3 * kMlaHeads + h]));
+            const int n = 32 * g + lane;
+            const float m = fmaxf(fmaxf(red[n], red[kMlaHeads + n]), fmaxf(red[2 * kMlaHeads + n], red[3 * kMlaHeads + n]));
             float alpha = 1.f;
             if (m > m_ref + TAU) {
               alpha = exp2f(m_ref - m);
               m_ref = m;
-              sh_sh[h] = SHIFT - m;
             }
-            alpha_sh[h] = alpha;
+            sh_sh[n] = m_ref == -INFINITY ? INFINITY : SHIFT - m_ref;
+            alpha_sh[n] = alpha;
           }
           named_bar_sync(2, MATH);
-          const float4* al4 = reinterpret_cast<const float4*>(alpha_sh + 32 * g);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 av = al4[i];
-            l2[2 * i].x *= av.x;
-            l2[2 * i].y *= av.y;
-            l2[2 * i + 1].x *= av.z;
-            l2[2 * i + 1].y *= av.w;
+          for (int b = 0; b < 4; ++b) {
+            const float2 av = *reinterpret_cast<const float2*>(alpha_sh + 32 * g + 8 * a + 2 * b);
+            sh2[b] = *reinterpret_cast<const float2*>(sh_sh + 32 * g + 8 * a + 2 * b);
+            l2[b].x *= av.x;
+            l2[b].y *= av.y;
           }
           if (j > s.j0 && ok) {
 #pragma unroll 1
@@ -957,18 +967,18 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
           logits();
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t t0[4], t1[4], t2[4];   // the three e5m2 terms of 16 weights, 4 per word
+        for (int i = 0; i < 4; ++i) {
+          uint32_t t0[2], t1[2], t2[2];   // the three e5m2 terms of 8 weights, 4 per word
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
+          for (int w = 0; w < 2; ++w) {
             uint32_t hi[2], mid[2], lo[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int k = 8 * i + 2 * w + e;
-              float2 pe = y[k];
+              const int b = 2 * w + e;
+              float2 pe = y[i][b];
               pe.x = ex2_fast(pe.x);
               pe.y = ex2_fast(pe.y);
-              l2[k] = add2(l2[k], pe);
+              l2[b] = add2(l2[b], pe);
               const __half2 ph = __floats2half2_rn(pe.x, pe.y);
               uint32_t r1, r2, r3;
               hi[e] = e5m2_term(*reinterpret_cast<const uint32_t*>(&ph), r1);
@@ -980,23 +990,23 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
             t2[w] = __byte_perm(lo[0], lo[1], 0x7531);
           }
           if (ok) {
-            uint8_t* dst = prow + ((i ^ swz) << 4);
-            sts128(dst, t0);
-            sts128(dst + P_TERM, t1);
-            sts128(dst + 2 * P_TERM, t2);
+            // row of 32 heads; 32-byte swizzle: the halves of rows 4..7 of 8 are swapped
+            const int row = 32 * quarter + 8 * i + r4;
+            uint8_t* dst = smem + OFF_P + g * P_BLOCK + row * 32 + ((8 * a) ^ ((row & 4) << 2));
+            *reinterpret_cast<uint2*>(dst) = make_uint2(t0[0], t0[1]);
+            *reinterpret_cast<uint2*>(dst + P_TERM) = make_uint2(t1[0], t1[1]);
+            *reinterpret_cast<uint2*>(dst + 2 * P_TERM) = make_uint2(t2[0], t2[1]);
           }
         }
         if (ok) {
           // Latents nobody sees are zeroed before the values read them (a weight of zero
-          // does not cancel a NaN): one row is 32 lanes x 16 bytes, three warps share the rows.
+          // does not cancel a NaN): 512 bytes a row, 4 lanes x 8 x 16 bytes, three warps share.
           if (border) {
-            uint32_t gone = __ballot_sync(0xffffffffu, !seen);
-            for (int n = 0; gone; ++n) {
-              const int row = 32 * quarter + __ffs(gone) - 1;
-              gone &= gone - 1;
-              if (n % 3 == g)
-                *reinterpret_cast<uint4*>(smem + OFF_LAT + (lane >> 3) * SLICE + row * 128 + (lane & 7) * 16) =
-                    make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+              if ((seen >> i) & 1u) continue;
+              uint8_t* dst = smem + OFF_LAT + a * SLICE + (32 * quarter + 8 * i + r4) * 128;
+              for (int k = g; k < 8; k += 3) *reinterpret_cast<uint4*>(dst + 16 * k) = make_uint4(0u, 0u, 0u, 0u);
             }
           }
           fence_proxy_async_smem();
@@ -1006,16 +1016,27 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
         if (ok && lane == 0) mbar_arrive(p_full);
       }
       // ---- the segment's result: sums over the tokens, then TMEM (thread = dim) -> global
-      red[quarter * kMlaHeads + 32 * g + lane] = transpose_sum(*reinterpret_cast<float(*)[32]>(l2));
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          l2[b].x += __shfl_xor_sync(0xffffffffu, l2[b].x, o);
+          l2[b].y += __shfl_xor_sync(0xffffffffu, l2[b].y, o);
+        }
+      if (r4 == 0) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          *reinterpret_cast<float2*>(red + quarter * kMlaHeads + 32 * g + 8 * a + 2 * b) = l2[b];
+      }
       named_bar_sync(2, MATH);
       if (quarter == 0) {
-        const int h = 32 * g + lane;
-        const float l = (red[h] + red[kMlaHeads + h]) + (red[2 * kMlaHeads + h] + red[3 * kMlaHeads + h]);
-        inv_sh[h] = l == 0.f ? 0.f : 1.f / l;   // nothing seen: output 0
+        const int n = 32 * g + lane;
+        const float l = (red[n] + red[kMlaHeads + n]) + (red[2 * kMlaHeads + n] + red[3 * kMlaHeads + n]);
+        inv_sh[n] = l == 0.f ? 0.f : 1.f / l;   // nothing seen: output 0
         const float m = m_ref == -INFINITY ? 0.f : m_ref - SHIFT;
         if (ok) {
-          if (s.slot >= 0) p.part_ml[static_cast<int64_t>(s.slot) * kMlaHeads + h] = make_float2(m, l);
-          else if (p.lse) p.lse[static_cast<int64_t>(s.t) * kMlaHeads + h] = (m + log2f(l)) * 0.69314718055994531f;
+          if (s.slot >= 0) p.part_ml[static_cast<int64_t>(s.slot) * kMlaHeads + my_head] = make_float2(m, l);
+          else if (p.lse) p.lse[static_cast<int64_t>(s.t) * kMlaHeads + my_head] = (m + log2f(l)) * 0.69314718055994531f;
         }
       }
       named_bar_sync(2, MATH);
@@ -1027,7 +1048,7 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
           uint32_t rr[32];
           DSA_TMEM_LD32(tmem + O_COL + 96 * v + 32 * g + lane_off, rr);
           tmem_wait_ld();
-          store_heads(p, s, rr, inv_sh, 32 * g, v * 128 + r);
+          store_heads<true>(p, s, rr, inv_sh, 32 * g, v * 128 + 32 * quarter + lane);
         }
       }
       tc_fence_before();
