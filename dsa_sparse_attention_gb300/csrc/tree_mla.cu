@@ -660,16 +660,16 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024_tree(smem_raw);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BARS);
-  uint64_t* lat_full = bars + 0;    // [4]
-  uint64_t* lat_empty = bars + 4;   // [4]
-  uint64_t* tail_full = bars + 8;
+  uint64_t* lat_full = bars + 0;    // [4] slices, then the tail
+  uint64_t* tail_full = bars + 4;
+  uint64_t* lat_empty = bars + 5;   // [4]
   uint64_t* tail_empty = bars + 9;
   uint64_t* q_full = bars + 10;
   uint64_t* q_done = bars + 11;     // a segment's QKs are done
   uint64_t* s_full = bars + 12;     // a tile's QK (and the PV before it) is done
-  uint64_t* p_full = bars + 13;
-  uint64_t* o_done = bars + 14;     // a segment's last PV is done
-  uint64_t* drain = bars + 15;
+  uint64_t* o_done = bars + 13;     // a segment's last PV is done
+  uint64_t* drain = bars + 14;
+  uint64_t* p_full = bars + 15;     // [3] P of the tokens 8 i + (0..7) of every quarter: i = 0, 1, 2 and 3
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
   int* abortf = reinterpret_cast<int*>(smem + OFF_MISC + 8);
   int* first_sh = reinterpret_cast<int*>(smem + OFF_MISC + 16);
@@ -680,10 +680,8 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 13; ++i) mbar_init(&bars[i], 1);
-    mbar_init(p_full, MATH_WARPS);
-    mbar_init(o_done, 1);
-    mbar_init(drain, 1);
+    for (int i = 0; i < 15; ++i) mbar_init(&bars[i], 1);
+    for (int i = 0; i < 3; ++i) mbar_init(&p_full[i], MATH_WARPS);
     *abortf = 0;
     *first_sh = 0;
     fence_mbar_init();
@@ -774,59 +772,94 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
     const uint64_t dq = make_sdesc_sw128(smem_u32(smem + OFF_Q), 16, 1024);        // query terms, K-major
     const uint64_t dl = make_sdesc_sw128(smem_u32(smem + OFF_LAT), 16, 1024);      // latents, K-major (QK)
     const uint64_t dt = make_sdesc_sw64(smem_u32(smem + OFF_TAIL), 16, 512);       // their last 64 dims
-    const uint64_t dv = make_sdesc_sw128(smem_u32(smem + OFF_LAT), SLICE, 1024);   // latents, MN-major (PV)
-    const uint64_t dp = make_sdesc_sw32(smem_u32(smem + OFF_P), P_BLOCK, 256);     // P terms, MN-major
+    // Values: K step i takes the tokens 8 i .. 8 i + 7 of every lane quarter (rows 32 apart, by
+    // the stride between 8-row groups), which every softmax warp writes i-th: the first
+    // steps run while the later weights are still computed.
+    const uint64_t dv = make_sdesc_sw128(smem_u32(smem + OFF_LAT), SLICE, 4096);   // latents, MN-major
+    const uint64_t dp = make_sdesc_sw32(smem_u32(smem + OFF_P), P_BLOCK, 1024);    // P terms, MN-major
+    auto values = [&](int v, int i, uint32_t acc) {
+      const uint32_t d = tmem + O_COL + 96 * v;
+      const uint64_t a = dv + ((v * SLICE + i * 1024) >> 4), b = dp + ((256 * i) >> 4);
+      mma_f8f6f4_keep_a<KeepA::kFill>(d, a, b, idesc_pv, acc);
+      mma_f8f6f4_keep_a<KeepA::kUse>(d, a, b + (P_TERM >> 4), idesc_pv, 1u);
+      mma_f8f6f4_keep_a<KeepA::kLast>(d, a, b + (2 * P_TERM >> 4), idesc_pv, 1u);
+    };
     bool ok = true;
     int it = 0;
     for (int seg = 0; ok && walk.next(s); ++seg) {
       ok = warp_wait(q_full, seg & 1, ab, ok);
       for (int j = s.j0; ok && j < s.j1; ++j, ++it) {
+        // A slice's arrival is awaited half-way through the MMAs of the one before it: the
+        // tensor core still has those to do.
         if (!(ok = warp_wait(tail_full, it & 1, ab, ok))) break;
         tc_fence_after();
         if (leader) {
-#pragma unroll
-          for (int kk = 0; kk < 2; ++kk) {   // chunk 4 of the query: hi | lo of dims 512..575
-            const uint64_t a = dt + ((32 * kk) >> 4), b = dq + ((4 * QCHUNK + 32 * kk) >> 4);
-            mma_f8f6f4_keep_a<KeepA::kFill>(tmem + S_COL, a, b, idesc_qk, kk ? 1u : 0u);
-            mma_f8f6f4_keep_a<KeepA::kLast>(tmem + S_COL, a, b + (64 >> 4), idesc_qk, 1u);
-          }
+          const uint64_t a = dt, b = dq + (4 * QCHUNK >> 4);   // chunk 4 of the query: hi | lo of dims 512..575
+          mma_f8f6f4_keep_a<KeepA::kFill>(tmem + S_COL, a, b, idesc_qk, 0u);
+          mma_f8f6f4_keep_a<KeepA::kLast>(tmem + S_COL, a, b + (64 >> 4), idesc_qk, 1u);
+          mma_f8f6f4_keep_a<KeepA::kFill>(tmem + S_COL, a + (32 >> 4), b + (32 >> 4), idesc_qk, 1u);
+          mma_f8f6f4_keep_a<KeepA::kLast>(tmem + S_COL, a + (32 >> 4), b + (96 >> 4), idesc_qk, 1u);
           tc_commit(tail_empty);
         }
         __syncwarp();
+        ok = warp_wait(&lat_full[0], it & 1, ab, ok);
+        tc_fence_after();
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          ok = warp_wait(&lat_full[k], it & 1, ab, ok);
-          tc_fence_after();
-          if (leader && ok) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              const uint64_t a = dl + ((k * SLICE + 32 * kk) >> 4), b = dq + ((k * QCHUNK + 32 * kk) >> 4);
-              mma_f8f6f4_keep_a<KeepA::kFill>(tmem + S_COL, a, b, idesc_qk, 1u);
-              mma_f8f6f4_keep_a<KeepA::kLast>(tmem + S_COL, a, b + (5 * QCHUNK >> 4), idesc_qk, 1u);
+          for (int half = 0; half < 2; ++half) {
+            if (leader && ok) {
+#pragma unroll
+              for (int kk = 2 * half; kk < 2 * half + 2; ++kk) {
+                const uint64_t a = dl + ((k * SLICE + 32 * kk) >> 4), b = dq + ((k * QCHUNK + 32 * kk) >> 4);
+                mma_f8f6f4_keep_a<KeepA::kFill>(tmem + S_COL, a, b, idesc_qk, 1u);
+                mma_f8f6f4_keep_a<KeepA::kLast>(tmem + S_COL, a, b + (5 * QCHUNK >> 4), idesc_qk, 1u);
+              }
+            }
+            __syncwarp();
+            if (half == 0 && k < 3) {
+              ok = warp_wait(&lat_full[k + 1], it & 1, ab, ok);
+              tc_fence_after();
             }
           }
-          __syncwarp();
         }
         if (!ok) break;
         if (leader) tc_commit(s_full);
         __syncwarp();
-        if (!(ok = warp_wait(p_full, it & 1, ab, ok))) break;
-        tc_fence_after();
         const uint32_t acc = j > s.j0 ? 1u : 0u;
         const bool last = j == s.j1 - 1;
+        if (!(ok = warp_wait(&p_full[0], it & 1, ab, ok))) break;
+        tc_fence_after();
         if (leader) {
           // the query may go once every softmax warp is past its own wait for it, too
           if (last) tc_commit(q_done);
+          values(2, 0, acc);
+          values(3, 0, acc);
+        }
+        __syncwarp();
+        if (!(ok = warp_wait(&p_full[1], it & 1, ab, ok))) break;
+        tc_fence_after();
+        if (leader) {
+          values(2, 1, 1u);
+          values(3, 1, 1u);
+          values(0, 0, acc);
+          values(0, 1, 1u);
+        }
+        __syncwarp();
+        if (!(ok = warp_wait(&p_full[2], it & 1, ab, ok))) break;
+        tc_fence_after();
+        if (leader) {
+          // slices come free one after the other, the first half-way through the values
+          values(0, 2, 1u);
+          values(0, 3, 1u);
+          tc_commit(&lat_empty[0]);
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
+          for (int i = 0; i < 4; ++i) values(1, i, i ? 1u : acc);
+          tc_commit(&lat_empty[1]);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              const uint32_t d = tmem + O_COL + 96 * v;
-              const uint64_t a = dv + ((v * SLICE + kk * 4096) >> 4), b = dp + ((1024 * kk) >> 4);
-              mma_f8f6f4_keep_a<KeepA::kFill>(d, a, b, idesc_pv, kk ? 1u : acc);
-              mma_f8f6f4_keep_a<KeepA::kUse>(d, a, b + (P_TERM >> 4), idesc_pv, 1u);
-              mma_f8f6f4_keep_a<KeepA::kLast>(d, a, b + (2 * P_TERM >> 4), idesc_pv, 1u);
-            }
+          for (int v = 2; v < 4; ++v) {
+            values(v, 2, 1u);
+            values(v, 3, 1u);
             tc_commit(&lat_empty[v]);
           }
           if (last) tc_commit(o_done);
@@ -874,7 +907,8 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
         uint32_t rr[2][16];
         const uint32_t ts = tmem + S_COL + 32 * g + lane_off;
         DSA_TMEM_LD_16X256_X4(ts, rr[0]);
-        DSA_TMEM_LD_16X256_X4(ts + (16u << 16), rr[1]);
+        tmem_wait_ld();
+        DSA_TMEM_LD_16X256_X4(ts + (16u << 16), rr[1]);   // lands while the first half is scaled
         const bool border = (j + 1) * kSelTile > plain;
         uint32_t seen = 15u;                  // bit i: token i of this thread is seen
         if (border) {
@@ -884,16 +918,15 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
             if (!(s0 <= pos && tree_sees(mrow, p.tree.words, base, s0))) seen &= ~(1u << i);
           }
         }
-        tmem_wait_ld();
         float2 y[4][4];
         auto raw = [&](int i, int b) {
           return make_float2(__uint_as_float(rr[i >> 1][4 * b + 2 * (i & 1)]),
                              __uint_as_float(rr[i >> 1][4 * b + 2 * (i & 1) + 1]));
         };
-        auto logits = [&]() {
+        auto logits = [&](int i0) {   // of the tokens i0 and i0 + 1; their maximum
           float mx = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = i0; i < i0 + 2; ++i) {
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
               y[i][b] = fma2(raw(i, b), c2[b], sh2[b]);
@@ -903,7 +936,9 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
           }
           return mx;
         };
-        const float mx = logits();
+        float mx = logits(0);
+        tmem_wait_ld();
+        mx = fmaxf(mx, logits(2));
         if (named_bar_any(1, MATH, mx > SHIFT + TAU)) {
           // some reference moves: the tile's maxima per head
           float hm[8];
@@ -964,8 +999,20 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
             }
             tmem_wait_st();
           }
-          logits();
+          logits(0);
+          logits(2);
         }
+        // Latents nobody sees are zeroed before the values read them (a weight of zero does not
+        // cancel a NaN): 512 bytes a row, 4 lanes x 8 x 16 bytes, three warps share the rows.
+        if (border && ok) {
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) {
+            if ((seen >> i) & 1u) continue;
+            uint8_t* dst = smem + OFF_LAT + a * SLICE + (32 * quarter + 8 * i + r4) * 128;
+            for (int k = g; k < 8; k += 3) *reinterpret_cast<uint4*>(dst + 16 * k) = make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+        tc_fence_before();   // the scores are in registers
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint32_t t0[2], t1[2], t2[2];   // the three e5m2 terms of 8 weights, 4 per word
@@ -996,24 +1043,13 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
             *reinterpret_cast<uint2*>(dst) = make_uint2(t0[0], t0[1]);
             *reinterpret_cast<uint2*>(dst + P_TERM) = make_uint2(t1[0], t1[1]);
             *reinterpret_cast<uint2*>(dst + 2 * P_TERM) = make_uint2(t2[0], t2[1]);
+            if (i != 2) fence_proxy_async_smem();
+          }
+          if (i != 2) {
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(&p_full[i < 2 ? i : 2]);
           }
         }
-        if (ok) {
-          // Latents nobody sees are zeroed before the values read them (a weight of zero
-          // does not cancel a NaN): 512 bytes a row, 4 lanes x 8 x 16 bytes, three warps share.
-          if (border) {
-#pragma unroll 1
-            for (int i = 0; i < 4; ++i) {
-              if ((seen >> i) & 1u) continue;
-              uint8_t* dst = smem + OFF_LAT + a * SLICE + (32 * quarter + 8 * i + r4) * 128;
-              for (int k = g; k < 8; k += 3) *reinterpret_cast<uint4*>(dst + 16 * k) = make_uint4(0u, 0u, 0u, 0u);
-            }
-          }
-          fence_proxy_async_smem();
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (ok && lane == 0) mbar_arrive(p_full);
       }
       // ---- the segment's result: sums over the tokens, then TMEM (thread = dim) -> global
 #pragma unroll
