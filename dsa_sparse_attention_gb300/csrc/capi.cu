@@ -216,7 +216,7 @@ bool make_qidx_map(CUtensorMap* m, const void* q_idx, int T, bool mx) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// q [T*96 rows, 576 bf16], box = 64 dims x 96 heads.
+// q [T*96 rows, 576 values of 16 bits], box = 64 dims x 96 heads.
 bool make_q_map(CUtensorMap* m, const void* q, int T) {
   auto enc = encode_fn();
   if (!enc) return false;
@@ -337,7 +337,7 @@ TreeView tree_view(const dsa_tree* t) { return TreeView{t->base, t->mask, t->mas
 
 // Workspace of dsa_tree_mla.
 struct TreeWs {
-  size_t status = 0, starts = 0, q_terms = 0, part_o = 0, part_ml = 0, total = 0;
+  size_t status = 0, starts = 0, q_terms = 0, q_exps = 0, part_o = 0, part_ml = 0, total = 0;
 };
 
 TreeWs plan_tree_ws(const dsa_kv_layout* l, const dsa_batch* b) {
@@ -345,7 +345,10 @@ TreeWs plan_tree_ws(const dsa_kv_layout* l, const dsa_batch* b) {
   const size_t slots = 2 * size_t(num_sms());
   w.starts = kStatusBytes;
   w.q_terms = align_up(w.starts + (size_t(b->num_tokens) + 1) * sizeof(int64_t));
-  w.part_o = align_up(w.q_terms + (l->lat_fmt == DSA_LAT_FP8 ? size_t(b->num_tokens) * kQTokenBytes : 0));
+  // FP8 latents: terms and exponents together; NVFP4: fp16 values, then exponents
+  const size_t T = size_t(b->num_tokens);
+  w.q_exps = align_up(w.q_terms + T * (l->lat_fmt == DSA_LAT_FP8 ? size_t(kQTokenBytes) : size_t(kMlaHeads) * kLatDim * 2));
+  w.part_o = align_up(w.q_exps + (l->lat_fmt == DSA_LAT_FP8 ? 0 : T * kMlaHeads * 4));
   w.part_ml = align_up(w.part_o + slots * kMlaHeads * kVDim * 2);
   w.total = align_up(w.part_ml + slots * kMlaHeads * sizeof(float2));
   return w;
@@ -914,12 +917,15 @@ dsa_status dsa_tree_mla(const dsa_kv_layout* layout, const dsa_batch* batch, con
   p.status = at<uint32_t>(workspace, wl.status);
   const bool fp8 = layout->lat_fmt == DSA_LAT_FP8;
   uint8_t* terms = fp8 ? at<uint8_t>(workspace, wl.q_terms) : nullptr;
+  __half* q16 = fp8 ? nullptr : at<__half>(workspace, wl.q_terms);
   p.q_terms = terms;
+  p.q_exps = at<int32_t>(workspace, wl.q_exps);
   CUtensorMap amap, bmap;
-  if (fp8 ? !(make_latent_map(&amap, layout, 128) && make_latent_map(&bmap, layout, 64)) : !make_q_map(&amap, q, T))
+  if (fp8 ? !(make_latent_map(&amap, layout, 128) && make_latent_map(&bmap, layout, 64)) : !make_q_map(&amap, q16, T))
     return encode_fail();
-  const cudaError_t e = launch_tree_prep(p.b, p.tree, static_cast<const __nv_bfloat16*>(q), terms,
-                                         at<int64_t>(workspace, wl.starts), p.status, stream);
+  const cudaError_t e = launch_tree_prep(p.b, p.tree, static_cast<const __nv_bfloat16*>(q), terms, q16,
+                                         at<int32_t>(workspace, wl.q_exps), at<int64_t>(workspace, wl.starts), p.status,
+                                         stream);
   if (e != cudaSuccess) return cuda_fail(e);
   return cuda_status(fp8 ? launch_tree_mla_fp8(amap, bmap, p, stream) : launch_tree_mla_nvfp4(amap, p, stream));
 }

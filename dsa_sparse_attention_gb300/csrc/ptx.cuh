@@ -459,6 +459,11 @@ __device__ __forceinline__ uint64_t make_sdesc_sw32(uint32_t saddr, uint32_t lbo
                : "r"(taddr)                                                                                         \
                : "memory")
 
+#define DSA_TMEM_ST8(taddr, r)                                                                                      \
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),   \
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])                         \
+               : "memory")
+
 // Prefetch `bytes` (a multiple of 16, 16-byte aligned) of global memory into L2.
 __device__ __forceinline__ void bulk_prefetch_l2(const void* src, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");

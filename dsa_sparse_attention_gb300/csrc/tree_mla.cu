@@ -21,19 +21,63 @@ namespace dsa {
 
 // --------------------------------------------------------- plan and query terms
 //
-// Block 0 sums the tokens' tiles; the other blocks (FP8 latents) split the queries
-// into the attention's e4m3 terms, one warp per head, three blocks of 32 heads a token.
+// Block 0 sums the tokens' tiles; the other blocks turn the queries into the attention's
+// operands, one warp per head, three blocks of 32 heads a token: two e4m3 terms (FP8
+// latents, mla_q.cuh) or fp16 values (NVFP4 latents), scaled per head by a power of two.
+
+// Head h of query q_tok (bf16 [96][576]) as fp16 times 2^k, the largest |q| in [2^14, 2^15):
+// exact above 2^-32 of it, off by at most 2^-25 below.  k goes to exps[h].
+__device__ __forceinline__ void q_head_to_f16(const __nv_bfloat16* q_tok, int h, __half* out, int32_t* exps) {
+  const int lane = threadIdx.x & 31;
+  const uint4* src = reinterpret_cast<const uint4*>(q_tok + static_cast<int64_t>(h) * kLatDim);
+  uint4 v[3];
+  uint32_t am = 0;   // |q| bits: non-negative floats order as unsigned integers
+#pragma unroll
+  for (int r = 0; r < 3; ++r) {
+    const int pc = lane + 32 * r;
+    v[r] = pc < 72 ? __ldg(src + pc) : make_uint4(0u, 0u, 0u, 0u);
+    const uint32_t w4[4] = {v[r].x, v[r].y, v[r].z, v[r].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) am = max(am, max((w4[j] << 16) & 0x7FFFFFFFu, w4[j] & 0x7FFF0000u));
+  }
+  am = __reduce_max_sync(0xffffffffu, am);
+  int k = am < 0x00800000u ? 0 : 14 + 127 - static_cast<int>(am >> 23);
+  k = k > 126 ? 126 : (k < -126 ? -126 : k);
+  const float sc = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+  if (lane == 0) exps[h] = k;
+  uint4* dst = reinterpret_cast<uint4*>(out + static_cast<int64_t>(h) * kLatDim);
+#pragma unroll
+  for (int r = 0; r < 3; ++r) {
+    const int pc = lane + 32 * r;
+    if (pc >= 72) break;
+    const uint32_t w4[4] = {v[r].x, v[r].y, v[r].z, v[r].w};
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const __half2 x =
+          __floats2half2_rn(__uint_as_float(w4[j] << 16) * sc, __uint_as_float(w4[j] & 0xFFFF0000u) * sc);
+      o[j] = *reinterpret_cast<const uint32_t*>(&x);
+    }
+    dst[pc] = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
 
 constexpr int kPrepThreads = 1024;
 
 __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(BatchView b, TreeView tree, const __nv_bfloat16* q,
-                                                                 uint8_t* terms, int64_t* starts, uint32_t* status) {
+                                                                 uint8_t* terms, __half* q16, int32_t* exps,
+                                                                 int64_t* starts, uint32_t* status) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (blockIdx.x > 0) {
     const int t = (blockIdx.x - 1) / 3, h = (blockIdx.x - 1) % 3 * 32 + warp;
-    uint8_t* tok = terms + static_cast<int64_t>(t) * kQTokenBytes;
-    q_head_to_terms(q + static_cast<int64_t>(t) * kMlaHeads * kLatDim, h, tok,
-                    reinterpret_cast<int32_t*>(tok + kQTermBytes));
+    const __nv_bfloat16* q_tok = q + static_cast<int64_t>(t) * kMlaHeads * kLatDim;
+    if (q16) {
+      q_head_to_f16(q_tok, h, q16 + static_cast<int64_t>(t) * kMlaHeads * kLatDim,
+                    exps + static_cast<int64_t>(t) * kMlaHeads);
+    } else {
+      uint8_t* tok = terms + static_cast<int64_t>(t) * kQTokenBytes;
+      q_head_to_terms(q_tok, h, tok, reinterpret_cast<int32_t*>(tok + kQTermBytes));
+    }
     return;
   }
   __shared__ int64_t wsum[kPrepThreads / 32];
@@ -66,9 +110,9 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(BatchView b, Tr
 }
 
 cudaError_t launch_tree_prep(const BatchView& b, const TreeView& tree, const __nv_bfloat16* q, uint8_t* terms,
-                             int64_t* starts, uint32_t* status, cudaStream_t st) {
-  return launch_ex(tree_prep_kernel, dim3(terms ? 1 + 3 * b.T : 1), dim3(kPrepThreads), 0, st, false, 0u, b, tree, q,
-                   terms, starts, status);
+                             __half* q16, int32_t* exps, int64_t* starts, uint32_t* status, cudaStream_t st) {
+  return launch_ex(tree_prep_kernel, dim3(1 + 3 * b.T), dim3(kPrepThreads), 0, st, false, 0u, b, tree, q, terms, q16,
+                   exps, starts, status);
 }
 
 // The first token of share [g0, ...): every thread of the CTA searches.
@@ -98,49 +142,6 @@ __device__ __forceinline__ SegmentWalk make_walk(const TreeMlaParams& p, int* fi
   return w;
 }
 
-// -------------------------------------------- attention with converted latents
-//
-// One CTA per SM.  A tile's 128 latents are converted to the tensor cores' 16-bit
-// operands on the way into shared memory, once per use:
-//   S^T[token, head] = C[token, 0:576] . q[head, 0:576]      M=128, N=96, K=576  (bf16 x bf16)
-//   O^T[dim, head]  += V^T[dim, token] . P^T[token, head]     M=128 (x4 dim blocks), N=96, K=128 (f16 x f16)
-// TMEM: S^T in columns [0, 96), O^T blocks at 128 + 96 v (v = 0..3): 480 of 512.
-// The layouts, the softmax across lanes and the sums of P by the tensor core are
-// those of mla.cu; here a CTA walks many tiles and several tokens.
-// Roles: warp 0 loads each token's query (96 x 576 bf16) once the one before has been
-// used; warp 1 issues MMAs; warps 2..9 convert; warps 10..13 run the softmax; all 12
-// math warps write a finished segment.
-namespace tconv {
-constexpr int QCHUNKS = kLatDim / 64;
-constexpr int Q_SLOT = kMlaHeads * 128;
-constexpr int OFF_Q = 0;
-constexpr int RSLOTS = 4;
-constexpr int RING_SLOT = 16384;
-constexpr int OFF_RING = QCHUNKS * Q_SLOT;
-constexpr int OFF_P = OFF_RING + RSLOTS * RING_SLOT;
-constexpr int P_BYTES = 2 * 16 * 1024;
-constexpr int OFF_ONES = OFF_P + P_BYTES;
-constexpr int OFF_RED = OFF_ONES + 1024;          // 4 x 96 floats
-constexpr int OFF_MUSE = OFF_RED + 4 * 96 * 4;
-constexpr int OFF_ALPHA = OFF_MUSE + 96 * 4;
-constexpr int OFF_INV = OFF_ALPHA + 96 * 4;
-constexpr int OFF_LFIN = OFF_INV + 96 * 4;
-constexpr int OFF_ROWOK = OFF_LFIN + 96 * 4;      // 2 x 128 bytes: position seen (by tile parity)
-constexpr int OFF_BARS = OFF_ROWOK + 256;
-constexpr int N_BARS = 20;
-constexpr int OFF_MISC = OFF_BARS + N_BARS * 8;
-constexpr int SMEM_BYTES = OFF_MISC + 64 + 1024;
-constexpr int THREADS = 448;
-constexpr int CONV_WARPS = 8;
-constexpr int SOFT_WARP0 = 2 + CONV_WARPS;
-constexpr int S_COL = 0;
-constexpr int O_COL = 128;
-constexpr float TAU = 8.0f;                       // log2 headroom before the running max moves
-static_assert(OFF_RING % 1024 == 0 && OFF_P % 1024 == 0 && OFF_ONES % 1024 == 0, "align");
-static_assert(OFF_MUSE % 16 == 0 && OFF_ALPHA % 16 == 0 && OFF_INV % 16 == 0, "vectors are read 16 bytes at a time");
-static_assert(OFF_BARS % 8 == 0 && SMEM_BYTES <= 232448, "smem");
-}  // namespace tconv
-
 __device__ __forceinline__ uint8_t* align1024_tree(uint8_t* p) {
   return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~static_cast<uintptr_t>(1023));
 }
@@ -152,13 +153,12 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Abort 
   return __all_sync(0xffffffffu, ok && mbar_wait_inline(bar, parity, ab));
 }
 
-// Head, in its group of 32, of column n of the group in the FP8 kernel's P and O.
+// Head, in its group of 32, of column n of the group in P and O.
 __device__ __forceinline__ constexpr int head_of_column(int n) { return 8 * ((n >> 1) & 3) + 2 * (n >> 3) + (n & 1); }
 
 // Writes 32 heads of one dim per lane: the segment's output (bf16) or its normalised
 // partial (fp16: 11 significant bits, above the output's 8), both [96][512], as 64
-// contiguous bytes per warp and head.  PERM: the columns hold heads by head_of_column.
-template <bool PERM>
+// contiguous bytes per warp and head.
 __device__ __forceinline__ void store_heads(const TreeMlaParams& p, const Segment& s, const uint32_t (&rr)[32],
                                             const float* inv, int h0, int dim) {
   float al[32];
@@ -166,404 +166,29 @@ __device__ __forceinline__ void store_heads(const TreeMlaParams& p, const Segmen
   if (s.slot < 0) {
     __nv_bfloat16* o = p.out + (static_cast<int64_t>(s.t) * kMlaHeads + h0) * kVDim + dim;
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      o[(PERM ? head_of_column(i) : i) * kVDim] = __float2bfloat16_rn(__uint_as_float(rr[i]) * al[i]);
+    for (int i = 0; i < 32; ++i) o[head_of_column(i) * kVDim] = __float2bfloat16_rn(__uint_as_float(rr[i]) * al[i]);
   } else {
     __half* o = p.part_o + (static_cast<int64_t>(s.slot) * kMlaHeads + h0) * kVDim + dim;
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      o[(PERM ? head_of_column(i) : i) * kVDim] = __float2half_rn(__uint_as_float(rr[i]) * al[i]);
+    for (int i = 0; i < 32; ++i) o[head_of_column(i) * kVDim] = __float2half_rn(__uint_as_float(rr[i]) * al[i]);
   }
 }
 
-__global__ void __launch_bounds__(tconv::THREADS, 1)
-    tree_mla_nvfp4_kernel(const __grid_constant__ CUtensorMap qmap, TreeMlaParams p) {
-  using namespace tconv;
-  constexpr int ROWB = 352;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = align1024_tree(smem_raw);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BARS);
-  uint64_t* q_full = bars + 0;
-  uint64_t* rows_ready = bars + 1;
-  uint64_t* ring_full = bars + 2;   // [RSLOTS]
-  uint64_t* ring_empty = bars + 6;  // [RSLOTS]
-  uint64_t* s_full = bars + 10;     // a tile's QK done
-  uint64_t* s_free = bars + 11;
-  uint64_t* p_full = bars + 12;
-  uint64_t* o_done = bars + 13;     // a tile's PV done
-  uint64_t* drain = bars + 14;
-  uint64_t* sum_done = bars + 15;
-  uint64_t* o_free = bars + 16;     // a segment's O has been read
-  uint64_t* q_done = bars + 17;     // a segment's QKs are done
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
-  int* abortf = reinterpret_cast<int*>(smem + OFF_MISC + 8);
-  int* rescale_sh = reinterpret_cast<int*>(smem + OFF_MISC + 16);
-  int* first_sh = reinterpret_cast<int*>(smem + OFF_MISC + 24);
-  float* red = reinterpret_cast<float*>(smem + OFF_RED);
-  float* m_use = reinterpret_cast<float*>(smem + OFF_MUSE);
-  float* alpha_sh = reinterpret_cast<float*>(smem + OFF_ALPHA);
-  float* inv_sh = reinterpret_cast<float*>(smem + OFF_INV);
-  float* l_fin = reinterpret_cast<float*>(smem + OFF_LFIN);
-  uint8_t* rowok = smem + OFF_ROWOK;
-
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
-    mbar_init(q_full, 1);
-    mbar_init(rows_ready, CONV_WARPS);
-    for (int i = 0; i < RSLOTS; ++i) {
-      mbar_init(&ring_full[i], CONV_WARPS);
-      mbar_init(&ring_empty[i], 1);
-    }
-    mbar_init(s_full, 1);
-    mbar_init(s_free, 4);
-    mbar_init(p_full, 4);
-    mbar_init(o_done, 1);
-    mbar_init(drain, 1);
-    mbar_init(sum_done, 1);
-    mbar_init(o_free, 12);
-    mbar_init(q_done, 1);
-    *abortf = 0;
-    *first_sh = 0;
-    fence_mbar_init();
-    prefetch_tensormap(&qmap);
-  }
-  for (int i = threadIdx.x; i < 256; i += THREADS) reinterpret_cast<uint32_t*>(smem + OFF_ONES)[i] = 0x3C003C00u;
-  fence_proxy_async_smem();
-  if (warp == 1) tmem_alloc(tslot, 512);
-  grid_dep_wait();   // the plan
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  SegmentWalk walk = make_walk(p, first_sh);
-  const uint32_t tmem = *tslot;
-  const Abort ab{abortf, p.status};
-  Segment s;
-
-  if (warp == 0) {
-    // --------------------------------------------------------- query loader
-    if (lane == 0) {
-      bool ok = true;
-      int seg = 0;
-      for (; ok && walk.next(s); ++seg) {
-        if (seg > 0 && !(ok = mbar_wait(q_done, (seg - 1) & 1, ab))) break;
-        mbar_arrive_expect_tx(q_full, QCHUNKS * Q_SLOT);
-        for (int kc = 0; kc < QCHUNKS; ++kc)
-          tma_load_2d(smem + OFF_Q + kc * Q_SLOT, &qmap, q_full, kc * 64, s.t * kMlaHeads);
-      }
-      if (seg > 0) drain_wait(q_full, (seg - 1) & 1);   // no copy into shared memory outlives the CTA
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      const uint32_t idesc_qk = make_idesc(1, 1, false, false, 128, kMlaHeads);
-      const uint32_t idesc_pv = make_idesc(0, 0, true, true, 128, kMlaHeads);
-      const uint32_t idesc_sum = make_idesc(0, 0, false, true, 128, kMlaHeads);
-      const uint64_t d_c = make_sdesc_sw128(smem_u32(smem + OFF_RING), 16, 1024);      // C chunk, K-major
-      const uint64_t d_q = make_sdesc_sw128(smem_u32(smem + OFF_Q), 16, 1024);         // q chunk, K-major
-      const uint64_t d_v = make_sdesc_sw128(smem_u32(smem + OFF_RING), 8192, 1024);    // V^T, MN-major
-      const uint64_t d_p = make_sdesc_sw128(smem_u32(smem + OFF_P), 16384, 1024);      // P^T, MN-major
-      const uint64_t d_one = make_sdesc_sw128(smem_u32(smem + OFF_ONES), 16, 0);       // the ones atom, repeated
-      constexpr uint64_t kSlot = RING_SLOT >> 4;
-      int fc = 0, it = 0;
-      bool ok = true;
-      for (int seg = 0; ok && walk.next(s); ++seg) {
-        ok = mbar_wait(q_full, seg & 1, ab);
-        for (int j = s.j0; ok && j < s.j1; ++j, ++it) {
-          if (it > 0 && !(ok = mbar_wait(s_free, (it - 1) & 1, ab))) break;
-#pragma unroll 1
-          for (int kc = 0; kc < QCHUNKS; ++kc, ++fc) {
-            const int slot = fc % RSLOTS;
-            if (!(ok = mbar_wait_inline(&ring_full[slot], (fc / RSLOTS) & 1, ab))) break;
-            tc_fence_after();
-            const uint64_t a = d_c + slot * kSlot;
-            const uint64_t b = d_q + kc * (Q_SLOT >> 4);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) mma_f16(tmem + S_COL, a + 2 * kk, b + 2 * kk, idesc_qk, (kc | kk) ? 1u : 0u);
-            tc_commit(&ring_empty[slot]);
-          }
-          if (!ok) break;
-          tc_commit(s_full);
-          if (j == s.j1 - 1) tc_commit(q_done);
-          if (!(ok = mbar_wait(p_full, it & 1, ab))) break;
-          tc_fence_after();
-#pragma unroll
-          for (int kh = 0; kh < 2; ++kh)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_f16(tmem + S_COL, d_one + 2 * k, d_p + (kh * 8 + k * 2) * 64, idesc_sum, (kh | k) ? 1u : 0u);
-          tc_commit(sum_done);
-          const bool first = j == s.j0;
-          if (first && seg > 0 && !(ok = mbar_wait(o_free, (seg - 1) & 1, ab))) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int f = 0; f < 8; ++f) {   // half-block f: dims [128 (f / 2), +128), tokens [64 (f % 2), +64)
-            if (!(ok = mbar_wait_inline(&ring_full[fc % RSLOTS], (fc / RSLOTS) & 1, ab))) break;
-            const uint64_t a = d_v + (fc % RSLOTS) * kSlot;
-            const int kh = f & 1;
-            tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_f16(tmem + O_COL + 96 * (f >> 1), a + 128 * k, d_p + (kh * 8 + k * 2) * 64, idesc_pv,
-                      (!first || kh > 0 || k > 0) ? 1u : 0u);
-            tc_commit(&ring_empty[fc % RSLOTS]);
-            ++fc;
-          }
-          if (!ok) break;
-          tc_commit(o_done);
-        }
-      }
-      if (!ok) {
-        tc_commit(drain);
-        drain_wait(drain, 0);
-      }
-    }
-  } else {
-    const bool conv = warp < SOFT_WARP0;
-    const int mw = warp - 2;                        // 0..11
-    const int quarter = warp & 3;
-    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    int fc = 0, it = 0;
-    bool ok = true;
-    for (int seg = 0; walk.next(s); ++seg) {
-      int req, pos, base;
-      load_tree_token(p.b, p.tree, s.t, p.status, req, pos, base);
-      if (conv) {
-        // ----------------------------------------------------- converters (2..9)
-        const int ct = threadIdx.x - 64;            // 0..255
-        const int row = ct >> 1, hf = ct & 1;       // this thread's half row: dims [64 kc + 32 hf, +32) of each chunk
-        const int vg = (ct >> 5) >> 2;              // V half-block of this warp's rows: tokens [64 vg, +64)
-        const int tl = row & 63;
-        const int bsm = p.pool.bs - 1;
-        const int32_t* btrow = p.b.bt + static_cast<int64_t>(req) * p.b.bt_stride;
-        const uint32_t* mrow = p.tree.mask + static_cast<int64_t>(s.t) * p.tree.words;
-        for (int j = s.j0; j < s.j1; ++j, ++it) {
-          const int sv = j * kSelTile + row;
-          const uint8_t* src = nullptr;
-          if (sv <= pos && tree_sees(mrow, p.tree.words, base, sv)) {
-            const int prow = __ldg(btrow + (sv >> p.pool.log2_bs));
-            if (prow < 0 || prow >= p.pool.num_rows) {
-              if (hf == 0) atomicOr(p.status, DEV_BAD_BLOCK);
-            } else {
-              src = p.pool.pool + static_cast<int64_t>(prow) * p.pool.row_stride + p.pool.lat_off +
-                    static_cast<int64_t>(sv & bsm) * ROWB;
-            }
-          }
-          // The flags of tile it - 2 have been used: this warp's last V fills of tile it - 1 waited
-          // for that tile's PV to start, which follows its softmax.
-          if (hf == 0) rowok[(it & 1) * kSelTile + row] = src != nullptr;
-          __syncwarp();
-          if (ok && lane == 0) mbar_arrive(rows_ready);
-          LatPiece cb[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) cb[u] = load_piece<true>(src, u, hf);
-#pragma unroll 1
-          for (int kb = 0; kb < QCHUNKS; kb += 4) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const int kc = kb + u;
-              if (kc >= QCHUNKS) break;
-              const int slot = fc % RSLOTS;
-              if (fc >= RSLOTS) ok = warp_wait(&ring_empty[slot], ((fc / RSLOTS) - 1) & 1, ab, ok);
-              if (ok) {
-                uint8_t* dst = smem + OFF_RING + slot * RING_SLOT + (row >> 3) * 1024;
-#pragma unroll
-                for (int q2 = 0; q2 < 2; ++q2) {
-                  const int q4 = 2 * hf + q2;
-                  uint32_t o[8];
-                  piece_to_bf16<true>(cb[u], q2, o);
-                  sts128(dst + sw128_off(row & 7, 2 * q4), o);
-                  sts128(dst + sw128_off(row & 7, 2 * q4 + 1), o + 4);
-                }
-                fence_proxy_async_smem();
-              }
-              __syncwarp();
-              if (ok && lane == 0) mbar_arrive(&ring_full[slot]);
-              ++fc;
-              if (kc + 4 < QCHUNKS) cb[u] = load_piece<true>(src, kc + 4, hf);
-            }
-          }
-          // V half-blocks: the warps of rows 0..63 fill the even ring fills, the others the odd ones
-#pragma unroll 1
-          for (int v = 0; v < 4; ++v) {
-            LatPiece c0 = load_piece<true>(src, 2 * v, hf), c1 = load_piece<true>(src, 2 * v + 1, hf);
-            const int myfc = fc + 2 * v + vg;
-            const int slot = myfc % RSLOTS;
-            if (myfc >= RSLOTS) ok = warp_wait(&ring_empty[slot], ((myfc / RSLOTS) - 1) & 1, ab, ok);
-            if (ok) {
-              uint8_t* dst = smem + OFF_RING + slot * RING_SLOT + (tl >> 3) * 1024;
-#pragma unroll
-              for (int a = 0; a < 2; ++a) {
-#pragma unroll
-                for (int q2 = 0; q2 < 2; ++q2) {
-                  const int q4 = 2 * hf + q2;
-                  uint32_t o[8];
-                  piece_to_f16<true>(a ? c1 : c0, q2, o);
-                  sts128(dst + a * 8192 + sw128_off(tl & 7, 2 * q4), o);
-                  sts128(dst + a * 8192 + sw128_off(tl & 7, 2 * q4 + 1), o + 4);
-                }
-              }
-              fence_proxy_async_smem();
-            }
-            __syncwarp();
-            if (ok && lane == 0) mbar_arrive_cnt(&ring_full[slot], 2);   // four warps complete a fill
-          }
-          fc += 8;
-        }
-      } else {
-        // ---------------------------------------------- softmax warps (10..13)
-        const int r = quarter * 32 + lane;          // token lane within the tile
-        float m_run[3] = {-INFINITY, -INFINITY, -INFINITY};   // per head (lane + 32 i), log2 units
-        float l_run[3] = {0.f, 0.f, 0.f};                      // first softmax warp only
-        float alpha_r[3] = {1.f, 1.f, 1.f};
-        for (int j = s.j0; j < s.j1; ++j, ++it) {
-          ok = warp_wait(s_full, it & 1, ab, ok);
-          ok = warp_wait(rows_ready, it & 1, ab, ok);
-          tc_fence_after();
-          const bool valid = rowok[(it & 1) * kSelTile + r] != 0;
-#pragma unroll 1
-          for (int c = 0; c < 3; ++c) {
-            uint32_t rr[32];
-            DSA_TMEM_LD32(tmem + S_COL + 32 * c + lane_off, rr);
-            tmem_wait_ld();
-            float mine = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float m = warp_max_f32(valid ? __uint_as_float(rr[i]) * p.scale_log2 : -INFINITY);
-              if (lane == i) mine = m;
-            }
-            red[quarter * kMlaHeads + 32 * c + lane] = mine;
-          }
-          named_bar_sync(1, 128);
-          if (warp == SOFT_WARP0) {
-            bool moved = false;
-#pragma unroll
-            for (int i = 0; i < 3; ++i) {
-              const int h = lane + 32 * i;
-              const float tm =
-                  fmaxf(fmaxf(red[h], red[kMlaHeads + h]), fmaxf(red[2 * kMlaHeads + h], red[3 * kMlaHeads + h]));
-              const float mo = m_run[i];
-              const float mn = (tm > mo + TAU) ? tm : mo;
-              alpha_r[i] = (mn == mo) ? 1.f : exp2f(mo - mn);
-              m_run[i] = mn;
-              m_use[h] = mn == -INFINITY ? 0.f : mn;
-              alpha_sh[h] = alpha_r[i];
-              moved |= (mn != mo);
-            }
-            moved = __any_sync(0xffffffffu, moved);
-            if (lane == 0) *rescale_sh = (moved && j > s.j0) ? 1 : 0;
-          }
-          named_bar_sync(1, 128);
-          const bool any_rescale = *reinterpret_cast<volatile int*>(rescale_sh) != 0;
-          // PV of the tile before must be done before P is overwritten or O rescaled
-          if (it > 0) ok = warp_wait(o_done, (it - 1) & 1, ab, ok);
-          if (any_rescale && ok) {
-            tc_fence_after();
-#pragma unroll 1
-            for (int v = 0; v < 4; ++v) {
-#pragma unroll 1
-              for (int c = 0; c < 3; ++c) {
-                uint32_t rr[32];
-                const uint32_t ta = tmem + O_COL + 96 * v + 32 * c + lane_off;
-                DSA_TMEM_LD32(ta, rr);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 32; ++i) rr[i] = __float_as_uint(__uint_as_float(rr[i]) * alpha_sh[32 * c + i]);
-                DSA_TMEM_ST32(ta, rr);
-              }
-            }
-            tmem_wait_st();
-          }
-          {
-            uint8_t* prow = smem + OFF_P + (r >> 3) * 1024;
-#pragma unroll 1
-            for (int c = 0; c < 3; ++c) {
-              uint32_t rr[32];
-              DSA_TMEM_LD32(tmem + S_COL + 32 * c + lane_off, rr);
-              tmem_wait_ld();
-              float pv[32];
-              lds_f32x32(m_use + 32 * c, pv);
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                pv[i] = valid ? ex2_fast(__uint_as_float(rr[i]) * p.scale_log2 - pv[i]) : 0.f;
-#pragma unroll
-              for (int cc4 = 0; cc4 < 4; ++cc4) {
-                uint32_t o[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const __half2 hp = __floats2half2_rn(pv[8 * cc4 + 2 * i], pv[8 * cc4 + 2 * i + 1]);
-                  o[i] = *reinterpret_cast<const uint32_t*>(&hp);
-                }
-                const int chunk = 4 * c + cc4;
-                sts128(prow + (chunk >> 3) * 16384 + sw128_off(r & 7, chunk & 7), o);
-              }
-            }
-          }
-          fence_proxy_async_smem();
-          tc_fence_before();
-          __syncwarp();
-          if (ok && lane == 0) {
-            mbar_arrive(p_full);
-            if (warp != SOFT_WARP0) mbar_arrive(s_free);
-          }
-          if (warp == SOFT_WARP0) {
-            ok = warp_wait(sum_done, it & 1, ab, ok);
-            tc_fence_after();
-#pragma unroll
-            for (int c = 0; c < 3; ++c) {
-              float ls = 0.f;
-#pragma unroll 1
-              for (int q = 0; q < 4; ++q) {
-                uint32_t rr[8];
-                DSA_TMEM_LD8(tmem + S_COL + 32 * c + 8 * q + lane_off, rr);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  if (lane == 8 * q + i) ls = __uint_as_float(rr[i]);
-              }
-              l_run[c] = l_run[c] * alpha_r[c] + ls;
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (ok && lane == 0) mbar_arrive(s_free);
-          }
-        }
-        if (warp == SOFT_WARP0) {
-#pragma unroll
-          for (int i = 0; i < 3; ++i) {
-            l_fin[lane + 32 * i] = l_run[i];
-            inv_sh[lane + 32 * i] = l_run[i] == 0.f ? 0.f : 1.f / l_run[i];   // nothing seen: output 0
-          }
-        }
-      }
-      // ---- the segment's result, all 12 math warps: TMEM (thread = dim) -> global
-      ok = warp_wait(o_done, (it - 1) & 1, ab, ok);
-      named_bar_sync(2, 384);
-      tc_fence_after();
-      if (ok) {
-        const int which = mw >> 2;                    // 0..2: the three warps of this lane quarter
-#pragma unroll 1
-        for (int pc = which; pc < 12; pc += 3) {      // (dim block v, head chunk c) pairs
-          const int v = pc / 3, c = pc % 3;
-          uint32_t rr[32];
-          DSA_TMEM_LD32(tmem + O_COL + 96 * v + 32 * c + lane_off, rr);
-          tmem_wait_ld();
-          store_heads<false>(p, s, rr, inv_sh, 32 * c, v * 128 + quarter * 32 + lane);
-        }
-        const int h = mw * 32 + lane;
-        if (h < kMlaHeads) {
-          const float l = l_fin[h];
-          if (s.slot >= 0) p.part_ml[static_cast<int64_t>(s.slot) * kMlaHeads + h] = make_float2(m_use[h], l);
-          else if (p.lse) p.lse[static_cast<int64_t>(s.t) * kMlaHeads + h] = (m_use[h] + log2f(l)) * 0.69314718055994531f;
-        }
-      }
-      tc_fence_before();
-      named_bar_sync(2, 384);   // sums and maxima are read before the next segment writes them
-      if (ok && lane == 0) mbar_arrive(o_free);
-    }
-  }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 1) tmem_dealloc(tmem, 512);
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)),
+        "l"(reinterpret_cast<const uint64_t&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
+  return d;
 }
 
 // ------------------------------------------------- attention with FP8 latents
@@ -634,23 +259,6 @@ __device__ __forceinline__ uint32_t e5m2_term(uint32_t v, uint32_t& rest) {
   const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&hi));
   rest = *reinterpret_cast<const uint32_t*>(&d);
   return t;
-}
-
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(reinterpret_cast<uint64_t&>(d))
-      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)),
-        "l"(reinterpret_cast<const uint64_t&>(c)));
-  return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("add.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<uint64_t&>(d))
-      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
-  return d;
 }
 
 __global__ void __launch_bounds__(t8::THREADS, 1)
@@ -1084,7 +692,515 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
           uint32_t rr[32];
           DSA_TMEM_LD32(tmem + O_COL + 96 * v + 32 * g + lane_off, rr);
           tmem_wait_ld();
-          store_heads<true>(p, s, rr, inv_sh, 32 * g, v * 128 + 32 * quarter + lane);
+          store_heads(p, s, rr, inv_sh, 32 * g, v * 128 + 32 * quarter + lane);
+        }
+      }
+      tc_fence_before();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------- attention with NVFP4 latents
+//
+// An NVFP4 latent (e2m1 times an e4m3 scale per 16) has up to 6 significant bits: exact in
+// fp16, not in any 8-bit type.  Its tiles are converted to fp16 operands, 64 dims of 128
+// tokens (16 KB, a "chunk") at a time; the query arrives as fp16, scaled per head by a
+// power of two (exact: a bf16 has 8 significant bits).
+//   S^T[token, head] = C[token, 0:576] . q[head, 0:576]     M=128, N=96, K=576   (f16)
+//   O^T[dim, head]  += V^T[dim, token] . P^T[token, head]    M=128 (x4 dim blocks), N=96, K=128   (f16)
+// The softmax is that of the FP8 kernel (tokens on lanes, a reference per head that rarely
+// moves, P handed over in three steps), with P in fp16.
+// A chunk is the A operand of both products (K-major, then MN-major).  Beside the query
+// (108 KB) and P (24 KB) five chunks fit, so of the nine that a tile's scores read, the
+// last four stay for the values and the first four are converted again: 13 fills a tile
+// through five fixed places, in the order of the table below.  Fill and use of a place
+// are ordered by one barrier per fill and one per group of MMAs, each once a tile.
+//   scores: chunk 8 in place 3, 0 in 0, 1 in 2, 2 in 1, 3 in 4, 4 in 0, 5 in 3, 6 in 1, 7 in 4
+//   values: dims 256..383 (chunks 4, 5), 384..511 (6, 7), 0..127 (0 in 0, 1 in 2), 128..255 (2 in 1, 3 in 4)
+// The 12 softmax warps convert, too: the four warps of group g (a row of the tile each
+// thread) take the chunks c with c % 3 = g and keep their packed rows in registers from
+// the first fill to the second; the next tile's rows are loaded as they are given up.
+// Warp 12 issues MMAs; warp 13 loads queries.
+namespace t16 {
+constexpr int THREADS = 448;
+constexpr int QCHUNKS = kLatDim / 64;
+constexpr int QCHUNK = 96 * 128;
+constexpr int PLACE = 128 * 128;
+constexpr int OFF_Q = 0;
+constexpr int OFF_C = QCHUNKS * QCHUNK;           // five places
+constexpr int OFF_P = OFF_C + 5 * PLACE;          // three [128 tokens x 32 heads] fp16 blocks, 64-byte swizzle
+constexpr int P_BLOCK = 128 * 64;
+constexpr int OFF_QEXP = OFF_P + 3 * P_BLOCK;     // [96] int
+constexpr int OFF_REDM = OFF_QEXP + 96 * 4;       // [4][96] float
+constexpr int OFF_SH = OFF_REDM + 4 * 96 * 4;     // [96] float
+constexpr int OFF_ALPHA = OFF_SH + 96 * 4;        // [96] float
+constexpr int OFF_INV = OFF_ALPHA + 96 * 4;       // [96] float
+constexpr int OFF_BARS = OFF_INV + 96 * 4;
+constexpr int N_BARS = 32;
+constexpr int OFF_MISC = OFF_BARS + N_BARS * 8;
+constexpr int SMEM_BYTES = OFF_MISC + 64 + 1024;
+constexpr int FILLS = 13;
+// chunk and place of fill f: the scores' nine in their order, then the values' four
+__device__ constexpr int kChunk[FILLS] = {8, 0, 1, 2, 3, 4, 5, 6, 7, 1, 0, 2, 3};
+__device__ constexpr int kPlace[FILLS] = {3, 0, 2, 1, 4, 0, 3, 1, 4, 2, 0, 1, 4};
+// events that free places: the scores of fill f (f < 5) done, or the values of dim block v done
+enum { EV_S8 = 0, EV_S0, EV_S1, EV_S2, EV_S3, EV_V0, EV_V1, EV_V2, EV_V3, EVENTS };
+constexpr int MATH_WARPS = 12;
+constexpr int MATH = MATH_WARPS * 32;
+constexpr int MMA_WARP = 12, LOAD_WARP = 13;
+constexpr int S_COL = 0;
+constexpr int O_COL = 128;
+constexpr float TAU = 4.0f;
+constexpr float SHIFT = 11.0f;                    // weights up to 2^15 in fp16
+static_assert(OFF_C % 1024 == 0 && OFF_P % 1024 == 0, "align");
+static_assert(OFF_SH % 16 == 0 && OFF_ALPHA % 16 == 0 && OFF_INV % 16 == 0 && OFF_QEXP % 16 == 0 && OFF_BARS % 8 == 0,
+              "vectors are read 16 bytes at a time");
+static_assert(SMEM_BYTES <= 232448, "smem");
+}  // namespace t16
+
+// One row of a chunk: 64 packed values and their four scales.
+struct RawRow {
+  uint4 a, b;
+  uint32_t s;
+};
+__device__ __forceinline__ RawRow load_raw(const uint8_t* rec, int chunk) {
+  RawRow r;
+  r.a = r.b = make_uint4(0, 0, 0, 0);
+  r.s = 0;
+  if (rec) {
+    r.a = __ldg(reinterpret_cast<const uint4*>(rec + 32 * chunk));
+    r.b = __ldg(reinterpret_cast<const uint4*>(rec + 32 * chunk + 16));
+    r.s = __ldg(reinterpret_cast<const uint32_t*>(rec + 288 + 4 * chunk));
+  }
+  return r;
+}
+// The row as fp16 into row `row` of a place (128-byte swizzle).
+__device__ __forceinline__ void fill_row(uint8_t* place, int row, const RawRow& r) {
+  uint8_t* dst = place + (row >> 3) * 1024;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint4 w = q < 2 ? r.a : r.b;
+    uint32_t o[8];
+    nvfp4x16_to_f16(q & 1 ? make_uint2(w.z, w.w) : make_uint2(w.x, w.y), (r.s >> (8 * q)) & 0xFFu, o);
+    sts128(dst + sw128_off(row & 7, 2 * q), o);
+    sts128(dst + sw128_off(row & 7, 2 * q + 1), o + 4);
+  }
+}
+
+__global__ void __launch_bounds__(t16::THREADS, 1)
+    tree_mla_nvfp4_kernel(const __grid_constant__ CUtensorMap qmap, TreeMlaParams p) {
+  using namespace t16;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024_tree(smem_raw);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BARS);
+  uint64_t* full = bars + 0;        // [FILLS]
+  uint64_t* event = bars + 13;      // [EVENTS]
+  uint64_t* q_full = bars + 22;
+  uint64_t* q_done = bars + 23;
+  uint64_t* s_full = bars + 24;
+  uint64_t* o_done = bars + 25;
+  uint64_t* drain = bars + 26;
+  uint64_t* p_full = bars + 27;     // [3]
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
+  int* abortf = reinterpret_cast<int*>(smem + OFF_MISC + 8);
+  int* first_sh = reinterpret_cast<int*>(smem + OFF_MISC + 16);
+  float* red = reinterpret_cast<float*>(smem + OFF_REDM);
+  float* sh_sh = reinterpret_cast<float*>(smem + OFF_SH);
+  float* alpha_sh = reinterpret_cast<float*>(smem + OFF_ALPHA);
+  float* inv_sh = reinterpret_cast<float*>(smem + OFF_INV);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < FILLS; ++i) mbar_init(&full[i], 4);
+    for (int i = 13; i < 27; ++i) mbar_init(&bars[i], 1);
+    for (int i = 0; i < 3; ++i) mbar_init(&p_full[i], MATH_WARPS);
+    *abortf = 0;
+    *first_sh = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&qmap);
+  }
+  if (warp == 0) tmem_alloc(tslot, 512);
+  grid_dep_wait();   // the plan and the query
+  grid_dep_launch();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  SegmentWalk walk = make_walk(p, first_sh);
+  const uint32_t tmem = *tslot;
+  const Abort ab{abortf, p.status};
+  Segment s;
+
+  if (warp == LOAD_WARP) {
+    // ------------------------------------------------------------- queries
+    bool ok = true;
+    int q_issued = -1;
+    for (int seg = 0; ok && walk.next(s); ++seg) {
+      if (seg > 0) ok = warp_wait(q_done, (seg - 1) & 1, ab, ok);
+      if (!ok) break;
+      q_issued = seg & 1;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(q_full, QCHUNKS * QCHUNK + kMlaHeads * 4);
+        for (int kc = 0; kc < QCHUNKS; ++kc)
+          tma_load_2d(smem + OFF_Q + kc * QCHUNK, &qmap, q_full, kc * 64, s.t * kMlaHeads);
+        bulk_load(smem + OFF_QEXP, p.q_exps + static_cast<int64_t>(s.t) * kMlaHeads, kMlaHeads * 4, q_full);
+      }
+    }
+    if (!ok && q_issued >= 0 && lane == 0) drain_wait(q_full, q_issued);
+  } else if (warp == MMA_WARP) {
+    // ------------------------------------------------------------ MMA issuer
+    const bool leader = elect_one();
+    const uint32_t idesc_qk = make_idesc(0, 0, false, false, 128, kMlaHeads);
+    const uint32_t idesc_pv = make_idesc(0, 0, true, true, 128, kMlaHeads);
+    const uint64_t dq = make_sdesc_sw128(smem_u32(smem + OFF_Q), 16, 1024);   // query, K-major
+    const uint64_t dc = make_sdesc_sw128(smem_u32(smem + OFF_C), 16, 1024);   // chunks, K-major (scores)
+    // Values: step i takes the tokens 8 i .. 8 i + 7 of every lane quarter (rows 32 apart), two
+    // quarters an MMA; the second 64 dims of a block lie 2 or 3 places behind the first.
+    const uint64_t dv2 = make_sdesc_sw128(smem_u32(smem + OFF_C), 2 * PLACE, 4096);
+    const uint64_t dv3 = make_sdesc_sw128(smem_u32(smem + OFF_C), 3 * PLACE, 4096);
+    const uint64_t dp = make_sdesc_sw64(smem_u32(smem + OFF_P), P_BLOCK, 2048);
+    auto values = [&](int v, int i, uint32_t acc) {
+      // first place of dim block v: 0 and 1 hold chunks (0, 1) in 0 and 2, (2, 3) in 1 and 4; 2 and 3 the kept ones
+      const uint64_t a = (v == 0 ? dv2 : dv3) + (((v & 1) * PLACE + i * 1024) >> 4);
+      const uint64_t b = dp + ((512 * i) >> 4);
+      const uint32_t d = tmem + O_COL + 96 * v;
+      mma_f16(d, a, b, idesc_pv, acc);
+      mma_f16(d, a + (8192 >> 4), b + (4096 >> 4), idesc_pv, 1u);
+    };
+    bool ok = true;
+    int it = 0;
+    for (int seg = 0; ok && walk.next(s); ++seg) {
+      ok = warp_wait(q_full, seg & 1, ab, ok);
+      for (int j = s.j0; ok && j < s.j1; ++j, ++it) {
+        ok = warp_wait(&full[0], it & 1, ab, ok);
+        tc_fence_after();
+#pragma unroll
+        for (int f = 0; f < 9; ++f) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            if (leader && ok) {
+#pragma unroll
+              for (int kk = 2 * half; kk < 2 * half + 2; ++kk)
+                mma_f16(tmem + S_COL, dc + ((kPlace[f] * PLACE + 32 * kk) >> 4), dq + ((kChunk[f] * QCHUNK + 32 * kk) >> 4),
+                        idesc_qk, (f | kk) ? 1u : 0u);
+              if (half == 1 && f < 5) tc_commit(&event[EV_S8 + f]);
+            }
+            __syncwarp();
+            if (half == 0 && f < 8) {   // the next chunk is awaited while the tensor core has work
+              ok = warp_wait(&full[f + 1], it & 1, ab, ok);
+              tc_fence_after();
+            }
+          }
+        }
+        if (!ok) break;
+        if (leader) tc_commit(s_full);
+        __syncwarp();
+        const uint32_t acc = j > s.j0 ? 1u : 0u;
+        const bool last = j == s.j1 - 1;
+        if (!(ok = warp_wait(&p_full[0], it & 1, ab, ok))) break;
+        tc_fence_after();
+        if (leader) {
+          if (last) tc_commit(q_done);   // every softmax warp is past its own wait for the query
+          values(3, 0, acc);
+          values(2, 0, acc);
+        }
+        __syncwarp();
+        if (!(ok = warp_wait(&p_full[1], it & 1, ab, ok))) break;
+        tc_fence_after();
+        if (leader) values(2, 1, 1u);
+        __syncwarp();
+        if (!(ok = warp_wait(&p_full[2], it & 1, ab, ok))) break;
+        tc_fence_after();
+        if (leader) {
+          values(2, 2, 1u);
+          values(2, 3, 1u);
+          tc_commit(&event[EV_V2]);
+          values(3, 1, 1u);
+          values(3, 2, 1u);
+          values(3, 3, 1u);
+          tc_commit(&event[EV_V3]);
+        }
+        __syncwarp();
+        ok = warp_wait(&full[9], it & 1, ab, ok);
+        if (!(ok = warp_wait(&full[10], it & 1, ab, ok))) break;
+        tc_fence_after();
+        if (leader) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) values(0, i, i ? 1u : acc);
+          tc_commit(&event[EV_V0]);
+        }
+        __syncwarp();
+        ok = warp_wait(&full[11], it & 1, ab, ok);
+        if (!(ok = warp_wait(&full[12], it & 1, ab, ok))) break;
+        tc_fence_after();
+        if (leader) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) values(1, i, i ? 1u : acc);
+          tc_commit(&event[EV_V1]);
+          if (last) tc_commit(o_done);
+        }
+        __syncwarp();
+      }
+    }
+    if (!ok && leader) {
+      tc_commit(drain);
+      drain_wait(drain, 0);
+    }
+    __syncwarp();
+  } else {
+    // -------------------------------- conversion, softmax and epilogue (0..11)
+    const int quarter = warp & 3, g = warp >> 2;
+    const int a = lane & 3, r4 = lane >> 2;
+    const int crow = 32 * quarter + lane;          // this thread's row of a chunk
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const int my_head = 32 * g + head_of_column(lane);
+    const int lg = p.pool.log2_bs, bsm = p.pool.bs - 1;
+    bool ok = true;
+    int it = 0;
+    // Fill f with a row, once the place is free (the event's phase `par`; none on the first tile).
+    auto fill = [&](int f, const RawRow& r, int ev, uint32_t par, bool wait) {
+      if (wait) ok = warp_wait(&event[ev], par, ab, ok);
+      if (ok) {
+        fill_row(smem + OFF_C + kPlace[f] * PLACE, crow, r);
+        fence_proxy_async_smem();
+      }
+      __syncwarp();
+      if (ok && lane == 0) mbar_arrive(&full[f]);
+    };
+    for (int seg = 0; walk.next(s); ++seg) {
+      int req, pos, base;
+      load_tree_token(p.b, p.tree, s.t, p.status, req, pos, base);
+      const uint32_t* mrow = p.tree.mask + static_cast<int64_t>(s.t) * p.tree.words;
+      const int32_t* btrow = p.b.bt + static_cast<int64_t>(req) * p.b.bt_stride;
+      const int plain = min(base, pos + 1);   // positions below are all seen
+      // the latent record of this thread's row in tile j, null (zeros) where nobody sees it
+      auto record = [&](int j) -> const uint8_t* {
+        const int sv = j * kSelTile + crow;
+        if (j >= s.j1 || !(sv < plain || (sv <= pos && tree_sees(mrow, p.tree.words, base, sv)))) return nullptr;
+        const int32_t id = __ldg(btrow + (sv >> lg));
+        if (id < 0 || id >= p.pool.num_rows) {
+          atomicOr(p.status, DEV_BAD_BLOCK);
+          return nullptr;
+        }
+        return p.pool.pool + static_cast<int64_t>(id) * p.pool.row_stride + p.pool.lat_off +
+               static_cast<int64_t>(sv & bsm) * 352;
+      };
+      // A row's record is prefetched into L2 two tiles ahead, 128 bytes by each group's thread.
+      auto prefetch = [&](const uint8_t* r) {
+        if (r) asm volatile("prefetch.global.L2 [%0];" ::"l"(r + 128 * g));
+      };
+      const uint8_t* rec = record(s.j0);
+      const uint8_t* next = record(s.j0 + 1);
+      prefetch(next);
+      // packed rows of the group's three chunks: g, g + 3, g + 6
+      RawRow w0 = load_raw(rec, g), w1 = load_raw(rec, g + 3), w2 = load_raw(rec, g + 6);
+      ok = warp_wait(q_full, seg & 1, ab, ok);
+      float2 c2[4], sh2[4], l2[4];            // per head pair b: logit scale (log2 units), SHIFT - reference, sum
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int2 qe = *reinterpret_cast<const int2*>(smem + OFF_QEXP + 4 * (32 * g + 8 * b + 2 * a));
+        c2[b] = make_float2(p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - qe.x) << 23),
+                            p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - qe.y) << 23));
+        sh2[b] = make_float2(INFINITY, INFINITY);   // any logit seen exceeds the reference
+        l2[b] = make_float2(0.f, 0.f);
+      }
+      float m_ref = -INFINITY;                // quarter 0: reference of column 32 g + lane
+      for (int j = s.j0; j < s.j1; ++j, ++it) {
+        const uint32_t par = it & 1, prev = par ^ 1;
+        const bool again = it > 0;
+        const uint8_t* after = record(j + 2);
+        prefetch(after);
+        // ---- the scores' chunks
+        if (g == 0) {
+          fill(1, w0, EV_V0, prev, again);    // chunk 0
+          fill(4, w1, EV_V1, prev, again);    // chunk 3
+          fill(7, w2, EV_S2, par, true);      // chunk 6
+        } else if (g == 1) {
+          fill(2, w0, EV_V0, prev, again);    // chunk 1
+          fill(5, w1, EV_S0, par, true);      // chunk 4
+          fill(8, w2, EV_S3, par, true);      // chunk 7
+          fill(9, w0, EV_S1, par, true);      // chunk 1 again, for the values
+        } else {
+          fill(0, w2, EV_V2, prev, again);    // chunk 8
+          fill(3, w0, EV_V1, prev, again);    // chunk 2
+          fill(6, w1, EV_S8, par, true);      // chunk 5
+        }
+        // what is not needed again gives way to the next tile's rows
+        w2 = load_raw(next, g + 6);
+        if (g != 0) w1 = load_raw(next, g + 3);
+        if (g == 1) w0 = load_raw(next, g);
+        // ---- softmax (as in the FP8 kernel)
+        ok = warp_wait(s_full, par, ab, ok);
+        tc_fence_after();
+        uint32_t rr[2][16];
+        const uint32_t ts = tmem + S_COL + 32 * g + lane_off;
+        DSA_TMEM_LD_16X256_X4(ts, rr[0]);
+        tmem_wait_ld();
+        DSA_TMEM_LD_16X256_X4(ts + (16u << 16), rr[1]);   // lands while the first half is scaled
+        uint32_t seen = 15u;                  // bit i: token i of this thread is seen
+        if ((j + 1) * kSelTile > plain) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int s0 = j * kSelTile + 32 * quarter + r4 + 8 * i;
+            if (!(s0 <= pos && tree_sees(mrow, p.tree.words, base, s0))) seen &= ~(1u << i);
+          }
+        }
+        float2 y[4][4];
+        auto raw = [&](int i, int b) {
+          return make_float2(__uint_as_float(rr[i >> 1][4 * b + 2 * (i & 1)]),
+                             __uint_as_float(rr[i >> 1][4 * b + 2 * (i & 1) + 1]));
+        };
+        auto logits = [&](int i0) {
+          float mx = -INFINITY;
+#pragma unroll
+          for (int i = i0; i < i0 + 2; ++i) {
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              y[i][b] = fma2(raw(i, b), c2[b], sh2[b]);
+              if (!((seen >> i) & 1u)) y[i][b] = make_float2(-INFINITY, -INFINITY);
+              mx = fmaxf(fmaxf(mx, y[i][b].x), y[i][b].y);
+            }
+          }
+          return mx;
+        };
+        float mx = logits(0);
+        tmem_wait_ld();
+        mx = fmaxf(mx, logits(2));
+        if (named_bar_any(1, MATH, mx > SHIFT + TAU)) {
+          // P of the tile before has been used (s_full follows its values); some reference moves
+          float hm[8];
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            hm[2 * b] = hm[2 * b + 1] = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 x = raw(i, b);
+              if ((seen >> i) & 1u) {
+                hm[2 * b] = fmaxf(hm[2 * b], x.x * c2[b].x);
+                hm[2 * b + 1] = fmaxf(hm[2 * b + 1], x.y * c2[b].y);
+              }
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) hm[k] = fmaxf(hm[k], __shfl_xor_sync(0xffffffffu, hm[k], o));
+          if (r4 == 0) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) red[quarter * kMlaHeads + 32 * g + 8 * a + k] = hm[k];
+          }
+          named_bar_sync(2, MATH);
+          if (quarter == 0) {
+            const int n = 32 * g + lane;
+            const float m = fmaxf(fmaxf(red[n], red[kMlaHeads + n]), fmaxf(red[2 * kMlaHeads + n], red[3 * kMlaHeads + n]));
+            float alpha = 1.f;
+            if (m > m_ref + TAU) {
+              alpha = exp2f(m_ref - m);
+              m_ref = m;
+            }
+            sh_sh[n] = m_ref == -INFINITY ? INFINITY : SHIFT - m_ref;
+            alpha_sh[n] = alpha;
+          }
+          named_bar_sync(2, MATH);
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const float2 av = *reinterpret_cast<const float2*>(alpha_sh + 32 * g + 8 * a + 2 * b);
+            sh2[b] = *reinterpret_cast<const float2*>(sh_sh + 32 * g + 8 * a + 2 * b);
+            l2[b].x *= av.x;
+            l2[b].y *= av.y;
+          }
+          if (j > s.j0 && ok) {
+#pragma unroll 1
+            for (int v = 0; v < 4; ++v) {
+#pragma unroll 1
+              for (int cc = 0; cc < 4; ++cc) {
+                uint32_t o[8];
+                const uint32_t ta = tmem + O_COL + 96 * v + 32 * g + 8 * cc + lane_off;
+                DSA_TMEM_LD8(ta, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha_sh[32 * g + 8 * cc + i]);
+                DSA_TMEM_ST8(ta, o);
+              }
+            }
+            tmem_wait_st();
+          }
+          logits(0);
+          logits(2);
+        }
+        tc_fence_before();   // the scores are in registers
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t t0[4];    // 8 weights in fp16
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            float2 pe = y[i][b];
+            pe.x = ex2_fast(pe.x);
+            pe.y = ex2_fast(pe.y);
+            l2[b] = add2(l2[b], pe);
+            const __half2 ph = __floats2half2_rn(pe.x, pe.y);
+            t0[b] = *reinterpret_cast<const uint32_t*>(&ph);
+          }
+          if (ok) {
+            // row of 32 heads, 64 bytes; 64-byte swizzle: the 16-byte piece moves by (row / 2) % 4
+            const int row = 32 * quarter + 8 * i + r4;
+            sts128(smem + OFF_P + g * P_BLOCK + row * 64 + ((a ^ ((row >> 1) & 3)) << 4), t0);
+            if (i != 2) fence_proxy_async_smem();
+          }
+          if (i != 2) {
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(&p_full[i < 2 ? i : 2]);
+          }
+        }
+        // ---- the values' chunks that did not stay, as the places come free
+        if (g == 0) {
+          fill(10, w0, EV_V2, par, true);     // chunk 0
+          w0 = load_raw(next, g);
+          fill(12, w1, EV_V3, par, true);     // chunk 3
+          w1 = load_raw(next, g + 3);
+        } else if (g == 2) {
+          fill(11, w0, EV_V3, par, true);     // chunk 2
+          w0 = load_raw(next, g);
+        }
+        next = after;
+      }
+      // ---- the segment's result: sums over the tokens, then TMEM (thread = dim) -> global
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          l2[b].x += __shfl_xor_sync(0xffffffffu, l2[b].x, o);
+          l2[b].y += __shfl_xor_sync(0xffffffffu, l2[b].y, o);
+        }
+      if (r4 == 0) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          *reinterpret_cast<float2*>(red + quarter * kMlaHeads + 32 * g + 8 * a + 2 * b) = l2[b];
+      }
+      named_bar_sync(2, MATH);
+      if (quarter == 0) {
+        const int n = 32 * g + lane;
+        const float l = (red[n] + red[kMlaHeads + n]) + (red[2 * kMlaHeads + n] + red[3 * kMlaHeads + n]);
+        inv_sh[n] = l == 0.f ? 0.f : 1.f / l;   // nothing seen: output 0
+        const float m = m_ref == -INFINITY ? 0.f : m_ref - SHIFT;
+        if (ok) {
+          if (s.slot >= 0) p.part_ml[static_cast<int64_t>(s.slot) * kMlaHeads + my_head] = make_float2(m, l);
+          else if (p.lse) p.lse[static_cast<int64_t>(s.t) * kMlaHeads + my_head] = (m + log2f(l)) * 0.69314718055994531f;
+        }
+      }
+      named_bar_sync(2, MATH);
+      ok = warp_wait(o_done, seg & 1, ab, ok);
+      tc_fence_after();
+      if (ok) {
+#pragma unroll 1
+        for (int v = 0; v < 4; ++v) {
+          uint32_t rr[32];
+          DSA_TMEM_LD32(tmem + O_COL + 96 * v + 32 * g + lane_off, rr);
+          tmem_wait_ld();
+          store_heads(p, s, rr, inv_sh, 32 * g, v * 128 + 32 * quarter + lane);
         }
       }
       tc_fence_before();
@@ -1173,9 +1289,9 @@ cudaError_t launch_tree_mla_fp8(const CUtensorMap& lmap, const CUtensorMap& tmap
 
 cudaError_t launch_tree_mla_nvfp4(const CUtensorMap& qmap, const TreeMlaParams& p, cudaStream_t st) {
   cudaError_t e = set_func_attr_once(reinterpret_cast<const void*>(tree_mla_nvfp4_kernel),
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, tconv::SMEM_BYTES);
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, t16::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  e = launch_ex(tree_mla_nvfp4_kernel, dim3(p.max_ctas), dim3(tconv::THREADS), tconv::SMEM_BYTES, st, true, 0u, qmap, p);
+  e = launch_ex(tree_mla_nvfp4_kernel, dim3(p.max_ctas), dim3(t16::THREADS), t16::SMEM_BYTES, st, true, 0u, qmap, p);
   return e != cudaSuccess ? e : launch_combine(p, st);
 }
 

@@ -19,6 +19,7 @@ struct TreeMlaParams {
   float scale_log2;          // sm_scale * log2(e)
   const int64_t* starts;     // [T + 1]
   const uint8_t* q_terms;    // FP8 latents: [T] query terms (mla_q.cuh)
+  const int32_t* q_exps;     // NVFP4 latents: [T, 96] exponents of the fp16 query's scales
   int max_ctas;              // G = min(max_ctas, W)
   int whole;
   __nv_bfloat16* out;        // [T, 96, 512]
@@ -76,13 +77,14 @@ __host__ __device__ inline int share_of(int64_t W, int G, int64_t u) {
   return static_cast<int>(((u + 1) * G - 1) / W);
 }
 
-// The list of tiles (starts), and with `terms` the query terms of every token.
+// The list of tiles (starts), and the queries as `terms` (FP8 latents) or as `q16` and `exps`
+// (NVFP4 latents; terms null).
 cudaError_t launch_tree_prep(const BatchView& b, const TreeView& tree, const __nv_bfloat16* q, uint8_t* terms,
-                             int64_t* starts, uint32_t* status, cudaStream_t st);
+                             __half* q16, int32_t* exps, int64_t* starts, uint32_t* status, cudaStream_t st);
 // FP8 latents: `lmap` boxes of 128 dims, `tmap` of the last 64 (both of up to 128 positions of a page).
 cudaError_t launch_tree_mla_fp8(const CUtensorMap& lmap, const CUtensorMap& tmap, const TreeMlaParams& p,
                                 cudaStream_t st);
-// NVFP4 latents.
+// NVFP4 latents; `qmap` over the fp16 queries.
 cudaError_t launch_tree_mla_nvfp4(const CUtensorMap& qmap, const TreeMlaParams& p, cudaStream_t st);
 
 }  // namespace dsa
