@@ -746,6 +746,8 @@ constexpr int FILLS = 13;
 // chunk and place of fill f: the scores' nine in their order, then the values' four
 __device__ constexpr int kChunk[FILLS] = {8, 0, 1, 2, 3, 4, 5, 6, 7, 1, 0, 2, 3};
 __device__ constexpr int kPlace[FILLS] = {3, 0, 2, 1, 4, 0, 3, 1, 4, 2, 0, 1, 4};
+// the same for a fill known at run time (4 bits each)
+__device__ __forceinline__ int place_of_fill(int f) { return static_cast<int>((0x4102413041203ull >> (4 * f)) & 15); }
 // events that free places: the scores of fill f (f < 5) done, or the values of dim block v done
 enum { EV_S8 = 0, EV_S0, EV_S1, EV_S2, EV_S3, EV_V0, EV_V1, EV_V2, EV_V3, EVENTS };
 constexpr int MATH_WARPS = 12;
@@ -959,11 +961,18 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
     const int lg = p.pool.log2_bs, bsm = p.pool.bs - 1;
     bool ok = true;
     int it = 0;
-    // Fill f with a row, once the place is free (the event's phase `par`; none on the first tile).
-    auto fill = [&](int f, const RawRow& r, int ev, uint32_t par, bool wait) {
-      if (wait) ok = warp_wait(&event[ev], par, ab, ok);
+    // This group's chunks in the order of their fills, and what frees the places (an event of
+    // this tile, or, bit 8, of the one before): chunk, fill, event.
+    const int chunk0 = g == 2 ? 8 : g, chunk1 = g == 2 ? 2 : g + 3, chunk2 = g == 2 ? 5 : g + 6;
+    const int fill0 = g == 2 ? 0 : g + 1;                       // then + 3, + 6
+    const int ev0 = (g == 2 ? EV_V2 : EV_V0) | 256, ev1 = g == 1 ? EV_S0 : (EV_V1 | 256),
+              ev2 = g == 0 ? EV_S2 : (g == 1 ? EV_S3 : EV_S8);
+    // Fills a place with a row once it is free (on the CTA's first tile all of them are).
+    auto fill = [&](int f, const RawRow& r, int ev) {
+      const uint32_t par = (it & 1) ^ (ev >> 8);
+      if (it > 0 || ev < 256) ok = warp_wait(&event[ev & 255], par, ab, ok);
       if (ok) {
-        fill_row(smem + OFF_C + kPlace[f] * PLACE, crow, r);
+        fill_row(smem + OFF_C + place_of_fill(f) * PLACE, crow, r);
         fence_proxy_async_smem();
       }
       __syncwarp();
@@ -975,27 +984,30 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
       const uint32_t* mrow = p.tree.mask + static_cast<int64_t>(s.t) * p.tree.words;
       const int32_t* btrow = p.b.bt + static_cast<int64_t>(req) * p.b.bt_stride;
       const int plain = min(base, pos + 1);   // positions below are all seen
-      // the latent record of this thread's row in tile j, null (zeros) where nobody sees it
-      auto record = [&](int j) -> const uint8_t* {
+      // The pool row of this thread's position in tile j (-1 where nobody sees it) is read three
+      // tiles ahead; its record is prefetched into L2 two ahead (128 bytes by each group's
+      // thread) and read one ahead.
+      auto block = [&](int j) {
         const int sv = j * kSelTile + crow;
-        if (j >= s.j1 || !(sv < plain || (sv <= pos && tree_sees(mrow, p.tree.words, base, sv)))) return nullptr;
+        if (j >= s.j1 || !(sv < plain || (sv <= pos && tree_sees(mrow, p.tree.words, base, sv)))) return -1;
         const int32_t id = __ldg(btrow + (sv >> lg));
+        return id == -1 ? -2 : id;   // (an id of -1 in the table is out of range, too)
+      };
+      auto record = [&](int j, int id) -> const uint8_t* {
+        if (id == -1) return nullptr;
         if (id < 0 || id >= p.pool.num_rows) {
           atomicOr(p.status, DEV_BAD_BLOCK);
           return nullptr;
         }
-        return p.pool.pool + static_cast<int64_t>(id) * p.pool.row_stride + p.pool.lat_off +
-               static_cast<int64_t>(sv & bsm) * 352;
+        const uint8_t* r = p.pool.pool + static_cast<int64_t>(id) * p.pool.row_stride + p.pool.lat_off +
+                           static_cast<int64_t>((j * kSelTile + crow) & bsm) * 352;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(r + 128 * g));
+        return r;
       };
-      // A row's record is prefetched into L2 two tiles ahead, 128 bytes by each group's thread.
-      auto prefetch = [&](const uint8_t* r) {
-        if (r) asm volatile("prefetch.global.L2 [%0];" ::"l"(r + 128 * g));
-      };
-      const uint8_t* rec = record(s.j0);
-      const uint8_t* next = record(s.j0 + 1);
-      prefetch(next);
-      // packed rows of the group's three chunks: g, g + 3, g + 6
-      RawRow w0 = load_raw(rec, g), w1 = load_raw(rec, g + 3), w2 = load_raw(rec, g + 6);
+      const uint8_t* rec = record(s.j0, block(s.j0));
+      const uint8_t* next = record(s.j0 + 1, block(s.j0 + 1));
+      int id2 = block(s.j0 + 2);
+      RawRow x0 = load_raw(rec, chunk0), x1 = load_raw(rec, chunk1), x2 = load_raw(rec, chunk2);
       ok = warp_wait(q_full, seg & 1, ab, ok);
       float2 c2[4], sh2[4], l2[4];            // per head pair b: logit scale (log2 units), SHIFT - reference, sum
 #pragma unroll
@@ -1008,31 +1020,17 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
       }
       float m_ref = -INFINITY;                // quarter 0: reference of column 32 g + lane
       for (int j = s.j0; j < s.j1; ++j, ++it) {
-        const uint32_t par = it & 1, prev = par ^ 1;
-        const bool again = it > 0;
-        const uint8_t* after = record(j + 2);
-        prefetch(after);
-        // ---- the scores' chunks
-        if (g == 0) {
-          fill(1, w0, EV_V0, prev, again);    // chunk 0
-          fill(4, w1, EV_V1, prev, again);    // chunk 3
-          fill(7, w2, EV_S2, par, true);      // chunk 6
-        } else if (g == 1) {
-          fill(2, w0, EV_V0, prev, again);    // chunk 1
-          fill(5, w1, EV_S0, par, true);      // chunk 4
-          fill(8, w2, EV_S3, par, true);      // chunk 7
-          fill(9, w0, EV_S1, par, true);      // chunk 1 again, for the values
-        } else {
-          fill(0, w2, EV_V2, prev, again);    // chunk 8
-          fill(3, w0, EV_V1, prev, again);    // chunk 2
-          fill(6, w1, EV_S8, par, true);      // chunk 5
-        }
-        // what is not needed again gives way to the next tile's rows
-        w2 = load_raw(next, g + 6);
-        if (g != 0) w1 = load_raw(next, g + 3);
-        if (g == 1) w0 = load_raw(next, g);
+        const uint8_t* after = record(j + 2, id2);
+        id2 = block(j + 3);
+        // ---- the scores' chunks; what is not needed again gives way to the next tile's rows
+        fill(fill0, x0, ev0);
+        fill(fill0 + 3, x1, ev1);
+        fill(fill0 + 6, x2, ev2);
+        x2 = load_raw(next, chunk2);
+        if (g == 1) x1 = load_raw(next, chunk1);
+        if (g == 2) x0 = load_raw(next, chunk0);
         // ---- softmax (as in the FP8 kernel)
-        ok = warp_wait(s_full, par, ab, ok);
+        ok = warp_wait(s_full, it & 1, ab, ok);
         tc_fence_after();
         uint32_t rr[2][16];
         const uint32_t ts = tmem + S_COL + 32 * g + lane_off;
@@ -1155,15 +1153,13 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
             if (ok && lane == 0) mbar_arrive(&p_full[i < 2 ? i : 2]);
           }
         }
-        // ---- the values' chunks that did not stay, as the places come free
+        // ---- the values' chunks that did not stay, as the places come free: 0, 1, 2, then 3
+        fill(g == 0 ? 10 : (g == 1 ? 9 : 11), g == 2 ? x1 : x0, g == 0 ? EV_V2 : (g == 1 ? EV_S1 : EV_V3));
+        if (g == 2) x1 = load_raw(next, chunk1);
+        else x0 = load_raw(next, chunk0);
         if (g == 0) {
-          fill(10, w0, EV_V2, par, true);     // chunk 0
-          w0 = load_raw(next, g);
-          fill(12, w1, EV_V3, par, true);     // chunk 3
-          w1 = load_raw(next, g + 3);
-        } else if (g == 2) {
-          fill(11, w0, EV_V3, par, true);     // chunk 2
-          w0 = load_raw(next, g);
+          fill(12, x1, EV_V3);
+          x1 = load_raw(next, chunk1);
         }
         next = after;
       }
