@@ -454,10 +454,9 @@ dsa_status run_indexer(const dsa_kv_layout* l, const dsa_batch* b, const void* q
 // `pre_hist`: histograms the scorer left for these scores, or null.
 dsa_status run_topk(const dsa_kv_layout* l, const dsa_batch* b, const float* scores, int64_t ld, int topk,
                     int32_t* idx, int32_t* phys, void* ws, const Ws& wl, cudaStream_t st, bool chained,
-                    uint32_t* pre_hist = nullptr, bool zeroed = false, const dsa_tree* tree = nullptr) {
+                    uint32_t* pre_hist = nullptr, bool zeroed = false) {
   if (b->num_tokens == 0) return DSA_OK;
   TopkParams p;
-  if (tree) p.tree = tree_view(tree);
   p.b = batch_view(b);
   p.scores = scores;
   p.ld = ld;
@@ -941,8 +940,29 @@ dsa_status dsa_tree_topk(const dsa_kv_layout* layout, const dsa_batch* batch, co
   dummy.block_size = 64;
   const Ws wl = plan_ws(layout ? layout : &dummy, batch, topk);
   if ((s = check_ws(workspace, workspace_bytes, wl)) != DSA_OK) return s;
-  return run_topk(layout, batch, scores, ld_scores, topk, idx, phys_slots, workspace, wl, stream, false, nullptr, false,
-                  tree);
+  const int T = batch->num_tokens;
+  if (T == 0) return DSA_OK;
+  const TopkScratch L = topk_scratch_layout(T, wl.topk_nchunks);
+  TreeTopkParams p;
+  p.b = batch_view(batch);
+  p.tree = tree_view(tree);
+  p.scores = scores;
+  p.ld = ld_scores;
+  p.k = topk;
+  p.nchunks = wl.topk_nchunks;
+  // the entries take the place of the scores that a layer step keeps in the workspace
+  p.list = at<uint2>(workspace, wl.scores);
+  p.cap = static_cast<int>(wl.ld / 2 < kTreeTopkCap ? wl.ld / 2 : kTreeTopkCap);
+  uint8_t* scratch = at<uint8_t>(workspace, wl.topk);
+  p.bound = reinterpret_cast<uint32_t*>(scratch + L.thr);
+  p.fill = reinterpret_cast<uint32_t*>(scratch + L.cand_count);
+  p.at = reinterpret_cast<uint32_t*>(scratch + L.gt);
+  p.num = reinterpret_cast<uint32_t*>(scratch + L.taken);
+  p.idx = idx;
+  p.phys = phys_slots;
+  p.log2_bs = layout ? log2_of(layout->block_size) : 0;
+  p.status = at<uint32_t>(workspace, wl.status);
+  return cuda_status(launch_tree_topk(p, stream));
 }
 
 dsa_status dsa_tree_commit(const dsa_kv_layout* layout, const dsa_batch* batch, const int32_t* base,

@@ -118,76 +118,13 @@ __device__ __forceinline__ int32_t emit_phys(const TopkParams& p, const int32_t*
   return (btrow[s >> p.log2_bs] << p.log2_bs) | (s & bs_mask);
 }
 
-// A query row: its request and length n (positions 0..pos).  With TREE, `base` of
-// them are committed and the rest are seen by the token's mask; `seen` counts what it
-// sees (n without TREE).  False for a padding token.
-struct Row {
-  int req, n, base, seen;
-  const uint32_t* mask;
-};
-
-template <bool TREE>
-__device__ __forceinline__ bool load_row(const TopkParams& p, int t, Row& r) {
-  int pos;
-  r.base = 0;
-  r.mask = nullptr;
-  if (!TREE) {
-    load_token(p.b, t, p.status, r.req, pos);
-    r.n = r.seen = pos + 1;
-    return true;
-  }
-  if (!load_tree_token(p.b, p.tree, t, p.status, r.req, pos, r.base)) return false;
-  r.n = pos + 1;
-  r.base = min(r.base, r.n);
-  r.mask = p.tree.mask + static_cast<int64_t>(t) * p.tree.words;
-  // bits of the drafted positions up to pos, one word per lane (at most 32 words)
-  const int lane = threadIdx.x & 31;
-  const int d = r.n - r.base;   // drafted positions in the row
-  uint32_t w = lane < p.tree.words && 32 * lane < d ? __ldg(r.mask + lane) : 0u;
-  if (32 * lane < d && 32 * lane + 32 > d) w &= (1u << (d - 32 * lane)) - 1u;
-  r.seen = r.base + static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<uint32_t>(__popc(w))));
-  return true;
-}
-
-template <bool TREE>
-__device__ __forceinline__ bool row_range(const TopkParams& p, int t, int& c0, int& c1, Row& r) {
-  c0 = c1 = 0;
-  if (!load_row<TREE>(p, t, r)) return false;
+__device__ __forceinline__ bool row_range(const TopkParams& p, int t, int& c0, int& c1, int& n) {
+  int req, pos;
+  load_token(p.b, t, p.status, req, pos);
+  n = pos + 1;
   c0 = blockIdx.x * p.chunk;
-  c1 = min(r.n, c0 + p.chunk);
-  return c0 < r.n;
-}
-
-// The positions s0 + i (i < 16) below c1 that take part, as bits.
-template <bool TREE>
-__device__ __forceinline__ uint32_t seen_bits(const TopkParams& p, const Row& r, int s0, int c1) {
-  const int nv = max(0, min(kPerThread, c1 - s0));
-  uint32_t m = (1u << nv) - 1u;
-  if (TREE && s0 + nv > r.base) {
-    for (int i = max(0, r.base - s0); i < nv; ++i)
-      if (!tree_sees(r.mask, p.tree.words, r.base, s0 + i)) m &= ~(1u << i);
-  }
-  return m;
-}
-
-// Position of output entry o when everything seen is selected (-1 past the last).
-template <bool TREE>
-__device__ __forceinline__ int seen_position(const TopkParams& p, const Row& r, int o) {
-  if (!TREE) return o < r.n ? o : -1;
-  if (o < r.base) return o;
-  if (o >= r.seen) return -1;
-  int left = o - r.base;   // the left-th set bit of the mask
-  for (int w = 0; w < p.tree.words; ++w) {
-    uint32_t bits = __ldg(r.mask + w);
-    const int c = __popc(bits);
-    if (left >= c) {
-      left -= c;
-      continue;
-    }
-    while (left-- > 0) bits &= bits - 1;
-    return r.base + 32 * w + __ffs(bits) - 1;
-  }
-  return -1;
+  c1 = min(n, c0 + p.chunk);
+  return c0 < n;
 }
 
 // The last CTA (by ticket) of row t to finish a pass; call with every thread.
@@ -203,14 +140,12 @@ __device__ __forceinline__ bool last_of_row(uint32_t* counter, int nchunks_row, 
 
 // ------------------------------------------------------------------- pass 1
 
-template <bool TREE>
 __global__ void __launch_bounds__(kTopkThreads) topk_hist_kernel(TopkParams p) {
   __shared__ uint32_t h[kBins];
   __shared__ uint32_t sh[48];
   const int t = blockIdx.y;
-  int c0, c1;
-  Row r;
-  const bool work = row_range<TREE>(p, t, c0, c1, r) && r.seen > p.k;   // inputs of the call, read before the wait
+  int c0, c1, n;
+  const bool work = row_range(p, t, c0, c1, n) && n > p.k;   // inputs of the call, read before the wait
   grid_dep_wait();     // the scores (and the zeroed scratch) of the work before
   grid_dep_launch();
   if (!work) return;
@@ -220,15 +155,14 @@ __global__ void __launch_bounds__(kTopkThreads) topk_hist_kernel(TopkParams p) {
   uint32_t u[kPerThread];
   const int s0 = c0 + threadIdx.x * kPerThread;
   load16(row, s0, c1, u);
-  const uint32_t vm = seen_bits<TREE>(p, r, s0, c1);
 #pragma unroll
   for (int i = 0; i < kPerThread; ++i)
-    if ((vm >> i) & 1u) atomicAdd(&h[u[i] >> 21], 1u);
+    if (s0 + i < c1) atomicAdd(&h[u[i] >> 21], 1u);
   __syncthreads();
   uint32_t* gh = p.hist + static_cast<int64_t>(t) * kBins;
   for (int i = threadIdx.x; i < kBins; i += kTopkThreads)
     if (h[i]) atomicAdd(gh + i, h[i]);
-  const int nch = static_cast<int>(cdiv(r.n, p.chunk));
+  const int nch = static_cast<int>(cdiv(n, p.chunk));
   if (!last_of_row(p.done + 2 * t, nch, sh)) return;
   for (int i = threadIdx.x; i < kBins; i += kTopkThreads) h[i] = __ldcg(gh + i);
   __syncthreads();
@@ -311,15 +245,13 @@ __device__ int32_t select_cut(Gen gen, int count, uint32_t T, uint32_t m, uint32
   return static_cast<int32_t>(0x3FFFFFFFu - prefix);
 }
 
-template <bool TREE>
 __global__ void __launch_bounds__(kTopkThreads) topk_candidates_kernel(TopkParams p) {
   __shared__ uint32_t sh[48];
   __shared__ uint32_t lcount, lbase;
   __shared__ uint2 lc[4096];       // this chunk's candidates (key, position)
   const int t = blockIdx.y;
-  int c0, c1;
-  Row r;
-  const bool work = row_range<TREE>(p, t, c0, c1, r) && r.seen > p.k;
+  int c0, c1, n;
+  const bool work = row_range(p, t, c0, c1, n) && n > p.k;
   grid_dep_wait();     // the histogram pass
   grid_dep_launch();
   if (!work) return;
@@ -330,11 +262,10 @@ __global__ void __launch_bounds__(kTopkThreads) topk_candidates_kernel(TopkParam
   uint32_t u[kPerThread];
   const int s0 = c0 + threadIdx.x * kPerThread;
   load16(row, s0, c1, u);
-  const uint32_t vm = seen_bits<TREE>(p, r, s0, c1);
   uint32_t gt = 0;
 #pragma unroll
   for (int i = 0; i < kPerThread; ++i) {
-    if (!((vm >> i) & 1u)) continue;
+    if (s0 + i >= c1) continue;
     const uint32_t d = u[i] >> 21;
     gt += d > b1;
     if (d == b1) {
@@ -358,18 +289,17 @@ __global__ void __launch_bounds__(kTopkThreads) topk_candidates_kernel(TopkParam
 // kResolveThreads per row, after every chunk of the row has listed its candidates.
 constexpr int kResolveThreads = 1024;
 
-template <bool TREE>
 __global__ void __launch_bounds__(kResolveThreads) topk_resolve_kernel(TopkParams p) {
   __shared__ uint32_t h[kBins];
   __shared__ uint32_t sh[48];
   __shared__ uint2 lc[4096];       // the row's candidates (key, position)
   const int t = blockIdx.x;
-  Row rw;
-  const bool real = load_row<TREE>(p, t, rw);   // inputs of the call, read before the wait
+  int req, pos;
+  load_token(p.b, t, p.status, req, pos);   // inputs of the call, read before the wait
   grid_dep_wait();     // the candidate pass
   grid_dep_launch();
-  if (!real || rw.seen <= p.k) return;
-  const int n = rw.n;
+  const int n = pos + 1;
+  if (n <= p.k) return;
   const int nch = static_cast<int>(cdiv(n, p.chunk));
   const uint32_t b1 = p.thr[4 * t + 0];
   const float* row = p.scores + static_cast<int64_t>(t) * p.ld;
@@ -423,7 +353,7 @@ __global__ void __launch_bounds__(kResolveThreads) topk_resolve_kernel(TopkParam
       const uint32_t k = score_key(__ldcg(row + i));
       key = k & 0x1FFFFFu;
       idx = i;
-      return (k >> 21) == b1 && (!TREE || tree_sees(rw.mask, p.tree.words, rw.base, i));
+      return (k >> 21) == b1;
     };
     select_low21(gen, n, r, Tlow, aboveT, h, sh);
     cut = select_cut(gen, n, Tlow, r - aboveT, h, sh);
@@ -442,17 +372,15 @@ __global__ void __launch_bounds__(kResolveThreads) topk_resolve_kernel(TopkParam
 
 // ------------------------------------------------------------------- pass 3
 
-template <bool TREE>
 __global__ void __launch_bounds__(kTopkThreads) topk_emit_kernel(TopkParams p) {
   __shared__ uint32_t sh[48];
   __shared__ uint32_t base_sh;
   const int t = blockIdx.y;
-  Row r;
-  const bool real = load_row<TREE>(p, t, r);
+  int req, pos;
+  load_token(p.b, t, p.status, req, pos);
   grid_dep_wait();     // the candidate pass
   grid_dep_launch();
-  if (!real) return;
-  const int n = r.n, req = r.req;
+  const int n = pos + 1;
   const int c0 = blockIdx.x * p.chunk;
   const int c1 = min(n, c0 + p.chunk);
   int32_t* out = p.idx + static_cast<int64_t>(t) * p.k;
@@ -460,16 +388,7 @@ __global__ void __launch_bounds__(kTopkThreads) topk_emit_kernel(TopkParams p) {
   const int32_t* btrow = p.b.bt + static_cast<int64_t>(req) * p.b.bt_stride;
   const int bs_mask = (1 << p.log2_bs) - 1;
 
-  if (TREE && r.seen <= p.k) {   // everything seen is selected; chunk 0 writes it
-    if (blockIdx.x == 0)
-      for (int o = threadIdx.x; o < p.k; o += kTopkThreads) {
-        const int s = seen_position<TREE>(p, r, o);
-        out[o] = s;
-        if (phys) phys[o] = s >= 0 ? emit_phys(p, btrow, s, bs_mask) : -1;
-      }
-    return;
-  }
-  if (!TREE && n <= p.k) {   // every position is selected; chunk 0 also writes the -1 tail
+  if (n <= p.k) {   // every position is selected; chunk 0 also writes the -1 tail
     for (int s = c0 + threadIdx.x; s < c1; s += kTopkThreads) {
       out[s] = s;
       if (phys) phys[s] = emit_phys(p, btrow, s, bs_mask);
@@ -499,12 +418,11 @@ __global__ void __launch_bounds__(kTopkThreads) topk_emit_kernel(TopkParams p) {
   uint32_t u[kPerThread];
   const int s0 = c0 + threadIdx.x * kPerThread;
   load16(row, s0, c1, u);
-  const uint32_t vm = seen_bits<TREE>(p, r, s0, c1);
   uint32_t mine = 0, flags = 0;
 #pragma unroll
   for (int i = 0; i < kPerThread; ++i) {
     const int s = s0 + i;
-    const bool take = ((vm >> i) & 1u) && (u[i] > T || (u[i] == T && s <= cut));
+    const bool take = s < c1 && (u[i] > T || (u[i] == T && s <= cut));
     flags |= static_cast<uint32_t>(take) << i;
     mine += take;
   }
@@ -652,7 +570,7 @@ __device__ __forceinline__ uint2 cl_find(uint4 c, uint32_t kk, uint32_t* wsh, ui
 //     3 through the cluster as in step 1, over the keys in registers.
 //  4. Ordered output: keys above the threshold key T, then keys equal to T at the
 //     lowest positions, each CTA after the selections of the CTAs before it.
-template <bool PRE, bool TREE>
+template <bool PRE>
 __global__ void __launch_bounds__(kClThreads) topk_cluster_kernel(TopkParams p) {
   __shared__ __align__(16) ClShared S;
   const int t = blockIdx.y;
@@ -661,10 +579,9 @@ __global__ void __launch_bounds__(kClThreads) topk_cluster_kernel(TopkParams p) 
   const bool multi = csize > 1;
   // Inputs of the call (not of the kernel before): the row length and the
   // block-table entry of this thread's 16 positions are read before the wait.
-  Row rw;
-  const bool real = load_row<TREE>(p, t, rw);
-  if (TREE && !real) return;   // a padding token (uniform over the cluster)
-  const int n = rw.n, req = rw.req;
+  int req, pos;
+  load_token(p.b, t, p.status, req, pos);
+  const int n = pos + 1;
   int32_t* out = p.idx + static_cast<int64_t>(t) * p.k;
   int32_t* phys = p.phys ? p.phys + static_cast<int64_t>(t) * p.k : nullptr;
   const int32_t* btrow = p.b.bt + static_cast<int64_t>(req) * p.b.bt_stride;
@@ -675,20 +592,18 @@ __global__ void __launch_bounds__(kClThreads) topk_cluster_kernel(TopkParams p) 
   const int c1 = min(n, c0 + SL);
   const int s0 = c0 + tid * kPerThread;
   const int nv = max(0, min(kPerThread, c1 - s0));
-  const uint32_t vm = seen_bits<TREE>(p, rw, s0, c1);   // the thread's scores that take part
   // 16 consecutive positions from a multiple of 16 share one block when bs >= 16
   const bool one_block = p.log2_bs >= 4;
-  const int32_t blk = (phys && one_block && nv > 0 && rw.seen > p.k) ? __ldcg(btrow + (s0 >> p.log2_bs)) : 0;
+  const int32_t blk = (phys && one_block && nv > 0 && n > p.k) ? __ldcg(btrow + (s0 >> p.log2_bs)) : 0;
   for (int i = tid; i < kClZeroWords; i += kClThreads) S.hl[i] = 0;
   grid_dep_wait();
   grid_dep_launch();
   uint4* gh = PRE ? reinterpret_cast<uint4*>(p.pre_hist + static_cast<int64_t>(t) * kBins) : nullptr;
 
-  if (rw.seen <= p.k) {   // everything seen is selected, then -1 padding
-    for (int o = rank * kClThreads + tid; o < p.k; o += csize * kClThreads) {
-      const int s = seen_position<TREE>(p, rw, o);
-      out[o] = s;
-      if (phys) phys[o] = s >= 0 ? emit_phys(p, btrow, s, bs_mask) : -1;
+  if (n <= p.k) {   // every position is selected, then -1 padding
+    for (int s = rank * kClThreads + tid; s < p.k; s += csize * kClThreads) {
+      out[s] = s < n ? s : -1;
+      if (phys) phys[s] = s < n ? emit_phys(p, btrow, s, bs_mask) : -1;
     }
     if (PRE && rank == 0) gh[tid] = make_uint4(0u, 0u, 0u, 0u);
     return;   // uniform over the cluster: no CTA touches another's shared memory
@@ -718,7 +633,7 @@ __global__ void __launch_bounds__(kClThreads) topk_cluster_kernel(TopkParams p) 
     if (exchange) {
 #pragma unroll
       for (int i = 0; i < kPerThread; ++i)
-        if ((vm >> i) & 1u) atomicAdd(&S.hl[u[i] >> 21], 1u);
+        if (i < nv) atomicAdd(&S.hl[u[i] >> 21], 1u);
       __syncthreads();
       if (multi) {
         const uint32_t own = ((kBins + csize - 1) / csize + 3u) & ~3u;   // four-bin multiple: one owner per thread
@@ -744,7 +659,7 @@ __global__ void __launch_bounds__(kClThreads) topk_cluster_kernel(TopkParams p) 
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
       const uint32_t d = u[i] >> 21;
-      if ((vm >> i) & 1u) {
+      if (i < nv) {
         gtm |= static_cast<uint32_t>(d > static_cast<uint32_t>(b1)) << i;
         cm |= static_cast<uint32_t>(d == static_cast<uint32_t>(b1)) << i;
       }
@@ -873,8 +788,8 @@ __global__ void __launch_bounds__(kClThreads) topk_cluster_kernel(TopkParams p) 
     uint32_t gt = 0, eq = 0;
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
-      gt += ((vm >> i) & 1u) && u[i] > T;
-      eq += ((vm >> i) & 1u) && u[i] == T;
+      gt += i < nv && u[i] > T;
+      eq += i < nv && u[i] == T;
     }
     excl = cl_scan_sum2((gt << 16) | eq, x, y, S.wsh[4], S.wsh[5]);
     const uint32_t eq_lo = min(x & 0xFFFFu, need_eq);
@@ -891,7 +806,7 @@ __global__ void __launch_bounds__(kClThreads) topk_cluster_kernel(TopkParams p) 
       uint32_t* hrr = d == 1 ? S.hr2 : S.hr3;
 #pragma unroll
       for (int i = 0; i < kPerThread; ++i)
-        if (((vm >> i) & 1u) && (u[i] & pmask) == pval) atomicAdd(&h[(u[i] >> shift) & (nb - 1)], 1u);
+        if (i < nv && (u[i] & pmask) == pval) atomicAdd(&h[(u[i] >> shift) & (nb - 1)], 1u);
       __syncthreads();
       uint4 cc = make_uint4(0u, 0u, 0u, 0u);
       const uint32_t b0 = 4u * tid;
@@ -921,8 +836,8 @@ __global__ void __launch_bounds__(kClThreads) topk_cluster_kernel(TopkParams p) 
     uint32_t gt = 0, eq = 0;
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
-      gt += ((vm >> i) & 1u) && u[i] > T;
-      eq += ((vm >> i) & 1u) && u[i] == T;
+      gt += i < nv && u[i] > T;
+      eq += i < nv && u[i] == T;
     }
     const uint2 sc = cl_excl_scan((gt << 16) | eq, S.wsh[4]);
     const uint32_t tot = sc.y;
@@ -948,8 +863,8 @@ __global__ void __launch_bounds__(kClThreads) topk_cluster_kernel(TopkParams p) 
   uint32_t flags = 0;
 #pragma unroll
   for (int i = 0; i < kPerThread; ++i) {
-    bool sel = ((vm >> i) & 1u) && u[i] > T;
-    if (((vm >> i) & 1u) && u[i] == T) sel = eq_rank++ < take;
+    bool sel = i < nv && u[i] > T;
+    if (i < nv && u[i] == T) sel = eq_rank++ < take;
     flags |= static_cast<uint32_t>(sel) << i;
   }
   while (flags) {
@@ -964,33 +879,25 @@ __global__ void __launch_bounds__(kClThreads) topk_cluster_kernel(TopkParams p) 
   if (gathered && multi) cluster_wait();   // no CTA leaves while another may still read its candidates
 }
 
-template <bool TREE>
-static cudaError_t launch_topk_t(const TopkParams& p, cudaStream_t st, bool chained, bool zeroed) {
+cudaError_t launch_topk(const TopkParams& p, cudaStream_t st, bool chained, bool zeroed) {
   if (p.b.T == 0) return cudaSuccess;
   if (p.b.max_ctx <= kClMaxRow) {
     const unsigned csize = static_cast<unsigned>(cdiv(p.b.max_ctx, kClSlice));
-    if (!TREE && p.pre_hist)
-      return launch_ex(topk_cluster_kernel<true, false>, dim3(csize, p.b.T), dim3(kClThreads), 0, st, chained, csize,
-                       p);
-    return launch_ex(topk_cluster_kernel<false, TREE>, dim3(csize, p.b.T), dim3(kClThreads), 0, st, chained, csize, p);
+    if (p.pre_hist)
+      return launch_ex(topk_cluster_kernel<true>, dim3(csize, p.b.T), dim3(kClThreads), 0, st, chained, csize, p);
+    return launch_ex(topk_cluster_kernel<false>, dim3(csize, p.b.T), dim3(kClThreads), 0, st, chained, csize, p);
   }
   const dim3 grid(p.nchunks, p.b.T);
   cudaError_t e = cudaSuccess;
   if (!zeroed && (e = cudaMemsetAsync(p.zero_begin, 0, p.zero_bytes, st)) != cudaSuccess) return e;
   // each pass starts while the one before drains (programmatic launch; each waits
   // for the one before before it reads anything that one writes)
-  if ((e = launch_ex(topk_hist_kernel<TREE>, grid, dim3(kTopkThreads), 0, st, chained && zeroed, 0u, p)) != cudaSuccess)
+  if ((e = launch_ex(topk_hist_kernel, grid, dim3(kTopkThreads), 0, st, chained && zeroed, 0u, p)) != cudaSuccess)
     return e;
-  if ((e = launch_ex(topk_candidates_kernel<TREE>, grid, dim3(kTopkThreads), 0, st, true, 0u, p)) != cudaSuccess)
+  if ((e = launch_ex(topk_candidates_kernel, grid, dim3(kTopkThreads), 0, st, true, 0u, p)) != cudaSuccess) return e;
+  if ((e = launch_ex(topk_resolve_kernel, dim3(p.b.T), dim3(kResolveThreads), 0, st, true, 0u, p)) != cudaSuccess)
     return e;
-  if ((e = launch_ex(topk_resolve_kernel<TREE>, dim3(p.b.T), dim3(kResolveThreads), 0, st, true, 0u, p)) !=
-      cudaSuccess)
-    return e;
-  return launch_ex(topk_emit_kernel<TREE>, grid, dim3(kTopkThreads), 0, st, true, 0u, p);
-}
-
-cudaError_t launch_topk(const TopkParams& p, cudaStream_t st, bool chained, bool zeroed) {
-  return p.tree.mask ? launch_topk_t<true>(p, st, chained, zeroed) : launch_topk_t<false>(p, st, chained, zeroed);
+  return launch_ex(topk_emit_kernel, grid, dim3(kTopkThreads), 0, st, true, 0u, p);
 }
 
 }  // namespace dsa
