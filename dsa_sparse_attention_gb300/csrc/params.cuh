@@ -74,7 +74,7 @@ constexpr int kTopkClusterMaxRow = 65536;   // rows up to this long take the one
 // Decode batches of at most this many tokens, one per group, are planned inside
 // the scorer (no separate planning launch).
 constexpr int kDirectMaxT = 128;
-constexpr int kTreeTopkCap = 16384;   // entries per row the tree top-k resolves in shared memory
+constexpr int kTreeTopkCap = 24576;   // entries per row the tree top-k resolves in shared memory (192 KB)
 constexpr int kTopkCap = 4096;     // candidates per row kept for the exact resolution
 
 // Byte offsets of the top-k scratch inside a region (256-byte aligned segments);

@@ -3,17 +3,17 @@
 //
 // A verification batch holds many long rows, so the pass over the scores is what
 // counts: it is made once.
-//  1. bound:  one CTA per row reads 8,192 scores, one at a hashed place of each of as
+//  1. bound:  one CTA per row reads 4,096 scores, one at a hashed place of each of as
 //             many equal stretches, and takes the sample's rank m + 6 sqrt(m) + 8 as the
-//             row's bound, m = 8,192 k / n being the number of samples expected among
+//             row's bound, m = 4,096 k / n being the number of samples expected among
 //             the k best.  Fewer than k scores then lie at or above the bound with
-//             probability below 1e-6, and typically 1.4 k (64K scores) to 3 k (1M) do.
+//             probability below 1e-6, and typically 1.6 k (64K scores) to 4 k (1M) do.
 //  2. filter: one CTA per 4,096 scores lists its scores at or above the bound, in
 //             position order, and notes where its entries lie.
 //  3. select: one CTA per row gathers the entries chunk by chunk, so in position order,
-//             into shared memory, resolves the threshold key in three digit passes, and
-//             the position cut among equal keys where not all of them fit (lowest
-//             positions first), and writes the selection with one scan.
+//             into shared memory, finds the k-th by one digit and comparisons within its bin
+//             (by digits down to the last bit where the bin is crowded; equal keys by lower
+//             position), and writes the selection with one scan.
 // Rows of at most 16,384 scores go to step 3 directly.  Steps 1 and 2 only choose what
 // step 3 looks at: it counts the entries, and a row whose entries are too few or too
 // many (more equal scores than the list holds) is resolved over the whole row, exactly
@@ -30,7 +30,8 @@ constexpr int kFilterThreads = 256;
 constexpr int kPer = 16;                 // scores per thread and chunk
 static_assert(kFilterThreads * kPer == kTopkChunk, "chunk");
 constexpr int kRowThreads = 1024;
-constexpr int kSamples = 8192;
+constexpr int kSamples = 4096;
+constexpr int kDirect = 16384;           // rows of at most this many scores skip steps 1 and 2
 
 // A row: n positions, `base` of them committed, `seen` seen by the token.
 struct Row {
@@ -56,7 +57,7 @@ __device__ __forceinline__ bool load_row(const TreeTopkParams& p, int t, Row& r)
 
 // Steps 1 and 2 take part.
 __device__ __forceinline__ bool filtered(const TreeTopkParams& p, const Row& r) {
-  return r.seen > p.k && r.n > kTreeTopkCap;
+  return r.seen > p.k && r.n > kDirect;
 }
 
 // Key of position s, 0 (below every score's key) where the token does not see it.
@@ -128,39 +129,64 @@ __device__ __forceinline__ uint2 find_digit(RowShared& S, int nb, uint32_t kk, i
   return r;
 }
 
-// The kk-th largest (1-based) of the values with (v >> hi_shift) == prefix that `each`
-// hands out, by digits of `bits` bits down to `lo_shift`: the value's upper part (the
-// rest zero), the number above, and in S.h the counts of the last digit.
+// The kk-th largest (1-based) of the values that `each` hands out (the same ones every
+// time, at least kk), exact down to bit `low`, and the number above it.  Digits of 11 bits
+// are taken of the difference to the smallest value, from its highest set bit down: the
+// scores that matter share their leading bits, and a histogram of those would send most
+// lanes of a warp to the same few counters.  `equal`: values that share all digits taken.
 template <typename Each>
-__device__ __forceinline__ uint32_t select_digits(RowShared& S, Each each, uint32_t kk, const int (&shift)[3],
-                                                  const int (&bits)[3], int digits, uint32_t& above) {
-  uint32_t prefix = 0, mask = 0;
+__device__ __forceinline__ uint32_t select_value(RowShared& S, Each each, uint32_t kk, int low, uint32_t& above,
+                                                 uint32_t& equal) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t lo = 0xFFFFFFFFu, hi = 0u, n = 0;
+  each([&](uint32_t v) {
+    lo = min(lo, v);
+    hi = max(hi, v);
+    ++n;
+  });
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  n = __reduce_add_sync(0xffffffffu, n);
+  if (lane == 0) {
+    S.wsh[0][warp] = lo;
+    S.wsh[1][warp] = hi;
+    S.wsh[2][warp] = n;
+  }
+  __syncthreads();
+  lo = __reduce_min_sync(0xffffffffu, S.wsh[0][lane]);
+  hi = __reduce_max_sync(0xffffffffu, S.wsh[1][lane]);
+  equal = __reduce_add_sync(0xffffffffu, S.wsh[2][lane]);
   above = 0;
-#pragma unroll
-  for (int d = 0; d < 3; ++d) {
-    if (d >= digits) break;
-    const int nb = 1 << bits[d];
+  uint32_t prefix = 0, mask = 0;
+  int top = 32 - __clz(hi - lo);   // bits of the difference still open
+  int slot = 3;
+  while (top > low) {
+    const int shift = max(top - 11, low);
+    const int nb = 1 << 11;
+    __syncthreads();
     for (int i = threadIdx.x; i < nb; i += kRowThreads) S.h[i] = 0;
     __syncthreads();
     each([&](uint32_t v) {
-      if ((v & mask) == prefix) atomicAdd(&S.h[(v >> shift[d]) & (nb - 1)], 1u);
+      const uint32_t d = v - lo;
+      if ((d & mask) == prefix) atomicAdd(&S.h[(d >> shift) & (nb - 1)], 1u);
     });
     __syncthreads();
-    const uint2 f = find_digit(S, nb, kk - above, d);
-    prefix |= f.x << shift[d];
-    mask |= static_cast<uint32_t>(nb - 1) << shift[d];
+    const uint2 f = find_digit(S, nb, kk - above, slot);
+    equal = S.h[f.x];
+    prefix |= f.x << shift;
+    mask = ~((1u << shift) - 1u);
     above += f.y;
+    top = shift;
+    slot = slot == 3 ? 0 : 3;
   }
-  return prefix;
+  return lo + prefix;
 }
-
-__device__ __constant__ constexpr int kKeyShift[3] = {21, 10, 0}, kKeyBits[3] = {11, 11, 10};
-__device__ __constant__ constexpr int kPosShift[3] = {20, 10, 0}, kPosBits[3] = {10, 10, 10};
 
 // ----------------------------------------------------------------------- step 1
 
 __global__ void __launch_bounds__(kRowThreads) tree_topk_bound_kernel(TreeTopkParams p) {
   __shared__ RowShared S;
+  grid_dep_launch();   // the filter's blocks load their scores meanwhile
   const int t = blockIdx.x;
   Row r;
   const bool work = load_row(p, t, r) && filtered(p, r);
@@ -180,17 +206,19 @@ __global__ void __launch_bounds__(kRowThreads) tree_topk_bound_kernel(TreeTopkPa
   }
   const float m = static_cast<float>(kSamples) * static_cast<float>(p.k) / static_cast<float>(r.n);
   const uint32_t rank = min(static_cast<uint32_t>(m + 6.f * sqrtf(m)) + 8u, static_cast<uint32_t>(kSamples));
-  uint32_t above;
-  const uint32_t bound = select_digits(
+  uint32_t above, equal;
+  const uint32_t bound = select_value(   // to within 2^10: a lower bound of the sample's rank
       S,
       [&](auto take) {
 #pragma unroll
-        for (int i = 0; i < kSamples / kRowThreads; ++i) take(u[i]);
+        for (int i = 0; i < kSamples / kRowThreads; ++i)
+          if (u[i]) take(u[i]);   // (a filtered row's samples are nearly all seen)
       },
-      rank, kKeyShift, kKeyBits, 2, above);
+      rank, 10, above, equal);
   if (threadIdx.x == 0) p.bound[t] = max(bound, 1u);   // positions not seen have key 0
 }
-static_assert(kTreeTopkCap >= kSamples, "a filtered row has a stretch of at least one score per sample");
+static_assert(kTreeTopkCap <= 32 * kRowThreads, "rounds of the ordered output");
+static_assert(kDirect >= kSamples && kTreeTopkCap >= kDirect, "a stretch of scores per sample; a direct row fits");
 
 // ----------------------------------------------------------------------- step 2
 
@@ -198,32 +226,29 @@ __global__ void __launch_bounds__(kFilterThreads) tree_topk_filter_kernel(TreeTo
   __shared__ uint32_t wsh[32];
   __shared__ uint32_t base_sh;
   const int t = blockIdx.y, c = blockIdx.x;
-  Row r;
-  const bool work = load_row(p, t, r) && filtered(p, r) && c * kTopkChunk < r.n;
   const float* row = p.scores + static_cast<int64_t>(t) * p.ld;
   const int s0 = c * kTopkChunk + static_cast<int>(threadIdx.x) * kPer;
-  // The scores are inputs of the call, not of the kernel before: read ahead of the wait.
+  // The scores are inputs of the call, not of the kernel before: they are read ahead of the
+  // wait, and before the row's length is known (within the row's memory).
+  float v[kPer];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const bool in = s0 + 4 * q + 4 <= p.ld;   // ld is a multiple of 4
+    const float4 x = in ? __ldcs(reinterpret_cast<const float4*>(row + s0) + q) : make_float4(0.f, 0.f, 0.f, 0.f);
+    v[4 * q] = x.x;
+    v[4 * q + 1] = x.y;
+    v[4 * q + 2] = x.z;
+    v[4 * q + 3] = x.w;
+  }
+  Row r;
+  const bool work = load_row(p, t, r) && filtered(p, r) && c * kTopkChunk < r.n;
   uint32_t u[kPer];
-  if (work) {
-    if (s0 + kPer <= r.n) {
-      const float4* p4 = reinterpret_cast<const float4*>(row + s0);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float4 v = __ldcs(p4 + q);
-        u[4 * q] = score_key(v.x);
-        u[4 * q + 1] = score_key(v.y);
-        u[4 * q + 2] = score_key(v.z);
-        u[4 * q + 3] = score_key(v.w);
-      }
-    } else {
+  for (int i = 0; i < kPer; ++i) u[i] = score_key(v[i]);
+  if (work && s0 + kPer > r.base) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) u[i] = s0 + i < r.n ? score_key(__ldcs(row + s0 + i)) : 0u;
-    }
-    if (s0 + kPer > r.base) {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (s0 + i < r.n && !(s0 + i < r.base || tree_sees(r.mask, p.tree.words, r.base, s0 + i))) u[i] = 0u;
-    }
+    for (int i = 0; i < kPer; ++i)
+      if (s0 + i >= r.n || !(s0 + i < r.base || tree_sees(r.mask, p.tree.words, r.base, s0 + i))) u[i] = 0u;
   }
   grid_dep_wait();
   grid_dep_launch();
@@ -282,11 +307,71 @@ __device__ __forceinline__ void each_score(const TreeTopkParams& p, const Row& r
   }
 }
 
+// The k-th best of n listed entries (equal keys: the lower position first) as (T, cut),
+// when one digit leaves few enough of them to compare each with each: the entries of the
+// digit's bin are listed, and the one that needs k - above - 1 others before it is it.
+// False (nothing decided) when the bin holds more.
+constexpr int kPairs = kBins / 2;   // pairs that fit the histogram's place
+__device__ __forceinline__ bool select_listed(RowShared& S, const uint2* ent, uint32_t n, uint32_t k, uint32_t& T,
+                                              uint32_t& cut) {
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+  uint32_t lo = 0xFFFFFFFFu, hi = 0u;
+  for (uint32_t i = tid; i < n; i += kRowThreads) {
+    const uint32_t key = ent[i].x;
+    if (key) lo = min(lo, key);
+    hi = max(hi, key);
+  }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (lane == 0) {
+    S.wsh[0][warp] = lo;
+    S.wsh[1][warp] = hi;
+  }
+  for (int i = tid; i < kBins; i += kRowThreads) S.h[i] = 0;
+  __syncthreads();
+  lo = __reduce_min_sync(0xffffffffu, S.wsh[0][lane]);
+  hi = __reduce_max_sync(0xffffffffu, S.wsh[1][lane]);
+  const int shift = max(32 - __clz(hi - lo) - 11, 0);
+  for (uint32_t i = tid; i < n; i += kRowThreads) {
+    const uint32_t key = ent[i].x;
+    if (key) atomicAdd(&S.h[(key - lo) >> shift], 1u);
+  }
+  __syncthreads();
+  const uint2 f = find_digit(S, kBins, k, 2);
+  const uint32_t count = S.h[f.x], need = k - f.y;
+  __syncthreads();
+  if (count > static_cast<uint32_t>(kPairs)) return false;   // uniform
+  uint2* bin = reinterpret_cast<uint2*>(S.h);
+  if (tid == 0) S.res[0] = 0;
+  __syncthreads();
+  for (uint32_t i = tid; i < n; i += kRowThreads) {
+    const uint2 e = ent[i];
+    if (e.x && ((e.x - lo) >> shift) == f.x) bin[atomicAdd(&S.res[0], 1u)] = e;
+  }
+  __syncthreads();
+  for (uint32_t i = tid; i < count; i += kRowThreads) {
+    const uint2 e = bin[i];
+    uint32_t better = 0;
+    for (uint32_t j = 0; j < count; ++j) {
+      const uint2 o = bin[j];
+      better += o.x > e.x || (o.x == e.x && o.y < e.y);
+    }
+    if (better == need - 1) {   // exactly one entry
+      S.wsh[3][0] = e.x;
+      S.wsh[3][1] = e.y;
+    }
+  }
+  __syncthreads();
+  T = S.wsh[3][0];
+  cut = S.wsh[3][1];
+  return true;
+}
+
 __global__ void __launch_bounds__(kRowThreads) tree_topk_select_kernel(TreeTopkParams p) {
   extern __shared__ __align__(16) uint2 ent[];   // [kTreeTopkCap]
   __shared__ RowShared S;
   const int t = blockIdx.x;
-  const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+  const int tid = static_cast<int>(threadIdx.x);
   Row r;
   const bool real = load_row(p, t, r);
   grid_dep_wait();
@@ -314,7 +399,8 @@ __global__ void __launch_bounds__(kRowThreads) tree_topk_select_kernel(TreeTopkP
     n = __ldcg(p.fill + t);
     listed = n >= k && n <= static_cast<uint32_t>(p.cap);
     if (listed) {
-      // chunk by chunk: a warp per chunk, behind the entries of the chunks before it
+      // Entry i of the row, in position order, is the entry i - pre of the chunk whose places
+      // [pre, next pre) hold it: found by bisection, so that every thread's loads are independent.
       const int nch = static_cast<int>(cdiv(r.n, kTopkChunk));
       const uint2* list = p.list + static_cast<int64_t>(t) * p.cap;
       const uint32_t* at = p.at + static_cast<int64_t>(t) * p.nchunks;
@@ -322,18 +408,28 @@ __global__ void __launch_bounds__(kRowThreads) tree_topk_select_kernel(TreeTopkP
       uint32_t before = 0;
       for (int c0 = 0; c0 < nch; c0 += kRowThreads) {
         const int c = c0 + tid;
-        uint32_t cn = c < nch ? __ldcg(num + c) : 0u;
+        const uint32_t cn = c < nch ? __ldcg(num + c) : 0u, ca = c < nch ? __ldcg(at + c) : 0u;
         uint32_t total;
         const uint32_t pre = before + scan(cn, S.wsh[0], total);
-        // this round's places, read by the warps below
         S.h[tid] = pre;
-        S.h[kRowThreads + tid] = cn;
+        S.h[kRowThreads + tid] = ca;
         __syncthreads();
-        for (int j = warp; j < kRowThreads && c0 + j < nch; j += kRowThreads / 32) {
-          const uint32_t m = S.h[kRowThreads + j], to = S.h[j];
-          if (m == 0) continue;
-          const uint32_t from = __ldcg(at + c0 + j);
-          for (uint32_t i = lane; i < m; i += 32) ent[to + i] = __ldcg(list + from + i);
+        for (uint32_t i = before + tid; i < before + total; i += 4 * kRowThreads) {
+          int lo[4] = {0, 0, 0, 0};   // the last chunk of this round with pre <= the entry
+#pragma unroll
+          for (int step = kRowThreads / 2; step > 0; step >>= 1)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (S.h[lo[q] + step] <= i + q * kRowThreads) lo[q] += step;
+          uint2 e[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t n = i + q * kRowThreads;
+            if (n < before + total) e[q] = __ldcg(list + S.h[kRowThreads + lo[q]] + (n - S.h[lo[q]]));
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (i + q * kRowThreads < before + total) ent[i + q * kRowThreads] = e[q];
         }
         before += total;
         __syncthreads();
@@ -343,41 +439,59 @@ __global__ void __launch_bounds__(kRowThreads) tree_topk_select_kernel(TreeTopkP
   __syncthreads();
   auto keys = [&](auto take) {
     if (listed)
-      for (uint32_t i = tid; i < n; i += kRowThreads) take(ent[i].x);
+      for (uint32_t i = tid; i < n; i += kRowThreads) {
+        const uint32_t key = ent[i].x;
+        if (key) take(key);
+      }
     else
       each_score(p, r, row, [&](uint32_t key, uint32_t) { take(key); });
   };
-  // the threshold key T, and how many of the keys equal to it are taken
-  uint32_t above;
-  const uint32_t T = select_digits(S, keys, k, kKeyShift, kKeyBits, 3, above);
-  const uint32_t need = k - above, equal = S.h[T & 1023u];
-  uint32_t cut = 0xFFFFFFFFu;   // keys equal to T are taken at positions <= cut
-  if (equal > need) {
-    auto places = [&](auto take) {
-      auto of = [&](uint32_t key, uint32_t s) {
-        if (key == T) take(0x3FFFFFFFu - s);   // lower positions are larger
+  // the threshold key T, and of the keys equal to it those at positions <= cut
+  uint32_t T, cut = 0xFFFFFFFFu;
+  if (!listed || !select_listed(S, ent, n, k, T, cut)) {
+    uint32_t above, equal;
+    T = select_value(S, keys, k, 0, above, equal);
+    const uint32_t need = k - above;
+    if (equal > need) {
+      auto places = [&](auto take) {
+        auto of = [&](uint32_t key, uint32_t s) {
+          if (key == T) take(0x3FFFFFFFu - s);   // lower positions are larger
+        };
+        if (listed)
+          for (uint32_t i = tid; i < n; i += kRowThreads) of(ent[i].x, ent[i].y);
+        else
+          each_score(p, r, row, of);
       };
-      if (listed)
-        for (uint32_t i = tid; i < n; i += kRowThreads) of(ent[i].x, ent[i].y);
-      else
-        each_score(p, r, row, of);
-    };
-    __syncthreads();
-    uint32_t a2;
-    cut = 0x3FFFFFFFu - select_digits(S, places, need, kPosShift, kPosBits, 3, a2);
+      __syncthreads();
+      uint32_t a2, e2;
+      cut = 0x3FFFFFFFu - select_value(S, places, need, 0, a2, e2);
+    }
   }
   __syncthreads();
   auto taken = [&](uint32_t key, uint32_t s) { return key > T || (key == T && s <= cut); };
   if (listed) {
-    // consecutive entries per thread: one scan orders the selection
-    const uint32_t per = (n + kRowThreads - 1) / kRowThreads;
-    const uint32_t i0 = min(n, per * static_cast<uint32_t>(tid)), i1 = min(n, i0 + per);
-    uint32_t c = 0;
-    for (uint32_t i = i0; i < i1; ++i) c += taken(ent[i].x, ent[i].y);
+    // Entry j * 1024 + thread: counts per (j, warp) in order, one scan over them.
+    constexpr int kWarps = kRowThreads / 32;
+    const uint32_t rounds = (n + kRowThreads - 1) / kRowThreads;   // <= 24
+    uint32_t mine = 0;                                             // bit j: this thread's entry of round j
+    for (uint32_t j = 0; j < rounds; ++j) {
+      const uint32_t i = j * kRowThreads + tid;
+      const bool take = i < n && taken(ent[i].x, ent[i].y);
+      const uint32_t b = __ballot_sync(0xffffffffu, take);
+      if (take) mine |= 1u << j;
+      if ((tid & 31) == 0) S.h[j * kWarps + (tid >> 5)] = __popc(b);
+    }
+    __syncthreads();
     uint32_t total;
-    uint32_t o = scan(c, S.wsh[3], total);
-    for (uint32_t i = i0; i < i1; ++i)
-      if (taken(ent[i].x, ent[i].y)) emit(o++, static_cast<int>(ent[i].y));
+    const uint32_t pre = scan(static_cast<uint32_t>(tid) < rounds * kWarps ? S.h[tid] : 0u, S.wsh[2], total);
+    S.h[kRowThreads + tid] = pre;
+    __syncthreads();
+    for (uint32_t j = 0; j < rounds; ++j) {
+      const uint32_t b = __ballot_sync(0xffffffffu, (mine >> j) & 1u);
+      if (!((mine >> j) & 1u)) continue;
+      emit(S.h[kRowThreads + j * kWarps + (tid >> 5)] + __popc(b & ((1u << (tid & 31)) - 1u)),
+           static_cast<int>(ent[j * kRowThreads + tid].y));
+    }
   } else {
     uint32_t base = 0;
     for (int c0 = 0; c0 < r.n; c0 += 4 * kRowThreads) {
@@ -403,7 +517,7 @@ __global__ void __launch_bounds__(kRowThreads) tree_topk_select_kernel(TreeTopkP
 cudaError_t launch_tree_topk(const TreeTopkParams& p, cudaStream_t st) {
   if (p.b.T == 0) return cudaSuccess;
   cudaError_t e = cudaSuccess;
-  const bool filter = p.b.max_ctx > kTreeTopkCap;
+  const bool filter = p.b.max_ctx > kDirect;
   if (filter) {
     e = launch_ex(tree_topk_bound_kernel, dim3(p.b.T), dim3(kRowThreads), 0, st, false, 0u, p);
     if (e != cudaSuccess) return e;

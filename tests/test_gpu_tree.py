@@ -319,6 +319,32 @@ def test_topk_unseen_scores_and_ties(base):
     _check_topk(case, scores, 2048, idx)
 
 
+@pytest.mark.parametrize("base", [3000, 20000, 100000])
+@pytest.mark.parametrize("shape", ["equal", "two", "falling", "rising", "lowest", "heavy"])
+def test_topk_distributions(base, shape):
+    # scores that a sampled bound judges badly: all equal, two values, sorted rows, infinities,
+    # a few large ones in one place
+    case, scores = _topk_case([base], [6], seed=8)
+    n = scores.shape[1]
+    g = np.random.default_rng(base)
+    if shape == "equal":
+        scores[:] = -2.5
+    elif shape == "two":
+        scores[:] = np.where(g.random(scores.shape) < 0.3, np.float32(1), np.float32(-1))
+    elif shape == "falling":
+        scores[:] = -np.arange(n, dtype=np.float32)
+    elif shape == "rising":
+        scores[:] = np.arange(n, dtype=np.float32) * np.float32(1e-3)
+    elif shape == "lowest":
+        scores[:] = np.float32(-3.4028235e38)
+        scores[:, 5:base:7] = -np.inf
+        scores[:, base // 2] = np.inf
+    else:
+        scores[:, 100:2300] += 50
+    idx, _ = _topk(case, scores, 2048)
+    _check_topk(case, scores, 2048, idx)
+
+
 @pytest.mark.parametrize("max_ctx", [None, 80 * 1024])
 def test_topk_empty_padding_and_mask_edges(max_ctx):
     case, scores = _topk_case([0, 2040, 3000], [4, 64, 40], seed=7, words=3)
