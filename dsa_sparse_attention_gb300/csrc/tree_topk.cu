@@ -223,32 +223,37 @@ static_assert(kDirect >= kSamples && kTreeTopkCap >= kDirect, "a stretch of scor
 // ----------------------------------------------------------------------- step 2
 
 __global__ void __launch_bounds__(kFilterThreads) tree_topk_filter_kernel(TreeTopkParams p) {
-  __shared__ uint32_t wsh[32];
+  __shared__ uint32_t wsh[2][32];
   __shared__ uint32_t base_sh;
   const int t = blockIdx.y, c = blockIdx.x;
   const float* row = p.scores + static_cast<int64_t>(t) * p.ld;
-  const int s0 = c * kTopkChunk + static_cast<int>(threadIdx.x) * kPer;
+  // Thread i holds the scores 4 i .. 4 i + 3 of each of the chunk's four quarters: whole lines per load.
+  const int s0 = c * kTopkChunk + 4 * static_cast<int>(threadIdx.x);
+  constexpr int kQuarter = kTopkChunk / 4;
   // The scores are inputs of the call, not of the kernel before: they are read ahead of the
   // wait, and before the row's length is known (within the row's memory).
-  float v[kPer];
+  float4 v[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    const bool in = s0 + 4 * q + 4 <= p.ld;   // ld is a multiple of 4
-    const float4 x = in ? __ldcs(reinterpret_cast<const float4*>(row + s0) + q) : make_float4(0.f, 0.f, 0.f, 0.f);
-    v[4 * q] = x.x;
-    v[4 * q + 1] = x.y;
-    v[4 * q + 2] = x.z;
-    v[4 * q + 3] = x.w;
+    const int s = s0 + kQuarter * q;
+    v[q] = s + 4 <= p.ld ? __ldcs(reinterpret_cast<const float4*>(row + s)) : make_float4(0.f, 0.f, 0.f, 0.f);
   }
   Row r;
   const bool work = load_row(p, t, r) && filtered(p, r) && c * kTopkChunk < r.n;
   uint32_t u[kPer];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) u[i] = score_key(v[i]);
-  if (work && s0 + kPer > r.base) {
+  for (int q = 0; q < 4; ++q) {
+    u[4 * q] = score_key(v[q].x);
+    u[4 * q + 1] = score_key(v[q].y);
+    u[4 * q + 2] = score_key(v[q].z);
+    u[4 * q + 3] = score_key(v[q].w);
+  }
+  if (work && (c + 1) * kTopkChunk > r.base) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (s0 + i >= r.n || !(s0 + i < r.base || tree_sees(r.mask, p.tree.words, r.base, s0 + i))) u[i] = 0u;
+    for (int i = 0; i < kPer; ++i) {
+      const int s = s0 + kQuarter * (i >> 2) + (i & 3);
+      if (s >= r.n || !(s < r.base || tree_sees(r.mask, p.tree.words, r.base, s))) u[i] = 0u;
+    }
   }
   grid_dep_wait();
   grid_dep_launch();
@@ -257,22 +262,31 @@ __global__ void __launch_bounds__(kFilterThreads) tree_topk_filter_kernel(TreeTo
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) m |= static_cast<uint32_t>(u[i] >= bound) << i;
-  uint32_t total;
-  const uint32_t o = scan(__popc(m), wsh, total);
+  // prefixes of the four quarters' counts, two to a word (at most 1,024 each)
+  const uint32_t n01 = __popc(m & 0xFu) | (__popc(m & 0xF0u) << 16), n23 = __popc(m & 0xF00u) | (__popc(m & 0xF000u) << 16);
+  uint32_t t01, t23;
+  const uint32_t o01 = scan(n01, wsh[0], t01), o23 = scan(n23, wsh[1], t23);
+  const uint32_t q1 = t01 & 0xFFFFu, q2 = q1 + (t01 >> 16), q3 = q2 + (t23 & 0xFFFFu), total = q3 + (t23 >> 16);
   if (threadIdx.x == 0) {
     base_sh = total ? atomicAdd(p.fill + t, total) : 0u;
     p.at[static_cast<int64_t>(t) * p.nchunks + c] = base_sh;
     p.num[static_cast<int64_t>(t) * p.nchunks + c] = total;
   }
   __syncthreads();
-  uint32_t at = base_sh + o;
+  const uint32_t first[4] = {o01 & 0xFFFFu, q1 + (o01 >> 16), q2 + (o23 & 0xFFFFu), q3 + (o23 >> 16)};
   uint2* list = p.list + static_cast<int64_t>(t) * p.cap;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i)
-    if ((m >> i) & 1u) {
-      if (at < static_cast<uint32_t>(p.cap)) list[at] = make_uint2(u[i], static_cast<uint32_t>(s0 + i));
-      ++at;
+  for (int q = 0; q < 4; ++q) {
+    uint32_t at = base_sh + first[q];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = 4 * q + e;
+      if ((m >> i) & 1u) {
+        if (at < static_cast<uint32_t>(p.cap)) list[at] = make_uint2(u[i], static_cast<uint32_t>(s0 + kQuarter * q + e));
+        ++at;
+      }
     }
+  }
 }
 
 // ----------------------------------------------------------------------- step 3
