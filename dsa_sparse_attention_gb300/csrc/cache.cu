@@ -9,6 +9,9 @@
 // arrival, so all results are deterministic.
 #include "cache.cuh"
 
+// Every kernel here may be scheduled before the kernel before it on the stream has ended
+// (programmatic launch) and waits for it before it touches memory: the launches of a
+// free, a fork and a copy in a row overlap.
 namespace dsa {
 
 namespace {
@@ -42,6 +45,8 @@ constexpr int kCopyVec = 4;
 constexpr int kCopyUnit = kCopyThreads * kCopyVec * 16;
 
 __global__ void __launch_bounds__(kCopyThreads) cache_copy_kernel(CacheCopyParams p) {
+  grid_dep_wait();
+  grid_dep_launch();
   const int64_t per_row = cdiv(p.row_bytes, kCopyUnit);
   int64_t n = p.n;
   if (p.count) {
@@ -80,21 +85,28 @@ cudaError_t launch_cache_copy(const CacheCopyParams& p, int nsm, cudaStream_t st
   const int64_t units = p.n * cdiv(p.row_bytes, kCopyUnit);
   const int64_t full = static_cast<int64_t>(nsm) * (2048 / kCopyThreads);
   const unsigned grid = static_cast<unsigned>(units < full ? units : full);
-  return launch_ex(cache_copy_kernel, dim3(grid), dim3(kCopyThreads), 0, st, false, 0u, p);
+  return launch_ex(cache_copy_kernel, dim3(grid), dim3(kCopyThreads), 0, st, true, 0u, p);
 }
 
 // ------------------------------------------------------------------------- fork
 //
-// Two launches.  The plan: one cluster of eight CTAs scans the counts (each an eighth
-// of the rows) and lists the first free rows in ascending order, while its first CTA
-// checks the forks and numbers those that need a row.  The apply: CTAs per fork copy
-// the table row and count the shared blocks.
+// The plan: one CTA, or a cluster of eight for more rows than kOneCtaRows, scans the counts
+// (each CTA its part of the rows) and lists the first free rows in ascending order; the
+// first CTA checks the forks and numbers those that need a row.  The apply copies the
+// table rows and counts the shared blocks: in the plan's CTAs when that is little, else
+// in a second launch with CTAs per fork.
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanCtas = 8;
+// Launches cost about as much as these kernels: measured on 600 rows and 8 forks, one CTA
+// and one launch take 5.9 us, a cluster and two launches 9.4 us.
+constexpr int64_t kOneCtaRows = 16384;
+constexpr int64_t kOneLaunchEntries = 8192;   // table entries per plan CTA
+
+unsigned plan_ctas(int64_t num_rows) { return num_rows <= kOneCtaRows ? 1u : static_cast<unsigned>(kPlanCtas); }
 
 // Rows [r0, r1) of the cluster's CTA `rank`, multiples of 4 rows.
 __device__ __forceinline__ void plan_rows(int64_t num_rows, uint32_t rank, int64_t& r0, int64_t& r1) {
-  const int64_t per = (cdiv(num_rows, kPlanCtas) + 3) / 4 * 4;
+  const int64_t per = (cdiv(num_rows, cluster_size()) + 3) / 4 * 4;
   r0 = per * rank;
   if (r0 > num_rows) r0 = num_rows;
   r1 = r0 + per < num_rows ? r0 + per : num_rows;
@@ -121,45 +133,18 @@ __device__ __forceinline__ uint32_t count_free(const int32_t* ref, int64_t r0, i
 // Every CTA's count in every CTA: `mine` of this one; the sum of the ranks before it and of all.
 __device__ __forceinline__ void share_counts(uint32_t mine, uint32_t* counts, uint32_t rank, int64_t& before,
                                              int64_t& all) {
-  if (threadIdx.x < kPlanCtas) st_cluster_u32(cluster_map(smem_u32(&counts[rank]), threadIdx.x), mine);
+  const uint32_t csize = cluster_size();
+  if (threadIdx.x < csize) st_cluster_u32(cluster_map(smem_u32(&counts[rank]), threadIdx.x), mine);
   cluster_sync();
   before = all = 0;
-  for (uint32_t r = 0; r < kPlanCtas; ++r) {
+  for (uint32_t r = 0; r < csize; ++r) {
     if (r < rank) before += counts[r];
     all += counts[r];
   }
 }
 
-__global__ void __launch_bounds__(kPlanThreads) cache_fork_plan_kernel(ForkParams p) {
-  __shared__ uint32_t wsh[33];
-  __shared__ uint32_t counts[kPlanCtas];
-  const uint32_t rank = cluster_rank();
-  cluster_sync();   // every CTA has started before any writes into it
-  int64_t r0, r1;
-  plan_rows(p.num_rows, rank, r0, r1);
-  const uint32_t mine = count_free(p.ref, r0, r1, wsh);
-  int64_t before, all;
-  share_counts(mine, counts, rank, before, all);
-  // list the first free rows, up to one per fork
-  uint32_t at = 0;   // free rows of this CTA before the chunk
-  for (int64_t c = r0; c < r1 && before + at < p.n; c += 4 * kPlanThreads) {
-    const int64_t r = c + 4 * threadIdx.x;
-    const uint32_t m = r < r1 ? free_bits(p.ref, r, r1) : 0u;
-    uint32_t total;
-    int64_t o = before + at + block_scan(__popc(m), wsh, total);
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if ((m >> k) & 1u) {
-        if (o < p.n) p.free_list[o] = static_cast<int32_t>(r + k);
-        ++o;
-      }
-    at += total;
-  }
-  if (rank == 0)
-    for (int i = threadIdx.x; i < p.num_reqs; i += kPlanThreads) p.marks[i] = 0;
-  __threadfence();
-  cluster_sync();   // the list is complete and visible
-  if (rank != 0) return;
+// Checks the forks and numbers those that need a row (of `all` free ones).  One CTA.
+__device__ __forceinline__ void plan_forks(const ForkParams& p, int64_t all, uint32_t* wsh) {
   // who is named: children counted in the low half, parents flagged above
   for (int i = threadIdx.x; i < p.n; i += kPlanThreads) {
     const int32_t a = p.parent[i], c = p.child[i];
@@ -205,43 +190,91 @@ __global__ void __launch_bounds__(kPlanThreads) cache_fork_plan_kernel(ForkParam
   }
 }
 
+// One table entry of a fork.
+__device__ __forceinline__ void apply_fork(const ForkParams& p, int i, int32_t row, int e) {
+  if (row == kForkSkip) return;
+  const int32_t a = p.parent[i], c = p.child[i];
+  const int32_t L = __ldcg(p.ctx + a);   // a parent is no child of this call: not written here
+  const int32_t full = L >> p.log2_bs;
+  int32_t b = -1;
+  if (e < full) {
+    b = p.bt[static_cast<int64_t>(a) * p.bt_stride + e];
+    if (b >= 0 && b < p.num_rows) {
+      atomicAdd(p.ref + b, 1);
+    } else {
+      atomicOr(p.status, DEV_BAD_BLOCK);
+      b = -1;
+    }
+  } else if (e == full && row >= 0) {
+    b = row;
+    p.ref[row] = 1;
+  }
+  p.bt[static_cast<int64_t>(c) * p.bt_stride + e] = b;
+  if (e == 0) p.ctx[c] = L;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) cache_fork_plan_kernel(ForkParams p) {
+  __shared__ uint32_t wsh[33];
+  __shared__ uint32_t counts[kPlanCtas];
+  const uint32_t rank = cluster_rank();
+  grid_dep_wait();
+  grid_dep_launch();
+  cluster_sync();   // every CTA has started before any writes into it
+  int64_t r0, r1;
+  plan_rows(p.num_rows, rank, r0, r1);
+  const uint32_t mine = count_free(p.ref, r0, r1, wsh);
+  int64_t before, all;
+  share_counts(mine, counts, rank, before, all);
+  // list the first free rows, up to one per fork
+  uint32_t at = 0;   // free rows of this CTA before the chunk
+  for (int64_t c = r0; c < r1 && before + at < p.n; c += 4 * kPlanThreads) {
+    const int64_t r = c + 4 * threadIdx.x;
+    const uint32_t m = r < r1 ? free_bits(p.ref, r, r1) : 0u;
+    uint32_t total;
+    int64_t o = before + at + block_scan(__popc(m), wsh, total);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if ((m >> k) & 1u) {
+        if (o < p.n) p.free_list[o] = static_cast<int32_t>(r + k);
+        ++o;
+      }
+    at += total;
+  }
+  if (rank == 0)
+    for (int i = threadIdx.x; i < p.num_reqs; i += kPlanThreads) p.marks[i] = 0;
+  __threadfence();
+  cluster_sync();   // the list is complete and visible
+  if (rank == 0) plan_forks(p, all, wsh);
+  if (!p.apply_here) return;
+  __threadfence();
+  cluster_sync();   // so is the plan
+  const int64_t entries = static_cast<int64_t>(p.n) * p.bt_stride;
+  for (int64_t e = static_cast<int64_t>(rank) * kPlanThreads + threadIdx.x; e < entries;
+       e += static_cast<int64_t>(cluster_size()) * kPlanThreads) {
+    const int i = static_cast<int>(e / p.bt_stride);
+    apply_fork(p, i, __ldcg(p.plan + i), static_cast<int>(e - static_cast<int64_t>(i) * p.bt_stride));
+  }
+}
+
 constexpr int kApplyThreads = 256;
 constexpr int kApplyEntries = 1024;   // table entries per CTA
 
 __global__ void __launch_bounds__(kApplyThreads) cache_fork_apply_kernel(ForkParams p) {
   grid_dep_wait();
+  grid_dep_launch();
   const int i = blockIdx.x;
   const int32_t row = p.plan[i];
-  if (row == kForkSkip) return;
-  const int32_t a = p.parent[i], c = p.child[i];
-  const int32_t L = p.ctx[a];   // a parent is no child of this call: not written here
-  const int32_t full = L >> p.log2_bs;
-  const int32_t* from = p.bt + static_cast<int64_t>(a) * p.bt_stride;
-  int32_t* to = p.bt + static_cast<int64_t>(c) * p.bt_stride;
   const int e1 = min(p.bt_stride, static_cast<int>(blockIdx.y + 1) * kApplyEntries);
-  for (int e = blockIdx.y * kApplyEntries + threadIdx.x; e < e1; e += kApplyThreads) {
-    int32_t b = -1;
-    if (e < full) {
-      b = from[e];
-      if (b >= 0 && b < p.num_rows) {
-        atomicAdd(p.ref + b, 1);
-      } else {
-        atomicOr(p.status, DEV_BAD_BLOCK);
-        b = -1;
-      }
-    } else if (e == full && row >= 0) {
-      b = row;
-      p.ref[row] = 1;
-    }
-    to[e] = b;
-  }
-  if (blockIdx.y == 0 && threadIdx.x == 0) p.ctx[c] = L;
+  for (int e = blockIdx.y * kApplyEntries + threadIdx.x; e < e1; e += kApplyThreads) apply_fork(p, i, row, e);
 }
 
-cudaError_t launch_cache_fork(const ForkParams& p, cudaStream_t st) {
-  if (p.n == 0) return cudaSuccess;
-  cudaError_t e = launch_ex(cache_fork_plan_kernel, dim3(kPlanCtas), dim3(kPlanThreads), 0, st, false, kPlanCtas, p);
-  if (e != cudaSuccess) return e;
+cudaError_t launch_cache_fork(const ForkParams& in, cudaStream_t st) {
+  if (in.n == 0) return cudaSuccess;
+  ForkParams p = in;
+  const unsigned ctas = plan_ctas(p.num_rows);
+  p.apply_here = static_cast<int64_t>(p.n) * p.bt_stride <= kOneLaunchEntries * ctas;
+  cudaError_t e = launch_ex(cache_fork_plan_kernel, dim3(ctas), dim3(kPlanThreads), 0, st, true, ctas, p);
+  if (e != cudaSuccess || p.apply_here) return e;
   return launch_ex(cache_fork_apply_kernel, dim3(p.n, static_cast<unsigned>(cdiv(p.bt_stride, kApplyEntries))),
                    dim3(kApplyThreads), 0, st, true, 0u, p);
 }
@@ -251,6 +284,8 @@ cudaError_t launch_cache_fork(const ForkParams& p, cudaStream_t st) {
 // Each entry is claimed by an exchange with -1, so a request that is named twice, or
 // by two CTAs, gives back every block once.
 __global__ void __launch_bounds__(kApplyThreads) cache_free_kernel(FreeParams p) {
+  grid_dep_wait();
+  grid_dep_launch();
   const int32_t r = p.reqs[blockIdx.x];
   if (r < 0) return;
   if (r >= p.num_reqs) {
@@ -276,19 +311,32 @@ __global__ void __launch_bounds__(kApplyThreads) cache_free_kernel(FreeParams p)
 cudaError_t launch_cache_free(const FreeParams& p, cudaStream_t st) {
   if (p.n == 0) return cudaSuccess;
   return launch_ex(cache_free_kernel, dim3(p.n, static_cast<unsigned>(cdiv(p.bt_stride, kApplyEntries))),
-                   dim3(kApplyThreads), 0, st, false, 0u, p);
+                   dim3(kApplyThreads), 0, st, true, 0u, p);
 }
 
 // ------------------------------------------------------------------- compaction
 //
-// One cluster counts the used rows L; then each CTA numbers its holes (free rows
+// The plan's CTAs count the used rows L; then each CTA numbers its holes (free rows
 // before L) and movers (used rows at or behind L) and writes them to their places in
 // the two lists; then the lists, complete, give the remaining counts and the map from
-// old row to new.  A second launch maps the block tables.
+// old row to new.  The block tables are mapped in the same launch when they are small.
+// One table entry's row after the moves.
+__device__ __forceinline__ void map_entry(const CompactParams& p, int64_t e) {
+  const int32_t b = p.bt[e];
+  int32_t to = -1;
+  if (b >= 0) {
+    if (b < p.num_rows) to = __ldcg(p.remap + b);
+    if (to < 0) atomicOr(p.status, DEV_BAD_BLOCK);
+  }
+  p.to_bt[e] = to;
+}
+
 __global__ void __launch_bounds__(kPlanThreads) cache_compact_plan_kernel(CompactParams p) {
   __shared__ uint32_t wsh[33];
   __shared__ uint32_t c_free[kPlanCtas], c_hole[kPlanCtas];
   const uint32_t rank = cluster_rank();
+  grid_dep_wait();
+  grid_dep_launch();
   cluster_sync();
   int64_t r0, r1;
   plan_rows(p.num_rows, rank, r0, r1);
@@ -343,7 +391,8 @@ __global__ void __launch_bounds__(kPlanThreads) cache_compact_plan_kernel(Compac
   cluster_sync();   // both lists are complete and visible
   const int64_t tid = static_cast<int64_t>(rank) * kPlanThreads + threadIdx.x;
   const int64_t cap = p.num_rows / 2 > 0 ? p.num_rows / 2 : 1;
-  for (int64_t i = tid; i < cap; i += kPlanCtas * kPlanThreads) {
+  const int64_t threads = static_cast<int64_t>(cluster_size()) * kPlanThreads;
+  for (int64_t i = tid; i < cap; i += threads) {
     if (i < m) {
       const int32_t s = __ldcg(p.copy_src + i), d = __ldcg(p.copy_dst + i);
       const int32_t v = __ldcg(p.ref + s);   // read before either place is written (they may be one array)
@@ -355,27 +404,30 @@ __global__ void __launch_bounds__(kPlanThreads) cache_compact_plan_kernel(Compac
       p.copy_dst[i] = -1;
     }
   }
+  if (!p.tables_here) return;
+  __threadfence();
+  cluster_sync();   // the map is complete and visible
+  const int64_t n = static_cast<int64_t>(p.num_reqs) * p.bt_stride;
+  for (int64_t e = tid; e < n; e += threads) map_entry(p, e);
 }
 
 __global__ void __launch_bounds__(kApplyThreads) cache_compact_tables_kernel(CompactParams p) {
   grid_dep_wait();
+  grid_dep_launch();
   const int64_t n = static_cast<int64_t>(p.num_reqs) * p.bt_stride;
   for (int64_t e = blockIdx.x * static_cast<int64_t>(kApplyThreads) + threadIdx.x; e < n;
-       e += static_cast<int64_t>(gridDim.x) * kApplyThreads) {
-    const int32_t b = p.bt[e];
-    int32_t to = -1;
-    if (b >= 0) {
-      if (b < p.num_rows) to = p.remap[b];
-      if (to < 0) atomicOr(p.status, DEV_BAD_BLOCK);
-    }
-    p.to_bt[e] = to;
-  }
+       e += static_cast<int64_t>(gridDim.x) * kApplyThreads)
+    map_entry(p, e);
 }
 
-cudaError_t launch_cache_compact(const CompactParams& p, int nsm, cudaStream_t st) {
-  cudaError_t e = launch_ex(cache_compact_plan_kernel, dim3(kPlanCtas), dim3(kPlanThreads), 0, st, false, kPlanCtas, p);
-  if (e != cudaSuccess) return e;
-  const int64_t blocks = cdiv(static_cast<int64_t>(p.num_reqs) * p.bt_stride, kApplyThreads);
+cudaError_t launch_cache_compact(const CompactParams& in, int nsm, cudaStream_t st) {
+  CompactParams p = in;
+  const int64_t entries = static_cast<int64_t>(p.num_reqs) * p.bt_stride;
+  const unsigned ctas = plan_ctas(p.num_rows);
+  p.tables_here = entries <= kOneLaunchEntries * ctas;
+  cudaError_t e = launch_ex(cache_compact_plan_kernel, dim3(ctas), dim3(kPlanThreads), 0, st, true, ctas, p);
+  if (e != cudaSuccess || p.tables_here) return e;
+  const int64_t blocks = cdiv(entries, kApplyThreads);
   const int64_t full = static_cast<int64_t>(nsm) * 8;
   return launch_ex(cache_compact_tables_kernel, dim3(static_cast<unsigned>(blocks < full ? blocks : full)),
                    dim3(kApplyThreads), 0, st, true, 0u, p);
@@ -394,6 +446,8 @@ constexpr int kCommitThreads = 384;  // >= 8 records x (8 + 36 + 1) pieces
 __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(CommitParams p) {
   __shared__ int32_t slots[kCommitChunk];
   __shared__ int bad_sh;
+  grid_dep_wait();
+  grid_dep_launch();
   const int r = blockIdx.x;
   const int32_t* acc = p.accept + static_cast<int64_t>(r) * p.max_accept;
   const int32_t base = p.base[r], L = p.ctx[r];
@@ -469,7 +523,7 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(CommitParam
 }
 
 cudaError_t launch_tree_commit(const CommitParams& p, int num_reqs, cudaStream_t st) {
-  return launch_ex(tree_commit_kernel, dim3(num_reqs), dim3(kCommitThreads), 0, st, false, 0u, p);
+  return launch_ex(tree_commit_kernel, dim3(num_reqs), dim3(kCommitThreads), 0, st, true, 0u, p);
 }
 
 }  // namespace dsa

@@ -32,6 +32,7 @@ struct ForkParams {
   int32_t* plan;        // [n]        scratch: the row of the partial block, -1 none, or kForkSkip
   int32_t* marks;       // [num_reqs] scratch
   uint32_t* status;
+  int apply_here = 0;   // the plan's CTAs apply the forks, too (set by the launcher)
 };
 
 struct FreeParams {
@@ -57,6 +58,7 @@ struct CompactParams {
   int32_t* counts;
   int32_t* remap;       // [num_rows] scratch
   uint32_t* status;
+  int tables_here = 0;  // the plan's CTAs map the tables, too (set by the launcher)
 };
 
 struct CommitParams {
