@@ -337,14 +337,16 @@ TreeView tree_view(const dsa_tree* t) { return TreeView{t->base, t->mask, t->mas
 
 // Workspace of dsa_tree_mla.
 struct TreeWs {
-  size_t status = 0, starts = 0, q_terms = 0, q_exps = 0, part_o = 0, part_ml = 0, total = 0;
+  size_t status = 0, starts = 0, toks = 0, shares = 0, q_terms = 0, q_exps = 0, part_o = 0, part_ml = 0, total = 0;
 };
 
 TreeWs plan_tree_ws(const dsa_kv_layout* l, const dsa_batch* b) {
   TreeWs w;
   const size_t slots = 2 * size_t(num_sms());
   w.starts = kStatusBytes;
-  w.q_terms = align_up(w.starts + (size_t(b->num_tokens) + 1) * sizeof(int64_t));
+  w.toks = align_up(w.starts + (size_t(b->num_tokens) + 1) * sizeof(int64_t));
+  w.shares = align_up(w.toks + size_t(b->num_tokens) * sizeof(TreeToken));
+  w.q_terms = align_up(w.shares + size_t(num_sms()) * sizeof(TreeShare));
   // FP8 latents: terms and exponents together; NVFP4: fp16 values, then exponents
   const size_t T = size_t(b->num_tokens);
   w.q_exps = align_up(w.q_terms + T * (l->lat_fmt == DSA_LAT_FP8 ? size_t(kQTokenBytes) : size_t(kMlaHeads) * kLatDim * 2));
@@ -907,6 +909,8 @@ dsa_status dsa_tree_mla(const dsa_kv_layout* layout, const dsa_batch* batch, con
   p.tree = tree_view(tree);
   p.scale_log2 = sm_scale * 1.4426950408889634f;
   p.starts = at<int64_t>(workspace, wl.starts);
+  p.toks = at<TreeToken>(workspace, wl.toks);
+  p.shares = at<TreeShare>(workspace, wl.shares);
   p.max_ctas = num_sms();
   p.whole = (batch->flags & DSA_BATCH_INVARIANT) ? 1 : 0;
   p.out = static_cast<__nv_bfloat16*>(out);
@@ -922,9 +926,19 @@ dsa_status dsa_tree_mla(const dsa_kv_layout* layout, const dsa_batch* batch, con
   CUtensorMap amap, bmap;
   if (fp8 ? !(make_latent_map(&amap, layout, 128) && make_latent_map(&bmap, layout, 64)) : !make_q_map(&amap, q16, T))
     return encode_fail();
-  const cudaError_t e = launch_tree_prep(p.b, p.tree, static_cast<const __nv_bfloat16*>(q), terms, q16,
-                                         at<int32_t>(workspace, wl.q_exps), at<int64_t>(workspace, wl.starts), p.status,
-                                         stream);
+  TreePrepParams pp;
+  pp.b = p.b;
+  pp.tree = p.tree;
+  pp.q = static_cast<const __nv_bfloat16*>(q);
+  pp.terms = terms;
+  pp.q16 = q16;
+  pp.exps = at<int32_t>(workspace, wl.q_exps);
+  pp.starts = at<int64_t>(workspace, wl.starts);
+  pp.toks = at<TreeToken>(workspace, wl.toks);
+  pp.shares = at<TreeShare>(workspace, wl.shares);
+  pp.max_ctas = p.max_ctas;
+  pp.status = p.status;
+  const cudaError_t e = launch_tree_prep(pp, stream);
   if (e != cudaSuccess) return cuda_fail(e);
   return cuda_status(fp8 ? launch_tree_mla_fp8(amap, bmap, p, stream) : launch_tree_mla_nvfp4(amap, p, stream));
 }

@@ -472,6 +472,15 @@ __device__ __forceinline__ void bulk_prefetch_l2(const void* src, uint32_t bytes
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Four 8 x 8 matrices of 16-bit values, transposed on the way into shared memory: thread l
+// holds of matrix i row l / 4, columns 2 (l % 4) and + 1 in r_i; column c of matrix i goes,
+// 16 contiguous bytes, to the address that lane 8 i + c passes.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t saddr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(saddr), "r"(r0), "r"(r1),
+               "r"(r2), "r"(r3)
+               : "memory");
+}
+
 // Warp-wide max of a float (sm_100-family redux).
 __device__ __forceinline__ float warp_max_f32(float v) {
   float r;

@@ -64,30 +64,33 @@ __device__ __forceinline__ void q_head_to_f16(const __nv_bfloat16* q_tok, int h,
 
 constexpr int kPrepThreads = 1024;
 
-__global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(BatchView b, TreeView tree, const __nv_bfloat16* q,
-                                                                 uint8_t* terms, __half* q16, int32_t* exps,
-                                                                 int64_t* starts, uint32_t* status) {
+__global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(TreePrepParams p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  grid_dep_wait();
+  grid_dep_launch();
   if (blockIdx.x > 0) {
     const int t = (blockIdx.x - 1) / 3, h = (blockIdx.x - 1) % 3 * 32 + warp;
-    const __nv_bfloat16* q_tok = q + static_cast<int64_t>(t) * kMlaHeads * kLatDim;
-    if (q16) {
-      q_head_to_f16(q_tok, h, q16 + static_cast<int64_t>(t) * kMlaHeads * kLatDim,
-                    exps + static_cast<int64_t>(t) * kMlaHeads);
+    const __nv_bfloat16* q_tok = p.q + static_cast<int64_t>(t) * kMlaHeads * kLatDim;
+    if (p.q16) {
+      q_head_to_f16(q_tok, h, p.q16 + static_cast<int64_t>(t) * kMlaHeads * kLatDim,
+                    p.exps + static_cast<int64_t>(t) * kMlaHeads);
     } else {
-      uint8_t* tok = terms + static_cast<int64_t>(t) * kQTokenBytes;
+      uint8_t* tok = p.terms + static_cast<int64_t>(t) * kQTokenBytes;
       q_head_to_terms(q_tok, h, tok, reinterpret_cast<int32_t*>(tok + kQTermBytes));
     }
     return;
   }
   __shared__ int64_t wsum[kPrepThreads / 32];
+  __shared__ int64_t st_sh[kPrepThreads + 1];   // the starts of a batch of up to 1,024 tokens
+  const int T = p.b.T;
   int64_t base = 0;
-  for (int t0 = 0; t0 < b.T; t0 += kPrepThreads) {
+  for (int t0 = 0; t0 < T; t0 += kPrepThreads) {
     const int t = t0 + threadIdx.x;
     int64_t v = 0;
-    if (t < b.T) {
-      int req, pos, committed;
-      if (load_tree_token(b, tree, t, status, req, pos, committed)) v = cdiv(pos + 1, kSelTile);
+    if (t < T) {
+      TreeToken k = {0, 0, 0, 0};
+      if (load_tree_token(p.b, p.tree, t, p.status, k.req, k.pos, k.base)) v = cdiv(k.pos + 1, kSelTile);
+      p.toks[t] = k;
     }
     int64_t x = v;
 #pragma unroll
@@ -102,45 +105,67 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(BatchView b, Tr
       if (w < warp) before += wsum[w];
       total += wsum[w];
     }
-    if (t < b.T) starts[t] = base + before + x - v;
+    if (t < T) p.starts[t] = base + before + x - v;
+    st_sh[threadIdx.x] = base + before + x - v;
     base += total;
     __syncthreads();
   }
-  if (threadIdx.x == 0) starts[b.T] = base;
+  if (threadIdx.x == 0) p.starts[T] = base;
+  __syncthreads();
+  // each CTA's share and its first token: the last one that starts at or before the share,
+  // so never one without tiles
+  const int G = static_cast<int>(base < p.max_ctas ? base : p.max_ctas);
+  for (int c = threadIdx.x; c < p.max_ctas; c += kPrepThreads) {
+    TreeShare s = {};
+    if (c < G) {
+      s.g0 = share_begin(base, G, c);
+      s.g1 = share_begin(base, G, c + 1);
+      int lo = 0, hi = T;   // starts[lo] <= g0 < starts[hi]
+      while (hi - lo > 1) {
+        const int m = (lo + hi) >> 1;
+        if ((T <= kPrepThreads ? st_sh[m] : __ldcg(p.starts + m)) <= s.g0) lo = m;
+        else hi = m;
+      }
+      s.t = lo;
+      s.u0 = T <= kPrepThreads ? st_sh[lo] : __ldcg(p.starts + lo);
+      s.u1 = lo + 1 == T ? base : (T <= kPrepThreads ? st_sh[lo + 1] : __ldcg(p.starts + lo + 1));
+      const int4 k = __ldcg(reinterpret_cast<const int4*>(p.toks) + lo);
+      s.tok = TreeToken{k.x, k.y, k.z, k.w};
+    }
+    p.shares[c] = s;
+  }
 }
 
-cudaError_t launch_tree_prep(const BatchView& b, const TreeView& tree, const __nv_bfloat16* q, uint8_t* terms,
-                             __half* q16, int32_t* exps, int64_t* starts, uint32_t* status, cudaStream_t st) {
-  return launch_ex(tree_prep_kernel, dim3(1 + 3 * b.T), dim3(kPrepThreads), 0, st, false, 0u, b, tree, q, terms, q16,
-                   exps, starts, status);
+cudaError_t launch_tree_prep(const TreePrepParams& p, cudaStream_t st) {
+  return launch_ex(tree_prep_kernel, dim3(1 + 3 * p.b.T), dim3(kPrepThreads), 0, st, true, 0u, p);
 }
 
-// The first token of share [g0, ...): every thread of the CTA searches.
-__device__ __forceinline__ SegmentWalk make_walk(const TreeMlaParams& p, int* first_sh) {
+__device__ __forceinline__ SegmentWalk make_walk(const TreeMlaParams& p) {
   SegmentWalk w;
-  const int64_t W = __ldcg(p.starts + p.b.T);
   w.starts = p.starts;
+  w.toks = p.toks;
   w.T = p.b.T;
   w.whole = p.whole;
   w.cta = blockIdx.x;
-  w.G = static_cast<int>(W < p.max_ctas ? W : p.max_ctas);
-  w.g0 = w.g = w.g1 = 0;
-  w.t = 0;
-  if (p.whole) {
-    w.G = p.max_ctas;
-    w.t = blockIdx.x;
-    return w;
+  w.G = p.max_ctas;
+  w.g0 = w.g = w.g1 = w.u0 = w.u1 = 0;
+  w.t = blockIdx.x;
+  if (!p.whole) {
+    const int4* r = reinterpret_cast<const int4*>(p.shares + blockIdx.x);
+    const int4 a = __ldcg(r), b = __ldcg(r + 1), c = __ldcg(r + 2), d = __ldcg(r + 3);
+    auto i64 = [](int lo, int hi) {
+      return static_cast<int64_t>(static_cast<uint32_t>(lo)) | (static_cast<int64_t>(hi) << 32);
+    };
+    w.g0 = w.g = i64(a.x, a.y);
+    w.g1 = i64(a.z, a.w);
+    w.u0 = i64(b.x, b.y);
+    w.u1 = i64(b.z, b.w);
+    w.t = c.x;
+    w.tok = TreeToken{d.x, d.y, d.z, d.w};
   }
-  if (static_cast<int>(blockIdx.x) < w.G) {
-    w.g0 = w.g = share_begin(W, w.G, blockIdx.x);
-    w.g1 = share_begin(W, w.G, blockIdx.x + 1);
-    for (int t = threadIdx.x; t < w.T; t += blockDim.x)
-      if (__ldcg(p.starts + t) <= w.g0 && w.g0 < __ldcg(p.starts + t + 1)) *first_sh = t;
-  }
-  __syncthreads();
-  w.t = *first_sh;
   return w;
 }
+static_assert(sizeof(TreeShare) == 64 && sizeof(TreeToken) == 16, "read 16 bytes at a time");
 
 __device__ __forceinline__ uint8_t* align1024_tree(uint8_t* p) {
   return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -156,21 +181,60 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Abort 
 // Head, in its group of 32, of column n of the group in P and O.
 __device__ __forceinline__ constexpr int head_of_column(int n) { return 8 * ((n >> 1) & 3) + 2 * (n >> 3) + (n & 1); }
 
-// Writes 32 heads of one dim per lane: the segment's output (bf16) or its normalised
-// partial (fp16: 11 significant bits, above the output's 8), both [96][512], as 64
-// contiguous bytes per warp and head.
-__device__ __forceinline__ void store_heads(const TreeMlaParams& p, const Segment& s, const uint32_t (&rr)[32],
-                                            const float* inv, int h0, int dim) {
-  float al[32];
-  lds_f32x32(inv + h0, al);
-  if (s.slot < 0) {
-    __nv_bfloat16* o = p.out + (static_cast<int64_t>(s.t) * kMlaHeads + h0) * kVDim + dim;
+// A warp's part of a finished segment: its 32 heads (columns n0 ..) of the 32 dims of its lane
+// quarter, for the four dim blocks, as the output (bf16) or as the normalised partial (fp16:
+// 11 significant bits, above the output's 8), both [96][512].  A thread gets two columns of
+// a dim side by side, a transposing matrix store turns 8 x 8 of them into 8 dims (16 bytes)
+// of a head in the warp's `stage` (2 KB of P's place, free by now), and stores write 64
+// contiguous bytes of 8 heads.  One segment of one tile took 2.4 us with single 2-byte
+// stores and 5.5 us with exchanges between lanes.  `inv`: 1 / sum per column.
+__device__ __forceinline__ void store_segment(const TreeMlaParams& p, const Segment& s, uint32_t o_tmem,
+                                              const float* inv, int n0, int dim0, uint8_t* stage) {
+  const int lane = threadIdx.x & 31;
+  const bool fin = s.slot < 0;
+  const int64_t row0 = (fin ? static_cast<int64_t>(s.t) : static_cast<int64_t>(s.slot)) * kMlaHeads + n0;
+  uint16_t* out = (fin ? reinterpret_cast<uint16_t*>(p.out) : reinterpret_cast<uint16_t*>(p.part_o)) + row0 * kVDim + dim0;
+  float2 iv[4];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) o[head_of_column(i) * kVDim] = __float2bfloat16_rn(__uint_as_float(rr[i]) * al[i]);
-  } else {
-    __half* o = p.part_o + (static_cast<int64_t>(s.slot) * kMlaHeads + h0) * kVDim + dim;
+  for (int b = 0; b < 4; ++b) iv[b] = *reinterpret_cast<const float2*>(inv + n0 + 8 * b + 2 * (lane & 3));
+  // The stage holds column c's 32 dims in 64 bytes, 16-byte piece k at k ^ (c / 2) % 4.
+  auto piece = [&](int c, int k) { return c * 64 + ((k ^ ((c >> 1) & 3)) << 4); };
+#pragma unroll 1
+  for (int v = 0; v < 4; ++v) {
+    uint32_t rr[2][16];
+    DSA_TMEM_LD_16X256_X4(o_tmem + 96 * v + n0, rr[0]);
+    DSA_TMEM_LD_16X256_X4(o_tmem + 96 * v + n0 + (16u << 16), rr[1]);
+    tmem_wait_ld();
 #pragma unroll
-    for (int i = 0; i < 32; ++i) o[head_of_column(i) * kVDim] = __float2half_rn(__uint_as_float(rr[i]) * al[i]);
+    for (int hh = 0; hh < 2; ++hh) {
+      uint32_t w[4][2];   // columns 8 b + 2 a, + 1; dims 16 hh + lane / 4, + 8
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float x = __uint_as_float(rr[hh][4 * b + 2 * u]) * iv[b].x, y = __uint_as_float(rr[hh][4 * b + 2 * u + 1]) * iv[b].y;
+          if (fin) {
+            const __nv_bfloat162 t = __floats2bfloat162_rn(x, y);
+            w[b][u] = *reinterpret_cast<const uint32_t*>(&t);
+          } else {
+            const __half2 t = __floats2half2_rn(x, y);
+            w[b][u] = *reinterpret_cast<const uint32_t*>(&t);
+          }
+        }
+#pragma unroll
+      for (int b = 0; b < 4; b += 2) {
+        const int c = 8 * (b + (lane >> 4)) + (lane & 7);
+        stmatrix_x4_trans(smem_u32(stage) + piece(c, 2 * hh + ((lane >> 3) & 1)), w[b][0], w[b][1], w[b + 1][0], w[b + 1][1]);
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = 8 * k + (lane >> 2);
+      const uint4 x = *reinterpret_cast<const uint4*>(stage + piece(c, lane & 3));
+      *reinterpret_cast<uint4*>(out + head_of_column(c) * kVDim + 128 * v + 8 * (lane & 3)) = x;
+    }
+    __syncwarp();
   }
 }
 
@@ -280,7 +344,6 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
   uint64_t* p_full = bars + 15;     // [3] P of the tokens 8 i + (0..7) of every quarter: i = 0, 1, 2 and 3
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
   int* abortf = reinterpret_cast<int*>(smem + OFF_MISC + 8);
-  int* first_sh = reinterpret_cast<int*>(smem + OFF_MISC + 16);
   float* red = reinterpret_cast<float*>(smem + OFF_REDM);
   float* sh_sh = reinterpret_cast<float*>(smem + OFF_SH);
   float* alpha_sh = reinterpret_cast<float*>(smem + OFF_ALPHA);
@@ -291,7 +354,6 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
     for (int i = 0; i < 15; ++i) mbar_init(&bars[i], 1);
     for (int i = 0; i < 3; ++i) mbar_init(&p_full[i], MATH_WARPS);
     *abortf = 0;
-    *first_sh = 0;
     fence_mbar_init();
     prefetch_tensormap(&lmap);
     prefetch_tensormap(&tmap);
@@ -299,10 +361,10 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
   if (warp == 0) tmem_alloc(tslot, 512);
   grid_dep_wait();   // the plan and the query terms
   grid_dep_launch();
+  SegmentWalk walk = make_walk(p);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  SegmentWalk walk = make_walk(p, first_sh);
   const uint32_t tmem = *tslot;
   const Abort ab{abortf, p.status};
   Segment s;
@@ -315,9 +377,8 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
     bool ok = true;
     int it = 0, q_issued = -1;   // q_issued: parity of the last query copy
     for (int seg = 0; ok && walk.next(s); ++seg) {
-      int req, pos, base;
-      load_tree_token(p.b, p.tree, s.t, p.status, req, pos, base);
-      const int32_t* btrow = p.b.bt + static_cast<int64_t>(req) * p.b.bt_stride;
+      const int pos = s.tok.pos;
+      const int32_t* btrow = p.b.bt + static_cast<int64_t>(s.tok.req) * p.b.bt_stride;
       // this lane's page of tile j: pool row (num_rows, which reads as zeros, for a bad id)
       auto page = [&](int j) {
         const int s0 = j * kSelTile + lane * box;
@@ -338,12 +399,11 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
       if (seg > 0) ok = warp_wait(q_done, (seg - 1) & 1, ab, ok);
       if (!ok) break;
       q_issued = seg & 1;
-      if (lane == 0) {
-        const uint8_t* src = p.q_terms + static_cast<int64_t>(s.t) * kQTokenBytes;
-        mbar_arrive_expect_tx(q_full, kQTokenBytes);
-        for (int c = 0; c < kQChunks; ++c) bulk_load(smem + OFF_Q + c * QCHUNK, src + c * QCHUNK, QCHUNK, q_full);
-        bulk_load(smem + OFF_QEXP, src + kQTermBytes, kMlaHeads * 4, q_full);
-      }
+      const uint8_t* src = p.q_terms + static_cast<int64_t>(s.t) * kQTokenBytes;
+      if (lane == 0) mbar_arrive_expect_tx(q_full, kQTokenBytes);
+      __syncwarp();
+      if (lane < kQChunks) bulk_load(smem + OFF_Q + lane * QCHUNK, src + lane * QCHUNK, QCHUNK, q_full);
+      else if (lane == kQChunks) bulk_load(smem + OFF_QEXP, src + kQTermBytes, kMlaHeads * 4, q_full);
       for (int j = s.j0; ok && j < s.j1; ++j, ++it) {
         const int c1 = (j * kSelTile + lane * box) & (p.pool.bs - 1);
         const int n = __popc(__ballot_sync(0xffffffffu, row >= 0));
@@ -493,8 +553,7 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
     bool ok = true;
     int it = 0;
     for (int seg = 0; walk.next(s); ++seg) {
-      int req, pos, base;
-      load_tree_token(p.b, p.tree, s.t, p.status, req, pos, base);
+      const int pos = s.tok.pos, base = s.tok.base;
       const uint32_t* mrow = p.tree.mask + static_cast<int64_t>(s.t) * p.tree.words;
       const int plain = min(base, pos + 1);   // positions below are all seen
       ok = warp_wait(q_full, seg & 1, ab, ok);
@@ -544,10 +603,16 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
           }
           return mx;
         };
-        float mx = logits(0);
-        tmem_wait_ld();
-        mx = fmaxf(mx, logits(2));
-        if (named_bar_any(1, MATH, mx > SHIFT + TAU)) {
+        bool moves = j == s.j0;   // a segment's first tile sets the references
+        if (moves) {
+          tmem_wait_ld();
+        } else {
+          float mx = logits(0);
+          tmem_wait_ld();
+          mx = fmaxf(mx, logits(2));
+          moves = named_bar_any(1, MATH, mx > SHIFT + TAU);
+        }
+        if (moves) {
           // some reference moves: the tile's maxima per head
           float hm[8];
 #pragma unroll
@@ -686,15 +751,7 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
       named_bar_sync(2, MATH);
       ok = warp_wait(o_done, seg & 1, ab, ok);
       tc_fence_after();
-      if (ok) {
-#pragma unroll 1
-        for (int v = 0; v < 4; ++v) {
-          uint32_t rr[32];
-          DSA_TMEM_LD32(tmem + O_COL + 96 * v + 32 * g + lane_off, rr);
-          tmem_wait_ld();
-          store_heads(p, s, rr, inv_sh, 32 * g, v * 128 + 32 * quarter + lane);
-        }
-      }
+      if (ok) store_segment(p, s, tmem + O_COL + lane_off, inv_sh, 32 * g, 32 * quarter, smem + OFF_P + warp * 2048);
       tc_fence_before();
     }
   }
@@ -808,7 +865,6 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
   uint64_t* p_full = bars + 27;     // [3]
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
   int* abortf = reinterpret_cast<int*>(smem + OFF_MISC + 8);
-  int* first_sh = reinterpret_cast<int*>(smem + OFF_MISC + 16);
   float* red = reinterpret_cast<float*>(smem + OFF_REDM);
   float* sh_sh = reinterpret_cast<float*>(smem + OFF_SH);
   float* alpha_sh = reinterpret_cast<float*>(smem + OFF_ALPHA);
@@ -820,17 +876,16 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
     for (int i = 13; i < 27; ++i) mbar_init(&bars[i], 1);
     for (int i = 0; i < 3; ++i) mbar_init(&p_full[i], MATH_WARPS);
     *abortf = 0;
-    *first_sh = 0;
     fence_mbar_init();
     prefetch_tensormap(&qmap);
   }
   if (warp == 0) tmem_alloc(tslot, 512);
   grid_dep_wait();   // the plan and the query
   grid_dep_launch();
+  SegmentWalk walk = make_walk(p);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  SegmentWalk walk = make_walk(p, first_sh);
   const uint32_t tmem = *tslot;
   const Abort ab{abortf, p.status};
   Segment s;
@@ -979,8 +1034,7 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
       if (ok && lane == 0) mbar_arrive(&full[f]);
     };
     for (int seg = 0; walk.next(s); ++seg) {
-      int req, pos, base;
-      load_tree_token(p.b, p.tree, s.t, p.status, req, pos, base);
+      const int req = s.tok.req, pos = s.tok.pos, base = s.tok.base;
       const uint32_t* mrow = p.tree.mask + static_cast<int64_t>(s.t) * p.tree.words;
       const int32_t* btrow = p.b.bt + static_cast<int64_t>(req) * p.b.bt_stride;
       const int plain = min(base, pos + 1);   // positions below are all seen
@@ -1063,10 +1117,16 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
           }
           return mx;
         };
-        float mx = logits(0);
-        tmem_wait_ld();
-        mx = fmaxf(mx, logits(2));
-        if (named_bar_any(1, MATH, mx > SHIFT + TAU)) {
+        bool moves = j == s.j0;
+        if (moves) {
+          tmem_wait_ld();
+        } else {
+          float mx = logits(0);
+          tmem_wait_ld();
+          mx = fmaxf(mx, logits(2));
+          moves = named_bar_any(1, MATH, mx > SHIFT + TAU);
+        }
+        if (moves) {
           // P of the tile before has been used (s_full follows its values); some reference moves
           float hm[8];
 #pragma unroll
@@ -1190,15 +1250,7 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
       named_bar_sync(2, MATH);
       ok = warp_wait(o_done, seg & 1, ab, ok);
       tc_fence_after();
-      if (ok) {
-#pragma unroll 1
-        for (int v = 0; v < 4; ++v) {
-          uint32_t rr[32];
-          DSA_TMEM_LD32(tmem + O_COL + 96 * v + 32 * g + lane_off, rr);
-          tmem_wait_ld();
-          store_heads(p, s, rr, inv_sh, 32 * g, v * 128 + 32 * quarter + lane);
-        }
-      }
+      if (ok) store_segment(p, s, tmem + O_COL + lane_off, inv_sh, 32 * g, 32 * quarter, smem + OFF_P + warp * 2048);
       tc_fence_before();
     }
   }

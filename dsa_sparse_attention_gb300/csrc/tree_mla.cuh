@@ -5,6 +5,19 @@
 
 namespace dsa {
 
+// A query token as the kernels need it: request, own position, committed length.
+struct TreeToken {
+  int32_t req, pos, base, pad;
+};
+
+// Where a CTA's share starts: its tiles [g0, g1), and the token t that holds the first.
+struct TreeShare {
+  int64_t g0, g1;
+  int64_t u0, u1;   // the token's tiles
+  int32_t t, pad[3];
+  TreeToken tok;
+};
+
 // The work is a list of key tiles (128 positions) in token order: token t's tiles are
 // [starts[t], starts[t + 1]), W = starts[T] in all.  CTA c of G takes the contiguous
 // share [W c / G, W (c + 1) / G); the part of a token inside a share is a segment.  A
@@ -18,6 +31,8 @@ struct TreeMlaParams {
   TreeView tree;
   float scale_log2;          // sm_scale * log2(e)
   const int64_t* starts;     // [T + 1]
+  const TreeToken* toks;     // [T]
+  const TreeShare* shares;   // [max_ctas]
   const uint8_t* q_terms;    // FP8 latents: [T] query terms (mla_q.cuh)
   const int32_t* q_exps;     // NVFP4 latents: [T, 96] exponents of the fp16 query's scales
   int max_ctas;              // G = min(max_ctas, W)
@@ -33,41 +48,55 @@ struct TreeMlaParams {
 struct Segment {
   int t, j0, j1;
   int slot;   // partial slot, or -1 when the segment is the whole token
+  TreeToken tok;
 };
 
 // A CTA's segments in order.  Every role of the CTA walks its own copy.
 struct SegmentWalk {
   const int64_t* starts;
-  int T, G, whole, cta;
+  const TreeToken* toks;
+  int T, whole, cta, G;
   int64_t g0, g, g1;    // share, and the next tile
+  int64_t u0, u1;       // tiles of token t
   int t;
+  TreeToken tok;
   __device__ bool next(Segment& s) {
     if (whole) {
       while (t < T) {
-        const int64_t u0 = __ldg(starts + t), u1 = __ldg(starts + t + 1);
-        const int tt = t;
+        u0 = __ldg(starts + t), u1 = __ldg(starts + t + 1);
+        s.t = t;
         t += G;
         if (u1 > u0) {
-          s = Segment{tt, 0, static_cast<int>(u1 - u0), -1};
+          s.j0 = 0;
+          s.j1 = static_cast<int>(u1 - u0);
+          s.slot = -1;
+          s.tok = load(s.t);
           return true;
         }
       }
       return false;
     }
     if (g >= g1) return false;
-    int64_t u0 = __ldg(starts + t), u1 = __ldg(starts + t + 1);
-    while (u1 <= g) {   // padding tokens hold no tiles
-      ++t;
-      u0 = u1;
-      u1 = __ldg(starts + t + 1);
+    if (u1 <= g) {
+      do {   // padding tokens hold no tiles
+        ++t;
+        u0 = u1;
+        u1 = __ldg(starts + t + 1);
+      } while (u1 <= g);
+      tok = load(t);
     }
     const int64_t e = u1 < g1 ? u1 : g1;
     s.t = t;
     s.j0 = static_cast<int>(g - u0);
     s.j1 = static_cast<int>(e - u0);
     s.slot = (g == u0 && e == u1) ? -1 : 2 * cta + (g == g0 ? 0 : 1);
+    s.tok = tok;
     g = e;
     return true;
+  }
+  __device__ TreeToken load(int i) const {
+    const int4 v = __ldg(reinterpret_cast<const int4*>(toks) + i);
+    return TreeToken{v.x, v.y, v.z, v.w};
   }
 };
 
@@ -77,10 +106,22 @@ __host__ __device__ inline int share_of(int64_t W, int G, int64_t u) {
   return static_cast<int>(((u + 1) * G - 1) / W);
 }
 
-// The list of tiles (starts), and the queries as `terms` (FP8 latents) or as `q16` and `exps`
+// The plan, and the queries as attention operands: `terms` (FP8 latents), or `q16` and `exps`
 // (NVFP4 latents; terms null).
-cudaError_t launch_tree_prep(const BatchView& b, const TreeView& tree, const __nv_bfloat16* q, uint8_t* terms,
-                             __half* q16, int32_t* exps, int64_t* starts, uint32_t* status, cudaStream_t st);
+struct TreePrepParams {
+  BatchView b;
+  TreeView tree;
+  const __nv_bfloat16* q;
+  uint8_t* terms;
+  __half* q16;
+  int32_t* exps;
+  int64_t* starts;
+  TreeToken* toks;
+  TreeShare* shares;
+  int max_ctas;
+  uint32_t* status;
+};
+cudaError_t launch_tree_prep(const TreePrepParams& p, cudaStream_t st);
 // FP8 latents: `lmap` boxes of 128 dims, `tmap` of the last 64 (both of up to 128 positions of a page).
 cudaError_t launch_tree_mla_fp8(const CUtensorMap& lmap, const CUtensorMap& tmap, const TreeMlaParams& p,
                                 cudaStream_t st);
