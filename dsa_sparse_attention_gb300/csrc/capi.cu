@@ -229,19 +229,20 @@ bool make_q_map(CUtensorMap* m, const void* q, int T) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The FP8 latents of every page, {576 dims, block slots, rows}: a box is `width` dims
-// (128 or 64, swizzled over as many bytes) of up to 128 positions of one page.
+// The latent records of every page, {record bytes, block slots, rows}: a box is `width` bytes
+// (128, 64 or 32, swizzled over as many) of up to 128 positions of one page.
 bool make_latent_map(CUtensorMap* m, const dsa_kv_layout* l, int width) {
   auto enc = encode_fn();
   if (!enc) return false;
-  cuuint64_t dims[3] = {kLatDim, cuuint64_t(l->block_size), cuuint64_t(l->num_rows)};
-  cuuint64_t strides[2] = {kLatDim, cuuint64_t(l->row_stride_bytes)};
+  const cuuint64_t rec = l->lat_fmt == DSA_LAT_FP8 ? kLatDim : 352;
+  cuuint64_t dims[3] = {rec, cuuint64_t(l->block_size), cuuint64_t(l->num_rows)};
+  cuuint64_t strides[2] = {rec, cuuint64_t(l->row_stride_bytes)};
   cuuint32_t box[3] = {cuuint32_t(width), cuuint32_t(l->block_size < kSelTile ? l->block_size : kSelTile), 1};
   cuuint32_t es[3] = {1, 1, 1};
   void* base = const_cast<uint8_t*>(static_cast<const uint8_t*>(l->pool)) + l->lat_page_offset;
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             width == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+             width == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : width == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // The FP8 attention's split partials [rows = T * nsplit * 512 dims][96 heads] fp16,
@@ -924,7 +925,8 @@ dsa_status dsa_tree_mla(const dsa_kv_layout* layout, const dsa_batch* batch, con
   p.q_terms = terms;
   p.q_exps = at<int32_t>(workspace, wl.q_exps);
   CUtensorMap amap, bmap;
-  if (fp8 ? !(make_latent_map(&amap, layout, 128) && make_latent_map(&bmap, layout, 64)) : !make_q_map(&amap, q16, T))
+  if (fp8 ? !(make_latent_map(&amap, layout, 128) && make_latent_map(&bmap, layout, 64))
+          : !(make_q_map(&amap, q16, T) && make_latent_map(&bmap, layout, 32)))
     return encode_fail();
   TreePrepParams pp;
   pp.b = p.b;
@@ -940,7 +942,7 @@ dsa_status dsa_tree_mla(const dsa_kv_layout* layout, const dsa_batch* batch, con
   pp.status = p.status;
   const cudaError_t e = launch_tree_prep(pp, stream);
   if (e != cudaSuccess) return cuda_fail(e);
-  return cuda_status(fp8 ? launch_tree_mla_fp8(amap, bmap, p, stream) : launch_tree_mla_nvfp4(amap, p, stream));
+  return cuda_status(fp8 ? launch_tree_mla_fp8(amap, bmap, p, stream) : launch_tree_mla_nvfp4(amap, bmap, p, stream));
 }
 
 dsa_status dsa_tree_topk(const dsa_kv_layout* layout, const dsa_batch* batch, const dsa_tree* tree,

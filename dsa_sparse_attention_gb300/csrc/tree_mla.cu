@@ -771,42 +771,61 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
 // The softmax is that of the FP8 kernel (tokens on lanes, a reference per head that rarely
 // moves, P handed over in three steps), with P in fp16.
 // A chunk is the A operand of both products (K-major, then MN-major).  Beside the query
-// (108 KB) and P (24 KB) five chunks fit, so of the nine that a tile's scores read, the
-// last four stay for the values and the first four are converted again: 13 fills a tile
-// through five fixed places, in the order of the table below.  Fill and use of a place
-// are ordered by one barrier per fill and one per group of MMAs, each once a tile.
-//   scores: chunk 8 in place 3, 0 in 0, 1 in 2, 2 in 1, 3 in 4, 4 in 0, 5 in 3, 6 in 1, 7 in 4
-//   values: dims 256..383 (chunks 4, 5), 384..511 (6, 7), 0..127 (0 in 0, 1 in 2), 128..255 (2 in 1, 3 in 4)
+// (108 KB), P (24 KB) and packed rows on their way (16 KB) four chunks fit, so of the
+// nine that a tile's scores read, the last four stay for the values and the first four
+// are converted again: 13 fills a tile through four fixed places, in the order of the
+// tables below.  Each fill, each group of MMAs that frees places and each copy of packed
+// rows has its own barrier, completed once a tile.
+// Warp 13 brings queries and packed rows (64 dims of 128 tokens, 4 KB, in four places) by
+// TMA, and prefetches pages into L2.
 // The 12 softmax warps convert, too: the four warps of group g (a row of the tile each
-// thread) take the chunks c with c % 3 = g and keep their packed rows in registers from
-// the first fill to the second; the next tile's rows are loaded as they are given up.
-// Warp 12 issues MMAs; warp 13 loads queries.
+// thread) make the fills f with f % 3 = g; their rows' scales they fetch a tile ahead,
+// into shared memory.  Warp 12 issues MMAs.
+// Bound by shared memory: the MMAs read 7 KB per 49 cycles (6.6K cycles a tile), the fills
+// write 16 KB each (1.7K), and packed rows and P add about 1K; a tile takes 12.2K, the
+// rest is the chain scores -> weights -> values, which four places cannot overlap fully.
+// 16 tokens over 256K: 1,319 us, 664 TFLOP/s.  Rows and scales loaded to registers by the
+// threads that convert them: 1,470 us (spilled a tile ahead of use, each spill waited).
 namespace t16 {
 constexpr int THREADS = 448;
 constexpr int QCHUNKS = kLatDim / 64;
 constexpr int QCHUNK = 96 * 128;
 constexpr int PLACE = 128 * 128;
+constexpr int RAW = 128 * 32;                     // packed rows of a chunk, 32-byte swizzle
+constexpr int RAWS = 4;
 constexpr int OFF_Q = 0;
-constexpr int OFF_C = QCHUNKS * QCHUNK;           // five places
-constexpr int OFF_P = OFF_C + 5 * PLACE;          // three [128 tokens x 32 heads] fp16 blocks, 64-byte swizzle
+constexpr int OFF_C = QCHUNKS * QCHUNK;           // four places
+constexpr int OFF_P = OFF_C + 4 * PLACE;          // three [128 tokens x 32 heads] fp16 blocks, 64-byte swizzle
 constexpr int P_BLOCK = 128 * 64;
-constexpr int OFF_QEXP = OFF_P + 3 * P_BLOCK;     // [96] int
+constexpr int OFF_RAW = OFF_P + 3 * P_BLOCK;
+constexpr int OFF_SCALE = OFF_RAW + RAWS * RAW;   // scale words of the rows: [2 tiles][3 chunks][384 threads]
+constexpr int OFF_QEXP = OFF_SCALE + 2 * 3 * 384 * 4;   // [96] int
 constexpr int OFF_REDM = OFF_QEXP + 96 * 4;       // [4][96] float
 constexpr int OFF_SH = OFF_REDM + 4 * 96 * 4;     // [96] float
 constexpr int OFF_ALPHA = OFF_SH + 96 * 4;        // [96] float
 constexpr int OFF_INV = OFF_ALPHA + 96 * 4;       // [96] float
 constexpr int OFF_BARS = OFF_INV + 96 * 4;
-constexpr int N_BARS = 32;
-constexpr int OFF_MISC = OFF_BARS + N_BARS * 8;
-constexpr int SMEM_BYTES = OFF_MISC + 64 + 1024;
 constexpr int FILLS = 13;
-// chunk and place of fill f: the scores' nine in their order, then the values' four
-__device__ constexpr int kChunk[FILLS] = {8, 0, 1, 2, 3, 4, 5, 6, 7, 1, 0, 2, 3};
-__device__ constexpr int kPlace[FILLS] = {3, 0, 2, 1, 4, 0, 3, 1, 4, 2, 0, 1, 4};
+constexpr int OFF_MISC = OFF_BARS + 64 * 8;
+constexpr int SMEM_BYTES = OFF_MISC + 64 + 1024;
+// chunk and place of fill f: the scores' nine, then the values' four.  Dim block v of the
+// values is the chunks 2 v and 2 v + 1, one or three places apart: 4 and 5 in places 1
+// and 2, 6 and 7 in 0 and 3 (kept), then 0 and 1 in 1 and 2, 2 and 3 in 0 and 3.
+// The fills f of group f % 3 touch three chunks: 0, 8, 3; 1, 4, 7; 2, 5, 6.
+__device__ constexpr int kChunk[FILLS] = {0, 1, 2, 8, 4, 5, 3, 7, 6, 0, 1, 2, 3};
+__device__ constexpr int kPlace[FILLS] = {1, 2, 3, 0, 1, 2, 0, 3, 0, 1, 2, 0, 3};
 // the same for a fill known at run time (4 bits each)
-__device__ __forceinline__ int place_of_fill(int f) { return static_cast<int>((0x4102413041203ull >> (4 * f)) & 15); }
-// events that free places: the scores of fill f (f < 5) done, or the values of dim block v done
-enum { EV_S8 = 0, EV_S0, EV_S1, EV_S2, EV_S3, EV_V0, EV_V1, EV_V2, EV_V3, EVENTS };
+__device__ __forceinline__ int chunk_of_fill(int f) { return static_cast<int>((0x3210673548210ull >> (4 * f)) & 15); }
+__device__ __forceinline__ int place_of_fill(int f) { return static_cast<int>((0x3021030210321ull >> (4 * f)) & 15); }
+// which of its group's three chunks a fill takes
+__device__ __forceinline__ int scale_of_fill(int f) { return f < 9 ? f / 3 : (f == 12 ? 2 : 0); }
+// events that free places: the scores of fill 0, 1, 2, 3 or 6 done, or the values of dim block v done
+enum { EV_S0 = 0, EV_S1, EV_S2, EV_S3, EV_S6, EV_V0, EV_V1, EV_V2, EV_V3, EVENTS };
+// the event that fill f waits for; bit 8: of the tile before
+__device__ __forceinline__ int event_of_fill(int f) {
+  return f < 2 ? (EV_V0 | 256) : f < 4 ? (EV_V1 | 256) : f < 6 ? EV_S0 + f - 4 : f == 6 ? EV_S3 : f == 7 ? EV_S2
+         : f == 8 ? EV_S6 : f < 11 ? EV_V2 : EV_V3;
+}
 constexpr int MATH_WARPS = 12;
 constexpr int MATH = MATH_WARPS * 32;
 constexpr int MMA_WARP = 12, LOAD_WARP = 13;
@@ -820,49 +839,32 @@ static_assert(OFF_SH % 16 == 0 && OFF_ALPHA % 16 == 0 && OFF_INV % 16 == 0 && OF
 static_assert(SMEM_BYTES <= 232448, "smem");
 }  // namespace t16
 
-// One row of a chunk: 64 packed values and their four scales.
-struct RawRow {
-  uint4 a, b;
-  uint32_t s;
-};
-__device__ __forceinline__ RawRow load_raw(const uint8_t* rec, int chunk) {
-  RawRow r;
-  r.a = r.b = make_uint4(0, 0, 0, 0);
-  r.s = 0;
-  if (rec) {
-    r.a = __ldg(reinterpret_cast<const uint4*>(rec + 32 * chunk));
-    r.b = __ldg(reinterpret_cast<const uint4*>(rec + 32 * chunk + 16));
-    r.s = __ldg(reinterpret_cast<const uint32_t*>(rec + 288 + 4 * chunk));
-  }
-  return r;
+// 4-byte global -> shared copy without registers (a register that holds a load for a whole
+// tile would be spilled, and the spill waits for the load: 1,600 cycles a tile).
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
-// The row as fp16 into row `row` of a place (128-byte swizzle).
-__device__ __forceinline__ void fill_row(uint8_t* place, int row, const RawRow& r) {
-  uint8_t* dst = place + (row >> 3) * 1024;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const uint4 w = q < 2 ? r.a : r.b;
-    uint32_t o[8];
-    nvfp4x16_to_f16(q & 1 ? make_uint2(w.z, w.w) : make_uint2(w.x, w.y), (r.s >> (8 * q)) & 0xFFu, o);
-    sts128(dst + sw128_off(row & 7, 2 * q), o);
-    sts128(dst + sw128_off(row & 7, 2 * q + 1), o + 4);
-  }
-}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but this thread's newest group are complete.
+__device__ __forceinline__ void cp_async_wait_but_one() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
 
 __global__ void __launch_bounds__(t16::THREADS, 1)
-    tree_mla_nvfp4_kernel(const __grid_constant__ CUtensorMap qmap, TreeMlaParams p) {
+    tree_mla_nvfp4_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap rmap,
+                          TreeMlaParams p) {
   using namespace t16;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024_tree(smem_raw);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BARS);
-  uint64_t* full = bars + 0;        // [FILLS]
-  uint64_t* event = bars + 13;      // [EVENTS]
-  uint64_t* q_full = bars + 22;
-  uint64_t* q_done = bars + 23;
-  uint64_t* s_full = bars + 24;
-  uint64_t* o_done = bars + 25;
-  uint64_t* drain = bars + 26;
-  uint64_t* p_full = bars + 27;     // [3]
+  uint64_t* full = bars + 0;        // [FILLS] a chunk is in its place
+  uint64_t* raw_full = bars + 13;   // [FILLS] its packed rows are in shared memory
+  uint64_t* raw_done = bars + 26;   // [FILLS] and have been read
+  uint64_t* event = bars + 39;      // [EVENTS]
+  uint64_t* q_full = bars + 48;
+  uint64_t* q_done = bars + 49;
+  uint64_t* s_full = bars + 50;
+  uint64_t* o_done = bars + 51;
+  uint64_t* drain = bars + 52;
+  uint64_t* p_full = bars + 53;     // [3]
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
   int* abortf = reinterpret_cast<int*>(smem + OFF_MISC + 8);
   float* red = reinterpret_cast<float*>(smem + OFF_REDM);
@@ -872,12 +874,17 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < FILLS; ++i) mbar_init(&full[i], 4);
-    for (int i = 13; i < 27; ++i) mbar_init(&bars[i], 1);
+    for (int i = 0; i < FILLS; ++i) {
+      mbar_init(&full[i], 4);
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_done[i], 4);
+    }
+    for (int i = 39; i < 53; ++i) mbar_init(&bars[i], 1);
     for (int i = 0; i < 3; ++i) mbar_init(&p_full[i], MATH_WARPS);
     *abortf = 0;
     fence_mbar_init();
     prefetch_tensormap(&qmap);
+    prefetch_tensormap(&rmap);
   }
   if (warp == 0) tmem_alloc(tslot, 512);
   grid_dep_wait();   // the plan and the query
@@ -891,21 +898,70 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
   Segment s;
 
   if (warp == LOAD_WARP) {
-    // ------------------------------------------------------------- queries
+    // ------------------------------------------- queries, packed rows, L2 prefetch
+    const int lg = p.pool.log2_bs;
+    const int box = min(p.pool.bs, kSelTile);     // positions of one copy
+    const int nbox = kSelTile / box;              // copies (lanes) per chunk
     bool ok = true;
-    int q_issued = -1;
+    int it = 0, q_issued = -1, f = 0;
     for (int seg = 0; ok && walk.next(s); ++seg) {
+      const int pos = s.tok.pos;
+      const int32_t* btrow = p.b.bt + static_cast<int64_t>(s.tok.req) * p.b.bt_stride;
+      // this lane's page of tile j: pool row (num_rows, which reads as zeros, for a bad id)
+      auto page = [&](int j) {
+        const int s0 = j * kSelTile + lane * box;
+        if (lane >= nbox || s0 > pos) return -1;
+        const int32_t id = __ldg(btrow + (s0 >> lg));
+        if (id >= 0 && id < p.pool.num_rows) return static_cast<int>(id);
+        atomicOr(p.status, DEV_BAD_BLOCK);
+        return static_cast<int>(p.pool.num_rows);
+      };
+      auto prefetch = [&](int j, int row) {   // the page's latents of tile j into L2
+        if (row >= 0 && row < p.pool.num_rows)
+          bulk_prefetch_l2(p.pool.pool + static_cast<int64_t>(row) * p.pool.row_stride + p.pool.lat_off +
+                               static_cast<int64_t>((j * kSelTile + lane * box) & (p.pool.bs - 1)) * 352,
+                           box * 352);
+      };
+      int row = page(s.j0);
+      prefetch(s.j0, row);
       if (seg > 0) ok = warp_wait(q_done, (seg - 1) & 1, ab, ok);
       if (!ok) break;
       q_issued = seg & 1;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(q_full, QCHUNKS * QCHUNK + kMlaHeads * 4);
-        for (int kc = 0; kc < QCHUNKS; ++kc)
-          tma_load_2d(smem + OFF_Q + kc * QCHUNK, &qmap, q_full, kc * 64, s.t * kMlaHeads);
+      if (lane == 0) mbar_arrive_expect_tx(q_full, QCHUNKS * QCHUNK + kMlaHeads * 4);
+      __syncwarp();
+      if (lane < QCHUNKS) tma_load_2d(smem + OFF_Q + lane * QCHUNK, &qmap, q_full, lane * 64, s.t * kMlaHeads);
+      else if (lane == QCHUNKS)
         bulk_load(smem + OFF_QEXP, p.q_exps + static_cast<int64_t>(s.t) * kMlaHeads, kMlaHeads * 4, q_full);
+      for (int j = s.j0; ok && j < s.j1; ++j, ++it) {
+        const int c1 = (j * kSelTile + lane * box) & (p.pool.bs - 1);
+        const int n = __popc(__ballot_sync(0xffffffffu, row >= 0));
+        const int next = j + 1 < s.j1 ? page(j + 1) : -1;
+        prefetch(j + 1, next);
+#pragma unroll 1
+        for (f = 0; f < FILLS; ++f) {
+          // the place of copy 13 it + f was last used four copies before
+          const int u = f < RAWS ? f + FILLS - RAWS : f - RAWS;
+          if (it > 0 || f >= RAWS) ok = warp_wait(&raw_done[u], (f < RAWS ? it - 1 : it) & 1, ab, ok);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&raw_full[f], n * box * 32);
+          __syncwarp();
+          const int place = (FILLS * it + f) % RAWS;
+          if (row >= 0)
+            tma_load_3d(smem + OFF_RAW + place * RAW + lane * box * 32, &rmap, &raw_full[f], 32 * chunk_of_fill(f), c1, row);
+        }
+        if (!ok) break;
+        row = next;
       }
     }
-    if (!ok && q_issued >= 0 && lane == 0) drain_wait(q_full, q_issued);
+    // after a failed wait: no copy into shared memory outlives the CTA (a barrier whose copy
+    // was not issued in this round keeps its earlier phase; the wait is bounded)
+    if (!ok && lane == 0) {
+      if (q_issued >= 0) drain_wait(q_full, q_issued);
+      for (int i = 0; i < RAWS && i < FILLS * it + f; ++i) {   // the last copies issued
+        const int n = FILLS * it + f - 1 - i;
+        drain_wait(&raw_full[n % FILLS], (n / FILLS) & 1);
+      }
+    }
   } else if (warp == MMA_WARP) {
     // ------------------------------------------------------------ MMA issuer
     const bool leader = elect_one();
@@ -914,13 +970,12 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
     const uint64_t dq = make_sdesc_sw128(smem_u32(smem + OFF_Q), 16, 1024);   // query, K-major
     const uint64_t dc = make_sdesc_sw128(smem_u32(smem + OFF_C), 16, 1024);   // chunks, K-major (scores)
     // Values: step i takes the tokens 8 i .. 8 i + 7 of every lane quarter (rows 32 apart), two
-    // quarters an MMA; the second 64 dims of a block lie 2 or 3 places behind the first.
-    const uint64_t dv2 = make_sdesc_sw128(smem_u32(smem + OFF_C), 2 * PLACE, 4096);
-    const uint64_t dv3 = make_sdesc_sw128(smem_u32(smem + OFF_C), 3 * PLACE, 4096);
+    // quarters an MMA; the second 64 dims of a block lie 1 or 3 places behind the first.
+    const uint64_t dv1 = make_sdesc_sw128(smem_u32(smem + OFF_C + PLACE), PLACE, 4096);   // places 1 and 2
+    const uint64_t dv3 = make_sdesc_sw128(smem_u32(smem + OFF_C), 3 * PLACE, 4096);       // places 0 and 3
     const uint64_t dp = make_sdesc_sw64(smem_u32(smem + OFF_P), P_BLOCK, 2048);
     auto values = [&](int v, int i, uint32_t acc) {
-      // first place of dim block v: 0 and 1 hold chunks (0, 1) in 0 and 2, (2, 3) in 1 and 4; 2 and 3 the kept ones
-      const uint64_t a = (v == 0 ? dv2 : dv3) + (((v & 1) * PLACE + i * 1024) >> 4);
+      const uint64_t a = (v & 1 ? dv3 : dv1) + ((i * 1024) >> 4);
       const uint64_t b = dp + ((512 * i) >> 4);
       const uint32_t d = tmem + O_COL + 96 * v;
       mma_f16(d, a, b, idesc_pv, acc);
@@ -942,7 +997,7 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
               for (int kk = 2 * half; kk < 2 * half + 2; ++kk)
                 mma_f16(tmem + S_COL, dc + ((kPlace[f] * PLACE + 32 * kk) >> 4), dq + ((kChunk[f] * QCHUNK + 32 * kk) >> 4),
                         idesc_qk, (f | kk) ? 1u : 0u);
-              if (half == 1 && f < 5) tc_commit(&event[EV_S8 + f]);
+              if (half == 1 && (f < 4 || f == 6)) tc_commit(&event[f < 4 ? EV_S0 + f : EV_S6]);
             }
             __syncwarp();
             if (half == 0 && f < 8) {   // the next chunk is awaited while the tensor core has work
@@ -1016,18 +1071,31 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
     const int lg = p.pool.log2_bs, bsm = p.pool.bs - 1;
     bool ok = true;
     int it = 0;
-    // This group's chunks in the order of their fills, and what frees the places (an event of
-    // this tile, or, bit 8, of the one before): chunk, fill, event.
-    const int chunk0 = g == 2 ? 8 : g, chunk1 = g == 2 ? 2 : g + 3, chunk2 = g == 2 ? 5 : g + 6;
-    const int fill0 = g == 2 ? 0 : g + 1;                       // then + 3, + 6
-    const int ev0 = (g == 2 ? EV_V2 : EV_V0) | 256, ev1 = g == 1 ? EV_S0 : (EV_V1 | 256),
-              ev2 = g == 0 ? EV_S2 : (g == 1 ? EV_S3 : EV_S8);
-    // Fills a place with a row once it is free (on the CTA's first tile all of them are).
-    auto fill = [&](int f, const RawRow& r, int ev) {
-      const uint32_t par = (it & 1) ^ (ev >> 8);
-      if (it > 0 || ev < 256) ok = warp_wait(&event[ev & 255], par, ab, ok);
+    // Fill f: the row's 32 packed bytes -> 64 fp16 values in registers, then, once the place is
+    // free (on the CTA's first tile the first ones are), into it.  A row nobody sees is zeros.
+    uint32_t* scales = reinterpret_cast<uint32_t*>(smem + OFF_SCALE) + threadIdx.x;
+    auto fill = [&](int f, bool seen_row) {
+      ok = warp_wait(&raw_full[f], it & 1, ab, ok);
+      const uint8_t* src = smem + OFF_RAW + (FILLS * it + f) % RAWS * RAW + crow * 32;
+      const int sw = ((crow >> 2) & 1) << 4;
+      const uint4 w0 = *reinterpret_cast<const uint4*>(src + sw), w1 = *reinterpret_cast<const uint4*>(src + (sw ^ 16));
+      __syncwarp();
+      if (ok && lane == 0) mbar_arrive(&raw_done[f]);
+      const uint32_t sw4 = seen_row ? scales[((it & 1) * 3 + scale_of_fill(f)) * 384] : 0u;
+      uint32_t o[4][8];
+      nvfp4x16_to_f16(make_uint2(w0.x, w0.y), sw4 & 0xFFu, o[0]);
+      nvfp4x16_to_f16(make_uint2(w0.z, w0.w), (sw4 >> 8) & 0xFFu, o[1]);
+      nvfp4x16_to_f16(make_uint2(w1.x, w1.y), (sw4 >> 16) & 0xFFu, o[2]);
+      nvfp4x16_to_f16(make_uint2(w1.z, w1.w), sw4 >> 24, o[3]);
+      const int ev = event_of_fill(f);
+      if (it > 0 || ev < 256) ok = warp_wait(&event[ev & 255], (it & 1) ^ (ev >> 8), ab, ok);
       if (ok) {
-        fill_row(smem + OFF_C + place_of_fill(f) * PLACE, crow, r);
+        uint8_t* dst = smem + OFF_C + place_of_fill(f) * PLACE + (crow >> 3) * 1024;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          sts128(dst + sw128_off(crow & 7, 2 * q), o[q]);
+          sts128(dst + sw128_off(crow & 7, 2 * q + 1), o[q] + 4);
+        }
         fence_proxy_async_smem();
       }
       __syncwarp();
@@ -1038,30 +1106,30 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
       const uint32_t* mrow = p.tree.mask + static_cast<int64_t>(s.t) * p.tree.words;
       const int32_t* btrow = p.b.bt + static_cast<int64_t>(req) * p.b.bt_stride;
       const int plain = min(base, pos + 1);   // positions below are all seen
-      // The pool row of this thread's position in tile j (-1 where nobody sees it) is read three
-      // tiles ahead; its record is prefetched into L2 two ahead (128 bytes by each group's
-      // thread) and read one ahead.
+      // The record of this thread's position in tile j, null where nobody sees it or the block id
+      // is bad (the loads report that); ids are read two tiles ahead, scales one.
       auto block = [&](int j) {
         const int sv = j * kSelTile + crow;
         if (j >= s.j1 || !(sv < plain || (sv <= pos && tree_sees(mrow, p.tree.words, base, sv)))) return -1;
-        const int32_t id = __ldg(btrow + (sv >> lg));
-        return id == -1 ? -2 : id;   // (an id of -1 in the table is out of range, too)
+        return static_cast<int>(__ldg(btrow + (sv >> lg)));
       };
       auto record = [&](int j, int id) -> const uint8_t* {
-        if (id == -1) return nullptr;
-        if (id < 0 || id >= p.pool.num_rows) {
-          atomicOr(p.status, DEV_BAD_BLOCK);
-          return nullptr;
+        if (id < 0 || id >= p.pool.num_rows) return nullptr;
+        return p.pool.pool + static_cast<int64_t>(id) * p.pool.row_stride + p.pool.lat_off +
+               static_cast<int64_t>((j * kSelTile + crow) & bsm) * 352;
+      };
+      // the scale words of the group's chunks for the CTA's tile `n`, on their way to shared memory
+      auto fetch_scales = [&](const uint8_t* r, int n) {
+        if (r) {
+#pragma unroll
+          for (int k = 0; k < 3; ++k)
+            cp_async4(smem_u32(scales + ((n & 1) * 3 + k) * 384), r + 288 + 4 * chunk_of_fill(g + 3 * k));
         }
-        const uint8_t* r = p.pool.pool + static_cast<int64_t>(id) * p.pool.row_stride + p.pool.lat_off +
-                           static_cast<int64_t>((j * kSelTile + crow) & bsm) * 352;
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(r + 128 * g));
-        return r;
+        cp_async_commit();
       };
       const uint8_t* rec = record(s.j0, block(s.j0));
-      const uint8_t* next = record(s.j0 + 1, block(s.j0 + 1));
-      int id2 = block(s.j0 + 2);
-      RawRow x0 = load_raw(rec, chunk0), x1 = load_raw(rec, chunk1), x2 = load_raw(rec, chunk2);
+      int id1 = block(s.j0 + 1);
+      fetch_scales(rec, it);
       ok = warp_wait(q_full, seg & 1, ab, ok);
       float2 c2[4], sh2[4], l2[4];            // per head pair b: logit scale (log2 units), SHIFT - reference, sum
 #pragma unroll
@@ -1074,15 +1142,14 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
       }
       float m_ref = -INFINITY;                // quarter 0: reference of column 32 g + lane
       for (int j = s.j0; j < s.j1; ++j, ++it) {
-        const uint8_t* after = record(j + 2, id2);
-        id2 = block(j + 3);
-        // ---- the scores' chunks; what is not needed again gives way to the next tile's rows
-        fill(fill0, x0, ev0);
-        fill(fill0 + 3, x1, ev1);
-        fill(fill0 + 6, x2, ev2);
-        x2 = load_raw(next, chunk2);
-        if (g == 1) x1 = load_raw(next, chunk1);
-        if (g == 2) x0 = load_raw(next, chunk0);
+        const uint8_t* next = record(j + 1, id1);
+        id1 = block(j + 2);
+        fetch_scales(next, it + 1);
+        cp_async_wait_but_one();
+        const bool seen_row = rec != nullptr;
+        // ---- the scores' chunks
+#pragma unroll 1
+        for (int f = g; f < 9; f += 3) fill(f, seen_row);
         // ---- softmax (as in the FP8 kernel)
         ok = warp_wait(s_full, it & 1, ab, ok);
         tc_fence_after();
@@ -1213,15 +1280,10 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
             if (ok && lane == 0) mbar_arrive(&p_full[i < 2 ? i : 2]);
           }
         }
-        // ---- the values' chunks that did not stay, as the places come free: 0, 1, 2, then 3
-        fill(g == 0 ? 10 : (g == 1 ? 9 : 11), g == 2 ? x1 : x0, g == 0 ? EV_V2 : (g == 1 ? EV_S1 : EV_V3));
-        if (g == 2) x1 = load_raw(next, chunk1);
-        else x0 = load_raw(next, chunk0);
-        if (g == 0) {
-          fill(12, x1, EV_V3);
-          x1 = load_raw(next, chunk1);
-        }
-        next = after;
+        // ---- the values' chunks that did not stay, as the places come free
+#pragma unroll 1
+        for (int f = 9 + g; f < FILLS; f += 3) fill(f, seen_row);
+        rec = next;
       }
       // ---- the segment's result: sums over the tokens, then TMEM (thread = dim) -> global
 #pragma unroll
@@ -1335,11 +1397,12 @@ cudaError_t launch_tree_mla_fp8(const CUtensorMap& lmap, const CUtensorMap& tmap
   return e != cudaSuccess ? e : launch_combine(p, st);
 }
 
-cudaError_t launch_tree_mla_nvfp4(const CUtensorMap& qmap, const TreeMlaParams& p, cudaStream_t st) {
+cudaError_t launch_tree_mla_nvfp4(const CUtensorMap& qmap, const CUtensorMap& rmap, const TreeMlaParams& p,
+                                  cudaStream_t st) {
   cudaError_t e = set_func_attr_once(reinterpret_cast<const void*>(tree_mla_nvfp4_kernel),
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, t16::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  e = launch_ex(tree_mla_nvfp4_kernel, dim3(p.max_ctas), dim3(t16::THREADS), t16::SMEM_BYTES, st, true, 0u, qmap, p);
+  e = launch_ex(tree_mla_nvfp4_kernel, dim3(p.max_ctas), dim3(t16::THREADS), t16::SMEM_BYTES, st, true, 0u, qmap, rmap, p);
   return e != cudaSuccess ? e : launch_combine(p, st);
 }
 

@@ -125,7 +125,8 @@ cudaError_t launch_tree_prep(const TreePrepParams& p, cudaStream_t st);
 // FP8 latents: `lmap` boxes of 128 dims, `tmap` of the last 64 (both of up to 128 positions of a page).
 cudaError_t launch_tree_mla_fp8(const CUtensorMap& lmap, const CUtensorMap& tmap, const TreeMlaParams& p,
                                 cudaStream_t st);
-// NVFP4 latents; `qmap` over the fp16 queries.
-cudaError_t launch_tree_mla_nvfp4(const CUtensorMap& qmap, const TreeMlaParams& p, cudaStream_t st);
+// NVFP4 latents; `qmap` over the fp16 queries, `rmap` boxes of 32 packed bytes.
+cudaError_t launch_tree_mla_nvfp4(const CUtensorMap& qmap, const CUtensorMap& rmap, const TreeMlaParams& p,
+                                  cudaStream_t st);
 
 }  // namespace dsa
