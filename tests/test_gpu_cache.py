@@ -230,3 +230,42 @@ def test_cache_calls_in_a_graph():
         assert list(zip(src.cpu().tolist(), dst.cpu().tolist())) == pairs
         for s, t in pairs:
             assert torch.equal(d.pool[s], d.pool[t])
+
+
+@pytest.mark.parametrize("alias", [False, True])
+def test_compact_in_a_cluster(alias):
+    # more rows than one CTA plans, and tables that take a launch of their own
+    bs, rows = 16, 20011
+    d = Dev(rows, [rows // 3 * bs, 100, 0, rows // 4 * bs + 5, 0], bs=bs, seed=31, stride=20000, extra=500)
+    d.fork([3], [4])
+    d.free([1])
+    _compact(d, alias)
+    d.check()
+    _compact(d, alias)
+    d.check()
+
+
+def test_cache_calls_behind_a_memset_in_a_graph():
+    # what a memset or a copy writes in front of a call in the same graph is seen by it
+    dsa = __import__("dsa_sparse_attention_gb300")
+    d = Dev(300, [1000, 777] + [0] * 2, seed=32)
+    cu = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
+    parent, child = cu([0, 1]), cu([2, 3])
+    table, ref, ctx = d.table.clone(), d.ref.clone(), d.ctx.clone()
+    src, dst = torch.empty((2, 2), dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for x, y in ((d.table, table), (d.ref, ref), (d.ctx, ctx)):
+            x.zero_()
+            x.copy_(y)
+        dsa.dsa_cache_fork(d.layout, d.pages, parent, child, src, dst, ws=d.ws)
+        dsa.dsa_cache_copy(d.layout, src, dst, ws=d.ws)
+    pairs, _ = d.plain.fork([0, 1], [2, 3])
+    for _ in range(5):
+        d.table.fill_(-1)
+        g.replay()
+        d.check()
+        assert list(zip(src.cpu().tolist(), dst.cpu().tolist())) == pairs
+    for s, t in pairs:
+        assert torch.equal(d.pool[s], d.pool[t])

@@ -234,6 +234,131 @@ def test_mla_bad_inputs_are_recorded(fmt):
     check_mla(case, out, lse, [1, 2, 3, 4])
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+def test_mla_more_tokens_than_the_plan_holds_at_once(fmt):
+    # 1,500 tokens, padding among them and at both ends: the plan takes them 1,024 at a time
+    case = make_case([130, 7, 390], [700, 60, 740], seed=81, lat_fmt=fmt, block_size=16)
+    d = DeviceTree(case)
+    pad = [0, 1, 1023, 1024, 1025, 1200, 1498, 1499]
+    for t in pad:
+        d.q_req[t] = -1
+    out, lse = d.mla()
+    torch.cuda.synchronize()
+    assert _check(d.ws) == 0
+    assert (out[pad] == 7.0).all() and (lse[pad] == 7.0).all()
+    check_mla(case, out, lse, [t for t in [2, 500, 699, 700, 759, 760, 1022, 1026, 1199, 1201, 1497]])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("scale", [0.0, -0.03])
+def test_mla_scales(fmt, scale):
+    # a scale of zero gives the mean of the values; a negative one turns the order around
+    case = make_case([40, 500], [3, 2], seed=82, lat_fmt=fmt)
+    case.wl.sm_scale = scale
+    d = DeviceTree(case)
+    out, lse = d.mla()
+    torch.cuda.synchronize()
+    assert _check(d.ws) == 0
+    check_mla(case, out, lse)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_mla_far_apart_logits(fmt):
+    # logits hundreds apart: a few positions take it all, and the others' weights are zeros, not NaN
+    case = make_case([300, 900], [4, 3], seed=83, lat_fmt=fmt)
+    case.wl.sm_scale *= 64.0
+    d = DeviceTree(case)
+    out, lse = d.mla()
+    torch.cuda.synchronize()
+    assert _check(d.ws) == 0
+    check_mla(case, out, lse)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_calls_behind_a_memset_in_a_graph(fmt):
+    # the first kernel of each call may be scheduled early: what a memset or a copy in front of it in the
+    # same graph writes has to be seen all the same
+    import dsa_sparse_attention_gb300 as dsa
+    case = make_case([300, 900], [4, 3], seed=84, lat_fmt=fmt)
+    d = DeviceTree(case)
+    T, k, ld = 7, 64, 904
+    q, base, q_req = d.q.clone(), d.base.clone(), d.q_req.clone()
+    scores = torch.from_numpy(np.random.default_rng(3).standard_normal((T, ld)).astype(np.float32)).cuda()
+    sc = scores.clone()
+    idx = torch.empty((T, k), dtype=torch.int32, device="cuda")
+    ws = dsa.alloc_workspace(d.layout, d.batch, k)
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        d.q.zero_()
+        d.q_req.zero_()
+        d.q_req.copy_(q_req)
+        d.q.copy_(q)
+        d.mla(stream=torch.cuda.current_stream())
+        d.q.zero_()                              # only after the attention has read it
+        sc.zero_()
+        sc.copy_(scores)
+        dsa.dsa_tree_topk(d.layout, d.batch, d.tree, sc, ld, k, idx, ws=ws)
+        sc.zero_()
+    for _ in range(5):
+        d.q.fill_(1.0)
+        idx.fill_(-7)
+        g.replay()
+    torch.cuda.synchronize()
+    assert _check(d.ws) == 0 and _check(ws) == 0
+    check_mla(case, d.out, d.lse)
+    _check_topk(case, scores.cpu().numpy(), k, idx.cpu().numpy())
+
+
+def test_mla_two_streams_at_once():
+    # two batches on two streams, each with its workspace, many calls in flight: each gives the bits it
+    # gives alone
+    cases = [make_case([1500, 40], [6, 9], seed=85), make_case([700, 90, 5], [8, 2, 4], seed=86, lat_fmt=W.LAT_NVFP4)]
+    devs = [DeviceTree(c) for c in cases]
+    alone = []
+    for d in devs:
+        d.mla()
+        torch.cuda.synchronize()
+        alone.append((d.out.clone(), d.lse.clone()))
+        d.out.fill_(7.0)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for d, s in zip(devs, streams):
+            d.mla(stream=s)
+    torch.cuda.synchronize()
+    for d, (out, lse) in zip(devs, alone):
+        assert _check(d.ws) == 0
+        assert torch.equal(d.out, out) and torch.equal(d.lse, lse)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_mla_and_commit_past_32_bits(fmt):
+    # the same rows of a pool, moved past 6 GB: the same bits, and the commit moves the same records
+    import dsa_sparse_attention_gb300 as dsa
+    case = make_case([300, 900], [4, 3], seed=87, lat_fmt=fmt)
+    wl = case.wl
+    near = DeviceTree(case)
+    out, lse = (x.clone() for x in near.mla())
+    acc = torch.tensor([[1, 3, -1], [0, 2, -1]], dtype=torch.int32, device="cuda")
+    new = torch.zeros(2, dtype=torch.int32, device="cuda")
+    dsa.dsa_tree_commit(near.layout, near.batch, near.base, acc, new, ws=near.ws)
+    far = DeviceTree(case)
+    shift = 6 * 2 ** 30 // wl.row_stride + 1
+    far.pool = torch.empty((shift + wl.num_rows) * wl.row_stride, dtype=torch.uint8, device="cuda")
+    far.pool[shift * wl.row_stride:] = torch.from_numpy(wl.pool.reshape(-1)).cuda()
+    far.bt = torch.where(far.bt >= 0, far.bt + shift, far.bt)
+    far.layout = dsa.make_layout(far.pool, shift + wl.num_rows, wl.row_stride, wl.idx_page_offset, wl.lat_page_offset,
+                                 wl.block_size, wl.idx_fmt, wl.lat_fmt)
+    far.batch = dsa.make_batch(far.q_req, far.q_pos, far.ctx, far.bt, wl.max_ctx_len)
+    far.mla()
+    dsa.dsa_tree_commit(far.layout, far.batch, far.base, acc, new, ws=far.ws)
+    torch.cuda.synchronize()
+    assert _check(near.ws) == 0 and _check(far.ws) == 0
+    assert torch.equal(far.out, out) and torch.equal(far.lse, lse)
+    assert torch.equal(far.pool[shift * wl.row_stride:], near.pool.reshape(-1))
+
+
 # ----------------------------------------------------------------------- top-k
 
 def _topk(case, scores, k, phys=False, max_ctx=None, pad=()):
@@ -359,6 +484,19 @@ def test_topk_empty_padding_and_mask_edges(max_ctx):
         scores = np.pad(scores, ((0, 0), (0, max_ctx - scores.shape[1])))
     idx, _ = _topk(case, scores, 2048, max_ctx=max_ctx, pad=(2, 70))
     _check_topk(case, scores, 2048, idx, skip=(2, 70))
+
+
+@pytest.mark.parametrize("base", [3000, 70000])
+def test_topk_infinities_and_signed_zeros(base):
+    # infinities are scores like any other; 0 and -0 are equal, so the lower position wins
+    case, scores = _topk_case([base], [4], 88)
+    rng = np.random.default_rng(88)
+    scores[0] = rng.choice(np.asarray([np.inf, -np.inf, 0.0, -0.0], np.float32), scores.shape[1])
+    scores[1] = -np.inf
+    scores[2] = np.where(rng.random(scores.shape[1]) < 0.5, np.float32(0.0), np.float32(-0.0))
+    scores[3, ::3] = np.inf
+    idx, _ = _topk(case, scores, 700)
+    _check_topk(case, scores, 700, idx)
 
 
 # ---------------------------------------------------------------------- commit

@@ -3,9 +3,10 @@ and the comparison of the dense attention with the oracle.
 
 Tolerance of the attention, from the roundings it makes (relative to the value a
 rounding is off by at most half a step: bf16 2^-8, 9 significant bits 2^-9, fp16 2^-11):
-a weight is rounded once, to 9 significant bits or more, and the sum is of the rounded
-weights, so the output moves by at most 2 * 2^-9 * A with A = sum p |v|; a partial is
-rounded to fp16 (2^-11 of it, and of A at most); the output to bf16.  Logits are sums of
+a weight is rounded once, to 9 significant bits or more, and the sum is of the weights
+before (or after) that rounding, so the output moves by at most 2 * 2^-9 * A with
+A = sum p |v|; a partial is rounded to fp16 (2^-11 of it, and of A at most); the output
+to bf16.  Logits are sums of
 576 exact products in fp32: their error e is at most 2^-18 * scale * sum |q c| (two bits
 for the order and the truncation of a tensor-core sum of 2^-24 terms over 576), a weight
 moves by e, the output by 2 e A.  The lse moves by 2^-9 + e.
@@ -92,8 +93,9 @@ def check_mla(case, out, lse, tokens=None):
             assert not out[t].any() and np.all(np.isneginf(lse[t])), f"token {t}: sees nothing"
             continue
         q = np.abs(O.decode_bf16(wl.q[t]).reshape(96, 576))
-        e = 2.0 ** -18 * wl.sm_scale * (q @ np.abs(lat).T).max(axis=1)
+        e = 2.0 ** -18 * abs(wl.sm_scale) * (q @ np.abs(lat).T).max(axis=1)
         tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -11 + 2 * e[:, None]) * (1 + 2.0 ** -7) * A
+        tol += 2.0 ** -25 + 2.0 ** -28 * np.abs(lat[:, :512]).sum(axis=0)
         use = (np.abs(out[t] - ref) / np.maximum(tol, 1e-30)).max()
         ul = (np.abs(lse[t] - ref_l) / (2.0 ** -9 + e + 1e-6 * np.abs(ref_l))).max()
         assert np.isfinite(out[t]).all() and use <= 1.0, f"token {t}: output {use:.3g} of the tolerance"
