@@ -184,29 +184,32 @@ __device__ __forceinline__ constexpr int head_of_column(int n) { return 8 * ((n 
 // A warp's part of a finished segment: its 32 heads (columns n0 ..) of the 32 dims of its lane
 // quarter, for the four dim blocks, as the output (bf16) or as the normalised partial (fp16:
 // 11 significant bits, above the output's 8), both [96][512].  A thread gets two columns of
-// a dim side by side, a transposing matrix store turns 8 x 8 of them into 8 dims (16 bytes)
-// of a head in the warp's `stage` (2 KB of P's place, free by now), and stores write 64
-// contiguous bytes of 8 heads.  One segment of one tile took 2.4 us with single 2-byte
-// stores and 5.5 us with exchanges between lanes.  `inv`: 1 / sum per column.
-__device__ __forceinline__ void store_segment(const TreeMlaParams& p, const Segment& s, uint32_t o_tmem,
-                                              const float* inv, int n0, int dim0, uint8_t* stage) {
+// a dim side by side; a transposing matrix store turns 8 x 8 of them into 8 dims (16 bytes)
+// of a head in the group's `stage` (8 KB of P's place, free by now: a dim block of the 32
+// heads of four warps), and every warp writes 8 heads, 256 contiguous bytes each.
+// `inv`: 1 / sum per column; `bar`: the group's named barrier.
+__device__ __forceinline__ void store_segment(const TreeMlaParams& p, const Segment& s, bool ok, uint32_t o_tmem,
+                                              const float* inv, int n0, int quarter, uint8_t* stage, int bar) {
   const int lane = threadIdx.x & 31;
   const bool fin = s.slot < 0;
   const int64_t row0 = (fin ? static_cast<int64_t>(s.t) : static_cast<int64_t>(s.slot)) * kMlaHeads + n0;
-  uint16_t* out = (fin ? reinterpret_cast<uint16_t*>(p.out) : reinterpret_cast<uint16_t*>(p.part_o)) + row0 * kVDim + dim0;
+  uint16_t* out = (fin ? reinterpret_cast<uint16_t*>(p.out) : reinterpret_cast<uint16_t*>(p.part_o)) + row0 * kVDim;
   float2 iv[4];
 #pragma unroll
   for (int b = 0; b < 4; ++b) iv[b] = *reinterpret_cast<const float2*>(inv + n0 + 8 * b + 2 * (lane & 3));
-  // The stage holds column c's 32 dims in 64 bytes, 16-byte piece k at k ^ (c / 2) % 4.
-  auto piece = [&](int c, int k) { return c * 64 + ((k ^ ((c >> 1) & 3)) << 4); };
+  // The stage holds column c's 128 dims in 256 bytes, 16-byte piece k at k ^ c % 8.
+  auto piece = [&](int c, int k) { return c * 256 + ((k ^ (c & 7)) << 4); };
 #pragma unroll 1
   for (int v = 0; v < 4; ++v) {
-    uint32_t rr[2][16];
-    DSA_TMEM_LD_16X256_X4(o_tmem + 96 * v + n0, rr[0]);
-    DSA_TMEM_LD_16X256_X4(o_tmem + 96 * v + n0 + (16u << 16), rr[1]);
-    tmem_wait_ld();
+    uint32_t rr[2][16] = {};
+    if (ok) {
+      DSA_TMEM_LD_16X256_X4(o_tmem + 96 * v + n0, rr[0]);
+      DSA_TMEM_LD_16X256_X4(o_tmem + 96 * v + n0 + (16u << 16), rr[1]);
+      tmem_wait_ld();
+    }
+    if (v > 0) named_bar_sync(bar, 128);   // the block before has left the stage
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
+    for (int hh = 0; hh < 2 && ok; ++hh) {
       uint32_t w[4][2];   // columns 8 b + 2 a, + 1; dims 16 hh + lane / 4, + 8
 #pragma unroll
       for (int b = 0; b < 4; ++b)
@@ -224,17 +227,19 @@ __device__ __forceinline__ void store_segment(const TreeMlaParams& p, const Segm
 #pragma unroll
       for (int b = 0; b < 4; b += 2) {
         const int c = 8 * (b + (lane >> 4)) + (lane & 7);
-        stmatrix_x4_trans(smem_u32(stage) + piece(c, 2 * hh + ((lane >> 3) & 1)), w[b][0], w[b][1], w[b + 1][0], w[b + 1][1]);
+        stmatrix_x4_trans(smem_u32(stage) + piece(c, 4 * quarter + 2 * hh + ((lane >> 3) & 1)), w[b][0], w[b][1],
+                          w[b + 1][0], w[b + 1][1]);
       }
     }
-    __syncwarp();
+    named_bar_sync(bar, 128);
+    if (ok) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int c = 8 * k + (lane >> 2);
-      const uint4 x = *reinterpret_cast<const uint4*>(stage + piece(c, lane & 3));
-      *reinterpret_cast<uint4*>(out + head_of_column(c) * kVDim + 128 * v + 8 * (lane & 3)) = x;
+      for (int k = 0; k < 4; ++k) {
+        const int c = 8 * quarter + 2 * k + (lane >> 4);
+        const uint4 x = *reinterpret_cast<const uint4*>(stage + piece(c, lane & 15));
+        *reinterpret_cast<uint4*>(out + head_of_column(c) * kVDim + 128 * v + 8 * (lane & 15)) = x;
+      }
     }
-    __syncwarp();
   }
 }
 
@@ -280,6 +285,9 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 // Shared memory holds the query terms (108 KB), one tile (72 KB: four 16 KB slices of
 // 128 dims and an 8 KB slice of the last 64) and P (36 KB).  A slice is refilled as soon
 // as the PV block that reads it is done, with the next tile prefetched into L2 meanwhile.
+// 8 x 6 tokens over 64K: 615 to 627 us, 1.06 PFLOP/s, with the SM clock held at about 1,950 MHz by
+// the power limit.  The 84 MMAs of a tile take 4.1K of its 7.4K cycles; the rest is what of
+// the softmax and the slices' refill no second S (TMEM) or tile (shared memory) can hide.
 // Roles: warps 0..11 run the softmax and the epilogue (lane quarter w % 4, heads
 // 32 (w / 4) ..); warp 12 issues MMAs; warp 13 loads.
 namespace t8 {
@@ -751,7 +759,7 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
       named_bar_sync(2, MATH);
       ok = warp_wait(o_done, seg & 1, ab, ok);
       tc_fence_after();
-      if (ok) store_segment(p, s, tmem + O_COL + lane_off, inv_sh, 32 * g, 32 * quarter, smem + OFF_P + warp * 2048);
+      store_segment(p, s, ok, tmem + O_COL + lane_off, inv_sh, 32 * g, quarter, smem + OFF_P + g * 8192, 3 + g);
       tc_fence_before();
     }
   }
@@ -784,7 +792,7 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
 // Bound by shared memory: the MMAs read 7 KB per 49 cycles (6.6K cycles a tile), the fills
 // write 16 KB each (1.7K), and packed rows and P add about 1K; a tile takes 12.2K, the
 // rest is the chain scores -> weights -> values, which four places cannot overlap fully.
-// 16 tokens over 256K: 1,319 us, 664 TFLOP/s.  Rows and scales loaded to registers by the
+// 16 tokens over 256K: 1,300 us, 674 TFLOP/s.  Rows and scales loaded to registers by the
 // threads that convert them: 1,470 us (spilled a tile ahead of use, each spill waited).
 namespace t16 {
 constexpr int THREADS = 448;
@@ -897,6 +905,18 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
   const Abort ab{abortf, p.status};
   Segment s;
 
+  // Query operands of token t, by a whole warp: the CTA's first by the MMA warp, which has nothing
+  // else to do then, the others by the load warp (1,300 us instead of 1,320 for 16 tokens over
+  // 256K; the FP8 kernel, at the power cap, gains nothing from it).
+  auto load_query = [&](int t) {
+    if (lane == 0) mbar_arrive_expect_tx(q_full, QCHUNKS * QCHUNK + kMlaHeads * 4);
+    __syncwarp();
+    if (lane < QCHUNKS) tma_load_2d(smem + OFF_Q + lane * QCHUNK, &qmap, q_full, lane * 64, t * kMlaHeads);
+    else if (lane == QCHUNKS)
+      bulk_load(smem + OFF_QEXP, p.q_exps + static_cast<int64_t>(t) * kMlaHeads, kMlaHeads * 4, q_full);
+    __syncwarp();
+  };
+
   if (warp == LOAD_WARP) {
     // ------------------------------------------- queries, packed rows, L2 prefetch
     const int lg = p.pool.log2_bs;
@@ -926,12 +946,8 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
       prefetch(s.j0, row);
       if (seg > 0) ok = warp_wait(q_done, (seg - 1) & 1, ab, ok);
       if (!ok) break;
+      if (seg > 0) load_query(s.t);
       q_issued = seg & 1;
-      if (lane == 0) mbar_arrive_expect_tx(q_full, QCHUNKS * QCHUNK + kMlaHeads * 4);
-      __syncwarp();
-      if (lane < QCHUNKS) tma_load_2d(smem + OFF_Q + lane * QCHUNK, &qmap, q_full, lane * 64, s.t * kMlaHeads);
-      else if (lane == QCHUNKS)
-        bulk_load(smem + OFF_QEXP, p.q_exps + static_cast<int64_t>(s.t) * kMlaHeads, kMlaHeads * 4, q_full);
       for (int j = s.j0; ok && j < s.j1; ++j, ++it) {
         const int c1 = (j * kSelTile + lane * box) & (p.pool.bs - 1);
         const int n = __popc(__ballot_sync(0xffffffffu, row >= 0));
@@ -984,6 +1000,7 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
     bool ok = true;
     int it = 0;
     for (int seg = 0; ok && walk.next(s); ++seg) {
+      if (seg == 0) load_query(s.t);
       ok = warp_wait(q_full, seg & 1, ab, ok);
       for (int j = s.j0; ok && j < s.j1; ++j, ++it) {
         ok = warp_wait(&full[0], it & 1, ab, ok);
@@ -1312,7 +1329,7 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
       named_bar_sync(2, MATH);
       ok = warp_wait(o_done, seg & 1, ab, ok);
       tc_fence_after();
-      if (ok) store_segment(p, s, tmem + O_COL + lane_off, inv_sh, 32 * g, 32 * quarter, smem + OFF_P + warp * 2048);
+      store_segment(p, s, ok, tmem + O_COL + lane_off, inv_sh, 32 * g, quarter, smem + OFF_P + g * 8192, 3 + g);
       tc_fence_before();
     }
   }
