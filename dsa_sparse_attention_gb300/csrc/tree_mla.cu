@@ -120,6 +120,7 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(TreePrepParams 
     if (c < G) {
       s.g0 = share_begin(base, G, c);
       s.g1 = share_begin(base, G, c + 1);
+      s.period = static_cast<int32_t>(base / G);
       int lo = 0, hi = T;   // starts[lo] <= g0 < starts[hi]
       while (hi - lo > 1) {
         const int m = (lo + hi) >> 1;
@@ -150,6 +151,7 @@ __device__ __forceinline__ SegmentWalk make_walk(const TreeMlaParams& p) {
   w.G = p.max_ctas;
   w.g0 = w.g = w.g1 = w.u0 = w.u1 = 0;
   w.t = blockIdx.x;
+  w.period = 1;
   if (!p.whole) {
     const int4* r = reinterpret_cast<const int4*>(p.shares + blockIdx.x);
     const int4 a = __ldcg(r), b = __ldcg(r + 1), c = __ldcg(r + 2), d = __ldcg(r + 3);
@@ -161,6 +163,7 @@ __device__ __forceinline__ SegmentWalk make_walk(const TreeMlaParams& p) {
     w.u0 = i64(b.x, b.y);
     w.u1 = i64(b.z, b.w);
     w.t = c.x;
+    w.period = c.y;
     w.tok = TreeToken{d.x, d.y, d.z, d.w};
   }
   return w;
@@ -285,8 +288,8 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 // Shared memory holds the query terms (108 KB), one tile (72 KB: four 16 KB slices of
 // 128 dims and an 8 KB slice of the last 64) and P (36 KB).  A slice is refilled as soon
 // as the PV block that reads it is done, with the next tile prefetched into L2 meanwhile.
-// 8 x 6 tokens over 64K: 615 to 627 us, 1.06 PFLOP/s, with the SM clock held at about 1,950 MHz by
-// the power limit.  The 84 MMAs of a tile take 4.1K of its 7.4K cycles; the rest is what of
+// 8 x 6 tokens over 64K: 588 us, 1.12 PFLOP/s, with the SM clock held at about 1,950 MHz by
+// the power limit.  The 84 MMAs of a tile take 4.1K of its 6.7K cycles; the rest is what of
 // the softmax and the slices' refill no second S (TMEM) or tile (shared memory) can hide.
 // Roles: warps 0..11 run the softmax and the epilogue (lane quarter w % 4, heads
 // 32 (w / 4) ..); warp 12 issues MMAs; warp 13 loads.
@@ -402,8 +405,8 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
                                static_cast<int64_t>((j * kSelTile + lane * box) & (p.pool.bs - 1)) * kLatDim,
                            box * kLatDim);
       };
-      int row = page(s.j0);
-      prefetch(s.j0, row);
+      int row = page(s.tile(0));
+      prefetch(s.tile(0), row);
       if (seg > 0) ok = warp_wait(q_done, (seg - 1) & 1, ab, ok);
       if (!ok) break;
       q_issued = seg & 1;
@@ -412,10 +415,10 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
       __syncwarp();
       if (lane < kQChunks) bulk_load(smem + OFF_Q + lane * QCHUNK, src + lane * QCHUNK, QCHUNK, q_full);
       else if (lane == kQChunks) bulk_load(smem + OFF_QEXP, src + kQTermBytes, kMlaHeads * 4, q_full);
-      for (int j = s.j0; ok && j < s.j1; ++j, ++it) {
-        const int c1 = (j * kSelTile + lane * box) & (p.pool.bs - 1);
+      for (int i = 0; ok && i < s.n; ++i, ++it) {
+        const int c1 = (s.tile(i) * kSelTile + lane * box) & (p.pool.bs - 1);
         const int n = __popc(__ballot_sync(0xffffffffu, row >= 0));
-        const int next = j + 1 < s.j1 ? page(j + 1) : -1;
+        const int next = i + 1 < s.n ? page(s.tile(i + 1)) : -1;
         if (it > 0) ok = warp_wait(tail_empty, (it - 1) & 1, ab, ok);
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(tail_full, n * box * 64);
@@ -430,7 +433,7 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
           if (row >= 0) tma_load_3d(smem + OFF_LAT + k * SLICE + lane * box * 128, &lmap, &lat_full[k], 128 * k, c1, row);
         }
         row = next;
-        prefetch(j + 1, row);
+        if (i + 1 < s.n) prefetch(s.tile(i + 1), row);
       }
     }
     // after a failed wait: no copy into shared memory outlives the CTA (a barrier whose copy
@@ -464,7 +467,7 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
     int it = 0;
     for (int seg = 0; ok && walk.next(s); ++seg) {
       ok = warp_wait(q_full, seg & 1, ab, ok);
-      for (int j = s.j0; ok && j < s.j1; ++j, ++it) {
+      for (int i = 0; ok && i < s.n; ++i, ++it) {
         // A slice's arrival is awaited half-way through the MMAs of the one before it: the
         // tensor core still has those to do.
         if (!(ok = warp_wait(tail_full, it & 1, ab, ok))) break;
@@ -502,8 +505,8 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
         if (!ok) break;
         if (leader) tc_commit(s_full);
         __syncwarp();
-        const uint32_t acc = j > s.j0 ? 1u : 0u;
-        const bool last = j == s.j1 - 1;
+        const uint32_t acc = i > 0 ? 1u : 0u;
+        const bool last = i == s.n - 1;
         if (!(ok = warp_wait(&p_full[0], it & 1, ab, ok))) break;
         tc_fence_after();
         if (leader) {
@@ -575,7 +578,8 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
         l2[b] = make_float2(0.f, 0.f);
       }
       float m_ref = -INFINITY;                // quarter 0: reference of column 32 g + lane
-      for (int j = s.j0; j < s.j1; ++j, ++it) {
+      for (int n = 0; n < s.n; ++n, ++it) {
+        const int j = s.tile(n);
         ok = warp_wait(s_full, it & 1, ab, ok);
         tc_fence_after();
         // y[i][b]: logits in log2 units less the reference, plus SHIFT
@@ -611,7 +615,7 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
           }
           return mx;
         };
-        bool moves = j == s.j0;   // a segment's first tile sets the references
+        bool moves = n == 0;   // a segment's first tile sets the references
         if (moves) {
           tmem_wait_ld();
         } else {
@@ -663,7 +667,7 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
             l2[b].x *= av.x;
             l2[b].y *= av.y;
           }
-          if (j > s.j0 && ok) {
+          if (n > 0 && ok) {
 #pragma unroll 1
             for (int v = 0; v < 4; ++v) {          // this warp's heads in all dim blocks, 16 at a time
 #pragma unroll 1
@@ -792,7 +796,7 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
 // Bound by shared memory: the MMAs read 7 KB per 49 cycles (6.6K cycles a tile), the fills
 // write 16 KB each (1.7K), and packed rows and P add about 1K; a tile takes 12.2K, the
 // rest is the chain scores -> weights -> values, which four places cannot overlap fully.
-// 16 tokens over 256K: 1,300 us, 674 TFLOP/s.  Rows and scales loaded to registers by the
+// 16 tokens over 256K: 1,290 us, 679 TFLOP/s.  Rows and scales loaded to registers by the
 // threads that convert them: 1,470 us (spilled a tile ahead of use, each spill waited).
 namespace t16 {
 constexpr int THREADS = 448;
@@ -942,17 +946,17 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
                                static_cast<int64_t>((j * kSelTile + lane * box) & (p.pool.bs - 1)) * 352,
                            box * 352);
       };
-      int row = page(s.j0);
-      prefetch(s.j0, row);
+      int row = page(s.tile(0));
+      prefetch(s.tile(0), row);
       if (seg > 0) ok = warp_wait(q_done, (seg - 1) & 1, ab, ok);
       if (!ok) break;
       if (seg > 0) load_query(s.t);
       q_issued = seg & 1;
-      for (int j = s.j0; ok && j < s.j1; ++j, ++it) {
-        const int c1 = (j * kSelTile + lane * box) & (p.pool.bs - 1);
+      for (int i = 0; ok && i < s.n; ++i, ++it) {
+        const int c1 = (s.tile(i) * kSelTile + lane * box) & (p.pool.bs - 1);
         const int n = __popc(__ballot_sync(0xffffffffu, row >= 0));
-        const int next = j + 1 < s.j1 ? page(j + 1) : -1;
-        prefetch(j + 1, next);
+        const int next = i + 1 < s.n ? page(s.tile(i + 1)) : -1;
+        if (i + 1 < s.n) prefetch(s.tile(i + 1), next);
 #pragma unroll 1
         for (f = 0; f < FILLS; ++f) {
           // the place of copy 13 it + f was last used four copies before
@@ -1002,7 +1006,7 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
     for (int seg = 0; ok && walk.next(s); ++seg) {
       if (seg == 0) load_query(s.t);
       ok = warp_wait(q_full, seg & 1, ab, ok);
-      for (int j = s.j0; ok && j < s.j1; ++j, ++it) {
+      for (int i = 0; ok && i < s.n; ++i, ++it) {
         ok = warp_wait(&full[0], it & 1, ab, ok);
         tc_fence_after();
 #pragma unroll
@@ -1026,8 +1030,8 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
         if (!ok) break;
         if (leader) tc_commit(s_full);
         __syncwarp();
-        const uint32_t acc = j > s.j0 ? 1u : 0u;
-        const bool last = j == s.j1 - 1;
+        const uint32_t acc = i > 0 ? 1u : 0u;
+        const bool last = i == s.n - 1;
         if (!(ok = warp_wait(&p_full[0], it & 1, ab, ok))) break;
         tc_fence_after();
         if (leader) {
@@ -1123,17 +1127,17 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
       const uint32_t* mrow = p.tree.mask + static_cast<int64_t>(s.t) * p.tree.words;
       const int32_t* btrow = p.b.bt + static_cast<int64_t>(req) * p.b.bt_stride;
       const int plain = min(base, pos + 1);   // positions below are all seen
-      // The record of this thread's position in tile j, null where nobody sees it or the block id
+      // The record of this thread's position in the segment's i-th tile, null where nobody sees it or the block id
       // is bad (the loads report that); ids are read two tiles ahead, scales one.
-      auto block = [&](int j) {
-        const int sv = j * kSelTile + crow;
-        if (j >= s.j1 || !(sv < plain || (sv <= pos && tree_sees(mrow, p.tree.words, base, sv)))) return -1;
+      auto block = [&](int i) {
+        const int sv = s.tile(i) * kSelTile + crow;
+        if (i >= s.n || !(sv < plain || (sv <= pos && tree_sees(mrow, p.tree.words, base, sv)))) return -1;
         return static_cast<int>(__ldg(btrow + (sv >> lg)));
       };
-      auto record = [&](int j, int id) -> const uint8_t* {
+      auto record = [&](int i, int id) -> const uint8_t* {
         if (id < 0 || id >= p.pool.num_rows) return nullptr;
         return p.pool.pool + static_cast<int64_t>(id) * p.pool.row_stride + p.pool.lat_off +
-               static_cast<int64_t>((j * kSelTile + crow) & bsm) * 352;
+               static_cast<int64_t>((s.tile(i) * kSelTile + crow) & bsm) * 352;
       };
       // the scale words of the group's chunks for the CTA's tile `n`, on their way to shared memory
       auto fetch_scales = [&](const uint8_t* r, int n) {
@@ -1144,8 +1148,8 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
         }
         cp_async_commit();
       };
-      const uint8_t* rec = record(s.j0, block(s.j0));
-      int id1 = block(s.j0 + 1);
+      const uint8_t* rec = record(0, block(0));
+      int id1 = block(1);
       fetch_scales(rec, it);
       ok = warp_wait(q_full, seg & 1, ab, ok);
       float2 c2[4], sh2[4], l2[4];            // per head pair b: logit scale (log2 units), SHIFT - reference, sum
@@ -1158,9 +1162,10 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
         l2[b] = make_float2(0.f, 0.f);
       }
       float m_ref = -INFINITY;                // quarter 0: reference of column 32 g + lane
-      for (int j = s.j0; j < s.j1; ++j, ++it) {
-        const uint8_t* next = record(j + 1, id1);
-        id1 = block(j + 2);
+      for (int n = 0; n < s.n; ++n, ++it) {
+        const int j = s.tile(n);
+        const uint8_t* next = record(n + 1, id1);
+        id1 = block(n + 2);
         fetch_scales(next, it + 1);
         cp_async_wait_but_one();
         const bool seen_row = rec != nullptr;
@@ -1201,7 +1206,7 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
           }
           return mx;
         };
-        bool moves = j == s.j0;
+        bool moves = n == 0;
         if (moves) {
           tmem_wait_ld();
         } else {
@@ -1253,7 +1258,7 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
             l2[b].x *= av.x;
             l2[b].y *= av.y;
           }
-          if (j > s.j0 && ok) {
+          if (n > 0 && ok) {
 #pragma unroll 1
             for (int v = 0; v < 4; ++v) {
 #pragma unroll 1
@@ -1338,14 +1343,23 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-// Merge of a token's partials: out = sum_j w_j o_j, w_j = l_j 2^(m_j - M) / sum.
-// Grid (96 heads, T); a block's 256 threads are 64 groups of 8 dims times 4 interleaved
-// quarters of the partials.  Tokens with one segment have their output already.
-constexpr int kTreeCombThreads = 256;
+// Merge of a token's partials: out = sum_j w_j o_j, w_j = l_j 2^(m_j - M) / sum.  Tokens with
+// one segment have their output already.  Grid (96 PARTS / 8, T): a block takes 8 / PARTS heads,
+// 64 threads (8 dims each) for each of PARTS interleaved parts of the partials.  Bound by
+// latency, two dependent rounds of loads: the block reads all (max, sum) pairs at once, and a
+// thread's partials are loaded eight at a time.  212 tokens of 2 or 3 partials: 69 us with a
+// block per head and a pass per pair, XXX us so.
+constexpr int kTreeCombThreads = 512;
+constexpr int kTreeCombMax = 256;   // CTAs at most, so partials of a token
+template <int PARTS>
 __global__ void __launch_bounds__(kTreeCombThreads) tree_combine_kernel(TreeMlaParams p) {
-  __shared__ float acc_sh[3][64][9];
-  const int h = blockIdx.x, t = blockIdx.y;
+  constexpr int HEADS = 8 / PARTS;
+  __shared__ float wgt[HEADS][kTreeCombMax];
+  __shared__ float2 ml_sh[HEADS][kTreeCombMax];
+  __shared__ float acc_sh[PARTS > 1 ? PARTS - 1 : 1][HEADS][64][8];
+  const int t = blockIdx.y, h0 = blockIdx.x * HEADS;
   grid_dep_wait();
+  grid_dep_launch();
   const int64_t W = __ldcg(p.starts + p.b.T);
   const int64_t u0 = __ldcg(p.starts + t), u1 = __ldcg(p.starts + t + 1);
   if (u1 <= u0) return;
@@ -1355,54 +1369,80 @@ __global__ void __launch_bounds__(kTreeCombThreads) tree_combine_kernel(TreeMlaP
   const int first = 2 * c0 + (share_begin(W, G, c0) < u0 ? 1 : 0);
   const int n = c1 - c0 + 1;
   auto slot = [&](int j) { return j == 0 ? first : 2 * (c0 + j); };
-  const int d8 = threadIdx.x & 63, part = threadIdx.x >> 6;
-  float M = -INFINITY;
-  for (int j = 0; j < n; ++j) {
-    const float2 ml = __ldcg(p.part_ml + static_cast<int64_t>(slot(j)) * kMlaHeads + h);
+  const int d8 = threadIdx.x & 63, unit = threadIdx.x >> 6;
+  const int part = unit % PARTS, hh = unit / PARTS;   // the first two warps of a head: part 0
+  for (int i = threadIdx.x; i < n * HEADS; i += kTreeCombThreads)
+    ml_sh[i % HEADS][i / HEADS] = __ldcg(p.part_ml + static_cast<int64_t>(slot(i / HEADS)) * kMlaHeads + h0 + i % HEADS);
+  // the first partials are on their way meanwhile
+  constexpr int U = 8;
+  const uint4* src = reinterpret_cast<const uint4*>(p.part_o + static_cast<int64_t>(h0 + hh) * kVDim) + d8;
+  auto load = [&](int j) {
+    return j < n ? __ldcg(src + static_cast<int64_t>(slot(j)) * (kMlaHeads * kVDim / 8)) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  uint4 v[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) v[u] = load(part + PARTS * u);
+  __syncthreads();
+  // weights of a head, by each of its warps (same values from each)
+  const int lane = threadIdx.x & 31;
+  float M = -INFINITY, L = 0.f;
+  for (int j = lane; j < n; j += 32) {
+    const float2 ml = ml_sh[hh][j];
     if (ml.y != 0.f) M = fmaxf(M, ml.x);
   }
-  float Ls = 0.f;
-  float acc[8] = {};
-#pragma unroll 4
-  for (int j = part; j < n; j += 4) {
-    const int64_t sl = static_cast<int64_t>(slot(j)) * kMlaHeads + h;
-    const float2 ml = __ldcg(p.part_ml + sl);
-    const uint4 v = __ldcg(reinterpret_cast<const uint4*>(p.part_o + sl * kVDim) + d8);
-    if (ml.y == 0.f) continue;
-    const float w = exp2f(ml.x - M) * ml.y;
-    Ls += w;
-    const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w4[e]));
-      acc[2 * e] = fmaf(w, f.x, acc[2 * e]);
-      acc[2 * e + 1] = fmaf(w, f.y, acc[2 * e + 1]);
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  for (int j = lane; j < n; j += 32) {
+    const float2 ml = ml_sh[hh][j];
+    const float w = ml.y == 0.f ? 0.f : exp2f(ml.x - M) * ml.y;
+    wgt[hh][j] = w;
+    L += w;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  __syncwarp();   // each warp reads what it wrote (its head's other warps write the same)
+  float acc[8] = {};
+  for (int j = part; j < n; j += PARTS * U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float w = j + PARTS * u < n ? wgt[hh][j + PARTS * u] : 0.f;
+      const uint32_t w4[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w4[e]));
+        acc[2 * e] = fmaf(w, f.x, acc[2 * e]);
+        acc[2 * e + 1] = fmaf(w, f.y, acc[2 * e + 1]);
+      }
+      v[u] = load(j + PARTS * (u + U));
     }
   }
-  if (part > 0) {
+  if constexpr (PARTS > 1) {
+    if (part > 0) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc_sh[part - 1][d8][e] = acc[e];
-    acc_sh[part - 1][d8][8] = Ls;
-  }
-  __syncthreads();
-  if (part > 0) return;
-  for (int q = 0; q < 3; ++q) {
+      for (int e = 0; e < 8; ++e) acc_sh[part - 1][hh][d8][e] = acc[e];
+    }
+    __syncthreads();
+    if (part > 0) return;
+    for (int q = 0; q < PARTS - 1; ++q)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] += acc_sh[q][d8][e];
-    Ls += acc_sh[q][d8][8];
+      for (int e = 0; e < 8; ++e) acc[e] += acc_sh[q][hh][d8][e];
   }
-  const float inv = Ls == 0.f ? 0.f : 1.f / Ls;
+  const float inv = L == 0.f ? 0.f : 1.f / L;
   __nv_bfloat162 o[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) o[e] = __floats2bfloat162_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-  __nv_bfloat16* dst = p.out + (static_cast<int64_t>(t) * kMlaHeads + h) * kVDim + 8 * d8;
-  *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(o);
-  if (d8 == 0 && p.lse) p.lse[static_cast<int64_t>(t) * kMlaHeads + h] = (M + log2f(Ls)) * 0.69314718055994531f;
+  const int64_t row = static_cast<int64_t>(t) * kMlaHeads + h0 + hh;
+  *reinterpret_cast<uint4*>(p.out + row * kVDim + 8 * d8) = *reinterpret_cast<const uint4*>(o);
+  if (d8 == 0 && p.lse) p.lse[row] = (M + log2f(L)) * 0.69314718055994531f;
 }
 
 static cudaError_t launch_combine(const TreeMlaParams& p, cudaStream_t st) {
   if (p.whole) return cudaSuccess;
-  return launch_ex(tree_combine_kernel, dim3(kMlaHeads, p.b.T), dim3(kTreeCombThreads), 0, st, true, 0u, p);
+  if (p.max_ctas > kTreeCombMax) return cudaErrorInvalidValue;
+  // Few tokens have many partials each: their heads are spread over four times the blocks.
+  if (12 * p.b.T < p.max_ctas)
+    return launch_ex(tree_combine_kernel<4>, dim3(48, p.b.T), dim3(kTreeCombThreads), 0, st, true, 0u, p);
+  return launch_ex(tree_combine_kernel<1>, dim3(12, p.b.T), dim3(kTreeCombThreads), 0, st, true, 0u, p);
 }
 
 cudaError_t launch_tree_mla_fp8(const CUtensorMap& lmap, const CUtensorMap& tmap, const TreeMlaParams& p,
