@@ -10,8 +10,7 @@
 //             probability below 1e-6, and typically 1.6 k (64K scores) to 4 k (1M) do.
 //  2. filter: one CTA per 4,096 scores lists its scores at or above the bound, in
 //             position order, and notes where its entries lie.
-//  3. select: one CTA per row gathers the entries chunk by chunk, so in position order,
-//             into shared memory, finds the k-th by one digit and comparisons within its bin
+//  3. select: one CTA per row puts the entries in position order into shared memory, finds the k-th by one digit and comparisons within its bin
 //             (by digits down to the last bit where the bin is crowded; equal keys by lower
 //             position), and writes the selection with one scan.
 // Rows of at most 16,384 scores go to step 3 directly.  Steps 1 and 2 only choose what
@@ -328,17 +327,12 @@ __device__ __forceinline__ void each_score(const TreeTopkParams& p, const Row& r
 // The k-th best of n listed entries (equal keys: the lower position first) as (T, cut),
 // when one digit leaves few enough of them to compare each with each: the entries of the
 // digit's bin are listed, and the one that needs k - above - 1 others before it is it.
-// False (nothing decided) when the bin holds more.
+// False (nothing decided) when the bin holds more.  lo, hi: the thread's part in the smallest
+// (at most) and the largest key; the entries have been written, no barrier since.
 constexpr int kPairs = kBins / 2;   // pairs that fit the histogram's place
-__device__ __forceinline__ bool select_listed(RowShared& S, const uint2* ent, uint32_t n, uint32_t k, uint32_t& T,
-                                              uint32_t& cut) {
+__device__ __forceinline__ bool select_listed(RowShared& S, const uint2* ent, uint32_t n, uint32_t lo, uint32_t hi,
+                                              uint32_t k, uint32_t& T, uint32_t& cut) {
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
-  uint32_t lo = 0xFFFFFFFFu, hi = 0u;
-  for (uint32_t i = tid; i < n; i += kRowThreads) {
-    const uint32_t key = ent[i].x;
-    if (key) lo = min(lo, key);
-    hi = max(hi, key);
-  }
   lo = __reduce_min_sync(0xffffffffu, lo);
   hi = __reduce_max_sync(0xffffffffu, hi);
   if (lane == 0) {
@@ -412,52 +406,60 @@ __global__ void __launch_bounds__(kRowThreads) tree_topk_select_kernel(TreeTopkP
   const float* row = p.scores + static_cast<int64_t>(t) * p.ld;
   const uint32_t k = static_cast<uint32_t>(p.k);
   uint32_t n;        // entries in shared memory, in position order
+  uint32_t lo = 0xFFFFFFFFu, hi = 0u;   // this thread's part in their extremes
   bool listed = true;
   if (!filtered(p, r)) {
     n = static_cast<uint32_t>(r.n);
-    for (int s = tid; s < r.n; s += kRowThreads) ent[s] = make_uint2(seen_key(p, r, s, __ldcg(row + s)), static_cast<uint32_t>(s));
+    for (int s = tid; s < r.n; s += kRowThreads) {
+      const uint32_t key = seen_key(p, r, s, __ldcg(row + s));
+      ent[s] = make_uint2(key, static_cast<uint32_t>(s));
+      if (key) lo = min(lo, key);
+      hi = max(hi, key);
+    }
   } else {
+    // The list holds the chunks' entries as the filter's CTAs arrived, each chunk's in order: entry i
+    // of chunk c belongs at (entries of the chunks before) + i - at[c].  Counts, places and the
+    // first entries are read at once, before it is known how many entries there are (up to the
+    // list's capacity they are the workspace's): one round trip to memory, not three.
+    constexpr int kAhead = 8;
+    const int nch = static_cast<int>(cdiv(r.n, kTopkChunk));
+    const uint2* list = p.list + static_cast<int64_t>(t) * p.cap;
+    const uint32_t* at = p.at + static_cast<int64_t>(t) * p.nchunks;
+    const uint32_t* num = p.num + static_cast<int64_t>(t) * p.nchunks;
+    uint2 e[kAhead];
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) {
+      const int i = tid + q * kRowThreads;
+      e[q] = i < p.cap ? __ldcg(list + i) : make_uint2(0u, 0u);
+    }
+    uint32_t cn = tid < nch ? __ldcg(num + tid) : 0u, ca = tid < nch ? __ldcg(at + tid) : 0u;
     n = __ldcg(p.fill + t);
+    lo = __ldcg(p.bound + t);
     listed = n >= k && n <= static_cast<uint32_t>(p.cap);
     if (listed) {
-      // Entry i of the row, in position order, is the entry i - pre of the chunk whose places
-      // [pre, next pre) hold it: found by bisection, so that every thread's loads are independent.
-      const int nch = static_cast<int>(cdiv(r.n, kTopkChunk));
-      const uint2* list = p.list + static_cast<int64_t>(t) * p.cap;
-      const uint32_t* at = p.at + static_cast<int64_t>(t) * p.nchunks;
-      const uint32_t* num = p.num + static_cast<int64_t>(t) * p.nchunks;
       uint32_t before = 0;
-      for (int c0 = 0; c0 < nch; c0 += kRowThreads) {
-        const int c = c0 + tid;
-        const uint32_t cn = c < nch ? __ldcg(num + c) : 0u, ca = c < nch ? __ldcg(at + c) : 0u;
-        uint32_t total;
-        const uint32_t pre = before + scan(cn, S.wsh[0], total);
-        S.h[tid] = pre;
-        S.h[kRowThreads + tid] = ca;
-        __syncthreads();
-        for (uint32_t i = before + tid; i < before + total; i += 4 * kRowThreads) {
-          int lo[4] = {0, 0, 0, 0};   // the last chunk of this round with pre <= the entry
-#pragma unroll
-          for (int step = kRowThreads / 2; step > 0; step >>= 1)
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              if (S.h[lo[q] + step] <= i + q * kRowThreads) lo[q] += step;
-          uint2 e[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t n = i + q * kRowThreads;
-            if (n < before + total) e[q] = __ldcg(list + S.h[kRowThreads + lo[q]] + (n - S.h[lo[q]]));
-          }
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (i + q * kRowThreads < before + total) ent[i + q * kRowThreads] = e[q];
+      for (int c0 = 0; c0 < nch; c0 += kRowThreads) {   // rounds of 1,024 chunks, 4M scores
+        if (c0 > 0) {
+          cn = c0 + tid < nch ? __ldcg(num + c0 + tid) : 0u;
+          ca = c0 + tid < nch ? __ldcg(at + c0 + tid) : 0u;
         }
+        uint32_t total;
+        S.h[tid] = before + scan(cn, S.wsh[0], total) - ca;   // (wraps; the sum with i does not)
         before += total;
+        __syncthreads();
+        auto place = [&](uint32_t i, uint2 x) {
+          const uint32_t c = x.y / kTopkChunk - static_cast<uint32_t>(c0);
+          if (i >= n || c >= static_cast<uint32_t>(kRowThreads)) return;
+          ent[S.h[c] + i] = x;
+          hi = max(hi, x.x);
+        };
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q) place(tid + q * kRowThreads, e[q]);
+        for (uint32_t i = tid + kAhead * kRowThreads; i < n; i += kRowThreads) place(i, __ldcg(list + i));
         __syncthreads();
       }
     }
   }
-  __syncthreads();
   auto keys = [&](auto take) {
     if (listed)
       for (uint32_t i = tid; i < n; i += kRowThreads) {
@@ -469,7 +471,7 @@ __global__ void __launch_bounds__(kRowThreads) tree_topk_select_kernel(TreeTopkP
   };
   // the threshold key T, and of the keys equal to it those at positions <= cut
   uint32_t T, cut = 0xFFFFFFFFu;
-  if (!listed || !select_listed(S, ent, n, k, T, cut)) {
+  if (!listed || !select_listed(S, ent, n, lo, hi, k, T, cut)) {
     uint32_t above, equal;
     T = select_value(S, keys, k, 0, above, equal);
     const uint32_t need = k - above;
