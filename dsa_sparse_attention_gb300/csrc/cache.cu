@@ -50,13 +50,13 @@ __global__ void __launch_bounds__(kCopyThreads) cache_copy_kernel(CacheCopyParam
   const int64_t per_row = cdiv(p.row_bytes, kCopyUnit);
   int64_t n = p.n;
   if (p.count) {
-    const int64_t c = __ldg(p.count);
+    const int64_t c = __ldcg(p.count);
     n = c < n ? (c < 0 ? 0 : c) : n;
   }
   for (int64_t u = blockIdx.x; u < n * per_row; u += gridDim.x) {
     const int64_t i = u / per_row;
     const int64_t off = (u - i * per_row) * kCopyUnit;
-    const int32_t s = __ldg(p.src + i), d = __ldg(p.dst + i);
+    const int32_t s = __ldcg(p.src + i), d = __ldcg(p.dst + i);
     if (s < 0 && d < 0) continue;
     if (s < 0 || d < 0 || s >= p.num_rows || d >= p.num_rows) {
       if (threadIdx.x == 0) atomicOr(p.status, DEV_BAD_BLOCK);
@@ -97,8 +97,8 @@ cudaError_t launch_cache_copy(const CacheCopyParams& p, int nsm, cudaStream_t st
 // in a second launch with CTAs per fork.
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanCtas = 8;
-// A free, a fork of 2 requests to 8 and the copies, 600 rows: 15.3 us a call (11.9 on the GPU) with
-// one CTA and one launch, 17.7 us (11.7) with a cluster and two, bound by the launches.
+// A free, a fork of 2 requests to 8 and the copies, 600 rows: 15.3 us together with one CTA and
+// one launch, 17.7 us with a cluster and two; the launches bound it (11.5 us in a graph).
 constexpr int64_t kOneCtaRows = 16384;
 constexpr int64_t kOneLaunchEntries = 8192;   // table entries per plan CTA
 
@@ -143,28 +143,45 @@ __device__ __forceinline__ void share_counts(uint32_t mine, uint32_t* counts, ui
   }
 }
 
-// Checks the forks and numbers those that need a row (of `all` free ones).  One CTA.
-__device__ __forceinline__ void plan_forks(const ForkParams& p, int64_t all, uint32_t* wsh) {
+// What the plan's first CTA keeps of the forks in shared memory, when there are at most
+// kPlanThreads of them and the list of free rows is this CTA's own.
+struct ForkShared {
+  int32_t rows[kPlanThreads];   // first free rows
+  int32_t plan[kPlanThreads];   // the plan, and the parents' lengths
+  int32_t lens[kPlanThreads];
+};
+
+// Checks the forks and numbers those that need a row (of `all` free ones).  One CTA; a0, c0: the
+// thread's first fork (-1 behind the last).  `marks`: zeroed counters of the requests.
+__device__ __forceinline__ void plan_forks(const ForkParams& p, int64_t all, int32_t* marks, bool small, ForkShared& fs,
+                                           int32_t a0, int32_t c0, uint32_t* wsh) {
+  // the first round's lengths arrive meanwhile
+  const bool in0 = a0 >= 0 && a0 < p.num_reqs && c0 >= 0 && c0 < p.num_reqs;
+  const int32_t la0 = in0 ? __ldcg(p.ctx + a0) : 0, lc0 = in0 ? __ldcg(p.ctx + c0) : 0;
   // who is named: children counted in the low half, parents flagged above
   for (int i = threadIdx.x; i < p.n; i += kPlanThreads) {
-    const int32_t a = p.parent[i], c = p.child[i];
+    const int32_t a = i < kPlanThreads ? a0 : __ldcg(p.parent + i), c = i < kPlanThreads ? c0 : __ldcg(p.child + i);
     if (a < 0) continue;
-    if (a < p.num_reqs) atomicOr(p.marks + a, 1 << 30);
-    if (c >= 0 && c < p.num_reqs) atomicAdd(p.marks + c, 1);
+    if (a < p.num_reqs) atomicOr(marks + a, 1 << 30);
+    if (c >= 0 && c < p.num_reqs) atomicAdd(marks + c, 1);
   }
+  __threadfence_block();
   __syncthreads();
   uint32_t base = 0;
   for (int i0 = 0; i0 < p.n; i0 += kPlanThreads) {
     const int i = i0 + threadIdx.x;
     bool ok = false, need = false, named = false;
     int64_t L = 0;
+    int32_t b = -1;
     if (i < p.n) {
-      const int32_t a = p.parent[i], c = p.child[i];
+      const int32_t a = i0 == 0 ? a0 : __ldcg(p.parent + i), c = i0 == 0 ? c0 : __ldcg(p.child + i);
       named = a >= 0;
-      if (named && a < p.num_reqs && c >= 0 && c < p.num_reqs && __ldcg(p.marks + c) == 1 && __ldcg(p.ctx + c) == 0) {
-        L = __ldcg(p.ctx + a);
+      if (named && a < p.num_reqs && c >= 0 && c < p.num_reqs && *static_cast<volatile int32_t*>(marks + c) == 1 &&
+          (i0 == 0 ? lc0 : __ldcg(p.ctx + c)) == 0) {
+        L = i0 == 0 ? la0 : __ldcg(p.ctx + a);
         ok = L >= 0 && L <= (static_cast<int64_t>(p.bt_stride) << p.log2_bs);
         need = ok && (L & ((1 << p.log2_bs) - 1)) != 0;
+        if (need) b = __ldcg(p.bt + static_cast<int64_t>(a) * p.bt_stride + (L >> p.log2_bs));
       }
     }
     uint32_t total;
@@ -172,15 +189,18 @@ __device__ __forceinline__ void plan_forks(const ForkParams& p, int64_t all, uin
     base += total;
     int32_t row = -1;
     if (need) {
-      if (o < all) row = p.free_list[o];
+      if (o < all) row = small ? fs.rows[o] : __ldcg(p.free_list + o);
       else ok = false;
     }
     if (i < p.n) {
       if (named && !ok) atomicOr(p.status, DEV_BAD_BATCH);
       p.plan[i] = ok ? row : kForkSkip;
+      if (small) {
+        fs.plan[i] = ok ? row : kForkSkip;
+        fs.lens[i] = static_cast<int32_t>(L);
+      }
       int32_t from = -1;
       if (ok && need) {
-        const int32_t b = __ldcg(p.bt + static_cast<int64_t>(p.parent[i]) * p.bt_stride + (L >> p.log2_bs));
         if (b >= 0 && b < p.num_rows) from = b;
         else atomicOr(p.status, DEV_BAD_BLOCK);
       }
@@ -190,15 +210,10 @@ __device__ __forceinline__ void plan_forks(const ForkParams& p, int64_t all, uin
   }
 }
 
-// One table entry of a fork.
-__device__ __forceinline__ void apply_fork(const ForkParams& p, int i, int32_t row, int e) {
-  if (row == kForkSkip) return;
-  const int32_t a = p.parent[i], c = p.child[i];
-  const int32_t L = __ldcg(p.ctx + a);   // a parent is no child of this call: not written here
+// One table entry of fork i of a parent with L tokens to request c; b: the parent's entry.
+__device__ __forceinline__ void apply_fork(const ForkParams& p, int32_t c, int32_t L, int32_t row, int32_t b, int e) {
   const int32_t full = L >> p.log2_bs;
-  int32_t b = -1;
   if (e < full) {
-    b = p.bt[static_cast<int64_t>(a) * p.bt_stride + e];
     if (b >= 0 && b < p.num_rows) {
       atomicAdd(p.ref + b, 1);
     } else {
@@ -208,51 +223,84 @@ __device__ __forceinline__ void apply_fork(const ForkParams& p, int i, int32_t r
   } else if (e == full && row >= 0) {
     b = row;
     p.ref[row] = 1;
+  } else {
+    b = -1;
   }
   p.bt[static_cast<int64_t>(c) * p.bt_stride + e] = b;
   if (e == 0) p.ctx[c] = L;
 }
 
+constexpr int kMarks = 4096;   // counters of as many requests fit shared memory
+
 __global__ void __launch_bounds__(kPlanThreads) cache_fork_plan_kernel(ForkParams p) {
   __shared__ uint32_t wsh[33];
   __shared__ uint32_t counts[kPlanCtas];
+  __shared__ ForkShared fs;
+  __shared__ int32_t marks_sh[kMarks];
   const uint32_t rank = cluster_rank();
+  const bool small = cluster_size() == 1 && p.n <= kPlanThreads;
+  int32_t* marks = p.num_reqs <= kMarks ? marks_sh : p.marks;
+  const int tid = static_cast<int>(threadIdx.x);
   grid_dep_wait();
   grid_dep_launch();
-  cluster_sync();   // every CTA has started before any writes into it
+  // loads that nothing depends on yet: the forks, and the free rows among this CTA's rows
+  int32_t a0 = -1, c0 = -1;
+  if (rank == 0 && tid < p.n) {
+    a0 = __ldcg(p.parent + tid);
+    c0 = __ldcg(p.child + tid);
+  }
   int64_t r0, r1;
   plan_rows(p.num_rows, rank, r0, r1);
-  const uint32_t mine = count_free(p.ref, r0, r1, wsh);
+  constexpr int kKept = 8;   // rounds of 4,096 rows whose bits stay in a register
+  uint32_t bits = 0, mine = 0;
+  {
+#pragma unroll
+    for (int q = 0; q < kKept; ++q) {
+      const int64_t r = r0 + 4 * (tid + q * kPlanThreads);
+      if (r < r1) bits |= free_bits(p.ref, r, r1) << (4 * q);
+    }
+    uint32_t k = __popc(bits);
+    for (int64_t r = r0 + 4 * (tid + kKept * kPlanThreads); r < r1; r += 4 * kPlanThreads)
+      k += __popc(free_bits(p.ref, r, r1));
+    block_scan(k, wsh, mine);
+  }
+  if (rank == 0)
+    for (int i = tid; i < p.num_reqs; i += kPlanThreads) marks[i] = 0;
+  cluster_sync();   // every CTA has started before any writes into it
   int64_t before, all;
   share_counts(mine, counts, rank, before, all);
   // list the first free rows, up to one per fork
-  uint32_t at = 0;   // free rows of this CTA before the chunk
-  for (int64_t c = r0; c < r1 && before + at < p.n; c += 4 * kPlanThreads) {
-    const int64_t r = c + 4 * threadIdx.x;
-    const uint32_t m = r < r1 ? free_bits(p.ref, r, r1) : 0u;
+  uint32_t at = 0;   // free rows of this CTA before the round
+  int q = 0;
+  for (int64_t c = r0; c < r1 && before + at < p.n; c += 4 * kPlanThreads, ++q) {
+    const int64_t r = c + 4 * tid;
+    const uint32_t m = q < kKept ? (bits >> (4 * q)) & 15u : (r < r1 ? free_bits(p.ref, r, r1) : 0u);
     uint32_t total;
     int64_t o = before + at + block_scan(__popc(m), wsh, total);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       if ((m >> k) & 1u) {
-        if (o < p.n) p.free_list[o] = static_cast<int32_t>(r + k);
+        if (o < p.n) (small ? fs.rows : p.free_list)[o] = static_cast<int32_t>(r + k);
         ++o;
       }
     at += total;
   }
-  if (rank == 0)
-    for (int i = threadIdx.x; i < p.num_reqs; i += kPlanThreads) p.marks[i] = 0;
   __threadfence();
   cluster_sync();   // the list is complete and visible
-  if (rank == 0) plan_forks(p, all, wsh);
+  if (rank == 0) plan_forks(p, all, marks, small, fs, a0, c0, wsh);
   if (!p.apply_here) return;
   __threadfence();
   cluster_sync();   // so is the plan
+  // (a parent is no child of this call, so its table row and length are not written here)
   const int64_t entries = static_cast<int64_t>(p.n) * p.bt_stride;
-  for (int64_t e = static_cast<int64_t>(rank) * kPlanThreads + threadIdx.x; e < entries;
-       e += static_cast<int64_t>(cluster_size()) * kPlanThreads) {
-    const int i = static_cast<int>(e / p.bt_stride);
-    apply_fork(p, i, __ldcg(p.plan + i), static_cast<int>(e - static_cast<int64_t>(i) * p.bt_stride));
+  for (int64_t x = static_cast<int64_t>(rank) * kPlanThreads + tid; x < entries;
+       x += static_cast<int64_t>(cluster_size()) * kPlanThreads) {
+    const int i = static_cast<int>(x / p.bt_stride), e = static_cast<int>(x - static_cast<int64_t>(i) * p.bt_stride);
+    const int32_t row = small ? fs.plan[i] : __ldcg(p.plan + i);
+    if (row == kForkSkip) continue;
+    const int32_t a = __ldcg(p.parent + i), c = __ldcg(p.child + i);
+    const int32_t L = small ? fs.lens[i] : __ldcg(p.ctx + a);
+    apply_fork(p, c, L, row, __ldcg(p.bt + static_cast<int64_t>(a) * p.bt_stride + e), e);
   }
 }
 
@@ -263,9 +311,12 @@ __global__ void __launch_bounds__(kApplyThreads) cache_fork_apply_kernel(ForkPar
   grid_dep_wait();
   grid_dep_launch();
   const int i = blockIdx.x;
-  const int32_t row = p.plan[i];
+  const int32_t row = __ldcg(p.plan + i), a = __ldcg(p.parent + i), c = __ldcg(p.child + i);
+  if (row == kForkSkip) return;
+  const int32_t L = __ldcg(p.ctx + a);
   const int e1 = min(p.bt_stride, static_cast<int>(blockIdx.y + 1) * kApplyEntries);
-  for (int e = blockIdx.y * kApplyEntries + threadIdx.x; e < e1; e += kApplyThreads) apply_fork(p, i, row, e);
+  for (int e = blockIdx.y * kApplyEntries + threadIdx.x; e < e1; e += kApplyThreads)
+    apply_fork(p, c, L, row, __ldcg(p.bt + static_cast<int64_t>(a) * p.bt_stride + e), e);
 }
 
 cudaError_t launch_cache_fork(const ForkParams& in, cudaStream_t st) {
@@ -286,7 +337,7 @@ cudaError_t launch_cache_fork(const ForkParams& in, cudaStream_t st) {
 __global__ void __launch_bounds__(kApplyThreads) cache_free_kernel(FreeParams p) {
   grid_dep_wait();
   grid_dep_launch();
-  const int32_t r = p.reqs[blockIdx.x];
+  const int32_t r = __ldcg(p.reqs + blockIdx.x);
   if (r < 0) return;
   if (r >= p.num_reqs) {
     if (threadIdx.x == 0 && blockIdx.y == 0) atomicOr(p.status, DEV_BAD_BATCH);
@@ -322,7 +373,7 @@ cudaError_t launch_cache_free(const FreeParams& p, cudaStream_t st) {
 // old row to new.  The block tables are mapped in the same launch when they are small.
 // One table entry's row after the moves.
 __device__ __forceinline__ void map_entry(const CompactParams& p, int64_t e) {
-  const int32_t b = p.bt[e];
+  const int32_t b = __ldcg(p.bt + e);
   int32_t to = -1;
   if (b >= 0) {
     if (b < p.num_rows) to = __ldcg(p.remap + b);
