@@ -954,9 +954,11 @@ dsa_status dsa_tree_topk(const dsa_kv_layout* layout, const dsa_batch* batch, co
   dsa_kv_layout dummy{};
   dummy.num_rows = 1;
   dummy.block_size = 64;
+  const int T = batch->num_tokens;
+  if (T > 65535) return DSA_ERR_UNSUPPORTED;   // the filter's launch grid
+  if (!aligned4(idx) || !aligned4(phys_slots)) return DSA_ERR_INVALID_ARG;
   const Ws wl = plan_ws(layout ? layout : &dummy, batch, topk);
   if ((s = check_ws(workspace, workspace_bytes, wl)) != DSA_OK) return s;
-  const int T = batch->num_tokens;
   if (T == 0) return DSA_OK;
   const TopkScratch L = topk_scratch_layout(T, wl.topk_nchunks);
   TreeTopkParams p;

@@ -378,7 +378,8 @@ dsa_status dsa_write_latent(const dsa_kv_layout *layout, const dsa_batch *batch,
  * causal whatever its mask.  A token with q_req[t] < 0 is padding: its output rows
  * are left as they are.  A token that sees nothing has output 0 and lse -inf, and
  * no selection.  What lies in the cache at positions nobody sees never reaches a
- * result, NaN codes included.
+ * result, NaN codes included.  A batch of more than 65,535 tokens is refused
+ * (DSA_ERR_UNSUPPORTED).
  */
 typedef struct {
   const int32_t *base;    /* device [B]: committed tokens of each request, 0..ctx_lens[r] */

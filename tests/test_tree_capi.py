@@ -127,6 +127,8 @@ def test_tree_topk_refusals(lib):
     for bad in (dict(bat=None), dict(k=0), dict(k=2049), dict(ld=999), dict(ld=1002), dict(scores=None),
                 dict(scores=0x80008), dict(idx=None), dict(lay=None, phys=0x1000)):
         assert call(**bad) == -1
+    assert call(idx=0x90002) == -1 and call(phys=0x90001) == -1
+    assert call(bat=_batch(T=65536)) == -2
     assert call(ws=(0x100000, 256)) == -4
     assert call(bat=_batch(T=0)) == 0
 
