@@ -126,17 +126,22 @@ def _ptr(t):
     return t.data_ptr()
 
 
-# The handle of a device's current stream without making a Stream object (3 us a call),
-# where this PyTorch has it.
+# The handle of the current device's current stream without making a Stream object (3 us a
+# call), where this PyTorch has it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = None
 
 
 def _stream(stream):
+    global _device
     if stream is not None:
         return ctypes.c_void_p(stream.cuda_stream)
-    if _raw_stream is not None:
-        return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    if _raw_stream is None:
+        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    if _device is None:
+        torch.cuda.current_device()   # initialises CUDA
+        _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    return ctypes.c_void_p(_raw_stream(_device()))
 
 
 def dsa_last_cuda_error():
@@ -281,23 +286,29 @@ def dsa_write_latent(layout, batch, latent, ws=None, stream=None):
                                       _stream(stream)), "dsa_write_latent")
 
 
+_I32 = torch.int32
+_byref = ctypes.byref
+
+
 def _int32(name, t, ndim):
-    """An int32 tensor whose elements lie one behind the other, as the C ABI reads it."""
-    if t is not None and (t.dtype != torch.int32 or t.dim() != ndim or not t.is_contiguous()):
+    """The address of an int32 tensor whose elements lie one behind the other, as the C ABI
+    reads it (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype is not _I32 or t.dim() != ndim or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor of {ndim} dimension(s)")
-    return t
+    return t.data_ptr()
 
 
 def make_tree(base, mask):
     """Descriptor of the drafted tokens' trees over device int32 tensors (kept alive by the
     caller): base [B] committed tokens, mask [T, words], bit i of row t set where token t sees
     drafted slot i."""
-    _int32("base", base, 1), _int32("mask", mask, 2)
-    return dsa_tree(_ptr(base), _ptr(mask), int(mask.shape[1]), 0)
+    return dsa_tree(_int32("base", base, 1), _int32("mask", mask, 2), int(mask.shape[1]), 0)
 
 
 def dsa_tree_workspace_size(layout, batch):
-    return int(library().dsa_tree_workspace_size(ctypes.byref(layout), ctypes.byref(batch)))
+    return int(library().dsa_tree_workspace_size(_byref(layout), _byref(batch)))
 
 
 def alloc_tree_workspace(layout, batch, device="cuda"):
@@ -310,39 +321,45 @@ def alloc_tree_workspace(layout, batch, device="cuda"):
 
 def dsa_tree_mla(layout, batch, tree, q, sm_scale, out, lse=None, ws=None, stream=None):
     """Dense attention of drafted tokens over the positions each sees (bf16 q [T, 96, 576])."""
-    _check(library().dsa_tree_mla(ctypes.byref(layout), ctypes.byref(batch), ctypes.byref(tree), _ptr(q),
-                                  float(sm_scale), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)),
-           "dsa_tree_mla")
+    s = library().dsa_tree_mla(_byref(layout), _byref(batch), _byref(tree), _ptr(q), float(sm_scale), _ptr(out),
+                               _ptr(lse), _ptr(ws), ws.numel(), _stream(stream))
+    if s:
+        _check(s, "dsa_tree_mla")
 
 
 def dsa_tree_topk(layout, batch, tree, scores, ld, topk, idx, phys_slots=None, ws=None, stream=None):
     """dsa_topk over the positions each drafted token sees (workspace as dsa_topk)."""
-    lay = ctypes.byref(layout) if layout is not None else None
-    _check(library().dsa_tree_topk(lay, ctypes.byref(batch), ctypes.byref(tree), _ptr(scores), int(ld), int(topk),
-                                   _ptr(idx), _ptr(phys_slots), _ptr(ws), ws.numel(), _stream(stream)),
-           "dsa_tree_topk")
+    s = library().dsa_tree_topk(_byref(layout) if layout is not None else None, _byref(batch), _byref(tree),
+                                _ptr(scores), int(ld), int(topk), _ptr(idx), _ptr(phys_slots), _ptr(ws), ws.numel(),
+                                _stream(stream))
+    if s:
+        _check(s, "dsa_tree_topk")
 
 
 def dsa_tree_commit(layout, batch, base, accept, new_lens=None, ws=None, stream=None):
     """The accepted drafted slots (accept [B, max_accept], -1 behind the last) become the
     positions behind the committed ones; new_lens [B] receives the committed lengths."""
-    _int32("base", base, 1), _int32("accept", accept, 2), _int32("new_lens", new_lens, 1)
-    _check(library().dsa_tree_commit(ctypes.byref(layout), ctypes.byref(batch), _ptr(base), _ptr(accept),
-                                     int(accept.shape[1]), _ptr(new_lens), _ptr(ws), ws.numel(), _stream(stream)),
-           "dsa_tree_commit")
+    pb, pa, pn = _int32("base", base, 1), _int32("accept", accept, 2), _int32("new_lens", new_lens, 1)
+    rows, most = accept.shape
+    if rows != batch.num_reqs:
+        raise ValueError("accept must have a row for every request")
+    s = library().dsa_tree_commit(_byref(layout), _byref(batch), pb, pa, most, pn, ws.data_ptr(), ws.numel(),
+                                  _stream(stream))
+    if s:
+        _check(s, "dsa_tree_commit")
 
 
 def make_pages(ref_count, block_table, ctx_lens):
     """Descriptor of who holds which rows, over device int32 tensors (kept alive by the caller)."""
-    _int32("ref_count", ref_count, 1), _int32("block_table", block_table, 2), _int32("ctx_lens", ctx_lens, 1)
+    pages = dsa_pages(_int32("ref_count", ref_count, 1), _int32("block_table", block_table, 2),
+                      _int32("ctx_lens", ctx_lens, 1), int(ctx_lens.shape[0]), int(block_table.shape[1]))
     if block_table.shape[0] != ctx_lens.shape[0]:
         raise ValueError("block_table and ctx_lens must have a row and a length for every request")
-    return dsa_pages(_ptr(ref_count), _ptr(block_table), _ptr(ctx_lens), int(ctx_lens.shape[0]),
-                     int(block_table.shape[1]))
+    return pages
 
 
 def dsa_cache_workspace_size(layout, num_reqs):
-    return int(library().dsa_cache_workspace_size(ctypes.byref(layout), int(num_reqs)))
+    return int(library().dsa_cache_workspace_size(_byref(layout), int(num_reqs)))
 
 
 def alloc_cache_workspace(layout, num_reqs, device="cuda"):
@@ -355,41 +372,52 @@ def alloc_cache_workspace(layout, num_reqs, device="cuda"):
 
 def dsa_cache_copy(layout, src, dst, count=None, ws=None, stream=None):
     """Rows src[i] of the pool copied to rows dst[i]; count: a device int32 that says how many."""
-    _int32("src", src, 1), _int32("dst", dst, 1)
-    if src.shape != dst.shape:
+    ps, pd, n = _int32("src", src, 1), _int32("dst", dst, 1), src.numel()
+    if dst.numel() != n:
         raise ValueError("src and dst must be of one length")
-    _check(library().dsa_cache_copy(ctypes.byref(layout), _ptr(src), _ptr(dst), int(src.numel()), _ptr(count),
-                                    _ptr(ws), ws.numel(), _stream(stream)), "dsa_cache_copy")
+    pc = None
+    if count is not None:
+        if count.dtype is not _I32 or count.numel() < 1:
+            raise ValueError("count must be an int32 tensor of an element")
+        pc = count.data_ptr()
+    s = library().dsa_cache_copy(_byref(layout), ps, pd, n, pc, ws.data_ptr(), ws.numel(), _stream(stream))
+    if s:
+        _check(s, "dsa_cache_copy")
 
 
 def dsa_cache_fork(layout, pages, parent, child, copy_src, copy_dst, ws=None, stream=None):
     """Requests child[i] become copies of parent[i] that share its full blocks; copy_src and
     copy_dst receive the rows dsa_cache_copy must copy (-1 where none)."""
-    for name, t in (("parent", parent), ("child", child), ("copy_src", copy_src), ("copy_dst", copy_dst)):
-        if _int32(name, t, 1).numel() != parent.numel():
-            raise ValueError("parent, child, copy_src and copy_dst must be of one length")
-    _check(library().dsa_cache_fork(ctypes.byref(layout), ctypes.byref(pages), _ptr(parent), _ptr(child),
-                                    int(parent.numel()), _ptr(copy_src), _ptr(copy_dst), _ptr(ws), ws.numel(),
-                                    _stream(stream)), "dsa_cache_fork")
+    pp, pc = _int32("parent", parent, 1), _int32("child", child, 1)
+    ps, pd, n = _int32("copy_src", copy_src, 1), _int32("copy_dst", copy_dst, 1), parent.numel()
+    if not child.numel() == copy_src.numel() == copy_dst.numel() == n:
+        raise ValueError("parent, child, copy_src and copy_dst must be of one length")
+    s = library().dsa_cache_fork(_byref(layout), _byref(pages), pp, pc, n, ps, pd, ws.data_ptr(), ws.numel(),
+                                 _stream(stream))
+    if s:
+        _check(s, "dsa_cache_fork")
 
 
 def dsa_cache_free(layout, pages, reqs, ws=None, stream=None):
     """Requests' blocks given back: table rows -1, counts down by one, lengths 0."""
-    _int32("reqs", reqs, 1)
-    _check(library().dsa_cache_free(ctypes.byref(layout), ctypes.byref(pages), _ptr(reqs), int(reqs.numel()),
-                                    _ptr(ws), ws.numel(), _stream(stream)), "dsa_cache_free")
+    s = library().dsa_cache_free(_byref(layout), _byref(pages), _int32("reqs", reqs, 1), reqs.numel(), ws.data_ptr(),
+                                 ws.numel(), _stream(stream))
+    if s:
+        _check(s, "dsa_cache_free")
 
 
 def dsa_cache_compact(layout, pages, to, copy_src, copy_dst, counts, ws=None, stream=None):
     """Plans the moves that bring the used rows to the front of the pool: counts and tables
     afterwards into `to`, (rows used, moves) into counts, the moves into copy_src -> copy_dst
     ([num_rows // 2], -1 behind the last), for dsa_cache_copy with count=counts[1:]."""
-    _int32("copy_src", copy_src, 1), _int32("copy_dst", copy_dst, 1), _int32("counts", counts, 1)
-    if min(copy_src.numel(), copy_dst.numel()) < max(1, layout.num_rows // 2) or counts.numel() < 2:
+    ps, pd = _int32("copy_src", copy_src, 1), _int32("copy_dst", copy_dst, 1)
+    pc, need = _int32("counts", counts, 1), max(1, layout.num_rows // 2)
+    if copy_src.numel() < need or copy_dst.numel() < need or counts.numel() < 2:
         raise ValueError("copy_src and copy_dst need num_rows // 2 elements, counts two")
-    _check(library().dsa_cache_compact(ctypes.byref(layout), ctypes.byref(pages), ctypes.byref(to), _ptr(copy_src),
-                                       _ptr(copy_dst), _ptr(counts), _ptr(ws), ws.numel(), _stream(stream)),
-           "dsa_cache_compact")
+    s = library().dsa_cache_compact(_byref(layout), _byref(pages), _byref(to), ps, pd, pc, ws.data_ptr(), ws.numel(),
+                                    _stream(stream))
+    if s:
+        _check(s, "dsa_cache_compact")
 
 
 def dsa_check(ws, stream=None):

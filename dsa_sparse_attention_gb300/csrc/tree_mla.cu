@@ -81,7 +81,9 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(TreePrepParams 
     return;
   }
   __shared__ int64_t wsum[kPrepThreads / 32];
-  __shared__ int64_t st_sh[kPrepThreads + 1];   // the starts of a batch of up to 1,024 tokens
+  // starts and records of a batch of up to 1,024 tokens
+  __shared__ int64_t st_sh[kPrepThreads];
+  __shared__ TreeToken tok_sh[kPrepThreads];
   const int T = p.b.T;
   int64_t base = 0;
   for (int t0 = 0; t0 < T; t0 += kPrepThreads) {
@@ -91,6 +93,7 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(TreePrepParams 
       TreeToken k = {0, 0, 0, 0};
       if (load_tree_token(p.b, p.tree, t, p.status, k.req, k.pos, k.base)) v = cdiv(k.pos + 1, kSelTile);
       p.toks[t] = k;
+      tok_sh[threadIdx.x] = k;
     }
     int64_t x = v;
 #pragma unroll
@@ -130,8 +133,12 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(TreePrepParams 
       s.t = lo;
       s.u0 = T <= kPrepThreads ? st_sh[lo] : __ldcg(p.starts + lo);
       s.u1 = lo + 1 == T ? base : (T <= kPrepThreads ? st_sh[lo + 1] : __ldcg(p.starts + lo + 1));
-      const int4 k = __ldcg(reinterpret_cast<const int4*>(p.toks) + lo);
-      s.tok = TreeToken{k.x, k.y, k.z, k.w};
+      if (T <= kPrepThreads) {
+        s.tok = tok_sh[lo];
+      } else {
+        const int4 k = __ldcg(reinterpret_cast<const int4*>(p.toks) + lo);
+        s.tok = TreeToken{k.x, k.y, k.z, k.w};
+      }
     }
     p.shares[c] = s;
   }

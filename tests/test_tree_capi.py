@@ -198,6 +198,11 @@ def test_binding_refuses_what_the_abi_cannot_see():
         dsa.dsa_cache_compact(lay, _pages(), _pages(), i(49), i(50), i(2), ws=ws)
     with pytest.raises(ValueError):
         dsa.dsa_tree_commit(lay, _batch(), i(2), i(2, 8)[:, ::2], ws=ws)
+    with pytest.raises(ValueError):
+        dsa.dsa_tree_commit(lay, _batch(), i(2), i(1, 8), ws=ws)       # a row short
+    for count in (i(1).long(), i(0)):
+        with pytest.raises(ValueError):
+            dsa.dsa_cache_copy(lay, i(2), i(2), count, ws=ws)
 
 
 def test_structure_layout(tmp_path):
