@@ -1353,7 +1353,7 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
 // Merge of a token's partials: out = sum_j w_j o_j, w_j = l_j 2^(m_j - M) / sum.  Tokens with
 // one segment have their output already.  Grid (96 PARTS / 8, T): a block takes 8 / PARTS heads,
 // 64 threads (8 dims each) for each of PARTS interleaved parts of the partials.  Bound by
-// latency, two dependent rounds of loads: the block reads all (max, sum) pairs at once, and a
+// latency, two rounds of loads: the block reads all (max, sum) pairs at once, and a
 // thread's partials are loaded eight at a time.  212 tokens of 2 or 3 partials: 69 us with a
 // block per head and a pass per pair, XXX us so.
 constexpr int kTreeCombThreads = 512;
@@ -1365,15 +1365,19 @@ __global__ void __launch_bounds__(kTreeCombThreads) tree_combine_kernel(TreeMlaP
   __shared__ float2 ml_sh[HEADS][kTreeCombMax];
   __shared__ float acc_sh[PARTS > 1 ? PARTS - 1 : 1][HEADS][64][8];
   const int t = blockIdx.y, h0 = blockIdx.x * HEADS;
-  grid_dep_wait();
-  grid_dep_launch();
+  // The plan was complete before the attention let this kernel start: it is read ahead of the wait.
   const int64_t W = __ldcg(p.starts + p.b.T);
   const int64_t u0 = __ldcg(p.starts + t), u1 = __ldcg(p.starts + t + 1);
-  if (u1 <= u0) return;
-  const int G = static_cast<int>(W < p.max_ctas ? W : p.max_ctas);
-  const int c0 = share_of(W, G, u0), c1 = share_of(W, G, u1 - 1);
-  if (c0 == c1) return;
-  const int first = 2 * c0 + (share_begin(W, G, c0) < u0 ? 1 : 0);
+  int c0 = 0, c1 = 0, first = 0;
+  if (u1 > u0) {
+    const int G = static_cast<int>(W < p.max_ctas ? W : p.max_ctas);
+    c0 = share_of(W, G, u0);
+    c1 = share_of(W, G, u1 - 1);
+    first = 2 * c0 + (share_begin(W, G, c0) < u0 ? 1 : 0);
+  }
+  grid_dep_wait();
+  grid_dep_launch();
+  if (c0 == c1) return;   // padding, or one segment
   const int n = c1 - c0 + 1;
   auto slot = [&](int j) { return j == 0 ? first : 2 * (c0 + j); };
   const int d8 = threadIdx.x & 63, unit = threadIdx.x >> 6;
