@@ -18,8 +18,9 @@
 // many (more equal scores than the list holds) is resolved over the whole row, exactly
 // and slowly.  No sum depends on an order of arrival: results are deterministic and
 // independent of the rest of the batch.
-// Bound by latency: 48 rows of 64K take 18 us, 16 rows of 1M 35 us, when reading the scores
-// alone would take 1.9 and 9.9 us; the launches overlap as far as their waits allow.
+// Bound by latency: 48 rows of 64K take 15.7 us, 16 rows of 1M 35 us, when reading the scores
+// alone would take 1.9 and 9.9 us; the launches overlap as far as their waits allow, and data that
+// another SM has just written takes 0.8 us to read.
 #include "params.cuh"
 
 namespace dsa {
@@ -187,36 +188,75 @@ __device__ __forceinline__ uint32_t select_value(RowShared& S, Each each, uint32
 
 __global__ void __launch_bounds__(kRowThreads) tree_topk_bound_kernel(TreeTopkParams p) {
   __shared__ RowShared S;
+  constexpr int kMine = kSamples / kRowThreads;
+  const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_dep_wait();
   grid_dep_launch();   // the filter's blocks load their scores meanwhile: this call's inputs are complete
-  const int t = blockIdx.x;
+  const float* row = p.scores + static_cast<int64_t>(t) * p.ld;
+  float v[kMine];
+  int at[kMine];
+  auto sample = [&](int n) {   // (n > kDirect, at most the row's memory)
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const uint32_t q = threadIdx.x + i * kRowThreads;
+      const uint32_t a = static_cast<uint32_t>(static_cast<uint64_t>(n) * q / kSamples);
+      const uint32_t b = static_cast<uint32_t>(static_cast<uint64_t>(n) * (q + 1) / kSamples);
+      uint32_t hsh = q * 2654435761u;
+      hsh ^= hsh >> 15;
+      at[i] = static_cast<int>(a + hsh % (b - a));   // b > a: n > samples
+      v[i] = __ldcg(row + at[i]);
+    }
+  };
+  // the samples are on their way while the rest of the token is read and checked
+  const int64_t end = static_cast<int64_t>(__ldcg(p.b.q_pos + t)) + 1;
+  const bool early = end > kDirect && end <= p.ld;
+  if (early) sample(static_cast<int>(end));
   Row r;
   const bool work = load_row(p, t, r) && filtered(p, r);
   if (!work) return;
   if (threadIdx.x == 0) p.fill[t] = 0;
-  const float* row = p.scores + static_cast<int64_t>(t) * p.ld;
-  uint32_t u[kSamples / kRowThreads];
+  if (!early || r.n != end) sample(r.n);   // a position that was out of range and has been clamped
+  uint32_t u[kMine], most = 0;
 #pragma unroll
-  for (int i = 0; i < kSamples / kRowThreads; ++i) {
-    const uint32_t q = threadIdx.x + i * kRowThreads;
-    const uint32_t a = static_cast<uint32_t>(static_cast<uint64_t>(r.n) * q / kSamples);
-    const uint32_t b = static_cast<uint32_t>(static_cast<uint64_t>(r.n) * (q + 1) / kSamples);
-    uint32_t hsh = q * 2654435761u;
-    hsh ^= hsh >> 15;
-    const int s = static_cast<int>(a + hsh % (b - a));   // b > a: n > samples
-    u[i] = seen_key(p, r, s, __ldcg(row + s));
+  for (int i = 0; i < kMine; ++i) {
+    u[i] = seen_key(p, r, at[i], v[i]);   // (a filtered row's samples are nearly all seen)
+    most = max(most, u[i]);
   }
   const float m = static_cast<float>(kSamples) * static_cast<float>(p.k) / static_cast<float>(r.n);
   const uint32_t rank = min(static_cast<uint32_t>(m + 6.f * sqrtf(m)) + 8u, static_cast<uint32_t>(kSamples));
-  uint32_t above, equal;
-  const uint32_t bound = select_value(   // to within 2^10: a lower bound of the sample's rank
-      S,
-      [&](auto take) {
+  // The samples' threshold lies above the smallest maximum of `rank` groups of samples, so with
+  // few ranks it lies above that of all groups of 4 lanes: what is left spans few octaves, and
+  // one digit of 11 bits divides it finely enough.
+  constexpr uint32_t kGroups = kRowThreads / 4;
+  uint32_t bound;
+  if (rank <= kGroups) {
+    uint32_t g = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+    g = max(g, __shfl_xor_sync(0xffffffffu, g, 2));
+    const uint32_t lo_w = __reduce_min_sync(0xffffffffu, g), hi_w = __reduce_max_sync(0xffffffffu, g);
+    if (lane == 0) {
+      S.wsh[0][warp] = lo_w;
+      S.wsh[1][warp] = hi_w;
+    }
+    for (int i = threadIdx.x; i < kBins; i += kRowThreads) S.h[i] = 0;
+    __syncthreads();
+    const uint32_t lo = __reduce_min_sync(0xffffffffu, S.wsh[0][lane]), hi = __reduce_max_sync(0xffffffffu, S.wsh[1][lane]);
+    const int shift = max(32 - __clz(hi - lo) - 11, 0);
 #pragma unroll
-        for (int i = 0; i < kSamples / kRowThreads; ++i)
-          if (u[i]) take(u[i]);   // (a filtered row's samples are nearly all seen)
-      },
-      rank, 10, above, equal);
+    for (int i = 0; i < kMine; ++i)
+      if (u[i] >= lo) atomicAdd(&S.h[(u[i] - lo) >> shift], 1u);
+    __syncthreads();
+    bound = lo + (find_digit(S, kBins, rank, 2).x << shift);
+  } else {   // to within 2^10: a lower bound of the sample's rank
+    uint32_t above, equal;
+    bound = select_value(
+        S,
+        [&](auto take) {
+#pragma unroll
+          for (int i = 0; i < kMine; ++i)
+            if (u[i]) take(u[i]);
+        },
+        rank, 10, above, equal);
+  }
   if (threadIdx.x == 0) p.bound[t] = max(bound, 1u);   // positions not seen have key 0
 }
 static_assert(kTreeTopkCap <= 32 * kRowThreads, "rounds of the ordered output");
