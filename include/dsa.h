@@ -380,6 +380,8 @@ dsa_status dsa_write_latent(const dsa_kv_layout *layout, const dsa_batch *batch,
  * no selection.  What lies in the cache at positions nobody sees never reaches a
  * result, NaN codes included.  A batch of more than 65,535 tokens is refused
  * (DSA_ERR_UNSUPPORTED).
+ * A workspace serves one call at a time: calls that share one, replayed graphs of them
+ * included, are issued in order on one stream.
  */
 typedef struct {
   const int32_t *base;    /* device [B]: committed tokens of each request, 0..ctx_lens[r] */
@@ -458,10 +460,11 @@ typedef struct {
 size_t dsa_cache_workspace_size(const dsa_kv_layout *layout, int32_t num_reqs);
 
 /*
- * Copies whole rows of the pool: row dst[i] <- row src[i] for i < n (i < min(n, *count)
- * with count given, a device int32).  Entries with both ids negative are skipped; any
- * other id outside the pool is recorded in the status word and its pair skipped.  A
- * source may repeat; a destination may not, and may be no pair's source (but its own).
+ * Copies whole rows of the pool, all row_stride_bytes of each: row dst[i] <- row src[i]
+ * for i < n (i < min(n, *count) with count given, a device int32).  Entries with both ids
+ * negative are skipped; any other id outside the pool is recorded in the status word and
+ * its pair skipped.  A source may repeat; a destination may not, and may be no pair's
+ * source (but its own).
  * One call per pool: with a pool per layer, the pairs that fork and compact write serve
  * every layer.
  */
