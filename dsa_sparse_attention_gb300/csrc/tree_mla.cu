@@ -1359,7 +1359,7 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
 constexpr int kTreeCombThreads = 512;
 constexpr int kTreeCombMax = 256;   // CTAs at most, so partials of a token
 template <int PARTS>
-__global__ void __launch_bounds__(kTreeCombThreads) tree_combine_kernel(TreeMlaParams p) {
+__global__ void __launch_bounds__(kTreeCombThreads, PARTS > 1 ? 2 : 3) tree_combine_kernel(TreeMlaParams p) {
   constexpr int HEADS = 8 / PARTS;
   __shared__ float wgt[HEADS][kTreeCombMax];
   __shared__ float2 ml_sh[HEADS][kTreeCombMax];
@@ -1385,7 +1385,7 @@ __global__ void __launch_bounds__(kTreeCombThreads) tree_combine_kernel(TreeMlaP
   for (int i = threadIdx.x; i < n * HEADS; i += kTreeCombThreads)
     ml_sh[i % HEADS][i / HEADS] = __ldcg(p.part_ml + static_cast<int64_t>(slot(i / HEADS)) * kMlaHeads + h0 + i % HEADS);
   // the first partials are on their way meanwhile
-  constexpr int U = 8;
+  constexpr int U = PARTS > 1 ? 8 : 4;
   const uint4* src = reinterpret_cast<const uint4*>(p.part_o + static_cast<int64_t>(h0 + hh) * kVDim) + d8;
   auto load = [&](int j) {
     return j < n ? __ldcg(src + static_cast<int64_t>(slot(j)) * (kMlaHeads * kVDim / 8)) : make_uint4(0u, 0u, 0u, 0u);
