@@ -65,6 +65,21 @@ def test_mla_many_tiles_a_cta(fmt):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+def test_mla_same_bits_every_time(fmt):
+    # many CTAs at work on many segments, again and again: a copy that lands before the place it goes to
+    # has been read shows as a call whose bits differ
+    case = make_case([800, 600, 12000], [300, 380, 20], seed=77, lat_fmt=fmt)
+    d = DeviceTree(case)
+    out, lse = (x.clone() for x in d.mla())
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(100):
+        d.out.fill_(7.0)
+        d.mla()
+        differ += (d.out != out).sum() + (d.lse != lse).sum()
+    assert int(differ) == 0 and _check(d.ws) == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 def test_mla_masks_and_padding(fmt):
     # rows that see nothing, rows that see only others, bits behind the token, a padding token,
     # a committed length equal to the context (causal whatever the mask)
