@@ -803,7 +803,7 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
 // Bound by shared memory: the MMAs read 7 KB per 49 cycles (6.6K cycles a tile), the fills
 // write 16 KB each (1.7K), and packed rows and P add about 1K; a tile takes 12.2K, the
 // rest is the chain scores -> weights -> values, which four places cannot overlap fully.
-// 16 tokens over 256K: 1,290 us, 679 TFLOP/s.  Rows and scales loaded to registers by the
+// 16 tokens over 256K: 1,262 us, 694 TFLOP/s.  Rows and scales loaded to registers by the
 // threads that convert them: 1,470 us (spilled a tile ahead of use, each spill waited).
 namespace t16 {
 constexpr int THREADS = 448;
@@ -830,20 +830,25 @@ constexpr int SMEM_BYTES = OFF_MISC + 64 + 1024;
 // chunk and place of fill f: the scores' nine, then the values' four.  Dim block v of the
 // values is the chunks 2 v and 2 v + 1, one or three places apart: 4 and 5 in places 1
 // and 2, 6 and 7 in 0 and 3 (kept), then 0 and 1 in 1 and 2, 2 and 3 in 0 and 3.
-// The fills f of group f % 3 touch three chunks: 0, 8, 3; 1, 4, 7; 2, 5, 6.
-__device__ constexpr int kChunk[FILLS] = {0, 1, 2, 8, 4, 5, 3, 7, 6, 0, 1, 2, 3};
-__device__ constexpr int kPlace[FILLS] = {1, 2, 3, 0, 1, 2, 0, 3, 0, 1, 2, 0, 3};
-// the same for a fill known at run time (4 bits each)
-__device__ __forceinline__ int chunk_of_fill(int f) { return static_cast<int>((0x3210673548210ull >> (4 * f)) & 15); }
-__device__ __forceinline__ int place_of_fill(int f) { return static_cast<int>((0x3021030210321ull >> (4 * f)) & 15); }
+// The fills f of group f % 3 touch three chunks: 0, 3, 7; 1, 8, 5; 2, 4, 6.  Group 0 makes five
+// and is the last to start a tile, so the scores take the chunks in the order kOrder.
+__device__ constexpr int kChunk[FILLS] = {0, 1, 2, 3, 8, 4, 7, 5, 6, 0, 1, 2, 3};
+__device__ constexpr int kPlace[FILLS] = {3, 1, 2, 3, 0, 1, 3, 2, 0, 1, 2, 0, 3};
+__device__ constexpr int kOrder[9] = {1, 2, 0, 4, 5, 3, 7, 8, 6};
+// the same for a fill known at run time (4 bits each), and the order in which packed rows come:
+// the fill of turn o, and the turn of fill f
+__device__ __forceinline__ int chunk_of_fill(int f) { return static_cast<int>((0x3210657483210ull >> (4 * f)) & 15); }
+__device__ __forceinline__ int place_of_fill(int f) { return static_cast<int>((0x3021023103213ull >> (4 * f)) & 15); }
+__device__ __forceinline__ int fill_of_turn(int o) { return static_cast<int>((0xC9BA687354021ull >> (4 * o)) & 15); }
+__device__ __forceinline__ int turn_of_fill(int f) { return static_cast<int>((0xCA9B768435102ull >> (4 * f)) & 15); }
 // which of its group's three chunks a fill takes
-__device__ __forceinline__ int scale_of_fill(int f) { return f < 9 ? f / 3 : (f == 12 ? 2 : 0); }
-// events that free places: the scores of fill 0, 1, 2, 3 or 6 done, or the values of dim block v done
-enum { EV_S0 = 0, EV_S1, EV_S2, EV_S3, EV_S6, EV_V0, EV_V1, EV_V2, EV_V3, EVENTS };
+__device__ __forceinline__ int scale_of_fill(int f) { return f < 9 ? f / 3 : (f == 12 ? 1 : 0); }
+// events that free places: the scores of fill 0 .. 4 done, or the values of dim block v done
+enum { EV_S0 = 0, EV_S1, EV_S2, EV_S3, EV_S4, EV_V0, EV_V1, EV_V2, EV_V3, EVENTS };
 // the event that fill f waits for; bit 8: of the tile before
 __device__ __forceinline__ int event_of_fill(int f) {
-  return f < 2 ? (EV_V0 | 256) : f < 4 ? (EV_V1 | 256) : f < 6 ? EV_S0 + f - 4 : f == 6 ? EV_S3 : f == 7 ? EV_S2
-         : f == 8 ? EV_S6 : f < 11 ? EV_V2 : EV_V3;
+  return f == 0 || f == 4 ? (EV_V1 | 256) : f < 3 ? (EV_V0 | 256) : f == 3 ? EV_S0 : f == 5 ? EV_S1 : f == 6 ? EV_S3
+         : f == 7 ? EV_S2 : f == 8 ? EV_S4 : f < 11 ? EV_V2 : EV_V3;
 }
 constexpr int MATH_WARPS = 12;
 constexpr int MATH = MATH_WARPS * 32;
@@ -934,7 +939,7 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
     const int box = min(p.pool.bs, kSelTile);     // positions of one copy
     const int nbox = kSelTile / box;              // copies (lanes) per chunk
     bool ok = true;
-    int it = 0, q_issued = -1, f = 0;
+    int it = 0, q_issued = -1, o = 0;
     for (int seg = 0; ok && walk.next(s); ++seg) {
       const int pos = s.tok.pos;
       const int32_t* btrow = p.b.bt + static_cast<int64_t>(s.tok.req) * p.b.bt_stride;
@@ -965,14 +970,14 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
         const int next = i + 1 < s.n ? page(s.tile(i + 1)) : -1;
         if (i + 1 < s.n) prefetch(s.tile(i + 1), next);
 #pragma unroll 1
-        for (f = 0; f < FILLS; ++f) {
-          // the place of copy 13 it + f was last used four copies before
-          const int u = f < RAWS ? f + FILLS - RAWS : f - RAWS;
-          if (it > 0 || f >= RAWS) ok = warp_wait(&raw_done[u], (f < RAWS ? it - 1 : it) & 1, ab, ok);
+        for (o = 0; o < FILLS; ++o) {
+          // the place of copy 13 it + o was last used four copies before
+          const int f = fill_of_turn(o), u = fill_of_turn(o < RAWS ? o + FILLS - RAWS : o - RAWS);
+          if (it > 0 || o >= RAWS) ok = warp_wait(&raw_done[u], (o < RAWS ? it - 1 : it) & 1, ab, ok);
           if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(&raw_full[f], n * box * 32);
           __syncwarp();
-          const int place = (FILLS * it + f) % RAWS;
+          const int place = (FILLS * it + o) % RAWS;
           if (row >= 0)
             tma_load_3d(smem + OFF_RAW + place * RAW + lane * box * 32, &rmap, &raw_full[f], 32 * chunk_of_fill(f), c1, row);
         }
@@ -984,9 +989,9 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
     // was not issued in this round keeps its earlier phase; the wait is bounded)
     if (!ok && lane == 0) {
       if (q_issued >= 0) drain_wait(q_full, q_issued);
-      for (int i = 0; i < RAWS && i < FILLS * it + f; ++i) {   // the last copies issued
-        const int n = FILLS * it + f - 1 - i;
-        drain_wait(&raw_full[n % FILLS], (n / FILLS) & 1);
+      for (int i = 0; i < RAWS && i < FILLS * it + o; ++i) {   // the last copies issued
+        const int n = FILLS * it + o - 1 - i;
+        drain_wait(&raw_full[fill_of_turn(n % FILLS)], (n / FILLS) & 1);
       }
     }
   } else if (warp == MMA_WARP) {
@@ -1014,22 +1019,23 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
       if (seg == 0) load_query(s.t);
       ok = warp_wait(q_full, seg & 1, ab, ok);
       for (int i = 0; ok && i < s.n; ++i, ++it) {
-        ok = warp_wait(&full[0], it & 1, ab, ok);
+        ok = warp_wait(&full[kOrder[0]], it & 1, ab, ok);
         tc_fence_after();
 #pragma unroll
-        for (int f = 0; f < 9; ++f) {
+        for (int o = 0; o < 9; ++o) {
+          const int f = kOrder[o];
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             if (leader && ok) {
 #pragma unroll
               for (int kk = 2 * half; kk < 2 * half + 2; ++kk)
                 mma_f16(tmem + S_COL, dc + ((kPlace[f] * PLACE + 32 * kk) >> 4), dq + ((kChunk[f] * QCHUNK + 32 * kk) >> 4),
-                        idesc_qk, (f | kk) ? 1u : 0u);
-              if (half == 1 && (f < 4 || f == 6)) tc_commit(&event[f < 4 ? EV_S0 + f : EV_S6]);
+                        idesc_qk, (o | kk) ? 1u : 0u);
+              if (half == 1 && f < 5) tc_commit(&event[EV_S0 + f]);
             }
             __syncwarp();
-            if (half == 0 && f < 8) {   // the next chunk is awaited while the tensor core has work
-              ok = warp_wait(&full[f + 1], it & 1, ab, ok);
+            if (half == 0 && o < 8) {   // the next chunk is awaited while the tensor core has work
+              ok = warp_wait(&full[kOrder[o + 1]], it & 1, ab, ok);
               tc_fence_after();
             }
           }
@@ -1105,7 +1111,7 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
     const uint32_t never = static_cast<uint32_t>(p.whole) >> 8;
     auto fill = [&](int f, bool seen_row) {
       ok = warp_wait(&raw_full[f], it & 1, ab, ok);
-      const uint8_t* src = smem + OFF_RAW + (FILLS * it + f) % RAWS * RAW + crow * 32;
+      const uint8_t* src = smem + OFF_RAW + (FILLS * it + turn_of_fill(f)) % RAWS * RAW + crow * 32;
       const int sw = ((crow >> 2) & 1) << 4;
       const uint4 w0 = *reinterpret_cast<const uint4*>(src + sw), w1 = *reinterpret_cast<const uint4*>(src + (sw ^ 16));
       // The place is given back once the loads have returned, which an arrival behind them does not
