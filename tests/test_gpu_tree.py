@@ -101,6 +101,26 @@ def test_mla_masks_and_padding(fmt):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("flags", [0, 1])
+def test_mla_nothing_to_do(fmt, flags):
+    # a batch of padding alone: nothing is written, and the next call on the workspace is whole
+    import dsa_sparse_attention_gb300 as dsa
+    flags *= dsa.DSA_BATCH_INVARIANT
+    case = make_case([300, 40], [4, 3], seed=11, lat_fmt=fmt)
+    d = DeviceTree(case, flags=flags)
+    q_req = d.q_req.clone()
+    d.q_req.fill_(-1)
+    out, lse = d.mla()
+    torch.cuda.synchronize()
+    assert _check(d.ws) == 0 and (out == 7.0).all() and (lse == 7.0).all()
+    d.q_req.copy_(q_req)
+    out, lse = d.mla()
+    torch.cuda.synchronize()
+    assert _check(d.ws) == 0
+    check_mla(case, out, lse)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 def test_mla_garbage_in_unseen_places(fmt):
     # NaN codes at drafted positions a token does not see and behind the context's end
     case = make_case([200, 70], [9, 30], seed=21, lat_fmt=fmt)
