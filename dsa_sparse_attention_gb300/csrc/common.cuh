@@ -72,34 +72,6 @@ __device__ __forceinline__ void load_token(const BatchView& b, int t, uint32_t* 
   pos = p;
 }
 
-// Device view of the drafted tokens' tree (include/dsa.h, dsa_tree).
-struct TreeView {
-  const int32_t* base;    // [B] committed tokens
-  const uint32_t* mask;   // [T, words]
-  int32_t words;
-};
-
-// Request, position and committed length of drafted token t, clamped as load_token
-// does; false for a padding token (negative request).
-__device__ __forceinline__ bool load_tree_token(const BatchView& b, const TreeView& tr, int t, uint32_t* status,
-                                                int& req, int& pos, int& base) {
-  if (b.q_req[t] < 0) return false;
-  load_token(b, t, status, req, pos);
-  base = tr.base[req];
-  if (base < 0 || base > b.max_ctx) {
-    atomicOr(status, DEV_BAD_BATCH);
-    base = base < 0 ? 0 : b.max_ctx;
-  }
-  return true;
-}
-
-// Whether a token with mask row `row` sees position s of its request (s <= its own position).
-__device__ __forceinline__ bool tree_sees(const uint32_t* row, int words, int base, int s) {
-  if (s < base) return true;
-  const int d = s - base;
-  return (d >> 5) < words && ((__ldg(row + (d >> 5)) >> (d & 31)) & 1u);
-}
-
 // Order-preserving map of a float score to uint32 (larger float -> larger key);
 // -0.0 is folded onto +0.0 first so the two compare equal.
 __device__ __forceinline__ uint32_t score_key(float f) {

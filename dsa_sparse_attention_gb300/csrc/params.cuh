@@ -74,7 +74,6 @@ constexpr int kTopkClusterMaxRow = 65536;   // rows up to this long take the one
 // Decode batches of at most this many tokens, one per group, are planned inside
 // the scorer (no separate planning launch).
 constexpr int kDirectMaxT = 128;
-constexpr int kTreeTopkCap = 24576;   // entries per row the tree top-k resolves in shared memory (192 KB)
 constexpr int kTopkCap = 4096;     // candidates per row kept for the exact resolution
 
 // Byte offsets of the top-k scratch inside a region (256-byte aligned segments);
@@ -194,26 +193,6 @@ int indexer_group_size(int idx_fmt, bool one_token_per_request);
 // `zeroed`: the scratch [hist .. zero_end) was cleared on the stream already
 // (otherwise the launch clears it first).
 cudaError_t launch_topk(const TopkParams& p, cudaStream_t st, bool chained, bool zeroed = false);
-// The same over the positions that drafted tokens see in their trees (tree_topk.cu).
-struct TreeTopkParams {
-  BatchView b;
-  TreeView tree;
-  const float* scores;
-  int64_t ld;
-  int k;
-  int nchunks;          // chunks of kTopkChunk scores per row at max_ctx_len
-  uint2* list;          // [T, cap]       (key, position) at or above a row's bound
-  int cap;
-  uint32_t* bound;      // [T]
-  uint32_t* fill;       // [T]            entries listed (may exceed cap)
-  uint32_t* at;         // [T, nchunks]   where a chunk's entries start, and how many they are
-  uint32_t* num;        // [T, nchunks]
-  int32_t* idx;         // [T, k]
-  int32_t* phys;        // [T, k] or null
-  int log2_bs;
-  uint32_t* status;
-};
-cudaError_t launch_tree_topk(const TreeTopkParams& p, cudaStream_t st);
 cudaError_t launch_sparse_mla(const CUtensorMap& qmap, const CUtensorMap& cmap, const MlaParams& p, cudaStream_t st,
                               bool chained);
 // FP8 latents, one 128-token tile per CTA (p.nsplit = tiles of the selection, p.tps

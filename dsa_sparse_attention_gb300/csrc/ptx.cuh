@@ -23,16 +23,6 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
-// True in one lane of the (converged) warp.  A role that issues tensor-core work runs its
-// loop in the whole warp and issues under this predicate: descriptors then stay in
-// uniform registers, where a loop inside a one-lane branch moves each of them there per
-// instruction and issues slower than the tensor core runs.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r != 0;
-}
-
 // ------------------------------------------------- clusters and launch chaining
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -191,17 +181,6 @@ __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
-// Barrier over `nthreads` threads that also returns whether any of them passed a non-zero value.
-__device__ __forceinline__ bool named_bar_any(uint32_t id, uint32_t nthreads, bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(static_cast<uint32_t>(v)), "r"(id), "r"(nthreads)
-      : "memory");
-  return r != 0;
-}
-
 // ------------------------------------------------------------ TMA and bulk
 
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1) {
@@ -317,33 +296,6 @@ __device__ __forceinline__ void mma_f8f6f4(uint32_t d_tmem, uint64_t adesc, uint
       : "memory");
 }
 
-// As mma_f8f6f4, with A kept in the tensor core's operand buffer: the first of a run of
-// MMAs on one A fills it, the following ones use it (the last one hands it back), so A is
-// read from shared memory once.
-enum class KeepA { kFill, kUse, kLast };
-template <KeepA OP>
-__device__ __forceinline__ void mma_f8f6f4_keep_a(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                                  uint32_t accumulate) {
-  if (OP == KeepA::kFill)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f8f6f4.collector::a::fill "
-        "[%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-  else if (OP == KeepA::kUse)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f8f6f4.collector::a::use "
-        "[%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f8f6f4.collector::a::lastuse "
-        "[%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
 // D(tmem) (+)= sum over the 32-wide K blocks of SFA * SFB * (A_blk * B_blk): 8/6/4-bit
 // operands with UE8M0 block scales read from TMEM (kind::mxf8f6f4, one scale per
 // row and operand for the instruction's K = 32).  Scale layout, per operand: the
@@ -373,8 +325,7 @@ __device__ __forceinline__ void tmem_st1(uint32_t taddr, uint32_t v) {
 }
 
 // Instruction descriptor (kind::f16 / kind::f8f6f4, dense).  Formats:
-//   D: 1 = f32.  A/B for kind::f16: 0 = f16, 1 = bf16; for kind::f8f6f4: 0 = e4m3,
-//   1 = e5m2, 5 = e2m1.
+//   D: 1 = f32.  A/B for kind::f16: 0 = f16, 1 = bf16; for kind::f8f6f4: 0 = e4m3, 5 = e2m1.
 //   *_mn: operand is MN-major (else K-major).
 __host__ __device__ constexpr uint32_t make_idesc(uint32_t a_fmt, uint32_t b_fmt, bool a_mn, bool b_mn, uint32_t M,
                                                   uint32_t N) {
@@ -392,16 +343,6 @@ __device__ __forceinline__ uint64_t make_sdesc_sw128(uint32_t saddr, uint32_t lb
   d |= static_cast<uint64_t>(1) << 46;  // descriptor version for tcgen05
   d |= static_cast<uint64_t>(2) << 61;  // SWIZZLE_128B
   return d;
-}
-
-// The same with a 64-byte swizzle (rows of 64 bytes, 512-byte aligned atoms of 8 rows).
-__device__ __forceinline__ uint64_t make_sdesc_sw64(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  return (make_sdesc_sw128(saddr, lbo, sbo) & ~(static_cast<uint64_t>(7) << 61)) | (static_cast<uint64_t>(4) << 61);
-}
-
-// And with a 32-byte swizzle.
-__device__ __forceinline__ uint64_t make_sdesc_sw32(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  return (make_sdesc_sw128(saddr, lbo, sbo) & ~(static_cast<uint64_t>(7) << 61)) | (static_cast<uint64_t>(6) << 61);
 }
 
 // 32 lanes x 32 consecutive 32-bit columns: thread i of the warp gets lane
@@ -427,41 +368,10 @@ __device__ __forceinline__ uint64_t make_sdesc_sw32(uint32_t saddr, uint32_t lbo
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])                                                                  \
       : "memory")
 
-#define DSA_TMEM_LD16(taddr, r)                                                                                      \
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, "     \
-               "[%16];"                                                                                              \
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),      \
-                 "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),             \
-                 "=r"(r[15])                                                                                         \
-               : "r"(taddr)                                                                                          \
-               : "memory")
-#define DSA_TMEM_ST16(taddr, r)                                                                                      \
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"    \
-               "%16};" ::"r"(taddr),                                                                                 \
-               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),     \
-               "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])                      \
-               : "memory")
-
-// 16 lanes (from the address's lane) x 32 columns as blocks of 8 columns: thread l gets, of
-// block b, lane l / 4 columns 2 (l % 4) and + 1 in r[4b], r[4b + 1], lane l / 4 + 8 in r[4b + 2], r[4b + 3].
-#define DSA_TMEM_LD_16X256_X4(taddr, r)                                                                              \
-  asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, "    \
-               "[%16];"                                                                                              \
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),      \
-                 "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),             \
-                 "=r"(r[15])                                                                                         \
-               : "r"(taddr)                                                                                          \
-               : "memory")
-
 #define DSA_TMEM_LD8(taddr, r)                                                                                      \
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"                            \
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])      \
                : "r"(taddr)                                                                                         \
-               : "memory")
-
-#define DSA_TMEM_ST8(taddr, r)                                                                                      \
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),   \
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])                         \
                : "memory")
 
 // Prefetch `bytes` (a multiple of 16, 16-byte aligned) of global memory into L2.
@@ -471,15 +381,6 @@ __device__ __forceinline__ void bulk_prefetch_l2(const void* src, uint32_t bytes
 
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// Four 8 x 8 matrices of 16-bit values, transposed on the way into shared memory: thread l
-// holds of matrix i row l / 4, columns 2 (l % 4) and + 1 in r_i; column c of matrix i goes,
-// 16 contiguous bytes, to the address that lane 8 i + c passes.
-__device__ __forceinline__ void stmatrix_x4_trans(uint32_t saddr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
-  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(saddr), "r"(r0), "r"(r1),
-               "r"(r2), "r"(r3)
-               : "memory");
-}
 
 // Warp-wide max of a float (sm_100-family redux).
 __device__ __forceinline__ float warp_max_f32(float v) {

@@ -15,6 +15,7 @@
 
 #include "mla_conv.cuh"
 #include "mla_q.cuh"
+#include "ptx_tree.cuh"
 #include "tree_mla.cuh"
 
 namespace dsa {
@@ -455,7 +456,7 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
     // ------------------------------------------------------------ MMA issuer
     const bool leader = elect_one();
     const uint32_t idesc_qk = make_idesc(0, 0, false, false, 128, kMlaHeads);
-    const uint32_t idesc_pv = make_idesc(0, 1, true, true, 128, kMlaHeads);
+    const uint32_t idesc_pv = make_idesc(0, 1, true, true, 128, kMlaHeads);   // e4m3 x e5m2 (format 1)
     const uint64_t dq = make_sdesc_sw128(smem_u32(smem + OFF_Q), 16, 1024);        // query terms, K-major
     const uint64_t dl = make_sdesc_sw128(smem_u32(smem + OFF_LAT), 16, 1024);      // latents, K-major (QK)
     const uint64_t dt = make_sdesc_sw64(smem_u32(smem + OFF_TAIL), 16, 512);       // their last 64 dims

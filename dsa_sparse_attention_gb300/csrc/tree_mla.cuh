@@ -1,7 +1,7 @@
 // tree_mla.cuh — parameters, work partition and launchers of the dense attention of
 // drafted tokens (tree_mla.cu).
 #pragma once
-#include "params.cuh"
+#include "tree.cuh"
 
 namespace dsa {
 

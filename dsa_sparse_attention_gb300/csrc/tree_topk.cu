@@ -21,7 +21,7 @@
 // Bound by latency: 48 rows of 64K take 15.7 us, 16 rows of 1M 35 us, when reading the scores
 // alone would take 1.9 and 9.9 us; the launches overlap as far as their waits allow, and data that
 // another SM has just written takes 0.8 us to read.
-#include "params.cuh"
+#include "tree.cuh"
 
 namespace dsa {
 
