@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
       }
     }
     // after a failed wait: no copy into shared memory outlives the CTA (a barrier whose copy
-    // was not issued in this round keeps its earlier phase; the wait is bounded)
+    // was not issued for this tile keeps its earlier phase; the wait is bounded)
     if (!ok && lane == 0) {
       if (q_issued >= 0) drain_wait(q_full, q_issued);
       drain_wait(tail_full, it & 1);
@@ -988,7 +988,7 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
       }
     }
     // after a failed wait: no copy into shared memory outlives the CTA (a barrier whose copy
-    // was not issued in this round keeps its earlier phase; the wait is bounded)
+    // was not issued for this tile keeps its earlier phase; the wait is bounded)
     if (!ok && lane == 0) {
       if (q_issued >= 0) drain_wait(q_full, q_issued);
       for (int i = 0; i < RAWS && i < FILLS * it + o; ++i) {   // the last copies issued

@@ -482,7 +482,7 @@ def test_topk_unseen_scores_and_ties(base):
 @pytest.mark.parametrize("base", [3000, 20000, 100000])
 @pytest.mark.parametrize("shape", ["equal", "two", "falling", "rising", "lowest", "heavy"])
 def test_topk_distributions(base, shape):
-    # scores that a sampled bound judges badly: all equal, two values, sorted rows, infinities,
+    # scores that a sampled bound serves badly: all equal, two values, sorted rows, infinities,
     # a few large ones in one place
     case, scores = _topk_case([base], [6], seed=8)
     n = scores.shape[1]
