@@ -18,7 +18,7 @@
 // many (more equal scores than the list holds) is resolved over the whole row, exactly
 // and slowly.  No sum depends on an order of arrival: results are deterministic and
 // independent of the rest of the batch.
-// Bound by latency: 48 rows of 64K take 15.7 us, 16 rows of 1M 35 us, when reading the scores
+// Bound by latency: 48 rows of 64K take 15.4 us, 16 rows of 1M 35 us, when reading the scores
 // alone would take 1.9 and 9.9 us; the launches overlap as far as their waits allow, and data that
 // another SM has just written takes 0.8 us to read.
 #include "tree.cuh"
@@ -33,6 +33,7 @@ constexpr int kPer = 16;                 // scores per thread and chunk
 static_assert(kFilterThreads * kPer == kTopkChunk, "chunk");
 constexpr int kRowThreads = 1024;
 constexpr int kSamples = 4096;
+constexpr int kDigit = 14;               // bits below the digit that the listed entries are counted by
 constexpr int kDirect = 16384;           // rows of at most this many scores skip steps 1 and 2
 
 // A row: n positions, `base` of them committed, `seen` seen by the token.
@@ -364,31 +365,17 @@ __device__ __forceinline__ void each_score(const TreeTopkParams& p, const Row& r
   }
 }
 
-// The k-th best of n listed entries (equal keys: the lower position first) as (T, cut),
-// when one digit leaves few enough of them to compare each with each: the entries of the
-// digit's bin are listed, and the one that needs k - above - 1 others before it is it.
-// False (nothing decided) when the bin holds more.  lo, hi: the thread's part in the smallest
-// (at most) and the largest key; the entries have been written, no barrier since.
+// The k-th best of n listed entries (equal keys: the lower position first) as (T, cut), from their
+// counts by the digit min((key - lo) >> shift, kBins - 1) in S.h, when its bin holds few enough
+// of them to compare each with each: the bin's entries are listed, and the one that needs
+// k - above - 1 others before it is it.  False (nothing decided) when the bin holds more.
 constexpr int kPairs = kBins / 2;   // pairs that fit the histogram's place
-__device__ __forceinline__ bool select_listed(RowShared& S, const uint2* ent, uint32_t n, uint32_t lo, uint32_t hi,
-                                              uint32_t k, uint32_t& T, uint32_t& cut) {
-  const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
-  lo = __reduce_min_sync(0xffffffffu, lo);
-  hi = __reduce_max_sync(0xffffffffu, hi);
-  if (lane == 0) {
-    S.wsh[0][warp] = lo;
-    S.wsh[1][warp] = hi;
-  }
-  for (int i = tid; i < kBins; i += kRowThreads) S.h[i] = 0;
-  __syncthreads();
-  lo = __reduce_min_sync(0xffffffffu, S.wsh[0][lane]);
-  hi = __reduce_max_sync(0xffffffffu, S.wsh[1][lane]);
-  const int shift = max(32 - __clz(hi - lo) - 11, 0);
-  for (uint32_t i = tid; i < n; i += kRowThreads) {
-    const uint32_t key = ent[i].x;
-    if (key) atomicAdd(&S.h[(key - lo) >> shift], 1u);
-  }
-  __syncthreads();
+__device__ __forceinline__ uint32_t digit_of(uint32_t key, uint32_t lo, int shift) {
+  return min((key - lo) >> shift, static_cast<uint32_t>(kBins - 1));
+}
+__device__ __forceinline__ bool resolve_digit(RowShared& S, const uint2* ent, uint32_t n, uint32_t lo, int shift, uint32_t k,
+                                              uint32_t& T, uint32_t& cut) {
+  const int tid = static_cast<int>(threadIdx.x);
   const uint2 f = find_digit(S, kBins, k, 2);
   const uint32_t count = S.h[f.x], need = k - f.y;
   __syncthreads();
@@ -398,7 +385,7 @@ __device__ __forceinline__ bool select_listed(RowShared& S, const uint2* ent, ui
   __syncthreads();
   for (uint32_t i = tid; i < n; i += kRowThreads) {
     const uint2 e = ent[i];
-    if (e.x && ((e.x - lo) >> shift) == f.x) bin[atomicAdd(&S.res[0], 1u)] = e;
+    if (e.x && digit_of(e.x, lo, shift) == f.x) bin[atomicAdd(&S.res[0], 1u)] = e;
   }
   __syncthreads();
   for (uint32_t i = tid; i < count; i += kRowThreads) {
@@ -419,9 +406,34 @@ __device__ __forceinline__ bool select_listed(RowShared& S, const uint2* ent, ui
   return true;
 }
 
+// The same with the digit chosen by the entries' extremes.  lo, hi: the thread's part in the
+// smallest (at most) and the largest key; the entries have been written, no barrier since.
+__device__ __forceinline__ bool select_listed(RowShared& S, const uint2* ent, uint32_t n, uint32_t lo, uint32_t hi,
+                                              uint32_t k, uint32_t& T, uint32_t& cut) {
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (lane == 0) {
+    S.wsh[0][warp] = lo;
+    S.wsh[1][warp] = hi;
+  }
+  for (int i = tid; i < kBins; i += kRowThreads) S.h[i] = 0;
+  __syncthreads();
+  lo = __reduce_min_sync(0xffffffffu, S.wsh[0][lane]);
+  hi = __reduce_max_sync(0xffffffffu, S.wsh[1][lane]);
+  const int shift = max(32 - __clz(hi - lo) - 11, 0);
+  for (uint32_t i = tid; i < n; i += kRowThreads) {
+    const uint32_t key = ent[i].x;
+    if (key) atomicAdd(&S.h[digit_of(key, lo, shift)], 1u);
+  }
+  __syncthreads();
+  return resolve_digit(S, ent, n, lo, shift, k, T, cut);
+}
+
 __global__ void __launch_bounds__(kRowThreads) tree_topk_select_kernel(TreeTopkParams p) {
   extern __shared__ __align__(16) uint2 ent[];   // [kTreeTopkCap]
   __shared__ RowShared S;
+  __shared__ uint32_t moved[kRowThreads];        // where a chunk's entries go, less where they are
   const int t = blockIdx.x;
   const int tid = static_cast<int>(threadIdx.x);
   Row r;
@@ -461,12 +473,15 @@ __global__ void __launch_bounds__(kRowThreads) tree_topk_select_kernel(TreeTopkP
     // of chunk c belongs at (entries of the chunks before) + i - at[c].  Counts, places and the
     // first entries are read at once, before it is known how many entries there are (up to the
     // list's capacity they are the workspace's): one round trip to memory, not three.
+    // Their first digit is counted on the way: the k-th lies close above the bound, mostly within the
+    // 2^25 keys (four octaves) that kDigit divides; the last bin counts what lies beyond.
     constexpr int kAhead = 8;
     const int nch = static_cast<int>(cdiv(r.n, kTopkChunk));
     const uint2* list = p.list + static_cast<int64_t>(t) * p.cap;
     const uint32_t* at = p.at + static_cast<int64_t>(t) * p.nchunks;
     const uint32_t* num = p.num + static_cast<int64_t>(t) * p.nchunks;
     uint2 e[kAhead];
+    for (int i = tid; i < kBins; i += kRowThreads) S.h[i] = 0;
 #pragma unroll
     for (int q = 0; q < kAhead; ++q) {
       const int i = tid + q * kRowThreads;
@@ -484,14 +499,15 @@ __global__ void __launch_bounds__(kRowThreads) tree_topk_select_kernel(TreeTopkP
           ca = c0 + tid < nch ? __ldcg(at + c0 + tid) : 0u;
         }
         uint32_t total;
-        S.h[tid] = before + scan(cn, S.wsh[0], total) - ca;   // (wraps; the sum with i does not)
+        moved[tid] = before + scan(cn, S.wsh[0], total) - ca;   // (wraps; the sum with i does not)
         before += total;
         __syncthreads();
         auto place = [&](uint32_t i, uint2 x) {
           const uint32_t c = x.y / kTopkChunk - static_cast<uint32_t>(c0);
           if (i >= n || c >= static_cast<uint32_t>(kRowThreads)) return;
-          ent[S.h[c] + i] = x;
+          ent[moved[c] + i] = x;
           hi = max(hi, x.x);
+          atomicAdd(&S.h[digit_of(x.x, lo, kDigit)], 1u);
         };
 #pragma unroll
         for (int q = 0; q < kAhead; ++q) place(tid + q * kRowThreads, e[q]);
@@ -511,7 +527,8 @@ __global__ void __launch_bounds__(kRowThreads) tree_topk_select_kernel(TreeTopkP
   };
   // the threshold key T, and of the keys equal to it those at positions <= cut
   uint32_t T, cut = 0xFFFFFFFFu;
-  if (!listed || !select_listed(S, ent, n, lo, hi, k, T, cut)) {
+  const bool counted = filtered(p, r);   // the entries' digits are in S.h
+  if (!listed || !((counted && resolve_digit(S, ent, n, lo, kDigit, k, T, cut)) || select_listed(S, ent, n, lo, hi, k, T, cut))) {
     uint32_t above, equal;
     T = select_value(S, keys, k, 0, above, equal);
     const uint32_t need = k - above;
