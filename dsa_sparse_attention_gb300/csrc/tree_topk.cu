@@ -10,10 +10,11 @@
 //             probability below 1e-6, and typically 1.6 k (64K scores) to 4 k (1M) do.
 //  2. filter: one CTA per 4,096 scores lists its scores at or above the bound, in
 //             position order, and notes where its entries lie.
-//  3. select: one CTA per row puts the entries in position order into shared memory, finds the k-th by one digit and comparisons within its bin
-//             (by digits down to the last bit where the bin is crowded; equal keys by lower
-//             position), and writes the selection with one scan.
-// Rows of at most 16,384 scores go to step 3 directly.  Steps 1 and 2 only choose what
+//  3. select: one CTA per row puts the entries in position order into shared memory, finds
+//             the k-th by one digit and comparisons within its bin (by digits down to the
+//             last bit where the bin is crowded; equal keys by lower position), and writes
+//             the selection with one scan.
+// Rows of at most 14,336 scores go to step 3 directly.  Steps 1 and 2 only choose what
 // step 3 looks at: it counts the entries, and a row whose entries are too few or too
 // many (more equal scores than the list holds) is resolved over the whole row, exactly
 // and slowly.  No sum depends on an order of arrival: results are deterministic and
@@ -33,8 +34,9 @@ constexpr int kPer = 16;                 // scores per thread and chunk
 static_assert(kFilterThreads * kPer == kTopkChunk, "chunk");
 constexpr int kRowThreads = 1024;
 constexpr int kSamples = 4096;
-constexpr int kDigit = 14;               // bits below the digit that the listed entries are counted by
-constexpr int kDirect = 16384;           // rows of at most this many scores skip steps 1 and 2
+// Rows of at most this many scores skip steps 1 and 2: 48 rows of 6,000 / 8,100 / 12,000 / 16,300 take
+// 8.0 / 9.8 / 12.1 / 14.3 us so, 12.6 / 12.6 / 13.1 / 13.1 us with them.
+constexpr int kDirect = 14336;
 
 // A row: n positions, `base` of them committed, `seen` seen by the token.
 struct Row {
@@ -61,6 +63,11 @@ __device__ __forceinline__ bool load_row(const TreeTopkParams& p, int t, Row& r)
 // Steps 1 and 2 take part.
 __device__ __forceinline__ bool filtered(const TreeTopkParams& p, const Row& r) {
   return r.seen > p.k && r.n > kDirect;
+}
+
+// The score of a key (score_key's inverse).
+__device__ __forceinline__ float score_of_key(uint32_t key) {
+  return __uint_as_float((key & 0x80000000u) ? key & 0x7FFFFFFFu : ~key);
 }
 
 // Key of position s, 0 (below every score's key) where the token does not see it.
@@ -365,15 +372,28 @@ __device__ __forceinline__ void each_score(const TreeTopkParams& p, const Row& r
   }
 }
 
+// A digit of a key, one that does not fall as the key grows: by the key's bits, or by its score.
+struct KeyDigit {   // of entries close above `lo`: 2^14 keys each, the last digit for all beyond
+  uint32_t lo;
+  __device__ uint32_t operator()(uint32_t key) const {
+    return min((key - lo) >> 14, static_cast<uint32_t>(kBins - 1));
+  }
+};
+struct ScoreDigit {   // of a whole row: equal steps between its smallest and largest score
+  float lo, scale;
+  __device__ uint32_t operator()(uint32_t key) const {
+    const float x = (score_of_key(key) - lo) * scale;   // (rounded, but never falling)
+    return min(static_cast<uint32_t>(max(x, 0.f)), static_cast<uint32_t>(kBins - 1));   // NaN: digit 0
+  }
+};
+
 // The k-th best of n listed entries (equal keys: the lower position first) as (T, cut), from their
-// counts by the digit min((key - lo) >> shift, kBins - 1) in S.h, when its bin holds few enough
-// of them to compare each with each: the bin's entries are listed, and the one that needs
-// k - above - 1 others before it is it.  False (nothing decided) when the bin holds more.
+// counts by digit in S.h, when the k-th's bin holds few enough of them to compare each with each:
+// the bin's entries are listed, and the one that needs k - above - 1 others before it is it.
+// False (nothing decided) when the bin holds more.
 constexpr int kPairs = kBins / 2;   // pairs that fit the histogram's place
-__device__ __forceinline__ uint32_t digit_of(uint32_t key, uint32_t lo, int shift) {
-  return min((key - lo) >> shift, static_cast<uint32_t>(kBins - 1));
-}
-__device__ __forceinline__ bool resolve_digit(RowShared& S, const uint2* ent, uint32_t n, uint32_t lo, int shift, uint32_t k,
+template <typename Digit>
+__device__ __forceinline__ bool resolve_digit(RowShared& S, const uint2* ent, uint32_t n, Digit digit, uint32_t k,
                                               uint32_t& T, uint32_t& cut) {
   const int tid = static_cast<int>(threadIdx.x);
   const uint2 f = find_digit(S, kBins, k, 2);
@@ -385,7 +405,7 @@ __device__ __forceinline__ bool resolve_digit(RowShared& S, const uint2* ent, ui
   __syncthreads();
   for (uint32_t i = tid; i < n; i += kRowThreads) {
     const uint2 e = ent[i];
-    if (e.x && digit_of(e.x, lo, shift) == f.x) bin[atomicAdd(&S.res[0], 1u)] = e;
+    if (e.x && digit(e.x) == f.x) bin[atomicAdd(&S.res[0], 1u)] = e;
   }
   __syncthreads();
   for (uint32_t i = tid; i < count; i += kRowThreads) {
@@ -406,7 +426,7 @@ __device__ __forceinline__ bool resolve_digit(RowShared& S, const uint2* ent, ui
   return true;
 }
 
-// The same with the digit chosen by the entries' extremes.  lo, hi: the thread's part in the
+// The same for a row whose digits have not been counted.  lo, hi: the thread's part in the
 // smallest (at most) and the largest key; the entries have been written, no barrier since.
 __device__ __forceinline__ bool select_listed(RowShared& S, const uint2* ent, uint32_t n, uint32_t lo, uint32_t hi,
                                               uint32_t k, uint32_t& T, uint32_t& cut) {
@@ -419,15 +439,15 @@ __device__ __forceinline__ bool select_listed(RowShared& S, const uint2* ent, ui
   }
   for (int i = tid; i < kBins; i += kRowThreads) S.h[i] = 0;
   __syncthreads();
-  lo = __reduce_min_sync(0xffffffffu, S.wsh[0][lane]);
-  hi = __reduce_max_sync(0xffffffffu, S.wsh[1][lane]);
-  const int shift = max(32 - __clz(hi - lo) - 11, 0);
+  const float flo = score_of_key(__reduce_min_sync(0xffffffffu, S.wsh[0][lane]));
+  const float fhi = score_of_key(__reduce_max_sync(0xffffffffu, S.wsh[1][lane]));
+  const ScoreDigit digit = {flo, static_cast<float>(kBins) / (fhi - flo)};
   for (uint32_t i = tid; i < n; i += kRowThreads) {
     const uint32_t key = ent[i].x;
-    if (key) atomicAdd(&S.h[digit_of(key, lo, shift)], 1u);
+    if (key) atomicAdd(&S.h[digit(key)], 1u);
   }
   __syncthreads();
-  return resolve_digit(S, ent, n, lo, shift, k, T, cut);
+  return resolve_digit(S, ent, n, digit, k, T, cut);
 }
 
 __global__ void __launch_bounds__(kRowThreads) tree_topk_select_kernel(TreeTopkParams p) {
@@ -474,7 +494,7 @@ __global__ void __launch_bounds__(kRowThreads) tree_topk_select_kernel(TreeTopkP
     // first entries are read at once, before it is known how many entries there are (up to the
     // list's capacity they are the workspace's): one round trip to memory, not three.
     // Their first digit is counted on the way: the k-th lies close above the bound, mostly within the
-    // 2^25 keys (four octaves) that kDigit divides; the last bin counts what lies beyond.
+    // 2^25 keys (four octaves) that the digits divide; the last bin counts what lies beyond.
     constexpr int kAhead = 8;
     const int nch = static_cast<int>(cdiv(r.n, kTopkChunk));
     const uint2* list = p.list + static_cast<int64_t>(t) * p.cap;
@@ -507,7 +527,7 @@ __global__ void __launch_bounds__(kRowThreads) tree_topk_select_kernel(TreeTopkP
           if (i >= n || c >= static_cast<uint32_t>(kRowThreads)) return;
           ent[moved[c] + i] = x;
           hi = max(hi, x.x);
-          atomicAdd(&S.h[digit_of(x.x, lo, kDigit)], 1u);
+          atomicAdd(&S.h[KeyDigit{lo}(x.x)], 1u);
         };
 #pragma unroll
         for (int q = 0; q < kAhead; ++q) place(tid + q * kRowThreads, e[q]);
@@ -528,7 +548,7 @@ __global__ void __launch_bounds__(kRowThreads) tree_topk_select_kernel(TreeTopkP
   // the threshold key T, and of the keys equal to it those at positions <= cut
   uint32_t T, cut = 0xFFFFFFFFu;
   const bool counted = filtered(p, r);   // the entries' digits are in S.h
-  if (!listed || !((counted && resolve_digit(S, ent, n, lo, kDigit, k, T, cut)) || select_listed(S, ent, n, lo, hi, k, T, cut))) {
+  if (!listed || !((counted && resolve_digit(S, ent, n, KeyDigit{lo}, k, T, cut)) || select_listed(S, ent, n, lo, hi, k, T, cut))) {
     uint32_t above, equal;
     T = select_value(S, keys, k, 0, above, equal);
     const uint32_t need = k - above;

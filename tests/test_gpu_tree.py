@@ -462,6 +462,24 @@ def test_topk_long_rows(bases, bs):
     _check_topk(case, scores, 2048, idx, ph)
 
 
+@pytest.mark.parametrize("base", [4090, 14330, 16380, 40000])
+@pytest.mark.parametrize("shape", ["normal", "outlier", "tiny", "huge", "tail"])
+def test_topk_around_the_rules(base, shape):
+    # rows around the length where the sampled bound sets in, scores whose spread the digits handle badly
+    case, scores = _topk_case([base, base + 3], [9, 20], seed=base)
+    if shape == "outlier":
+        scores[:, 77] = np.float32(3e38)
+        scores[:, 99] = np.float32(-3e38)
+    elif shape == "tiny":
+        scores *= np.float32(1e-42)              # subnormal, few distinct values
+    elif shape == "huge":
+        scores *= np.float32(1e38)
+    elif shape == "tail":
+        scores = np.exp(3 * np.abs(scores)).astype(np.float32)
+    idx, ph = _topk(case, scores, 2048, phys=True)
+    _check_topk(case, scores, 2048, idx, ph)
+
+
 @pytest.mark.parametrize("base", [5000, 70000])
 def test_topk_unseen_scores_and_ties(base):
     # NaN, infinities and the best scores at unseen positions; thousands of equal scores
