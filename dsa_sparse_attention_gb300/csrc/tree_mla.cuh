@@ -115,10 +115,15 @@ struct SegmentWalk {
   }
 };
 
-__host__ __device__ inline int64_t share_begin(int64_t W, int G, int c) { return W * c / G; }
+// (A division of 64 bits takes some hundred instructions: done only where 32 do not hold it.)
+__host__ __device__ inline int64_t share_begin(int64_t W, int G, int c) {
+  const int64_t x = W * c;
+  return x >> 32 ? x / G : static_cast<uint32_t>(x) / static_cast<uint32_t>(G);
+}
 // The CTA whose share holds tile u.
 __host__ __device__ inline int share_of(int64_t W, int G, int64_t u) {
-  return static_cast<int>(((u + 1) * G - 1) / W);
+  const int64_t x = (u + 1) * G - 1;
+  return static_cast<int>((x | W) >> 32 ? x / W : static_cast<uint32_t>(x) / static_cast<uint32_t>(W));
 }
 
 // The plan, and the queries as attention operands: `terms` (FP8 latents), or `q16` and `exps`
