@@ -55,7 +55,8 @@ __global__ void __launch_bounds__(kCopyThreads) cache_copy_kernel(CacheCopyParam
     n = c < n ? (c < 0 ? 0 : c) : n;
   }
   for (int64_t u = blockIdx.x; u < n * per_row; u += gridDim.x) {
-    const int64_t i = u / per_row;
+    // (32 bits divide in a tenth of the instructions)
+    const int64_t i = u >> 32 ? u / per_row : static_cast<uint32_t>(u) / static_cast<uint32_t>(per_row);
     const int64_t off = (u - i * per_row) * kCopyUnit;
     const int32_t s = __ldcg(p.src + i), d = __ldcg(p.dst + i);
     if (s < 0 && d < 0) continue;
@@ -293,10 +294,9 @@ __global__ void __launch_bounds__(kPlanThreads) cache_fork_plan_kernel(ForkParam
   __threadfence();
   cluster_sync();   // so is the plan
   // (a parent is no child of this call, so its table row and length are not written here)
-  const int64_t entries = static_cast<int64_t>(p.n) * p.bt_stride;
-  for (int64_t x = static_cast<int64_t>(rank) * kPlanThreads + tid; x < entries;
-       x += static_cast<int64_t>(cluster_size()) * kPlanThreads) {
-    const int i = static_cast<int>(x / p.bt_stride), e = static_cast<int>(x - static_cast<int64_t>(i) * p.bt_stride);
+  const uint32_t stride = static_cast<uint32_t>(p.bt_stride), entries = p.n * stride;   // few: apply_here
+  for (uint32_t x = rank * kPlanThreads + tid; x < entries; x += cluster_size() * kPlanThreads) {
+    const int i = static_cast<int>(x / stride), e = static_cast<int>(x % stride);
     const int32_t row = small ? fs.plan[i] : __ldcg(p.plan + i);
     if (row == kForkSkip) continue;
     const int32_t a = __ldcg(p.parent + i), c = __ldcg(p.child + i);
