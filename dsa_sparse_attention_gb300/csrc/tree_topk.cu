@@ -118,7 +118,8 @@ struct RowShared {
 };
 
 // One digit: counts (in S.h, `nb` bins of ascending value) to the bin holding the kk-th
-// largest and the number above it.  Every thread of a row CTA.
+// largest and the number above it.  The bins count kk values at least, so one of them
+// holds it.  Every thread of a row CTA.
 __device__ __forceinline__ uint2 find_digit(RowShared& S, int nb, uint32_t kk, int slot) {
   const int per = nb / kRowThreads;                           // 2 or 1
   const int hi = nb - static_cast<int>(threadIdx.x) * per;    // this thread's bins, from the top
@@ -140,10 +141,11 @@ __device__ __forceinline__ uint2 find_digit(RowShared& S, int nb, uint32_t kk, i
 }
 
 // The kk-th largest (1-based) of the values that `each` hands out (the same ones every
-// time, at least kk), exact down to bit `low`, and the number above it.  Digits of 11 bits
-// are taken of the difference to the smallest value, from its highest set bit down: the
-// scores that matter share their leading bits, and a histogram of those would send most
-// lanes of a warp to the same few counters.  `equal`: values that share all digits taken.
+// time), exact down to bit `low`, and the number above it; 0 when there are fewer than kk,
+// which no bin would hold.  Digits of 11 bits are taken of the difference to the smallest
+// value, from its highest set bit down: the scores that matter share their leading bits, and
+// a histogram of those would send most lanes of a warp to the same few counters.  `equal`:
+// values that share all digits taken.
 template <typename Each>
 __device__ __forceinline__ uint32_t select_value(RowShared& S, Each each, uint32_t kk, int low, uint32_t& above,
                                                  uint32_t& equal) {
@@ -167,6 +169,7 @@ __device__ __forceinline__ uint32_t select_value(RowShared& S, Each each, uint32
   hi = __reduce_max_sync(0xffffffffu, S.wsh[1][lane]);
   equal = __reduce_add_sync(0xffffffffu, S.wsh[2][lane]);
   above = 0;
+  if (equal < kk) return 0u;   // uniform
   uint32_t prefix = 0, mask = 0;
   int top = 32 - __clz(hi - lo);   // bits of the difference still open
   int slot = 3;
@@ -227,7 +230,7 @@ __global__ void __launch_bounds__(kRowThreads) tree_topk_bound_kernel(TreeTopkPa
   uint32_t u[kMine], most = 0;
 #pragma unroll
   for (int i = 0; i < kMine; ++i) {
-    u[i] = seen_key(p, r, at[i], v[i]);   // (a filtered row's samples are nearly all seen)
+    u[i] = seen_key(p, r, at[i], v[i]);   // (few of them are seen where a token far behind its base has a narrow mask)
     most = max(most, u[i]);
   }
   const float m = static_cast<float>(kSamples) * static_cast<float>(p.k) / static_cast<float>(r.n);
@@ -265,7 +268,9 @@ __global__ void __launch_bounds__(kRowThreads) tree_topk_bound_kernel(TreeTopkPa
         },
         rank, 10, above, equal);
   }
-  if (threadIdx.x == 0) p.bound[t] = max(bound, 1u);   // positions not seen have key 0
+  // Positions not seen have key 0.  With fewer samples seen than `rank` the bound is 1 and everything
+  // seen is listed, which is then little: about `rank` of the row's 4,096 stretches.
+  if (threadIdx.x == 0) p.bound[t] = max(bound, 1u);
 }
 static_assert(kTreeTopkCap <= 32 * kRowThreads, "rounds of the ordered output");
 static_assert(kDirect >= kSamples && kTreeTopkCap >= kDirect, "a stretch of scores per sample; a direct row fits");

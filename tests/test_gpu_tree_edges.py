@@ -1,0 +1,92 @@
+"""Trees of drafted tokens where tests at ordinary sizes do not look."""
+import numpy as np
+import pytest
+import torch
+
+from dsa_sparse_attention_gb300 import workloads as W
+from tests.test_gpu_tree import _check, _check_topk, _topk, _topk_case
+from tests.tree_cases import DeviceTree, check_mla, make_case
+
+FMTS = [W.LAT_FP8, W.LAT_NVFP4]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from dsa_sparse_attention_gb300.build import build
+    build()
+
+
+# --------------------------------------------------------------- few seen positions
+
+def _samples_seen(n, base, bits, samples=4096):
+    """How many of the top-k's sampled positions (one of each of as many equal stretches, at a place
+    hashed from its number) a token at position n - 1 sees."""
+    q = np.arange(samples, dtype=np.uint64)
+    a, b = n * q // samples, n * (q + 1) // samples
+    h = (q * 2654435761) & 0xFFFFFFFF
+    h ^= h >> 15
+    at = a + h % (b - a)
+    d = at.astype(np.int64) - base
+    return int(np.sum((d < 0) | np.isin(d, np.flatnonzero(bits))))
+
+
+def _rank(n, k, samples=4096):
+    m = np.float32(samples) * np.float32(k) / np.float32(n)
+    return min(int(m + np.float32(6) * np.sqrt(m)) + 8, samples)
+
+
+# positions of the context, committed, k, mask words, and whether fewer samples are seen than the bound's rank
+# where that is taken from all samples (it is above the 256 groups')
+FEW = [(20000, 2100, 2048, 1, True), (19996, 1100, 1024, 1, True), (16000, 0, 900, 32, True), (15000, 300, 1200, 32, True),
+       (40000, 2060, 2048, 2, True), (60000, 2100, 2048, 1, False), (200000, 2100, 2048, 1, False),
+       (30000, 1, 20, 1, False)]
+
+
+def _few_case(n, base, k, words, tokens=4):
+    rng = np.random.default_rng(n + base)
+    case, scores = _topk_case([n - tokens], [tokens], seed=n, words=words)
+    case.base[0] = base
+    bits = rng.random((tokens, words * 32)) < 0.97
+    bits[:, 0] = True
+    case.mask[:] = np.packbits(bits, axis=1, bitorder="little").view(np.uint32)
+    unseen = np.ones(scores.shape, bool)
+    for t in range(tokens):
+        unseen[t, case.seen(t)] = False
+    scores[unseen] = np.where(rng.random(int(unseen.sum())) < 0.5, np.float32(np.nan), np.float32(9.0))
+    return case, scores, bits
+
+
+def test_few_seen_cases_are_what_they_say():
+    # (no GPU) the cases do have more positions seen than k, and fewer samples seen than the rank where they say so
+    for n, base, k, words, fewer in FEW:
+        case, _, bits = _few_case(n, base, k, words)
+        for t in range(4):
+            pos = int(case.wl.q_pos[t])
+            assert case.seen(t).size > k
+            rank = _rank(pos + 1, k)
+            assert (rank > 256 and _samples_seen(pos + 1, base, bits[t]) < rank) == fewer
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,base,k,words,fewer", FEW)
+def test_topk_few_seen_on_long_rows(n, base, k, words, fewer):
+    # a small committed context, a narrow mask and a position far behind both: most of the row is not
+    # seen, and what lies there, NaN and larger scores, is not compared
+    case, scores, _ = _few_case(n, base, k, words)
+    idx, ph = _topk(case, scores, k, phys=True)
+    _check_topk(case, scores, k, idx, ph)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", FMTS)
+def test_mla_few_seen_in_a_long_context(fmt):
+    # whole tiles that nobody sees between the committed context and the token
+    case = make_case([4990, 3000], [4, 2], seed=303, lat_fmt=fmt)
+    case.base[:] = [300, 0]
+    case.mask[:4, 0] = [0xFFFFFFFF, 0x80000001, 0, 0x00F0F0F0]
+    case.mask[4:, 0] = [0x80000000, 0]          # one position of 3,000; nothing
+    d = DeviceTree(case)
+    out, lse = d.mla()
+    torch.cuda.synchronize()
+    assert _check(d.ws) == 0
+    check_mla(case, out, lse)
