@@ -1452,7 +1452,7 @@ __global__ void __launch_bounds__(kTreeCombThreads, PARTS > 1 ? 2 : 3) tree_comb
       for (int e = 0; e < 8; ++e) acc[e] += acc_sh[q][hh][d8][e];
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
-  __nv_bfloat162 o[4];
+  alignas(16) __nv_bfloat162 o[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) o[e] = __floats2bfloat162_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
   const int64_t row = static_cast<int64_t>(t) * kMlaHeads + h0 + hh;

@@ -22,6 +22,8 @@
 // Bound by latency: 48 rows of 64K take 15.4 us, 16 rows of 1M 35 us, when reading the scores
 // alone would take 1.9 and 9.9 us; the launches overlap as far as their waits allow, and data that
 // another SM has just written takes 0.8 us to read.
+#include <cstddef>
+
 #include "tree.cuh"
 
 namespace dsa {
@@ -110,12 +112,14 @@ __device__ __forceinline__ uint32_t scan(uint32_t v, uint32_t* wsh, uint32_t& to
   return __reduce_add_sync(0xffffffffu, lane < warp ? wv : 0u) + x - v;
 }
 
-// Shared scratch of the row CTAs.
+// Shared scratch of the row CTAs.  The histogram's place also holds pairs (resolve_digit).
 struct RowShared {
-  uint32_t h[kBins];
+  alignas(16) uint32_t h[kBins];
   uint32_t wsh[4][32];
   uint32_t res[2];
 };
+static_assert(alignof(RowShared) % alignof(uint2) == 0 && offsetof(RowShared, h) % alignof(uint2) == 0,
+              "pairs are read and written 8 bytes at a time");
 
 // One digit: counts (in S.h, `nb` bins of ascending value) to the bin holding the kk-th
 // largest and the number above it.  The bins count kk values at least, so one of them
