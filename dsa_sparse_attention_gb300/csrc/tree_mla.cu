@@ -273,6 +273,22 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
+// A tile's logits less their references, capped half a step above what the references allow.  From
+// logits of 2^24 (log2 units) on, fp32 rounds the logits and SHIFT - reference by whole units, so that
+// a weight could pass fp16's range (and be infinite, the result NaN); the cap leaves up to 2^28, where
+// units are 16 apart, a largest weight between 2^-5 and 2^15.5.  Below 2^20 it is never reached.  Tiles
+// that move no reference have had their maximum compared instead.  NaN stays NaN.
+constexpr float kTreeCap = 15.5f;   // SHIFT + TAU + 1/2
+__device__ __forceinline__ void cap_weights(float2 (&y)[4][4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      asm("min.NaN.f32 %0, %0, %1;" : "+f"(y[i][b].x) : "f"(kTreeCap));
+      asm("min.NaN.f32 %0, %0, %1;" : "+f"(y[i][b].y) : "f"(kTreeCap));
+    }
+}
+
 // ------------------------------------------------- attention with FP8 latents
 //
 // No conversion: e4m3 is the tensor core's operand type, and one copy of the tile in
@@ -333,6 +349,7 @@ static_assert(OFF_LAT % 1024 == 0 && OFF_TAIL % 1024 == 0 && OFF_P % 1024 == 0, 
 static_assert(OFF_SH % 16 == 0 && OFF_ALPHA % 16 == 0 && OFF_INV % 16 == 0 && OFF_QEXP % 16 == 0,
               "vectors are read 16 bytes at a time");
 static_assert(OFF_BARS % 8 == 0 && SMEM_BYTES <= 232448, "smem");
+static_assert(SHIFT + TAU + 0.5f == kTreeCap, "weights' cap");
 }  // namespace t8
 
 // One term of two fp16 values, both to nearest: the upper byte of each half of the result
@@ -662,7 +679,7 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
             const int n = 32 * g + lane;
             const float m = fmaxf(fmaxf(red[n], red[kMlaHeads + n]), fmaxf(red[2 * kMlaHeads + n], red[3 * kMlaHeads + n]));
             float alpha = 1.f;
-            if (m > m_ref + TAU) {
+            if (m - m_ref > TAU) {   // (exact near TAU, where a sum would be rounded)
               alpha = exp2f(m_ref - m);
               m_ref = m;
             }
@@ -696,6 +713,7 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
           }
           logits(0);
           logits(2);
+          cap_weights(y);
         }
         // Latents nobody sees are zeroed before the values read them (a weight of zero does not
         // cancel a NaN): 512 bytes a row, 4 lanes x 8 x 16 bytes, three warps share the rows.
@@ -864,6 +882,7 @@ static_assert(OFF_C % 1024 == 0 && OFF_P % 1024 == 0, "align");
 static_assert(OFF_SH % 16 == 0 && OFF_ALPHA % 16 == 0 && OFF_INV % 16 == 0 && OFF_QEXP % 16 == 0 && OFF_BARS % 8 == 0,
               "vectors are read 16 bytes at a time");
 static_assert(SMEM_BYTES <= 232448, "smem");
+static_assert(SHIFT + TAU + 0.5f == kTreeCap, "weights' cap");
 }  // namespace t16
 
 // 4-byte global -> shared copy without registers (a register that holds a load for a whole
@@ -1263,7 +1282,7 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
             const int n = 32 * g + lane;
             const float m = fmaxf(fmaxf(red[n], red[kMlaHeads + n]), fmaxf(red[2 * kMlaHeads + n], red[3 * kMlaHeads + n]));
             float alpha = 1.f;
-            if (m > m_ref + TAU) {
+            if (m - m_ref > TAU) {   // (exact near TAU, where a sum would be rounded)
               alpha = exp2f(m_ref - m);
               m_ref = m;
             }
@@ -1297,6 +1316,7 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
           }
           logits(0);
           logits(2);
+          cap_weights(y);
         }
         tc_fence_before();   // the scores are in registers
 #pragma unroll

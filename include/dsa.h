@@ -402,6 +402,8 @@ size_t dsa_tree_workspace_size(const dsa_kv_layout *layout, const dsa_batch *bat
  *   lse[t,h]  = ln sum_{s in V_t} exp(logit(s))
  *  q  : device bf16 [T, 96, 576], finite;  out: device bf16 [T, 96, 512];  both 16-byte aligned
  *  lse: device fp32 [T, 96] or NULL
+ * Logits are fp32; up to 2^27 in magnitude the weights stay in range (results are then as
+ * exact as fp32 logits of that size are).
  * Work is split over the positions and merged by log-sum-exp.  The split follows the
  * batch; with DSA_BATCH_INVARIANT it does not (every token's positions are then summed
  * in one order, whatever else the batch holds).  A block id outside the pool is recorded

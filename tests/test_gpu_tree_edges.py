@@ -4,6 +4,8 @@ import pytest
 import torch
 
 from dsa_sparse_attention_gb300 import workloads as W
+from oracle import dsa_oracle as O
+from tests.parity import oracle_layout
 from tests.test_gpu_tree import _check, _check_topk, _topk, _topk_case
 from tests.tree_cases import DeviceTree, check_mla, make_case
 
@@ -90,3 +92,39 @@ def test_mla_few_seen_in_a_long_context(fmt):
     torch.cuda.synchronize()
     assert _check(d.ws) == 0
     check_mla(case, out, lse)
+
+
+# ------------------------------------------------------------------ far-out logits
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("scale", [1e3, 1e5, 1e6, 1.7e6])
+def test_mla_logits_of_hundred_millions(fmt, scale):
+    # Logits up to 2^28 in log2 units, where an fp32 logit is 16 apart from the next: one position takes
+    # a head's weight, and its latent, exact in bf16 (6 significant bits at most), is the result, but for
+    # the others' weights: each is at most exp(2 e - gap) < exp(-40), 702 of them times the largest latent.
+    # Heads whose two largest logits lie nearer than four times their error e have no such answer.
+    case = make_case([700], [2], seed=305, lat_fmt=fmt)
+    wl = case.wl
+    wl.sm_scale = scale
+    d = DeviceTree(case)
+    out, lse = d.mla()
+    torch.cuda.synchronize()
+    assert _check(d.ws) == 0
+    out, lse = out.float().cpu().numpy(), lse.cpu().numpy().astype(np.float64)
+    assert np.isfinite(out).all() and np.isfinite(lse).all()
+    clear = 0
+    for t in range(2):
+        lat = O.gather_latents(oracle_layout(wl), wl.block_table[0], case.seen(t))
+        q = O.decode_bf16(wl.q[t]).reshape(96, 576)
+        logits = scale * (q @ lat.T)
+        assert np.abs(logits).max() * 1.4427 < 2.0 ** 28
+        e = 2.0 ** -18 * scale * (np.abs(q) @ np.abs(lat).T).max(axis=1)
+        best = logits.argmax(axis=1)
+        two = np.sort(logits, axis=1)[:, -2:]
+        for h in np.flatnonzero(two[:, 1] - two[:, 0] > 4 * e + 40):
+            off = np.abs(out[t, h] - lat[best[h], :512]).max()
+            assert off <= 702 * np.exp(-40.0) * np.abs(lat).max(), f"token {t}, head {h}: {off}"
+            assert abs(lse[t, h] - two[h, 1]) <= e[h] + 1e-6 * abs(two[h, 1])
+            clear += 1
+    assert clear > 150
