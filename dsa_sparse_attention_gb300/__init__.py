@@ -55,11 +55,13 @@ class dsa_batch(ctypes.Structure):
 class dsa_tree(ctypes.Structure):
     _fields_ = [("base", ctypes.c_void_p), ("mask", ctypes.c_void_p), ("mask_words", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+    rows = None   # (base, mask): the arrays' rows, where make_tree knows them
 
 
 class dsa_pages(ctypes.Structure):
     _fields_ = [("ref_count", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("ctx_lens", ctypes.c_void_p),
                 ("num_reqs", ctypes.c_int32), ("bt_stride", ctypes.c_int32)]
+    rows = None   # of ref_count, where make_pages knows it
 
 
 class dsa_host_io(ctypes.Structure):
@@ -132,16 +134,20 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _device = None
 
 
-def _stream(stream):
+def _handle(stream):
     global _device
     if stream is not None:
-        return ctypes.c_void_p(stream.cuda_stream)
+        return stream.cuda_stream
     if _raw_stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        return torch.cuda.current_stream().cuda_stream
     if _device is None:
         torch.cuda.current_device()   # initialises CUDA
         _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-    return ctypes.c_void_p(_raw_stream(_device()))
+    return _raw_stream(_device())
+
+
+def _stream(stream):
+    return ctypes.c_void_p(_handle(stream))
 
 
 def dsa_last_cuda_error():
@@ -291,20 +297,56 @@ _byref = ctypes.byref
 
 
 def _int32(name, t, ndim):
-    """The address of an int32 tensor whose elements lie one behind the other, as the C ABI
-    reads it (None stays None)."""
+    """The address of a device int32 tensor whose elements lie one behind the other, as the
+    C ABI reads it (None stays None)."""
     if t is None:
         return None
     if t.dtype is not _I32 or t.dim() != ndim or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor of {ndim} dimension(s)")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
     return t.data_ptr()
+
+
+def _array(name, t, dtype, count):
+    """The address of a device tensor of `count` elements at least, one behind the other
+    (None and addresses stay what they are)."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.dtype is not dtype or not t.is_contiguous() or t.numel() < count or not t.is_cuda:
+        raise ValueError(f"{name} must be a contiguous device tensor of {dtype} with {count} elements")
+    return t.data_ptr()
+
+
+def _rows(name, t, dtype, rows, ld):
+    """The same for `rows` rows `ld` elements apart: one array, or a view of the first columns of one."""
+    if t is None or isinstance(t, int) or (t.is_contiguous() and t.numel() >= rows * ld):
+        return _array(name, t, dtype, rows * ld)
+    if (t.dtype is not dtype or t.dim() != 2 or t.shape[0] < rows or t.stride(1) != 1 or (rows > 1 and t.stride(0) != ld) or
+            not t.is_cuda or t.untyped_storage().nbytes() < (t.storage_offset() + rows * ld) * t.element_size()):
+        raise ValueError(f"{name} must be a device tensor of {dtype} with {rows} rows of {ld} elements")
+    return t.data_ptr()
+
+
+def _space(ws):
+    if not ws.is_cuda:
+        raise ValueError("ws must be a device tensor")
+    return ws.data_ptr()
 
 
 def make_tree(base, mask):
     """Descriptor of the drafted tokens' trees over device int32 tensors (kept alive by the
     caller): base [B] committed tokens, mask [T, words], bit i of row t set where token t sees
     drafted slot i."""
-    return dsa_tree(_int32("base", base, 1), _int32("mask", mask, 2), int(mask.shape[1]), 0)
+    tree = dsa_tree(_int32("base", base, 1), _int32("mask", mask, 2), int(mask.shape[1]), 0)
+    tree.rows = (base.shape[0], mask.shape[0])
+    return tree
+
+
+def _check_tree(batch, tree):
+    rows = tree.rows
+    if rows is not None and (rows[0] < batch.num_reqs or rows[1] < batch.num_tokens):
+        raise ValueError("base must have an element for every request, mask a row for every token")
 
 
 def dsa_tree_workspace_size(layout, batch):
@@ -320,18 +362,27 @@ def alloc_tree_workspace(layout, batch, device="cuda"):
 
 
 def dsa_tree_mla(layout, batch, tree, q, sm_scale, out, lse=None, ws=None, stream=None):
-    """Dense attention of drafted tokens over the positions each sees (bf16 q [T, 96, 576])."""
-    s = library().dsa_tree_mla(_byref(layout), _byref(batch), _byref(tree), _ptr(q), float(sm_scale), _ptr(out),
-                               _ptr(lse), _ptr(ws), ws.numel(), _stream(stream))
+    """Dense attention of drafted tokens over the positions each sees: bf16 q [T, 96, 576] and out
+    [T, 96, 512], fp32 lse [T, 96]."""
+    _check_tree(batch, tree)
+    heads = 96 * batch.num_tokens
+    s = library().dsa_tree_mla(_byref(layout), _byref(batch), _byref(tree), _array("q", q, torch.bfloat16, 576 * heads),
+                               float(sm_scale), _array("out", out, torch.bfloat16, 512 * heads),
+                               _array("lse", lse, torch.float32, heads), _space(ws), ws.numel(), _handle(stream))
     if s:
         _check(s, "dsa_tree_mla")
 
 
 def dsa_tree_topk(layout, batch, tree, scores, ld, topk, idx, phys_slots=None, ws=None, stream=None):
-    """dsa_topk over the positions each drafted token sees (workspace as dsa_topk)."""
+    """dsa_topk over the positions each drafted token sees (workspace as dsa_topk): fp32 scores
+    [T, ld], int32 idx and phys_slots [T, topk]."""
+    _check_tree(batch, tree)
+    tokens, ld, topk = batch.num_tokens, int(ld), int(topk)
     s = library().dsa_tree_topk(_byref(layout) if layout is not None else None, _byref(batch), _byref(tree),
-                                _ptr(scores), int(ld), int(topk), _ptr(idx), _ptr(phys_slots), _ptr(ws), ws.numel(),
-                                _stream(stream))
+                                _rows("scores", scores, torch.float32, tokens, ld), ld, topk,
+                                _array("idx", idx, _I32, tokens * topk),
+                                _array("phys_slots", phys_slots, _I32, tokens * topk), _space(ws), ws.numel(),
+                                _handle(stream))
     if s:
         _check(s, "dsa_tree_topk")
 
@@ -341,10 +392,11 @@ def dsa_tree_commit(layout, batch, base, accept, new_lens=None, ws=None, stream=
     positions behind the committed ones; new_lens [B] receives the committed lengths."""
     pb, pa, pn = _int32("base", base, 1), _int32("accept", accept, 2), _int32("new_lens", new_lens, 1)
     rows, most = accept.shape
-    if rows != batch.num_reqs:
-        raise ValueError("accept must have a row for every request")
-    s = library().dsa_tree_commit(_byref(layout), _byref(batch), pb, pa, most, pn, ws.data_ptr(), ws.numel(),
-                                  _stream(stream))
+    reqs = batch.num_reqs
+    if rows != reqs or base.numel() < reqs or (pn and new_lens.numel() < reqs):
+        raise ValueError("base, accept and new_lens must have a row for every request")
+    s = library().dsa_tree_commit(_byref(layout), _byref(batch), pb, pa, most, pn, _space(ws), ws.numel(),
+                                  _handle(stream))
     if s:
         _check(s, "dsa_tree_commit")
 
@@ -355,7 +407,13 @@ def make_pages(ref_count, block_table, ctx_lens):
                       _int32("ctx_lens", ctx_lens, 1), int(ctx_lens.shape[0]), int(block_table.shape[1]))
     if block_table.shape[0] != ctx_lens.shape[0]:
         raise ValueError("block_table and ctx_lens must have a row and a length for every request")
+    pages.rows = ref_count.shape[0]
     return pages
+
+
+def _check_pages(layout, pages):
+    if pages.rows is not None and pages.rows < layout.num_rows:
+        raise ValueError("ref_count must have an element for every row of the pool")
 
 
 def dsa_cache_workspace_size(layout, num_reqs):
@@ -377,10 +435,10 @@ def dsa_cache_copy(layout, src, dst, count=None, ws=None, stream=None):
         raise ValueError("src and dst must be of one length")
     pc = None
     if count is not None:
-        if count.dtype is not _I32 or count.numel() < 1:
-            raise ValueError("count must be an int32 tensor of an element")
+        if count.dtype is not _I32 or count.numel() < 1 or not count.is_cuda:
+            raise ValueError("count must be a device int32 tensor of an element")
         pc = count.data_ptr()
-    s = library().dsa_cache_copy(_byref(layout), ps, pd, n, pc, ws.data_ptr(), ws.numel(), _stream(stream))
+    s = library().dsa_cache_copy(_byref(layout), ps, pd, n, pc, _space(ws), ws.numel(), _handle(stream))
     if s:
         _check(s, "dsa_cache_copy")
 
@@ -392,16 +450,18 @@ def dsa_cache_fork(layout, pages, parent, child, copy_src, copy_dst, ws=None, st
     ps, pd, n = _int32("copy_src", copy_src, 1), _int32("copy_dst", copy_dst, 1), parent.numel()
     if not child.numel() == copy_src.numel() == copy_dst.numel() == n:
         raise ValueError("parent, child, copy_src and copy_dst must be of one length")
-    s = library().dsa_cache_fork(_byref(layout), _byref(pages), pp, pc, n, ps, pd, ws.data_ptr(), ws.numel(),
-                                 _stream(stream))
+    _check_pages(layout, pages)
+    s = library().dsa_cache_fork(_byref(layout), _byref(pages), pp, pc, n, ps, pd, _space(ws), ws.numel(),
+                                 _handle(stream))
     if s:
         _check(s, "dsa_cache_fork")
 
 
 def dsa_cache_free(layout, pages, reqs, ws=None, stream=None):
     """Requests' blocks given back: table rows -1, counts down by one, lengths 0."""
-    s = library().dsa_cache_free(_byref(layout), _byref(pages), _int32("reqs", reqs, 1), reqs.numel(), ws.data_ptr(),
-                                 ws.numel(), _stream(stream))
+    _check_pages(layout, pages)
+    s = library().dsa_cache_free(_byref(layout), _byref(pages), _int32("reqs", reqs, 1), reqs.numel(), _space(ws),
+                                 ws.numel(), _handle(stream))
     if s:
         _check(s, "dsa_cache_free")
 
@@ -414,8 +474,10 @@ def dsa_cache_compact(layout, pages, to, copy_src, copy_dst, counts, ws=None, st
     pc, need = _int32("counts", counts, 1), max(1, layout.num_rows // 2)
     if copy_src.numel() < need or copy_dst.numel() < need or counts.numel() < 2:
         raise ValueError("copy_src and copy_dst need num_rows // 2 elements, counts two")
-    s = library().dsa_cache_compact(_byref(layout), _byref(pages), _byref(to), ps, pd, pc, ws.data_ptr(), ws.numel(),
-                                    _stream(stream))
+    _check_pages(layout, pages)
+    _check_pages(layout, to)
+    s = library().dsa_cache_compact(_byref(layout), _byref(pages), _byref(to), ps, pd, pc, _space(ws), ws.numel(),
+                                    _handle(stream))
     if s:
         _check(s, "dsa_cache_compact")
 
