@@ -1130,7 +1130,6 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
     // Fill f: the row's 32 packed bytes -> 64 fp16 values in registers, then, once the place is
     // free (on the CTA's first tile the first ones are), into it.  A row nobody sees is zeros.
     uint32_t* scales = reinterpret_cast<uint32_t*>(smem + OFF_SCALE) + threadIdx.x;
-    const uint32_t never = static_cast<uint32_t>(p.whole) >> 8;
     auto fill = [&](int f, bool seen_row) {
       ok = warp_wait(&raw_full[f], it & 1, ab, ok);
       const uint8_t* src = smem + OFF_RAW + (FILLS * it + turn_of_fill(f)) % RAWS * RAW + crow * 32;
@@ -1138,9 +1137,9 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
       const uint4 w0 = *reinterpret_cast<const uint4*>(src + sw), w1 = *reinterpret_cast<const uint4*>(src + (sw ^ 16));
       // The place is given back once the loads have returned, which an arrival behind them does not
       // imply: with shared memory busy the next copy was faster than they.  So the barrier's address
-      // takes a bit of both (`never` is 0, and not known to be).
+      // takes a bit of both (p.never is 0, and not known to be).
       __syncwarp();
-      if (ok && lane == 0) mbar_arrive(&raw_done[f] + ((w0.x ^ w1.x) & never));
+      if (ok && lane == 0) mbar_arrive(&raw_done[f] + ((w0.x ^ w1.x) & p.never));
       const uint32_t sw4 = seen_row ? scales[((it & 1) * 3 + scale_of_fill(f)) * 384] : 0u;
       uint32_t o[4][8];
       nvfp4x16_to_f16(make_uint2(w0.x, w0.y), sw4 & 0xFFu, o[0]);

@@ -44,6 +44,7 @@ struct TreeMlaParams {
   __half* part_o;            // [2 max_ctas, 96, 512], each normalised by its own sum
   float2* part_ml;           // [2 max_ctas, 96]: (max in log2 units, sum)
   uint32_t* status;
+  uint32_t never = 0;        // always 0, which the compiler cannot know (the NVFP4 kernel's fills)
 };
 
 // One segment: the n key tiles from j0 on of token t, taken in the order tile(0), tile(1), ...:
