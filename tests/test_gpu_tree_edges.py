@@ -1,10 +1,13 @@
-"""Trees of drafted tokens where tests at ordinary sizes do not look."""
+"""Trees of drafted tokens where tests at ordinary sizes do not look: rows on which a token
+sees little, rows of millions of scores, errors that a worst-case bound would hide, and
+logits far beyond a softmax's usual range."""
 import numpy as np
 import pytest
 import torch
 
 from dsa_sparse_attention_gb300 import workloads as W
 from oracle import dsa_oracle as O
+from oracle import tree as OT
 from tests.parity import oracle_layout
 from tests.test_gpu_tree import _check, _check_topk, _topk, _topk_case
 from tests.tree_cases import DeviceTree, check_mla, make_case
@@ -16,6 +19,81 @@ FMTS = [W.LAT_FP8, W.LAT_NVFP4]
 def _built():
     from dsa_sparse_attention_gb300.build import build
     build()
+
+
+# ------------------------------------------------ errors of a few values, not of all
+
+def rms_use(case, out, t):
+    """Largest share that the rms error of any head's 64 dims (a chunk) takes of its bound.
+
+    The roundings of a token's result, independent of each other: the output to bf16, uniform
+    within half a step, so at most 2^-8 / sqrt(3) of the value in the mean square; every weight,
+    to 9 significant bits or more, so a dim moves by at most (2^-9 / sqrt(3)) sqrt(sum p^2 v^2), and
+    with it the fp16 partials (2^-11); the logits, off by at most e of check_mla each.  The bound is
+    twice the root of the sum of squares: the error of a chunk's 64 dims scatters by 9 % around its
+    mean square, and where one weight carries the result its rounding is at most sqrt(3) times its mean.
+    Where check_mla's bound stays at 2^-8 of sum p |v|, this one shrinks with the number of positions,
+    as the result does, so wrong values at a few positions show."""
+    wl = case.wl
+    lat = O.gather_latents(oracle_layout(wl), wl.block_table[int(wl.q_req[t])], case.seen(t))
+    ref, lse, _ = OT.dense_mla(wl.q[t], lat, wl.sm_scale)
+    q = O.decode_bf16(wl.q[t]).reshape(96, 576)
+    p = np.exp(wl.sm_scale * (q @ lat.T) - lse[:, None])
+    spread = (p * p) @ (lat[:, :512] ** 2)
+    e = 2.0 ** -18 * abs(wl.sm_scale) * (np.abs(q) @ np.abs(lat).T).max(axis=1)
+    chunks = lambda x: x.reshape(96, 8, 64).mean(axis=2)
+    bound = 2 * np.sqrt(2.0 ** -16 / 3 * chunks(ref ** 2) + (2.0 ** -18 / 3 + e[:, None] ** 2) * chunks(spread))
+    err = out[t].astype(np.float64) - ref
+    return float((np.sqrt(chunks(err ** 2)) / bound).max())
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_rms_bound_sees_one_wrong_warp(fmt):
+    # (no GPU) the exact result, rounded, passes; with 32 positions' values of 64 dims exchanged for
+    # others', which the worst-case bound lets pass, it does not
+    case = make_case([25000], [1], seed=301, lat_fmt=fmt)
+    wl = case.wl
+    lat = O.gather_latents(oracle_layout(wl), wl.block_table[0], case.seen(0))
+    ref, _, _ = OT.dense_mla(wl.q[0], lat, wl.sm_scale)
+    bf16 = lambda x: torch.from_numpy(x).to(torch.bfloat16).float().numpy()[None]
+    assert rms_use(case, bf16(ref), 0) < 1.0
+    bad = lat.copy()
+    bad[1312:1344, 192:256] = lat[2312:2344, 192:256]
+    q = O.decode_bf16(wl.q[0]).reshape(96, 576)
+    logits = wl.sm_scale * (q @ lat.T)
+    p = np.exp(logits - logits.max(axis=1, keepdims=True))
+    out = (p / p.sum(axis=1, keepdims=True)) @ bad[:, :512]
+    assert rms_use(case, bf16(out), 0) > 2.0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("flags", [0, 1])
+def test_mla_rms(fmt, flags):
+    # a token over 196 tiles, alone (more tiles than CTAs) and among others, and with the fixed order
+    import dsa_sparse_attention_gb300 as dsa
+    case = make_case([25000, 800, 3000], [1, 40, 9], seed=302, lat_fmt=fmt)
+    d = DeviceTree(case, flags=flags * dsa.DSA_BATCH_INVARIANT)
+    out, _ = d.mla()
+    torch.cuda.synchronize()
+    assert _check(d.ws) == 0
+    out = out.float().cpu().numpy()
+    for t in [0, 1, 2, 7, 20, 39, 40, 41, 45, 49]:
+        use = rms_use(case, out, t)
+        assert use < 1.0, f"token {t}: rms error {use:.3g} of its bound"
+
+
+# ------------------------------------------------------------------- very long rows
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", ["normal", "late"])
+def test_topk_row_of_millions(shape):
+    # more than 1,024 chunks of 4,096 scores: the selection places its entries in more than one round
+    case, scores = _topk_case([4300000], [3], seed=304)
+    if shape == "late":
+        scores[:, 4194304 - 700:4194304 + 900] += 20
+    idx, _ = _topk(case, scores, 2048)
+    _check_topk(case, scores, 2048, idx)
 
 
 # --------------------------------------------------------------- few seen positions
@@ -104,6 +182,7 @@ def test_mla_logits_of_hundred_millions(fmt, scale):
     # a head's weight, and its latent, exact in bf16 (6 significant bits at most), is the result, but for
     # the others' weights: each is at most exp(2 e - gap) < exp(-40), 702 of them times the largest latent.
     # Heads whose two largest logits lie nearer than four times their error e have no such answer.
+    # (Without the weights' cap 4 and 7 of the 192 heads were not finite at 1e6, 175 and 179 at 1.7e6.)
     case = make_case([700], [2], seed=305, lat_fmt=fmt)
     wl = case.wl
     wl.sm_scale = scale
