@@ -102,7 +102,11 @@ constexpr int kPlanCtas = 8;
 // A free, a fork of 2 requests to 8 and the copies, 600 rows: 15.3 us together with one CTA and
 // one launch, 17.7 us with a cluster and two; the launches bound it (11.5 us in a graph).
 constexpr int64_t kOneCtaRows = 16384;
-constexpr int64_t kOneLaunchEntries = 8192;   // table entries per plan CTA
+// The plan's CTAs handle the tables, too, where each of their threads has one entry at most.  Free + fork
+// of 512 / 1,024 / 2,048 / 4,096 / 8,192 entries by one CTA: 9.3 / 9.4 / 10.8 / 13.9 / 18.7 us so, 11.3 / 11.1 /
+// 11.0 / 11.2 / 13.5 with a launch of their own; by the cluster, 8,192 / 32,768 entries: 12.3 / 17.3 and
+// 12.7 / 14.9; compaction alike, 1,024 / 8,192 by one CTA: 11.2 / 14.5 and 10.6 / 11.2, and a launch less.
+constexpr int64_t kOneLaunchEntries = kPlanThreads;   // table entries per plan CTA
 
 unsigned plan_ctas(int64_t num_rows) { return num_rows <= kOneCtaRows ? 1u : static_cast<unsigned>(kPlanCtas); }
 
