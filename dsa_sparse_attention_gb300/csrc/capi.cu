@@ -338,7 +338,8 @@ TreeView tree_view(const dsa_tree* t) { return TreeView{t->base, t->mask, t->mas
 
 // Workspace of dsa_tree_mla.
 struct TreeWs {
-  size_t status = 0, starts = 0, toks = 0, shares = 0, q_terms = 0, q_exps = 0, part_o = 0, part_ml = 0, total = 0;
+  size_t status = 0, starts = 0, toks = 0, shares = 0, q_terms = 0, q_exps = 0, part_o = 0, part_ml = 0, run = 0, total = 0;
+  bool runs = false;   // a token may have more tiles than are summed in one run
 };
 
 TreeWs plan_tree_ws(const dsa_kv_layout* l, const dsa_batch* b) {
@@ -353,7 +354,9 @@ TreeWs plan_tree_ws(const dsa_kv_layout* l, const dsa_batch* b) {
   w.q_exps = align_up(w.q_terms + T * (l->lat_fmt == DSA_LAT_FP8 ? size_t(kQTokenBytes) : size_t(kMlaHeads) * kLatDim * 2));
   w.part_o = align_up(w.q_exps + (l->lat_fmt == DSA_LAT_FP8 ? 0 : T * kMlaHeads * 4));
   w.part_ml = align_up(w.part_o + slots * kMlaHeads * kVDim * 2);
-  w.total = align_up(w.part_ml + slots * kMlaHeads * sizeof(float2));
+  w.run = align_up(w.part_ml + slots * kMlaHeads * sizeof(float2));
+  w.runs = cdiv(b->max_ctx_len, kSelTile) > kRunTiles;
+  w.total = align_up(w.run + (w.runs ? size_t(num_sms()) * kRunFloats * sizeof(float) : 0));
   return w;
 }
 
@@ -918,6 +921,7 @@ dsa_status dsa_tree_mla(const dsa_kv_layout* layout, const dsa_batch* batch, con
   p.lse = lse;
   p.part_o = at<__half>(workspace, wl.part_o);
   p.part_ml = at<float2>(workspace, wl.part_ml);
+  p.run = wl.runs ? at<float>(workspace, wl.run) : nullptr;
   p.status = at<uint32_t>(workspace, wl.status);
   const bool fp8 = layout->lat_fmt == DSA_LAT_FP8;
   uint8_t* terms = fp8 ? at<uint8_t>(workspace, wl.q_terms) : nullptr;

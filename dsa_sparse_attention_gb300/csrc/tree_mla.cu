@@ -289,6 +289,37 @@ __device__ __forceinline__ void cap_weights(float2 (&y)[4][4]) {
     }
 }
 
+// A warp's part of O (32 heads from column n0 on of its lanes' dims, in the four dim blocks) added to
+// the CTA's running sums, or, at a segment's end, the sums to it.  The sums have the references that
+// `run_sh` (SHIFT - reference, per column) kept of their last addition, O those of `sh`; a sum belongs
+// to one thread, which alone reads and writes it.  Between runs rather than in the tiles' loop, which
+// has no register to spare (8 x 6 tokens over 64K, which take no part in it: 582 us, 588 as a call).
+template <bool END>
+__device__ __forceinline__ void add_running_sums(float* runs, bool first, uint32_t o_tmem, const float* sh,
+                                                 const float* run_sh, int n0, int quarter) {
+  float* mine = runs + blockIdx.x * kRunFloats + n0 * 128 + 32 * quarter + (threadIdx.x & 31);
+#pragma unroll 1
+  for (int v = 0; v < 4; ++v) {
+#pragma unroll 1
+    for (int c = 0; c < 32; c += 8) {
+      uint32_t o[8];
+      float* r = mine + (v * kMlaHeads + c) * 128;
+      DSA_TMEM_LD8(o_tmem + 96 * v + n0 + c, o);
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float now = sh[n0 + c + i], then = run_sh[n0 + c + i];
+        // (equal: both infinite where a head has seen nothing)
+        const float x = first ? 0.f : r[i * 128] * (now == then ? 1.f : exp2f(now - then));
+        o[i] = __float_as_uint(__uint_as_float(o[i]) + x);
+        if (!END) r[i * 128] = __uint_as_float(o[i]);
+      }
+      if (END) DSA_TMEM_ST8(o_tmem + 96 * v + n0 + c, o);
+    }
+  }
+  if (END) tmem_wait_st();
+}
+
 // ------------------------------------------------- attention with FP8 latents
 //
 // No conversion: e4m3 is the tensor core's operand type, and one copy of the tile in
@@ -334,7 +365,8 @@ constexpr int OFF_REDM = OFF_QEXP + 96 * 4;       // [4][96] float: maxima, then
 constexpr int OFF_SH = OFF_REDM + 4 * 96 * 4;     // [96] float: SHIFT - reference
 constexpr int OFF_ALPHA = OFF_SH + 96 * 4;        // [96] float
 constexpr int OFF_INV = OFF_ALPHA + 96 * 4;       // [96] float
-constexpr int OFF_BARS = OFF_INV + 96 * 4;
+constexpr int OFF_RUN = OFF_INV + 96 * 4;         // [96] float: SHIFT - reference of the running sums
+constexpr int OFF_BARS = OFF_RUN + 96 * 4;
 constexpr int N_BARS = 20;
 constexpr int OFF_MISC = OFF_BARS + N_BARS * 8;
 constexpr int SMEM_BYTES = OFF_MISC + 64 + 1024;
@@ -386,6 +418,7 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
   float* sh_sh = reinterpret_cast<float*>(smem + OFF_SH);
   float* alpha_sh = reinterpret_cast<float*>(smem + OFF_ALPHA);
   float* inv_sh = reinterpret_cast<float*>(smem + OFF_INV);
+  float* run_sh = reinterpret_cast<float*>(smem + OFF_RUN);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -532,7 +565,7 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
         if (!ok) break;
         if (leader) tc_commit(s_full);
         __syncwarp();
-        const uint32_t acc = i > 0 ? 1u : 0u;
+        const uint32_t acc = i % kRunTiles ? 1u : 0u;   // the accumulators start again
         const bool last = i == s.n - 1;
         if (!(ok = warp_wait(&p_full[0], it & 1, ab, ok))) break;
         tc_fence_after();
@@ -605,164 +638,173 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
         l2[b] = make_float2(0.f, 0.f);
       }
       float m_ref = -INFINITY;                // quarter 0: reference of column 32 g + lane
-      for (int n = 0; n < s.n; ++n, ++it) {
-        const int j = s.tile(n);
-        ok = warp_wait(s_full, it & 1, ab, ok);
-        tc_fence_after();
-        // y[i][b]: logits in log2 units less the reference, plus SHIFT
-        uint32_t rr[2][16];
-        const uint32_t ts = tmem + S_COL + 32 * g + lane_off;
-        DSA_TMEM_LD_16X256_X4(ts, rr[0]);
-        tmem_wait_ld();
-        DSA_TMEM_LD_16X256_X4(ts + (16u << 16), rr[1]);   // lands while the first half is scaled
-        const bool border = (j + 1) * kSelTile > plain;
-        uint32_t seen = 15u;                  // bit i: token i of this thread is seen
-        if (border) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int s0 = j * kSelTile + 32 * quarter + r4 + 8 * i;
-            if (!(s0 <= pos && tree_sees(mrow, p.tree.words, base, s0))) seen &= ~(1u << i);
-          }
-        }
-        float2 y[4][4];
-        auto raw = [&](int i, int b) {
-          return make_float2(__uint_as_float(rr[i >> 1][4 * b + 2 * (i & 1)]),
-                             __uint_as_float(rr[i >> 1][4 * b + 2 * (i & 1) + 1]));
-        };
-        auto logits = [&](int i0) {   // of the tokens i0 and i0 + 1; their maximum
-          float mx = -INFINITY;
-#pragma unroll
-          for (int i = i0; i < i0 + 2; ++i) {
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              y[i][b] = fma2(raw(i, b), c2[b], sh2[b]);
-              if (!((seen >> i) & 1u)) y[i][b] = make_float2(-INFINITY, -INFINITY);
-              mx = fmaxf(fmaxf(mx, y[i][b].x), y[i][b].y);
-            }
-          }
-          return mx;
-        };
-        bool moves = n == 0;   // a segment's first tile sets the references
-        if (moves) {
+      for (int n = 0;;) {
+        for (const int end = min(s.n, n + kRunTiles); n < end; ++n, ++it) {
+          const int j = s.tile(n);
+          ok = warp_wait(s_full, it & 1, ab, ok);
+          tc_fence_after();
+          // y[i][b]: logits in log2 units less the reference, plus SHIFT
+          uint32_t rr[2][16];
+          const uint32_t ts = tmem + S_COL + 32 * g + lane_off;
+          DSA_TMEM_LD_16X256_X4(ts, rr[0]);
           tmem_wait_ld();
-        } else {
-          float mx = logits(0);
-          tmem_wait_ld();
-          mx = fmaxf(mx, logits(2));
-          moves = named_bar_any(1, MATH, mx > SHIFT + TAU);
-        }
-        if (moves) {
-          // some reference moves: the tile's maxima per head
-          float hm[8];
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            hm[2 * b] = hm[2 * b + 1] = -INFINITY;
+          DSA_TMEM_LD_16X256_X4(ts + (16u << 16), rr[1]);   // lands while the first half is scaled
+          const bool border = (j + 1) * kSelTile > plain;
+          uint32_t seen = 15u;                  // bit i: token i of this thread is seen
+          if (border) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float2 x = raw(i, b);
-              if ((seen >> i) & 1u) {
-                hm[2 * b] = fmaxf(hm[2 * b], x.x * c2[b].x);
-                hm[2 * b + 1] = fmaxf(hm[2 * b + 1], x.y * c2[b].y);
+              const int s0 = j * kSelTile + 32 * quarter + r4 + 8 * i;
+              if (!(s0 <= pos && tree_sees(mrow, p.tree.words, base, s0))) seen &= ~(1u << i);
+            }
+          }
+          float2 y[4][4];
+          auto raw = [&](int i, int b) {
+            return make_float2(__uint_as_float(rr[i >> 1][4 * b + 2 * (i & 1)]),
+                               __uint_as_float(rr[i >> 1][4 * b + 2 * (i & 1) + 1]));
+          };
+          auto logits = [&](int i0) {   // of the tokens i0 and i0 + 1; their maximum
+            float mx = -INFINITY;
+#pragma unroll
+            for (int i = i0; i < i0 + 2; ++i) {
+#pragma unroll
+              for (int b = 0; b < 4; ++b) {
+                y[i][b] = fma2(raw(i, b), c2[b], sh2[b]);
+                if (!((seen >> i) & 1u)) y[i][b] = make_float2(-INFINITY, -INFINITY);
+                mx = fmaxf(fmaxf(mx, y[i][b].x), y[i][b].y);
               }
             }
+            return mx;
+          };
+          bool moves = n == 0;   // a segment's first tile sets the references
+          if (moves) {
+            tmem_wait_ld();
+          } else {
+            float mx = logits(0);
+            tmem_wait_ld();
+            mx = fmaxf(mx, logits(2));
+            moves = named_bar_any(1, MATH, mx > SHIFT + TAU);
           }
+          if (moves) {
+            // some reference moves: the tile's maxima per head
+            float hm[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
+            for (int b = 0; b < 4; ++b) {
+              hm[2 * b] = hm[2 * b + 1] = -INFINITY;
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) hm[k] = fmaxf(hm[k], __shfl_xor_sync(0xffffffffu, hm[k], o));
-          if (r4 == 0) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) red[quarter * kMlaHeads + 32 * g + 8 * a + k] = hm[k];
-          }
-          named_bar_sync(2, MATH);
-          if (quarter == 0) {
-            const int n = 32 * g + lane;
-            const float m = fmaxf(fmaxf(red[n], red[kMlaHeads + n]), fmaxf(red[2 * kMlaHeads + n], red[3 * kMlaHeads + n]));
-            float alpha = 1.f;
-            if (m - m_ref > TAU) {   // (exact near TAU, where a sum would be rounded)
-              alpha = exp2f(m_ref - m);
-              m_ref = m;
-            }
-            sh_sh[n] = m_ref == -INFINITY ? INFINITY : SHIFT - m_ref;
-            alpha_sh[n] = alpha;
-          }
-          named_bar_sync(2, MATH);
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const float2 av = *reinterpret_cast<const float2*>(alpha_sh + 32 * g + 8 * a + 2 * b);
-            sh2[b] = *reinterpret_cast<const float2*>(sh_sh + 32 * g + 8 * a + 2 * b);
-            l2[b].x *= av.x;
-            l2[b].y *= av.y;
-          }
-          if (n > 0 && ok) {
-#pragma unroll 1
-            for (int v = 0; v < 4; ++v) {          // this warp's heads in all dim blocks, 16 at a time
-#pragma unroll 1
-              for (int cc = 0; cc < 2; ++cc) {
-                uint32_t o[16];
-                const uint32_t ta = tmem + O_COL + 96 * v + 32 * g + 16 * cc + lane_off;
-                DSA_TMEM_LD16(ta, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                  o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha_sh[32 * g + 16 * cc + i]);
-                DSA_TMEM_ST16(ta, o);
+              for (int i = 0; i < 4; ++i) {
+                const float2 x = raw(i, b);
+                if ((seen >> i) & 1u) {
+                  hm[2 * b] = fmaxf(hm[2 * b], x.x * c2[b].x);
+                  hm[2 * b + 1] = fmaxf(hm[2 * b + 1], x.y * c2[b].y);
+                }
               }
             }
-            tmem_wait_st();
-          }
-          logits(0);
-          logits(2);
-          cap_weights(y);
-        }
-        // Latents nobody sees are zeroed before the values read them (a weight of zero does not
-        // cancel a NaN): 512 bytes a row, 4 lanes x 8 x 16 bytes, three warps share the rows.
-        if (border && ok) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) hm[k] = fmaxf(hm[k], __shfl_xor_sync(0xffffffffu, hm[k], o));
+            if (r4 == 0) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) red[quarter * kMlaHeads + 32 * g + 8 * a + k] = hm[k];
+            }
+            named_bar_sync(2, MATH);
+            if (quarter == 0) {
+              const int n = 32 * g + lane;
+              const float m = fmaxf(fmaxf(red[n], red[kMlaHeads + n]), fmaxf(red[2 * kMlaHeads + n], red[3 * kMlaHeads + n]));
+              float alpha = 1.f;
+              if (m - m_ref > TAU) {   // (exact near TAU, where a sum would be rounded)
+                alpha = exp2f(m_ref - m);
+                m_ref = m;
+              }
+              sh_sh[n] = m_ref == -INFINITY ? INFINITY : SHIFT - m_ref;
+              alpha_sh[n] = alpha;
+            }
+            named_bar_sync(2, MATH);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              const float2 av = *reinterpret_cast<const float2*>(alpha_sh + 32 * g + 8 * a + 2 * b);
+              sh2[b] = *reinterpret_cast<const float2*>(sh_sh + 32 * g + 8 * a + 2 * b);
+              l2[b].x *= av.x;
+              l2[b].y *= av.y;
+            }
+            if (n > 0 && ok) {
 #pragma unroll 1
+              for (int v = 0; v < 4; ++v) {          // this warp's heads in all dim blocks, 16 at a time
+#pragma unroll 1
+                for (int cc = 0; cc < 2; ++cc) {
+                  uint32_t o[16];
+                  const uint32_t ta = tmem + O_COL + 96 * v + 32 * g + 16 * cc + lane_off;
+                  DSA_TMEM_LD16(ta, o);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int i = 0; i < 16; ++i)
+                    o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha_sh[32 * g + 16 * cc + i]);
+                  DSA_TMEM_ST16(ta, o);
+                }
+              }
+              tmem_wait_st();
+            }
+            logits(0);
+            logits(2);
+            cap_weights(y);
+          }
+          // Latents nobody sees are zeroed before the values read them (a weight of zero does not
+          // cancel a NaN): 512 bytes a row, 4 lanes x 8 x 16 bytes, three warps share the rows.
+          if (border && ok) {
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+              if ((seen >> i) & 1u) continue;
+              uint8_t* dst = smem + OFF_LAT + a * SLICE + (32 * quarter + 8 * i + r4) * 128;
+              for (int k = g; k < 8; k += 3) *reinterpret_cast<uint4*>(dst + 16 * k) = make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+          tc_fence_before();   // the scores are in registers
+#pragma unroll
           for (int i = 0; i < 4; ++i) {
-            if ((seen >> i) & 1u) continue;
-            uint8_t* dst = smem + OFF_LAT + a * SLICE + (32 * quarter + 8 * i + r4) * 128;
-            for (int k = g; k < 8; k += 3) *reinterpret_cast<uint4*>(dst + 16 * k) = make_uint4(0u, 0u, 0u, 0u);
-          }
-        }
-        tc_fence_before();   // the scores are in registers
+            uint32_t t0[2], t1[2], t2[2];   // the three e5m2 terms of 8 weights, 4 per word
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t t0[2], t1[2], t2[2];   // the three e5m2 terms of 8 weights, 4 per word
+            for (int w = 0; w < 2; ++w) {
+              uint32_t hi[2], mid[2], lo[2];
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            uint32_t hi[2], mid[2], lo[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int b = 2 * w + e;
-              float2 pe = y[i][b];
-              pe.x = ex2_fast(pe.x);
-              pe.y = ex2_fast(pe.y);
-              l2[b] = add2(l2[b], pe);
-              const __half2 ph = __floats2half2_rn(pe.x, pe.y);
-              uint32_t r1, r2, r3;
-              hi[e] = e5m2_term(*reinterpret_cast<const uint32_t*>(&ph), r1);
-              mid[e] = e5m2_term(r1, r2);
-              lo[e] = e5m2_term(r2, r3);
+              for (int e = 0; e < 2; ++e) {
+                const int b = 2 * w + e;
+                float2 pe = y[i][b];
+                pe.x = ex2_fast(pe.x);
+                pe.y = ex2_fast(pe.y);
+                l2[b] = add2(l2[b], pe);
+                const __half2 ph = __floats2half2_rn(pe.x, pe.y);
+                uint32_t r1, r2, r3;
+                hi[e] = e5m2_term(*reinterpret_cast<const uint32_t*>(&ph), r1);
+                mid[e] = e5m2_term(r1, r2);
+                lo[e] = e5m2_term(r2, r3);
+              }
+              t0[w] = __byte_perm(hi[0], hi[1], 0x7531);
+              t1[w] = __byte_perm(mid[0], mid[1], 0x7531);
+              t2[w] = __byte_perm(lo[0], lo[1], 0x7531);
             }
-            t0[w] = __byte_perm(hi[0], hi[1], 0x7531);
-            t1[w] = __byte_perm(mid[0], mid[1], 0x7531);
-            t2[w] = __byte_perm(lo[0], lo[1], 0x7531);
-          }
-          if (ok) {
-            // row of 32 heads; 32-byte swizzle: the halves of rows 4..7 of 8 are swapped
-            const int row = 32 * quarter + 8 * i + r4;
-            uint8_t* dst = smem + OFF_P + g * P_BLOCK + row * 32 + ((8 * a) ^ ((row & 4) << 2));
-            *reinterpret_cast<uint2*>(dst) = make_uint2(t0[0], t0[1]);
-            *reinterpret_cast<uint2*>(dst + P_TERM) = make_uint2(t1[0], t1[1]);
-            *reinterpret_cast<uint2*>(dst + 2 * P_TERM) = make_uint2(t2[0], t2[1]);
-            if (i != 2) fence_proxy_async_smem();
-          }
-          if (i != 2) {
-            __syncwarp();
-            if (ok && lane == 0) mbar_arrive(&p_full[i < 2 ? i : 2]);
+            if (ok) {
+              // row of 32 heads; 32-byte swizzle: the halves of rows 4..7 of 8 are swapped
+              const int row = 32 * quarter + 8 * i + r4;
+              uint8_t* dst = smem + OFF_P + g * P_BLOCK + row * 32 + ((8 * a) ^ ((row & 4) << 2));
+              *reinterpret_cast<uint2*>(dst) = make_uint2(t0[0], t0[1]);
+              *reinterpret_cast<uint2*>(dst + P_TERM) = make_uint2(t1[0], t1[1]);
+              *reinterpret_cast<uint2*>(dst + 2 * P_TERM) = make_uint2(t2[0], t2[1]);
+              if (i != 2) fence_proxy_async_smem();
+            }
+            if (i != 2) {
+              __syncwarp();
+              if (ok && lane == 0) mbar_arrive(&p_full[i < 2 ? i : 2]);
+            }
           }
         }
+        if (n == s.n) break;
+        // between runs: the next tile's scores are done, and with them the values before
+        ok = warp_wait(s_full, it & 1, ab, ok);
+        tc_fence_after();
+        if (ok) add_running_sums<false>(p.run, n == kRunTiles, tmem + O_COL + lane_off, sh_sh, run_sh, 32 * g, quarter);
+        named_bar_sync(2, MATH);   // everyone has read the sums' references
+        if (quarter == 0) run_sh[32 * g + lane] = sh_sh[32 * g + lane];
       }
       // ---- the segment's result: sums over the tokens, then TMEM (thread = dim) -> global
 #pragma unroll
@@ -791,6 +833,8 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
       named_bar_sync(2, MATH);
       ok = warp_wait(o_done, seg & 1, ab, ok);
       tc_fence_after();
+      if (s.n > kRunTiles && ok)
+        add_running_sums<true>(p.run, false, tmem + O_COL + lane_off, sh_sh, run_sh, 32 * g, quarter);
       store_segment(p, s, ok, tmem + O_COL + lane_off, inv_sh, 32 * g, quarter, smem + OFF_P + g * 8192, 3 + g);
       tc_fence_before();
     }
@@ -844,7 +888,8 @@ constexpr int OFF_REDM = OFF_QEXP + 96 * 4;       // [4][96] float
 constexpr int OFF_SH = OFF_REDM + 4 * 96 * 4;     // [96] float
 constexpr int OFF_ALPHA = OFF_SH + 96 * 4;        // [96] float
 constexpr int OFF_INV = OFF_ALPHA + 96 * 4;       // [96] float
-constexpr int OFF_BARS = OFF_INV + 96 * 4;
+constexpr int OFF_RUN = OFF_INV + 96 * 4;         // [96] float: SHIFT - reference of the running sums
+constexpr int OFF_BARS = OFF_RUN + 96 * 4;
 constexpr int FILLS = 13;
 constexpr int OFF_MISC = OFF_BARS + 64 * 8;
 constexpr int SMEM_BYTES = OFF_MISC + 64 + 1024;
@@ -917,6 +962,7 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
   float* sh_sh = reinterpret_cast<float*>(smem + OFF_SH);
   float* alpha_sh = reinterpret_cast<float*>(smem + OFF_ALPHA);
   float* inv_sh = reinterpret_cast<float*>(smem + OFF_INV);
+  float* run_sh = reinterpret_cast<float*>(smem + OFF_RUN);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -1065,7 +1111,7 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
         if (!ok) break;
         if (leader) tc_commit(s_full);
         __syncwarp();
-        const uint32_t acc = i > 0 ? 1u : 0u;
+        const uint32_t acc = i % kRunTiles ? 1u : 0u;   // the accumulators start again
         const bool last = i == s.n - 1;
         if (!(ok = warp_wait(&p_full[0], it & 1, ab, ok))) break;
         tc_fence_after();
@@ -1200,151 +1246,160 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
         l2[b] = make_float2(0.f, 0.f);
       }
       float m_ref = -INFINITY;                // quarter 0: reference of column 32 g + lane
-      for (int n = 0; n < s.n; ++n, ++it) {
-        const int j = s.tile(n);
-        const uint8_t* next = record(n + 1, id1);
-        id1 = block(n + 2);
-        fetch_scales(next, it + 1);
-        cp_async_wait_but_one();
-        const bool seen_row = rec != nullptr;
-        // ---- the scores' chunks
+      for (int n = 0;;) {
+        for (const int end = min(s.n, n + kRunTiles); n < end; ++n, ++it) {
+          const int j = s.tile(n);
+          const uint8_t* next = record(n + 1, id1);
+          id1 = block(n + 2);
+          fetch_scales(next, it + 1);
+          cp_async_wait_but_one();
+          const bool seen_row = rec != nullptr;
+          // ---- the scores' chunks
 #pragma unroll 1
-        for (int f = g; f < 9; f += 3) fill(f, seen_row);
-        // ---- softmax (as in the FP8 kernel)
-        ok = warp_wait(s_full, it & 1, ab, ok);
-        tc_fence_after();
-        uint32_t rr[2][16];
-        const uint32_t ts = tmem + S_COL + 32 * g + lane_off;
-        DSA_TMEM_LD_16X256_X4(ts, rr[0]);
-        tmem_wait_ld();
-        DSA_TMEM_LD_16X256_X4(ts + (16u << 16), rr[1]);   // lands while the first half is scaled
-        uint32_t seen = 15u;                  // bit i: token i of this thread is seen
-        if ((j + 1) * kSelTile > plain) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int s0 = j * kSelTile + 32 * quarter + r4 + 8 * i;
-            if (!(s0 <= pos && tree_sees(mrow, p.tree.words, base, s0))) seen &= ~(1u << i);
-          }
-        }
-        float2 y[4][4];
-        auto raw = [&](int i, int b) {
-          return make_float2(__uint_as_float(rr[i >> 1][4 * b + 2 * (i & 1)]),
-                             __uint_as_float(rr[i >> 1][4 * b + 2 * (i & 1) + 1]));
-        };
-        auto logits = [&](int i0) {
-          float mx = -INFINITY;
-#pragma unroll
-          for (int i = i0; i < i0 + 2; ++i) {
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              y[i][b] = fma2(raw(i, b), c2[b], sh2[b]);
-              if (!((seen >> i) & 1u)) y[i][b] = make_float2(-INFINITY, -INFINITY);
-              mx = fmaxf(fmaxf(mx, y[i][b].x), y[i][b].y);
-            }
-          }
-          return mx;
-        };
-        bool moves = n == 0;
-        if (moves) {
+          for (int f = g; f < 9; f += 3) fill(f, seen_row);
+          // ---- softmax (as in the FP8 kernel)
+          ok = warp_wait(s_full, it & 1, ab, ok);
+          tc_fence_after();
+          uint32_t rr[2][16];
+          const uint32_t ts = tmem + S_COL + 32 * g + lane_off;
+          DSA_TMEM_LD_16X256_X4(ts, rr[0]);
           tmem_wait_ld();
-        } else {
-          float mx = logits(0);
-          tmem_wait_ld();
-          mx = fmaxf(mx, logits(2));
-          moves = named_bar_any(1, MATH, mx > SHIFT + TAU);
-        }
-        if (moves) {
-          // P of the tile before has been used (s_full follows its values); some reference moves
-          float hm[8];
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            hm[2 * b] = hm[2 * b + 1] = -INFINITY;
+          DSA_TMEM_LD_16X256_X4(ts + (16u << 16), rr[1]);   // lands while the first half is scaled
+          uint32_t seen = 15u;                  // bit i: token i of this thread is seen
+          if ((j + 1) * kSelTile > plain) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float2 x = raw(i, b);
-              if ((seen >> i) & 1u) {
-                hm[2 * b] = fmaxf(hm[2 * b], x.x * c2[b].x);
-                hm[2 * b + 1] = fmaxf(hm[2 * b + 1], x.y * c2[b].y);
+              const int s0 = j * kSelTile + 32 * quarter + r4 + 8 * i;
+              if (!(s0 <= pos && tree_sees(mrow, p.tree.words, base, s0))) seen &= ~(1u << i);
+            }
+          }
+          float2 y[4][4];
+          auto raw = [&](int i, int b) {
+            return make_float2(__uint_as_float(rr[i >> 1][4 * b + 2 * (i & 1)]),
+                               __uint_as_float(rr[i >> 1][4 * b + 2 * (i & 1) + 1]));
+          };
+          auto logits = [&](int i0) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int i = i0; i < i0 + 2; ++i) {
+#pragma unroll
+              for (int b = 0; b < 4; ++b) {
+                y[i][b] = fma2(raw(i, b), c2[b], sh2[b]);
+                if (!((seen >> i) & 1u)) y[i][b] = make_float2(-INFINITY, -INFINITY);
+                mx = fmaxf(fmaxf(mx, y[i][b].x), y[i][b].y);
               }
             }
+            return mx;
+          };
+          bool moves = n == 0;
+          if (moves) {
+            tmem_wait_ld();
+          } else {
+            float mx = logits(0);
+            tmem_wait_ld();
+            mx = fmaxf(mx, logits(2));
+            moves = named_bar_any(1, MATH, mx > SHIFT + TAU);
           }
+          if (moves) {
+            // P of the tile before has been used (s_full follows its values); some reference moves
+            float hm[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
+            for (int b = 0; b < 4; ++b) {
+              hm[2 * b] = hm[2 * b + 1] = -INFINITY;
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) hm[k] = fmaxf(hm[k], __shfl_xor_sync(0xffffffffu, hm[k], o));
-          if (r4 == 0) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) red[quarter * kMlaHeads + 32 * g + 8 * a + k] = hm[k];
-          }
-          named_bar_sync(2, MATH);
-          if (quarter == 0) {
-            const int n = 32 * g + lane;
-            const float m = fmaxf(fmaxf(red[n], red[kMlaHeads + n]), fmaxf(red[2 * kMlaHeads + n], red[3 * kMlaHeads + n]));
-            float alpha = 1.f;
-            if (m - m_ref > TAU) {   // (exact near TAU, where a sum would be rounded)
-              alpha = exp2f(m_ref - m);
-              m_ref = m;
-            }
-            sh_sh[n] = m_ref == -INFINITY ? INFINITY : SHIFT - m_ref;
-            alpha_sh[n] = alpha;
-          }
-          named_bar_sync(2, MATH);
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const float2 av = *reinterpret_cast<const float2*>(alpha_sh + 32 * g + 8 * a + 2 * b);
-            sh2[b] = *reinterpret_cast<const float2*>(sh_sh + 32 * g + 8 * a + 2 * b);
-            l2[b].x *= av.x;
-            l2[b].y *= av.y;
-          }
-          if (n > 0 && ok) {
-#pragma unroll 1
-            for (int v = 0; v < 4; ++v) {
-#pragma unroll 1
-              for (int cc = 0; cc < 4; ++cc) {
-                uint32_t o[8];
-                const uint32_t ta = tmem + O_COL + 96 * v + 32 * g + 8 * cc + lane_off;
-                DSA_TMEM_LD8(ta, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha_sh[32 * g + 8 * cc + i]);
-                DSA_TMEM_ST8(ta, o);
+              for (int i = 0; i < 4; ++i) {
+                const float2 x = raw(i, b);
+                if ((seen >> i) & 1u) {
+                  hm[2 * b] = fmaxf(hm[2 * b], x.x * c2[b].x);
+                  hm[2 * b + 1] = fmaxf(hm[2 * b + 1], x.y * c2[b].y);
+                }
               }
             }
-            tmem_wait_st();
-          }
-          logits(0);
-          logits(2);
-          cap_weights(y);
-        }
-        tc_fence_before();   // the scores are in registers
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t t0[4];    // 8 weights in fp16
+            for (int k = 0; k < 8; ++k)
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            float2 pe = y[i][b];
-            pe.x = ex2_fast(pe.x);
-            pe.y = ex2_fast(pe.y);
-            l2[b] = add2(l2[b], pe);
-            const __half2 ph = __floats2half2_rn(pe.x, pe.y);
-            t0[b] = *reinterpret_cast<const uint32_t*>(&ph);
-          }
-          if (ok) {
-            // row of 32 heads, 64 bytes; 64-byte swizzle: the 16-byte piece moves by (row / 2) % 4
-            const int row = 32 * quarter + 8 * i + r4;
-            sts128(smem + OFF_P + g * P_BLOCK + row * 64 + ((a ^ ((row >> 1) & 3)) << 4), t0);
-            if (i != 2) fence_proxy_async_smem();
-          }
-          if (i != 2) {
-            __syncwarp();
-            if (ok && lane == 0) mbar_arrive(&p_full[i < 2 ? i : 2]);
-          }
-        }
-        // ---- the values' chunks that did not stay, as the places come free
+              for (int o = 4; o < 32; o <<= 1) hm[k] = fmaxf(hm[k], __shfl_xor_sync(0xffffffffu, hm[k], o));
+            if (r4 == 0) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) red[quarter * kMlaHeads + 32 * g + 8 * a + k] = hm[k];
+            }
+            named_bar_sync(2, MATH);
+            if (quarter == 0) {
+              const int n = 32 * g + lane;
+              const float m = fmaxf(fmaxf(red[n], red[kMlaHeads + n]), fmaxf(red[2 * kMlaHeads + n], red[3 * kMlaHeads + n]));
+              float alpha = 1.f;
+              if (m - m_ref > TAU) {   // (exact near TAU, where a sum would be rounded)
+                alpha = exp2f(m_ref - m);
+                m_ref = m;
+              }
+              sh_sh[n] = m_ref == -INFINITY ? INFINITY : SHIFT - m_ref;
+              alpha_sh[n] = alpha;
+            }
+            named_bar_sync(2, MATH);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              const float2 av = *reinterpret_cast<const float2*>(alpha_sh + 32 * g + 8 * a + 2 * b);
+              sh2[b] = *reinterpret_cast<const float2*>(sh_sh + 32 * g + 8 * a + 2 * b);
+              l2[b].x *= av.x;
+              l2[b].y *= av.y;
+            }
+            if (n > 0 && ok) {
 #pragma unroll 1
-        for (int f = 9 + g; f < FILLS; f += 3) fill(f, seen_row);
-        rec = next;
+              for (int v = 0; v < 4; ++v) {
+#pragma unroll 1
+                for (int cc = 0; cc < 4; ++cc) {
+                  uint32_t o[8];
+                  const uint32_t ta = tmem + O_COL + 96 * v + 32 * g + 8 * cc + lane_off;
+                  DSA_TMEM_LD8(ta, o);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int i = 0; i < 8; ++i)
+                    o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha_sh[32 * g + 8 * cc + i]);
+                  DSA_TMEM_ST8(ta, o);
+                }
+              }
+              tmem_wait_st();
+            }
+            logits(0);
+            logits(2);
+            cap_weights(y);
+          }
+          tc_fence_before();   // the scores are in registers
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t t0[4];    // 8 weights in fp16
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              float2 pe = y[i][b];
+              pe.x = ex2_fast(pe.x);
+              pe.y = ex2_fast(pe.y);
+              l2[b] = add2(l2[b], pe);
+              const __half2 ph = __floats2half2_rn(pe.x, pe.y);
+              t0[b] = *reinterpret_cast<const uint32_t*>(&ph);
+            }
+            if (ok) {
+              // row of 32 heads, 64 bytes; 64-byte swizzle: the 16-byte piece moves by (row / 2) % 4
+              const int row = 32 * quarter + 8 * i + r4;
+              sts128(smem + OFF_P + g * P_BLOCK + row * 64 + ((a ^ ((row >> 1) & 3)) << 4), t0);
+              if (i != 2) fence_proxy_async_smem();
+            }
+            if (i != 2) {
+              __syncwarp();
+              if (ok && lane == 0) mbar_arrive(&p_full[i < 2 ? i : 2]);
+            }
+          }
+          // ---- the values' chunks that did not stay, as the places come free
+#pragma unroll 1
+          for (int f = 9 + g; f < FILLS; f += 3) fill(f, seen_row);
+          rec = next;
+        }
+        if (n == s.n) break;
+        // between runs: the last values of the tile before are done, and with them all of them
+        ok = warp_wait(&event[EV_V1], (it - 1) & 1, ab, ok);
+        tc_fence_after();
+        if (ok) add_running_sums<false>(p.run, n == kRunTiles, tmem + O_COL + lane_off, sh_sh, run_sh, 32 * g, quarter);
+        named_bar_sync(2, MATH);   // everyone has read the sums' references
+        if (quarter == 0) run_sh[32 * g + lane] = sh_sh[32 * g + lane];
       }
       // ---- the segment's result: sums over the tokens, then TMEM (thread = dim) -> global
 #pragma unroll
@@ -1373,6 +1428,8 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
       named_bar_sync(2, MATH);
       ok = warp_wait(o_done, seg & 1, ab, ok);
       tc_fence_after();
+      if (s.n > kRunTiles && ok)
+        add_running_sums<true>(p.run, false, tmem + O_COL + lane_off, sh_sh, run_sh, 32 * g, quarter);
       store_segment(p, s, ok, tmem + O_COL + lane_off, inv_sh, 32 * g, quarter, smem + OFF_P + g * 8192, 3 + g);
       tc_fence_before();
     }

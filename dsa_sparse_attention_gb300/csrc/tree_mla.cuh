@@ -20,6 +20,14 @@ struct TreeShare {
   TreeToken tok;
 };
 
+// The tensor core adds to its fp32 accumulator by truncation: values of one sign lose 2.5e-7 (FP8
+// latents) or 7.5e-7 (NVFP4) of their sum a tile, so a million positions summed in one run came out
+// 0.25 % and 0.6 % small.  After this many tiles the accumulators are added, rounded to nearest, to
+// running sums in fp32 in the workspace, and start again: a run loses less than 2^-11 of its sum
+// (measured: 1e-4 and 3.5e-4, the output's own rounding to bf16 being 1.4e-3 in the mean square).
+constexpr int kRunTiles = 512;
+constexpr int64_t kRunFloats = 4 * kMlaHeads * 128;   // a CTA's running sums
+
 // The work is a list of key tiles (128 positions) in token order: token t's tiles are
 // [starts[t], starts[t + 1]), W = starts[T] in all.  CTA c of G takes the contiguous
 // share [W c / G, W (c + 1) / G); the part of a token inside a share is a segment.  A
@@ -43,6 +51,8 @@ struct TreeMlaParams {
   float* lse;                // [T, 96] or null
   __half* part_o;            // [2 max_ctas, 96, 512], each normalised by its own sum
   float2* part_ml;           // [2 max_ctas, 96]: (max in log2 units, sum)
+  float* run;                // [max_ctas, 4, 96, 128]: running sums of segments of more than kRunTiles tiles
+                             // (null where no token has as many)
   uint32_t* status;
   uint32_t never = 0;        // always 0, which the compiler cannot know (the NVFP4 kernel's fills)
 };
