@@ -378,7 +378,7 @@ cudaError_t launch_cache_free(const FreeParams& p, cudaStream_t st) {
 // the two lists; then the lists, complete, give the remaining counts and the map from
 // old row to new.  The block tables are mapped in the same launch when they are small.
 // Latency bound, barriers of the cluster and round trips to memory: 10.5 us by itself for 600
-// rows, 15 us for 24K.
+// rows, 12 us for 24K and 3.5 for their tables.
 
 // One table entry's row after the moves.
 __device__ __forceinline__ void map_entry(const CompactParams& p, int64_t e) {

@@ -327,13 +327,15 @@ __device__ __forceinline__ void add_running_sums(float* runs, bool first, uint32
 // scores, MN-major for the values).
 //   S^T[token, head] = sum_k c[token, k] . q_term[head, k]      M=128, N=96, K=1152
 //   O^T[dim, head] += V^T[dim, token] . P_term^T[token, head]   M=128 (x4 dim blocks), N=96, K=3 x 128
-// q arrives as two e4m3 terms (mla_q.cuh, exact).  P is the sum of three e5m2 terms,
-// each the nearest to what the ones before it left: off by at most 2^-9 of it, half the
-// error of a bf16 P.  e5m2 is the upper byte of an fp16, so a term is an addition, a mask
-// and a subtraction on two weights at a time, and its range (2^-16 .. 2^15 with the
-// reference at 2^11) keeps weights down to 2^-27 of the largest, which a million
-// positions beside one heavy one need; e4m3 terms would lose those below 2^-18.  The sum
-// of the weights is of the unrounded ones, in fp32.
+// q arrives as two e4m3 terms, exact for values above about 2^-10 of a head's largest, off by at
+// most 2^-17 of the largest below (mla_q.cuh).  P, rounded to fp16 (2^-11 of it, a bf16 P 2^-8), is
+// the sum of three e5m2 terms, each the nearest to what the ones before it left.  e5m2 is the upper
+// byte of an fp16, so a term is an addition, a mask and a subtraction on two weights at a time.
+// With the reference at 2^11 the three terms are the fp16 weight exactly down to 2^-17 of the
+// reference; below, a bit goes per octave (2^-10 of the weight at 2^-18, 2^-3 at 2^-25), and weights
+// below 2^-28 are left out of O while the sum has them: a million positions just under that beside
+// one heavy one lose 2^-8 of the result, one rounding to bf16 (e4m3 terms would lose them from 2^-18
+// on).  The sum of the weights is of the unrounded ones, in fp32.
 // Tokens on TMEM lanes use all four lane quarters and waste no rows (96 heads are N);
 // the price, maxima across lanes, is not paid per tile: weights are taken against a
 // reference per head, and only when some logit exceeds it by 2^4 do the warps reduce the
@@ -345,9 +347,10 @@ __device__ __forceinline__ void add_running_sums(float* runs, bool first, uint32
 // Shared memory holds the query terms (108 KB), one tile (72 KB: four 16 KB slices of
 // 128 dims and an 8 KB slice of the last 64) and P (36 KB).  A slice is refilled as soon
 // as the PV block that reads it is done, with the next tile prefetched into L2 meanwhile.
-// 8 x 6 tokens over 64K: 588 us, 1.12 PFLOP/s, with the SM clock held at about 1,950 MHz by
-// the power limit.  The 84 MMAs of a tile take 4.1K of its 6.7K cycles; the rest is what of
-// the softmax and the slices' refill no second S (TMEM) or tile (shared memory) can hide.
+// 8 x 6 tokens over 64K: 577 us a call, 1.14 PFLOP/s, at the power limit (SM clock about 1,950 of
+// 2,070 MHz).  The 84 MMAs of a tile take 4.1K of its 6.7K cycles; the rest is the softmax and the
+// slices' refill, which the next tile's scores could fill (S is free once it is in registers) if
+// shared memory had a place for its latents beside the query's 108 KB.
 // Roles: warps 0..11 run the softmax and the epilogue (lane quarter w % 4, heads
 // 32 (w / 4) ..); warp 12 issues MMAs; warp 13 loads.
 namespace t8 {
@@ -866,9 +869,9 @@ __global__ void __launch_bounds__(t8::THREADS, 1)
 // thread) make the fills f with f % 3 = g; their rows' scales they fetch a tile ahead,
 // into shared memory.  Warp 12 issues MMAs.
 // Bound by shared memory: the MMAs read 7 KB per 49 cycles (6.6K cycles a tile), the fills
-// write 16 KB each (1.7K), and packed rows and P add about 1K; a tile takes 12.2K, the
+// write 16 KB each (1.7K), and packed rows and P add about 1K; a tile takes 11.8K, the
 // rest is the chain scores -> weights -> values, which four places cannot overlap fully.
-// 16 tokens over 256K: 1,262 us, 694 TFLOP/s.  Rows and scales loaded to registers by the
+// 16 tokens over 256K: 1,255 us a call, 698 TFLOP/s.  Rows and scales loaded to registers by the
 // threads that convert them: 1,470 us (spilled a tile ahead of use, each spill waited).
 namespace t16 {
 constexpr int THREADS = 448;
@@ -1444,7 +1447,7 @@ __global__ void __launch_bounds__(t16::THREADS, 1)
 // 64 threads (8 dims each) for each of PARTS interleaved parts of the partials.  Bound by
 // latency, two rounds of loads: the block reads all (max, sum) pairs at once, and a
 // thread's partials are loaded eight at a time.  212 tokens of 2 or 3 partials: 69 us with a
-// block per head and a pass per pair, XXX us so.
+// block per head and a pass per pair, 22 us so.
 constexpr int kTreeCombThreads = 512;
 constexpr int kTreeCombMax = 256;   // CTAs at most, so partials of a token
 template <int PARTS>

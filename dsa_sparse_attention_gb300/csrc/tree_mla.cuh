@@ -34,7 +34,8 @@ constexpr int64_t kRunFloats = 4 * kMlaHeads * 128;   // a CTA's running sums
 // segment that holds all of its token writes the output; any other writes a partial
 // to the CTA's slot 2c (its first segment) or 2c + 1 (its last), and the combine
 // merges a token's partials in tile order.  With `whole` (DSA_BATCH_INVARIANT) CTA c
-// takes the tokens c, c + G, ... whole.
+// takes the tokens c, c + G, ... whole: one order of summation, and as many CTAs at work as
+// there are tokens (one token over 256K 6.8 ms instead of 72 us, 8 x 6 over 64K 1.7 ms instead of 0.58).
 struct TreeMlaParams {
   PoolView pool;
   BatchView b;
@@ -111,7 +112,7 @@ struct SegmentWalk {
     // The tokens of a request read the same pages, from as many CTAs: each tile is taken at the
     // time (tiles done so far) that equals its place in the context modulo a share, so all of
     // them read a page at the same time and it comes from DRAM about once: 0.48 GB instead of
-    // 1.82 for 8 x 6 tokens over 64K, 588 us instead of 615 (DRAM's power is the tensor cores').
+    // 1.82 for 8 x 6 tokens over 64K, in 4 % less time (DRAM's power is the tensor cores').
     s.rot = (static_cast<int>(g - g0) - s.j0) % period;
     if (s.rot < 0) s.rot += period;
     if (s.rot >= s.n) s.rot = 0;   // no tile of the segment is due now
