@@ -13,7 +13,8 @@ prepare_layer_step_host, the same call with its arguments marshalled once),
 dsa_topk_noalloc, dsa_indexer_front, dsa_write_latent, dsa_selftest_wait_timeout,
 dsa_check, dsa_status_string, dsa_abi_version; for trees of drafted tokens
 dsa_tree_mla, dsa_tree_topk, dsa_tree_commit; for the rows of the cache
-dsa_cache_copy, dsa_cache_fork, dsa_cache_free, dsa_cache_compact.
+dsa_cache_copy, dsa_cache_fork, dsa_cache_free, dsa_cache_compact; for prompts
+dsa_write_tokens, dsa_read_tokens, dsa_prompt_attn.
 """
 import ctypes
 import os
@@ -29,6 +30,9 @@ DSA_MAX_TOPK = 2048
 DSA_BATCH_INVARIANT = 1
 DSA_BATCH_QIDX_MXFP4 = 2
 DSA_HOST_PACKED = 1
+DSA_BF16, DSA_FP16 = 0, 1
+DSA_PROMPT_CAUSAL = 1
+DSA_PROMPT_INVARIANT = 2
 STATUS_NAMES = {0: "DSA_OK", -1: "DSA_ERR_INVALID_ARG", -2: "DSA_ERR_UNSUPPORTED", -3: "DSA_ERR_CUDA",
                 -4: "DSA_ERR_WORKSPACE", -5: "DSA_ERR_TIMEOUT", -6: "DSA_ERR_DEVICE_CHECK"}
 
@@ -64,6 +68,22 @@ class dsa_pages(ctypes.Structure):
     rows = None   # of ref_count, where make_pages knows it
 
 
+class dsa_spans(ctypes.Structure):
+    _fields_ = [("cu", ctypes.c_void_p), ("start", ctypes.c_void_p), ("rows", ctypes.c_int64)]
+    reqs = None   # requests that cu and start cover, where make_spans knows it
+    held = None   # the tensors
+
+
+class dsa_prompt(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_seqs", "heads", "kv_heads", "dim", "shared_dim", "dtype", "flags",
+                                              "reserved")] + \
+               [(n, ctypes.c_int64) for n in ("total_q", "total_k", "max_q", "max_k")] + \
+               [("cu_q", ctypes.c_void_p), ("cu_k", ctypes.c_void_p)] + \
+               [(n, ctypes.c_int64) for n in ("q_token_stride", "q_head_stride", "k_token_stride", "k_head_stride",
+                                              "v_token_stride", "v_head_stride", "shared_stride")]
+    held = None   # (cu_q, cu_k): the tensors, where make_prompt has them
+
+
 class dsa_host_io(ctypes.Structure):
     _fields_ = [("q_idx", ctypes.c_void_p), ("w", ctypes.c_void_p), ("q", ctypes.c_void_p), ("q_req", ctypes.c_void_p),
                 ("q_pos", ctypes.c_void_p), ("ctx_lens", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
@@ -76,6 +96,7 @@ def _load():
     lib = ctypes.CDLL(_LIB_PATH)
     P = ctypes.POINTER
     L, B, R, G = P(dsa_kv_layout), P(dsa_batch), P(dsa_tree), P(dsa_pages)
+    S, Q = P(dsa_spans), P(dsa_prompt)
     vp, i32, i64, sz, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
     sig = {
         "dsa_abi_version": (i32, []),
@@ -101,6 +122,10 @@ def _load():
         "dsa_cache_fork": (i32, [L, G, vp, vp, i32, vp, vp, vp, sz, vp]),
         "dsa_cache_free": (i32, [L, G, vp, i32, vp, sz, vp]),
         "dsa_cache_compact": (i32, [L, G, G, vp, vp, vp, vp, sz, vp]),
+        "dsa_write_tokens": (i32, [L, B, vp, vp, vp, sz, vp]),
+        "dsa_read_tokens": (i32, [L, B, S, vp, vp, vp, sz, vp]),
+        "dsa_prompt_workspace_size": (sz, [Q]),
+        "dsa_prompt_attn": (i32, [Q, vp, vp, vp, vp, f32, vp, vp, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -480,6 +505,121 @@ def dsa_cache_compact(layout, pages, to, copy_src, copy_dst, counts, ws=None, st
                                     _handle(stream))
     if s:
         _check(s, "dsa_cache_compact")
+
+
+def dsa_write_tokens(layout, batch, k_new=None, latent=None, ws=None, stream=None):
+    """The new tokens' index keys (bf16 k_new [T, 128]) and latents (bf16 [T, 576]) quantised into
+    the pages at their positions; either may be left out."""
+    t = batch.num_tokens
+    s = library().dsa_write_tokens(_byref(layout), _byref(batch), _array("k_new", k_new, torch.bfloat16, 128 * t),
+                                   _array("latent", latent, torch.bfloat16, 576 * t), _space(ws), ws.numel(),
+                                   _handle(stream))
+    if s:
+        _check(s, "dsa_write_tokens")
+
+
+def make_spans(cu, start=None, rows=0):
+    """Descriptor of ranges of a batch's requests packed into `rows` rows, over device int32 tensors
+    (kept alive by the descriptor): row cu[r] + i stands for position start[r] + i (start None: 0)."""
+    spans = dsa_spans(_int32("cu", cu, 1), _int32("start", start, 1), int(rows))
+    spans.held = (cu, start)
+    spans.reqs = cu.shape[0] - 1 if start is None else min(cu.shape[0] - 1, start.shape[0])
+    return spans
+
+
+def dsa_read_tokens(layout, batch, spans, k_out=None, latent_out=None, ws=None, stream=None):
+    """The values of the spans' positions out of the pages, as bf16 index keys [rows, 128] and
+    latents [rows, 576]; either may be left out."""
+    if spans.reqs is not None and spans.reqs < batch.num_reqs:
+        raise ValueError("cu must have an element more than the batch has requests, start one for each")
+    n = spans.rows
+    s = library().dsa_read_tokens(_byref(layout), _byref(batch), _byref(spans),
+                                  _array("k_out", k_out, torch.bfloat16, 128 * n),
+                                  _array("latent_out", latent_out, torch.bfloat16, 576 * n), _space(ws), ws.numel(),
+                                  _handle(stream))
+    if s:
+        _check(s, "dsa_read_tokens")
+
+
+_HALF = {torch.bfloat16: DSA_BF16, torch.float16: DSA_FP16}
+
+
+def _heads(name, t, dtype, ndim):
+    """(token stride, head stride) of a device tensor [tokens, heads, dims] whose dims lie one
+    behind the other."""
+    if t.dim() != ndim or t.dtype is not dtype or not t.is_cuda or (t.numel() and t.stride(-1) != 1):
+        raise ValueError(f"{name} must be a device tensor of {dtype} and {ndim} dimensions with contiguous rows")
+    # the stride of a dimension of one element is never used; any valid one will do
+    least = (t.shape[-1] + 7) // 8 * 8
+    return [st if n > 1 else max(least, (st + 7) // 8 * 8) for n, st in zip(t.shape[:-1], t.stride()[:-1])]
+
+
+def make_prompt(cu_q, cu_k, q, k, v, k_shared=None, max_q=None, max_k=None, flags=0):
+    """Descriptor of packed sequences over device int32 tensors cu_q and cu_k [num_seqs + 1] (kept
+    alive by the descriptor) and tensors laid out like q [total_q, heads, dim + shared], k and v
+    [total_k, kv_heads, dim], k_shared [total_k, shared]: their sizes, types and strides.  max_q and
+    max_k bound the sequences' lengths (totals where left out).  flags: DSA_PROMPT_CAUSAL,
+    DSA_PROMPT_INVARIANT."""
+    if q.dtype not in _HALF:
+        raise ValueError("q must be of torch.bfloat16 or torch.float16")
+    (qt, qh), (kt, kh), (vt, vh) = (_heads(n, t, q.dtype, 3) for n, t in (("q", q), ("k", k), ("v", v)))
+    (st,) = _heads("k_shared", k_shared, q.dtype, 2) if k_shared is not None else (0,)
+    shared = k_shared.shape[1] if k_shared is not None else 0
+    if k.shape != v.shape or q.shape[2] != k.shape[2] + shared or (shared and k_shared.shape[0] != k.shape[0]):
+        raise ValueError("k and v must be of one shape, and q's rows as long as k's and k_shared's together")
+    pq, pk = _int32("cu_q", cu_q, 1), _int32("cu_k", cu_k, 1)
+    if cu_q.shape[0] != cu_k.shape[0]:
+        raise ValueError("cu_q and cu_k must be of one length")
+    total_q, total_k = q.shape[0], k.shape[0]
+    prompt = dsa_prompt(cu_q.shape[0] - 1, q.shape[1], k.shape[1], k.shape[2], shared, _HALF[q.dtype], int(flags), 0, total_q,
+                        total_k, total_q if max_q is None else int(max_q), total_k if max_k is None else int(max_k), pq, pk,
+                        qt, qh, kt, kh, vt, vh, st)
+    prompt.held = (cu_q, cu_k)
+    return prompt
+
+
+def dsa_prompt_workspace_size(prompt):
+    return int(library().dsa_prompt_workspace_size(_byref(prompt)))
+
+
+def alloc_prompt_workspace(prompt, device="cuda"):
+    """A zeroed workspace for dsa_prompt_attn."""
+    n = dsa_prompt_workspace_size(prompt)
+    if n == 0:
+        raise DSAError(-1, "dsa_prompt_workspace_size")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def _laid(name, t, dtype, shape, strides):
+    """The address of a device tensor of the shape and strides that make_prompt was given."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor of {dtype} and shape {shape}")
+    got = t.stride()
+    if t.numel() and (got[-1] != 1 or any(n > 1 and a != b for n, a, b in zip(shape, got, strides))):
+        raise ValueError(f"{name} must be laid out like the tensor that make_prompt was given")
+    return t.data_ptr()
+
+
+def dsa_prompt_attn(prompt, q, k, v, sm_scale, out, lse=None, k_shared=None, prev_out=None, prev_lse=None, ws=None,
+                    stream=None):
+    """Attention of packed sequences with the heads' own keys and values; tensors as make_prompt was
+    given them, out [total_q, heads, dim], fp32 lse [total_q, heads].  prev_out and prev_lse: an
+    earlier result over other keys of the same queries, joined with this one's."""
+    p = prompt
+    dt = torch.float16 if p.dtype else torch.bfloat16
+    t, n, d, e = p.total_q, p.total_k, p.dim, p.shared_dim
+    if (k_shared is not None) != (e > 0):
+        raise ValueError("k_shared must be given exactly where make_prompt was given it")
+    rows = t * p.heads
+    s = library().dsa_prompt_attn(
+        _byref(p), _laid("q", q, dt, (t, p.heads, d + e), (p.q_token_stride, p.q_head_stride)),
+        _laid("k", k, dt, (n, p.kv_heads, d), (p.k_token_stride, p.k_head_stride)),
+        _laid("k_shared", k_shared, dt, (n, e), (p.shared_stride,)) if e else None,
+        _laid("v", v, dt, (n, p.kv_heads, d), (p.v_token_stride, p.v_head_stride)), float(sm_scale),
+        _array("prev_out", prev_out, dt, rows * d), _array("prev_lse", prev_lse, torch.float32, rows),
+        _array("out", out, dt, rows * d), _array("lse", lse, torch.float32, rows), _space(ws), ws.numel(), _handle(stream))
+    if s:
+        _check(s, "dsa_prompt_attn")
 
 
 def dsa_check(ws, stream=None):

@@ -12,6 +12,7 @@
 #include "../../include/dsa.h"
 
 #include "cache.cuh"
+#include "prompt.cuh"
 #include "hostcopy.cuh"
 #include "mla_q.cuh"
 #include "params.cuh"
@@ -358,6 +359,99 @@ TreeWs plan_tree_ws(const dsa_kv_layout* l, const dsa_batch* b) {
   w.runs = cdiv(b->max_ctx_len, kSelTile) > kRunTiles;
   w.total = align_up(w.run + (w.runs ? size_t(num_sms()) * kRunFloats * sizeof(float) : 0));
   return w;
+}
+
+// ------------------------------------------------------------------ prompts
+
+bool stride_ok(int64_t stride, int64_t least) {
+  return stride >= least && (stride & 7) == 0 && stride < (int64_t(1) << 38);
+}
+
+dsa_status check_prompt(const dsa_prompt* p) {
+  constexpr int64_t kMost = (int64_t(1) << 31) - 1;
+  if (!p || p->reserved != 0 || p->num_seqs < 1 || p->num_seqs > (1 << 24) || !p->cu_q || !p->cu_k ||
+      !aligned4(p->cu_q) || !aligned4(p->cu_k))
+    return DSA_ERR_INVALID_ARG;
+  if (p->heads < 1 || p->kv_heads < 1 || p->heads % p->kv_heads || (p->flags & ~(DSA_PROMPT_CAUSAL | DSA_PROMPT_INVARIANT)) ||
+      (p->dtype != DSA_BF16 && p->dtype != DSA_FP16))
+    return DSA_ERR_INVALID_ARG;
+  if ((p->dim != 64 && p->dim != 128) || (p->shared_dim != 0 && p->shared_dim != 64) ||
+      p->heads / p->kv_heads > kPromptRows || p->heads > 65536)
+    return DSA_ERR_UNSUPPORTED;
+  if (p->total_q < 0 || p->total_k < 0 || p->total_q > kMost || p->total_k > kMost || p->max_q < 0 || p->max_k < 0 ||
+      p->max_q > kMost || p->max_k > kMost)
+    return DSA_ERR_INVALID_ARG;
+  if (p->total_q * p->heads > (int64_t(1) << 33)) return DSA_ERR_UNSUPPORTED;   // rows of the merge
+  if (!stride_ok(p->q_token_stride, p->dim + p->shared_dim) || !stride_ok(p->q_head_stride, p->dim + p->shared_dim) ||
+      !stride_ok(p->k_token_stride, p->dim) || !stride_ok(p->k_head_stride, p->dim) ||
+      !stride_ok(p->v_token_stride, p->dim) || !stride_ok(p->v_head_stride, p->dim) ||
+      (p->shared_dim && !stride_ok(p->shared_stride, p->shared_dim)))
+    return DSA_ERR_INVALID_ARG;
+  return DSA_OK;
+}
+
+// How dsa_prompt_attn divides a batch.
+struct PromptPlan {
+  int64_t pairs = 0;    // upper bound of the pairs of query tiles of one key head
+  int nparts = 1;
+  int part_keys = 0;
+  size_t part_o = 0, part_lse = 0, total = 0;
+};
+
+PromptPlan plan_prompt(const dsa_prompt* p) {
+  PromptPlan w;
+  const int pair = 2 * (kPromptRows / (p->heads / p->kv_heads));
+  const int64_t seqs = p->num_seqs < p->total_q ? p->num_seqs : p->total_q;
+  w.pairs = p->total_q / pair + seqs;
+  const int64_t by_len = seqs * cdiv(p->max_q, pair);
+  if (by_len < w.pairs) w.pairs = by_len;
+  // Too few tiles for the GPU: the keys of every sequence in parts of `part_keys`, at least 512,
+  // so that about two CTAs an SM share the work.
+  const int64_t ctas = w.pairs * p->kv_heads, sms = num_sms();
+  if (ctas > 0 && ctas < sms && p->max_k > 512 && !(p->flags & DSA_PROMPT_INVARIANT)) {
+    const int64_t want = cdiv(2 * sms, ctas);
+    int64_t keys = cdiv(cdiv(p->max_k, want), kPromptKeys) * kPromptKeys;
+    if (keys < 512) keys = 512;
+    w.part_keys = static_cast<int>(keys);
+    w.nparts = static_cast<int>(cdiv(p->max_k, keys));
+  }
+  w.part_o = kStatusBytes;
+  w.part_lse = w.total = kStatusBytes;
+  if (w.nparts > 1) {
+    const size_t rows = size_t(w.nparts) * size_t(p->total_q) * size_t(p->heads);
+    w.part_lse = align_up(w.part_o + rows * size_t(p->dim) * 4);
+    w.total = align_up(w.part_lse + rows * 4);
+  }
+  return w;
+}
+
+// Rows of 16-bit values of `heads` heads, {64 of a row's dims, `box_heads` heads, 1 of `outer`
+// groups of heads, `rows` rows} a box, 128-byte swizzle.
+bool make_heads_map(CUtensorMap* m, const void* base, bool fp16, int dims_of, int group, int groups, int64_t rows,
+                    int64_t head_stride, int64_t token_stride, int box_rows) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[4] = {cuuint64_t(dims_of), cuuint64_t(group), cuuint64_t(groups), cuuint64_t(rows)};
+  cuuint64_t strides[3] = {cuuint64_t(head_stride) * 2, cuuint64_t(head_stride) * 2 * cuuint64_t(group), cuuint64_t(token_stride) * 2};
+  cuuint32_t box[4] = {64, cuuint32_t(group), 1, cuuint32_t(box_rows)};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return enc(m, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
+             strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The same for one head's keys or values ({dims, heads, rows}).
+bool make_keys_map(CUtensorMap* m, const void* base, bool fp16, int dims_of, int heads, int64_t rows, int64_t head_stride,
+                   int64_t token_stride, int box_rows) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {cuuint64_t(dims_of), cuuint64_t(heads), cuuint64_t(rows)};
+  cuuint64_t strides[2] = {cuuint64_t(head_stride) * 2, cuuint64_t(token_stride) * 2};
+  cuuint32_t box[3] = {64, 1, cuuint32_t(box_rows)};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+             strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Workspace of the calls on the cache's rows.
@@ -1116,6 +1210,113 @@ dsa_status dsa_cache_compact(const dsa_kv_layout* layout, const dsa_pages* from,
   p.remap = at<int32_t>(workspace, wl.rows);
   p.status = static_cast<uint32_t*>(workspace);
   return cuda_status(launch_cache_compact(p, num_sms(), stream));
+}
+
+dsa_status dsa_write_tokens(const dsa_kv_layout* layout, const dsa_batch* batch, const void* k_new, const void* latent,
+                            void* workspace, size_t workspace_bytes, dsa_stream_t stream) {
+  dsa_status s = check_layout(layout);
+  if (s != DSA_OK) return s;
+  if ((s = check_batch(batch, layout->block_size)) != DSA_OK) return s;
+  if (!aligned16(k_new) || !aligned16(latent)) return DSA_ERR_INVALID_ARG;
+  if ((s = check_ws_bytes(workspace, workspace_bytes, kStatusBytes)) != DSA_OK) return s;
+  if (batch->num_tokens == 0 || (!k_new && !latent)) return DSA_OK;
+  WriteTokensParams p;
+  p.b = batch_view(batch);
+  p.pool = pool_view(layout);
+  p.k_new = static_cast<const __nv_bfloat16*>(k_new);
+  p.latent = static_cast<const __nv_bfloat16*>(latent);
+  p.pool_w = static_cast<uint8_t*>(const_cast<void*>(layout->pool));
+  p.status = static_cast<uint32_t*>(workspace);
+  return cuda_status(launch_write_tokens(p, stream));
+}
+
+dsa_status dsa_read_tokens(const dsa_kv_layout* layout, const dsa_batch* batch, const dsa_spans* spans, void* k_out,
+                           void* latent_out, void* workspace, size_t workspace_bytes, dsa_stream_t stream) {
+  dsa_status s = check_layout(layout);
+  if (s != DSA_OK) return s;
+  if (!batch || batch->num_reqs < 1 || !batch->ctx_lens || !batch->block_table || batch->bt_stride < 1 ||
+      batch->max_ctx_len < 1 || batch->max_ctx_len > (int64_t(1) << 30) ||
+      batch->max_ctx_len > int64_t(batch->bt_stride) * layout->block_size)
+    return DSA_ERR_INVALID_ARG;
+  if (!spans || !spans->cu || !aligned4(spans->cu) || !aligned4(spans->start) || spans->rows < 0 ||
+      spans->rows >= (int64_t(1) << 31) || !aligned16(k_out) || !aligned16(latent_out))
+    return DSA_ERR_INVALID_ARG;
+  if ((s = check_ws_bytes(workspace, workspace_bytes, kStatusBytes)) != DSA_OK) return s;
+  if (spans->rows == 0 || (!k_out && !latent_out)) return DSA_OK;
+  ReadTokensParams p;
+  p.b = batch_view(batch);
+  p.pool = pool_view(layout);
+  p.cu = spans->cu;
+  p.start = spans->start;
+  p.rows = spans->rows;
+  p.k_out = static_cast<__nv_bfloat16*>(k_out);
+  p.lat_out = static_cast<__nv_bfloat16*>(latent_out);
+  p.status = static_cast<uint32_t*>(workspace);
+  return cuda_status(launch_read_tokens(p, stream));
+}
+
+size_t dsa_prompt_workspace_size(const dsa_prompt* prompt) {
+  return check_prompt(prompt) == DSA_OK ? plan_prompt(prompt).total : 0;
+}
+
+dsa_status dsa_prompt_attn(const dsa_prompt* prompt, const void* q, const void* k, const void* k_shared, const void* v,
+                           float sm_scale, const void* prev_out, const float* prev_lse, void* out, float* lse,
+                           void* workspace, size_t workspace_bytes, dsa_stream_t stream) {
+  dsa_status s = check_prompt(prompt);
+  if (s != DSA_OK) return s;
+  if (!std::isfinite(sm_scale) || sm_scale <= 0.f || !prev_out != !prev_lse) return DSA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(k_shared) || !aligned16(v) || !aligned16(prev_out) || !aligned16(out) ||
+      !aligned4(prev_lse) || !aligned4(lse) || (!prompt->shared_dim && k_shared))
+    return DSA_ERR_INVALID_ARG;
+  const bool no_keys = prompt->total_k == 0;
+  if (prompt->total_q > 0 && (!q || !out || (!no_keys && (!k || !v || (prompt->shared_dim && !k_shared)))))
+    return DSA_ERR_INVALID_ARG;
+  const PromptPlan w = plan_prompt(prompt);
+  if ((s = check_ws_bytes(workspace, workspace_bytes, w.total)) != DSA_OK) return s;
+  const int64_t grid = w.pairs * prompt->kv_heads * w.nparts;
+  if (grid > (int64_t(1) << 31) - 1) return DSA_ERR_UNSUPPORTED;
+  if (grid == 0) return DSA_OK;
+  const int group = prompt->heads / prompt->kv_heads, dim = prompt->dim;
+  const bool fp16 = prompt->dtype == DSA_FP16;
+  PromptParams p;
+  p.cu_q = prompt->cu_q;
+  p.cu_k = prompt->cu_k;
+  p.B = prompt->num_seqs;
+  p.heads = prompt->heads;
+  p.kv_heads = prompt->kv_heads;
+  p.group = group;
+  p.tile_toks = kPromptRows / group;
+  p.causal = (prompt->flags & DSA_PROMPT_CAUSAL) ? 1 : 0;
+  p.total_q = prompt->total_q;
+  p.total_k = prompt->total_k;
+  p.max_q = prompt->max_q;
+  p.max_k = prompt->max_k;
+  p.scale_log2 = sm_scale * 1.4426950408889634f;
+  p.nparts = w.nparts;
+  p.part_keys = w.part_keys;
+  p.out = out;
+  p.lse = lse;
+  p.prev_out = prev_out;
+  p.prev_lse = prev_lse;
+  p.part_o = at<float>(workspace, w.part_o);
+  p.part_lse = at<float>(workspace, w.part_lse);
+  p.status = at<uint32_t>(workspace, 0);
+  // without keys the maps of k and v are made over q, and nothing is loaded through them
+  const int64_t rows = no_keys ? 1 : prompt->total_k;
+  PromptMaps m;
+  if (!make_heads_map(&m.q, q, fp16, dim + prompt->shared_dim, group, prompt->kv_heads, prompt->total_q, prompt->q_head_stride,
+                      prompt->q_token_stride, p.tile_toks) ||
+      !make_keys_map(&m.k, no_keys ? q : k, fp16, dim, prompt->kv_heads, rows, prompt->k_head_stride, prompt->k_token_stride,
+                     kPromptKeys) ||
+      !make_keys_map(&m.v, no_keys ? q : v, fp16, dim, prompt->kv_heads, rows, prompt->v_head_stride, prompt->v_token_stride,
+                     dim == 128 ? 64 : kPromptKeys))
+    return encode_fail();
+  m.ks = m.k;
+  if (prompt->shared_dim &&
+      !make_keys_map(&m.ks, no_keys ? q : k_shared, fp16, prompt->shared_dim, 1, rows, prompt->shared_stride,
+                     prompt->shared_stride, kPromptKeys))
+    return encode_fail();
+  return cuda_status(launch_prompt_attn(m, p, dim, prompt->shared_dim, fp16, grid, stream));
 }
 
 dsa_status dsa_check(void* workspace, size_t workspace_bytes, dsa_stream_t stream) {

@@ -1,0 +1,64 @@
+// prompt.cuh — parameter blocks and launchers of the prompt calls (prompt.cu, tokens.cu).
+#pragma once
+#include "params.cuh"
+
+namespace dsa {
+
+// Query rows of one MMA tile (its M).  A row is a (token, head of the key head's group), so
+// the heads that share keys share a tile and its reads.
+constexpr int kPromptRows = 128;
+constexpr int kPromptKeys = 128;   // keys per tile
+
+struct PromptParams {
+  const int32_t* cu_q;     // [B + 1]
+  const int32_t* cu_k;     // [B + 1]
+  int32_t B;
+  int32_t heads, kv_heads;
+  int32_t group;           // heads / kv_heads
+  int32_t tile_toks;       // tokens of a tile: 128 / group
+  int32_t causal;
+  int64_t total_q, total_k;
+  int64_t max_q, max_k;
+  float scale_log2;        // sm_scale * log2(e)
+  int32_t nparts;          // parts that the keys of a sequence are cut into
+  int32_t part_keys;       // keys of a part (a multiple of 128)
+  void* out;               // [total_q, heads, D]
+  float* lse;              // [total_q, heads] or null
+  const void* prev_out;    // [total_q, heads, D] or null
+  const float* prev_lse;
+  float* part_o;           // [nparts, total_q, heads, D] (nparts > 1), normalised
+  float* part_lse;         // [nparts, total_q, heads], log2 units
+  uint32_t* status;
+};
+
+struct PromptMaps {
+  CUtensorMap q, k, ks, v;
+};
+
+cudaError_t launch_prompt_attn(const PromptMaps& maps, const PromptParams& p, int dim, int shared_dim, bool fp16,
+                               int64_t grid, cudaStream_t st);
+
+struct WriteTokensParams {
+  BatchView b;
+  PoolView pool;
+  const __nv_bfloat16* k_new;    // [T, 128] or null
+  const __nv_bfloat16* latent;   // [T, 576] or null
+  uint8_t* pool_w;
+  uint32_t* status;
+};
+
+struct ReadTokensParams {
+  BatchView b;
+  PoolView pool;
+  const int32_t* cu;       // [B + 1]
+  const int32_t* start;    // [B] or null
+  int64_t rows;
+  __nv_bfloat16* k_out;    // [rows, 128] or null
+  __nv_bfloat16* lat_out;  // [rows, 576] or null
+  uint32_t* status;
+};
+
+cudaError_t launch_write_tokens(const WriteTokensParams& p, cudaStream_t st);
+cudaError_t launch_read_tokens(const ReadTokensParams& p, cudaStream_t st);
+
+}  // namespace dsa

@@ -518,6 +518,110 @@ dsa_status dsa_cache_compact(const dsa_kv_layout *layout, const dsa_pages *from,
                              size_t workspace_bytes, dsa_stream_t stream);
 
 /*
+ * Prompts over the cache.  A prompt of up to 2,048 tokens selects every token, so it needs no
+ * indexer; its attention is done in per-head form (each head's keys and values expanded from
+ * the latents by the caller's projections), as is a chunk's attention to a context that is
+ * read back from the cache.  dsa_write_tokens puts the new tokens' records where the decode
+ * calls above read them; the vLLM post describes no such calls.
+ */
+
+/*
+ * The new tokens' records into the cache, both pages in one call: the index key of query
+ * token t by the rules of dsa_indexer_front, its latent by those of dsa_write_latent, at
+ * position q_pos[t] of request q_req[t].  A token with q_req[t] < 0 is padding: nothing is
+ * written for it.  Two tokens must not name one position.
+ *  k_new    : device bf16 [T, 128] or NULL (no keys are written);  latent: device bf16
+ *             [T, 576] or NULL;  both 16-byte aligned, finite
+ *  workspace: only its status word is used (>= 256 bytes); a block id or position out of
+ *             range is recorded there and nothing is written for it
+ */
+dsa_status dsa_write_tokens(const dsa_kv_layout *layout, const dsa_batch *batch, const void *k_new, const void *latent,
+                            void *workspace, size_t workspace_bytes, dsa_stream_t stream);
+
+/* Ranges of the batch's requests, packed one behind the other: row cu[r] + i, i < cu[r + 1] -
+ * cu[r], stands for position start[r] + i of request r.  B is the batch's num_reqs. */
+typedef struct {
+  const int32_t *cu;      /* device [B + 1], ascending, cu[B] <= rows */
+  const int32_t *start;   /* device [B], or NULL: every range starts at position 0 */
+  int64_t rows;           /* rows of the outputs, 0 .. 2^31 - 1; those outside cu[0] .. cu[B] are left as they are */
+} dsa_spans;
+
+/*
+ * The values of cached positions, as the decode calls above use them, rounded once to bf16
+ * (latents of both formats and MXFP4 keys are exact in bf16): code * scale.
+ *  batch    : num_reqs, ctx_lens, block_table, bt_stride and max_ctx_len are read; positions
+ *             must lie below ctx_lens[r]
+ *  k_out    : device bf16 [rows, 128] or NULL;  latent_out: device bf16 [rows, 576] or NULL;
+ *             both 16-byte aligned
+ *  workspace: only its status word is used (>= 256 bytes); a block id or position out of
+ *             range is recorded there and its row left as it is
+ */
+dsa_status dsa_read_tokens(const dsa_kv_layout *layout, const dsa_batch *batch, const dsa_spans *spans, void *k_out,
+                           void *latent_out, void *workspace, size_t workspace_bytes, dsa_stream_t stream);
+
+/*
+ * Packed sequences with the heads' own keys and values.  The queries of sequence r are rows
+ * cu_q[r] .. cu_q[r + 1] - 1 of q, its keys and values rows cu_k[r] .. cu_k[r + 1] - 1 of k
+ * and v; with lq and lk of each, query i sits at key position i + lk - lq.  Query head h
+ * uses key head h / (heads / kv_heads).  Element x of head h of row t of q is at t *
+ * q_token_stride + h * q_head_stride + x, likewise of k and v; strides are in elements,
+ * multiples of 8, at least the dims of a row.  dims `dim` .. `dim + shared_dim - 1` of a query
+ * meet k_shared[s, :], which all heads have in common (with latents of 576 dims whose last 64
+ * are not projected: k_shared = latent + 512, shared_stride = 576).
+ * Device arrays must ascend, begin at 0 or above and end at total_q / total_k or below, and
+ * no sequence may be longer than max_q / max_k; a sequence that breaks this is recorded in
+ * the status word and its outputs left as they are.
+ */
+enum { DSA_BF16 = 0, DSA_FP16 = 1 };
+#define DSA_PROMPT_CAUSAL 1      /* query i sees keys s <= i + lk - lq only */
+#define DSA_PROMPT_INVARIANT 2   /* a row's result does not depend on the batch, see below */
+typedef struct {
+  int32_t num_seqs;              /* >= 1 */
+  int32_t heads, kv_heads;       /* heads a multiple of kv_heads, heads / kv_heads <= 128 */
+  int32_t dim;                   /* 64 or 128 */
+  int32_t shared_dim;            /* 0 or 64 */
+  int32_t dtype;                 /* DSA_BF16 or DSA_FP16: q, k, k_shared, v, out and prev_out */
+  int32_t flags;                 /* DSA_PROMPT_* bits */
+  int32_t reserved;              /* must be 0 */
+  int64_t total_q, total_k;      /* rows of q and of k and v, 0 .. 2^31 - 1 */
+  int64_t max_q, max_k;          /* host-side upper bounds of a sequence's lengths, used for sizing */
+  const int32_t *cu_q, *cu_k;    /* device [num_seqs + 1] */
+  int64_t q_token_stride, q_head_stride;
+  int64_t k_token_stride, k_head_stride;
+  int64_t v_token_stride, v_head_stride;
+  int64_t shared_stride;         /* of k_shared, per token */
+} dsa_prompt;
+
+/* Bytes of workspace dsa_prompt_attn needs (256-byte aligned, zeroed once); 0 on invalid arguments. */
+size_t dsa_prompt_workspace_size(const dsa_prompt *prompt);
+
+/*
+ * Attention of packed sequences: for each query row i of a sequence and head h, over the keys
+ * s that it sees (s < lk, causal or not),
+ *   logit(s) = sm_scale * (q[i, h, :dim] . k[s, g, :] + q[i, h, dim:] . k_shared[s, :])
+ *   out[i, h, :] = sum_s softmax(logit)(s) * v[s, g, :],  lse[i, h] = ln sum_s exp(logit(s))
+ * A row that sees nothing has out 0 and lse -inf.  With prev_out and prev_lse (an earlier
+ * call's results for the same queries over other keys) the two are joined as if one call had
+ * seen both: L = ln(e^prev_lse + e^lse), out = e^(prev_lse - L) prev_out + e^(lse - L) out, lse
+ * = L; a prev_lse of -inf leaves prev_out unread.  prev_out and prev_lse may be out and lse.
+ *  q: device [total_q, heads, dim + shared_dim];  k, v: device [total_k, kv_heads, dim]
+ *  (NULL allowed when total_k is 0);  k_shared: device [total_k, shared_dim], NULL exactly when
+ *  shared_dim is 0;  out: device [total_q, heads, dim], contiguous;  lse: device fp32
+ *  [total_q, heads] or NULL;  prev_out, prev_lse: as out and lse, both or neither
+ *  All of them 16-byte aligned (lse and prev_lse 4-byte).  sm_scale > 0, finite.
+ * The rows of a sequence must be finite, and so must its logits be; what stands in rows of no
+ * sequence (NaN included) never reaches a result, and their rows of out and lse are left as
+ * they are.  Weights are rounded to the inputs' type, sums are fp32.
+ * Where the batch has too few rows to fill the GPU, the keys are split over more CTAs and
+ * merged; how depends on the batch and the GPU.  With DSA_PROMPT_INVARIANT nothing is split,
+ * and a row's result depends on its query and its sequence's keys alone.
+ * A workspace serves one call at a time, as above.
+ */
+dsa_status dsa_prompt_attn(const dsa_prompt *prompt, const void *q, const void *k, const void *k_shared, const void *v,
+                           float sm_scale, const void *prev_out, const float *prev_lse, void *out, float *lse,
+                           void *workspace, size_t workspace_bytes, dsa_stream_t stream);
+
+/*
  * Synchronises `stream`, reads the workspace status word written by earlier
  * calls, clears it, and returns DSA_OK, DSA_ERR_TIMEOUT or DSA_ERR_DEVICE_CHECK.
  */
