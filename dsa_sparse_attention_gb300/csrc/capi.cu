@@ -392,7 +392,8 @@ dsa_status check_prompt(const dsa_prompt* p) {
 
 // How dsa_prompt_attn divides a batch.
 struct PromptPlan {
-  int64_t pairs = 0;    // upper bound of the pairs of query tiles of one key head
+  int ctas = 2;         // CTAs of an item, tiles of which are ctas * ctas
+  int64_t blocks = 0;   // upper bound of the blocks of queries of one key head
   int nparts = 1;
   int part_keys = 0;
   size_t part_o = 0, part_lse = 0, total = 0;
@@ -400,15 +401,19 @@ struct PromptPlan {
 
 PromptPlan plan_prompt(const dsa_prompt* p) {
   PromptPlan w;
-  const int pair = 2 * (kPromptRows / (p->heads / p->kv_heads));
+  const int tile = kPromptRows / (p->heads / p->kv_heads);
+  const bool fixed = p->flags & DSA_PROMPT_INVARIANT;
+  // one tile holds every sequence's rows: a single CTA, its two softmaxes on alternate key tiles
+  if (!fixed && p->max_q <= tile) w.ctas = 1;
+  const int span = w.ctas * w.ctas * tile;
   const int64_t seqs = p->num_seqs < p->total_q ? p->num_seqs : p->total_q;
-  w.pairs = p->total_q / pair + seqs;
-  const int64_t by_len = seqs * cdiv(p->max_q, pair);
-  if (by_len < w.pairs) w.pairs = by_len;
-  // Too few tiles for the GPU: the keys of every sequence in parts of `part_keys`, at least 512,
+  w.blocks = p->total_q / span + seqs;
+  const int64_t by_len = seqs * cdiv(p->max_q, span);
+  if (by_len < w.blocks) w.blocks = by_len;
+  // Too few items for the GPU: the keys of every sequence in parts of `part_keys`, at least 512,
   // so that about two CTAs an SM share the work.
-  const int64_t ctas = w.pairs * p->kv_heads, sms = num_sms();
-  if (ctas > 0 && ctas < sms && p->max_k > 512 && !(p->flags & DSA_PROMPT_INVARIANT)) {
+  const int64_t ctas = w.blocks * p->kv_heads * w.ctas, sms = num_sms();
+  if (ctas > 0 && ctas < sms && p->max_k > 512 && !fixed) {
     const int64_t want = cdiv(2 * sms, ctas);
     int64_t keys = cdiv(cdiv(p->max_k, want), kPromptKeys) * kPromptKeys;
     if (keys < 512) keys = 512;
@@ -440,17 +445,19 @@ bool make_heads_map(CUtensorMap* m, const void* base, bool fp16, int dims_of, in
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The same for one head's keys or values ({dims, heads, rows}).
+// The same for one head's keys or values ({dims, heads, rows}), `width` of a row's dims a box (64,
+// or 32 with a 64-byte swizzle).
 bool make_keys_map(CUtensorMap* m, const void* base, bool fp16, int dims_of, int heads, int64_t rows, int64_t head_stride,
-                   int64_t token_stride, int box_rows) {
+                   int64_t token_stride, int box_rows, int width) {
   auto enc = encode_fn();
   if (!enc) return false;
   cuuint64_t dims[3] = {cuuint64_t(dims_of), cuuint64_t(heads), cuuint64_t(rows)};
   cuuint64_t strides[2] = {cuuint64_t(head_stride) * 2, cuuint64_t(token_stride) * 2};
-  cuuint32_t box[3] = {64, 1, cuuint32_t(box_rows)};
+  cuuint32_t box[3] = {cuuint32_t(width), 1, cuuint32_t(box_rows)};
   cuuint32_t es[3] = {1, 1, 1};
   return enc(m, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
-             strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, width == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1273,9 +1280,9 @@ dsa_status dsa_prompt_attn(const dsa_prompt* prompt, const void* q, const void* 
     return DSA_ERR_INVALID_ARG;
   const PromptPlan w = plan_prompt(prompt);
   if ((s = check_ws_bytes(workspace, workspace_bytes, w.total)) != DSA_OK) return s;
-  const int64_t grid = w.pairs * prompt->kv_heads * w.nparts;
-  if (grid > (int64_t(1) << 31) - 1) return DSA_ERR_UNSUPPORTED;
-  if (grid == 0) return DSA_OK;
+  const int64_t items = w.blocks * prompt->kv_heads * w.nparts;
+  if (items > (int64_t(1) << 30) - 1) return DSA_ERR_UNSUPPORTED;   // the launch grid
+  if (items == 0) return DSA_OK;
   const int group = prompt->heads / prompt->kv_heads, dim = prompt->dim;
   const bool fp16 = prompt->dtype == DSA_FP16;
   PromptParams p;
@@ -1307,16 +1314,16 @@ dsa_status dsa_prompt_attn(const dsa_prompt* prompt, const void* q, const void* 
   if (!make_heads_map(&m.q, q, fp16, dim + prompt->shared_dim, group, prompt->kv_heads, prompt->total_q, prompt->q_head_stride,
                       prompt->q_token_stride, p.tile_toks) ||
       !make_keys_map(&m.k, no_keys ? q : k, fp16, dim, prompt->kv_heads, rows, prompt->k_head_stride, prompt->k_token_stride,
-                     kPromptKeys) ||
+                     kPromptKeys / w.ctas, 64) ||
       !make_keys_map(&m.v, no_keys ? q : v, fp16, dim, prompt->kv_heads, rows, prompt->v_head_stride, prompt->v_token_stride,
-                     dim == 128 ? 64 : kPromptKeys))
+                     kPromptKeys, dim / w.ctas < 64 ? dim / w.ctas : 64))
     return encode_fail();
   m.ks = m.k;
   if (prompt->shared_dim &&
       !make_keys_map(&m.ks, no_keys ? q : k_shared, fp16, prompt->shared_dim, 1, rows, prompt->shared_stride,
-                     prompt->shared_stride, kPromptKeys))
+                     prompt->shared_stride, kPromptKeys / w.ctas, 64))
     return encode_fail();
-  return cuda_status(launch_prompt_attn(m, p, dim, prompt->shared_dim, fp16, grid, stream));
+  return cuda_status(launch_prompt_attn(m, p, dim, prompt->shared_dim, fp16, w.ctas, items, stream));
 }
 
 dsa_status dsa_check(void* workspace, size_t workspace_bytes, dsa_stream_t stream) {

@@ -4,13 +4,19 @@
 //   logit(i, s) = scale * (q_i . [k_s | k_shared_s]),  out_i = sum_s softmax(logit)(s) v_s
 //
 // over the keys s of the query's sequence (causal: s <= i + lk - lq), 2 (2 D + E) operations
-// per pair and head.  One CTA takes two tiles of 128 query rows of one key head and walks the
-// keys 128 at a time; a row is a (token, head of the group), so grouped heads fill a tile with
-// fewer tokens and each key is read once for all of them.  Both products run on the tensor
-// cores (tcgen05, M = 128 rows): S = Q.K^T into TMEM, the softmax in registers (a thread owns
-// a row, so no exchange between lanes), P rounded to the inputs' type back into TMEM over S's
-// own columns, O += P.V with P as the TMEM operand.  While one tile's softmax runs, the
-// tensor core works on the other's products.  TMEM is full: two S of 128 columns, two O of D.
+// per pair and head.  A row of a tile is a (token, head of the key head's group), so grouped
+// heads fill a tile with fewer tokens and each key is read once for all of them.  Both products
+// run on the tensor cores: S = Q.K^T into TMEM, the softmax in registers (a thread owns a row,
+// so no exchange between lanes), P rounded to the inputs' type back into TMEM over S's own
+// columns, O += P.V with P as the TMEM operand.  Two S are in flight: while one's softmax runs,
+// the tensor core works on the other's products.  TMEM is full: two S of 128 columns, two O.
+//
+//  - Many rows (CTAS = 2): a pair of CTAs takes 512 rows, two tiles of 256, and each holds half
+//    of every key and value tile.  One CTA alone reads 8 KB of shared memory in the 64 cycles of
+//    an M = N = 128, K = 16 product of two shared operands, all that shared memory gives, with
+//    the next tiles' copies on top; of a pair each reads 6 KB, and loads half.
+//  - Few rows (CTAS = 1): one CTA takes one tile of 128 rows; the two S are consecutive key
+//    tiles, each with an O and a sum of its own, merged at the end.
 //
 // The softmax keeps a reference per row that moves only when a logit exceeds it by 2^8 (the
 // sums and O are then scaled); a weight is at most 2^8 (bf16) or 2^15 (fp16, whose weights
@@ -24,29 +30,36 @@
 namespace dsa {
 
 namespace prompt {
-constexpr int CHUNK = 16384;          // 128 rows x 64 values of 16 bits
-constexpr int SOFTMAX_WARPS = 8;      // four per query tile
-constexpr int MMA_WARP = 8, LOAD_WARP = 9, WARPS = 12;
+constexpr int SOFTMAX_WARPS = 8;      // four per S
+constexpr int MMA_WARP = 8, LOAD_WARP = 10, WARPS = 12;   // MMA_WARP and the next: S_0's and S_1's
 constexpr int THREADS = WARPS * 32;
-constexpr int MISC = 1024;            // barriers and scalars
+constexpr int MISC = 3072;            // barriers and scalars, and 2 KB of references and sums
 constexpr int SMEM_MAX = 232448;
 constexpr float GROW = 8.f;           // log2 units a logit may exceed the reference by
 
-template <int D, int E>
+template <int D, int E, int CTAS>
 struct Shape {
-  static constexpr int NQK = (D + E) / 64;   // chunks of a query tile and of 128 keys: [128][64]
-  static constexpr int NV = D / 64;          // chunks of 128 values: D = 128 [64 keys][128], D = 64 [128 keys][64]
-  static constexpr int Q_BYTES = 2 * NQK * CHUNK;
-  static constexpr int RING = (SMEM_MAX - 1024 - MISC - Q_BYTES) / CHUNK < 12
-                                  ? (SMEM_MAX - 1024 - MISC - Q_BYTES) / CHUNK : 12;
-  static constexpr int SMEM = 1024 + Q_BYTES + RING * CHUNK + MISC;
-  static_assert(RING >= NQK + NV + 1, "the values of a tile and the keys of the next are in use at a time");
+  static constexpr int NQK = (D + E) / 64;                        // 64-dim chunks of a query or key row
+  static constexpr int Q_TILES = CTAS;                            // query tiles of a CTA
+  static constexpr int Q_CHUNK = kPromptRows * 128;               // [128 rows][64 dims]
+  static constexpr int Q_BYTES = Q_TILES * NQK * Q_CHUNK;
+  static constexpr int K_ROWS = kPromptKeys / CTAS;               // keys of a tile in this CTA
+  static constexpr int K_CHUNK = K_ROWS * 128;
+  static constexpr int V_DIMS = D / CTAS;                         // value dims in this CTA
+  static constexpr int V_WIDTH = V_DIMS < 64 ? V_DIMS : 64;       // of a block [128 keys][V_WIDTH]
+  static constexpr int V_BLOCK = kPromptKeys * V_WIDTH * 2;
+  static constexpr int K_BYTES = NQK * K_CHUNK, V_BYTES = V_DIMS / V_WIDTH * V_BLOCK;
+  static constexpr int FIT = (SMEM_MAX - 1024 - MISC - Q_BYTES) / (K_BYTES + V_BYTES);
+  static constexpr int STAGES = FIT < 6 ? FIT : 6;
+  static constexpr int SMEM = 1024 + Q_BYTES + STAGES * (K_BYTES + V_BYTES) + MISC;
+  static_assert(STAGES >= 2, "the values of a tile and the keys of the next are in use at a time");
+  static_assert(CTAS == 2 || STAGES * (K_BYTES + V_BYTES) >= kPromptRows * D * 4, "room to exchange O in");
 };
 
-// One CTA's work: two tiles of query rows of one key head over a range of one sequence's keys.
+// The work of a CTA or of a pair: query tiles of one key head over a range of one sequence's keys.
 struct Item {
   int head;            // key head
-  int t0;              // first token of tile 0, within the sequence
+  int t0;              // first token, within the sequence
   int lq, lk;
   int64_t q0, k0;      // packed places of the sequence's first query and key
   int part, beg, end;  // keys [beg, end) of the sequence are in this part
@@ -69,19 +82,18 @@ __device__ __forceinline__ bool prompt_seq(const PromptParams& p, int r, int& q0
   return true;
 }
 
-// The CTA's item: sequences in order, of each its key heads, of each head its tile pairs, the
-// last (the longest, causally) first, and the parts of the keys.  Every thread sums the pairs
-// of a run of sequences; the thread whose run holds the CTA's number writes the item.
-__device__ __forceinline__ void find_item(const PromptParams& p, prompt::Item* item, int64_t* totals) {
+// Item number `me`: sequences in order, of each its key heads, of each head its blocks of `span`
+// tokens, the last (the longest, causally) first, and the parts of the keys.  Every thread sums
+// the blocks of a run of sequences; the thread whose run holds the number writes the item.
+__device__ __forceinline__ void find_item(const PromptParams& p, int span, int64_t me, prompt::Item* item, int64_t* totals) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.B + prompt::THREADS - 1) / prompt::THREADS;
   const int r0 = min(p.B, tid * per), r1 = min(p.B, r0 + per);
-  const int pair = 2 * p.tile_toks;
   int64_t n = 0;
   int q0, lq, k0, lk;
   for (int r = r0; r < r1; ++r) {
     prompt_seq(p, r, q0, lq, k0, lk);
-    n += (lq + pair - 1) / pair;
+    n += (lq + span - 1) / span;
   }
   int64_t incl = n;
 #pragma unroll
@@ -96,18 +108,17 @@ __device__ __forceinline__ void find_item(const PromptParams& p, prompt::Item* i
 #pragma unroll
   for (int w = 0; w < prompt::WARPS; ++w)
     if (w < warp) before += totals[w];
-  const int64_t each = static_cast<int64_t>(p.kv_heads) * p.nparts;   // items of a pair of tiles
-  const int64_t me = blockIdx.x;
+  const int64_t each = static_cast<int64_t>(p.kv_heads) * p.nparts;   // items of a block of tokens
   if (me >= before * each && me < (before + n) * each) {
     int64_t at = me - before * each;
     for (int r = r0; r < r1; ++r) {
       prompt_seq(p, r, q0, lq, k0, lk);
-      const int64_t pairs = (lq + pair - 1) / pair;
-      if (at < pairs * each) {
+      const int64_t blocks = (lq + span - 1) / span;
+      if (at < blocks * each) {
         item->part = static_cast<int>(at % p.nparts);
         at /= p.nparts;
-        item->t0 = static_cast<int>(pairs - 1 - at % pairs) * pair;
-        item->head = static_cast<int>(at / pairs);
+        item->t0 = static_cast<int>(blocks - 1 - at % blocks) * span;
+        item->head = static_cast<int>(at / blocks);
         item->lq = lq;
         item->lk = lk;
         item->q0 = q0;
@@ -117,7 +128,7 @@ __device__ __forceinline__ void find_item(const PromptParams& p, prompt::Item* i
         item->any = true;
         break;
       }
-      at -= pairs * each;
+      at -= blocks * each;
     }
   }
   __syncthreads();
@@ -153,225 +164,257 @@ __device__ __forceinline__ float join_lse(float a, float b, float& wa, float& wb
   return m + logf(sum);
 }
 
-template <int D, int E, bool FP16>
+template <int D, int E, bool FP16, int CTAS>
 __global__ void __launch_bounds__(prompt::THREADS, 1)
     prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap smap, const __grid_constant__ CUtensorMap vmap,
                        const PromptParams p) {
   using namespace prompt;
-  using S = Shape<D, E>;
-  constexpr int NQK = S::NQK, NV = S::NV, RING = S::RING, PER = NQK + NV;
+  using S = Shape<D, E, CTAS>;
+  constexpr int NQK = S::NQK, STAGES = S::STAGES;
+  constexpr bool PAIR = CTAS == 2;
   extern __shared__ uint8_t psm_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(psm_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* qs = smem;                                   // [2][NQK] chunks
-  uint8_t* ring = smem + S::Q_BYTES;                    // [RING] chunks
-  uint64_t* bars = reinterpret_cast<uint64_t*>(ring + RING * CHUNK);
-  uint64_t* full = bars;                                // [RING] chunk landed
-  uint64_t* empty = bars + RING;                        // [RING] its MMAs are done
-  uint64_t* q_full = bars + 2 * RING;                   // [2] query tile landed
-  uint64_t* s_full = q_full + 2;                        // [2] S of a tile done, and with it every MMA before; then O
-  uint64_t* p_full = s_full + 2;                        // [2] P written (four warps)
-  uint64_t* drain = p_full + 2;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint8_t* qs = smem;                                   // [Q_TILES][NQK] chunks
+  uint8_t* ks = smem + S::Q_BYTES;                      // [STAGES][NQK] chunks
+  uint8_t* vs = ks + STAGES * S::K_BYTES;               // [STAGES] blocks
+  uint64_t* bars = reinterpret_cast<uint64_t*>(vs + STAGES * S::V_BYTES);
+  // In the CTA of rank 0: what the MMAs wait for, from both CTAs.
+  uint64_t* k_full = bars;                              // [STAGES] keys landed
+  uint64_t* v_full = k_full + STAGES;                   // [STAGES] values landed
+  uint64_t* q_full = v_full + STAGES;                   // [2] query tile landed
+  uint64_t* p_full = q_full + 2;                        // [2][2] P written, the first 64 keys and the others
+  // In each CTA: what the MMAs signal.
+  uint64_t* k_empty = p_full + 4;                       // [STAGES]
+  uint64_t* v_empty = k_empty + STAGES;                 // [STAGES]
+  uint64_t* s_full = v_empty + STAGES;                  // [2] S done, and with it every MMA before; at last O
+  uint64_t* drain = s_full + 2;                         // [2]
+  uint64_t* tail = drain + 2;                           // a last tile's values landed, to be cut by the loading warp
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(tail + 1);
   int* abortf = reinterpret_cast<int*>(tslot + 1);
   Item* item = reinterpret_cast<Item*>(bars + 40);
   int64_t* totals = reinterpret_cast<int64_t*>(bars + 60);
-  static_assert(2 * 12 + 9 <= 40 && sizeof(Item) <= 160 && (60 + WARPS) * 8 <= MISC, "shared scalars");
+  static_assert(4 * STAGES + 12 <= 40 && sizeof(Item) <= 160 && 60 + WARPS <= 128, "shared scalars");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = PAIR ? static_cast<int>(cluster_rank()) : 0;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < RING; ++i) {
-      mbar_init(full + i, 1);
-      mbar_init(empty + i, 1);
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(k_full + i, CTAS);
+      mbar_init(v_full + i, CTAS);
+      mbar_init(k_empty + i, PAIR ? 2 : 1);   // a pair's tiles serve both S
+      mbar_init(v_empty + i, PAIR ? 2 : 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(q_full + i, 1);
+      mbar_init(q_full + i, CTAS);
       mbar_init(s_full + i, 1);
-      mbar_init(p_full + i, 4);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(p_full + i, 4 * CTAS);
     mbar_init(drain, 1);
+    mbar_init(drain + 1, 1);
+    mbar_init(tail, 1);
     *abortf = 0;
     fence_mbar_init();
   }
   grid_dep_wait();
-  find_item(p, item, totals);
+  find_item(p, CTAS * CTAS * p.tile_toks, blockIdx.x / CTAS, item, totals);
   const Item it = *item;
   if (!it.any) return;
-  // keys of each tile: up to the last that its last token sees
-  int n[2], first_tok[2];
+  // Key tiles of either S: up to the last key that its last token sees.  A pair's S_i are the
+  // tokens t0 + 2 i tile_toks on, half of them in each CTA, over all key tiles; a single CTA's
+  // are the even and the odd key tiles of its one query tile.
+  int n[2], tiles = 0;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    first_tok[i] = it.t0 + i * p.tile_toks;
-    const int last = min(first_tok[i] + p.tile_toks, it.lq) - 1;
+    const int first = it.t0 + (PAIR ? i * CTAS * p.tile_toks : 0);
+    const int last = min(first + CTAS * p.tile_toks, it.lq) - 1;
     int64_t vis = it.lk;
     if (p.causal) vis = min(vis, static_cast<int64_t>(last) + 1 + it.lk - it.lq);
     const int64_t end = min(static_cast<int64_t>(it.end), vis);
-    n[i] = first_tok[i] < it.lq && end > it.beg ? static_cast<int>((end - it.beg + kPromptKeys - 1) / kPromptKeys) : 0;
+    n[i] = first < it.lq && end > it.beg ? static_cast<int>((end - it.beg + kPromptKeys - 1) / kPromptKeys) : 0;
+    tiles = max(tiles, n[i]);
   }
-  const int nmax = max(n[0], n[1]);
-  if (p.nparts > 1 && nmax == 0) return;   // the merge does not look for this part
-  if (warp == MMA_WARP) tmem_alloc(tslot, 512);
+  if (p.nparts > 1 && tiles == 0) return;   // the merge does not look for this part
+  if (!PAIR) {
+    n[0] = (tiles + 1) / 2;
+    n[1] = tiles / 2;
+  }
+  if (warp == MMA_WARP) tmem_alloc_all<CTAS>(tslot, 512);
   tc_fence_before();
-  __syncthreads();
+  if (PAIR) cluster_sync();   // the other CTA's barriers are there
+  else __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tslot;
   const Abort ab{abortf, p.status};
-  constexpr uint32_t S_COL = 0, O_COL = 256;   // S (and P) of tile i at 128 i, O at 256 + 128 i
+  constexpr uint32_t S_COL = 0, O_COL = 256;   // S_i (and P_i) at 128 i, O_i at 256 + 128 i
+  // A barrier of the CTA of rank 0, as both CTAs reach it.
+  auto at_leader = [&](uint64_t* bar) { return PAIR ? cluster_map(smem_u32(bar), 0) : smem_u32(bar); };
 
   if (warp == LOAD_WARP) {
     // ---------------------------------------------------------------- loads
     const bool leader = elect_one();
     bool ok = true;
-    int c = 0;   // chunks issued
-    const int q_bytes = p.tile_toks * p.group * 128;
+    int loaded = 0;      // tiles whose copies were issued
+    bool cut = false;    // and whether the last one's values went by `tail`
     auto load_q = [&](int i) {
-      if (n[i] == 0 || !leader) return;
-      mbar_arrive_expect_tx(q_full + i, NQK * q_bytes);
+      if (!leader) return;
+      mbar_arrive_expect_tx_at(at_leader(q_full + i), NQK * p.tile_toks * p.group * 128);
+      const int tok = static_cast<int>(it.q0) + it.t0 + (PAIR ? (i * CTAS + rank) * p.tile_toks : 0);
       for (int k = 0; k < NQK; ++k)
-        tma_load_4d(qs + (i * NQK + k) * CHUNK, &qmap, q_full + i, 64 * k, 0, it.head,
-                    static_cast<int>(it.q0) + first_tok[i]);
+        tma_load_4d_at<CTAS>(qs + (i * NQK + k) * S::Q_CHUNK, &qmap, at_leader(q_full + i), 64 * k, 0, it.head, tok);
     };
-    auto slot = [&]() {   // the next chunk's place, once it is free
-      const int s = c % RING;
-      if (c >= RING) ok = ok && __all_sync(0xffffffffu, mbar_wait_inline(empty + s, (c / RING - 1) & 1, ab));
-      return s;
-    };
-    load_q(0);
-    for (int j = 0; ok && j < nmax; ++j) {
-      const int row = static_cast<int>(it.k0) + it.beg + j * kPromptKeys;
-      for (int k = 0; ok && k < NQK; ++k, ++c) {
-        const int s = slot();
-        if (!ok) break;
-        if (leader) {
-          mbar_arrive_expect_tx(full + s, CHUNK);
-          if (E && k == NQK - 1) tma_load_3d(ring + s * CHUNK, &smap, full + s, 0, 0, row);
-          else tma_load_3d(ring + s * CHUNK, &kmap, full + s, 64 * k, it.head, row);
-        }
-        __syncwarp();
-      }
-      if (j == 0) load_q(1);
-      for (int k = 0; ok && k < NV; ++k, ++c) {
-        const int s = slot();
-        if (!ok) break;
-        if (leader) {
-          mbar_arrive_expect_tx(full + s, CHUNK);
-          if (D == 128) {
-            tma_load_3d(ring + s * CHUNK, &vmap, full + s, 0, it.head, row + 64 * k);
-            tma_load_3d(ring + s * CHUNK + CHUNK / 2, &vmap, full + s, 64, it.head, row + 64 * k);
-          } else {
-            tma_load_3d(ring + s * CHUNK, &vmap, full + s, 0, it.head, row);
-          }
-        }
-        __syncwarp();
-      }
-    }
-    if (!ok && leader) {   // no copy into shared memory outlives the CTA
-      for (int i = max(0, c - RING); i < c; ++i) drain_wait(full + i % RING, (i / RING) & 1);
-      for (int i = 0; i < 2; ++i)
-        if (n[i]) drain_wait(q_full + i, 0);
-    }
-    __syncwarp();
-  } else if (warp == MMA_WARP) {
-    // ------------------------------------------------------------ MMA issuer
-    const bool leader = elect_one();
-    constexpr uint32_t fmt = FP16 ? 0u : 1u;
-    constexpr uint32_t idesc_qk = make_idesc(fmt, fmt, false, false, 128, kPromptKeys);
-    constexpr uint32_t idesc_pv = make_idesc(fmt, fmt, false, true, 128, D);
-    const uint64_t dq = make_sdesc_sw128(smem_u32(qs), 16, 1024);                  // queries, K-major
-    const uint64_t dk = make_sdesc_sw128(smem_u32(ring), 16, 1024);                // keys, K-major
-    const uint64_t dv = make_sdesc_sw128(smem_u32(ring), CHUNK / 2, 1024);         // values, MN-major
-    bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       ok = ok && __all_sync(0xffffffffu, mbar_wait_inline(bar, parity, ab));
     };
-    auto wait_chunks = [&](int c0, int cnt) {
-      for (int c = c0; c < c0 + cnt; ++c) wait(full + c % RING, (c / RING) & 1);
-      tc_fence_after();
-    };
-    auto release = [&](int c0, int cnt) {
-      if (leader)
-        for (int c = c0; c < c0 + cnt; ++c) tc_commit(empty + c % RING);
-    };
-    auto scores = [&](int i, int j) {   // S_i = Q_i K_j^T
-      if (leader) {
-#pragma unroll
-        for (int k = 0; k < NQK; ++k) {
-          const uint64_t a = dq + (((i * NQK + k) * CHUNK) >> 4);
-          const uint64_t b = dk + ((((j * PER + k) % RING) * CHUNK) >> 4);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_f16(tmem + S_COL + 128 * i, a + ((32 * kk) >> 4), b + ((32 * kk) >> 4), idesc_qk, k || kk ? 1u : 0u);
-        }
-        tc_commit(s_full + i);
-      }
-      __syncwarp();
-    };
-    auto values = [&](int i, int j, int steps) {   // O_i += P_i V_j over 16 `steps` keys
-      if (leader) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if (k >= steps) break;
-          const int c = j * PER + NQK + (D == 128 ? k / 4 : 0);
-          const uint64_t b = dv + ((((c % RING) * CHUNK) + (D == 128 ? k % 4 : k) * 2048) >> 4);
-          mma_f16_ts(tmem + O_COL + 128 * i, tmem + S_COL + 128 * i + 8 * k, b, idesc_pv, j || k ? 1u : 0u);
-        }
-      }
-      __syncwarp();
-    };
-    if (nmax > 0) {
-      wait_chunks(0, NQK);
-      for (int i = 0; i < 2; ++i)
-        if (n[i] > 0) {
-          wait(q_full + i, 0);
-          tc_fence_after();
-          if (ok) scores(i, 0);
-        }
-      if (ok) release(0, NQK);
-      __syncwarp();
-    }
-    for (int j = 0; ok && j < nmax; ++j) {
-      const int v0 = j * PER + NQK, k1 = (j + 1) * PER;
-      const int keys = min(kPromptKeys, it.end - it.beg - j * kPromptKeys);   // behind them: another sequence's, or none
-      const int steps = (keys + 15) / 16;
-      wait_chunks(v0, NV);
+    if (tiles > 0 && (!PAIR || n[0] > 0)) load_q(0);
+    for (int j = 0, st = 0, ph = 0; j < tiles; ++j) {
+      const int row = static_cast<int>(it.k0) + it.beg + j * kPromptKeys;
+      if (j >= STAGES) wait(k_empty + st, ph ^ 1);
       if (!ok) break;
-      if (keys & 15) {
-        // Weights of keys behind the last are zero; what stands in the places of their values
-        // (another sequence's, NaN and all) is set to zero, up to the MMA's step of 16 keys.
-        for (int x = lane; x < (16 * steps - keys) * (D / 8); x += 32) {
-          const int r = keys + x / (D / 8), piece = x % (D / 8);
-          const int c = (v0 + (D == 128 ? r / 64 : 0)) % RING;
-          *reinterpret_cast<uint4*>(ring + c * CHUNK + (piece / 8) * (CHUNK / 2) + (D == 128 ? r % 64 : r) * 128 +
-                                    (piece % 8) * 16) = make_uint4(0, 0, 0, 0);
+      if (leader) {
+        const uint32_t bar = at_leader(k_full + st);
+        mbar_arrive_expect_tx_at(bar, S::K_BYTES);
+        for (int k = 0; k < NQK; ++k) {
+          uint8_t* dst = ks + st * S::K_BYTES + k * S::K_CHUNK;
+          if (E && k == NQK - 1) tma_load_3d_at<CTAS>(dst, &smap, bar, 0, 0, row + rank * S::K_ROWS);
+          else tma_load_3d_at<CTAS>(dst, &kmap, bar, 64 * k, it.head, row + rank * S::K_ROWS);
+        }
+      }
+      __syncwarp();
+      if (j == 0 && PAIR && n[1] > 0) load_q(1);
+      if (j >= STAGES) wait(v_empty + st, ph ^ 1);
+      if (!ok) break;
+      // Weights of keys behind the last are zero; what stands in the places of their values
+      // (another sequence's, NaN and all) is set to zero, up to the MMA's step of 16 keys.
+      const int keys = min(kPromptKeys, it.end - it.beg - j * kPromptKeys);
+      cut = (keys & 15) != 0;
+      uint8_t* v0 = vs + st * S::V_BYTES;
+      if (leader) {
+        const uint32_t bar = cut ? smem_u32(tail) : at_leader(v_full + st);
+        if (cut) mbar_arrive_expect_tx(tail, S::V_BYTES);
+        else mbar_arrive_expect_tx_at(bar, S::V_BYTES);
+        for (int k = 0; k < S::V_DIMS / S::V_WIDTH; ++k)
+          tma_load_3d_at<CTAS>(v0 + k * S::V_BLOCK, &vmap, bar, rank * S::V_DIMS + k * S::V_WIDTH, it.head, row);
+      }
+      __syncwarp();
+      loaded = j + 1;
+      if (cut) {   // the last tile
+        wait(tail, 0);
+        if (!ok) break;
+        constexpr int PIECES = S::V_WIDTH / 8;
+        const int rows = (16 - (keys & 15));
+        for (int x = lane; x < rows * (S::V_DIMS / 8); x += 32) {
+          const int r = keys + x / (S::V_DIMS / 8), piece = x % (S::V_DIMS / 8);
+          *reinterpret_cast<uint4*>(v0 + piece / PIECES * S::V_BLOCK + r * S::V_WIDTH * 2 + piece % PIECES * 16) =
+              make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
         __syncwarp();
-      }
-      bool have_keys = false;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (j >= n[i]) continue;
-        wait(p_full + i, j & 1);
-        if (!ok) break;
-        tc_fence_after();
-        values(i, j, steps);
-        if (i == 1 || j >= n[1]) release(v0, NV);
-        if (j + 1 < n[i]) {
-          if (!have_keys) wait_chunks(k1, NQK);
-          have_keys = true;
-          if (!ok) break;
-          scores(i, j + 1);
-        } else if (leader) {
-          tc_commit(s_full + i);   // O is done
-        }
+        if (leader) mbar_arrive_release_at(at_leader(v_full + st));
         __syncwarp();
       }
-      if (ok && have_keys) release(k1, NQK);
+      if (++st == STAGES) st = 0, ph ^= 1;
+    }
+    // After a failed wait: no copy into shared memory outlives the CTA.  The barriers that the
+    // other CTA's copies count on are in the CTA of rank 0, which waits for them.
+    if (!ok && leader && rank == 0) {
+      for (int j = max(0, loaded - STAGES); j < loaded; ++j) {
+        drain_wait(k_full + j % STAGES, (j / STAGES) & 1);
+        if (!(cut && j == loaded - 1)) drain_wait(v_full + j % STAGES, (j / STAGES) & 1);
+      }
+      if (n[0] > 0) drain_wait(q_full, 0);
+      if (PAIR && n[1] > 0) drain_wait(q_full + 1, 0);
+    }
+    if (!ok && leader && cut) drain_wait(tail, 0);
+    __syncwarp();
+  } else if ((warp == MMA_WARP || warp == MMA_WARP + 1) && rank == 0) {
+    // ------------------------------------------------------------ MMA issuers
+    // One warp per S, so that the waits and the bookkeeping of one (about 100 cycles a wait) run
+    // beside the products of the other: one warp for both took 1,750 cycles a tile, the products
+    // of D = 128, E = 64 take 1,280.
+    const bool leader = elect_one();
+    const int i = warp - MMA_WARP;
+    constexpr uint32_t fmt = FP16 ? 0u : 1u;
+    constexpr uint32_t idesc_qk = make_idesc(fmt, fmt, false, false, 128 * CTAS, kPromptKeys);
+    constexpr uint32_t idesc_pv = make_idesc(fmt, fmt, false, true, 128 * CTAS, D);
+    const uint64_t dq = make_sdesc_sw128(smem_u32(qs) + (PAIR ? i : 0) * NQK * S::Q_CHUNK, 16, 1024);   // queries, K-major
+    const uint64_t dk = make_sdesc_sw128(smem_u32(ks), 16, 1024);                                       // keys, K-major
+    const uint64_t dv = S::V_WIDTH == 64 ? make_sdesc_sw128(smem_u32(vs), S::V_BLOCK, 1024)             // values, MN-major
+                                         : make_sdesc_sw64(smem_u32(vs), S::V_BLOCK, 512);
+    const uint32_t kf = smem_u32(k_full), vf = smem_u32(v_full), pf = smem_u32(p_full + 2 * i);
+    const uint32_t s_tmem = tmem + S_COL + 128 * i, o_tmem = tmem + O_COL + 128 * i;
+    constexpr int STEP = PAIR ? 1 : 2;   // key tiles from one of this S to its next
+    const int ni = n[i];
+    bool ok = true;
+    int kst = 0, kph = 0, vst = 0, vph = 0;   // stage and parity of the next key and value tile
+    auto next = [](int& st, int& ph, int by) {
+      if ((st += by) >= STAGES) st -= STAGES, ph ^= 1;
+    };
+    if (!PAIR && i == 1) next(kst, kph, 1), next(vst, vph, 1);
+    auto scores = [&]() {   // S_i = Q_i K^T
+      if (leader) {
+        const uint64_t b = dk + ((kst * S::K_BYTES) >> 4);
+#pragma unroll
+        for (int k = 0; k < NQK; ++k)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f16_ss<CTAS>(s_tmem, dq + ((k * S::Q_CHUNK + 32 * kk) >> 4), b + ((k * S::K_CHUNK + 32 * kk) >> 4), idesc_qk,
+                             k || kk ? 1u : 0u);
+        tc_commit_all<CTAS>(s_full + i);
+        tc_commit_all<CTAS>(k_empty + kst);
+      }
+      __syncwarp();
+      next(kst, kph, STEP);
+    };
+    if (ni > 0) {
+      const uint32_t q = smem_u32(q_full + (PAIR ? i : 0));
+      ok = warp_wait2(kf + 8 * kst, kph, q, 0, ab);
+      tc_fence_after();
+      if (ok) scores();
+    }
+    for (int j = 0; ok && j < ni; ++j) {
+      const int keys = it.end - it.beg - (PAIR ? j : 2 * j + i) * kPromptKeys;
+      const int todo = (min(kPromptKeys, keys) + 15) / 16;   // MMAs of 16 keys
+      const bool more = j + 1 < ni;
+      const uint64_t b = dv + ((vst * S::V_BYTES) >> 4);
+      // O_i += P_i V; the first half waits for the values, too, the second for the next keys
+      if (!(ok = warp_wait2(pf, j & 1, vf + 8 * vst, vph, ab))) break;
+      if (PAIR && keys < kPromptKeys) mbar_acquire_cluster(v_full + vst, vph);   // values cut by plain stores
+      tc_fence_after();
+      if (leader) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (k < todo) mma_f16_ts<CTAS>(o_tmem, s_tmem + 8 * k, b + ((k * 32 * S::V_WIDTH) >> 4), idesc_pv, j || k ? 1u : 0u);
+      }
+      __syncwarp();
+      if (!(ok = warp_wait2(pf + 8, j & 1, more ? kf + 8 * kst : pf + 8, more ? kph : j & 1, ab))) break;
+      tc_fence_after();
+      if (leader) {
+#pragma unroll
+        for (int k = 4; k < 8; ++k)
+          if (k < todo) mma_f16_ts<CTAS>(o_tmem, s_tmem + 8 * k, b + ((k * 32 * S::V_WIDTH) >> 4), idesc_pv, 1u);
+        tc_commit_all<CTAS>(v_empty + vst);
+      }
+      __syncwarp();
+      next(vst, vph, STEP);
+      if (more) scores();
+      else if (leader) tc_commit_all<CTAS>(s_full + i);   // O_i is done
       __syncwarp();
     }
+    // a pair's tiles behind this S's last go back as they come
+    for (int j = ni; PAIR && ok && j < tiles; ++j) {
+      if (!(ok = warp_wait2(kf + 8 * kst, kph, vf + 8 * vst, vph, ab))) break;
+      if (leader) {
+        tc_commit_all<CTAS>(k_empty + kst);
+        tc_commit_all<CTAS>(v_empty + vst);
+      }
+      __syncwarp();
+      next(kst, kph, 1);
+      next(vst, vph, 1);
+    }
     if (!ok && leader) {
-      tc_commit(drain);
-      drain_wait(drain, 0);
+      tc_commit_all<CTAS>(drain + i);
+      drain_wait(drain + i, 0);
     }
     __syncwarp();
   } else if (warp < SOFTMAX_WARPS) {
@@ -380,9 +423,8 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t ts = tmem + S_COL + 128 * i + lanes, to = tmem + O_COL + 128 * i + lanes;
     const int row = 32 * quarter + lane;
-    const int tok = first_tok[i] + row / p.group, g = row % p.group;
+    const int tok = it.t0 + (PAIR ? (i * CTAS + rank) * p.tile_toks : 0) + row / p.group, g = row % p.group;
     const bool valid = row < p.tile_toks * p.group && tok < it.lq;
-    const int ni = n[i];
     // keys of this part that the row sees
     int64_t sees = it.lk;
     if (p.causal) sees = min(sees, static_cast<int64_t>(tok) + 1 + it.lk - it.lq);
@@ -391,9 +433,11 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
     const int all_see = __reduce_min_sync(0xffffffffu, vis);
     const float sc = p.scale_log2;
     constexpr float SHIFT = FP16 ? 7.f : 0.f;
+    const uint32_t p_bar[2] = {at_leader(p_full + 2 * i), at_leader(p_full + 2 * i + 1)};
     float m = -INFINITY;           // reference: a logit of m has weight 2^SHIFT
     float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     bool ok = true;
+    const int ni = n[i];
     for (int j = 0; j < ni; ++j) {
       ok = __all_sync(0xffffffffu, ok && mbar_wait_inline(s_full + i, j & 1, ab));
       if (!ok) break;
@@ -402,8 +446,9 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
 #pragma unroll
       for (int b = 0; b < 4; ++b) DSA_TMEM_LD32(ts + 32 * b, r[b]);
       tmem_wait_ld();
-      const int limit = vis - j * kPromptKeys;
-      if (all_see < (j + 1) * kPromptKeys) {
+      const int k0 = (PAIR ? j : 2 * j + i) * kPromptKeys;
+      if (all_see < k0 + kPromptKeys) {
+        const int limit = vis - k0;
 #pragma unroll
         for (int b = 0; b < 4; ++b)
 #pragma unroll
@@ -452,20 +497,55 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
           r[b][x >> 1] = pack16(y.x, y.y, FP16);
         }
         DSA_TMEM_ST16(ts + 16 * b, r[b]);
+        if (b & 1) {
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_at(p_bar[b >> 1]);
+        }
       }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_full + i);
     }
     if (ok && ni > 0) ok = __all_sync(0xffffffffu, mbar_wait_inline(s_full + i, ni & 1, ab));
     tc_fence_after();
     // ---- O / sum, joined with an earlier result where there is one
-    const float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
+    float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y), other = 0.f;
+    constexpr int MINE = PAIR ? D : D / 2;        // dims that this thread writes, from d0 on
+    const int d0 = PAIR ? 0 : i * MINE;
+    float4* swap = reinterpret_cast<float4*>(ks);   // [D / 4][128 rows]: every key and value is read by now
+    if (!PAIR) {
+      // The two S of a tile: each thread hands over half of its O, weighed by the common reference.
+      float* ml = reinterpret_cast<float*>(bars + 128);   // [2][128] references, sums
+      ml[128 * i + row] = m;
+      ok = !named_bar_any(1, 32 * SOFTMAX_WARPS, !ok);
+      const float mo = ml[128 * (1 - i) + row], both = fmaxf(m, mo);
+      const float w = both == -INFINITY ? 0.f : ex2(m - both);
+      l *= w;
+      m = both;
+      const int dh = (1 - i) * MINE;                // the other thread's dims
+      if (ok) {
+#pragma unroll 1
+        for (int b = 0; b < MINE / 16; ++b) {
+          uint32_t o[16] = {};
+          if (ni > 0) {
+            DSA_TMEM_LD16(to + dh + 16 * b, o);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            swap[((dh + 16 * b) / 4 + x) * kPromptRows + row] =
+                make_float4(__uint_as_float(o[4 * x]) * w, __uint_as_float(o[4 * x + 1]) * w, __uint_as_float(o[4 * x + 2]) * w,
+                            __uint_as_float(o[4 * x + 3]) * w);
+        }
+      }
+      ml[256 + 128 * i + row] = l;
+      named_bar_sync(1, 32 * SOFTMAX_WARPS);
+      l += ml[256 + 128 * (1 - i) + row];
+      other = w;
+    }
     const bool empty_row = !(l > 0.f);   // nothing seen
     const float lse2 = empty_row ? -INFINITY : m - SHIFT + log2f(l);
     const int64_t at = (it.q0 + tok) * p.heads + static_cast<int64_t>(it.head) * p.group + g;
-    if (ok && (ni > 0 || p.nparts == 1)) {
+    if (ok) {
       float w = empty_row ? 0.f : 1.f / l, wp = 0.f;
       float lse = lse2 * 0.6931471805599453f;
       const bool last = p.nparts == 1;
@@ -474,22 +554,34 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
         lse = join_lse(p.prev_lse[at], lse, wp, wn);
         w *= wn;
       }
-      if (valid) {
+      if (!PAIR) named_bar_sync(1, 32 * SOFTMAX_WARPS);   // prev_lse may be lse: both threads of a row have read it
+      if (valid && d0 == 0) {
         if (!last) p.part_lse[static_cast<int64_t>(it.part) * p.total_q * p.heads + at] = lse2;
         else if (p.lse) p.lse[at] = lse;
       }
 #pragma unroll 1
-      for (int b = 0; b < D / 32; ++b) {
-        uint32_t o[32];
+      for (int b = 0; b < MINE / 32; ++b) {
+        uint32_t o[32] = {};
         if (ni > 0) {
-          DSA_TMEM_LD32(to + 32 * b, o);
+          DSA_TMEM_LD32(to + d0 + 32 * b, o);
           tmem_wait_ld();
         }
         if (!valid) continue;
+        if (!PAIR) {
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const float4 v = swap[((d0 + 32 * b) / 4 + x) * kPromptRows + row];
+            o[4 * x] = __float_as_uint(fmaf(__uint_as_float(o[4 * x]), other, v.x));
+            o[4 * x + 1] = __float_as_uint(fmaf(__uint_as_float(o[4 * x + 1]), other, v.y));
+            o[4 * x + 2] = __float_as_uint(fmaf(__uint_as_float(o[4 * x + 2]), other, v.z));
+            o[4 * x + 3] = __float_as_uint(fmaf(__uint_as_float(o[4 * x + 3]), other, v.w));
+          }
+        }
 #pragma unroll
         for (int x = 0; x < 32; ++x) o[x] = empty_row ? 0u : __float_as_uint(__uint_as_float(o[x]) * w);
         if (!last) {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + (static_cast<int64_t>(it.part) * p.total_q * p.heads + at) * D + 32 * b);
+          float4* dst = reinterpret_cast<float4*>(p.part_o + (static_cast<int64_t>(it.part) * p.total_q * p.heads + at) * D +
+                                                  d0 + 32 * b);
 #pragma unroll
           for (int x = 0; x < 8; ++x)
             dst[x] = make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]), __uint_as_float(o[4 * x + 2]),
@@ -497,7 +589,7 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
           continue;
         }
         if (p.prev_out && wp > 0.f) {
-          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.prev_out) + at * D + 32 * b);
+          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.prev_out) + at * D + d0 + 32 * b);
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const uint4 v = src[x];
@@ -510,7 +602,7 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
             }
           }
         }
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * D + 32 * b);
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * D + d0 + 32 * b);
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           uint32_t v[4];
@@ -523,8 +615,10 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
     }
   }
   tc_fence_before();
-  __syncthreads();
-  if (warp == MMA_WARP) tmem_dealloc(tmem, 512);
+  __syncwarp();
+  if (PAIR) cluster_sync();   // neither CTA leaves while the other's copies, MMAs or arrivals may still reach it
+  else __syncthreads();
+  if (warp == MMA_WARP) tmem_dealloc_all<CTAS>(tmem, 512);
 }
 
 // The parts of a row merged by log-sum-exp, joined with an earlier result where there is one.
@@ -592,29 +686,31 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const PromptParams p)
 }
 
 namespace {
-template <int D, int E, bool FP16>
-cudaError_t launch_one(const PromptMaps& m, const PromptParams& p, int64_t grid, cudaStream_t st) {
-  constexpr int smem = prompt::Shape<D, E>::SMEM;
-  cudaError_t e = set_func_attr_once(reinterpret_cast<const void*>(prompt_attn_kernel<D, E, FP16>),
+template <int D, int E, bool FP16, int CTAS>
+cudaError_t launch_one(const PromptMaps& m, const PromptParams& p, int64_t items, cudaStream_t st) {
+  constexpr int smem = prompt::Shape<D, E, CTAS>::SMEM;
+  cudaError_t e = set_func_attr_once(reinterpret_cast<const void*>(prompt_attn_kernel<D, E, FP16, CTAS>),
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  e = launch_ex(prompt_attn_kernel<D, E, FP16>, dim3(static_cast<unsigned>(grid)), dim3(prompt::THREADS), smem, st, false, 0u,
-                m.q, m.k, m.ks, m.v, p);
+  e = launch_ex(prompt_attn_kernel<D, E, FP16, CTAS>, dim3(static_cast<unsigned>(items * CTAS)), dim3(prompt::THREADS), smem, st,
+                false, CTAS == 2 ? 2u : 0u, m.q, m.k, m.ks, m.v, p);
   if (e != cudaSuccess || p.nparts == 1) return e;
   const int64_t rows = p.total_q * p.heads;
   return launch_ex(prompt_merge_kernel<D, FP16>, dim3(static_cast<unsigned>(cdiv(rows, 8))), dim3(256), 0, st, true, 0u, p);
 }
 
 template <int D, int E>
-cudaError_t launch_type(const PromptMaps& m, const PromptParams& p, bool fp16, int64_t grid, cudaStream_t st) {
-  return fp16 ? launch_one<D, E, true>(m, p, grid, st) : launch_one<D, E, false>(m, p, grid, st);
+cudaError_t launch_type(const PromptMaps& m, const PromptParams& p, bool fp16, int ctas, int64_t items, cudaStream_t st) {
+  if (ctas == 2) return fp16 ? launch_one<D, E, true, 2>(m, p, items, st) : launch_one<D, E, false, 2>(m, p, items, st);
+  return fp16 ? launch_one<D, E, true, 1>(m, p, items, st) : launch_one<D, E, false, 1>(m, p, items, st);
 }
 }  // namespace
 
-cudaError_t launch_prompt_attn(const PromptMaps& m, const PromptParams& p, int dim, int shared_dim, bool fp16,
-                               int64_t grid, cudaStream_t st) {
-  if (dim == 128) return shared_dim ? launch_type<128, 64>(m, p, fp16, grid, st) : launch_type<128, 0>(m, p, fp16, grid, st);
-  return shared_dim ? launch_type<64, 64>(m, p, fp16, grid, st) : launch_type<64, 0>(m, p, fp16, grid, st);
+cudaError_t launch_prompt_attn(const PromptMaps& m, const PromptParams& p, int dim, int shared_dim, bool fp16, int ctas,
+                               int64_t items, cudaStream_t st) {
+  if (dim == 128)
+    return shared_dim ? launch_type<128, 64>(m, p, fp16, ctas, items, st) : launch_type<128, 0>(m, p, fp16, ctas, items, st);
+  return shared_dim ? launch_type<64, 64>(m, p, fp16, ctas, items, st) : launch_type<64, 0>(m, p, fp16, ctas, items, st);
 }
 
 }  // namespace dsa

@@ -35,8 +35,10 @@ struct PromptMaps {
   CUtensorMap q, k, ks, v;
 };
 
-cudaError_t launch_prompt_attn(const PromptMaps& maps, const PromptParams& p, int dim, int shared_dim, bool fp16,
-                               int64_t grid, cudaStream_t st);
+// `ctas`: CTAs that share a block of queries, 1 (a tile of 128 rows) or 2 (four tiles); `items`:
+// blocks of queries x key heads x parts.
+cudaError_t launch_prompt_attn(const PromptMaps& maps, const PromptParams& p, int dim, int shared_dim, bool fp16, int ctas,
+                               int64_t items, cudaStream_t st);
 
 struct WriteTokensParams {
   BatchView b;

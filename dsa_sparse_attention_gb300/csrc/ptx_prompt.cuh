@@ -4,17 +4,6 @@
 
 namespace dsa {
 
-// D(tmem) (+)= A(tmem) * B(smem), 16-bit operands: row r of A lies in TMEM lane r, two
-// consecutive K elements a column.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                           uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(
-          d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -39,13 +28,157 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
   return d;
 }
 
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2,
-                                            int c3) {
+// ---------------------------------------------------------- pairs of CTAs (cta_group::2)
+// CTAS = 2: a tensor-core tile of 256 rows over the two CTAs of a cluster, 128 rows of A and D
+// in each; each holds half of B's N dimension, at the same shared-memory offset.  The CTA of
+// rank 0 issues.
+
+template <int CTAS>
+__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  if (CTAS == 1)
+    mma_f16(d_tmem, adesc, bdesc, idesc, accumulate);
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// D(tmem) (+)= A(tmem) * B(smem), 16-bit operands: row r of A lies in TMEM lane r, two
+// consecutive K elements a column.
+template <int CTAS>
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  if (CTAS == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(
+            d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(
+            d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Arrive once on `bar`, in every CTA of the pair, when all tcgen05 operations issued so far complete.
+template <int CTAS>
+__device__ __forceinline__ void tc_commit_all(uint64_t* bar) {
+  if (CTAS == 1)
+    tc_commit(bar);
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+
+template <int CTAS>
+__device__ __forceinline__ void tmem_alloc_all(uint32_t* slot, uint32_t ncols) {
+  if (CTAS == 1) {
+    tmem_alloc(slot, ncols);
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(ncols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+
+template <int CTAS>
+__device__ __forceinline__ void tmem_dealloc_all(uint32_t taddr, uint32_t ncols) {
+  if (CTAS == 1)
+    tmem_dealloc(taddr, ncols);
+  else
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
+// Barriers given by their address in the cluster's shared memory (cluster_map), for those of the
+// CTA of rank 0 that both CTAs signal.  What these two order is in tensor memory (behind a
+// tcgen05 fence) or counted in bytes, so they carry no fence of the cluster's scope, which would
+// take about 1,000 cycles.
+__device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_expect_tx_at(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+// The same behind plain stores to shared memory, for the other CTA's threads that wait by mbar_wait_cluster.
+__device__ __forceinline__ void mbar_arrive_release_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t addr, uint32_t parity) {
+  uint32_t ok;
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
-      "[%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(addr), "r"(parity)
       : "memory");
+  return ok != 0;
+}
+// After mbar_wait_inline of a phase in which a thread of the other CTA arrived by
+// mbar_arrive_release_at: its stores are visible, too (the phase is complete, so this returns at once).
+__device__ __forceinline__ void mbar_acquire_cluster(uint64_t* bar, uint32_t parity) {
+  mbar_try_wait_cluster(smem_u32(bar), parity);
+}
+
+// Waits, as a converged warp, for two phases at a time (addresses in this CTA's shared memory);
+// as mbar_wait_inline otherwise.
+__device__ __forceinline__ bool warp_wait2(uint32_t a, uint32_t pa, uint32_t b, uint32_t pb, Abort ab) {
+  auto done = [&] {
+    const bool x = mbar_try_wait(a, pa), y = mbar_try_wait(b, pb);
+    return __all_sync(0xffffffffu, x && y);
+  };
+  if (done()) return true;
+  const long long t0 = clock64();
+  for (uint32_t it = 1;; ++it) {
+    if (done()) return true;
+    if ((it & 15u) == 0u) {
+      bool late = false;
+      if (clock64() - t0 > kWaitLimitCycles) {
+        *reinterpret_cast<volatile int*>(ab.flag) = 1;
+        atomicOr(ab.status, DEV_TIMEOUT);
+        late = true;
+      }
+      if (__any_sync(0xffffffffu, late || *reinterpret_cast<volatile int*>(ab.flag))) return false;
+    }
+  }
+}
+
+// Copies into this CTA's shared memory whose bytes count on a barrier of either CTA of the pair.
+template <int CTAS>
+__device__ __forceinline__ void tma_load_3d_at(void* dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2) {
+  if (CTAS == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+            smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+template <int CTAS>
+__device__ __forceinline__ void tma_load_4d_at(void* dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2, int c3) {
+  if (CTAS == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
+        "[%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
 }
 
 }  // namespace dsa
