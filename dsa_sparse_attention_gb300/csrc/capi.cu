@@ -1303,6 +1303,7 @@ dsa_status dsa_prompt_attn(const dsa_prompt* prompt, const void* q, const void* 
   p.part_keys = w.part_keys;
   p.out = out;
   p.lse = lse;
+  p.out_aligned32 = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
   p.prev_out = prev_out;
   p.prev_lse = prev_lse;
   p.part_o = at<float>(workspace, w.part_o);

@@ -31,8 +31,13 @@ namespace dsa {
 
 namespace prompt {
 constexpr int SOFTMAX_WARPS = 8;      // four per S
-constexpr int MMA_WARP = 8, LOAD_WARP = 10, WARPS = 12;   // MMA_WARP and the next: S_0's and S_1's
+constexpr int MMA_WARP = 8;           // and the next: S_0's and S_1's
+constexpr int LOAD_WARP = 10, ITEM_WARP = 11, WARPS = 12;
 constexpr int THREADS = WARPS * 32;
+// Registers a thread: launched with 168, of which the softmax warps (two warpgroups) take more.
+constexpr int LAUNCH_REGS = 168, SOFTMAX_REGS = 200, OTHER_REGS = 104;
+static_assert(SOFTMAX_WARPS * SOFTMAX_REGS + (WARPS - SOFTMAX_WARPS) * OTHER_REGS <= WARPS * LAUNCH_REGS, "register shares");
+static_assert(WARPS * 32 * LAUNCH_REGS <= 65536 && SOFTMAX_WARPS % 4 == 0, "whole warpgroups");
 constexpr int MISC = 3072;            // barriers and scalars, and 2 KB of references and sums
 constexpr int SMEM_MAX = 232448;
 constexpr float GROW = 8.f;           // log2 units a logit may exceed the reference by
@@ -53,18 +58,24 @@ struct Shape {
   static constexpr int STAGES = FIT < 6 ? FIT : 6;
   static constexpr int SMEM = 1024 + Q_BYTES + STAGES * (K_BYTES + V_BYTES) + MISC;
   static_assert(STAGES >= 2, "the values of a tile and the keys of the next are in use at a time");
-  static_assert(CTAS == 2 || STAGES * (K_BYTES + V_BYTES) >= kPromptRows * D * 4, "room to exchange O in");
+  // Warps that issue MMAs: one for both S of a pair at D = 128, whose products then alternate of
+  // themselves (with a warp each, both softmaxes fall into step and the tensor core waits for them:
+  // 3,300 cycles a key tile, not 2,800); else one per S.
+  static constexpr int MMA_WARPS = CTAS == 2 && D == 128 ? 1 : 2;
 };
 
 // The work of a CTA or of a pair: query tiles of one key head over a range of one sequence's keys.
-struct Item {
-  int head;            // key head
-  int t0;              // first token, within the sequence
+struct __align__(16) Item {
+  int head;      // key head; -1: no more work
+  int t0;        // first token, within the sequence
   int lq, lk;
-  int64_t q0, k0;      // packed places of the sequence's first query and key
-  int part, beg, end;  // keys [beg, end) of the sequence are in this part
-  bool any;
+  int q0, k0;    // packed places of the sequence's first query and key
+  int part;
+  int beg, end;  // keys [beg, end) of the sequence are in this part
+  int tiles;     // key tiles that a row of the item sees
+  int n[2];      // of either S
 };
+static_assert(sizeof(Item) == 48, "read 16 bytes at a time");
 }  // namespace prompt
 
 // Lengths of sequence r; nothing to do (false) where the arrays break their rules.
@@ -82,57 +93,78 @@ __device__ __forceinline__ bool prompt_seq(const PromptParams& p, int r, int& q0
   return true;
 }
 
-// Item number `me`: sequences in order, of each its key heads, of each head its blocks of `span`
-// tokens, the last (the longest, causally) first, and the parts of the keys.  Every thread sums
-// the blocks of a run of sequences; the thread whose run holds the number writes the item.
-__device__ __forceinline__ void find_item(const PromptParams& p, int span, int64_t me, prompt::Item* item, int64_t* totals) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (p.B + prompt::THREADS - 1) / prompt::THREADS;
-  const int r0 = min(p.B, tid * per), r1 = min(p.B, r0 + per);
-  int64_t n = 0;
+// Finds items by their numbers: sequences in order, of each its key heads, of each head its blocks
+// of queries, the last (the longest, causally) first, and the parts of the keys.  One warp, a lane
+// a sequence; numbers come in ascending order but for a few, so it walks on from where it was.
+template <int CTAS>
+struct ItemFinder {
+  int r0 = 0;            // first sequence of the lanes'
+  uint32_t before = 0;   // blocks of the sequences before it
+  bool loaded = false;
+  bool good;             // of this lane's sequence:
   int q0, lq, k0, lk;
-  for (int r = r0; r < r1; ++r) {
-    prompt_seq(p, r, q0, lq, k0, lk);
-    n += (lq + span - 1) / span;
-  }
-  int64_t incl = n;
+  uint32_t blocks, upto; // its blocks, and those of the lanes up to it
+
+  __device__ __forceinline__ bool find(const PromptParams& p, uint32_t me, prompt::Item& it) {
+    const int lane = threadIdx.x & 31;
+    const int span = CTAS * CTAS * p.tile_toks;
+    const uint32_t each = static_cast<uint32_t>(p.kv_heads) * p.nparts;   // items of a block
+    if (me < before * each) r0 = 0, before = 0, loaded = false;
+    for (;;) {
+      if (!loaded) {
+        good = r0 + lane < p.B && prompt_seq(p, r0 + lane, q0, lq, k0, lk);
+        blocks = good ? static_cast<uint32_t>((lq + span - 1) / span) : 0u;
+        upto = blocks;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 31) totals[warp] = incl;
-  if (tid == 0) item->any = false;
-  __syncthreads();
-  int64_t before = incl - n;
-#pragma unroll
-  for (int w = 0; w < prompt::WARPS; ++w)
-    if (w < warp) before += totals[w];
-  const int64_t each = static_cast<int64_t>(p.kv_heads) * p.nparts;   // items of a block of tokens
-  if (me >= before * each && me < (before + n) * each) {
-    int64_t at = me - before * each;
-    for (int r = r0; r < r1; ++r) {
-      prompt_seq(p, r, q0, lq, k0, lk);
-      const int64_t blocks = (lq + span - 1) / span;
-      if (at < blocks * each) {
-        item->part = static_cast<int>(at % p.nparts);
-        at /= p.nparts;
-        item->t0 = static_cast<int>(blocks - 1 - at % blocks) * span;
-        item->head = static_cast<int>(at / blocks);
-        item->lq = lq;
-        item->lk = lk;
-        item->q0 = q0;
-        item->k0 = k0;
-        item->beg = static_cast<int>(min(static_cast<int64_t>(lk), static_cast<int64_t>(item->part) * p.part_keys));
-        item->end = p.nparts > 1 ? static_cast<int>(min(static_cast<int64_t>(lk), static_cast<int64_t>(item->beg) + p.part_keys)) : lk;
-        item->any = true;
-        break;
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += v;
+        }
+        loaded = true;
       }
-      at -= blocks * each;
+      const unsigned here = __ballot_sync(0xffffffffu, me < (before + upto) * each);
+      if (here) {
+        const int src = __ffs(here) - 1;
+        const uint32_t n = __shfl_sync(0xffffffffu, blocks, src);
+        uint32_t at = me - (before + __shfl_sync(0xffffffffu, upto, src) - n) * each;
+        it.q0 = __shfl_sync(0xffffffffu, q0, src);
+        it.lq = __shfl_sync(0xffffffffu, lq, src);
+        it.k0 = __shfl_sync(0xffffffffu, k0, src);
+        it.lk = __shfl_sync(0xffffffffu, lk, src);
+        it.part = static_cast<int>(at % p.nparts);
+        at /= p.nparts;
+        it.t0 = static_cast<int>(n - 1 - at % n) * span;
+        it.head = static_cast<int>(at / n);
+        const int64_t beg = static_cast<int64_t>(it.part) * p.part_keys;
+        it.beg = static_cast<int>(min(static_cast<int64_t>(it.lk), beg));
+        it.end = p.nparts > 1 ? static_cast<int>(min(static_cast<int64_t>(it.lk), beg + p.part_keys)) : it.lk;
+        // Key tiles of either S: up to the last key that its last token sees.  A pair's S_i are the
+        // tokens t0 + 2 i tile_toks on, half of them in each CTA, over all key tiles; a single
+        // CTA's are the even and the odd key tiles of its one query tile.
+        it.tiles = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int first = it.t0 + (CTAS == 2 ? i * CTAS * p.tile_toks : 0);
+          const int last = min(first + CTAS * p.tile_toks, it.lq) - 1;
+          int64_t vis = it.lk;
+          if (p.causal) vis = min(vis, static_cast<int64_t>(last) + 1 + it.lk - it.lq);
+          const int64_t end = min(static_cast<int64_t>(it.end), vis);
+          it.n[i] = first < it.lq && end > it.beg ? static_cast<int>((end - it.beg + kPromptKeys - 1) / kPromptKeys) : 0;
+          it.tiles = max(it.tiles, it.n[i]);
+        }
+        if (CTAS == 1) {
+          it.n[0] = (it.tiles + 1) / 2;
+          it.n[1] = it.tiles / 2;
+        }
+        return p.nparts == 1 || it.tiles > 0;   // the merge does not look for parts that nothing is in
+      }
+      if (r0 + 32 >= p.B) return false;
+      before += __shfl_sync(0xffffffffu, upto, 31);
+      r0 += 32;
+      loaded = false;
     }
   }
-  __syncthreads();
-}
+};
 
 __device__ __forceinline__ uint32_t pack16(float lo, float hi, bool fp16) {
   if (fp16) {
@@ -173,6 +205,7 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
   using S = Shape<D, E, CTAS>;
   constexpr int NQK = S::NQK, STAGES = S::STAGES;
   constexpr bool PAIR = CTAS == 2;
+  constexpr int MW = S::MMA_WARPS;
   extern __shared__ uint8_t psm_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(psm_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* qs = smem;                                   // [Q_TILES][NQK] chunks
@@ -184,17 +217,27 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
   uint64_t* v_full = k_full + STAGES;                   // [STAGES] values landed
   uint64_t* q_full = v_full + STAGES;                   // [2] query tile landed
   uint64_t* p_full = q_full + 2;                        // [2][2] P written, the first 64 keys and the others
+  uint64_t* asked = p_full + 4;                         // both CTAs have read the last answer
   // In each CTA: what the MMAs signal.
-  uint64_t* k_empty = p_full + 4;                       // [STAGES]
+  uint64_t* k_empty = asked + 1;                        // [STAGES]
   uint64_t* v_empty = k_empty + STAGES;                 // [STAGES]
-  uint64_t* s_full = v_empty + STAGES;                  // [2] S done, and with it every MMA before; at last O
-  uint64_t* drain = s_full + 2;                         // [2]
+  uint64_t* q_empty = v_empty + STAGES;                 // [2] the item's last product with a query tile is done
+  uint64_t* s_full = q_empty + 2;                       // [2] S done, and with it every MMA of this S before
+  uint64_t* o_full = s_full + 2;                        // [2] the item's O done
+  uint64_t* drain = o_full + 2;                         // [2]
+  // And within each CTA.
   uint64_t* tail = drain + 2;                           // a last tile's values landed, to be cut by the loading warp
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(tail + 1);
+  uint64_t* item_full = tail + 1;                       // [2]
+  uint64_t* item_empty = item_full + 2;                 // [2]
+  uint64_t* answered = item_empty + 2;                  // the launch's answer is there
+  uint64_t* ask = answered + 1;                         // the item's first copies are issued: time for the next
+  uint64_t* both = ask + 1;                             // the softmax warps of a single CTA
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(both + 1);
   int* abortf = reinterpret_cast<int*>(tslot + 1);
-  Item* item = reinterpret_cast<Item*>(bars + 40);
-  int64_t* totals = reinterpret_cast<int64_t*>(bars + 60);
-  static_assert(4 * STAGES + 12 <= 40 && sizeof(Item) <= 160 && 60 + WARPS <= 128, "shared scalars");
+  uint4* answer = reinterpret_cast<uint4*>(bars + 56);
+  Item* items = reinterpret_cast<Item*>(bars + 58);     // [2]
+  float* ml = reinterpret_cast<float*>(bars + 128);     // [4][128] references and sums of a single CTA's two S
+  static_assert(4 * STAGES + 26 <= 56 && 1024 + 4 * 128 * 4 <= MISC, "shared scalars");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = PAIR ? static_cast<int>(cluster_rank()) : 0;
 
@@ -202,350 +245,434 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(k_full + i, CTAS);
       mbar_init(v_full + i, CTAS);
-      mbar_init(k_empty + i, PAIR ? 2 : 1);   // a pair's tiles serve both S
-      mbar_init(v_empty + i, PAIR ? 2 : 1);
+      mbar_init(k_empty + i, PAIR ? MW : 1);   // a pair's tiles serve both S
+      mbar_init(v_empty + i, PAIR ? MW : 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(q_full + i, CTAS);
+      mbar_init(q_empty + i, PAIR ? 1 : MW);
       mbar_init(s_full + i, 1);
+      mbar_init(o_full + i, 1);
+      mbar_init(drain + i, 1);
+      mbar_init(item_full + i, 1);
+      mbar_init(item_empty + i, SOFTMAX_WARPS + 1 + (rank == 0 ? MW : 0));
     }
     for (int i = 0; i < 4; ++i) mbar_init(p_full + i, 4 * CTAS);
-    mbar_init(drain, 1);
-    mbar_init(drain + 1, 1);
+    mbar_init(asked, CTAS);
     mbar_init(tail, 1);
+    mbar_init(answered, 1);
+    mbar_init(ask, 1);
+    mbar_init(both, SOFTMAX_WARPS);
     *abortf = 0;
     fence_mbar_init();
-  }
-  grid_dep_wait();
-  find_item(p, CTAS * CTAS * p.tile_toks, blockIdx.x / CTAS, item, totals);
-  const Item it = *item;
-  if (!it.any) return;
-  // Key tiles of either S: up to the last key that its last token sees.  A pair's S_i are the
-  // tokens t0 + 2 i tile_toks on, half of them in each CTA, over all key tiles; a single CTA's
-  // are the even and the odd key tiles of its one query tile.
-  int n[2], tiles = 0;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int first = it.t0 + (PAIR ? i * CTAS * p.tile_toks : 0);
-    const int last = min(first + CTAS * p.tile_toks, it.lq) - 1;
-    int64_t vis = it.lk;
-    if (p.causal) vis = min(vis, static_cast<int64_t>(last) + 1 + it.lk - it.lq);
-    const int64_t end = min(static_cast<int64_t>(it.end), vis);
-    n[i] = first < it.lq && end > it.beg ? static_cast<int>((end - it.beg + kPromptKeys - 1) / kPromptKeys) : 0;
-    tiles = max(tiles, n[i]);
-  }
-  if (p.nparts > 1 && tiles == 0) return;   // the merge does not look for this part
-  if (!PAIR) {
-    n[0] = (tiles + 1) / 2;
-    n[1] = tiles / 2;
   }
   if (warp == MMA_WARP) tmem_alloc_all<CTAS>(tslot, 512);
   tc_fence_before();
   if (PAIR) cluster_sync();   // the other CTA's barriers are there
   else __syncthreads();
   tc_fence_after();
+  grid_dep_wait();
   const uint32_t tmem = *tslot;
   const Abort ab{abortf, p.status};
   constexpr uint32_t S_COL = 0, O_COL = 256;   // S_i (and P_i) at 128 i, O_i at 256 + 128 i
   // A barrier of the CTA of rank 0, as both CTAs reach it.
   auto at_leader = [&](uint64_t* bar) { return PAIR ? cluster_map(smem_u32(bar), 0) : smem_u32(bar); };
+  auto warp_wait = [&](uint64_t* bar, uint32_t parity) { return warp_wait1(smem_u32(bar), parity, ab); };
+  // Item c of this CTA, for every warp but the one that writes it; false: no more.
+  auto take = [&](int c, Item& it) {
+    if (!warp_wait(item_full + (c & 1), (c >> 1) & 1)) return false;
+    const int4* src = reinterpret_cast<const int4*>(items + (c & 1));
+    const int4 x = src[0], y = src[1], z = src[2];
+    it.head = x.x, it.t0 = x.y, it.lq = x.z, it.lk = x.w;
+    it.q0 = y.x, it.k0 = y.y, it.part = y.z, it.beg = y.w;
+    it.end = z.x, it.tiles = z.y, it.n[0] = z.z, it.n[1] = z.w;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(item_empty + (c & 1));
+    return it.head >= 0;
+  };
+  Item it;
 
-  if (warp == LOAD_WARP) {
-    // ---------------------------------------------------------------- loads
-    const bool leader = elect_one();
-    bool ok = true;
-    int loaded = 0;      // tiles whose copies were issued
-    bool cut = false;    // and whether the last one's values went by `tail`
-    auto load_q = [&](int i) {
-      if (!leader) return;
-      mbar_arrive_expect_tx_at(at_leader(q_full + i), NQK * p.tile_toks * p.group * 128);
-      const int tok = static_cast<int>(it.q0) + it.t0 + (PAIR ? (i * CTAS + rank) * p.tile_toks : 0);
-      for (int k = 0; k < NQK; ++k)
-        tma_load_4d_at<CTAS>(qs + (i * NQK + k) * S::Q_CHUNK, &qmap, at_leader(q_full + i), 64 * k, 0, it.head, tok);
-    };
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      ok = ok && __all_sync(0xffffffffu, mbar_wait_inline(bar, parity, ab));
-    };
-    if (tiles > 0 && (!PAIR || n[0] > 0)) load_q(0);
-    for (int j = 0, st = 0, ph = 0; j < tiles; ++j) {
-      const int row = static_cast<int>(it.k0) + it.beg + j * kPromptKeys;
-      if (j >= STAGES) wait(k_empty + st, ph ^ 1);
-      if (!ok) break;
-      if (leader) {
-        const uint32_t bar = at_leader(k_full + st);
-        mbar_arrive_expect_tx_at(bar, S::K_BYTES);
-        for (int k = 0; k < NQK; ++k) {
-          uint8_t* dst = ks + st * S::K_BYTES + k * S::K_CHUNK;
-          if (E && k == NQK - 1) tma_load_3d_at<CTAS>(dst, &smap, bar, 0, 0, row + rank * S::K_ROWS);
-          else tma_load_3d_at<CTAS>(dst, &kmap, bar, 64 * k, it.head, row + rank * S::K_ROWS);
+  if (warp >= SOFTMAX_WARPS) {
+    regs_down<OTHER_REGS>();
+    if (warp == ITEM_WARP) {
+      // ----------------------------------------------------------------- items
+      // The first by the CTA's own number; then, as the last one is begun, those of clusters that
+      // have not started, taken over from the launch one at a time.
+      ItemFinder<CTAS> finder;
+      uint32_t me = blockIdx.x / CTAS;
+      bool ok = true, more = true, pending = false;
+      int given = 0, asks = 0;
+      while (ok) {
+        const bool any = more && finder.find(p, me, it);
+        if (any || !more) {
+          const int slot = given & 1;
+          if (given >= 2) ok = warp_wait(item_empty + slot, ((given >> 1) - 1) & 1);
+          if (!ok) break;
+          if (lane == 0) {
+            int4* dst = reinterpret_cast<int4*>(items + slot);
+            dst[0] = make_int4(more ? it.head : -1, it.t0, it.lq, it.lk);
+            dst[1] = make_int4(it.q0, it.k0, it.part, it.beg);
+            dst[2] = make_int4(it.end, it.tiles, it.n[0], it.n[1]);
+            mbar_arrive(item_full + slot);
+          }
+          __syncwarp();
+          ++given;
+          if (!more) break;
+          if (rank == 0 && !(ok = warp_wait(ask, (given - 1) & 1))) break;
         }
-      }
-      __syncwarp();
-      if (j == 0 && PAIR && n[1] > 0) load_q(1);
-      if (j >= STAGES) wait(v_empty + st, ph ^ 1);
-      if (!ok) break;
-      // Weights of keys behind the last are zero; what stands in the places of their values
-      // (another sequence's, NaN and all) is set to zero, up to the MMA's step of 16 keys.
-      const int keys = min(kPromptKeys, it.end - it.beg - j * kPromptKeys);
-      cut = (keys & 15) != 0;
-      uint8_t* v0 = vs + st * S::V_BYTES;
-      if (leader) {
-        const uint32_t bar = cut ? smem_u32(tail) : at_leader(v_full + st);
-        if (cut) mbar_arrive_expect_tx(tail, S::V_BYTES);
-        else mbar_arrive_expect_tx_at(bar, S::V_BYTES);
-        for (int k = 0; k < S::V_DIMS / S::V_WIDTH; ++k)
-          tma_load_3d_at<CTAS>(v0 + k * S::V_BLOCK, &vmap, bar, rank * S::V_DIMS + k * S::V_WIDTH, it.head, row);
-      }
-      __syncwarp();
-      loaded = j + 1;
-      if (cut) {   // the last tile
-        wait(tail, 0);
-        if (!ok) break;
-        constexpr int PIECES = S::V_WIDTH / 8;
-        const int rows = (16 - (keys & 15));
-        for (int x = lane; x < rows * (S::V_DIMS / 8); x += 32) {
-          const int r = keys + x / (S::V_DIMS / 8), piece = x % (S::V_DIMS / 8);
-          *reinterpret_cast<uint4*>(v0 + piece / PIECES * S::V_BLOCK + r * S::V_WIDTH * 2 + piece % PIECES * 16) =
-              make_uint4(0, 0, 0, 0);
+        if (rank == 0 && asks > 0 && !(ok = warp_wait(asked, (asks - 1) & 1))) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(answered, 16);
+          if (rank == 0) clc_try_cancel<CTAS>(answer, answered);
         }
-        fence_proxy_async_smem();
         __syncwarp();
-        if (leader) mbar_arrive_release_at(at_leader(v_full + st));
+        pending = true;
+        if (!(ok = warp_wait(answered, asks & 1))) break;
+        pending = false;
+        ++asks;
+        uint32_t x;
+        more = clc_answer(answer, x);
+        me = x / CTAS;
+        fence_proxy_async_smem();   // the next answer is written behind these reads
+        __syncwarp();
+        if (lane == 0) mbar_arrive_release_at(at_leader(asked));
+      }
+      if (!ok && pending && lane == 0) drain_wait(answered, asks & 1);
+      __syncwarp();
+    } else if (warp == LOAD_WARP) {
+      // ---------------------------------------------------------------- loads
+      const bool leader = elect_one();
+      bool ok = true;
+      int st = 0, ph = 0;         // stage and parity of the next tile
+      int loaded = 0;             // tiles whose copies were issued
+      int cuts = 0;               // tiles whose values went by `tail`
+      bool cut = false;           // the last one's did
+      int q_loads[2] = {0, 0};
+      auto wait = [&](uint64_t* bar, uint32_t parity) { ok = ok && warp_wait(bar, parity); };
+      for (int c = 0; ok && take(c, it); ++c) {
+        auto load_q = [&](int i) {
+          if (c > 0) wait(q_empty + i, (c - 1) & 1);
+          if (!ok) return;
+          ++q_loads[i];
+          if (leader) {
+            const uint32_t bar = at_leader(q_full + i);
+            mbar_arrive_expect_tx_at(bar, NQK * p.tile_toks * p.group * 128);
+            const int tok = it.q0 + it.t0 + (PAIR ? (i * CTAS + rank) * p.tile_toks : 0);
+            for (int k = 0; k < NQK; ++k)
+              tma_load_4d_at<CTAS>(qs + (i * NQK + k) * S::Q_CHUNK, &qmap, bar, 64 * k, 0, it.head, tok);
+          }
+          __syncwarp();
+        };
+        for (int j = 0; ok && j < it.tiles; ++j) {
+          const int row = it.k0 + it.beg + j * kPromptKeys;
+          if (loaded >= STAGES) wait(k_empty + st, ph ^ 1);
+          if (!ok) break;
+          if (leader) {
+            const uint32_t bar = at_leader(k_full + st);
+            mbar_arrive_expect_tx_at(bar, S::K_BYTES);
+            for (int k = 0; k < NQK; ++k) {
+              uint8_t* dst = ks + st * S::K_BYTES + k * S::K_CHUNK;
+              if (E && k == NQK - 1) tma_load_3d_at<CTAS>(dst, &smap, bar, 0, 0, row + rank * S::K_ROWS);
+              else tma_load_3d_at<CTAS>(dst, &kmap, bar, 64 * k, it.head, row + rank * S::K_ROWS);
+            }
+          }
+          __syncwarp();
+          if (j == 0) {   // behind the first keys' copies the next item is asked for, and the queries' places are awaited
+            if (rank == 0 && leader) mbar_arrive(ask);
+            if (it.n[0] > 0) load_q(0);
+            if (PAIR && it.n[1] > 0) load_q(1);
+          }
+          if (loaded >= STAGES) wait(v_empty + st, ph ^ 1);
+          if (!ok) break;
+          // Weights of keys behind the last are zero; what stands in the places of their values
+          // (another sequence's, NaN and all) is set to zero, up to the MMA's step of 16 keys.
+          const int keys = min(kPromptKeys, it.end - it.beg - j * kPromptKeys);
+          cut = (keys & 15) != 0;
+          uint8_t* v0 = vs + st * S::V_BYTES;
+          if (leader) {
+            const uint32_t bar = cut ? smem_u32(tail) : at_leader(v_full + st);
+            if (cut) mbar_arrive_expect_tx(tail, S::V_BYTES);
+            else mbar_arrive_expect_tx_at(bar, S::V_BYTES);
+            for (int k = 0; k < S::V_DIMS / S::V_WIDTH; ++k)
+              tma_load_3d_at<CTAS>(v0 + k * S::V_BLOCK, &vmap, bar, rank * S::V_DIMS + k * S::V_WIDTH, it.head, row);
+          }
+          __syncwarp();
+          ++loaded;
+          if (cut) {   // the item's last tile
+            wait(tail, cuts & 1);
+            if (!ok) break;
+            ++cuts;
+            constexpr int PIECES = S::V_WIDTH / 8;
+            const int rows = 16 - (keys & 15);
+            for (int x = lane; x < rows * (S::V_DIMS / 8); x += 32) {
+              const int r = keys + x / (S::V_DIMS / 8), piece = x % (S::V_DIMS / 8);
+              *reinterpret_cast<uint4*>(v0 + piece / PIECES * S::V_BLOCK + r * S::V_WIDTH * 2 + piece % PIECES * 16) =
+                  make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (leader) mbar_arrive_release_at(at_leader(v_full + st));
+            __syncwarp();
+          }
+          if (++st == STAGES) st = 0, ph ^= 1;
+        }
+        if (it.tiles == 0 && rank == 0 && leader) mbar_arrive(ask);
         __syncwarp();
       }
-      if (++st == STAGES) st = 0, ph ^= 1;
-    }
-    // After a failed wait: no copy into shared memory outlives the CTA.  The barriers that the
-    // other CTA's copies count on are in the CTA of rank 0, which waits for them.
-    if (!ok && leader && rank == 0) {
-      for (int j = max(0, loaded - STAGES); j < loaded; ++j) {
-        drain_wait(k_full + j % STAGES, (j / STAGES) & 1);
-        if (!(cut && j == loaded - 1)) drain_wait(v_full + j % STAGES, (j / STAGES) & 1);
+      // After a failed wait: no copy into shared memory outlives the CTA.  The barriers that the
+      // other CTA's copies count on are in the CTA of rank 0, which waits for them.
+      if (*reinterpret_cast<volatile int*>(abortf) && leader) {
+        if (rank == 0) {
+          for (int j = max(0, loaded - STAGES); j < loaded; ++j) {
+            drain_wait(k_full + j % STAGES, (j / STAGES) & 1);
+            if (!(cut && j == loaded - 1)) drain_wait(v_full + j % STAGES, (j / STAGES) & 1);
+          }
+          for (int i = 0; i < 2; ++i)
+            if (q_loads[i] > 0) drain_wait(q_full + i, (q_loads[i] - 1) & 1);
+        }
+        if (cut && !ok) drain_wait(tail, cuts & 1);
       }
-      if (n[0] > 0) drain_wait(q_full, 0);
-      if (PAIR && n[1] > 0) drain_wait(q_full + 1, 0);
-    }
-    if (!ok && leader && cut) drain_wait(tail, 0);
-    __syncwarp();
-  } else if ((warp == MMA_WARP || warp == MMA_WARP + 1) && rank == 0) {
-    // ------------------------------------------------------------ MMA issuers
-    // One warp per S, so that the waits and the bookkeeping of one (about 100 cycles a wait) run
-    // beside the products of the other: one warp for both took 1,750 cycles a tile, the products
-    // of D = 128, E = 64 take 1,280.
-    const bool leader = elect_one();
-    const int i = warp - MMA_WARP;
-    constexpr uint32_t fmt = FP16 ? 0u : 1u;
-    constexpr uint32_t idesc_qk = make_idesc(fmt, fmt, false, false, 128 * CTAS, kPromptKeys);
-    constexpr uint32_t idesc_pv = make_idesc(fmt, fmt, false, true, 128 * CTAS, D);
-    const uint64_t dq = make_sdesc_sw128(smem_u32(qs) + (PAIR ? i : 0) * NQK * S::Q_CHUNK, 16, 1024);   // queries, K-major
-    const uint64_t dk = make_sdesc_sw128(smem_u32(ks), 16, 1024);                                       // keys, K-major
-    const uint64_t dv = S::V_WIDTH == 64 ? make_sdesc_sw128(smem_u32(vs), S::V_BLOCK, 1024)             // values, MN-major
-                                         : make_sdesc_sw64(smem_u32(vs), S::V_BLOCK, 512);
-    const uint32_t kf = smem_u32(k_full), vf = smem_u32(v_full), pf = smem_u32(p_full + 2 * i);
-    const uint32_t s_tmem = tmem + S_COL + 128 * i, o_tmem = tmem + O_COL + 128 * i;
-    constexpr int STEP = PAIR ? 1 : 2;   // key tiles from one of this S to its next
-    const int ni = n[i];
-    bool ok = true;
-    int kst = 0, kph = 0, vst = 0, vph = 0;   // stage and parity of the next key and value tile
-    auto next = [](int& st, int& ph, int by) {
-      if ((st += by) >= STAGES) st -= STAGES, ph ^= 1;
-    };
-    if (!PAIR && i == 1) next(kst, kph, 1), next(vst, vph, 1);
-    auto scores = [&]() {   // S_i = Q_i K^T
-      if (leader) {
-        const uint64_t b = dk + ((kst * S::K_BYTES) >> 4);
+      __syncwarp();
+    } else if (warp < MMA_WARP + MW && rank == 0) {
+      // ------------------------------------------------------------ MMA issuer(s)
+      const bool leader = elect_one();
+      const int w = warp - MMA_WARP;
+      constexpr uint32_t fmt = FP16 ? 0u : 1u;
+      constexpr uint32_t idesc_qk = make_idesc(fmt, fmt, false, false, 128 * CTAS, kPromptKeys);
+      constexpr uint32_t idesc_pv = make_idesc(fmt, fmt, false, true, 128 * CTAS, D);
+      const uint64_t dq = make_sdesc_sw128(smem_u32(qs), 16, 1024);                              // queries, K-major
+      const uint64_t dk = make_sdesc_sw128(smem_u32(ks), 16, 1024);                              // keys, K-major
+      const uint64_t dv = S::V_WIDTH == 64 ? make_sdesc_sw128(smem_u32(vs), S::V_BLOCK, 1024)    // values, MN-major
+                                           : make_sdesc_sw64(smem_u32(vs), S::V_BLOCK, 512);
+      const uint32_t kf = smem_u32(k_full), vf = smem_u32(v_full), pf = smem_u32(p_full), qf = smem_u32(q_full);
+      bool ok = true;
+      int bst = 0, bph = 0;            // stage and parity of the item's first key tile
+      int q_loads[2] = {0, 0}, turns[2] = {0, 0};   // of either S: query tiles taken, P's taken
+      for (int c = 0; ok && take(c, it); ++c) {
+        // Step s is S_i's, i = s % 2, on its key tile j = s / 2: tile j of a pair, tile s of a single
+        // CTA.  A warp takes both S, or one of them.
+        auto stage = [&](int t, int& st, int& ph) {
+          const int x = bst + t;
+          st = x % STAGES;
+          ph = bph ^ ((x / STAGES) & 1);
+        };
+        auto last_user = [&](int i, int j) { return !PAIR || MW == 2 || i == 1 || j >= it.n[1]; };
+        auto scores = [&](int i, int j, int st) {   // S_i = Q_i K^T
+          if (leader) {
+            const uint64_t a = dq + (((PAIR ? i : 0) * NQK * S::Q_CHUNK) >> 4), b = dk + ((st * S::K_BYTES) >> 4);
 #pragma unroll
-        for (int k = 0; k < NQK; ++k)
+            for (int k = 0; k < NQK; ++k)
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_f16_ss<CTAS>(s_tmem, dq + ((k * S::Q_CHUNK + 32 * kk) >> 4), b + ((k * S::K_CHUNK + 32 * kk) >> 4), idesc_qk,
-                             k || kk ? 1u : 0u);
-        tc_commit_all<CTAS>(s_full + i);
-        tc_commit_all<CTAS>(k_empty + kst);
-      }
-      __syncwarp();
-      next(kst, kph, STEP);
-    };
-    if (ni > 0) {
-      const uint32_t q = smem_u32(q_full + (PAIR ? i : 0));
-      ok = warp_wait2(kf + 8 * kst, kph, q, 0, ab);
-      tc_fence_after();
-      if (ok) scores();
-    }
-    for (int j = 0; ok && j < ni; ++j) {
-      const int keys = it.end - it.beg - (PAIR ? j : 2 * j + i) * kPromptKeys;
-      const int todo = (min(kPromptKeys, keys) + 15) / 16;   // MMAs of 16 keys
-      const bool more = j + 1 < ni;
-      const uint64_t b = dv + ((vst * S::V_BYTES) >> 4);
-      // O_i += P_i V; the first half waits for the values, too, the second for the next keys
-      if (!(ok = warp_wait2(pf, j & 1, vf + 8 * vst, vph, ab))) break;
-      if (PAIR && keys < kPromptKeys) mbar_acquire_cluster(v_full + vst, vph);   // values cut by plain stores
-      tc_fence_after();
-      if (leader) {
+              for (int kk = 0; kk < 4; ++kk)
+                mma_f16_ss<CTAS>(tmem + S_COL + 128 * i, a + ((k * S::Q_CHUNK + 32 * kk) >> 4), b + ((k * S::K_CHUNK + 32 * kk) >> 4),
+                                 idesc_qk, k || kk ? 1u : 0u);
+            tc_commit_all<CTAS>(s_full + i);
+            if (last_user(i, j)) tc_commit_all<CTAS>(k_empty + st);
+          }
+          __syncwarp();
+        };
+        // This warp has issued its last product with the query tile(s) of S_i.
+        auto queries_done = [&](int i) {
+          if (leader && (PAIR || MW == 2 || i == 1)) tc_commit_all<CTAS>(q_empty + (PAIR ? i : 0));
+          __syncwarp();
+        };
+        for (int i = w; i < 2; i += MW) {
+          const int ni = i ? it.n[1] : it.n[0];
+          if (ni > 0) {
+            int st, ph;
+            stage(PAIR ? 0 : i, st, ph);
+            ok = ok && warp_wait2(kf + 8 * st, ph, qf + (PAIR ? 8 * i : 0), (i ? q_loads[1] : q_loads[0]) & 1, ab);
+            tc_fence_after();
+            if (!ok) break;
+            scores(i, 0, st);
+          }
+          if (ni <= 1) queries_done(i);
+          (i ? q_loads[1] : q_loads[0]) += (PAIR ? ni : it.tiles) > 0;
+        }
+        const int steps = 2 * max(it.n[0], it.n[1]);
+        for (int s = w; ok && s < steps; s += MW) {
+          const int i = s & 1, j = s >> 1, ni = i ? it.n[1] : it.n[0], t = PAIR ? j : s;
+          int vst, vph, kst, kph;
+          stage(t, vst, vph);
+          stage(t + (PAIR ? 1 : 2), kst, kph);
+          if (j >= ni) {   // nothing left for this S
+            if (PAIR && MW == 2) {   // the other's tiles go back as they come
+              if (!(ok = warp_wait2(kf + 8 * vst, vph, vf + 8 * vst, vph, ab))) break;
+              if (leader) {
+                tc_commit_all<CTAS>(k_empty + vst);
+                tc_commit_all<CTAS>(v_empty + vst);
+              }
+              __syncwarp();
+            }
+            continue;
+          }
+          const int keys = it.end - it.beg - t * kPromptKeys;
+          const int todo = (min(kPromptKeys, keys) + 15) / 16;   // MMAs of 16 keys
+          const bool more = j + 1 < ni;
+          const uint32_t pi = pf + 16 * i, turn = (i ? turns[1] : turns[0]) & 1;
+          const uint32_t s_tmem = tmem + S_COL + 128 * i, o_tmem = tmem + O_COL + 128 * i;
+          const uint64_t b = dv + ((vst * S::V_BYTES) >> 4);
+          // O_i += P_i V; the first half waits for the values, too, the second for the next keys.  P's
+          // of a new item come when the softmax is done with the last one's O.
+          if (!(ok = warp_wait2(pi, turn, vf + 8 * vst, vph, ab))) break;
+          if (PAIR && keys < kPromptKeys) mbar_acquire_cluster(v_full + vst, vph);   // values cut by plain stores
+          tc_fence_after();
+          if (leader) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (k < todo) mma_f16_ts<CTAS>(o_tmem, s_tmem + 8 * k, b + ((k * 32 * S::V_WIDTH) >> 4), idesc_pv, j || k ? 1u : 0u);
-      }
-      __syncwarp();
-      if (!(ok = warp_wait2(pf + 8, j & 1, more ? kf + 8 * kst : pf + 8, more ? kph : j & 1, ab))) break;
-      tc_fence_after();
-      if (leader) {
+            for (int k = 0; k < 4; ++k)
+              if (k < todo) mma_f16_ts<CTAS>(o_tmem, s_tmem + 8 * k, b + ((k * 32 * S::V_WIDTH) >> 4), idesc_pv, j || k ? 1u : 0u);
+          }
+          __syncwarp();
+          if (!(ok = warp_wait2(pi + 8, turn, more ? kf + 8 * kst : pi + 8, more ? kph : turn, ab))) break;
+          tc_fence_after();
+          if (leader) {
 #pragma unroll
-        for (int k = 4; k < 8; ++k)
-          if (k < todo) mma_f16_ts<CTAS>(o_tmem, s_tmem + 8 * k, b + ((k * 32 * S::V_WIDTH) >> 4), idesc_pv, 1u);
-        tc_commit_all<CTAS>(v_empty + vst);
+            for (int k = 4; k < 8; ++k)
+              if (k < todo) mma_f16_ts<CTAS>(o_tmem, s_tmem + 8 * k, b + ((k * 32 * S::V_WIDTH) >> 4), idesc_pv, 1u);
+            if (last_user(i, j)) tc_commit_all<CTAS>(v_empty + vst);
+            if (!more) tc_commit_all<CTAS>(o_full + i);
+          }
+          __syncwarp();
+          if (more) scores(i, j + 1, kst);
+          if (j + 2 == ni) queries_done(i);
+          ++(i ? turns[1] : turns[0]);
+        }
+        const int total = bst + it.tiles;
+        bph ^= (total / STAGES) & 1;
+        bst = total % STAGES;
+      }
+      if (*reinterpret_cast<volatile int*>(abortf) && leader) {
+        tc_commit_all<CTAS>(drain + w);
+        drain_wait(drain + w, 0);
       }
       __syncwarp();
-      next(vst, vph, STEP);
-      if (more) scores();
-      else if (leader) tc_commit_all<CTAS>(s_full + i);   // O_i is done
-      __syncwarp();
     }
-    // a pair's tiles behind this S's last go back as they come
-    for (int j = ni; PAIR && ok && j < tiles; ++j) {
-      if (!(ok = warp_wait2(kf + 8 * kst, kph, vf + 8 * vst, vph, ab))) break;
-      if (leader) {
-        tc_commit_all<CTAS>(k_empty + kst);
-        tc_commit_all<CTAS>(v_empty + vst);
-      }
-      __syncwarp();
-      next(kst, kph, 1);
-      next(vst, vph, 1);
-    }
-    if (!ok && leader) {
-      tc_commit_all<CTAS>(drain + i);
-      drain_wait(drain + i, 0);
-    }
-    __syncwarp();
-  } else if (warp < SOFTMAX_WARPS) {
+  } else {
     // ------------------------------------------------ softmax and epilogue (0..7)
+    regs_up<SOFTMAX_REGS>();
     const int i = warp >> 2, quarter = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t ts = tmem + S_COL + 128 * i + lanes, to = tmem + O_COL + 128 * i + lanes;
+    const uint32_t ts = tmem + S_COL + 128 * i + lanes, to = tmem + O_COL + lanes;   // O_i at to + 128 i
     const int row = 32 * quarter + lane;
-    const int tok = it.t0 + (PAIR ? (i * CTAS + rank) * p.tile_toks : 0) + row / p.group, g = row % p.group;
-    const bool valid = row < p.tile_toks * p.group && tok < it.lq;
-    // keys of this part that the row sees
-    int64_t sees = it.lk;
-    if (p.causal) sees = min(sees, static_cast<int64_t>(tok) + 1 + it.lk - it.lq);
-    const int vis = valid ? static_cast<int>(max(static_cast<int64_t>(0), min(sees, static_cast<int64_t>(it.end)) - it.beg))
-                          : it.end - it.beg;
-    const int all_see = __reduce_min_sync(0xffffffffu, vis);
+    const int row_tok = (PAIR ? (i * CTAS + rank) * p.tile_toks : 0) + row / p.group, g = row % p.group;
+    const bool row_used = row < p.tile_toks * p.group;
     const float sc = p.scale_log2;
     constexpr float SHIFT = FP16 ? 7.f : 0.f;
     const uint32_t p_bar[2] = {at_leader(p_full + 2 * i), at_leader(p_full + 2 * i + 1)};
-    float m = -INFINITY;           // reference: a logit of m has weight 2^SHIFT
-    float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     bool ok = true;
-    const int ni = n[i];
-    for (int j = 0; j < ni; ++j) {
-      ok = __all_sync(0xffffffffu, ok && mbar_wait_inline(s_full + i, j & 1, ab));
+    int turns = 0, outs = 0, syncs = 0;   // phases of s_full, o_full and both
+    // All softmax warps of a single CTA, for which a failed wait ends this one, too.
+    auto sync = [&]() {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(both);
+      ok = ok && warp_wait(both, syncs++ & 1);
+      tc_fence_after();
+    };
+    for (int c = 0; ok && take(c, it); ++c) {
+      const int tok = it.t0 + row_tok;
+      const bool valid = row_used && tok < it.lq;
+      // keys of this part that the row sees
+      int64_t sees = it.lk;
+      if (p.causal) sees = min(sees, static_cast<int64_t>(tok) + 1 + it.lk - it.lq);
+      const int vis = valid ? static_cast<int>(max(static_cast<int64_t>(0), min(sees, static_cast<int64_t>(it.end)) - it.beg))
+                            : it.end - it.beg;
+      const int all_see = __reduce_min_sync(0xffffffffu, vis);
+      float m = -INFINITY;           // reference: a logit of m has weight 2^SHIFT
+      float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      const int ni = i ? it.n[1] : it.n[0];
+      for (int j = 0; j < ni; ++j, ++turns) {
+        ok = ok && warp_wait(s_full + i, turns & 1);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t r[4][32];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) DSA_TMEM_LD32(ts + 32 * b, r[b]);
+        tmem_wait_ld();
+        const int k0 = (PAIR ? j : 2 * j + i) * kPromptKeys;
+        if (all_see < k0 + kPromptKeys) {
+          const int limit = vis - k0;
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              if (32 * b + x >= limit) r[b][x] = 0xFF800000u;   // -inf
+        }
+        float mx[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          mx[b] = fmaxf(__uint_as_float(r[b][0]), __uint_as_float(r[b][1]));
+#pragma unroll
+          for (int x = 2; x < 32; x += 2) mx[b] = fmaxf(mx[b], fmaxf(__uint_as_float(r[b][x]), __uint_as_float(r[b][x + 1])));
+        }
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+        const bool moves = valid && top > m + GROW;
+        if (__any_sync(0xffffffffu, moves)) {
+          // A row moves its own reference alone: its result does not depend on its neighbours.
+          const float now = moves ? top : m;
+          const float f = now == -INFINITY ? 1.f : ex2(m - now);
+          m = now;
+          l2[0].x *= f, l2[0].y *= f, l2[1].x *= f, l2[1].y *= f;
+          if (j > 0) {
+            // every MMA before S is done, so O is still
+#pragma unroll 1
+            for (int b = 0; b < D / 16; ++b) {
+              uint32_t o[16];
+              DSA_TMEM_LD16(to + 128 * i + 16 * b, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+              DSA_TMEM_ST16(to + 128 * i + 16 * b, o);
+            }
+            tmem_wait_st();
+          }
+        }
+        const float ref = m == -INFINITY ? 0.f : SHIFT - m;   // nothing seen yet: weights 2^-inf
+        const float2 sc2 = make_float2(sc, sc), ref2 = make_float2(ref, ref);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+#pragma unroll
+          for (int x = 0; x < 32; x += 2) {
+            float2 y = ffma2(make_float2(__uint_as_float(r[b][x]), __uint_as_float(r[b][x + 1])), sc2, ref2);
+            y.x = ex2(y.x);
+            y.y = ex2(y.y);
+            l2[(x >> 1) & 1] = fadd2(l2[(x >> 1) & 1], y);
+            r[b][x >> 1] = pack16(y.x, y.y, FP16);
+          }
+          DSA_TMEM_ST16(ts + 16 * b, r[b]);
+          if (b & 1) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_at(p_bar[b >> 1]);
+          }
+        }
+      }
+      if (ok && ni > 0) ok = warp_wait(o_full + i, outs & 1);
+      outs += ni > 0;
       if (!ok) break;
       tc_fence_after();
-      uint32_t r[4][32];
-#pragma unroll
-      for (int b = 0; b < 4; ++b) DSA_TMEM_LD32(ts + 32 * b, r[b]);
-      tmem_wait_ld();
-      const int k0 = (PAIR ? j : 2 * j + i) * kPromptKeys;
-      if (all_see < k0 + kPromptKeys) {
-        const int limit = vis - k0;
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-#pragma unroll
-          for (int x = 0; x < 32; ++x)
-            if (32 * b + x >= limit) r[b][x] = 0xFF800000u;   // -inf
+      // ---- O / sum, joined with an earlier result where there is one
+      float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
+      constexpr int MINE = PAIR ? D : D / 2;        // dims that this thread writes, from d0 on
+      const int d0 = PAIR ? 0 : i * MINE;
+      float w0 = 1.f, w1 = 1.f;                     // a single CTA: weights of O_0 and O_1
+      if (!PAIR) {
+        // Both threads of a row (they reach the same lanes of tensor memory) take the common
+        // reference, and half of the dims of either O.
+        ml[128 * i + row] = m;
+        ml[256 + 128 * i + row] = l;
+        sync();
+        if (!ok) break;
+        const float m0 = ml[row], m1 = ml[128 + row];
+        m = fmaxf(m0, m1);
+        w0 = m == -INFINITY ? 0.f : ex2(m0 - m);
+        w1 = m == -INFINITY ? 0.f : ex2(m1 - m);
+        l = ml[256 + row] * w0 + ml[384 + row] * w1;
       }
-      float mx[4];
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        mx[b] = fmaxf(__uint_as_float(r[b][0]), __uint_as_float(r[b][1]));
-#pragma unroll
-        for (int x = 2; x < 32; x += 2) mx[b] = fmaxf(mx[b], fmaxf(__uint_as_float(r[b][x]), __uint_as_float(r[b][x + 1])));
-      }
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
-      const bool moves = valid && top > m + GROW;
-      if (__any_sync(0xffffffffu, moves)) {
-        // A row moves its own reference alone: its result does not depend on its neighbours.
-        const float now = moves ? top : m;
-        const float f = now == -INFINITY ? 1.f : ex2(m - now);
-        m = now;
-        l2[0].x *= f, l2[0].y *= f, l2[1].x *= f, l2[1].y *= f;
-        if (j > 0) {
-          // every MMA before S is done, so O is still
-#pragma unroll 1
-          for (int b = 0; b < D / 16; ++b) {
-            uint32_t o[16];
-            DSA_TMEM_LD16(to + 16 * b, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-            DSA_TMEM_ST16(to + 16 * b, o);
-          }
-          tmem_wait_st();
-        }
-      }
-      const float ref = m == -INFINITY ? 0.f : SHIFT - m;   // nothing seen yet: weights 2^-inf
-      const float2 sc2 = make_float2(sc, sc), ref2 = make_float2(ref, ref);
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-#pragma unroll
-        for (int x = 0; x < 32; x += 2) {
-          float2 y = ffma2(make_float2(__uint_as_float(r[b][x]), __uint_as_float(r[b][x + 1])), sc2, ref2);
-          y.x = ex2(y.x);
-          y.y = ex2(y.y);
-          l2[(x >> 1) & 1] = fadd2(l2[(x >> 1) & 1], y);
-          r[b][x >> 1] = pack16(y.x, y.y, FP16);
-        }
-        DSA_TMEM_ST16(ts + 16 * b, r[b]);
-        if (b & 1) {
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_at(p_bar[b >> 1]);
-        }
-      }
-    }
-    if (ok && ni > 0) ok = __all_sync(0xffffffffu, mbar_wait_inline(s_full + i, ni & 1, ab));
-    tc_fence_after();
-    // ---- O / sum, joined with an earlier result where there is one
-    float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y), other = 0.f;
-    constexpr int MINE = PAIR ? D : D / 2;        // dims that this thread writes, from d0 on
-    const int d0 = PAIR ? 0 : i * MINE;
-    float4* swap = reinterpret_cast<float4*>(ks);   // [D / 4][128 rows]: every key and value is read by now
-    if (!PAIR) {
-      // The two S of a tile: each thread hands over half of its O, weighed by the common reference.
-      float* ml = reinterpret_cast<float*>(bars + 128);   // [2][128] references, sums
-      ml[128 * i + row] = m;
-      ok = !named_bar_any(1, 32 * SOFTMAX_WARPS, !ok);
-      const float mo = ml[128 * (1 - i) + row], both = fmaxf(m, mo);
-      const float w = both == -INFINITY ? 0.f : ex2(m - both);
-      l *= w;
-      m = both;
-      const int dh = (1 - i) * MINE;                // the other thread's dims
-      if (ok) {
-#pragma unroll 1
-        for (int b = 0; b < MINE / 16; ++b) {
-          uint32_t o[16] = {};
-          if (ni > 0) {
-            DSA_TMEM_LD16(to + dh + 16 * b, o);
-            tmem_wait_ld();
-          }
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            swap[((dh + 16 * b) / 4 + x) * kPromptRows + row] =
-                make_float4(__uint_as_float(o[4 * x]) * w, __uint_as_float(o[4 * x + 1]) * w, __uint_as_float(o[4 * x + 2]) * w,
-                            __uint_as_float(o[4 * x + 3]) * w);
-        }
-      }
-      ml[256 + 128 * i + row] = l;
-      named_bar_sync(1, 32 * SOFTMAX_WARPS);
-      l += ml[256 + 128 * (1 - i) + row];
-      other = w;
-    }
-    const bool empty_row = !(l > 0.f);   // nothing seen
-    const float lse2 = empty_row ? -INFINITY : m - SHIFT + log2f(l);
-    const int64_t at = (it.q0 + tok) * p.heads + static_cast<int64_t>(it.head) * p.group + g;
-    if (ok) {
+      const bool empty_row = !(l > 0.f);   // nothing seen
+      const float lse2 = empty_row ? -INFINITY : m - SHIFT + log2f(l);
+      const int64_t at = static_cast<int64_t>(it.q0 + tok) * p.heads + static_cast<int64_t>(it.head) * p.group + g;
       float w = empty_row ? 0.f : 1.f / l, wp = 0.f;
       float lse = lse2 * 0.6931471805599453f;
       const bool last = p.nparts == 1;
@@ -554,7 +681,10 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
         lse = join_lse(p.prev_lse[at], lse, wp, wn);
         w *= wn;
       }
-      if (!PAIR) named_bar_sync(1, 32 * SOFTMAX_WARPS);   // prev_lse may be lse: both threads of a row have read it
+      w0 *= w;
+      w1 *= w;
+      if (!PAIR) sync();   // prev_lse may be lse, and ml is written again
+      if (!ok) break;
       if (valid && d0 == 0) {
         if (!last) p.part_lse[static_cast<int64_t>(it.part) * p.total_q * p.heads + at] = lse2;
         else if (p.lse) p.lse[at] = lse;
@@ -562,23 +692,23 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
 #pragma unroll 1
       for (int b = 0; b < MINE / 32; ++b) {
         uint32_t o[32] = {};
-        if (ni > 0) {
-          DSA_TMEM_LD32(to + d0 + 32 * b, o);
+        if (PAIR) {
+          if (ni > 0) {
+            DSA_TMEM_LD32(to + 128 * i + 32 * b, o);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int x = 0; x < 32; ++x) o[x] = empty_row ? 0u : __float_as_uint(__uint_as_float(o[x]) * w0);
+        } else {
+          uint32_t o1[32] = {};
+          if (it.n[0] > 0) DSA_TMEM_LD32(to + d0 + 32 * b, o);
+          if (it.n[1] > 0) DSA_TMEM_LD32(to + 128 + d0 + 32 * b, o1);
           tmem_wait_ld();
+#pragma unroll
+          for (int x = 0; x < 32; ++x)
+            o[x] = empty_row ? 0u : __float_as_uint(fmaf(__uint_as_float(o1[x]), w1, __uint_as_float(o[x]) * w0));
         }
         if (!valid) continue;
-        if (!PAIR) {
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            const float4 v = swap[((d0 + 32 * b) / 4 + x) * kPromptRows + row];
-            o[4 * x] = __float_as_uint(fmaf(__uint_as_float(o[4 * x]), other, v.x));
-            o[4 * x + 1] = __float_as_uint(fmaf(__uint_as_float(o[4 * x + 1]), other, v.y));
-            o[4 * x + 2] = __float_as_uint(fmaf(__uint_as_float(o[4 * x + 2]), other, v.z));
-            o[4 * x + 3] = __float_as_uint(fmaf(__uint_as_float(o[4 * x + 3]), other, v.w));
-          }
-        }
-#pragma unroll
-        for (int x = 0; x < 32; ++x) o[x] = empty_row ? 0u : __float_as_uint(__uint_as_float(o[x]) * w);
         if (!last) {
           float4* dst = reinterpret_cast<float4*>(p.part_o + (static_cast<int64_t>(it.part) * p.total_q * p.heads + at) * D +
                                                   d0 + 32 * b);
@@ -602,16 +732,21 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
             }
           }
         }
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * D + d0 + 32 * b);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          uint32_t v[4];
+        for (int x = 0; x < 16; ++x) o[x] = pack16(__uint_as_float(o[2 * x]), __uint_as_float(o[2 * x + 1]), FP16);
+        uint16_t* dst = static_cast<uint16_t*>(p.out) + at * D + d0 + 32 * b;
+        if (p.out_aligned32) {   // whole sectors
+          st_global_v8(dst, o);
+          st_global_v8(dst + 16, o + 8);
+        } else {
 #pragma unroll
-          for (int y = 0; y < 4; ++y)
-            v[y] = pack16(__uint_as_float(o[8 * x + 2 * y]), __uint_as_float(o[8 * x + 2 * y + 1]), FP16);
-          dst[x] = make_uint4(v[0], v[1], v[2], v[3]);
+          for (int x = 0; x < 4; ++x)
+            reinterpret_cast<uint4*>(dst)[x] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
         }
       }
+      // the next item's O is written once every warp that reads this one's has its next P in place
+      tc_fence_before();
+      if (!PAIR) sync();
     }
   }
   tc_fence_before();

@@ -24,6 +24,7 @@ struct PromptParams {
   int32_t part_keys;       // keys of a part (a multiple of 128)
   void* out;               // [total_q, heads, D]
   float* lse;              // [total_q, heads] or null
+  int32_t out_aligned32;   // out begins at a multiple of 32 bytes
   const void* prev_out;    // [total_q, heads, D] or null
   const float* prev_lse;
   float* part_o;           // [nparts, total_q, heads, D] (nparts > 1), normalised

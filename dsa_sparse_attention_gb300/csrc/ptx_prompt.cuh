@@ -10,6 +10,24 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// 32 bytes in one store (32-byte aligned).
+__device__ __forceinline__ void st_global_v8(void* dst, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+               "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// Registers a thread from here on; every warp of a warpgroup (four warps) calls it.  A block's
+// shares together must not exceed what it was launched with.
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // Two fp32 operations an instruction.
 __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
   float2 d;
@@ -126,17 +144,43 @@ __device__ __forceinline__ void mbar_acquire_cluster(uint64_t* bar, uint32_t par
   mbar_try_wait_cluster(smem_u32(bar), parity);
 }
 
-// Waits, as a converged warp, for two phases at a time (addresses in this CTA's shared memory);
-// as mbar_wait_inline otherwise.
-__device__ __forceinline__ bool warp_wait2(uint32_t a, uint32_t pa, uint32_t b, uint32_t pb, Abort ab) {
-  auto done = [&] {
-    const bool x = mbar_try_wait(a, pa), y = mbar_try_wait(b, pb);
-    return __all_sync(0xffffffffu, x && y);
-  };
-  if (done()) return true;
+// ------------------------------------------------- work handed out by the launch (cluster launch control)
+// A running cluster takes over one that has not started: its first CTA's number comes as a
+// 16-byte answer, with its bytes counted on `bar`, in every CTA of the cluster.
+template <int CTAS>
+__device__ __forceinline__ void clc_try_cancel(void* answer, uint64_t* bar) {
+  if (CTAS == 1)
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     smem_u32(answer)),
+                 "r"(smem_u32(bar))
+                 : "memory");
+  else
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.multicast::cluster::all.b128 [%0], "
+        "[%1];" ::"r"(smem_u32(answer)),
+        "r"(smem_u32(bar))
+        : "memory");
+}
+// Whether a cluster was taken over, and the number (x) of its first CTA.
+__device__ __forceinline__ bool clc_answer(const void* answer, uint32_t& cta_x) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 a;\n\tld.shared.b128 a, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\tselp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, a;\n\t}"
+      : "=r"(ok), "=r"(cta_x)
+      : "r"(smem_u32(answer))
+      : "memory");
+  return ok != 0;
+}
+
+// Waits, as a converged warp, until `done()` holds in every lane; gives up as mbar_wait_inline does.
+template <typename Done>
+__device__ __forceinline__ bool warp_wait_until(Done done, Abort ab) {
+  if (__all_sync(0xffffffffu, done())) return true;
   const long long t0 = clock64();
   for (uint32_t it = 1;; ++it) {
-    if (done()) return true;
+    if (__all_sync(0xffffffffu, done())) return true;
     if ((it & 15u) == 0u) {
       bool late = false;
       if (clock64() - t0 > kWaitLimitCycles) {
@@ -147,6 +191,18 @@ __device__ __forceinline__ bool warp_wait2(uint32_t a, uint32_t pa, uint32_t b, 
       if (__any_sync(0xffffffffu, late || *reinterpret_cast<volatile int*>(ab.flag))) return false;
     }
   }
+}
+// For a phase of one barrier, or of two at a time (addresses in this CTA's shared memory).
+__device__ __forceinline__ bool warp_wait1(uint32_t a, uint32_t pa, Abort ab) {
+  return warp_wait_until([&] { return mbar_try_wait(a, pa); }, ab);
+}
+__device__ __forceinline__ bool warp_wait2(uint32_t a, uint32_t pa, uint32_t b, uint32_t pb, Abort ab) {
+  return warp_wait_until(
+      [&] {
+        const bool x = mbar_try_wait(a, pa), y = mbar_try_wait(b, pb);
+        return x && y;
+      },
+      ab);
 }
 
 // Copies into this CTA's shared memory whose bytes count on a barrier of either CTA of the pair.
