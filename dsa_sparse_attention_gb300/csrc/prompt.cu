@@ -23,6 +23,8 @@
 // start from 2^7 to keep more of what is small), sums are fp32 of the unrounded weights.
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "../../include/dsa.h"
 #include "prompt.cuh"
 #include "ptx_prompt.cuh"
@@ -58,11 +60,20 @@ struct Shape {
   static constexpr int STAGES = FIT < 6 ? FIT : 6;
   static constexpr int SMEM = 1024 + Q_BYTES + STAGES * (K_BYTES + V_BYTES) + MISC;
   static_assert(STAGES >= 2, "the values of a tile and the keys of the next are in use at a time");
-  // Warps that issue MMAs: one for both S of a pair at D = 128, whose products then alternate of
-  // themselves (with a warp each, both softmaxes fall into step and the tensor core waits for them:
-  // 3,300 cycles a key tile, not 2,800); else one per S.
-  static constexpr int MMA_WARPS = CTAS == 2 && D == 128 ? 1 : 2;
+  // Warps that issue MMAs.  One for both S: their products alternate of themselves, where two warps
+  // fall into step, both softmaxes at a time with the tensor core waiting (3,300 cycles a key tile of
+  // D = 128, not 2,800).  At D = 64 the waits and the bookkeeping of a step (about 900 cycles) exceed
+  // its products (512), and a pair has a warp per S.  (A single CTA's S take every other tile, and a
+  // warp that passed over tiles could mistake a phase of their barriers for the one before it.)
+  static constexpr int MMA_WARPS = CTAS == 2 && D == 64 ? 2 : 1;
 };
+
+// The item's query tile that the CTA of rank r has in S_i.  Of a pair's four the inner two make S_0,
+// the outer two S_1: causally their last keys are then within a tile of each other.
+template <int CTAS>
+__host__ __device__ constexpr int query_tile(int i, int r) {
+  return CTAS == 1 ? 0 : i == 0 ? 1 + r : 3 * r;
+}
 
 // The work of a CTA or of a pair: query tiles of one key head over a range of one sequence's keys.
 struct __align__(16) Item {
@@ -93,9 +104,10 @@ __device__ __forceinline__ bool prompt_seq(const PromptParams& p, int r, int& q0
   return true;
 }
 
-// Finds items by their numbers: sequences in order, of each its key heads, of each head its blocks
-// of queries, the last (the longest, causally) first, and the parts of the keys.  One warp, a lane
-// a sequence; numbers come in ascending order but for a few, so it walks on from where it was.
+// Finds items by their numbers: sequences in order, of each groups of key heads, of a group its
+// blocks of queries, the last (the longest, causally) first, of a block the heads and the parts of
+// the keys: the shortest items of a group come last, and so do the launch's.  One warp, a lane a
+// sequence; numbers come in ascending order but for a few, so it walks on from where it was.
 template <int CTAS>
 struct ItemFinder {
   int r0 = 0;            // first sequence of the lanes'
@@ -131,25 +143,33 @@ struct ItemFinder {
         it.lq = __shfl_sync(0xffffffffu, lq, src);
         it.k0 = __shfl_sync(0xffffffffu, k0, src);
         it.lk = __shfl_sync(0xffffffffu, lk, src);
-        it.part = static_cast<int>(at % p.nparts);
-        at /= p.nparts;
-        it.t0 = static_cast<int>(n - 1 - at % n) * span;
-        it.head = static_cast<int>(at / n);
+        // key heads in groups whose keys and values stay in L2 together
+        const uint32_t heads = p.kv_heads, parts = p.nparts;
+        const uint32_t in_l2 = min(heads, max(1u, p.l2_rows / static_cast<uint32_t>(max(it.lk, 1))));
+        const uint32_t per_group = in_l2 * parts * n, h0 = at / per_group * in_l2, hs = min(in_l2, heads - h0);
+        at %= per_group;
+        it.part = static_cast<int>(at % parts);
+        at /= parts;
+        it.head = static_cast<int>(h0 + at % hs);
+        it.t0 = static_cast<int>(n - 1 - at / hs) * span;
         const int64_t beg = static_cast<int64_t>(it.part) * p.part_keys;
         it.beg = static_cast<int>(min(static_cast<int64_t>(it.lk), beg));
         it.end = p.nparts > 1 ? static_cast<int>(min(static_cast<int64_t>(it.lk), beg + p.part_keys)) : it.lk;
-        // Key tiles of either S: up to the last key that its last token sees.  A pair's S_i are the
-        // tokens t0 + 2 i tile_toks on, half of them in each CTA, over all key tiles; a single
-        // CTA's are the even and the odd key tiles of its one query tile.
+        // Key tiles of either S: up to the last key that its last token sees.  A single CTA's are the
+        // even and the odd key tiles of its one query tile.
         it.tiles = 0;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int first = it.t0 + (CTAS == 2 ? i * CTAS * p.tile_toks : 0);
-          const int last = min(first + CTAS * p.tile_toks, it.lq) - 1;
+          int last = -1;   // its last token
+#pragma unroll
+          for (int r = 0; r < CTAS; ++r) {
+            const int first = it.t0 + prompt::query_tile<CTAS>(i, r) * p.tile_toks;
+            if (first < it.lq) last = max(last, min(first + p.tile_toks, it.lq) - 1);
+          }
           int64_t vis = it.lk;
           if (p.causal) vis = min(vis, static_cast<int64_t>(last) + 1 + it.lk - it.lq);
           const int64_t end = min(static_cast<int64_t>(it.end), vis);
-          it.n[i] = first < it.lq && end > it.beg ? static_cast<int>((end - it.beg + kPromptKeys - 1) / kPromptKeys) : 0;
+          it.n[i] = last >= 0 && end > it.beg ? static_cast<int>((end - it.beg + kPromptKeys - 1) / kPromptKeys) : 0;
           it.tiles = max(it.tiles, it.n[i]);
         }
         if (CTAS == 1) {
@@ -250,7 +270,7 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(q_full + i, CTAS);
-      mbar_init(q_empty + i, PAIR ? 1 : MW);
+      mbar_init(q_empty + i, 1);
       mbar_init(s_full + i, 1);
       mbar_init(o_full + i, 1);
       mbar_init(drain + i, 1);
@@ -351,13 +371,13 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
       auto wait = [&](uint64_t* bar, uint32_t parity) { ok = ok && warp_wait(bar, parity); };
       for (int c = 0; ok && take(c, it); ++c) {
         auto load_q = [&](int i) {
-          if (c > 0) wait(q_empty + i, (c - 1) & 1);
+          if (q_loads[i] > 0) wait(q_empty + i, (q_loads[i] - 1) & 1);
           if (!ok) return;
           ++q_loads[i];
           if (leader) {
             const uint32_t bar = at_leader(q_full + i);
             mbar_arrive_expect_tx_at(bar, NQK * p.tile_toks * p.group * 128);
-            const int tok = it.q0 + it.t0 + (PAIR ? (i * CTAS + rank) * p.tile_toks : 0);
+            const int tok = it.q0 + it.t0 + query_tile<CTAS>(i, rank) * p.tile_toks;
             for (int k = 0; k < NQK; ++k)
               tma_load_4d_at<CTAS>(qs + (i * NQK + k) * S::Q_CHUNK, &qmap, bar, 64 * k, 0, it.head, tok);
           }
@@ -380,7 +400,6 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
           if (j == 0) {   // behind the first keys' copies the next item is asked for, and the queries' places are awaited
             if (rank == 0 && leader) mbar_arrive(ask);
             if (it.n[0] > 0) load_q(0);
-            if (PAIR && it.n[1] > 0) load_q(1);
           }
           if (loaded >= STAGES) wait(v_empty + st, ph ^ 1);
           if (!ok) break;
@@ -415,6 +434,7 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
             __syncwarp();
           }
           if (++st == STAGES) st = 0, ph ^= 1;
+          if (j == 0 && PAIR && it.n[1] > 0) load_q(1);
         }
         if (it.tiles == 0 && rank == 0 && leader) mbar_arrive(ask);
         __syncwarp();
@@ -446,100 +466,135 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
                                            : make_sdesc_sw64(smem_u32(vs), S::V_BLOCK, 512);
       const uint32_t kf = smem_u32(k_full), vf = smem_u32(v_full), pf = smem_u32(p_full), qf = smem_u32(q_full);
       bool ok = true;
-      int bst = 0, bph = 0;            // stage and parity of the item's first key tile
-      int q_loads[2] = {0, 0}, turns[2] = {0, 0};   // of either S: query tiles taken, P's taken
-      for (int c = 0; ok && take(c, it); ++c) {
-        // Step s is S_i's, i = s % 2, on its key tile j = s / 2: tile j of a pair, tile s of a single
-        // CTA.  A warp takes both S, or one of them.
-        auto stage = [&](int t, int& st, int& ph) {
-          const int x = bst + t;
-          st = x % STAGES;
-          ph = bph ^ ((x / STAGES) & 1);
-        };
-        auto last_user = [&](int i, int j) { return !PAIR || MW == 2 || i == 1 || j >= it.n[1]; };
-        auto scores = [&](int i, int j, int st) {   // S_i = Q_i K^T
-          if (leader) {
-            const uint64_t a = dq + (((PAIR ? i : 0) * NQK * S::Q_CHUNK) >> 4), b = dk + ((st * S::K_BYTES) >> 4);
+      struct Pos {   // stage and parity of a key tile
+        int st, ph;
+        __device__ __forceinline__ Pos next() const { return st + 1 == STAGES ? Pos{0, ph ^ 1} : Pos{st + 1, ph}; }
+      };
+      struct Work {   // what there is to issue for an item
+        int n0, n1, tiles, keys;   // keys < 0: no more items
+      };
+      auto take_work = [&](int c, Work& x) {
+        const bool got = take(c, it);
+        x = Work{it.n[0], it.n[1], it.tiles, got ? it.end - it.beg : -1};
+        return got;
+      };
+      Work cur_item = {}, after = {};  // the item, and the one behind, where it is taken already
+      bool have_after = false, begun = false;       // and its first S_0 issued
+      Pos first = {0, 0};              // of the item's first key tile
+      uint32_t q_turn = 0, p_turn = 0; // bit i: parity of S_i's next query tile, of its next P
+      // S is numbered by a variable, not by an instance of this code for either: the descriptors are then
+      // sums in uniform registers, where constants of 40 MMAs would be kept in, and moved from, others.
+      auto scores = [&](int i, const Work& x, int j, Pos k) {   // S_i = Q_i K^T, from the leader
+        const uint64_t a = dq + (((PAIR ? i : 0) * NQK * S::Q_CHUNK) >> 4), b = dk + ((k.st * S::K_BYTES) >> 4);
 #pragma unroll
-            for (int k = 0; k < NQK; ++k)
+        for (int c = 0; c < NQK; ++c)
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_f16_ss<CTAS>(tmem + S_COL + 128 * i, a + ((k * S::Q_CHUNK + 32 * kk) >> 4), b + ((k * S::K_CHUNK + 32 * kk) >> 4),
-                                 idesc_qk, k || kk ? 1u : 0u);
-            tc_commit_all<CTAS>(s_full + i);
-            if (last_user(i, j)) tc_commit_all<CTAS>(k_empty + st);
-          }
-          __syncwarp();
-        };
-        // This warp has issued its last product with the query tile(s) of S_i.
-        auto queries_done = [&](int i) {
-          if (leader && (PAIR || MW == 2 || i == 1)) tc_commit_all<CTAS>(q_empty + (PAIR ? i : 0));
-          __syncwarp();
-        };
-        for (int i = w; i < 2; i += MW) {
-          const int ni = i ? it.n[1] : it.n[0];
-          if (ni > 0) {
-            int st, ph;
-            stage(PAIR ? 0 : i, st, ph);
-            ok = ok && warp_wait2(kf + 8 * st, ph, qf + (PAIR ? 8 * i : 0), (i ? q_loads[1] : q_loads[0]) & 1, ab);
-            tc_fence_after();
-            if (!ok) break;
-            scores(i, 0, st);
-          }
-          if (ni <= 1) queries_done(i);
-          (i ? q_loads[1] : q_loads[0]) += (PAIR ? ni : it.tiles) > 0;
-        }
-        const int steps = 2 * max(it.n[0], it.n[1]);
-        for (int s = w; ok && s < steps; s += MW) {
-          const int i = s & 1, j = s >> 1, ni = i ? it.n[1] : it.n[0], t = PAIR ? j : s;
-          int vst, vph, kst, kph;
-          stage(t, vst, vph);
-          stage(t + (PAIR ? 1 : 2), kst, kph);
-          if (j >= ni) {   // nothing left for this S
-            if (PAIR && MW == 2) {   // the other's tiles go back as they come
-              if (!(ok = warp_wait2(kf + 8 * vst, vph, vf + 8 * vst, vph, ab))) break;
-              if (leader) {
-                tc_commit_all<CTAS>(k_empty + vst);
-                tc_commit_all<CTAS>(v_empty + vst);
-              }
-              __syncwarp();
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f16_ss<CTAS>(tmem + S_COL + 128 * i, a + ((c * S::Q_CHUNK + 32 * kk) >> 4), b + ((c * S::K_CHUNK + 32 * kk) >> 4),
+                             idesc_qk, c || kk ? 1u : 0u);
+        tc_commit_all<CTAS>(s_full + i);
+        if (!PAIR || MW == 2 || i == 1 || j >= x.n1) tc_commit_all<CTAS>(k_empty + k.st);
+        // the last product with this query tile (a single CTA's one tile: with both S)
+        if (j + 1 == (i ? x.n1 : x.n0) && (PAIR || i == ((x.tiles - 1) & 1))) tc_commit_all<CTAS>(q_empty + (PAIR ? i : 0));
+      };
+      // The first S_i of an item: behind its keys, and its queries (a single CTA's come with S_0).
+      auto begin = [&](int i, Pos k) {
+        if (!ok || (i ? cur_item.n1 : cur_item.n0) == 0) return;
+        const uint32_t kb = kf + 8 * k.st;
+        const bool q = PAIR || i == 0;
+        if (!(ok = warp_wait2(kb, k.ph, q ? qf + 8 * i : kb, q ? (q_turn >> i) & 1 : k.ph, ab))) return;
+        q_turn ^= 1u << i;
+        tc_fence_after();
+        if (leader) scores(i, cur_item, 0, k);
+        __syncwarp();
+      };
+      // O_i += P_i V on tile j of this S, then its next S; v, k: the tile's place and the next one's.
+      auto step = [&](int i, int j, Pos v, Pos k) {
+        const int ni = i ? cur_item.n1 : cur_item.n0;
+        if (!ok) return;
+        if (j >= ni) {   // nothing left for this S
+          if (PAIR && MW == 2) {   // the other's tiles go back as they come
+            if (!(ok = warp_wait2(kf + 8 * v.st, v.ph, vf + 8 * v.st, v.ph, ab))) return;
+            if (leader) {
+              tc_commit_all<CTAS>(k_empty + v.st);
+              tc_commit_all<CTAS>(v_empty + v.st);
             }
-            continue;
+            __syncwarp();
           }
-          const int keys = it.end - it.beg - t * kPromptKeys;
-          const int todo = (min(kPromptKeys, keys) + 15) / 16;   // MMAs of 16 keys
-          const bool more = j + 1 < ni;
-          const uint32_t pi = pf + 16 * i, turn = (i ? turns[1] : turns[0]) & 1;
-          const uint32_t s_tmem = tmem + S_COL + 128 * i, o_tmem = tmem + O_COL + 128 * i;
-          const uint64_t b = dv + ((vst * S::V_BYTES) >> 4);
-          // O_i += P_i V; the first half waits for the values, too, the second for the next keys.  P's
-          // of a new item come when the softmax is done with the last one's O.
-          if (!(ok = warp_wait2(pi, turn, vf + 8 * vst, vph, ab))) break;
-          if (PAIR && keys < kPromptKeys) mbar_acquire_cluster(v_full + vst, vph);   // values cut by plain stores
-          tc_fence_after();
-          if (leader) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (k < todo) mma_f16_ts<CTAS>(o_tmem, s_tmem + 8 * k, b + ((k * 32 * S::V_WIDTH) >> 4), idesc_pv, j || k ? 1u : 0u);
-          }
-          __syncwarp();
-          if (!(ok = warp_wait2(pi + 8, turn, more ? kf + 8 * kst : pi + 8, more ? kph : turn, ab))) break;
-          tc_fence_after();
-          if (leader) {
-#pragma unroll
-            for (int k = 4; k < 8; ++k)
-              if (k < todo) mma_f16_ts<CTAS>(o_tmem, s_tmem + 8 * k, b + ((k * 32 * S::V_WIDTH) >> 4), idesc_pv, 1u);
-            if (last_user(i, j)) tc_commit_all<CTAS>(v_empty + vst);
-            if (!more) tc_commit_all<CTAS>(o_full + i);
-          }
-          __syncwarp();
-          if (more) scores(i, j + 1, kst);
-          if (j + 2 == ni) queries_done(i);
-          ++(i ? turns[1] : turns[0]);
+          return;
         }
-        const int total = bst + it.tiles;
-        bph ^= (total / STAGES) & 1;
-        bst = total % STAGES;
+        const int keys = cur_item.keys - (PAIR ? j : 2 * j + i) * kPromptKeys;
+        const bool more = j + 1 < ni;
+        const uint32_t pi = pf + 16 * i, turn = (p_turn >> i) & 1;
+        p_turn ^= 1u << i;
+        const uint32_t s_tmem = tmem + S_COL + 128 * i, o_tmem = tmem + O_COL + 128 * i;
+        const uint64_t b = dv + ((v.st * S::V_BYTES) >> 4);
+        auto values = [&](int k, int to) {   // the MMAs of 16 keys each
+          if (keys >= kPromptKeys) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              mma_f16_ts<CTAS>(o_tmem, s_tmem + 8 * (k + x), b + (((k + x) * 32 * S::V_WIDTH) >> 4), idesc_pv, j || k + x ? 1u : 0u);
+          } else {
+            for (int x = k; x < min(to, (keys + 15) / 16); ++x)
+              mma_f16_ts<CTAS>(o_tmem, s_tmem + 8 * x, b + ((x * 32 * S::V_WIDTH) >> 4), idesc_pv, j || x ? 1u : 0u);
+          }
+        };
+        // The first half waits for the values, too, the second for the next keys.  P's of a new item
+        // come when the softmax is done with the last one's O.
+        if (!(ok = warp_wait2(pi, turn, vf + 8 * v.st, v.ph, ab))) return;
+        if (PAIR && keys < kPromptKeys) mbar_acquire_cluster(v_full + v.st, v.ph);   // values cut by plain stores
+        tc_fence_after();
+        if (leader) values(0, 4);
+        __syncwarp();
+        if (!(ok = warp_wait2(pi + 8, turn, more ? kf + 8 * k.st : pi + 8, more ? k.ph : turn, ab))) return;
+        tc_fence_after();
+        if (leader) {
+          values(4, 8);
+          if (!PAIR || MW == 2 || i == 1 || j >= cur_item.n1) tc_commit_all<CTAS>(v_empty + v.st);
+          if (more) scores(i, cur_item, j + 1, k);
+          else tc_commit_all<CTAS>(o_full + i);
+        }
+        __syncwarp();
+      };
+      for (int c = 0; ok; ++c) {
+        if (have_after) cur_item = after;
+        else if (!take_work(c, cur_item)) break;
+        have_after = false;
+        // A pair's S both go over every key tile, a single CTA's over every other one.
+        Pos cur = first, nxt = cur.next();
+        if ((MW == 1 || w == 0) && !begun) begin(0, cur);
+        if (MW == 1 || w == 1) begin(1, PAIR ? cur : nxt);
+        begun = false;
+        const int steps = 2 * max(cur_item.n0, cur_item.n1);
+        const int total = first.st + cur_item.tiles;
+        first = Pos{total % STAGES, first.ph ^ ((total / STAGES) & 1)};
+#pragma unroll 1
+        for (int s = w; s < steps; s += MW) {
+          const int i = s & 1, j = s >> 1;
+          if (PAIR && MW == 1 && i == 1 && j + 1 >= cur_item.n0 && j < cur_item.n1 && j + STAGES >= cur_item.tiles && !begun) {
+            // S_0 is through, S_1 is not: the next item's first S_0, where it is there to begin with (the keys
+            // that were at its place before have been waited for, so their phase is not mistaken for its own)
+            if (!have_after && __all_sync(0xffffffffu, mbar_test(smem_u32(item_full + ((c + 1) & 1)), ((c + 1) >> 1) & 1)))
+              have_after = true, take_work(c + 1, after);
+            if (have_after && after.keys >= 0 && after.n0 > 0 &&
+                __all_sync(0xffffffffu, mbar_test(kf + 8 * first.st, first.ph) && mbar_test(qf, q_turn & 1))) {
+              q_turn ^= 1u;
+              tc_fence_after();
+              if (leader) scores(0, after, 0, first);
+              __syncwarp();
+              begun = true;
+            }
+          }
+          if (PAIR) {
+            step(i, j, cur, nxt);
+            if (MW == 2 || i == 1) cur = nxt, nxt = nxt.next();
+          } else {   // cur: tile s, nxt: tile s + 1
+            step(i, j, cur, nxt.next());
+            cur = nxt, nxt = nxt.next();
+          }
+          if (!ok) break;
+        }
+        if (have_after && after.keys < 0) break;
       }
       if (*reinterpret_cast<volatile int*>(abortf) && leader) {
         tc_commit_all<CTAS>(drain + w);
@@ -554,7 +609,7 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t ts = tmem + S_COL + 128 * i + lanes, to = tmem + O_COL + lanes;   // O_i at to + 128 i
     const int row = 32 * quarter + lane;
-    const int row_tok = (PAIR ? (i * CTAS + rank) * p.tile_toks : 0) + row / p.group, g = row % p.group;
+    const int row_tok = query_tile<CTAS>(i, rank) * p.tile_toks + row / p.group, g = row % p.group;
     const bool row_used = row < p.tile_toks * p.group;
     const float sc = p.scale_log2;
     constexpr float SHIFT = FP16 ? 7.f : 0.f;
@@ -657,6 +712,10 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
       constexpr int MINE = PAIR ? D : D / 2;        // dims that this thread writes, from d0 on
       const int d0 = PAIR ? 0 : i * MINE;
       float w0 = 1.f, w1 = 1.f;                     // a single CTA: weights of O_0 and O_1
+      uint32_t o[MINE] = {};
+      if (PAIR && ni > 0)                           // on its way while the sums are looked at
+#pragma unroll
+        for (int b = 0; b < MINE / 32; ++b) DSA_TMEM_LD32(to + 128 * i + 32 * b, (o + 32 * b));
       if (!PAIR) {
         // Both threads of a row (they reach the same lanes of tensor memory) take the common
         // reference, and half of the dims of either O.
@@ -689,39 +748,35 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
         if (!last) p.part_lse[static_cast<int64_t>(it.part) * p.total_q * p.heads + at] = lse2;
         else if (p.lse) p.lse[at] = lse;
       }
-#pragma unroll 1
-      for (int b = 0; b < MINE / 32; ++b) {
-        uint32_t o[32] = {};
-        if (PAIR) {
-          if (ni > 0) {
-            DSA_TMEM_LD32(to + 128 * i + 32 * b, o);
-            tmem_wait_ld();
-          }
+      if (PAIR) {
+        if (ni > 0) tmem_wait_ld();
 #pragma unroll
-          for (int x = 0; x < 32; ++x) o[x] = empty_row ? 0u : __float_as_uint(__uint_as_float(o[x]) * w0);
-        } else {
-          uint32_t o1[32] = {};
-          if (it.n[0] > 0) DSA_TMEM_LD32(to + d0 + 32 * b, o);
-          if (it.n[1] > 0) DSA_TMEM_LD32(to + 128 + d0 + 32 * b, o1);
-          tmem_wait_ld();
+        for (int x = 0; x < MINE; ++x) o[x] = empty_row ? 0u : __float_as_uint(__uint_as_float(o[x]) * w0);
+      } else {
+        if (it.n[0] > 0)
 #pragma unroll
-          for (int x = 0; x < 32; ++x)
-            o[x] = empty_row ? 0u : __float_as_uint(fmaf(__uint_as_float(o1[x]), w1, __uint_as_float(o[x]) * w0));
-        }
-        if (!valid) continue;
-        if (!last) {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + (static_cast<int64_t>(it.part) * p.total_q * p.heads + at) * D +
-                                                  d0 + 32 * b);
+          for (int b = 0; b < MINE / 32; ++b) DSA_TMEM_LD32(to + d0 + 32 * b, (o + 32 * b));
+        uint32_t o1[MINE] = {};
+        if (it.n[1] > 0)
 #pragma unroll
-          for (int x = 0; x < 8; ++x)
-            dst[x] = make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]), __uint_as_float(o[4 * x + 2]),
-                                 __uint_as_float(o[4 * x + 3]));
-          continue;
-        }
+          for (int b = 0; b < MINE / 32; ++b) DSA_TMEM_LD32(to + 128 + d0 + 32 * b, (o1 + 32 * b));
+        tmem_wait_ld();
+#pragma unroll
+        for (int x = 0; x < MINE; ++x)
+          o[x] = empty_row ? 0u : __float_as_uint(fmaf(__uint_as_float(o1[x]), w1, __uint_as_float(o[x]) * w0));
+      }
+      if (valid && !last) {
+        float4* dst = reinterpret_cast<float4*>(p.part_o + (static_cast<int64_t>(it.part) * p.total_q * p.heads + at) * D + d0);
+#pragma unroll
+        for (int x = 0; x < MINE / 4; ++x)
+          dst[x] = make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]), __uint_as_float(o[4 * x + 2]),
+                               __uint_as_float(o[4 * x + 3]));
+      }
+      if (valid && last) {
         if (p.prev_out && wp > 0.f) {
-          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.prev_out) + at * D + d0 + 32 * b);
+          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.prev_out) + at * D + d0);
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
+          for (int x = 0; x < MINE / 8; ++x) {
             const uint4 v = src[x];
             const uint32_t v4[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -733,14 +788,14 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
           }
         }
 #pragma unroll
-        for (int x = 0; x < 16; ++x) o[x] = pack16(__uint_as_float(o[2 * x]), __uint_as_float(o[2 * x + 1]), FP16);
-        uint16_t* dst = static_cast<uint16_t*>(p.out) + at * D + d0 + 32 * b;
+        for (int x = 0; x < MINE / 2; ++x) o[x] = pack16(__uint_as_float(o[2 * x]), __uint_as_float(o[2 * x + 1]), FP16);
+        uint16_t* dst = static_cast<uint16_t*>(p.out) + at * D + d0;
         if (p.out_aligned32) {   // whole sectors
-          st_global_v8(dst, o);
-          st_global_v8(dst + 16, o + 8);
+#pragma unroll
+          for (int x = 0; x < MINE / 16; ++x) st_global_v8(dst + 16 * x, o + 8 * x);
         } else {
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
+          for (int x = 0; x < MINE / 8; ++x)
             reinterpret_cast<uint4*>(dst)[x] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
         }
       }

@@ -174,6 +174,17 @@ __device__ __forceinline__ bool clc_answer(const void* answer, uint32_t& cta_x) 
   return ok != 0;
 }
 
+// Whether the phase with the given parity is complete (without waiting).
+__device__ __forceinline__ bool mbar_test(uint32_t addr, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(addr), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Waits, as a converged warp, until `done()` holds in every lane; gives up as mbar_wait_inline does.
 template <typename Done>
 __device__ __forceinline__ bool warp_wait_until(Done done, Abort ab) {
