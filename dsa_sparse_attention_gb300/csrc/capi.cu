@@ -1301,7 +1301,7 @@ dsa_status dsa_prompt_attn(const dsa_prompt* prompt, const void* q, const void* 
   p.scale_log2 = sm_scale * 1.4426950408889634f;
   p.nparts = w.nparts;
   p.part_keys = w.part_keys;
-  p.l2_rows = (64u << 20) / (4u * static_cast<uint32_t>(dim));
+  p.l2_rows = (32u << 20) / (4u * static_cast<uint32_t>(dim));
   p.out = out;
   p.lse = lse;
   p.out_aligned32 = (reinterpret_cast<uintptr_t>(out) & 31) == 0;

@@ -18,9 +18,12 @@
 //  - Few rows (CTAS = 1): one CTA takes one tile of 128 rows; the two S are consecutive key
 //    tiles, each with an O and a sum of its own, merged at the end.
 //
-// The softmax keeps a reference per row that moves only when a logit exceeds it by 2^8 (the
-// sums and O are then scaled); a weight is at most 2^8 (bf16) or 2^15 (fp16, whose weights
-// start from 2^7 to keep more of what is small), sums are fp32 of the unrounded weights.
+// The softmax keeps a reference per row.  The first tile sets it to the row's maximum; behind it the
+// weights are taken without looking for another, and their sum, which is wanted anyway, tells
+// whether one may be out of range (above 2^20 in bf16; 2^15 in fp16, whose weights start from 2^7 to
+// keep more of what is small): only then the maximum is found, the reference moves, and the sums and
+// O are scaled.  (Finding the maximum of every tile took 400 of 1,300 cycles.)  Sums are fp32 of the
+// unrounded weights.
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -42,7 +45,6 @@ static_assert(SOFTMAX_WARPS * SOFTMAX_REGS + (WARPS - SOFTMAX_WARPS) * OTHER_REG
 static_assert(WARPS * 32 * LAUNCH_REGS <= 65536 && SOFTMAX_WARPS % 4 == 0, "whole warpgroups");
 constexpr int MISC = 3072;            // barriers and scalars, and 2 KB of references and sums
 constexpr int SMEM_MAX = 232448;
-constexpr float GROW = 8.f;           // log2 units a logit may exceed the reference by
 
 template <int D, int E, int CTAS>
 struct Shape {
@@ -236,8 +238,8 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
   uint64_t* k_full = bars;                              // [STAGES] keys landed
   uint64_t* v_full = k_full + STAGES;                   // [STAGES] values landed
   uint64_t* q_full = v_full + STAGES;                   // [2] query tile landed
-  uint64_t* p_full = q_full + 2;                        // [2][2] P written, the first 64 keys and the others
-  uint64_t* asked = p_full + 4;                         // both CTAs have read the last answer
+  uint64_t* p_full = q_full + 2;                        // [2] P written
+  uint64_t* asked = p_full + 2;                         // both CTAs have read the last answer
   // In each CTA: what the MMAs signal.
   uint64_t* k_empty = asked + 1;                        // [STAGES]
   uint64_t* v_empty = k_empty + STAGES;                 // [STAGES]
@@ -277,7 +279,7 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
       mbar_init(item_full + i, 1);
       mbar_init(item_empty + i, SOFTMAX_WARPS + 1 + (rank == 0 ? MW : 0));
     }
-    for (int i = 0; i < 4; ++i) mbar_init(p_full + i, 4 * CTAS);
+    for (int i = 0; i < 2; ++i) mbar_init(p_full + i, 4 * CTAS);
     mbar_init(asked, CTAS);
     mbar_init(tail, 1);
     mbar_init(answered, 1);
@@ -525,31 +527,23 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
         }
         const int keys = cur_item.keys - (PAIR ? j : 2 * j + i) * kPromptKeys;
         const bool more = j + 1 < ni;
-        const uint32_t pi = pf + 16 * i, turn = (p_turn >> i) & 1;
+        const uint32_t pi = pf + 8 * i, turn = (p_turn >> i) & 1;
         p_turn ^= 1u << i;
         const uint32_t s_tmem = tmem + S_COL + 128 * i, o_tmem = tmem + O_COL + 128 * i;
         const uint64_t b = dv + ((v.st * S::V_BYTES) >> 4);
-        auto values = [&](int k, int to) {   // the MMAs of 16 keys each
-          if (keys >= kPromptKeys) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              mma_f16_ts<CTAS>(o_tmem, s_tmem + 8 * (k + x), b + (((k + x) * 32 * S::V_WIDTH) >> 4), idesc_pv, j || k + x ? 1u : 0u);
-          } else {
-            for (int x = k; x < min(to, (keys + 15) / 16); ++x)
-              mma_f16_ts<CTAS>(o_tmem, s_tmem + 8 * x, b + ((x * 32 * S::V_WIDTH) >> 4), idesc_pv, j || x ? 1u : 0u);
-          }
-        };
-        // The first half waits for the values, too, the second for the next keys.  P's of a new item
-        // come when the softmax is done with the last one's O.
-        if (!(ok = warp_wait2(pi, turn, vf + 8 * v.st, v.ph, ab))) return;
+        // P's of a new item come when the softmax is done with the last one's O.
+        if (!(ok = warp_wait3(pi, turn, vf + 8 * v.st, v.ph, more ? kf + 8 * k.st : pi, more ? k.ph : turn, ab))) return;
         if (PAIR && keys < kPromptKeys) mbar_acquire_cluster(v_full + v.st, v.ph);   // values cut by plain stores
         tc_fence_after();
-        if (leader) values(0, 4);
-        __syncwarp();
-        if (!(ok = warp_wait2(pi + 8, turn, more ? kf + 8 * k.st : pi + 8, more ? k.ph : turn, ab))) return;
-        tc_fence_after();
         if (leader) {
-          values(4, 8);
+          if (keys >= kPromptKeys) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              mma_f16_ts<CTAS>(o_tmem, s_tmem + 8 * x, b + ((x * 32 * S::V_WIDTH) >> 4), idesc_pv, j || x ? 1u : 0u);
+          } else {
+            for (int x = 0; x < (keys + 15) / 16; ++x)   // 16 keys each
+              mma_f16_ts<CTAS>(o_tmem, s_tmem + 8 * x, b + ((x * 32 * S::V_WIDTH) >> 4), idesc_pv, j || x ? 1u : 0u);
+          }
           if (!PAIR || MW == 2 || i == 1 || j >= cur_item.n1) tc_commit_all<CTAS>(v_empty + v.st);
           if (more) scores(i, cur_item, j + 1, k);
           else tc_commit_all<CTAS>(o_full + i);
@@ -613,7 +607,8 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
     const bool row_used = row < p.tile_toks * p.group;
     const float sc = p.scale_log2;
     constexpr float SHIFT = FP16 ? 7.f : 0.f;
-    const uint32_t p_bar[2] = {at_leader(p_full + 2 * i), at_leader(p_full + 2 * i + 1)};
+    constexpr float LIMIT = FP16 ? 32768.f : 1048576.f;   // of a tile's sum of weights, and so of each of them
+    const uint32_t p_bar = at_leader(p_full + i);
     bool ok = true;
     int turns = 0, outs = 0, syncs = 0;   // phases of s_full, o_full and both
     // All softmax warps of a single CTA, for which a failed wait ends this one, too.
@@ -640,31 +635,50 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
         ok = ok && warp_wait(s_full + i, turns & 1);
         if (!ok) break;
         tc_fence_after();
-        uint32_t r[4][32];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) DSA_TMEM_LD32(ts + 32 * b, r[b]);
-        tmem_wait_ld();
+        uint32_t r[128];
         const int k0 = (PAIR ? j : 2 * j + i) * kPromptKeys;
-        if (all_see < k0 + kPromptKeys) {
-          const int limit = vis - k0;
+        auto load = [&]() {   // the row's scores
 #pragma unroll
-          for (int b = 0; b < 4; ++b)
+          for (int b = 0; b < 4; ++b) DSA_TMEM_LD32(ts + 32 * b, (r + 32 * b));
+          tmem_wait_ld();
+          if (all_see < k0 + kPromptKeys) {
+            const int limit = vis - k0;
 #pragma unroll
-            for (int x = 0; x < 32; ++x)
-              if (32 * b + x >= limit) r[b][x] = 0xFF800000u;   // -inf
+            for (int x = 0; x < 128; ++x)
+              if (x >= limit) r[x] = 0xFF800000u;   // -inf
+          }
+        };
+        float2 sum[2];
+        const float2 sc2 = make_float2(sc, sc);
+        auto weights = [&]() {   // in the scores' place, two a register, and their sums
+          const float ref = m == -INFINITY ? 0.f : SHIFT - m;   // nothing seen: weights 2^-inf
+          const float2 ref2 = make_float2(ref, ref);
+          sum[0] = sum[1] = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int x = 0; x < 128; x += 2) {
+            float2 v = ffma2(make_float2(__uint_as_float(r[x]), __uint_as_float(r[x + 1])), sc2, ref2);
+            v.x = ex2(v.x);
+            v.y = ex2(v.y);
+            sum[(x >> 1) & 1] = fadd2(sum[(x >> 1) & 1], v);
+            r[x >> 1] = pack16(v.x, v.y, FP16);
+          }
+        };
+        load();
+        bool moves = j == 0;
+        if (j > 0) {
+          weights();
+          moves = !((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y) <= LIMIT);
         }
-        float mx[4];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          mx[b] = fmaxf(__uint_as_float(r[b][0]), __uint_as_float(r[b][1]));
-#pragma unroll
-          for (int x = 2; x < 32; x += 2) mx[b] = fmaxf(mx[b], fmaxf(__uint_as_float(r[b][x]), __uint_as_float(r[b][x + 1])));
-        }
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
-        const bool moves = valid && top > m + GROW;
         if (__any_sync(0xffffffffu, moves)) {
-          // A row moves its own reference alone: its result does not depend on its neighbours.
-          const float now = moves ? top : m;
+          // The first tile, or one whose weights pass the limit: the scores again, and their maximum.  A
+          // row moves its own reference alone: its result does not depend on its neighbours.
+          if (j > 0) load();
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int x = 0; x < 128; x += 2)
+            mx[(x >> 1) & 3] = max3(mx[(x >> 1) & 3], __uint_as_float(r[x]), __uint_as_float(r[x + 1]));
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+          const float now = moves ? fmaxf(m, top) : m;
           const float f = now == -INFINITY ? 1.f : ex2(m - now);
           m = now;
           l2[0].x *= f, l2[0].y *= f, l2[1].x *= f, l2[1].y *= f;
@@ -679,29 +693,17 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
               for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
               DSA_TMEM_ST16(to + 128 * i + 16 * b, o);
             }
-            tmem_wait_st();
           }
+          weights();
         }
-        const float ref = m == -INFINITY ? 0.f : SHIFT - m;   // nothing seen yet: weights 2^-inf
-        const float2 sc2 = make_float2(sc, sc), ref2 = make_float2(ref, ref);
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-#pragma unroll
-          for (int x = 0; x < 32; x += 2) {
-            float2 y = ffma2(make_float2(__uint_as_float(r[b][x]), __uint_as_float(r[b][x + 1])), sc2, ref2);
-            y.x = ex2(y.x);
-            y.y = ex2(y.y);
-            l2[(x >> 1) & 1] = fadd2(l2[(x >> 1) & 1], y);
-            r[b][x >> 1] = pack16(y.x, y.y, FP16);
-          }
-          DSA_TMEM_ST16(ts + 16 * b, r[b]);
-          if (b & 1) {
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_at(p_bar[b >> 1]);
-          }
-        }
+        DSA_TMEM_ST32(ts, r);
+        DSA_TMEM_ST32(ts + 32, (r + 32));
+        l2[0] = fadd2(l2[0], sum[0]);
+        l2[1] = fadd2(l2[1], sum[1]);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_at(p_bar);
       }
       if (ok && ni > 0) ok = warp_wait(o_full + i, outs & 1);
       outs += ni > 0;

@@ -22,7 +22,7 @@ struct PromptParams {
   float scale_log2;        // sm_scale * log2(e)
   int32_t nparts;          // parts that the keys of a sequence are cut into
   int32_t part_keys;       // keys of a part (a multiple of 128)
-  uint32_t l2_rows;        // keys of one head whose keys and values together fill half of L2
+  uint32_t l2_rows;        // keys of one head whose keys and values together take 32 MB (of 129 of L2: 16 to 64 measured within 1 %, 1 and 128 slower by 1 to 9 %)
   void* out;               // [total_q, heads, D]
   float* lse;              // [total_q, heads] or null
   int32_t out_aligned32;   // out begins at a multiple of 32 bytes

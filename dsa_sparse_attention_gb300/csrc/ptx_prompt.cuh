@@ -10,6 +10,12 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // 32 bytes in one store (32-byte aligned).
 __device__ __forceinline__ void st_global_v8(void* dst, const uint32_t* v) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
@@ -212,6 +218,15 @@ __device__ __forceinline__ bool warp_wait2(uint32_t a, uint32_t pa, uint32_t b, 
       [&] {
         const bool x = mbar_try_wait(a, pa), y = mbar_try_wait(b, pb);
         return x && y;
+      },
+      ab);
+}
+
+__device__ __forceinline__ bool warp_wait3(uint32_t a, uint32_t pa, uint32_t b, uint32_t pb, uint32_t c, uint32_t pc, Abort ab) {
+  return warp_wait_until(
+      [&] {
+        const bool x = mbar_try_wait(a, pa), y = mbar_try_wait(b, pb), z = mbar_try_wait(c, pc);
+        return x && y && z;
       },
       ab);
 }
