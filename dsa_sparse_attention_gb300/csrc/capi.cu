@@ -399,6 +399,43 @@ struct PromptPlan {
   size_t part_o = 0, part_lse = 0, total = 0;
 };
 
+constexpr int64_t kRunKeys = 65536;   // keys summed in one accumulator
+constexpr int64_t kMinPart = 512;     // keys of a part, at least
+
+// Parts of the keys, at least `least`, for `blocks` blocks of queries (of each key head), by the time
+// they should take.  Items of one length go in rounds; of other lengths in equal shares, with part of
+// the longest item behind them.  About 6,000 cycles begin and end an item, a tile of 128 keys takes
+// about 2,500 of a CTA or a pair; the merge is a launch, and 3,000 bytes a cycle.  Measured (us): 16 x 1
+// token over 1K to 32K keys, 64 heads in 8 groups: 240 in 3 parts, 160 in 5, 131 to 139 in 15 or 16;
+// 500 tokens on 64K, 96 heads (96 items for 76 pairs): 1,540 whole, 1,284 in 6; 4 x 301 tokens on
+// 7,891, 32 heads (128 items): 153 whole, 180 in 3.
+int64_t parts_of(const dsa_prompt* p, int ctas, int64_t blocks, int64_t least) {
+  const double units = double(num_sms()) / ctas, heads = double(p->kv_heads);
+  // keys of a block: causally half of a sequence's own queries are behind it
+  const double seqs = double(p->num_seqs < p->total_q ? p->num_seqs : p->total_q);
+  const double hidden = (p->flags & DSA_PROMPT_CAUSAL) ? 0.5 * double(p->total_q) / seqs : 0.;
+  double mean = double(p->total_k) / double(p->num_seqs) - hidden;
+  if (mean > double(p->max_k)) mean = double(p->max_k);
+  if (mean < kPromptKeys) mean = kPromptKeys;
+  const bool alike = mean >= 0.9 * double(p->max_k);
+  const double tiles = double(blocks) * heads * mean / kPromptKeys;
+  const double rows = double(p->total_q) * p->heads;
+  static const int kTry[] = {1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 12, 14, 16, 20, 24, 32, 48, 64, 96, 128, 192, 256, 384, 512};
+  int64_t best = least;
+  double best_cost = 0.;
+  for (int n : kTry) {
+    const int64_t parts = n * least;
+    if (parts > 1 && p->max_k < parts * kMinPart) break;
+    const double longest = double(p->max_k) / double(parts) / kPromptKeys;
+    const double items = double(blocks) * heads + tiles / longest;
+    double cost = alike ? std::ceil(double(blocks) * heads * double(parts) / units) * (longest * 2500. + 6000.)
+                        : (tiles * 2500. + items * 6000.) / units + 0.7 * longest * 2500.;
+    if (parts > 1) cost += 6000. + rows * double(parts) * double(p->dim) * 8. / 3000.;
+    if (best_cost == 0. || cost < best_cost) best = parts, best_cost = cost;
+  }
+  return best;
+}
+
 PromptPlan plan_prompt(const dsa_prompt* p) {
   PromptPlan w;
   const int tile = kPromptRows / (p->heads / p->kv_heads);
@@ -410,13 +447,12 @@ PromptPlan plan_prompt(const dsa_prompt* p) {
   w.blocks = p->total_q / span + seqs;
   const int64_t by_len = seqs * cdiv(p->max_q, span);
   if (by_len < w.blocks) w.blocks = by_len;
-  // Too few items for the GPU: the keys of every sequence in parts of `part_keys`, at least 512,
-  // so that about two CTAs an SM share the work.
-  const int64_t ctas = w.blocks * p->kv_heads * w.ctas, sms = num_sms();
-  if (ctas > 0 && ctas < sms && p->max_k > 512 && !fixed) {
-    const int64_t want = cdiv(2 * sms, ctas);
-    int64_t keys = cdiv(cdiv(p->max_k, want), kPromptKeys) * kPromptKeys;
-    if (keys < 512) keys = 512;
+  // The tensor core truncates where it adds to its accumulator (7.5e-7 of the sum a tile of 128 keys
+  // where the terms have one sign), so a run of sums is at most kRunKeys long; runs are merged in fp32.
+  int64_t parts = cdiv(p->max_k, kRunKeys);
+  if (!fixed && w.blocks > 0 && p->max_k > kMinPart) parts = parts_of(p, w.ctas, w.blocks, parts);
+  if (parts > 1) {
+    const int64_t keys = fixed ? kRunKeys : cdiv(cdiv(p->max_k, parts), kPromptKeys) * kPromptKeys;
     w.part_keys = static_cast<int>(keys);
     w.nparts = static_cast<int>(cdiv(p->max_k, keys));
   }
