@@ -81,7 +81,8 @@ class dsa_prompt(ctypes.Structure):
                [("cu_q", ctypes.c_void_p), ("cu_k", ctypes.c_void_p)] + \
                [(n, ctypes.c_int64) for n in ("q_token_stride", "q_head_stride", "k_token_stride", "k_head_stride",
                                               "v_token_stride", "v_head_stride", "shared_stride")]
-    held = None   # (cu_q, cu_k): the tensors, where make_prompt has them
+    held = None   # (cu_q, cu_k): the tensors
+    like = None   # type, and shape and strides of q, k, v, k_shared (make_prompt)
 
 
 class dsa_host_io(ctypes.Structure):
@@ -575,6 +576,7 @@ def make_prompt(cu_q, cu_k, q, k, v, k_shared=None, max_q=None, max_k=None, flag
                         total_k, total_q if max_q is None else int(max_q), total_k if max_k is None else int(max_k), pq, pk,
                         qt, qh, kt, kh, vt, vh, st)
     prompt.held = (cu_q, cu_k)
+    prompt.like = (q.dtype,) + tuple(None if t is None else (t.shape, t.stride()) for t in (q, k, v, k_shared))
     return prompt
 
 
@@ -590,12 +592,11 @@ def alloc_prompt_workspace(prompt, device="cuda"):
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
-def _laid(name, t, dtype, shape, strides):
-    """The address of a device tensor of the shape and strides that make_prompt was given."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor of {dtype} and shape {shape}")
-    got = t.stride()
-    if t.numel() and (got[-1] != 1 or any(n > 1 and a != b for n, a, b in zip(shape, got, strides))):
+def _laid(name, t, dtype, like):
+    """The address of a device tensor of the shape and strides (`like`) that make_prompt was given."""
+    if t.dtype is not dtype or not t.is_cuda or t.shape != like[0]:
+        raise ValueError(f"{name} must be a device tensor of {dtype} and shape {tuple(like[0])}")
+    if t.stride() != like[1] and t.numel() and any(n > 1 and a != b for n, a, b in zip(like[0], t.stride(), like[1])):
         raise ValueError(f"{name} must be laid out like the tensor that make_prompt was given")
     return t.data_ptr()
 
@@ -605,19 +606,16 @@ def dsa_prompt_attn(prompt, q, k, v, sm_scale, out, lse=None, k_shared=None, pre
     """Attention of packed sequences with the heads' own keys and values; tensors as make_prompt was
     given them, out [total_q, heads, dim], fp32 lse [total_q, heads].  prev_out and prev_lse: an
     earlier result over other keys of the same queries, joined with this one's."""
-    p = prompt
-    dt = torch.float16 if p.dtype else torch.bfloat16
-    t, n, d, e = p.total_q, p.total_k, p.dim, p.shared_dim
-    if (k_shared is not None) != (e > 0):
+    dt, lq, lk, lv, ls = prompt.like
+    if (k_shared is None) != (ls is None):
         raise ValueError("k_shared must be given exactly where make_prompt was given it")
-    rows = t * p.heads
+    rows = prompt.total_q * prompt.heads
     s = library().dsa_prompt_attn(
-        _byref(p), _laid("q", q, dt, (t, p.heads, d + e), (p.q_token_stride, p.q_head_stride)),
-        _laid("k", k, dt, (n, p.kv_heads, d), (p.k_token_stride, p.k_head_stride)),
-        _laid("k_shared", k_shared, dt, (n, e), (p.shared_stride,)) if e else None,
-        _laid("v", v, dt, (n, p.kv_heads, d), (p.v_token_stride, p.v_head_stride)), float(sm_scale),
-        _array("prev_out", prev_out, dt, rows * d), _array("prev_lse", prev_lse, torch.float32, rows),
-        _array("out", out, dt, rows * d), _array("lse", lse, torch.float32, rows), _space(ws), ws.numel(), _handle(stream))
+        _byref(prompt), _laid("q", q, dt, lq), _laid("k", k, dt, lk),
+        None if ls is None else _laid("k_shared", k_shared, dt, ls), _laid("v", v, dt, lv), float(sm_scale),
+        _array("prev_out", prev_out, dt, rows * prompt.dim), _array("prev_lse", prev_lse, torch.float32, rows),
+        _array("out", out, dt, rows * prompt.dim), _array("lse", lse, torch.float32, rows), _space(ws), ws.numel(),
+        _handle(stream))
     if s:
         _check(s, "dsa_prompt_attn")
 

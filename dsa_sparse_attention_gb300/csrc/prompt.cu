@@ -150,10 +150,10 @@ struct ItemFinder {
         const uint32_t in_l2 = min(heads, max(1u, p.l2_rows / static_cast<uint32_t>(max(it.lk, 1))));
         const uint32_t per_group = in_l2 * parts * n, h0 = at / per_group * in_l2, hs = min(in_l2, heads - h0);
         at %= per_group;
-        it.part = static_cast<int>(at % parts);
-        at /= parts;
         it.head = static_cast<int>(h0 + at % hs);
-        it.t0 = static_cast<int>(n - 1 - at / hs) * span;
+        at /= hs;
+        it.part = static_cast<int>(at % parts);
+        it.t0 = static_cast<int>(n - 1 - at / parts) * span;
         const int64_t beg = static_cast<int64_t>(it.part) * p.part_keys;
         it.beg = static_cast<int>(min(static_cast<int64_t>(it.lk), beg));
         it.end = p.nparts > 1 ? static_cast<int>(min(static_cast<int64_t>(it.lk), beg + p.part_keys)) : it.lk;
@@ -885,7 +885,7 @@ cudaError_t launch_one(const PromptMaps& m, const PromptParams& p, int64_t items
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   e = launch_ex(prompt_attn_kernel<D, E, FP16, CTAS>, dim3(static_cast<unsigned>(items * CTAS)), dim3(prompt::THREADS), smem, st,
-                false, CTAS == 2 ? 2u : 0u, m.q, m.k, m.ks, m.v, p);
+                true, CTAS == 2 ? 2u : 0u, m.q, m.k, m.ks, m.v, p);
   if (e != cudaSuccess || p.nparts == 1) return e;
   const int64_t rows = p.total_q * p.heads;
   return launch_ex(prompt_merge_kernel<D, FP16>, dim3(static_cast<unsigned>(cdiv(rows, 8))), dim3(256), 0, st, true, 0u, p);

@@ -117,6 +117,7 @@ __device__ __forceinline__ void from_e2m1x16(uint2 c, float* v) {
 
 __global__ void __launch_bounds__(kTokThreads) write_tokens_kernel(WriteTokensParams p) {
   __shared__ Place place[kWriteToks];
+  grid_dep_launch();
   grid_dep_wait();
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kWriteToks;
   const int nt = static_cast<int>(min(static_cast<int64_t>(kWriteToks), p.b.T - t0));
@@ -216,6 +217,7 @@ __device__ __forceinline__ int find_span(const int32_t* cu, int B, int64_t n) {
 
 __global__ void __launch_bounds__(kTokThreads) read_tokens_kernel(ReadTokensParams p) {
   __shared__ Place place[kReadRows];
+  grid_dep_launch();
   grid_dep_wait();
   const int64_t n0 = static_cast<int64_t>(blockIdx.x) * kReadRows;
   const int nr = static_cast<int>(min(static_cast<int64_t>(kReadRows), p.rows - n0));
@@ -284,12 +286,12 @@ __global__ void __launch_bounds__(kTokThreads) read_tokens_kernel(ReadTokensPara
 }
 
 cudaError_t launch_write_tokens(const WriteTokensParams& p, cudaStream_t st) {
-  return launch_ex(write_tokens_kernel, dim3(static_cast<unsigned>(cdiv(p.b.T, kWriteToks))), dim3(kTokThreads), 0, st, false,
+  return launch_ex(write_tokens_kernel, dim3(static_cast<unsigned>(cdiv(p.b.T, kWriteToks))), dim3(kTokThreads), 0, st, true,
                    0u, p);
 }
 
 cudaError_t launch_read_tokens(const ReadTokensParams& p, cudaStream_t st) {
-  return launch_ex(read_tokens_kernel, dim3(static_cast<unsigned>(cdiv(p.rows, kReadRows))), dim3(kTokThreads), 0, st, false, 0u,
+  return launch_ex(read_tokens_kernel, dim3(static_cast<unsigned>(cdiv(p.rows, kReadRows))), dim3(kTokThreads), 0, st, true, 0u,
                    p);
 }
 
