@@ -1270,7 +1270,7 @@ dsa_status dsa_write_tokens(const dsa_kv_layout* layout, const dsa_batch* batch,
   p.latent = static_cast<const __nv_bfloat16*>(latent);
   p.pool_w = static_cast<uint8_t*>(const_cast<void*>(layout->pool));
   p.status = static_cast<uint32_t*>(workspace);
-  return cuda_status(launch_write_tokens(p, stream));
+  return cuda_status(launch_write_tokens(p, num_sms(), stream));
 }
 
 dsa_status dsa_read_tokens(const dsa_kv_layout* layout, const dsa_batch* batch, const dsa_spans* spans, void* k_out,
@@ -1294,8 +1294,10 @@ dsa_status dsa_read_tokens(const dsa_kv_layout* layout, const dsa_batch* batch, 
   p.rows = spans->rows;
   p.k_out = static_cast<__nv_bfloat16*>(k_out);
   p.lat_out = static_cast<__nv_bfloat16*>(latent_out);
+  p.k_aligned32 = (reinterpret_cast<uintptr_t>(k_out) & 31) == 0;
+  p.lat_aligned32 = (reinterpret_cast<uintptr_t>(latent_out) & 31) == 0;
   p.status = static_cast<uint32_t*>(workspace);
-  return cuda_status(launch_read_tokens(p, stream));
+  return cuda_status(launch_read_tokens(p, num_sms(), stream));
 }
 
 size_t dsa_prompt_workspace_size(const dsa_prompt* prompt) {

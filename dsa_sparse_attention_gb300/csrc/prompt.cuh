@@ -49,6 +49,7 @@ struct WriteTokensParams {
   const __nv_bfloat16* latent;   // [T, 576] or null
   uint8_t* pool_w;
   uint32_t* status;
+  int cta_toks = 0;              // set by the launcher
 };
 
 struct ReadTokensParams {
@@ -57,12 +58,14 @@ struct ReadTokensParams {
   const int32_t* cu;       // [B + 1]
   const int32_t* start;    // [B] or null
   int64_t rows;
+  int cta_rows = 0;        // set by the launcher
   __nv_bfloat16* k_out;    // [rows, 128] or null
   __nv_bfloat16* lat_out;  // [rows, 576] or null
+  bool k_aligned32, lat_aligned32;   // they begin at multiples of 32 bytes
   uint32_t* status;
 };
 
-cudaError_t launch_write_tokens(const WriteTokensParams& p, cudaStream_t st);
-cudaError_t launch_read_tokens(const ReadTokensParams& p, cudaStream_t st);
+cudaError_t launch_write_tokens(const WriteTokensParams& p, int num_sms, cudaStream_t st);
+cudaError_t launch_read_tokens(const ReadTokensParams& p, int num_sms, cudaStream_t st);
 
 }  // namespace dsa
