@@ -402,18 +402,36 @@ struct PromptPlan {
 constexpr int64_t kRunKeys = 65536;   // keys summed in one accumulator
 constexpr int64_t kMinPart = 512;     // keys of a part, at least
 
-// Parts of the keys, at least `least`, for `blocks` blocks of queries (of each key head), by the time
-// they should take.  Items of one length go in rounds; of other lengths in equal shares, with part of
-// the longest item behind them.  About 6,000 cycles begin and end an item, a tile of 128 keys takes
-// about 2,500 of a CTA or a pair; the merge is a launch, and 3,000 bytes a cycle.  Measured (us): 16 x 1
-// token over 1K to 32K keys, 64 heads in 8 groups: 240 in 3 parts, 160 in 5, 131 to 139 in 15 or 16;
-// 500 tokens on 64K, 96 heads (96 items for 76 pairs): 1,540 whole, 1,284 in 6; 4 x 301 tokens on
-// 7,891, 32 heads (128 items): 153 whole, 180 in 3.
-int64_t parts_of(const dsa_prompt* p, int ctas, int64_t blocks, int64_t least) {
+// How a batch is best divided: blocks of queries for single CTAs (one tile of 128 rows) or for pairs
+// (four tiles), and the keys in `parts` parts, a multiple of `least`, by the time that should take.
+// Items of one length go in rounds; of other lengths in equal shares, with part of the longest item
+// behind them.  About 6,000 cycles begin and end an item; the merge is a launch, and 3,000 bytes a
+// cycle.  Measured (us), pairs against single CTAs: 8,192 tokens of 96 heads 1,210, 1,611; 32 ragged
+// prompts 708, 1,030; 4 x 301 tokens on 7,891 keys, 32 heads of 64 dims, 150, 120; 33 tokens 14, 8.
+// Whole against in parts: 16 x 1 token over 1K to 32K keys 240 (3 parts), 160 (5), 134 (16); 500 tokens
+// on 64K, 96 heads (96 items for 76 pairs) 1,500, 1,290 (2), 1,245 (3), 1,290 (6).
+struct Division {
+  int ctas;
+  int64_t blocks, parts;
+  double cycles;
+};
+
+Division divide_prompt(const dsa_prompt* p, int ctas, int64_t least) {
+  const int tile = kPromptRows / (p->heads / p->kv_heads), span = ctas * ctas * tile;
+  const int64_t used = p->num_seqs < p->total_q ? p->num_seqs : p->total_q;   // sequences with queries, at most
+  int64_t blocks = p->total_q / span + used;                                  // of each key head, at most
+  const int64_t by_len = used * cdiv(p->max_q, span);
+  if (by_len < blocks) blocks = by_len;
+  Division best{ctas, blocks, least, 0.};
+  if (blocks == 0) return best;
   const double units = double(num_sms()) / ctas, heads = double(p->kv_heads);
+  // cycles a tile of 128 keys takes: a pair's products, or the chain from scores to scores; a single
+  // CTA's, or its share of the memory's rate where no other block reads the same keys
+  double tile_cycles = ctas == 2 ? (p->dim == 64 ? 1900. : p->shared_dim ? 2700. : 2460.)
+                                 : (p->dim == 64 ? 1200. : p->shared_dim ? 2300. : 1900.);
+  if (ctas == 1 && blocks <= used && p->dim == 128) tile_cycles = 2850.;
   // keys of a block: causally half of a sequence's own queries are behind it
-  const double seqs = double(p->num_seqs < p->total_q ? p->num_seqs : p->total_q);
-  const double hidden = (p->flags & DSA_PROMPT_CAUSAL) ? 0.5 * double(p->total_q) / seqs : 0.;
+  const double hidden = (p->flags & DSA_PROMPT_CAUSAL) ? 0.5 * double(p->total_q) / double(used) : 0.;
   double mean = double(p->total_k) / double(p->num_seqs) - hidden;
   if (mean > double(p->max_k)) mean = double(p->max_k);
   if (mean < kPromptKeys) mean = kPromptKeys;
@@ -421,36 +439,34 @@ int64_t parts_of(const dsa_prompt* p, int ctas, int64_t blocks, int64_t least) {
   const double tiles = double(blocks) * heads * mean / kPromptKeys;
   const double rows = double(p->total_q) * p->heads;
   static const int kTry[] = {1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 12, 14, 16, 20, 24, 32, 48, 64, 96, 128, 192, 256, 384, 512};
-  int64_t best = least;
-  double best_cost = 0.;
   for (int n : kTry) {
     const int64_t parts = n * least;
-    if (parts > 1 && p->max_k < parts * kMinPart) break;
+    if (n > 1 && p->max_k < parts * kMinPart) break;
     const double longest = double(p->max_k) / double(parts) / kPromptKeys;
     const double items = double(blocks) * heads + tiles / longest;
-    double cost = alike ? std::ceil(double(blocks) * heads * double(parts) / units) * (longest * 2500. + 6000.)
-                        : (tiles * 2500. + items * 6000.) / units + 0.7 * longest * 2500.;
-    if (parts > 1) cost += 6000. + rows * double(parts) * double(p->dim) * 8. / 3000.;
-    if (best_cost == 0. || cost < best_cost) best = parts, best_cost = cost;
+    double cycles = alike ? std::ceil(double(blocks) * heads * double(parts) / units) * (longest * tile_cycles + 6000.)
+                          : (tiles * tile_cycles + items * 6000.) / units + 0.7 * longest * tile_cycles;
+    if (parts > 1) cycles += 6000. + rows * double(parts) * double(p->dim) * 8. / 3000.;
+    if (best.cycles == 0. || cycles < best.cycles) best.parts = parts, best.cycles = cycles;
   }
   return best;
 }
 
 PromptPlan plan_prompt(const dsa_prompt* p) {
   PromptPlan w;
-  const int tile = kPromptRows / (p->heads / p->kv_heads);
   const bool fixed = p->flags & DSA_PROMPT_INVARIANT;
-  // one tile holds every sequence's rows: a single CTA, its two softmaxes on alternate key tiles
-  if (!fixed && p->max_q <= tile) w.ctas = 1;
-  const int span = w.ctas * w.ctas * tile;
-  const int64_t seqs = p->num_seqs < p->total_q ? p->num_seqs : p->total_q;
-  w.blocks = p->total_q / span + seqs;
-  const int64_t by_len = seqs * cdiv(p->max_q, span);
-  if (by_len < w.blocks) w.blocks = by_len;
   // The tensor core truncates where it adds to its accumulator (7.5e-7 of the sum a tile of 128 keys
   // where the terms have one sign), so a run of sums is at most kRunKeys long; runs are merged in fp32.
-  int64_t parts = cdiv(p->max_k, kRunKeys);
-  if (!fixed && w.blocks > 0 && p->max_k > kMinPart) parts = parts_of(p, w.ctas, w.blocks, parts);
+  const int64_t least = p->max_k > kRunKeys ? cdiv(p->max_k, kRunKeys) : 1;
+  Division d = divide_prompt(p, 2, least);
+  int64_t parts = least;
+  if (!fixed) {
+    const Division one = divide_prompt(p, 1, least);
+    if (one.cycles < d.cycles) d = one;
+    parts = d.parts;
+  }
+  w.ctas = d.ctas;
+  w.blocks = d.blocks;
   if (parts > 1) {
     const int64_t keys = fixed ? kRunKeys : cdiv(cdiv(p->max_k, parts), kPromptKeys) * kPromptKeys;
     w.part_keys = static_cast<int>(keys);

@@ -239,13 +239,14 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
   uint64_t* v_full = k_full + STAGES;                   // [STAGES] values landed
   uint64_t* q_full = v_full + STAGES;                   // [2] query tile landed
   uint64_t* p_full = q_full + 2;                        // [2] P written
-  uint64_t* asked = p_full + 2;                         // both CTAs have read the last answer
+  uint64_t* s_free = p_full + 2;                        // [2] S read (where P has a place of its own)
+  uint64_t* asked = s_free + 2;                         // both CTAs have read the last answer
   // In each CTA: what the MMAs signal.
   uint64_t* k_empty = asked + 1;                        // [STAGES]
   uint64_t* v_empty = k_empty + STAGES;                 // [STAGES]
   uint64_t* q_empty = v_empty + STAGES;                 // [2] the item's last product with a query tile is done
-  uint64_t* s_full = q_empty + 2;                       // [2] S done, and with it every MMA of this S before
-  uint64_t* o_full = s_full + 2;                        // [2] the item's O done
+  uint64_t* s_full = q_empty + 2;                       // [2] S done (and every P V before, where P lies over S)
+  uint64_t* o_full = s_full + 2;                        // [2] the item's O done (OWN_P: every P V done)
   uint64_t* drain = o_full + 2;                         // [2]
   // And within each CTA.
   uint64_t* tail = drain + 2;                           // a last tile's values landed, to be cut by the loading warp
@@ -259,7 +260,7 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
   uint4* answer = reinterpret_cast<uint4*>(bars + 56);
   Item* items = reinterpret_cast<Item*>(bars + 58);     // [2]
   float* ml = reinterpret_cast<float*>(bars + 128);     // [4][128] references and sums of a single CTA's two S
-  static_assert(4 * STAGES + 26 <= 56 && 1024 + 4 * 128 * 4 <= MISC, "shared scalars");
+  static_assert(4 * STAGES + 28 <= 56 && 1024 + 4 * 128 * 4 <= MISC, "shared scalars");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = PAIR ? static_cast<int>(cluster_rank()) : 0;
 
@@ -279,7 +280,10 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
       mbar_init(item_full + i, 1);
       mbar_init(item_empty + i, SOFTMAX_WARPS + 1 + (rank == 0 ? MW : 0));
     }
-    for (int i = 0; i < 2; ++i) mbar_init(p_full + i, 4 * CTAS);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(p_full + i, 4 * CTAS);
+      mbar_init(s_free + i, 4 * CTAS);
+    }
     mbar_init(asked, CTAS);
     mbar_init(tail, 1);
     mbar_init(answered, 1);
@@ -296,7 +300,11 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
   grid_dep_wait();
   const uint32_t tmem = *tslot;
   const Abort ab{abortf, p.status};
-  constexpr uint32_t S_COL = 0, O_COL = 256;   // S_i (and P_i) at 128 i, O_i at 256 + 128 i
+  // S_i at 128 i, O_i at 256 + 128 i; P_i over S_i or, where O_i leaves room, behind O_i: then the
+  // next S_i is made as soon as this one is read, while its softmax runs.
+  constexpr uint32_t S_COL = 0, O_COL = 256;
+  constexpr bool OWN_P = D == 64;
+  constexpr uint32_t P_COL = OWN_P ? O_COL + 64 : S_COL;
   // A barrier of the CTA of rank 0, as both CTAs reach it.
   auto at_leader = [&](uint64_t* bar) { return PAIR ? cluster_map(smem_u32(bar), 0) : smem_u32(bar); };
   auto warp_wait = [&](uint64_t* bar, uint32_t parity) { return warp_wait1(smem_u32(bar), parity, ab); };
@@ -529,24 +537,32 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
         const bool more = j + 1 < ni;
         const uint32_t pi = pf + 8 * i, turn = (p_turn >> i) & 1;
         p_turn ^= 1u << i;
-        const uint32_t s_tmem = tmem + S_COL + 128 * i, o_tmem = tmem + O_COL + 128 * i;
+        const uint32_t p_tmem = tmem + P_COL + 128 * i, o_tmem = tmem + O_COL + 128 * i;
         const uint64_t b = dv + ((v.st * S::V_BYTES) >> 4);
+        if (OWN_P) {
+          const uint32_t si = smem_u32(s_free + i);
+          if (!(ok = warp_wait2(si, turn, more ? kf + 8 * k.st : si, more ? k.ph : turn, ab))) return;
+          tc_fence_after();
+          if (leader && more) scores(i, cur_item, j + 1, k);
+          __syncwarp();
+        }
         // P's of a new item come when the softmax is done with the last one's O.
-        if (!(ok = warp_wait3(pi, turn, vf + 8 * v.st, v.ph, more ? kf + 8 * k.st : pi, more ? k.ph : turn, ab))) return;
+        const bool keys_too = !OWN_P && more;
+        if (!(ok = warp_wait3(pi, turn, vf + 8 * v.st, v.ph, keys_too ? kf + 8 * k.st : pi, keys_too ? k.ph : turn, ab))) return;
         if (PAIR && keys < kPromptKeys) mbar_acquire_cluster(v_full + v.st, v.ph);   // values cut by plain stores
         tc_fence_after();
         if (leader) {
           if (keys >= kPromptKeys) {
 #pragma unroll
             for (int x = 0; x < 8; ++x)
-              mma_f16_ts<CTAS>(o_tmem, s_tmem + 8 * x, b + ((x * 32 * S::V_WIDTH) >> 4), idesc_pv, j || x ? 1u : 0u);
+              mma_f16_ts<CTAS>(o_tmem, p_tmem + 8 * x, b + ((x * 32 * S::V_WIDTH) >> 4), idesc_pv, j || x ? 1u : 0u);
           } else {
             for (int x = 0; x < (keys + 15) / 16; ++x)   // 16 keys each
-              mma_f16_ts<CTAS>(o_tmem, s_tmem + 8 * x, b + ((x * 32 * S::V_WIDTH) >> 4), idesc_pv, j || x ? 1u : 0u);
+              mma_f16_ts<CTAS>(o_tmem, p_tmem + 8 * x, b + ((x * 32 * S::V_WIDTH) >> 4), idesc_pv, j || x ? 1u : 0u);
           }
           if (!PAIR || MW == 2 || i == 1 || j >= cur_item.n1) tc_commit_all<CTAS>(v_empty + v.st);
-          if (more) scores(i, cur_item, j + 1, k);
-          else tc_commit_all<CTAS>(o_full + i);
+          if (OWN_P || !more) tc_commit_all<CTAS>(o_full + i);
+          if (!OWN_P && more) scores(i, cur_item, j + 1, k);
         }
         __syncwarp();
       };
@@ -601,14 +617,16 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
     regs_up<SOFTMAX_REGS>();
     const int i = warp >> 2, quarter = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t ts = tmem + S_COL + 128 * i + lanes, to = tmem + O_COL + lanes;   // O_i at to + 128 i
+    const uint32_t ts = tmem + S_COL + 128 * i + lanes, tp = tmem + P_COL + 128 * i + lanes;
+    const uint32_t to = tmem + O_COL + lanes;   // O_i at to + 128 i
     const int row = 32 * quarter + lane;
     const int row_tok = query_tile<CTAS>(i, rank) * p.tile_toks + row / p.group, g = row % p.group;
     const bool row_used = row < p.tile_toks * p.group;
     const float sc = p.scale_log2;
     constexpr float SHIFT = FP16 ? 7.f : 0.f;
     constexpr float LIMIT = FP16 ? 32768.f : 1048576.f;   // of a tile's sum of weights, and so of each of them
-    const uint32_t p_bar = at_leader(p_full + i);
+    constexpr float GROW = 8.f;   // log2 units that a logit may exceed the reference by, where it is looked at
+    const uint32_t p_bar = at_leader(p_full + i), s_bar = at_leader(s_free + i);
     bool ok = true;
     int turns = 0, outs = 0, syncs = 0;   // phases of s_full, o_full and both
     // All softmax warps of a single CTA, for which a failed wait ends this one, too.
@@ -663,27 +681,21 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
             r[x >> 1] = pack16(v.x, v.y, FP16);
           }
         };
-        load();
-        bool moves = j == 0;
-        if (j > 0) {
-          weights();
-          moves = !((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y) <= LIMIT);
-        }
-        if (__any_sync(0xffffffffu, moves)) {
-          // The first tile, or one whose weights pass the limit: the scores again, and their maximum.  A
-          // row moves its own reference alone: its result does not depend on its neighbours.
-          if (j > 0) load();
+        auto largest = [&]() {   // the row's largest logit of the tile, in log2 units
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int x = 0; x < 128; x += 2)
             mx[(x >> 1) & 3] = max3(mx[(x >> 1) & 3], __uint_as_float(r[x]), __uint_as_float(r[x + 1]));
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+          return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+        };
+        // A row moves its own reference alone: its result does not depend on its neighbours.
+        auto move = [&](bool moves, float top) {
           const float now = moves ? fmaxf(m, top) : m;
           const float f = now == -INFINITY ? 1.f : ex2(m - now);
           m = now;
           l2[0].x *= f, l2[0].y *= f, l2[1].x *= f, l2[1].y *= f;
           if (j > 0) {
-            // every MMA before S is done, so O is still
+            // every P V before is done, so O is still
 #pragma unroll 1
             for (int b = 0; b < D / 16; ++b) {
               uint32_t o[16];
@@ -694,10 +706,36 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
               DSA_TMEM_ST16(to + 128 * i + 16 * b, o);
             }
           }
+        };
+        load();
+        if (OWN_P) {
+          const float top = largest();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_at(s_bar);
+          if (j > 0) {   // the last P is read, and O is still
+            if (!(ok = warp_wait(o_full + i, outs & 1))) break;
+            ++outs;
+            tc_fence_after();
+          }
+          const bool moves = j == 0 || top > m + GROW;
+          if (__any_sync(0xffffffffu, moves)) move(moves, top);
           weights();
+        } else {
+          bool moves = j == 0;
+          if (j > 0) {
+            weights();
+            moves = !((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y) <= LIMIT);
+          }
+          if (__any_sync(0xffffffffu, moves)) {
+            // The first tile, or one whose weights pass the limit: the scores again, and their maximum.
+            if (j > 0) load();
+            move(moves, largest());
+            weights();
+          }
         }
-        DSA_TMEM_ST32(ts, r);
-        DSA_TMEM_ST32(ts + 32, (r + 32));
+        DSA_TMEM_ST32(tp, r);
+        DSA_TMEM_ST32(tp + 32, (r + 32));
         l2[0] = fadd2(l2[0], sum[0]);
         l2[1] = fadd2(l2[1], sum[1]);
         tmem_wait_st();
