@@ -113,7 +113,7 @@ __device__ __forceinline__ bool prompt_seq(const PromptParams& p, int r, int& q0
 template <int CTAS>
 struct ItemFinder {
   int r0 = 0;            // first sequence of the lanes'
-  uint32_t before = 0;   // blocks of the sequences before it
+  uint64_t before = 0;   // blocks of the sequences before it
   bool loaded = false;
   bool good;             // of this lane's sequence:
   int q0, lq, k0, lk;
@@ -122,7 +122,7 @@ struct ItemFinder {
   __device__ __forceinline__ bool find(const PromptParams& p, uint32_t me, prompt::Item& it) {
     const int lane = threadIdx.x & 31;
     const int span = CTAS * CTAS * p.tile_toks;
-    const uint32_t each = static_cast<uint32_t>(p.kv_heads) * p.nparts;   // items of a block
+    const uint64_t each = static_cast<uint64_t>(p.kv_heads) * p.nparts;   // items of a block
     if (me < before * each) r0 = 0, before = 0, loaded = false;
     for (;;) {
       if (!loaded) {
@@ -140,7 +140,7 @@ struct ItemFinder {
       if (here) {
         const int src = __ffs(here) - 1;
         const uint32_t n = __shfl_sync(0xffffffffu, blocks, src);
-        uint32_t at = me - (before + __shfl_sync(0xffffffffu, upto, src) - n) * each;
+        uint32_t at = static_cast<uint32_t>(me - (before + __shfl_sync(0xffffffffu, upto, src) - n) * each);
         it.q0 = __shfl_sync(0xffffffffu, q0, src);
         it.lq = __shfl_sync(0xffffffffu, lq, src);
         it.k0 = __shfl_sync(0xffffffffu, k0, src);

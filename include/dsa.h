@@ -612,9 +612,10 @@ size_t dsa_prompt_workspace_size(const dsa_prompt *prompt);
  * The rows of a sequence must be finite, and so must its logits be; what stands in rows of no
  * sequence (NaN included) never reaches a result, and their rows of out and lse are left as
  * they are.  Weights are rounded to the inputs' type, sums are fp32.
- * Where the batch has too few rows to fill the GPU, the keys are split over more CTAs and
- * merged; how depends on the batch and the GPU.  With DSA_PROMPT_INVARIANT nothing is split,
- * and a row's result depends on its query and its sequence's keys alone.
+ * Where the batch has few rows for the GPU, the keys are split over more CTAs and merged; how
+ * depends on the batch and the GPU.  With DSA_PROMPT_INVARIANT they are split every 65,536 keys
+ * and nowhere else (longer runs of sums would lose precision), and a row's result depends on its
+ * query and its sequence's keys alone, at the cost of idle SMs where rows are few.
  * A workspace serves one call at a time, as above.
  */
 dsa_status dsa_prompt_attn(const dsa_prompt *prompt, const void *q, const void *k, const void *k_shared, const void *v,

@@ -8,7 +8,7 @@ scale * sum |q k| (two bits for the order and the truncation of a tensor-core su
 (1 + their size) for the fp32 scaling and the exponential; a weight moves by that error e, the
 output by 2 e A, the lse by e.  The tensor core truncates where it adds 16 keys' products to the
 accumulator: 2^-23 of the sum's terms for each of the 8 steps of a tile of 128 keys, 2^-20 A a
-tile.  An fp16 weight is exact to 2^-25 of 2^7 or more that the heaviest weighs: 2^-32 * sum |v|.
+tile, of which 512 at most are summed in a run.  An fp16 weight is exact to 2^-25 of 2^7 or more that the heaviest weighs: 2^-32 * sum |v|.
 A joined result weighs both sides in fp32: 2^-20 of each.
 """
 import numpy as np
@@ -94,7 +94,7 @@ class PromptCase:
                                           f(self.ks, c, c + lk) if self.shared else None)
             e = 2.0 ** -18 * big + 2.0 ** -21 * (1 + big)
             vsum = np.repeat(np.abs(v).sum(axis=0), self.heads // self.kv, axis=0)[None]
-            part = (u + 2 * e[..., None] + ((lk + 127) // 128) * 2.0 ** -20) * (1 + 2 * u) * A + 2.0 ** -32 * vsum
+            part = (u + 2 * e[..., None] + min((lk + 127) // 128, 512) * 2.0 ** -20) * (1 + 2 * u) * A + 2.0 ** -32 * vsum
             tl = e + 2.0 ** -20 * (1 + np.abs(np.where(np.isfinite(rl), rl, 0.0)))
             if prev[0] is not None:
                 po, pl = f(prev[0], a, a + lq), f(prev[1], a, a + lq)

@@ -63,8 +63,63 @@ def test_few_rows_split_over_the_keys(shape, causal, prev, dt):
 
 
 @pytest.mark.parametrize("causal", [True, False])
-def test_joined_with_an_earlier_result(causal):
-    _run(PromptCase(RAGGED, 4, 2, 128, 64, BF, causal, seed=3, prev=True))
+@pytest.mark.parametrize("lens", [RAGGED, [(1, 5000), (2, 700)], [(3, 0), (100, 90)]])
+@pytest.mark.parametrize("dim,shared", [(128, 64), (64, 0)])
+def test_joined_with_an_earlier_result(lens, dim, shared, causal):
+    _run(PromptCase(lens, 4, 2, dim, shared, BF, causal, seed=3, prev=True))
+    # and in its place
+    case = PromptCase(lens, 4, 2, dim, shared, FP, causal, seed=4, prev=True).to_device()
+    rows = slice(int(case.cu_q[0]), int(case.cu_q[-1]))
+    case.out[rows], case.lse[rows] = case.d_prev[0][rows], case.d_prev[1][rows]
+    case.d_prev = (case.out, case.lse)
+    case.run()
+    case.check()
+
+
+def test_outputs_that_begin_off_32_bytes():
+    for lens in ([(300, 300)], [(1, 900)], [(40, 300)]):
+        case = PromptCase(lens, 4, 2, 128, 0, BF, True, seed=3).to_device()
+        t = case.out.shape[0]
+        room = torch.full((t * 4 * 128 + 16,), 7.0, dtype=BF, device="cuda")
+        case.out = room[8:8 + t * 4 * 128].view(t, 4, 128)
+        assert case.out.data_ptr() % 32 == 16
+        case.run()
+        case.check()
+        assert torch.all(room[:8] == 7.0) and torch.all(room[-8:] == 7.0)
+
+
+@pytest.mark.parametrize("shape", [(8, 8, 128, 64), (64, 8, 128, 0), (4, 2, 64, 0), (3, 3, 64, 64)])
+def test_items_of_a_tile_or_none(shape):
+    """Many single tokens whose keys, or whose last part's keys, are one tile or none: CTAs go from item to
+    item with one S or neither in use."""
+    import dsa_sparse_attention_gb300 as dsa
+    h, g, d, e = shape
+    lens = [(1, n) for n in (1, 513, 128, 129, 0, 640, 600, 1, 1025, 90, 1100, 0, 0, 16, 1537, 2)] * 6
+    case = PromptCase(lens, h, g, d, e, BF, True, seed=21).to_device()
+    case.run()
+    assert dsa.dsa_check(case.ws) == 0
+    case.check()
+    first, fl = case.out.clone(), case.lse.clone()
+    for _ in range(200):
+        case.run()
+    assert dsa.dsa_check(case.ws) == 0 and torch.equal(case.out, first) and torch.equal(case.lse, fl)
+
+
+def test_runs_longer_than_one_accumulator_sums():
+    """150,000 keys whose values have one sign, in fp16: runs of 65,536 keys merged in fp32, and with the
+    invariant flag the same bits alone and beside a longer sequence."""
+    import dsa_sparse_attention_gb300 as dsa
+    kw = dict(heads=2, kv=1, dim=64, dt=FP, causal=True, flags=dsa.DSA_PROMPT_INVARIANT)
+    long = PromptCase([(3, 150_000), (5, 700), (2, 66_000)], seed=31, **kw)
+    long.v = long.v.abs() + 0.5
+    long.to_device().run()
+    assert dsa.dsa_check(long.ws) == 0
+    long.check()
+    a, b = int(long.cu_q[1]), int(long.cu_k[1])
+    one = PromptCase([(5, 700)], seed=0, **kw)
+    one.q, one.k, one.v, one.ks = long.q[a:a + 5], long.k[b:b + 700], long.v[b:b + 700], long.ks[b:b + 700]
+    one.to_device().run()
+    assert torch.equal(one.out, long.out[a:a + 5]) and torch.equal(one.lse, long.lse[a:a + 5])
 
 
 def test_joining_chunks_is_one_call_over_both():
@@ -100,14 +155,33 @@ def test_earlier_results_that_weigh_nothing_are_not_read():
     _run(case)
 
 
+@pytest.mark.parametrize("dim", [128, 64])
+@pytest.mark.parametrize("lens", [[(600, 1500), (130, 130)], [(1, 2000)], [(100, 1500)]])
 @pytest.mark.parametrize("dt", [BF, FP])
-def test_growing_logits_move_the_reference(dt):
-    # Keys grow along the sequence and point where the queries do: every tile's logits pass the last's by far.
-    case = PromptCase([(130, 1500), (1, 2000)], 2, 2, 128, 0, dt, True, seed=4)
-    q = torch.sign(torch.randn(1, 2, 128, generator=torch.Generator().manual_seed(1)))
+@pytest.mark.parametrize("top", [12.0, 300.0])
+def test_growing_logits_move_the_reference(dt, lens, dim, top):
+    # Keys grow along the sequence and point where the queries do: every tile's logits pass the last's by far
+    # (by 3,400 at most, which is more than a bf16 weight holds).
+    case = PromptCase(lens, 2, 2, dim, 0, dt, True, seed=4)
+    q = torch.sign(torch.randn(1, 2, dim, generator=torch.Generator().manual_seed(1)))
     n = case.k.shape[0]
     case.q = (q + 0.01 * case.q.float()).to(dt)
-    case.k = (q * torch.linspace(0.0, 12.0, n)[:, None, None] + 0.05 * case.k.float()).to(dt)
+    case.k = (q * torch.linspace(0.0, top, n)[:, None, None] + 0.05 * case.k.float()).to(dt)
+    _run(case)
+
+
+@pytest.mark.parametrize("dim", [128, 64])
+@pytest.mark.parametrize("lens", [[(600, 1500)], [(1, 2000)]])
+@pytest.mark.parametrize("dt", [BF, FP])
+def test_single_logits_far_above_the_others(dt, lens, dim):
+    # One key in each of some tiles, in every half of them, passes all before it; between them the weights are small.
+    case = PromptCase(lens, 2, 1, dim, 0, dt, False, seed=4)
+    q = torch.sign(torch.randn(1, 1, dim, generator=torch.Generator().manual_seed(1)))
+    case.q = (q + 0.1 * case.q.float()).to(dt)
+    k = 0.1 * case.k.float()
+    for n, at in enumerate((3, 70, 200, 383, 384, 700, 1279, 1499)):
+        k[at] = q * (0.5 * (n + 1))
+    case.k = k.to(dt)
     _run(case)
 
 
@@ -133,6 +207,31 @@ def test_all_empty():
     k = torch.zeros(9, 4, 128, dtype=BF, device="cuda")
     pr = dsa.make_prompt(i32(0, 0), i32(0, 9), q, k, k)
     dsa.dsa_prompt_attn(pr, q, k, k, 1.0, q, ws=dsa.alloc_prompt_workspace(pr))
+
+
+@pytest.mark.parametrize("lens", [[(300, 300)], [(1, 3000)]])
+def test_without_lse(lens):
+    import dsa_sparse_attention_gb300 as dsa
+    case = PromptCase(lens, 4, 2, 64, 0, BF, True, seed=1).to_device()
+    case.run()
+    out = torch.empty_like(case.out)
+    dsa.dsa_prompt_attn(case.prompt, case.dq, case.dk, case.dv, case.scale, out, ws=case.ws)
+    assert torch.equal(out, case.out)
+
+
+def test_arrays_that_go_up_and_down():
+    """Overlapping sequences between descending ones: recorded, and nothing is written out of range."""
+    import dsa_sparse_attention_gb300 as dsa
+    case = PromptCase([(90, 90)] + [(0, 0)] * 40, 4, 4, 64, 0, BF, True, seed=3, max_q=90, max_k=90).to_device()
+    room = torch.full((3 * case.out.numel(),), 7.0, dtype=BF, device="cuda")
+    case.out = room[case.out.numel():2 * case.out.numel()].view(case.out.shape)
+    up_down = torch.tensor([0, 90] * 20 + [0], dtype=torch.int32)
+    case.d_cu_q[:41].copy_(up_down)
+    case.d_cu_k[:41].copy_(up_down)
+    case.run()
+    assert dsa.dsa_check(case.ws) == -6
+    n = case.out.numel()
+    assert torch.all(room[:n] == 7.0) and torch.all(room[2 * n:] == 7.0)
 
 
 def test_lengths_that_break_the_rules_are_recorded_and_left():

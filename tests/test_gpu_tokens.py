@@ -148,6 +148,54 @@ def test_read_values(lens, start, take, bs, fmt):
         _same(lat, want_l)
 
 
+@pytest.mark.parametrize("fmt", FORMATS[:2])
+def test_outputs_that_begin_off_32_bytes(fmt):
+    import dsa_sparse_attention_gb300 as dsa
+    wl, dw = _work([100], 1, fmt, 64, 7)
+    cu, spans = _spans(dsa, [5], [90], 0)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    k = torch.full((90 * 128 + 16,), 7.0, dtype=torch.bfloat16, device="cuda")
+    lat = torch.full((90 * 576 + 16,), 7.0, dtype=torch.bfloat16, device="cuda")
+    dsa.dsa_read_tokens(dw.layout, dw.batch, spans, k[8:-8].view(90, 128), lat[8:-8].view(90, 576), ws=ws)
+    assert dsa.dsa_check(ws) == 0
+    kk, ll = P.token_values(oracle_layout(wl), wl.block_table[0], 5 + np.arange(90))
+    _same(k[8:-8].view(90, 128), decode_bf16(_bits(kk.astype(np.float32))))
+    _same(lat[8:-8].view(90, 576), ll)
+    assert all(torch.all(x[e] == 7.0) for x in (k, lat) for e in (slice(0, 8), slice(-8, None)))
+
+
+@pytest.mark.parametrize("rows", [4900, 9000, 20_000, 40_000])
+def test_sizes_of_a_cta(rows):
+    """As many rows as take 4 to 32 of them a CTA to read, and 8 to 64 to write."""
+    import dsa_sparse_attention_gb300 as dsa
+    wl, dw = _work([rows], [rows], (0, 1), 64, 7)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    lat = torch.randn((rows, 576), generator=g, device="cuda").to(torch.bfloat16)
+    k = torch.randn((rows, 128), generator=g, device="cuda").to(torch.bfloat16)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    dsa.dsa_write_tokens(dw.layout, dw.batch, k, lat, ws=ws)
+    ko, lo = torch.zeros_like(k), torch.zeros_like(lat)
+    cu, spans = _spans(dsa, None, [rows], 0)
+    dsa.dsa_read_tokens(dw.layout, dw.batch, spans, ko, lo, ws=ws)
+    assert dsa.dsa_check(ws) == 0
+    at = sorted({0, 1, rows - 1, rows // 2} | {int(x) for x in np.random.default_rng(rows).integers(0, rows, 300)})
+    bits = lambda x, t: x[t].view(torch.int16).cpu().numpy().view(np.uint16)
+    pool = dw.pool.cpu().numpy()
+    wl.pool[:] = pool
+    lay = oracle_layout(wl)
+    for t in at:
+        row, slot = wl.block_table[0, t // 64], t % 64
+        base = int(row) * wl.row_stride
+        codes, scale = F.index_key_fp8(bits(k, t))
+        p = base + wl.idx_page_offset
+        assert np.array_equal(pool[p + slot * 128:p + slot * 128 + 128], codes)
+        p = base + wl.lat_page_offset + slot * 352
+        assert np.array_equal(pool[p:p + 352], F.latent_record(bits(lat, t), 1))
+    kk, ll = P.token_values(lay, wl.block_table[0], np.asarray(at))
+    _same(ko[at], decode_bf16(_bits(kk.astype(np.float32))))
+    _same(lo[at], ll)
+
+
 def test_many_requests():
     import dsa_sparse_attention_gb300 as dsa
     rng = np.random.default_rng(2)
