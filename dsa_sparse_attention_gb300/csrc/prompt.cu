@@ -11,21 +11,28 @@
 // columns, O += P.V with P as the TMEM operand.  Two S are in flight: while one's softmax runs,
 // the tensor core works on the other's products.  TMEM is full: two S of 128 columns, two O.
 //
-//  - Many rows (CTAS = 2): a pair of CTAs takes 512 rows, two tiles of 256, and each holds half
-//    of every key and value tile.  One CTA alone reads 8 KB of shared memory in the 64 cycles of
+//  - Many rows (CTAS = 2): a pair of CTAs takes 512 rows, an inner and an outer tile of 256, and
+//    each holds half of every key and value tile.  One CTA alone reads 8 KB of shared memory in the 64 cycles of
 //    an M = N = 128, K = 16 product of two shared operands, all that shared memory gives, with
 //    the next tiles' copies on top; of a pair each reads 6 KB, and loads half.
 //  - Few rows (CTAS = 1): one CTA takes one tile of 128 rows; the two S are consecutive key
 //    tiles, each with an O and a sum of its own, merged at the end.
 //
-// The softmax keeps a reference per row.  The first tile sets it to the row's maximum; behind it the
-// weights are taken without looking for another, and their sum, which is wanted anyway, tells
-// whether one may be out of range (above 2^20 in bf16; 2^15 in fp16, whose weights start from 2^7 to
-// keep more of what is small): only then the maximum is found, the reference moves, and the sums and
-// O are scaled.  (Finding the maximum of every tile took 400 of 1,300 cycles.)  Sums are fp32 of the
-// unrounded weights.
+// The softmax keeps a reference per row, which moves when it must.  Sums are fp32 of the unrounded
+// weights.
+//  - D = 128: the first tile sets the reference to the row's maximum; behind it the weights are taken
+//    without looking for another, and the sum of each half tile's, which is wanted anyway, tells whether
+//    one may be out of range (above 2^20 in bf16; 2^15 in fp16, whose weights start from 2^7 to keep more
+//    of what is small): only then the maximum is found, the reference moves, and the sums and O are
+//    scaled.  Finding the maximum of every tile took 400 of 1,300 cycles.  The products with a tile's
+//    first 64 keys begin while the other weights are taken: 32 ragged prompts 720 -> 701 us, a step of 16
+//    134 -> 128.
+//  - D = 64: products are short, and the chain from scores to scores is what a step takes.  The maximum is
+//    found first, P has columns of its own behind O, and S is given back as soon as it is read: the next
+//    scores are made while the weights are taken.
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <type_traits>
 
 #include "../../include/dsa.h"
@@ -43,7 +50,7 @@ constexpr int THREADS = WARPS * 32;
 constexpr int LAUNCH_REGS = 168, SOFTMAX_REGS = 200, OTHER_REGS = 104;
 static_assert(SOFTMAX_WARPS * SOFTMAX_REGS + (WARPS - SOFTMAX_WARPS) * OTHER_REGS <= WARPS * LAUNCH_REGS, "register shares");
 static_assert(WARPS * 32 * LAUNCH_REGS <= 65536 && SOFTMAX_WARPS % 4 == 0, "whole warpgroups");
-constexpr int MISC = 3072;            // barriers and scalars, and 2 KB of references and sums
+constexpr int MISC = 3 << 10;          // barriers and scalars, and 2 KB of references and sums
 constexpr int SMEM_MAX = 232448;
 
 template <int D, int E, int CTAS>
@@ -238,8 +245,8 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
   uint64_t* k_full = bars;                              // [STAGES] keys landed
   uint64_t* v_full = k_full + STAGES;                   // [STAGES] values landed
   uint64_t* q_full = v_full + STAGES;                   // [2] query tile landed
-  uint64_t* p_full = q_full + 2;                        // [2] P written
-  uint64_t* s_free = p_full + 2;                        // [2] S read (where P has a place of its own)
+  uint64_t* p_full = q_full + 2;                        // [2][2] P written: the first 64 keys, the others (OWN_P: all)
+  uint64_t* s_free = p_full + 4;                        // [2] S read (where P has a place of its own)
   uint64_t* asked = s_free + 2;                         // both CTAs have read the last answer
   // In each CTA: what the MMAs signal.
   uint64_t* k_empty = asked + 1;                        // [STAGES]
@@ -247,7 +254,8 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
   uint64_t* q_empty = v_empty + STAGES;                 // [2] the item's last product with a query tile is done
   uint64_t* s_full = q_empty + 2;                       // [2] S done (and every P V before, where P lies over S)
   uint64_t* o_full = s_full + 2;                        // [2] the item's O done (OWN_P: every P V done)
-  uint64_t* drain = o_full + 2;                         // [2]
+  uint64_t* half_done = o_full + 2;                     // [2] O += P V over a tile's first 64 keys done (not OWN_P)
+  uint64_t* drain = half_done + 2;                      // [2]
   // And within each CTA.
   uint64_t* tail = drain + 2;                           // a last tile's values landed, to be cut by the loading warp
   uint64_t* item_full = tail + 1;                       // [2]
@@ -260,7 +268,7 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
   uint4* answer = reinterpret_cast<uint4*>(bars + 56);
   Item* items = reinterpret_cast<Item*>(bars + 58);     // [2]
   float* ml = reinterpret_cast<float*>(bars + 128);     // [4][128] references and sums of a single CTA's two S
-  static_assert(4 * STAGES + 28 <= 56 && 1024 + 4 * 128 * 4 <= MISC, "shared scalars");
+  static_assert(4 * STAGES + 32 <= 56 && 1024 + 4 * 128 * 4 <= MISC, "shared scalars");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = PAIR ? static_cast<int>(cluster_rank()) : 0;
 
@@ -281,8 +289,10 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
       mbar_init(item_empty + i, SOFTMAX_WARPS + 1 + (rank == 0 ? MW : 0));
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(p_full + i, 4 * CTAS);
+      mbar_init(p_full + 2 * i, 4 * CTAS);
+      mbar_init(p_full + 2 * i + 1, 4 * CTAS);
       mbar_init(s_free + i, 4 * CTAS);
+      mbar_init(half_done + i, 1);
     }
     mbar_init(asked, CTAS);
     mbar_init(tail, 1);
@@ -535,10 +545,18 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
         }
         const int keys = cur_item.keys - (PAIR ? j : 2 * j + i) * kPromptKeys;
         const bool more = j + 1 < ni;
-        const uint32_t pi = pf + 8 * i, turn = (p_turn >> i) & 1;
+        const uint32_t pi = pf + 16 * i, turn = (p_turn >> i) & 1;
         p_turn ^= 1u << i;
         const uint32_t p_tmem = tmem + P_COL + 128 * i, o_tmem = tmem + O_COL + 128 * i;
         const uint64_t b = dv + ((v.st * S::V_BYTES) >> 4);
+        const int parts16 = (keys + 15) / 16;   // MMAs, of 16 keys each
+        auto values = [&](int from) {           // four of them
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (from + x < parts16)
+              mma_f16_ts<CTAS>(o_tmem, p_tmem + 8 * (from + x), b + (((from + x) * 32 * S::V_WIDTH) >> 4), idesc_pv,
+                               j || from || x ? 1u : 0u);
+        };
         if (OWN_P) {
           const uint32_t si = smem_u32(s_free + i);
           if (!(ok = warp_wait2(si, turn, more ? kf + 8 * k.st : si, more ? k.ph : turn, ab))) return;
@@ -547,19 +565,21 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
           __syncwarp();
         }
         // P's of a new item come when the softmax is done with the last one's O.
-        const bool keys_too = !OWN_P && more;
-        if (!(ok = warp_wait3(pi, turn, vf + 8 * v.st, v.ph, keys_too ? kf + 8 * k.st : pi, keys_too ? k.ph : turn, ab))) return;
+        if (!(ok = warp_wait2(pi, turn, vf + 8 * v.st, v.ph, ab))) return;
         if (PAIR && keys < kPromptKeys) mbar_acquire_cluster(v_full + v.st, v.ph);   // values cut by plain stores
         tc_fence_after();
-        if (leader) {
-          if (keys >= kPromptKeys) {
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-              mma_f16_ts<CTAS>(o_tmem, p_tmem + 8 * x, b + ((x * 32 * S::V_WIDTH) >> 4), idesc_pv, j || x ? 1u : 0u);
-          } else {
-            for (int x = 0; x < (keys + 15) / 16; ++x)   // 16 keys each
-              mma_f16_ts<CTAS>(o_tmem, p_tmem + 8 * x, b + ((x * 32 * S::V_WIDTH) >> 4), idesc_pv, j || x ? 1u : 0u);
+        if (!OWN_P) {
+          if (leader) {
+            values(0);
+            tc_commit_all<CTAS>(half_done + i);
           }
+          __syncwarp();
+          if (!(ok = warp_wait2(pi + 8, turn, more ? kf + 8 * k.st : pi + 8, more ? k.ph : turn, ab))) return;
+          tc_fence_after();
+        }
+        if (leader) {
+          if (OWN_P) values(0);
+          values(4);
           if (!PAIR || MW == 2 || i == 1 || j >= cur_item.n1) tc_commit_all<CTAS>(v_empty + v.st);
           if (OWN_P || !more) tc_commit_all<CTAS>(o_full + i);
           if (!OWN_P && more) scores(i, cur_item, j + 1, k);
@@ -624,9 +644,9 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
     const bool row_used = row < p.tile_toks * p.group;
     const float sc = p.scale_log2;
     constexpr float SHIFT = FP16 ? 7.f : 0.f;
-    constexpr float LIMIT = FP16 ? 32768.f : 1048576.f;   // of a tile's sum of weights, and so of each of them
+    constexpr float LIMIT = FP16 ? 32768.f : 1048576.f;   // of the sum of half a tile's weights, and so of each of them
     constexpr float GROW = 8.f;   // log2 units that a logit may exceed the reference by, where it is looked at
-    const uint32_t p_bar = at_leader(p_full + i), s_bar = at_leader(s_free + i);
+    const uint32_t p_bar = at_leader(p_full + 2 * i), s_bar = at_leader(s_free + i);
     bool ok = true;
     int turns = 0, outs = 0, syncs = 0;   // phases of s_full, o_full and both
     // All softmax warps of a single CTA, for which a failed wait ends this one, too.
@@ -655,46 +675,53 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
         tc_fence_after();
         uint32_t r[128];
         const int k0 = (PAIR ? j : 2 * j + i) * kPromptKeys;
-        auto load = [&]() {   // the row's scores
+        auto load = [&](int from) {   // the row's scores from `from` (0 or 64) on
 #pragma unroll
-          for (int b = 0; b < 4; ++b) DSA_TMEM_LD32(ts + 32 * b, (r + 32 * b));
+          for (int b = 0; b < 4; ++b)
+            if (32 * b >= from) DSA_TMEM_LD32(ts + 32 * b, (r + 32 * b));
           tmem_wait_ld();
           if (all_see < k0 + kPromptKeys) {
             const int limit = vis - k0;
 #pragma unroll
             for (int x = 0; x < 128; ++x)
-              if (x >= limit) r[x] = 0xFF800000u;   // -inf
+              if (x >= from && x >= limit) r[x] = 0xFF800000u;   // -inf
           }
         };
         float2 sum[2];
         const float2 sc2 = make_float2(sc, sc);
-        auto weights = [&]() {   // in the scores' place, two a register, and their sums
-          const float ref = m == -INFINITY ? 0.f : SHIFT - m;   // nothing seen: weights 2^-inf
+        auto weights = [&](int from, int to) {   // of scores `from` .. `to` - 1, two a register, and their sums
+          const float ref = m == -INFINITY ? FLT_MAX : SHIFT - m;   // nothing seen yet: 0 or infinity, which moves the reference
           const float2 ref2 = make_float2(ref, ref);
           sum[0] = sum[1] = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int x = 0; x < 128; x += 2) {
-            float2 v = ffma2(make_float2(__uint_as_float(r[x]), __uint_as_float(r[x + 1])), sc2, ref2);
-            v.x = ex2(v.x);
-            v.y = ex2(v.y);
-            sum[(x >> 1) & 1] = fadd2(sum[(x >> 1) & 1], v);
-            r[x >> 1] = pack16(v.x, v.y, FP16);
-          }
+          for (int x = 0; x < 128; x += 2)
+            if (x >= from && x < to) {
+              float2 v = ffma2(make_float2(__uint_as_float(r[x]), __uint_as_float(r[x + 1])), sc2, ref2);
+              v.x = ex2(v.x);
+              v.y = ex2(v.y);
+              sum[(x >> 1) & 1] = fadd2(sum[(x >> 1) & 1], v);
+              r[x >> 1] = pack16(v.x, v.y, FP16);
+            }
         };
-        auto largest = [&]() {   // the row's largest logit of the tile, in log2 units
+        auto too_large = [&]() { return !((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y) <= LIMIT); };
+        auto add_sums = [&]() {
+          l2[0] = fadd2(l2[0], sum[0]);
+          l2[1] = fadd2(l2[1], sum[1]);
+        };
+        auto largest = [&](int from) {   // the row's largest logit from `from` on, in log2 units
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int x = 0; x < 128; x += 2)
-            mx[(x >> 1) & 3] = max3(mx[(x >> 1) & 3], __uint_as_float(r[x]), __uint_as_float(r[x + 1]));
+            if (x >= from) mx[(x >> 1) & 3] = max3(mx[(x >> 1) & 3], __uint_as_float(r[x]), __uint_as_float(r[x + 1]));
           return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
         };
         // A row moves its own reference alone: its result does not depend on its neighbours.
-        auto move = [&](bool moves, float top) {
+        auto move = [&](bool moves, float top, bool has_o) {
           const float now = moves ? fmaxf(m, top) : m;
           const float f = now == -INFINITY ? 1.f : ex2(m - now);
           m = now;
           l2[0].x *= f, l2[0].y *= f, l2[1].x *= f, l2[1].y *= f;
-          if (j > 0) {
+          if (has_o) {
             // every P V before is done, so O is still
 #pragma unroll 1
             for (int b = 0; b < D / 16; ++b) {
@@ -707,9 +734,15 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
             }
           }
         };
-        load();
+        auto hand_over = [&](uint32_t bar) {
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_at(bar);
+        };
+        load(0);
         if (OWN_P) {
-          const float top = largest();
+          const float top = largest(0);
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_at(s_bar);
@@ -719,29 +752,38 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
             tc_fence_after();
           }
           const bool moves = j == 0 || top > m + GROW;
-          if (__any_sync(0xffffffffu, moves)) move(moves, top);
-          weights();
+          if (__any_sync(0xffffffffu, moves)) move(moves, top, j > 0);
+          weights(0, 128);
+          DSA_TMEM_ST32(tp, r);
+          DSA_TMEM_ST32(tp + 32, (r + 32));
+          add_sums();
+          hand_over(p_bar);
         } else {
-          bool moves = j == 0;
-          if (j > 0) {
-            weights();
-            moves = !((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y) <= LIMIT);
+          // By halves, so that the products with the first begin while the second's weights are taken.
+          if (j == 0) move(true, largest(0), false);
+          weights(0, 64);
+          bool moves = too_large();
+          if (__any_sync(0xffffffffu, moves)) {   // the scores again, and the tile's maximum
+            load(0);
+            move(moves, largest(0), j > 0);
+            weights(0, 64);
           }
-          if (__any_sync(0xffffffffu, moves)) {
-            // The first tile, or one whose weights pass the limit: the scores again, and their maximum.
-            if (j > 0) load();
-            move(moves, largest());
-            weights();
+          DSA_TMEM_ST32(tp, r);
+          add_sums();
+          hand_over(p_bar);
+          weights(64, 128);
+          moves = too_large();
+          if (__any_sync(0xffffffffu, moves)) {   // O has the first half's products already
+            if (!(ok = warp_wait(half_done + i, turns & 1))) break;
+            tc_fence_after();
+            load(64);
+            move(moves, largest(64), true);
+            weights(64, 128);
           }
+          DSA_TMEM_ST32(tp + 32, (r + 32));
+          add_sums();
+          hand_over(p_bar + 8);
         }
-        DSA_TMEM_ST32(tp, r);
-        DSA_TMEM_ST32(tp + 32, (r + 32));
-        l2[0] = fadd2(l2[0], sum[0]);
-        l2[1] = fadd2(l2[1], sum[1]);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_at(p_bar);
       }
       if (ok && ni > 0) ok = warp_wait(o_full + i, outs & 1);
       outs += ni > 0;

@@ -193,6 +193,20 @@ def test_falling_logits_underflow():
     _run(case)
 
 
+@pytest.mark.parametrize("dim,shared", [(128, 64), (128, 0), (64, 0)])
+@pytest.mark.parametrize("lens", [[(600, 1500)], [(1, 2000)], [(100, 330)]])
+@pytest.mark.parametrize("dt", [BF, FP])
+def test_keys_whose_logits_are_minus_infinity(dt, lens, dim, shared):
+    # They weigh nothing, though the first tiles hold no other: the result is that over the keys behind.
+    case = PromptCase(lens, 2, 1, dim, shared, dt, False, seed=8)
+    case.q[..., 0] = 0.5
+    case.k[:300, :, 0] = float("-inf")
+    case.to_device().run()
+    (lq, lk), = lens
+    case.lens, case.cu_k = [(lq, lk - 300)], np.asarray([300, lk])
+    case.check()
+
+
 def test_many_short_sequences():
     rng = np.random.default_rng(0)
     lens = [(int(a), int(b)) for a, b in rng.integers(0, 4, (1500, 2))]
