@@ -25,8 +25,8 @@
 //    one may be out of range (above 2^20 in bf16; 2^15 in fp16, whose weights start from 2^7 to keep more
 //    of what is small): only then the maximum is found, the reference moves, and the sums and O are
 //    scaled.  Finding the maximum of every tile took 400 of 1,300 cycles.  The products with a tile's
-//    first 64 keys begin while the other weights are taken: 32 ragged prompts 720 -> 701 us, a step of 16
-//    134 -> 128.
+//    first 64 keys begin while the other weights are taken: 16 single tokens 134 -> 128 us, 32 ragged
+//    prompts 732 -> 724.
 //  - D = 64: products are short, and the chain from scores to scores is what a step takes.  The maximum is
 //    found first, P has columns of its own behind O, and S is given back as soon as it is read: the next
 //    scores are made while the weights are taken.
@@ -210,10 +210,10 @@ __device__ __forceinline__ float2 unpack16(uint32_t v, bool fp16) {
 }
 
 // Weights of an earlier result and of the new one, and the joined log-sum-exp, all in natural
-// logarithms.  Two empty results join to an empty one.
+// logarithms.  Two empty results join to an empty one.  (fmaxf passes over a NaN; the sum does not.)
 __device__ __forceinline__ float join_lse(float a, float b, float& wa, float& wb) {
   const float m = fmaxf(a, b);
-  if (m == -INFINITY) {
+  if (a == -INFINITY && b == -INFINITY) {
     wa = wb = 0.f;
     return -INFINITY;
   }
@@ -549,13 +549,16 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
         p_turn ^= 1u << i;
         const uint32_t p_tmem = tmem + P_COL + 128 * i, o_tmem = tmem + O_COL + 128 * i;
         const uint64_t b = dv + ((v.st * S::V_BYTES) >> 4);
-        const int parts16 = (keys + 15) / 16;   // MMAs, of 16 keys each
-        auto values = [&](int from) {           // four of them
+        auto values = [&](int from, int to) {   // with 16 keys each; a whole tile's without asking for each (5% at 64 dims)
+          if (keys >= kPromptKeys) {
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            if (from + x < parts16)
-              mma_f16_ts<CTAS>(o_tmem, p_tmem + 8 * (from + x), b + (((from + x) * 32 * S::V_WIDTH) >> 4), idesc_pv,
-                               j || from || x ? 1u : 0u);
+            for (int x = 0; x < 8; ++x)
+              if (x >= from && x < to)
+                mma_f16_ts<CTAS>(o_tmem, p_tmem + 8 * x, b + ((x * 32 * S::V_WIDTH) >> 4), idesc_pv, j || x ? 1u : 0u);
+          } else {
+            for (int x = from; x < min(to, (keys + 15) / 16); ++x)
+              mma_f16_ts<CTAS>(o_tmem, p_tmem + 8 * x, b + ((x * 32 * S::V_WIDTH) >> 4), idesc_pv, j || x ? 1u : 0u);
+          }
         };
         if (OWN_P) {
           const uint32_t si = smem_u32(s_free + i);
@@ -570,7 +573,7 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
         tc_fence_after();
         if (!OWN_P) {
           if (leader) {
-            values(0);
+            values(0, 4);
             tc_commit_all<CTAS>(half_done + i);
           }
           __syncwarp();
@@ -578,8 +581,7 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
           tc_fence_after();
         }
         if (leader) {
-          if (OWN_P) values(0);
-          values(4);
+          values(OWN_P ? 0 : 4, 8);
           if (!PAIR || MW == 2 || i == 1 || j >= cur_item.n1) tc_commit_all<CTAS>(v_empty + v.st);
           if (OWN_P || !more) tc_commit_all<CTAS>(o_full + i);
           if (!OWN_P && more) scores(i, cur_item, j + 1, k);
@@ -811,17 +813,14 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
         w1 = m == -INFINITY ? 0.f : ex2(m1 - m);
         l = ml[256 + row] * w0 + ml[384 + row] * w1;
       }
-      const bool empty_row = !(l > 0.f);   // nothing seen
+      const bool empty_row = l == 0.f;   // nothing seen
       const float lse2 = empty_row ? -INFINITY : m - SHIFT + log2f(l);
       const int64_t at = static_cast<int64_t>(it.q0 + tok) * p.heads + static_cast<int64_t>(it.head) * p.group + g;
-      float w = empty_row ? 0.f : 1.f / l, wp = 0.f;
+      const float w = empty_row ? 0.f : 1.f / l;
+      float wp = 0.f, wn = 1.f;   // of the earlier result and this one
       float lse = lse2 * 0.6931471805599453f;
       const bool last = p.nparts == 1;
-      if (last && p.prev_lse && valid) {
-        float wn;
-        lse = join_lse(p.prev_lse[at], lse, wp, wn);
-        w *= wn;
-      }
+      if (last && p.prev_lse && valid) lse = join_lse(p.prev_lse[at], lse, wp, wn);
       w0 *= w;
       w1 *= w;
       if (!PAIR) sync();   // prev_lse may be lse, and ml is written again
@@ -855,6 +854,10 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
                                __uint_as_float(o[4 * x + 3]));
       }
       if (valid && last) {
+        if (p.prev_out) {   // in the merge's order of roundings
+#pragma unroll
+          for (int x = 0; x < MINE; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * wn);
+        }
         if (p.prev_out && wp > 0.f) {
           const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.prev_out) + at * D + d0);
 #pragma unroll
@@ -916,12 +919,18 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const PromptParams p)
   const int parts = vis > 0 ? static_cast<int>((vis + p.part_keys - 1) / p.part_keys) : 0;
   const int64_t step = p.total_q * p.heads;
   float m = -INFINITY;
-  for (int k = lane; k < parts; k += 32) m = fmaxf(m, p.part_lse[k * step + at]);
+  bool any = false;   // a part that is not empty (fmaxf passes over a NaN)
+  for (int k = lane; k < parts; k += 32) {
+    const float x = p.part_lse[k * step + at];
+    any = any || x != -INFINITY;
+    m = fmaxf(m, x);
+  }
   m = warp_max_f32(m);
+  any = __any_sync(0xffffffffu, any);
   float sum = 0.f;
   constexpr int PER = D / 32;
   float o[PER] = {};
-  if (m > -INFINITY)
+  if (any)
     for (int k = 0; k < parts; ++k) {
       const float w = exp2f(p.part_lse[k * step + at] - m);
       sum += w;
@@ -935,13 +944,14 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const PromptParams p)
         o[0] = fmaf(w, v.x, o[0]), o[1] = fmaf(w, v.y, o[1]);
       }
     }
-  float lse = sum > 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
-  float w = sum > 0.f ? 1.f / sum : 0.f, wp = 0.f;
+  float lse = any ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+  float w = any ? 1.f / sum : 0.f, wp = 0.f;
   if (p.prev_lse) {
     float wn;
     lse = join_lse(p.prev_lse[at], lse, wp, wn);
     w *= wn;
   }
+  __syncwarp();   // prev_lse may be lse
   if (lane == 0 && p.lse) p.lse[at] = lse;
 #pragma unroll
   for (int x = 0; x < PER; ++x) o[x] *= w;

@@ -130,7 +130,7 @@ __device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
 __device__ __forceinline__ void mbar_arrive_expect_tx_at(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
-// The same behind plain stores to shared memory, for the other CTA's threads that wait by mbar_wait_cluster.
+// The same behind plain stores to shared memory, for the other CTA's threads that follow their wait by mbar_acquire_cluster.
 __device__ __forceinline__ void mbar_arrive_release_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -144,7 +144,7 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t addr, uint32_t pa
       : "memory");
   return ok != 0;
 }
-// After mbar_wait_inline of a phase in which a thread of the other CTA arrived by
+// After a wait for a phase in which a thread of the other CTA arrived by
 // mbar_arrive_release_at: its stores are visible, too (the phase is complete, so this returns at once).
 __device__ __forceinline__ void mbar_acquire_cluster(uint64_t* bar, uint32_t parity) {
   mbar_try_wait_cluster(smem_u32(bar), parity);
@@ -218,15 +218,6 @@ __device__ __forceinline__ bool warp_wait2(uint32_t a, uint32_t pa, uint32_t b, 
       [&] {
         const bool x = mbar_try_wait(a, pa), y = mbar_try_wait(b, pb);
         return x && y;
-      },
-      ab);
-}
-
-__device__ __forceinline__ bool warp_wait3(uint32_t a, uint32_t pa, uint32_t b, uint32_t pb, uint32_t c, uint32_t pc, Abort ab) {
-  return warp_wait_until(
-      [&] {
-        const bool x = mbar_try_wait(a, pa), y = mbar_try_wait(b, pb), z = mbar_try_wait(c, pc);
-        return x && y && z;
       },
       ab);
 }

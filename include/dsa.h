@@ -609,9 +609,10 @@ size_t dsa_prompt_workspace_size(const dsa_prompt *prompt);
  *  shared_dim is 0;  out: device [total_q, heads, dim], contiguous;  lse: device fp32
  *  [total_q, heads] or NULL;  prev_out, prev_lse: as out and lse, both or neither
  *  All of them 16-byte aligned (lse and prev_lse 4-byte).  sm_scale > 0, finite.
- * The rows of a sequence must be finite, and so must its logits be; what stands in rows of no
- * sequence (NaN included) never reaches a result, and their rows of out and lse are left as
- * they are.  Weights are rounded to the inputs' type, sums are fp32.
+ * The values v of a sequence must be finite, those of keys that a row does not see, too.  A logit
+ * of -inf weighs nothing; one that is NaN or +inf makes the row that sees it NaN, and no other row.
+ * What stands in rows of no sequence (NaN included) never reaches a result, and their rows of out
+ * and lse are left as they are.  Weights are rounded to the inputs' type, sums are fp32.
  * Where the batch has few rows for the GPU, the keys are split over more CTAs and merged; how
  * depends on the batch and the GPU.  With DSA_PROMPT_INVARIANT they are split every 65,536 keys
  * and nowhere else (longer runs of sums would lose precision), and a row's result depends on its

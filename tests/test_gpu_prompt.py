@@ -207,6 +207,40 @@ def test_keys_whose_logits_are_minus_infinity(dt, lens, dim, shared):
     case.check()
 
 
+@pytest.mark.parametrize("dim,shared", [(128, 64), (128, 0), (64, 0)])
+@pytest.mark.parametrize("lens,prev", [([(600, 1500)], False), ([(1, 2000)], True), ([(100, 330)], True), ([(600, 700)], True)])
+def test_nan_stays_in_the_rows_that_see_it(lens, prev, dim, shared):
+    case = PromptCase(lens, 2, 1, dim, shared, BF, True, seed=8, prev=prev).to_device()
+    out, lse = (x.clone() for x in case.run())
+    (lq, lk), = lens
+    row, key = lq // 2, lk - lq // 3 - 1      # a query, and a key that the last third sees
+    case.dq[row, 1, 0] = float("nan")
+    case.dk[key, 0, 5] = float("nan")
+    if prev:
+        case.d_prev[1][0] = float("-inf")     # the first row sees keys alone
+    case.run()
+    nan = torch.zeros(lq, 2, dtype=torch.bool, device="cuda")
+    nan[key - (lk - lq):] = True
+    nan[row, 1] = True
+    assert torch.equal(torch.isnan(case.lse), nan)
+    assert torch.equal(torch.isnan(case.out), nan[..., None].expand(case.out.shape))
+    rest = ~nan
+    rest[0] = False
+    assert torch.equal(case.out[rest], out[rest]) and torch.equal(case.lse[rest], lse[rest])
+
+
+@pytest.mark.parametrize("dim,shared", [(128, 64), (64, 0)])
+def test_invariant_rows_do_not_depend_on_the_bound(dim, shared):
+    import dsa_sparse_attention_gb300 as dsa
+    got = []
+    for max_k in (900, 70000):                # one run of keys, or two of which one is empty
+        case = PromptCase([(300, 900), (1, 40), (3, 0)], 2, 1, dim, shared, BF, True, seed=8, prev=True,
+                          flags=dsa.DSA_PROMPT_INVARIANT, max_k=max_k)
+        _run(case)
+        got.append((case.out, case.lse))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
 def test_many_short_sequences():
     rng = np.random.default_rng(0)
     lens = [(int(a), int(b)) for a, b in rng.integers(0, 4, (1500, 2))]
