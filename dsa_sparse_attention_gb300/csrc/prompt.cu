@@ -246,8 +246,7 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
   uint64_t* v_full = k_full + STAGES;                   // [STAGES] values landed
   uint64_t* q_full = v_full + STAGES;                   // [2] query tile landed
   uint64_t* p_full = q_full + 2;                        // [2][2] P written: the first 64 keys, the others (OWN_P: all)
-  uint64_t* s_free = p_full + 4;                        // [2] S read (where P has a place of its own)
-  uint64_t* asked = s_free + 2;                         // both CTAs have read the last answer
+  uint64_t* asked = p_full + 4;                         // both CTAs have read the last answer
   // In each CTA: what the MMAs signal.
   uint64_t* k_empty = asked + 1;                        // [STAGES]
   uint64_t* v_empty = k_empty + STAGES;                 // [STAGES]
@@ -268,7 +267,7 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
   uint4* answer = reinterpret_cast<uint4*>(bars + 56);
   Item* items = reinterpret_cast<Item*>(bars + 58);     // [2]
   float* ml = reinterpret_cast<float*>(bars + 128);     // [4][128] references and sums of a single CTA's two S
-  static_assert(4 * STAGES + 32 <= 56 && 1024 + 4 * 128 * 4 <= MISC, "shared scalars");
+  static_assert(4 * STAGES + 30 <= 56 && 1024 + 4 * 128 * 4 <= MISC, "shared scalars");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = PAIR ? static_cast<int>(cluster_rank()) : 0;
 
@@ -291,7 +290,6 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(p_full + 2 * i, 4 * CTAS);
       mbar_init(p_full + 2 * i + 1, 4 * CTAS);
-      mbar_init(s_free + i, 4 * CTAS);
       mbar_init(half_done + i, 1);
     }
     mbar_init(asked, CTAS);
@@ -560,15 +558,10 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
               mma_f16_ts<CTAS>(o_tmem, p_tmem + 8 * x, b + ((x * 32 * S::V_WIDTH) >> 4), idesc_pv, j || x ? 1u : 0u);
           }
         };
-        if (OWN_P) {
-          const uint32_t si = smem_u32(s_free + i);
-          if (!(ok = warp_wait2(si, turn, more ? kf + 8 * k.st : si, more ? k.ph : turn, ab))) return;
-          tc_fence_after();
-          if (leader && more) scores(i, cur_item, j + 1, k);
-          __syncwarp();
-        }
         // P's of a new item come when the softmax is done with the last one's O.
-        if (!(ok = warp_wait2(pi, turn, vf + 8 * v.st, v.ph, ab))) return;
+        const bool next_too = OWN_P && more;   // S is read before P is written
+        if (!(ok = next_too ? warp_wait3(pi, turn, vf + 8 * v.st, v.ph, kf + 8 * k.st, k.ph, ab)
+                            : warp_wait2(pi, turn, vf + 8 * v.st, v.ph, ab))) return;
         if (PAIR && keys < kPromptKeys) mbar_acquire_cluster(v_full + v.st, v.ph);   // values cut by plain stores
         tc_fence_after();
         if (!OWN_P) {
@@ -581,6 +574,7 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
           tc_fence_after();
         }
         if (leader) {
+          if (next_too) scores(i, cur_item, j + 1, k);
           values(OWN_P ? 0 : 4, 8);
           if (!PAIR || MW == 2 || i == 1 || j >= cur_item.n1) tc_commit_all<CTAS>(v_empty + v.st);
           if (OWN_P || !more) tc_commit_all<CTAS>(o_full + i);
@@ -647,8 +641,7 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
     const float sc = p.scale_log2;
     constexpr float SHIFT = FP16 ? 7.f : 0.f;
     constexpr float LIMIT = FP16 ? 32768.f : 1048576.f;   // of the sum of half a tile's weights, and so of each of them
-    constexpr float GROW = 8.f;   // log2 units that a logit may exceed the reference by, where it is looked at
-    const uint32_t p_bar = at_leader(p_full + 2 * i), s_bar = at_leader(s_free + i);
+    const uint32_t p_bar = at_leader(p_full + 2 * i);
     bool ok = true;
     int turns = 0, outs = 0, syncs = 0;   // phases of s_full, o_full and both
     // All softmax warps of a single CTA, for which a failed wait ends this one, too.
@@ -744,18 +737,26 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
         };
         load(0);
         if (OWN_P) {
-          const float top = largest(0);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_at(s_bar);
-          if (j > 0) {   // the last P is read, and O is still
-            if (!(ok = warp_wait(o_full + i, outs & 1))) break;
-            ++outs;
-            tc_fence_after();
-          }
-          const bool moves = j == 0 || top > m + GROW;
-          if (__any_sync(0xffffffffu, moves)) move(moves, top, j > 0);
+          bool still = j == 0;   // the last P is read, and O is still
+          auto last_read = [&]() {
+            if (!still) {
+              ok = warp_wait(o_full + i, outs & 1);
+              ++outs;
+              tc_fence_after();
+              still = true;
+            }
+            return ok;
+          };
+          if (j == 0) move(true, largest(0), false);
           weights(0, 128);
+          const bool moves = too_large();
+          if (__any_sync(0xffffffffu, moves)) {   // the scores again, and the tile's maximum
+            if (!last_read()) break;
+            load(0);
+            move(moves, largest(0), j > 0);
+            weights(0, 128);
+          }
+          if (!last_read()) break;
           DSA_TMEM_ST32(tp, r);
           DSA_TMEM_ST32(tp + 32, (r + 32));
           add_sums();

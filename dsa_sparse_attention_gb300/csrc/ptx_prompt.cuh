@@ -209,7 +209,7 @@ __device__ __forceinline__ bool warp_wait_until(Done done, Abort ab) {
     }
   }
 }
-// For a phase of one barrier, or of two at a time (addresses in this CTA's shared memory).
+// For a phase of one barrier, or of two or three at a time (addresses in this CTA's shared memory).
 __device__ __forceinline__ bool warp_wait1(uint32_t a, uint32_t pa, Abort ab) {
   return warp_wait_until([&] { return mbar_try_wait(a, pa); }, ab);
 }
@@ -218,6 +218,14 @@ __device__ __forceinline__ bool warp_wait2(uint32_t a, uint32_t pa, uint32_t b, 
       [&] {
         const bool x = mbar_try_wait(a, pa), y = mbar_try_wait(b, pb);
         return x && y;
+      },
+      ab);
+}
+__device__ __forceinline__ bool warp_wait3(uint32_t a, uint32_t pa, uint32_t b, uint32_t pb, uint32_t c, uint32_t pc, Abort ab) {
+  return warp_wait_until(
+      [&] {
+        const bool x = mbar_try_wait(a, pa), y = mbar_try_wait(b, pb), z = mbar_try_wait(c, pc);
+        return x && y && z;
       },
       ab);
 }
