@@ -204,6 +204,12 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi, bool fp16) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+__device__ __forceinline__ float2 get2(const uint32_t* r) { return make_float2(__uint_as_float(r[0]), __uint_as_float(r[1])); }
+__device__ __forceinline__ void set2(uint32_t* r, float2 v) {
+  r[0] = __float_as_uint(v.x);
+  r[1] = __float_as_uint(v.y);
+}
+
 __device__ __forceinline__ float2 unpack16(uint32_t v, bool fp16) {
   if (fp16) return __half22float2(*reinterpret_cast<const __half2*>(&v));
   return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
@@ -797,10 +803,6 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
       constexpr int MINE = PAIR ? D : D / 2;        // dims that this thread writes, from d0 on
       const int d0 = PAIR ? 0 : i * MINE;
       float w0 = 1.f, w1 = 1.f;                     // a single CTA: weights of O_0 and O_1
-      uint32_t o[MINE] = {};
-      if (PAIR && ni > 0)                           // on its way while the sums are looked at
-#pragma unroll
-        for (int b = 0; b < MINE / 32; ++b) DSA_TMEM_LD32(to + 128 * i + 32 * b, (o + 32 * b));
       if (!PAIR) {
         // Both threads of a row (they reach the same lanes of tensor memory) take the common
         // reference, and half of the dims of either O.
@@ -830,60 +832,61 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
         if (!last) p.part_lse[static_cast<int64_t>(it.part) * p.total_q * p.heads + at] = lse2;
         else if (p.lse) p.lse[at] = lse;
       }
-      if (PAIR) {
-        if (ni > 0) tmem_wait_ld();
+      // A row that sees nothing has weights of 0, and O with them, or no O at all.  32 dims at a time, in a
+      // loop: code that runs once an item comes cold, at about 5 cycles an instruction.
+#pragma unroll 1
+      for (int b = 0; b < MINE / 32; ++b) {
+        const int c0 = d0 + 32 * b;
+        uint32_t o[32] = {};
+        if (PAIR) {
+          if (ni > 0) DSA_TMEM_LD32(to + 128 * i + c0, o);
+          tmem_wait_ld();
 #pragma unroll
-        for (int x = 0; x < MINE; ++x) o[x] = empty_row ? 0u : __float_as_uint(__uint_as_float(o[x]) * w0);
-      } else {
-        if (it.n[0] > 0)
+          for (int x = 0; x < 32; x += 2) set2(o + x, fmul2(get2(o + x), make_float2(w0, w0)));
+        } else {
+          uint32_t o1[32] = {};
+          if (it.n[0] > 0) DSA_TMEM_LD32(to + c0, o);
+          if (it.n[1] > 0) DSA_TMEM_LD32(to + 128 + c0, o1);
+          tmem_wait_ld();
 #pragma unroll
-          for (int b = 0; b < MINE / 32; ++b) DSA_TMEM_LD32(to + d0 + 32 * b, (o + 32 * b));
-        uint32_t o1[MINE] = {};
-        if (it.n[1] > 0)
-#pragma unroll
-          for (int b = 0; b < MINE / 32; ++b) DSA_TMEM_LD32(to + 128 + d0 + 32 * b, (o1 + 32 * b));
-        tmem_wait_ld();
-#pragma unroll
-        for (int x = 0; x < MINE; ++x)
-          o[x] = empty_row ? 0u : __float_as_uint(fmaf(__uint_as_float(o1[x]), w1, __uint_as_float(o[x]) * w0));
-      }
-      if (valid && !last) {
-        float4* dst = reinterpret_cast<float4*>(p.part_o + (static_cast<int64_t>(it.part) * p.total_q * p.heads + at) * D + d0);
-#pragma unroll
-        for (int x = 0; x < MINE / 4; ++x)
-          dst[x] = make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]), __uint_as_float(o[4 * x + 2]),
-                               __uint_as_float(o[4 * x + 3]));
-      }
-      if (valid && last) {
-        if (p.prev_out) {   // in the merge's order of roundings
-#pragma unroll
-          for (int x = 0; x < MINE; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * wn);
+          for (int x = 0; x < 32; x += 2)
+            set2(o + x, ffma2(get2(o1 + x), make_float2(w1, w1), fmul2(get2(o + x), make_float2(w0, w0))));
         }
-        if (p.prev_out && wp > 0.f) {
-          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.prev_out) + at * D + d0);
+        if (valid && !last) {
+          float4* dst = reinterpret_cast<float4*>(p.part_o + (static_cast<int64_t>(it.part) * p.total_q * p.heads + at) * D + c0);
 #pragma unroll
-          for (int x = 0; x < MINE / 8; ++x) {
-            const uint4 v = src[x];
-            const uint32_t v4[4] = {v.x, v.y, v.z, v.w};
+          for (int x = 0; x < 8; ++x)
+            dst[x] = make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]), __uint_as_float(o[4 * x + 2]),
+                                 __uint_as_float(o[4 * x + 3]));
+        } else if (valid) {
+          if (p.prev_out) {   // in the merge's order of roundings
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const float2 f = unpack16(v4[y], FP16);
-              o[8 * x + 2 * y] = __float_as_uint(fmaf(f.x, wp, __uint_as_float(o[8 * x + 2 * y])));
-              o[8 * x + 2 * y + 1] = __float_as_uint(fmaf(f.y, wp, __uint_as_float(o[8 * x + 2 * y + 1])));
+            for (int x = 0; x < 32; x += 2) set2(o + x, fmul2(get2(o + x), make_float2(wn, wn)));
+            if (wp > 0.f) {
+              const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.prev_out) + at * D + c0);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const uint4 v = src[x];
+                const uint32_t v4[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                  set2(o + 8 * x + 2 * y, ffma2(unpack16(v4[y], FP16), make_float2(wp, wp), get2(o + 8 * x + 2 * y)));
+              }
             }
           }
+#pragma unroll
+          for (int x = 0; x < 16; ++x) o[x] = pack16(__uint_as_float(o[2 * x]), __uint_as_float(o[2 * x + 1]), FP16);
+          uint16_t* dst = static_cast<uint16_t*>(p.out) + at * D + c0;
+          if (p.out_aligned32) {   // whole sectors
+            st_global_v8(dst, o);
+            st_global_v8(dst + 16, o + 8);
+          } else {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              reinterpret_cast<uint4*>(dst)[x] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+          }
         }
-#pragma unroll
-        for (int x = 0; x < MINE / 2; ++x) o[x] = pack16(__uint_as_float(o[2 * x]), __uint_as_float(o[2 * x + 1]), FP16);
-        uint16_t* dst = static_cast<uint16_t*>(p.out) + at * D + d0;
-        if (p.out_aligned32) {   // whole sectors
-#pragma unroll
-          for (int x = 0; x < MINE / 16; ++x) st_global_v8(dst + 16 * x, o + 8 * x);
-        } else {
-#pragma unroll
-          for (int x = 0; x < MINE / 8; ++x)
-            reinterpret_cast<uint4*>(dst)[x] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
-        }
+        __syncwarp();
       }
       // the next item's O is written once every warp that reads this one's has its next P in place
       tc_fence_before();
