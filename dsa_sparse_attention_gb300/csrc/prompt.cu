@@ -662,10 +662,8 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
       const int tok = it.t0 + row_tok;
       const bool valid = row_used && tok < it.lq;
       // keys of this part that the row sees
-      int64_t sees = it.lk;
-      if (p.causal) sees = min(sees, static_cast<int64_t>(tok) + 1 + it.lk - it.lq);
-      const int vis = valid ? static_cast<int>(max(static_cast<int64_t>(0), min(sees, static_cast<int64_t>(it.end)) - it.beg))
-                            : it.end - it.beg;
+      const int sees = p.causal ? it.lk + (min(tok + 1, it.lq) - it.lq) : it.lk;
+      const int vis = valid ? max(0, min(sees, it.end) - it.beg) : it.end - it.beg;
       const int all_see = __reduce_min_sync(0xffffffffu, vis);
       float m = -INFINITY;           // reference: a logit of m has weight 2^SHIFT
       float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
