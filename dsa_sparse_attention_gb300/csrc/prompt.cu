@@ -27,9 +27,10 @@
 //    scaled.  Finding the maximum of every tile took 400 of 1,300 cycles.  The products with a tile's
 //    first 64 keys begin while the other weights are taken: 16 single tokens 134 -> 128 us, 32 ragged
 //    prompts 732 -> 724.
-//  - D = 64: products are short, and the chain from scores to scores is what a step takes.  The maximum is
-//    found first, P has columns of its own behind O, and S is given back as soon as it is read: the next
-//    scores are made while the weights are taken.
+//  - D = 64: the same by whole tiles, with P in columns of its own behind O: the next scores go ahead of
+//    a P's products, and one wait serves both.  What bounds it is the warp that issues the products,
+//    1,130 cycles for a key tile's 512.  (Scores given back before the weights: a wait more, 122 us, not
+//    119, for 4 x 301 tokens on 7,891 keys.)
 #include <cuda_runtime.h>
 
 #include <cfloat>
@@ -646,7 +647,7 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
     const bool row_used = row < p.tile_toks * p.group;
     const float sc = p.scale_log2;
     constexpr float SHIFT = FP16 ? 7.f : 0.f;
-    constexpr float LIMIT = FP16 ? 32768.f : 1048576.f;   // of the sum of half a tile's weights, and so of each of them
+    constexpr float LIMIT = FP16 ? 32768.f : 1048576.f;   // of the sum of a tile's or half a tile's weights, and so of each
     const uint32_t p_bar = at_leader(p_full + 2 * i);
     bool ok = true;
     int turns = 0, outs = 0, syncs = 0;   // phases of s_full, o_full and both
@@ -831,7 +832,8 @@ __global__ void __launch_bounds__(prompt::THREADS, 1)
         else if (p.lse) p.lse[at] = lse;
       }
       // A row that sees nothing has weights of 0, and O with them, or no O at all.  32 dims at a time, in a
-      // loop: code that runs once an item comes cold, at about 5 cycles an instruction.
+      // loop: code that runs once an item comes cold, at about 5 cycles an instruction (all at once: 708 us, not
+      // 684, for 32 ragged prompts).
 #pragma unroll 1
       for (int b = 0; b < MINE / 32; ++b) {
         const int c0 = d0 + 32 * b;
