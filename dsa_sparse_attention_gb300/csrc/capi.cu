@@ -406,10 +406,11 @@ constexpr int64_t kMinPart = 512;     // keys of a part, at least
 // (four tiles), and the keys in `parts` parts, a multiple of `least`, by the time that should take.
 // Items of one length go in rounds; of other lengths in equal shares, with part of the longest item
 // behind them.  About 6,000 cycles begin and end an item; the merge is a launch, and 3,000 bytes a
-// cycle.  Measured (us), pairs against single CTAs: 8,192 tokens of 96 heads 1,210, 1,611; 32 ragged
-// prompts 708, 1,030; 4 x 301 tokens on 7,891 keys, 32 heads of 64 dims, 150, 120; 33 tokens 14, 8.
-// Whole against in parts: 16 x 1 token over 1K to 32K keys 240 (3 parts), 160 (5), 134 (16); 500 tokens
-// on 64K, 96 heads (96 items for 76 pairs) 1,500, 1,290 (2), 1,245 (3), 1,290 (6).
+// cycle.  Measured (us, calls back to back), pairs against single CTAs: 8,192 tokens of 96 heads 1,235,
+// 1,522; 32 ragged prompts 642, 935; 4 x 301 tokens on 7,891 keys, 32 heads of 64 dims, 172, 118; 33
+// tokens 13, 9.  Whole against in parts: 16 x 1 token over 1K to 32K keys 326, 237 (3 parts), 159 (5), 131
+// (8), 128 (16); 500 tokens on 64K, 96 heads (96 items for 76 pairs) 1,512, 1,315 (2), 1,275 (3), 1,353
+// (4), 1,286 (6).
 struct Division {
   int ctas;
   int64_t blocks, parts;
