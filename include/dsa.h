@@ -611,6 +611,7 @@ size_t dsa_prompt_workspace_size(const dsa_prompt *prompt);
  *  All of them 16-byte aligned (lse and prev_lse 4-byte).  sm_scale > 0, finite.
  * The values v of a sequence must be finite, those of keys that a row does not see, too.  A logit
  * of -inf weighs nothing; one that is NaN or +inf makes the row that sees it NaN, and no other row.
+ * Finite logits may be as large as 2^27 (in fp16; a weight passes its range behind that).
  * What stands in rows of no sequence (NaN included) never reaches a result, and their rows of out
  * and lse are left as they are.  Weights are rounded to the inputs' type, sums are fp32.
  * Where the batch has few rows for the GPU, the keys are split over more CTAs and merged; how

@@ -207,6 +207,25 @@ def test_keys_whose_logits_are_minus_infinity(dt, lens, dim, shared):
     case.check()
 
 
+@pytest.mark.parametrize("dim", [128, 64])
+@pytest.mark.parametrize("lens", [[(600, 700)], [(1, 2000)]])
+@pytest.mark.parametrize("dt", [BF, FP])
+def test_logits_of_a_hundred_million_are_finite(dt, lens, dim):
+    # fp32 holds them to 16 at best: a weight may be 2^8 too large, which either type holds (0.86 * 2^27)
+    case = PromptCase(lens, 2, 2, dim, 0, dt, True, seed=4, scale=2.5 * 128 / dim)
+    sign = torch.sign(torch.randn(1, 2, dim, generator=torch.Generator().manual_seed(1)))
+    case.q = (sign * 600.0 + case.q.float()).to(dt)
+    case.k = (sign * 600.0 + case.k.float()).to(dt)
+    case.to_device().run()
+    # Logits known to 2^-18 of 10^8 leave the weights of keys within 400 of the largest open (the tolerance of
+    # other cases is of first order in that error, which must be below 1): any mean of the values is right, up to
+    # a rounding of a weight and of the result.
+    u = torch.finfo(dt).eps / 2
+    most = case.v.abs().amax(0).cuda().double() * (1 + 4 * u)
+    assert torch.isfinite(case.out).all() and (case.out.double().abs() <= most).all()
+    assert torch.isfinite(case.lse).all() and (case.lse > 0.9e8).all() and (case.lse < 1.5e8).all()
+
+
 @pytest.mark.parametrize("dim,shared", [(128, 64), (128, 0), (64, 0)])
 @pytest.mark.parametrize("lens,prev", [([(600, 1500)], False), ([(1, 2000)], True), ([(100, 330)], True), ([(600, 700)], True)])
 def test_nan_stays_in_the_rows_that_see_it(lens, prev, dim, shared):
